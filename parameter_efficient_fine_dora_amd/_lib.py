@@ -16,6 +16,8 @@ ERR = {0: "DORA_OK", -1: "DORA_ERR_NULL", -2: "DORA_ERR_SHAPE", -3: "DORA_ERR_DT
        -4: "DORA_ERR_ALIGN", -5: "DORA_ERR_WORKSPACE", -6: "DORA_ERR_HIP", -7: "DORA_ERR_FLAGS"}
 ERR_CODE = {v: k for k, v in ERR.items()}
 NOALLOC_SCRATCH_BYTES = 64 << 20   # DORA_NOALLOC_SCRATCH_BYTES
+LOGPROB_MAX_TOP = 64               # DORA_LOGPROB_MAX_TOP
+STATE_BLOCK = 128                  # DORA_STATE_BLOCK
 
 
 class DoraShape(ctypes.Structure):
@@ -23,6 +25,39 @@ class DoraShape(ctypes.Structure):
         ("d_out", ctypes.c_int64), ("d_in", ctypes.c_int64), ("r", ctypes.c_int64),
         ("tokens", ctypes.c_int64), ("dtype", ctypes.c_int32), ("s", ctypes.c_float),
         ("flags", ctypes.c_uint32), ("reserved", ctypes.c_uint32),
+    ]
+
+
+class DoraLayernormShape(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("width", ctypes.c_int64), ("ld_x", ctypes.c_int64),
+        ("ld_gy", ctypes.c_int64), ("dtype", ctypes.c_int32), ("eps", ctypes.c_float),
+        ("flags", ctypes.c_uint32), ("reserved", ctypes.c_uint32),
+    ]
+
+
+class DoraLogprobShape(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("vocab", ctypes.c_int64), ("ld", ctypes.c_int64),
+        ("dtype", ctypes.c_int32), ("top", ctypes.c_int32), ("scale", ctypes.c_float),
+        ("reserved", ctypes.c_uint32),
+    ]
+
+
+class DoraAdamwTensor(ctypes.Structure):
+    _fields_ = [
+        ("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("exp_avg", ctypes.c_void_p),
+        ("exp_avg_sq", ctypes.c_void_p), ("exp_avg_scale", ctypes.c_void_p),
+        ("exp_avg_sq_scale", ctypes.c_void_p), ("master", ctypes.c_void_p), ("n", ctypes.c_int64),
+    ]
+
+
+class DoraAdamwOptions(ctypes.Structure):
+    _fields_ = [
+        ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32),
+        ("state_bits", ctypes.c_int32), ("reserved", ctypes.c_uint32), ("step", ctypes.c_int64),
+        ("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+        ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("grad_scale", ctypes.c_void_p),
     ]
 
 
@@ -46,6 +81,22 @@ _SIGS = {
     "dora_merge": (_i, [ctypes.POINTER(DoraShape), _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "dora_vera_scale": (_i, [ctypes.POINTER(DoraShape), _vp, _vp, _vp, _vp, _vp]),
     "dora_vera_grads": (_i, [ctypes.POINTER(DoraShape), _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "dora_layernorm_workspace_bytes": (_sz, [ctypes.POINTER(DoraLayernormShape)]),
+    "dora_layernorm_forward": (_i, [ctypes.POINTER(DoraLayernormShape), _vp, _vp, _vp, _vp, _vp, _vp,
+                                    _vp]),
+    "dora_layernorm_backward": (_i, [ctypes.POINTER(DoraLayernormShape), _vp, _vp, _vp, _vp, _vp, _vp,
+                                     _vp, _vp, _vp, _sz, _vp]),
+    "dora_token_logprob_workspace_bytes": (_sz, [ctypes.POINTER(DoraLogprobShape)]),
+    "dora_token_logprob_forward": (_i, [ctypes.POINTER(DoraLogprobShape), _vp, _vp, _vp, _vp, _vp,
+                                        _vp, _vp, _vp, _sz, _vp]),
+    "dora_token_logprob_backward": (_i, [ctypes.POINTER(DoraLogprobShape), _vp, _vp, _vp, _vp, _vp,
+                                         _vp, _vp, _vp]),
+    "dora_adamw_step": (_i, [_vp, ctypes.c_int64, ctypes.POINTER(DoraAdamwOptions), _vp]),
+    "dora_grad_norm_workspace_bytes": (_sz, [_vp, ctypes.c_int64]),
+    "dora_grad_norm": (_i, [_vp, ctypes.c_int64, ctypes.c_int32, ctypes.c_double, _vp, _vp, _vp, _sz,
+                            _vp]),
+    "dora_adamw_dequantize": (_i, [_vp, _vp, ctypes.c_int64, _i, _vp, ctypes.c_int32, _vp]),
+    "dora_adamw_quantize": (_i, [_vp, ctypes.c_int64, _i, _vp, _vp, _vp]),
     "dora_strerror": (ctypes.c_char_p, [_i]),
     "dora_timing_enable": (_i, [_i]),
     "dora_timing_collect": (_i, [ctypes.c_char_p, _sz]),

@@ -1,0 +1,108 @@
+// Rows of any length and alignment: loads and stores of 16-byte vectors that
+// start at any element (global memory takes unaligned 16-byte accesses on
+// gfx950; a row that starts inside a cache line costs one more line per wave),
+// and reductions over a wave and a workgroup.
+#pragma once
+#include "common.h"
+
+namespace dora {
+
+template <bool BF>
+struct Elem;   // element type of a tensor: bf16 (8 per vector) or float32 (4)
+
+template <>
+struct Elem<true> {
+  using T = uint16_t;
+  static constexpr int kN = 8;
+  typedef u32x4 Raw __attribute__((aligned(2)));
+  __device__ static float get(const T* p) { return bf16_to_f32(*p); }
+  __device__ static void put(T* p, float v) { *p = f32_to_bf16(v); }
+  __device__ static void load(const T* p, float* out) {
+    const u32x4 v = *reinterpret_cast<const Raw*>(p);
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      out[2 * d] = bf_lo(v[d]);
+      out[2 * d + 1] = bf_hi(v[d]);
+    }
+  }
+  __device__ static void store(T* p, const float* in) {
+    u32x4 v;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) v[d] = pack_bf16x2(in[2 * d], in[2 * d + 1]);
+    *reinterpret_cast<Raw*>(p) = v;
+  }
+};
+
+template <>
+struct Elem<false> {
+  using T = float;
+  static constexpr int kN = 4;
+  typedef f32x4 Raw __attribute__((aligned(4)));
+  __device__ static float get(const T* p) { return *p; }
+  __device__ static void put(T* p, float v) { *p = v; }
+  __device__ static void load(const T* p, float* out) {
+    const f32x4 v = *reinterpret_cast<const Raw*>(p);
+#pragma unroll
+    for (int d = 0; d < 4; ++d) out[d] = v[d];
+  }
+  __device__ static void store(T* p, const float* in) {
+    *reinterpret_cast<Raw*>(p) = f32x4{in[0], in[1], in[2], in[3]};
+  }
+};
+
+// Elements [j, j + kN) of a row of n, absent ones as `fill`.
+template <bool BF>
+__device__ __forceinline__ void load_part(const typename Elem<BF>::T* row, int64_t j, int64_t n,
+                                          float fill, float* out) {
+  using E = Elem<BF>;
+  if (j + E::kN <= n) {
+    E::load(row + j, out);
+  } else {
+#pragma unroll
+    for (int q = 0; q < E::kN; ++q) out[q] = j + q < n ? E::get(row + j + q) : fill;
+  }
+}
+
+template <bool BF>
+__device__ __forceinline__ void store_part(typename Elem<BF>::T* row, int64_t j, int64_t n,
+                                           const float* in) {
+  using E = Elem<BF>;
+  if (j + E::kN <= n) {
+    E::store(row + j, in);
+  } else {
+#pragma unroll
+    for (int q = 0; q < E::kN; ++q)
+      if (j + q < n) E::put(row + j + q, in[q]);
+  }
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
+  return v;
+}
+
+// Sums of N values over a workgroup of WAVES waves, in a fixed order; every
+// thread gets them.  `lds` holds WAVES * N floats; a barrier stands between two
+// uses of it.
+template <int WAVES, int N>
+__device__ __forceinline__ void block_sum(float* v, float* lds) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
+  if (WAVES == 1) return;
+  const int wave = threadIdx.x >> 6;
+  if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) lds[wave * N + i] = v[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    float s = lds[i];
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) s += lds[w * N + i];
+    v[i] = s;
+  }
+}
+
+}  // namespace dora

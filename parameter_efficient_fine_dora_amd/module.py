@@ -1,4 +1,5 @@
-"""DoRA and DVoRA linear layers on top of the C ABI (autograd glue only).
+"""DoRA and DVoRA linear layers, layer norm and token log probabilities on top of the C ABI
+(autograd glue only).
 
 Forward saves norm, xs = s (x A^T) and y for the backward; the norm is
 detached there (DoRA reading notes, Sec. 3.4).  DVoRA (Sec. 3.5) runs the same
@@ -123,3 +124,78 @@ class DVoRALinear(torch.nn.Module):
         y = DVoRAFunction.apply(x2, self.W0, self.A_shared, self.B_shared, self.b, self.d, self.m,
                                 self.s, self.flags)
         return y.reshape(*lead, y.shape[-1])
+
+
+class LayerNormFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, eps):
+        y, mean, rstd = ops.dora_layernorm(x, weight, bias, eps=eps)
+        ctx.save_for_backward(x, weight, mean, rstd)
+        return y
+
+    @staticmethod
+    def backward(ctx, gy):
+        x, weight, mean, rstd = ctx.saved_tensors
+        need = tuple(n for n, k in (("x", 0), ("weight", 1), ("bias", 2)) if ctx.needs_input_grad[k])
+        gx, gw, gb = ops.dora_layernorm_backward(gy.contiguous(), x, weight, mean, rstd, need=need)
+        return gx, gw, gb, None
+
+
+class LayerNorm(torch.nn.Module):
+    """y = weight (x - mean) / sqrt(var + eps) + bias over the last dimension of x.
+
+    weight and bias may be frozen (``requires_grad_(False)``): their gradients are then not formed.
+    """
+
+    def __init__(self, width: int, eps: float = 1e-5, bias: bool = True, device=None, dtype=None):
+        super().__init__()
+        self.weight = torch.nn.Parameter(torch.ones(width, device=device, dtype=dtype))
+        self.bias = torch.nn.Parameter(torch.zeros(width, device=device, dtype=dtype)) if bias else None
+        self.eps = float(eps)
+
+    def forward(self, x: torch.Tensor) -> torch.Tensor:
+        x2 = x.reshape(-1, x.shape[-1])
+        if x2.stride(-1) != 1:
+            x2 = x2.contiguous()
+        return LayerNormFunction.apply(x2, self.weight, self.bias, self.eps).reshape(x.shape)
+
+
+class TokenLogProbFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, targets, scale, top):
+        logp, entropy, lse, top_logp, top_index = ops.dora_token_logprob(logits, targets, scale=scale,
+                                                                         top=top)
+        ctx.scale = scale
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(logits, targets, lse, entropy)
+        if top:
+            ctx.mark_non_differentiable(top_logp, top_index)
+        return logp, entropy, top_logp, top_index
+
+    @staticmethod
+    def backward(ctx, g_logp, g_entropy, _g_top, _g_index):
+        if g_logp is None and g_entropy is None:
+            return None, None, None, None
+        logits, targets, lse, entropy = ctx.saved_tensors
+        g = [None if t is None else t.contiguous() for t in (g_logp, g_entropy)]
+        return ops.dora_token_logprob_backward(g[0], g[1], logits, targets, lse, entropy,
+                                               scale=ctx.scale), None, None, None
+
+
+def token_logprob(logits: torch.Tensor, targets: torch.Tensor, *, scale: float = 1.0, top: int = 0):
+    """Log probability of each target under softmax(scale * logits) and the entropy of that
+    distribution, differentiable in the logits; with ``top`` > 0 also the likeliest tokens.
+
+    logits [..., vocab], targets int64 [...].  Returns (logp, entropy, top_logp, top_index), the
+    first two float32 [...], the others [..., top] or None.  Targets outside [0, vocab) (-100, say)
+    give zeros and no gradient.
+    """
+    lead = targets.shape
+    z = logits.reshape(-1, logits.shape[-1])
+    if z.stride(-1) != 1:
+        z = z.contiguous()
+    logp, entropy, top_logp, top_index = TokenLogProbFunction.apply(z, targets.reshape(-1).contiguous(),
+                                                                    float(scale), int(top))
+    if top:
+        top_logp, top_index = top_logp.reshape(*lead, top), top_index.reshape(*lead, top)
+    return logp.reshape(lead), entropy.reshape(lead), top_logp, top_index

@@ -248,6 +248,304 @@ def dora_vera_grads(grad_B_eff, B_shared, b, d, *, need=("b", "d"), workspace=No
     return gb, gd
 
 
+def _rows(t, name, dtype=None, shape=None, dev=None):
+    """Checks a [rows, width] tensor whose rows are contiguous; returns its row stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device (HIP) tensor")
+    if dev is not None and t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, has {t.dim()}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if t.shape[0] <= 1:
+        return t.shape[1]
+    if t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name} must have rows that do not overlap")
+    return t.stride(0)
+
+
+def dora_layernorm(x, weight=None, bias=None, *, eps=1e-5, y=None, mean=None, rstd=None):
+    """Layer norm over the rows of x [rows, width] (rows contiguous, any row stride).
+
+    Returns (y, mean, rstd); mean and rstd are float32 [rows], for the backward.
+    """
+    ld = _rows(x, "x")
+    dev, dt = x.device, x.dtype
+    R, D = x.shape
+    code = _layer_dtype(x)
+    for t, nm in ((weight, "weight"), (bias, "bias")):
+        if t is not None:
+            _need(t, nm, dt, (D,), dev)
+    if y is None:
+        y = torch.empty(R, D, dtype=dt, device=dev)
+    if mean is None:
+        mean = torch.empty(R, dtype=torch.float32, device=dev)
+    if rstd is None:
+        rstd = torch.empty(R, dtype=torch.float32, device=dev)
+    _need(y, "y", dt, (R, D), dev)
+    _need(mean, "mean", torch.float32, (R,), dev)
+    _need(rstd, "rstd", torch.float32, (R,), dev)
+    sh = _lib.DoraLayernormShape(R, D, ld, ld, code, eps, 0, 0)
+    _check(_lib.lib().dora_layernorm_forward(ctypes.byref(sh), _ptr(x), _ptr(weight), _ptr(bias),
+                                             _ptr(y), _ptr(mean), _ptr(rstd), _stream(dev)),
+           "dora_layernorm_forward")
+    return y, mean, rstd
+
+
+def dora_layernorm_backward(grad_y, x, weight, mean, rstd, *, need=("x", "weight", "bias"),
+                            grad_x=None, grad_weight=None, grad_bias=None, workspace=None):
+    """Layer norm backward.  Returns (grad_x, grad_weight, grad_bias), layer dtype; entries not
+    in ``need`` are None."""
+    ld = _rows(x, "x")
+    dev, dt = x.device, x.dtype
+    R, D = x.shape
+    code = _layer_dtype(x)
+    ldg = _rows(grad_y, "grad_y", dt, (R, D), dev)
+    if weight is not None:
+        _need(weight, "weight", dt, (D,), dev)
+    _need(mean, "mean", torch.float32, (R,), dev)
+    _need(rstd, "rstd", torch.float32, (R,), dev)
+    if "x" in need and grad_x is None:
+        grad_x = torch.empty(R, D, dtype=dt, device=dev)
+    if "weight" in need and grad_weight is None:
+        grad_weight = torch.empty(D, dtype=dt, device=dev)
+    if "bias" in need and grad_bias is None:
+        grad_bias = torch.empty(D, dtype=dt, device=dev)
+    for t, nm, shp in ((grad_x, "grad_x", (R, D)), (grad_weight, "grad_weight", (D,)),
+                       (grad_bias, "grad_bias", (D,))):
+        if t is not None:
+            _need(t, nm, dt, shp, dev)
+    sh = _lib.DoraLayernormShape(R, D, ld, ldg, code, 0.0, 0, 0)
+    nb = 0
+    if grad_weight is not None or grad_bias is not None:
+        nb = _lib.lib().dora_layernorm_workspace_bytes(ctypes.byref(sh))
+        if workspace is None:
+            workspace = torch.empty(max(nb, 1), dtype=torch.uint8, device=dev)
+        nb = workspace.numel() * workspace.element_size()
+    _check(_lib.lib().dora_layernorm_backward(ctypes.byref(sh), _ptr(grad_y), _ptr(x), _ptr(weight),
+                                              _ptr(mean), _ptr(rstd), _ptr(grad_x),
+                                              _ptr(grad_weight), _ptr(grad_bias), _ptr(workspace),
+                                              nb, _stream(dev)), "dora_layernorm_backward")
+    return grad_x, grad_weight, grad_bias
+
+
+def dora_token_logprob(logits, targets, *, scale=1.0, top=0, workspace=None):
+    """Log probabilities of ``targets`` (int64 [rows]) under softmax(scale * logits) per row.
+
+    Returns (logp, entropy, lse, top_logp, top_index): float32 [rows] each, and, for top > 0, the
+    ``top`` likeliest tokens of each row, float32 and int64 [rows, top] (None for top = 0).  Rows
+    whose target lies outside [0, vocab) are skipped: zeros, and top_index -1.
+    """
+    ld = _rows(logits, "logits")
+    dev = logits.device
+    T, V = logits.shape
+    _need(targets, "targets", torch.int64, (T,), dev)
+    sh = _lib.DoraLogprobShape(T, V, ld, _layer_dtype(logits), int(top), float(scale), 0)
+    logp, entropy, lse = torch.empty(3, T, dtype=torch.float32, device=dev).unbind(0)
+    top_logp = top_index = None
+    if top > 0:
+        top_logp = torch.empty(T, top, dtype=torch.float32, device=dev)
+        top_index = torch.empty(T, top, dtype=torch.int64, device=dev)
+    nb = _lib.lib().dora_token_logprob_workspace_bytes(ctypes.byref(sh))
+    if nb and workspace is None:
+        workspace = torch.empty(nb, dtype=torch.uint8, device=dev)
+    if workspace is not None:
+        nb = workspace.numel() * workspace.element_size()
+    _check(_lib.lib().dora_token_logprob_forward(ctypes.byref(sh), _ptr(logits), _ptr(targets),
+                                                 _ptr(logp), _ptr(entropy), _ptr(lse),
+                                                 _ptr(top_logp), _ptr(top_index), _ptr(workspace),
+                                                 nb, _stream(dev)), "dora_token_logprob_forward")
+    return logp, entropy, lse, top_logp, top_index
+
+
+def dora_token_logprob_backward(grad_logp, grad_entropy, logits, targets, lse, entropy, *, scale=1.0,
+                                grad_logits=None):
+    """Gradient of dora_token_logprob's logp and entropy (either gradient may be None) with respect
+    to the logits, [rows, vocab] in their dtype; lse and entropy as it returned them."""
+    ld = _rows(logits, "logits")
+    dev = logits.device
+    T, V = logits.shape
+    _need(targets, "targets", torch.int64, (T,), dev)
+    for t, nm in ((grad_logp, "grad_logp"), (grad_entropy, "grad_entropy"), (entropy, "entropy")):
+        if t is not None:
+            _need(t, nm, torch.float32, (T,), dev)
+    _need(lse, "lse", torch.float32, (T,), dev)
+    if grad_logits is None:
+        grad_logits = torch.empty(T, V, dtype=logits.dtype, device=dev)
+    _need(grad_logits, "grad_logits", logits.dtype, (T, V), dev)
+    sh = _lib.DoraLogprobShape(T, V, ld, _layer_dtype(logits), 0, float(scale), 0)
+    _check(_lib.lib().dora_token_logprob_backward(ctypes.byref(sh), _ptr(grad_logp),
+                                                  _ptr(grad_entropy), _ptr(logits), _ptr(targets),
+                                                  _ptr(lse), _ptr(entropy), _ptr(grad_logits),
+                                                  _stream(dev)), "dora_token_logprob_backward")
+    return grad_logits
+
+
+class AdamWPlan:
+    """The tensors of an AdamW step, checked once and kept for the steps that follow.
+
+    params         contiguous tensors of one dtype (bf16 or float32) on one device
+    exp_avg, exp_avg_sq   the moments, one tensor per parameter: float32 of its size, or 8-bit codes
+                   (int8 and uint8) with ``exp_avg_scales`` / ``exp_avg_sq_scales``, float32
+                   [ceil(n / 128)] each
+    masters        float32 copies of bf16 parameters, or None
+
+    The plan refers to the tensors (they stay alive with it) and writes through them.  A parameter
+    whose storage was exchanged since (``p.data = ...``) is an error at the next step.
+    """
+
+    def __init__(self, params, exp_avg, exp_avg_sq, *, masters=None, exp_avg_scales=None,
+                 exp_avg_sq_scales=None):
+        params, exp_avg, exp_avg_sq = list(params), list(exp_avg), list(exp_avg_sq)
+        if not params:
+            raise ValueError("params is empty")
+        n = len(params)
+        small = exp_avg_scales is not None or exp_avg_sq_scales is not None
+        if small and (exp_avg_scales is None or exp_avg_sq_scales is None):
+            raise ValueError("8-bit states need exp_avg_scales and exp_avg_sq_scales")
+        sc1 = list(exp_avg_scales) if small else [None] * n
+        sc2 = list(exp_avg_sq_scales) if small else [None] * n
+        mst = list(masters) if masters is not None else [None] * n
+        for nm, lst in (("exp_avg", exp_avg), ("exp_avg_sq", exp_avg_sq), ("masters", mst),
+                        ("exp_avg_scales", sc1), ("exp_avg_sq_scales", sc2)):
+            if len(lst) != n:
+                raise ValueError(f"{nm} has {len(lst)} tensors, expected {n}")
+        _need(params[0], "params[0]")
+        dev, dt = params[0].device, params[0].dtype
+        self.param_code = _layer_dtype(params[0])
+        if masters is not None and dt != torch.bfloat16:
+            raise ValueError("masters go with bfloat16 params")
+        self.table = (_lib.DoraAdamwTensor * n)()
+        for i in range(n):
+            p = _need(params[i], f"params[{i}]", dt, None, dev)
+            k = p.numel()
+            one = torch.int8 if small else torch.float32
+            two = torch.uint8 if small else torch.float32
+            for t, nm, tdt, size in ((exp_avg[i], "exp_avg", one, k),
+                                     (exp_avg_sq[i], "exp_avg_sq", two, k),
+                                     (sc1[i], "exp_avg_scales", torch.float32, -(-k // _lib.STATE_BLOCK)),
+                                     (sc2[i], "exp_avg_sq_scales", torch.float32, -(-k // _lib.STATE_BLOCK)),
+                                     (mst[i], "masters", torch.float32, k)):
+                if t is None and ((nm == "masters" and masters is None)
+                                  or (nm.endswith("scales") and not small)):
+                    continue
+                _need(t, f"{nm}[{i}]", tdt, None, dev)
+                if t.numel() != size:
+                    raise ValueError(f"{nm}[{i}] has {t.numel()} elements, expected {size}")
+            e = self.table[i]
+            e.param, e.n = p.data_ptr(), k
+            e.exp_avg, e.exp_avg_sq = exp_avg[i].data_ptr(), exp_avg_sq[i].data_ptr()
+            if small:
+                e.exp_avg_scale, e.exp_avg_sq_scale = sc1[i].data_ptr(), sc2[i].data_ptr()
+            if masters is not None:
+                e.master = mst[i].data_ptr()
+        self.params, self.device, self.dtype = params, dev, dt
+        self.state_bits = 8 if small else 32
+        self._keep = (exp_avg, exp_avg_sq, sc1, sc2, mst)
+        self._at = [p.data_ptr() for p in params]
+        self._sizes = [p.numel() for p in params]
+
+    def _take_grads(self, grads):
+        """Checks the gradients and notes where they are; returns their dtype."""
+        if len(grads) != len(self.params):
+            raise ValueError(f"{len(grads)} gradients for {len(self.params)} params")
+        if [p.data_ptr() for p in self.params] != self._at:
+            raise ValueError("a parameter's storage has changed since the plan was made")
+        gdt = grads[0].dtype
+        if gdt not in _DT:
+            raise ValueError(f"unsupported dtype {gdt}; use float32 or bfloat16")
+        dev = self.device
+        for i, (g, k) in enumerate(zip(grads, self._sizes)):
+            if g.dtype is not gdt or g.device != dev or g.numel() != k or not g.is_contiguous():
+                _need(g, f"grads[{i}]", gdt, None, dev)
+                raise ValueError(f"grads[{i}] has {g.numel()} elements, expected {k}")
+            self.table[i].grad = g.data_ptr()
+        return gdt
+
+
+def dora_grad_norm(plan, grads, max_norm=1.0, *, workspace=None):
+    """Global norm of the gradients of a plan's params and the factor min(1, max_norm / (norm +
+    1e-6)) that clips them to ``max_norm``: two float32 scalars on the device."""
+    gdt = plan._take_grads(grads)
+    return _grad_norm(plan, gdt, max_norm, workspace)
+
+
+def _grad_norm(plan, gdt, max_norm, workspace):
+    L, n = _lib.lib(), len(plan.params)
+    nb = L.dora_grad_norm_workspace_bytes(plan.table, n)
+    if workspace is None:
+        workspace = torch.empty(max(nb, 1), dtype=torch.uint8, device=plan.device)
+    norm, factor = torch.empty(2, dtype=torch.float32, device=plan.device).unbind(0)
+    _check(L.dora_grad_norm(plan.table, n, _DT[gdt], float(max_norm), _ptr(norm), _ptr(factor),
+                            _ptr(workspace), workspace.numel() * workspace.element_size(),
+                            _stream(plan.device)), "dora_grad_norm")
+    return norm, factor
+
+
+def dora_adamw(plan, grads, *, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01,
+               max_norm=None, grad_scale=None, workspace=None):
+    """One AdamW step (``step`` counts from 1) on the tensors of a plan, in place.
+
+    ``grads``: one contiguous tensor per parameter, all bf16 or all float32.  With ``max_norm`` the
+    gradients are first clipped by their global norm, which is returned (a float32 scalar on the
+    device); ``grad_scale`` is a float32 scalar on the device to multiply them by instead.
+    """
+    if max_norm is not None and grad_scale is not None:
+        raise ValueError("max_norm and grad_scale exclude each other")
+    gdt = plan._take_grads(grads)
+    norm = None
+    if max_norm is not None:
+        norm, grad_scale = _grad_norm(plan, gdt, max_norm, workspace)
+    elif grad_scale is not None:
+        _need(grad_scale, "grad_scale", torch.float32, None, plan.device)
+    o = _lib.DoraAdamwOptions(plan.param_code, _DT[gdt], plan.state_bits, 0, int(step), float(lr),
+                              float(betas[0]), float(betas[1]), float(eps), float(weight_decay),
+                              _ptr(grad_scale))
+    _check(_lib.lib().dora_adamw_step(plan.table, len(plan.params), ctypes.byref(o),
+                                      _stream(plan.device)), "dora_adamw_step")
+    return norm
+
+
+def _second_moment(codes):
+    if codes.dtype not in (torch.int8, torch.uint8):
+        raise ValueError(f"codes have dtype {codes.dtype}, expected int8 (exp_avg) or uint8 (exp_avg_sq)")
+    return codes.dtype == torch.uint8
+
+
+def dora_adamw_dequantize(codes, scales, *, dtype=torch.float32):
+    """The values of 8-bit states: exp_avg of int8 codes, exp_avg_sq of uint8 codes."""
+    _need(codes, "codes")
+    second = _second_moment(codes)
+    n = codes.numel()
+    _need(scales, "scales", torch.float32, (-(-n // _lib.STATE_BLOCK),), codes.device)
+    if dtype not in _DT:
+        raise ValueError(f"unsupported dtype {dtype}; use float32 or bfloat16")
+    out = torch.empty(codes.shape, dtype=dtype, device=codes.device)
+    _check(_lib.lib().dora_adamw_dequantize(_ptr(codes), _ptr(scales), n, int(second), _ptr(out),
+                                            _DT[dtype], _stream(codes.device)),
+           "dora_adamw_dequantize")
+    return out
+
+
+def dora_adamw_quantize(values, *, second_moment):
+    """8-bit codes and scales of float32 moments: (int8, float32) of exp_avg, (uint8, float32) of
+    exp_avg_sq (``second_moment``)."""
+    _need(values, "values", torch.float32)
+    n, dev = values.numel(), values.device
+    codes = torch.empty(values.shape, dtype=torch.uint8 if second_moment else torch.int8, device=dev)
+    scales = torch.empty(-(-n // _lib.STATE_BLOCK), dtype=torch.float32, device=dev)
+    _check(_lib.lib().dora_adamw_quantize(_ptr(values), n, int(bool(second_moment)), _ptr(codes),
+                                          _ptr(scales), _stream(dev)), "dora_adamw_quantize")
+    return codes, scales
+
+
 def timing_enable(on: bool = True):
     _lib.lib().dora_timing_enable(1 if on else 0)
 

@@ -1,0 +1,351 @@
+"""The AdamW step over many tensors, its 8-bit states and the gradients' norm against float64.
+
+Bars.  u = 2^-24.  A moment is two products and a sum (and the clip factor, and (1 - beta) rounded
+to float32): 6 u of the sum of its terms' magnitudes.  A parameter is its decayed value and a
+quotient of a moment by a root, each with a few roundings of its own: 4 u |p| + 24 u |update|, plus
+half a last place of a bf16 parameter (up to 2^-8 relative).  Where cancellation makes a first moment
+small beside its terms, the update carries the terms' 6 u.  The norm is summed in float64 and
+rounded once: 2 u relative.  An 8-bit code is within half a step of the exact position of its
+value (0.5 + 255 * 16 u for the roundings on the way), its scale within 8 u."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import finetune as ref
+from tests.gpu_util import download
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+HYPER = dict(lr=1e-2, beta1=0.9, beta2=0.99, eps=1e-8, weight_decay=0.1)
+
+
+@pytest.fixture(scope="module")
+def ops():
+    assert torch.cuda.is_available(), "GPU tests need a HIP device"
+    from parameter_efficient_fine_dora_amd import ops as _ops, _lib
+    _lib.lib()
+    return _ops
+
+
+def say(*a):
+    print(*a, flush=True)
+
+
+def held(got, want, bar, what):
+    bad = ~(np.abs(got - want) <= bar)
+    assert not bad.any(), (what, int(bad.sum()), got[bad][:4], want[bad][:4])
+
+
+LENGTHS = [1, 2, 7, 8, 9, 127, 128, 129, 255, 1000, 4095, 4096, 4097, 8191, 12289, 70001]
+
+
+class Tensors:
+    """Tensors of the given lengths, `shift` elements into buffers with guards on both sides."""
+
+    def __init__(self, ops, lengths, pdt, gdt, bits, master, seed, shift=0):
+        self.ops, self.bits, self.lengths = ops, bits, lengths
+        rng = np.random.default_rng(seed)
+        self.guards = []
+
+        def put(a, dt):
+            a = torch.as_tensor(a).to(dt).cuda()
+            buf = torch.full((a.numel() + 2 * 16 + shift,), 77, dtype=dt, device="cuda")
+            buf[16 + shift:16 + shift + a.numel()] = a
+            self.guards.append((buf, 16 + shift, a.numel()))
+            return buf[16 + shift:16 + shift + a.numel()]
+
+        self.p, self.g, self.m, self.v, self.ms, self.vs, self.w = ([] for _ in range(7))
+        for n in lengths:
+            grad = rng.standard_normal(n) * 1e-2 * np.exp(rng.standard_normal(n))
+            w = rng.standard_normal(n).astype(np.float32)
+            m = (0.3 * grad + 1e-3 * rng.standard_normal(n)).astype(np.float32)
+            v = ((0.5 * grad) ** 2 + 1e-6 * rng.random(n)).astype(np.float32)
+            self.p.append(put(w, pdt))
+            self.g.append(put(grad, gdt))
+            if master:
+                self.w.append(put(w, torch.float32))
+            if bits == 8:
+                c, s = ops.dora_adamw_quantize(torch.from_numpy(m).cuda(), second_moment=False)
+                self.m.append(put(c.cpu(), torch.int8)), self.ms.append(put(s.cpu(), torch.float32))
+                c, s = ops.dora_adamw_quantize(torch.from_numpy(v).cuda(), second_moment=True)
+                self.v.append(put(c.cpu(), torch.uint8)), self.vs.append(put(s.cpu(), torch.float32))
+            else:
+                self.m.append(put(m, torch.float32)), self.v.append(put(v, torch.float32))
+        self.master = master
+
+    def plan(self):
+        return self.ops.AdamWPlan(self.p, self.m, self.v, masters=self.w if self.master else None,
+                                  exp_avg_scales=self.ms if self.bits == 8 else None,
+                                  exp_avg_sq_scales=self.vs if self.bits == 8 else None)
+
+    def state(self, i):
+        """(p, m, v) of tensor i in float64 as they stand."""
+        p = download(self.w[i] if self.master else self.p[i])
+        if self.bits == 32:
+            return p, download(self.m[i]), download(self.v[i])
+        m = ref.state_values(self.m[i].cpu().numpy(), self.ms[i].cpu().numpy())
+        r = ref.state_values(self.v[i].cpu().numpy(), self.vs[i].cpu().numpy())
+        return p, m, r ** 2
+
+    def guards_hold(self):
+        return all((b[:o] == 77).all() and (b[o + n:] == 77).all() for b, o, n in self.guards)
+
+
+def check_step(t, step, factor, **hyper):
+    """Takes a step through `t` and holds every tensor to the float64 step from the same state."""
+    before = [t.state(i) for i in range(len(t.lengths))]
+    yield
+    h = hyper
+    for i, n in enumerate(t.lengths):
+        p0, m0, v0 = before[i]
+        g = download(t.g[i])
+        p, m, v = ref.adamw(p0, g, m0, v0, step=step, factor=factor, **h)
+        mt = h["beta1"] * np.abs(m0) + (1 - h["beta1"]) * np.abs(g * factor)
+        denom = np.sqrt(v / (1 - h["beta2"] ** step)) + h["eps"]
+        per = h["lr"] / (1 - h["beta1"] ** step) / denom
+        bar = 4 * U * np.abs(p0) + 24 * U * per * np.abs(m) + 6 * U * per * mt
+        got = download(t.w[i] if t.master else t.p[i])
+        bf = t.p[i].dtype == torch.bfloat16
+        held(got, p, bar + (2.0 ** -8 * np.abs(p) if bf and not t.master else 0), ("param", n))
+        if t.master:
+            assert torch.equal(t.p[i], t.w[i].to(t.p[i].dtype)), "param is the master's rounding"
+        if t.bits == 32:
+            held(download(t.m[i]), m, 6 * U * mt, ("exp_avg", n))
+            held(download(t.v[i]), v, 8 * U * v + 1e-45, ("exp_avg_sq", n))
+            continue
+        for codes, scales, val, most in ((t.m[i], t.ms[i], m, 127), (t.v[i], t.vs[i], np.sqrt(v), 255)):
+            c, s = codes.cpu().numpy(), scales.cpu().numpy()
+            held(s.astype(np.float64), ref.state_scales(val), 8 * U * ref.state_scales(val)
+                 + (6 * U * ref.state_scales(mt) if most == 127 else 0), ("scale", n))
+            at = ref.state_positions(val, s, most)
+            if most == 255:
+                at = np.where(val > 0, np.maximum(at, 0.5), at)   # a nonzero one keeps code 1
+                assert (c[val > 0] >= 1).all()
+            # cancellation moves a small first moment by 6 u of its terms
+            move = 0.0
+            if most == 127:
+                wide = ref.state_positions(np.abs(val) + 6 * U * mt, s, most)
+                move = np.where(at > 0, wide - at, 0.0)
+            held(np.abs(c.astype(np.float64)), at, 0.5 + 255 * 16 * U + move, ("code", n))
+            if most == 127:
+                sign = (c != 0) & (at > 1)
+                assert (np.sign(c[sign]) == np.sign(val[sign])).all()
+    assert t.guards_hold()
+    yield
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("pdt,gdt,master", [("bf16", "bf16", False), ("bf16", "f32", False),
+                                            ("f32", "f32", False), ("f32", "bf16", False),
+                                            ("bf16", "bf16", True), ("bf16", "f32", True)])
+@pytest.mark.parametrize("shift", [0, 1])
+def test_step(ops, pdt, gdt, master, bits, shift):
+    say("adamw", pdt, gdt, master, bits, shift)
+    t = Tensors(ops, LENGTHS, DT[pdt], DT[gdt], bits, master, bits + shift, shift)
+    plan = t.plan()
+    for step in (1, 2, 1000):
+        c = check_step(t, step, 1.0, **HYPER)
+        next(c)
+        assert ops.dora_adamw(plan, t.g, step=step, lr=HYPER["lr"],
+                              betas=(HYPER["beta1"], HYPER["beta2"]), eps=HYPER["eps"],
+                              weight_decay=HYPER["weight_decay"]) is None
+        next(c)
+
+
+@pytest.mark.parametrize("gdt", ["bf16", "f32"])
+def test_clipped_by_the_global_norm(ops, gdt):
+    lengths = [5, 300, 40000, 1] * 60                      # more tensors than one launch takes
+    t = Tensors(ops, lengths, torch.float32, DT[gdt], 32, False, 3)
+    plan = t.plan()
+    for max_norm in (1e-3, 1e6):
+        norm, factor = ref.clip_factor([download(g) for g in t.g], max_norm)
+        c = check_step(t, 7, factor, **HYPER)
+        next(c)
+        got = ops.dora_adamw(plan, t.g, step=7, lr=HYPER["lr"], betas=(HYPER["beta1"], HYPER["beta2"]),
+                             eps=HYPER["eps"], weight_decay=HYPER["weight_decay"], max_norm=max_norm)
+        next(c)
+        assert abs(float(got) - norm) <= 2 * U * norm
+        n2, f2 = ops.dora_grad_norm(plan, t.g, max_norm)
+        assert n2 == got and abs(float(f2) - factor) <= 4 * U * factor
+    scaled = torch.tensor(0.25, device="cuda")
+    c = check_step(t, 8, 0.25, **HYPER)
+    next(c)
+    ops.dora_adamw(plan, t.g, step=8, lr=HYPER["lr"], betas=(HYPER["beta1"], HYPER["beta2"]),
+                   eps=HYPER["eps"], weight_decay=HYPER["weight_decay"], grad_scale=scaled)
+    next(c)
+
+
+def test_norm_of_extreme_gradients(ops):
+    p = [torch.zeros(9, device="cuda"), torch.zeros(70000, device="cuda")]
+    m, v = [torch.zeros_like(a) for a in p], [torch.zeros_like(a) for a in p]
+    plan = ops.AdamWPlan(p, m, v)
+    g = [torch.full((9,), 1e30, device="cuda"), torch.full((70000,), 1e30, device="cuda")]
+    norm, f = ops.dora_grad_norm(plan, g, 1.0)          # its square passes float32's range
+    want = 1e30 * np.sqrt(70009.0)
+    assert abs(float(norm) - want) <= 1e-6 * want and 0 < float(f) < 1e-31
+    zero = [torch.zeros_like(a) for a in p]
+    norm, f = ops.dora_grad_norm(plan, zero, 1.0)
+    assert norm == 0 and f == 1
+    g[0][3] = float("nan")
+    norm, f = ops.dora_grad_norm(plan, g, 1.0)
+    assert torch.isnan(norm) and torch.isnan(f)
+
+
+@pytest.mark.parametrize("n", [1, 100, 128, 129, 5000])
+def test_state_codes_and_values(ops, n):
+    rng = np.random.default_rng(n)
+    m = (rng.standard_normal(n) * np.exp(3 * rng.standard_normal(n))).astype(np.float32)
+    v = (m.astype(np.float64) ** 2).astype(np.float32)
+    if n > 4:
+        m[1], v[1] = 0.0, 0.0
+        v[2] = 1e-38
+    c, s = ops.dora_adamw_quantize(torch.from_numpy(m).cuda(), second_moment=False)
+    assert np.array_equal(s.cpu().numpy(), ref.state_scales(m).astype(np.float32))
+    at = ref.state_positions(m, s.cpu().numpy(), 127)
+    held(np.abs(c.cpu().numpy().astype(np.float64)), at, 0.5 + 255 * 16 * U, "codes")
+    back = download(ops.dora_adamw_dequantize(c, s))
+    held(back, ref.state_values(c.cpu().numpy(), s.cpu().numpy()), 8 * U * np.abs(back), "values")
+    assert (np.sign(back) * np.sign(m) >= 0).all()
+    c2, s2 = ops.dora_adamw_quantize(torch.from_numpy(v).cuda(), second_moment=True)
+    r = np.sqrt(v.astype(np.float64))
+    held(download(s2), ref.state_scales(r), 2 * U * ref.state_scales(r), "root scales")
+    assert ((c2.cpu().numpy() >= 1) == (v > 0)).all()
+    back2 = download(ops.dora_adamw_dequantize(c2, s2))
+    want = ref.state_values(c2.cpu().numpy(), s2.cpu().numpy()) ** 2
+    held(back2, want, 16 * U * want + 1e-45, "second moments")
+    bf = download(ops.dora_adamw_dequantize(c2, s2, dtype=torch.bfloat16))
+    held(bf, want, 2.0 ** -8 * want + 1e-40, "second moments in bf16")
+    # values that are codes already keep them
+    again, _ = ops.dora_adamw_quantize(torch.from_numpy(back.astype(np.float32)).cuda(),
+                                       second_moment=False)
+    assert torch.equal(again, c)
+
+
+def test_tiny_scales_zeros_and_lost_numbers(ops):
+    """Blocks of zeros, blocks whose scale is a denormal, and a NaN that stays in its block."""
+    n = 128 * 4
+    m = torch.zeros(n, device="cuda")
+    m[128:256] = 1e-41
+    m[130] = 4e-41
+    m[256:] = torch.randn(256, device="cuda")
+    c, s = ops.dora_adamw_quantize(m, second_moment=False)
+    assert (c[:128] == 0).all() and s[0] == 0 and c[130] == 127 and int(c[131]) in range(62, 66)
+    p, g = torch.randn(n, device="cuda"), torch.randn(n, device="cuda")
+    v, vs = ops.dora_adamw_quantize(torch.rand(n, device="cuda"), second_moment=True)
+    plan = ops.AdamWPlan([p], [c], [v], exp_avg_scales=[s], exp_avg_sq_scales=[vs])
+    g[300] = float("nan")
+    ops.dora_adamw(plan, [g], step=3, lr=1e-3)
+    keep = torch.ones(n, dtype=torch.bool, device="cuda")
+    keep[300] = False
+    assert torch.isnan(p[300]) and torch.isfinite(p[keep]).all()
+    value = ops.dora_adamw_dequantize(c, s)
+    assert torch.isnan(value[256:384]).all()
+    assert torch.isfinite(value[:256]).all() and torch.isfinite(value[384:]).all()
+
+
+def test_zero_gradients_and_states_leave_only_the_decay(ops):
+    p = torch.randn(1000, device="cuda")
+    want = p * np.float32(1 - 1e-2 * 0.1)
+    z = torch.zeros(1000, device="cuda")
+    c, s = ops.dora_adamw_quantize(z, second_moment=False)
+    c2, s2 = ops.dora_adamw_quantize(z, second_moment=True)
+    q = p.clone()
+    ops.dora_adamw(ops.AdamWPlan([p], [z.clone()], [z.clone()]), [z], step=1, lr=1e-2, weight_decay=0.1)
+    ops.dora_adamw(ops.AdamWPlan([q], [c], [c2], exp_avg_scales=[s], exp_avg_sq_scales=[s2]), [z],
+                   step=1, lr=1e-2, weight_decay=0.1)
+    assert torch.equal(p, want) and torch.equal(q, want)
+
+
+def test_8_bit_states_train_like_32_bit_ones(ops):
+    """200 steps on a least-squares problem whose columns differ in scale by 1e3."""
+    torch.manual_seed(0)
+    a = torch.randn(512, 256, device="cuda") * torch.logspace(-1.5, 1.5, 256, device="cuda")
+    y = a @ torch.randn(256, device="cuda")
+    loss = {}
+    for bits in (32, 8):
+        x = torch.zeros(256, device="cuda")
+        m, v = torch.zeros_like(x), torch.zeros_like(x)
+        if bits == 8:
+            (m, ms), (v, vs) = (ops.dora_adamw_quantize(m, second_moment=False),
+                                ops.dora_adamw_quantize(v, second_moment=True))
+            plan = ops.AdamWPlan([x], [m], [v], exp_avg_scales=[ms], exp_avg_sq_scales=[vs])
+        else:
+            plan = ops.AdamWPlan([x], [m], [v])
+        for step in range(1, 201):
+            ops.dora_adamw(plan, [a.t() @ (a @ x - y) / 512], step=step, lr=2e-2, weight_decay=0.0)
+        loss[bits] = float((a @ x - y).square().mean() / y.square().mean())
+    say("least squares after 200 steps", loss)
+    # both remove nearly everything; 8-bit moments (a few percent of a step's length) do not change that
+    assert loss[32] < 0.01 and loss[8] < max(2 * loss[32], 0.01)
+
+
+def test_refusals(ops):
+    p, s = torch.zeros(64, device="cuda"), torch.zeros(64, device="cuda")
+    plan = ops.AdamWPlan([p], [s], [s.clone()])
+    with pytest.raises(ValueError, match="1 params"):
+        ops.dora_adamw(plan, [s, s], step=1, lr=1e-3)
+    with pytest.raises(ValueError, match=r"grads\[0\] has 63 elements"):
+        ops.dora_adamw(plan, [s[:63]], step=1, lr=1e-3)
+    with pytest.raises(ValueError, match="contiguous"):
+        ops.dora_adamw(plan, [torch.zeros(128, device="cuda")[::2]], step=1, lr=1e-3)
+    with pytest.raises(ValueError, match="exclude"):
+        ops.dora_adamw(plan, [s], step=1, lr=1e-3, max_norm=1.0, grad_scale=s[:1])
+    for kw in (dict(step=0), dict(step=1, betas=(1.0, 0.9)), dict(step=1, eps=-1.0)):
+        with pytest.raises(ops.DoraError, match="DORA_ERR_FLAGS"):
+            ops.dora_adamw(plan, [s], lr=1e-3, **kw)
+    with pytest.raises(ops.DoraError, match="DORA_ERR_WORKSPACE"):
+        ops.dora_adamw(plan, [s], step=1, lr=1e-3, max_norm=1.0,
+                       workspace=torch.empty(4, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError, match="go with bfloat16"):
+        ops.AdamWPlan([p], [s], [s], masters=[s])
+    with pytest.raises(ValueError, match="expected 64"):
+        ops.AdamWPlan([p], [s[:3]], [s])
+    with pytest.raises(ValueError, match="8-bit states need"):
+        ops.AdamWPlan([p], [s.char()], [s.byte()], exp_avg_scales=[s])
+    p.data = torch.ones(64, device="cuda")
+    with pytest.raises(ValueError, match="storage has changed"):
+        ops.dora_adamw(plan, [s], step=1, lr=1e-3)
+
+
+def test_side_stream_and_graph(ops):
+    def fresh():
+        return Tensors(ops, [500, 4097, 33], torch.bfloat16, torch.bfloat16, 8, True, 9)
+
+    def step(t, plan):
+        return ops.dora_adamw(plan, t.g, step=4, lr=1e-3, max_norm=0.1)
+
+    def bits(t):
+        return [x.clone() for lst in (t.p, t.w, t.m, t.v, t.ms, t.vs) for x in lst]
+
+    a = fresh()
+    plan = a.plan()
+    start = bits(a)
+    want = []
+    for _ in range(3):
+        step(a, plan)
+        want.append(bits(a))
+    b = fresh()
+    plan_b = b.plan()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(b, plan_b)
+    side.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(bits(b), want[0]))
+    c = fresh()
+    plan_c = c.plan()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(c, plan_c)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(bits(c), start))   # capture runs nothing
+    for k in range(3):
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(bits(c), want[k]))
+        d = fresh()
+        step(d, d.plan())
+        assert all(torch.equal(x, y) for x, y in zip(bits(d), want[0]))

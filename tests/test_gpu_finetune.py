@@ -1,0 +1,172 @@
+"""The operators together: the autograd layers against torch's own on the CPU in float64, the
+optimizer's groups, clipping and checkpoints, and the fine-tuning example."""
+from __future__ import annotations
+
+import copy
+import importlib.util
+import os
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module")
+def pkg():
+    assert torch.cuda.is_available(), "GPU tests need a HIP device"
+    from parameter_efficient_fine_dora_amd import _lib, module, optim
+    _lib.lib()
+    return module, optim
+
+
+def close(a, b, tol):
+    a, b = a.detach().double().cpu(), b.detach().double().cpu()
+    assert a.shape == b.shape
+    assert float((a - b).abs().max()) <= tol * max(1.0, float(b.abs().max()))
+
+
+def test_layer_norm_and_log_probabilities_through_autograd(pkg):
+    """float32 on the GPU against float64 on the CPU: chains of a few hundred float32 roundings."""
+    module, _ = pkg
+    torch.manual_seed(1)
+    x = torch.randn(2, 5, 96, device="cuda").transpose(0, 1).requires_grad_()      # strided leaf
+    norm = module.LayerNorm(96, device="cuda")
+    with torch.no_grad():
+        norm.weight.normal_(1.0, 0.2)
+        norm.bias.normal_()
+    w = torch.randn(301, 96, device="cuda")
+    y = torch.randint(301, (5, 2), device="cuda")
+    y[0, 1] = -100
+    logp, H, best, index = module.token_logprob(norm(x) @ w.t(), y, scale=0.8, top=4)
+    (2.0 * logp.sum() - 0.3 * (H * H).sum()).backward()
+
+    xr = x.detach().double().cpu().requires_grad_()
+    wr, br = (t.detach().double().cpu().requires_grad_() for t in (norm.weight, norm.bias))
+    z = torch.nn.functional.layer_norm(xr, (96,), wr, br) @ w.double().cpu().t() * 0.8
+    lp = z.log_softmax(-1)
+    live = (y >= 0).cpu()
+    lpr = torch.where(live, lp.gather(-1, y.clamp(min=0).cpu()[..., None])[..., 0], 0.0)
+    Hr = torch.where(live, -(lp.exp() * lp).sum(-1), 0.0)
+    (2.0 * lpr.sum() - 0.3 * (Hr * Hr).sum()).backward()
+    close(logp, lpr, 1e-4)
+    close(H, Hr, 1e-4)
+    close(x.grad, xr.grad, 1e-4)
+    close(norm.weight.grad, wr.grad, 1e-4)
+    close(norm.bias.grad, br.grad, 1e-4)
+    assert best.shape == index.shape == (5, 2, 4) and (index[0, 1] == -1).all()
+    close(best[live.cuda()], lp.topk(4, -1).values[live], 1e-4)
+
+
+def test_only_the_used_outputs_gradients(pkg):
+    module, _ = pkg
+    z = torch.randn(6, 40, device="cuda", requires_grad=True)
+    y = torch.arange(6, device="cuda")
+    logp, H, _, _ = module.token_logprob(z, y)
+    H.sum().backward()
+    close(z.grad.sum(1), torch.zeros(6), 1e-6)
+    norm = module.LayerNorm(40, device="cuda").requires_grad_(False)
+    x = torch.randn(6, 40, device="cuda", requires_grad=True)
+    norm(x).sum().backward()
+    assert norm.weight.grad is None and norm.bias.grad is None and x.grad is not None
+
+
+def _models(n, dtype):
+    torch.manual_seed(2)
+    first = torch.nn.ParameterList([torch.nn.Parameter(torch.randn(k, 3, device="cuda").to(dtype))
+                                    for k in (1, 40, 700)])
+    return [copy.deepcopy(first) for _ in range(n)]
+
+
+def test_optimizer_follows_torch(pkg):
+    """Groups, a parameter that joins late, clipping: float32 against torch's AdamW on the CPU in
+    float64; steps of 1e-2, so 5e-6 is a few float32 roundings of each parameter and update."""
+    _, optim = pkg
+    a, b = _models(2, torch.float32)
+    b = [torch.nn.Parameter(p.detach().double().cpu()) for p in b]
+
+    def groups(ps):
+        return [dict(params=[ps[0], ps[2]]), dict(params=[ps[1]], lr=1e-3, weight_decay=0.0)]
+
+    oa = optim.AdamW(groups(list(a)), lr=1e-2, weight_decay=0.1, max_norm=0.7)
+    ob = torch.optim.AdamW(groups(b), lr=1e-2, weight_decay=0.1)
+    for step in range(6):
+        for i, (p, q) in enumerate(zip(a, b)):
+            if i == 2 and step < 2:
+                continue
+            g = torch.randn(p.shape, generator=torch.Generator().manual_seed(10 * step + i))
+            p.grad, q.grad = g.cuda(), g.double()
+        norm = torch.nn.utils.clip_grad_norm_(b, 0.7)
+        oa.step()
+        ob.step()
+        assert abs(float(oa.grad_norm) - float(norm)) <= 1e-6 * float(norm)
+        for p, q in zip(a, b):
+            close(p, q, 5e-6)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_checkpoint_resumes_bit_for_bit(pkg, bits):
+    _, optim = pkg
+    a, b = _models(2, torch.bfloat16)
+
+    def grads(ps, step):
+        for i, p in enumerate(ps):
+            g = torch.randn(p.shape, generator=torch.Generator().manual_seed(10 * step + i))
+            p.grad = g.cuda().to(p.dtype)
+
+    oa = optim.AdamW(a.parameters(), lr=1e-2, state_bits=bits, master=True)
+    for step in range(4):
+        grads(a, step)
+        oa.step()
+        if step == 1:
+            saved, weights = copy.deepcopy(oa.state_dict()), copy.deepcopy(a.state_dict())
+    b.load_state_dict(weights)
+    ob = optim.AdamW(b.parameters(), lr=1e-2, state_bits=bits, master=True)
+    ob.load_state_dict(saved)
+    s = ob.state[b[1]]
+    assert s["exp_avg"].dtype == (torch.int8 if bits == 8 else torch.float32)
+    assert s["master"].dtype == torch.float32
+    for step in (2, 3):
+        grads(b, step)
+        ob.step()
+    for p, q in zip(a, b):
+        assert torch.equal(p, q)
+        for k, v in oa.state[p].items():
+            assert v == ob.state[q][k] if k == "step" else torch.equal(v, ob.state[q][k])
+
+
+def test_new_storage_and_mixed_types(pkg):
+    _, optim = pkg
+    a, b = _models(2, torch.float32)
+    oa, ob = (optim.AdamW(m.parameters(), lr=1e-2) for m in (a, b))
+    for step in range(3):
+        for p, q in zip(a, b):
+            p.grad = torch.ones_like(p)
+            q.grad = torch.ones_like(q)
+        if step == 1:
+            a[1].data = a[1].data.clone()       # the plan is made anew
+        oa.step()
+        ob.step()
+    assert all(torch.equal(p, q) for p, q in zip(a, b))
+    mixed = [torch.nn.Parameter(torch.zeros(4, device="cuda")),
+             torch.nn.Parameter(torch.zeros(4, device="cuda").bfloat16())]
+    for p in mixed:
+        p.grad = torch.ones_like(p)
+    optim.AdamW(mixed, lr=1e-2).step()
+    assert all((p < 0).all() for p in mixed)
+    with pytest.raises(ValueError, match="one dtype"):
+        optim.AdamW(mixed, lr=1e-2, max_norm=1.0).step()
+    with pytest.raises(ValueError, match="state_bits"):
+        optim.AdamW(mixed, state_bits=16)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_example_learns(pkg, bits):
+    spec = importlib.util.spec_from_file_location("finetune", os.path.join(ROOT, "examples", "finetune.py"))
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    model, successor, losses = ex.train(steps=60, state_bits=bits)
+    assert losses[-1] < 0.5 * losses[0], losses[::10]
+    logp, entropy, best = ex.serve(model, successor, 3)
+    assert len(best) == 5 and best[0][1] >= best[1][1] and entropy > 0
