@@ -281,7 +281,7 @@ DORA_API int dora_layernorm_backward(const dora_layernorm_shape* shape, const vo
 #define DORA_LOGPROB_MAX_TOP 64
 typedef struct {
     int64_t  rows;      /* 0 <= rows < 2^31                                          */
-    int64_t  vocab;     /* 1 <= vocab < 2^31                                         */
+    int64_t  vocab;     /* 1 <= vocab <= 2^24                                        */
     int64_t  ld;        /* row stride of the logits in elements, vocab <= ld < 2^31  */
     int32_t  dtype;     /* dora_dtype of logits and grad_logits                      */
     int32_t  top;       /* alternatives per row, 0 <= top <= min(vocab, 64)          */
