@@ -14,40 +14,44 @@ template <>
 struct Elem<true> {
   using T = uint16_t;
   static constexpr int kN = 8;
-  typedef u32x4 Raw __attribute__((aligned(2)));
+  using Vec = u32x4;
+  typedef Vec Raw __attribute__((aligned(2)));
   __device__ static float get(const T* p) { return bf16_to_f32(*p); }
   __device__ static void put(T* p, float v) { *p = f32_to_bf16(v); }
-  __device__ static void load(const T* p, float* out) {
-    const u32x4 v = *reinterpret_cast<const Raw*>(p);
+  __device__ static Vec raw(const T* p) { return *reinterpret_cast<const Raw*>(p); }
+  __device__ static void decode(const Vec& v, float* out) {
 #pragma unroll
     for (int d = 0; d < 4; ++d) {
       out[2 * d] = bf_lo(v[d]);
       out[2 * d + 1] = bf_hi(v[d]);
     }
   }
-  __device__ static void store(T* p, const float* in) {
-    u32x4 v;
+  __device__ static void load(const T* p, float* out) { decode(raw(p), out); }
+  __device__ static Vec encode(const float* in) {
+    Vec v;
 #pragma unroll
     for (int d = 0; d < 4; ++d) v[d] = pack_bf16x2(in[2 * d], in[2 * d + 1]);
-    *reinterpret_cast<Raw*>(p) = v;
+    return v;
   }
+  __device__ static void store(T* p, const float* in) { *reinterpret_cast<Raw*>(p) = encode(in); }
 };
 
 template <>
 struct Elem<false> {
   using T = float;
   static constexpr int kN = 4;
-  typedef f32x4 Raw __attribute__((aligned(4)));
+  using Vec = f32x4;
+  typedef Vec Raw __attribute__((aligned(4)));
   __device__ static float get(const T* p) { return *p; }
   __device__ static void put(T* p, float v) { *p = v; }
-  __device__ static void load(const T* p, float* out) {
-    const f32x4 v = *reinterpret_cast<const Raw*>(p);
+  __device__ static Vec raw(const T* p) { return *reinterpret_cast<const Raw*>(p); }
+  __device__ static void decode(const Vec& v, float* out) {
 #pragma unroll
     for (int d = 0; d < 4; ++d) out[d] = v[d];
   }
-  __device__ static void store(T* p, const float* in) {
-    *reinterpret_cast<Raw*>(p) = f32x4{in[0], in[1], in[2], in[3]};
-  }
+  __device__ static void load(const T* p, float* out) { decode(raw(p), out); }
+  __device__ static Vec encode(const float* in) { return Vec{in[0], in[1], in[2], in[3]}; }
+  __device__ static void store(T* p, const float* in) { *reinterpret_cast<Raw*>(p) = encode(in); }
 };
 
 // Elements [j, j + kN) of a row of n, absent ones as `fill`.
