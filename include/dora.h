@@ -269,8 +269,8 @@ DORA_API int dora_layernorm_forward(const dora_layernorm_shape* shape, const voi
  *   grad_weight = sum_t grad_y xhat,  grad_bias = sum_t grad_y
  *   grad_x [rows, width] contiguous, grad_weight, grad_bias [width], layer
  *   dtype; each may be NULL to skip it.
- *   ws  workspace of dora_layernorm_workspace_bytes(shape), needed for
- *       grad_weight and grad_bias (may be NULL without them)
+ *   ws  workspace of dora_layernorm_workspace_bytes(shape); may be NULL for
+ *       grad_x alone where width <= 8192
  */
 DORA_API int dora_layernorm_backward(const dora_layernorm_shape* shape, const void* grad_y,
                                      const void* x, const void* weight, const float* mean,

@@ -80,24 +80,37 @@ __device__ __forceinline__ void store_part(typename Elem<BF>::T* row, int64_t j,
   }
 }
 
+// Sum over a wave to every lane, in a fixed order: neighbours inside rows of 16
+// lanes through DPP, then the four rows.  (Shuffles through LDS take several
+// times as long, and the row reductions stand between a row's load and its
+// store.)
+template <int CTRL>
+__device__ __forceinline__ float dpp_move(float v) {
+  return __int_as_float(
+      __builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float lane_value(float v, int lane) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
+}
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
-  return v;
+  v += dpp_move<0xB1>(v);    // quad_perm 1,0,3,2
+  v += dpp_move<0x4E>(v);    // quad_perm 2,3,0,1
+  v += dpp_move<0x141>(v);   // row_half_mirror: the other quad of eight lanes
+  v += dpp_move<0x140>(v);   // row_mirror: the other half of sixteen
+  return (lane_value(v, 0) + lane_value(v, 16)) + (lane_value(v, 32) + lane_value(v, 48));
 }
 
-// Sums of N values over a workgroup of WAVES waves, in a fixed order; every
-// thread gets them.  `lds` holds WAVES * N floats; a barrier stands between two
-// uses of it.
+// Sums of N values over WAVES waves, in a fixed order, to every thread of them;
+// `t` is the thread's number among them.  `lds` holds WAVES * N floats; a barrier
+// of the whole workgroup stands between two uses of it.
 template <int WAVES, int N>
-__device__ __forceinline__ void block_sum(float* v, float* lds) {
+__device__ __forceinline__ void group_sum(float* v, float* lds, int t) {
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
   if (WAVES == 1) return;
-  const int wave = threadIdx.x >> 6;
-  if ((threadIdx.x & 63) == 0) {
+  if ((t & 63) == 0) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) lds[wave * N + i] = v[i];
+    for (int i = 0; i < N; ++i) lds[(t >> 6) * N + i] = v[i];
   }
   __syncthreads();
 #pragma unroll
@@ -107,6 +120,11 @@ __device__ __forceinline__ void block_sum(float* v, float* lds) {
     for (int w = 1; w < WAVES; ++w) s += lds[w * N + i];
     v[i] = s;
   }
+}
+// The same over a whole workgroup.
+template <int WAVES, int N>
+__device__ __forceinline__ void block_sum(float* v, float* lds) {
+  group_sum<WAVES, N>(v, lds, threadIdx.x);
 }
 
 }  // namespace dora

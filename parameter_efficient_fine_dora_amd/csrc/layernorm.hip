@@ -33,39 +33,43 @@ struct Share {
   using E = Elem<BF>;
   using T = typename E::T;
   typename E::Vec v[NV];
-  float t;
+  T tail;   // undecoded too: a use right after its load would wait for every load
   // 32-bit offsets from a row's address, which all threads share
-  __device__ static uint32_t at(int u) { return ((uint32_t)u * THREADS + threadIdx.x) * E::kN; }
+  __device__ static uint32_t lane() { return threadIdx.x % THREADS; }
+  __device__ static uint32_t at(int u) { return ((uint32_t)u * THREADS + lane()) * E::kN; }
   __device__ static uint32_t body(uint32_t D) { return D & ~(uint32_t)(E::kN - 1); }
   __device__ static bool has(int u, uint32_t D) { return at(u) < body(D); }
-  __device__ static bool has_tail(uint32_t D) { return threadIdx.x < D - body(D); }
+  __device__ static bool has_tail(uint32_t D) { return lane() < D - body(D); }
   __device__ void load(const T* row, uint32_t D) {
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
       v[u] = typename E::Vec{0, 0, 0, 0};
       if (has(u, D)) v[u] = E::raw(row + at(u));
     }
-    t = has_tail(D) ? E::get(row + body(D) + threadIdx.x) : 0.f;
+    tail = 0;
+    if (has_tail(D)) tail = row[body(D) + lane()];
   }
-  // The second use of a share decodes it anew instead of keeping its decoded
-  // elements across a barrier.
-  __device__ void forget() {
+  // Vector u decoded, not before `after` is known: the second use of a share does
+  // not keep its decoded elements from the first, and one vector's elements are
+  // decoded at a time.
+  __device__ void decode(int u, float* out, float& after) {
+    typename E::Vec r = v[u];
 #pragma unroll
-    for (int u = 0; u < NV; ++u)
-#pragma unroll
-      for (int d = 0; d < 4; ++d) {
-        auto r = v[u][d];
-        asm volatile("" : "+v"(r));
-        v[u][d] = r;
-      }
+    for (int d = 0; d < 4; ++d) {
+      auto e = r[d];
+      asm volatile("" : "+v"(e), "+v"(after));
+      r[d] = e;
+    }
+    E::decode(r, out);
   }
+  __device__ float t() const { return E::get(&tail); }
   __device__ void fill(float one) {   // every element that value (1 or 0)
     float f[E::kN];
 #pragma unroll
     for (int q = 0; q < E::kN; ++q) f[q] = one;
 #pragma unroll
     for (int u = 0; u < NV; ++u) v[u] = E::encode(f);
-    t = one;
+    E::put(&tail, one);
   }
 };
 
@@ -90,22 +94,21 @@ __global__ __launch_bounds__(THREADS) void dora_layernorm_fwd(
       b.load(reinterpret_cast<const T*>(b_), D);
     else
       b.fill(0.f);
-    float sum = x.t;   // absent elements are 0
+    float sum = x.t();   // absent elements are 0
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
       float v[E::kN];
-      E::decode(x.v[u], v);
+      x.decode(u, v, sum);
 #pragma unroll
       for (int q = 0; q < E::kN; ++q) sum += v[q];
     }
     block_sum<kWaves, 1>(&sum, lds[0]);
-    const float mean = sum / (float)D;
-    x.forget();
-    float sq = S::has_tail(D) ? (x.t - mean) * (x.t - mean) : 0.f;
+    float mean = sum / (float)D;
+    float sq = S::has_tail(D) ? (x.t() - mean) * (x.t() - mean) : 0.f;
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
       float v[E::kN];
-      E::decode(x.v[u], v);
+      x.decode(u, v, sq);
       if (S::has(u, D)) {
 #pragma unroll
         for (int q = 0; q < E::kN; ++q) sq = fmaf(v[q] - mean, v[q] - mean, sq);
@@ -117,75 +120,87 @@ __global__ __launch_bounds__(THREADS) void dora_layernorm_fwd(
       if (mean_out) mean_out[row] = mean;
       if (rstd_out) rstd_out[row] = rstd;
     }
-    x.forget();
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
       float v[E::kN], wv[E::kN], bv[E::kN];
-      E::decode(x.v[u], v);
-      E::decode(w.v[u], wv);
-      E::decode(b.v[u], bv);
+      x.decode(u, v, mean);
+      w.decode(u, wv, mean);
+      b.decode(u, bv, mean);
 #pragma unroll
       for (int q = 0; q < E::kN; ++q) v[q] = fmaf((v[q] - mean) * rstd, wv[q], bv[q]);
       if (S::has(u, D)) E::store(y + S::at(u), v);
     }
     if (S::has_tail(D))
-      E::put(y + S::body(D) + threadIdx.x, fmaf((x.t - mean) * rstd, w.t, b.t));
+      E::put(y + S::body(D) + S::lane(), fmaf((x.t() - mean) * rstd, w.t(), b.t()));
   }
 }
 
-// grad_x, and with W the workgroup's share of grad_weight and grad_bias: its
-// rows are blockIdx.x, blockIdx.x + gridDim.x, ...; every thread keeps the sums
-// of its own columns in registers and writes them at the end as
+// grad_x, and with W the workgroup's share of grad_weight and grad_bias.  A
+// workgroup of 512 threads holds R rows at a time, THREADS threads to a row;
+// every thread keeps the sums of its own columns in registers over all its
+// rows, and at the end the R rows' threads add theirs through LDS:
 // part[blockIdx.x][0 or 1][column].  The next row is loaded before this row's
-// reduction, where registers allow (1024 threads have 128 each).
+// reduction where registers allow.
+constexpr int kBwdThreads = 512;
 template <bool BF, int THREADS, int NV, bool W>
-__global__ __launch_bounds__(THREADS) void dora_layernorm_bwd(
+__global__ __launch_bounds__(kBwdThreads) void dora_layernorm_bwd(
     const void* gy_, int64_t ldg, const void* x_, int64_t ldx, const void* w_, const float* mean_in,
     const float* rstd_in, void* gx_, float* part, int64_t rows, uint32_t D) {
   using E = Elem<BF>;
   using T = typename E::T;
   using S = Share<BF, THREADS, NV>;
+  constexpr int R = kBwdThreads / THREADS;
   constexpr int kWaves = THREADS / 64;
-  constexpr bool kAhead = THREADS < 1024 || 5 * 4 * NV + (W ? 2 * NV * E::kN : 0) <= 96;
-  __shared__ float lds[2][2 * kWaves];
+  // 256 registers per thread: the shares in flight and the sums
+  constexpr bool kAhead = 5 * 4 * NV + (W ? 2 * NV * E::kN : 0) <= 160;
+  __shared__ float lds[2][R][2 * kWaves];
+  __shared__ __align__(16) float comb[W && R > 1 ? R : 1][W && R > 1 ? THREADS * NV * E::kN : 4];
+  const int sub = __builtin_amdgcn_readfirstlane((int)threadIdx.x / THREADS);   // per wave
   S w, g, x, g_next, x_next;
   float mean_next = 0.f, rstd_next = 0.f;
   float gw[NV * E::kN], gb[NV * E::kN], gw_t = 0.f, gb_t = 0.f;
 #pragma unroll
   for (int i = 0; i < NV * E::kN; ++i) gw[i] = gb[i] = 0.f;
+  const int64_t stride = (int64_t)gridDim.x * R;
+  // rows past the last load as zeros, which add nothing
   auto fetch = [&](int64_t row) {
-    g_next.load(reinterpret_cast<const T*>(gy_) + row * ldg, D);
-    x_next.load(reinterpret_cast<const T*>(x_) + row * ldx, D);
-    mean_next = mean_in[row];
-    rstd_next = rstd_in[row];
+    const bool valid = row < rows;
+    const int64_t at = valid ? row : 0;
+    const uint32_t n = valid ? D : 0;
+    g_next.load(reinterpret_cast<const T*>(gy_) + at * ldg, n);
+    x_next.load(reinterpret_cast<const T*>(x_) + at * ldx, n);
+    mean_next = valid ? mean_in[row] : 0.f;
+    rstd_next = valid ? rstd_in[row] : 0.f;
   };
-  if (kAhead && blockIdx.x < rows) fetch(blockIdx.x);
+  int64_t row = (int64_t)blockIdx.x * R + sub;
+  if (kAhead) fetch(row);
   if (w_)
     w.load(reinterpret_cast<const T*>(w_), D);
   else
     w.fill(1.f);
   int buf = 0;
-  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, buf ^= 1) {
-    w.forget();
+  // every thread of the workgroup takes the same number of turns
+  for (int64_t first = (int64_t)blockIdx.x * R; first < rows;
+       first += stride, row += stride, buf ^= 1) {
     if (!kAhead) fetch(row);
     const float mean = mean_next, rstd = rstd_next;
     g = g_next;
     x = x_next;
-    if (kAhead && row + gridDim.x < rows) fetch(row + gridDim.x);
+    if (kAhead && first + stride < rows) fetch(row + stride);
     float s[2];   // absent elements have gy = 0
     {
-      const float n = (x.t - mean) * rstd, h = g.t * w.t;
-      gw_t = fmaf(g.t, n, gw_t);
-      gb_t += g.t;
+      const float n = (x.t() - mean) * rstd, h = g.t() * w.t();
+      gw_t = fmaf(g.t(), n, gw_t);
+      gb_t += g.t();
       s[0] = h;
       s[1] = h * n;
     }
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
       float gv[E::kN], xv[E::kN], wv[E::kN];
-      E::decode(g.v[u], gv);
-      E::decode(x.v[u], xv);
-      E::decode(w.v[u], wv);
+      g.decode(u, gv, s[0]);
+      x.decode(u, xv, s[0]);
+      w.decode(u, wv, s[0]);
 #pragma unroll
       for (int q = 0; q < E::kN; ++q) {
         const float n = (xv[q] - mean) * rstd, h = gv[q] * wv[q];
@@ -198,42 +213,52 @@ __global__ __launch_bounds__(THREADS) void dora_layernorm_bwd(
       }
     }
     if (!gx_) continue;
-    block_sum<kWaves, 2>(s, lds[buf]);
-    const float c1 = s[0] / (float)D, c2 = s[1] / (float)D;
+    group_sum<kWaves, 2>(s, lds[buf][sub], threadIdx.x % THREADS);
+    if (row >= rows) continue;
+    const float c2 = s[1] / (float)D;
+    float c1 = s[0] / (float)D;
     T* gx = reinterpret_cast<T*>(gx_) + row * D;
-    w.forget();
-    g.forget();
-    x.forget();
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
       float gv[E::kN], xv[E::kN], wv[E::kN];
-      E::decode(g.v[u], gv);
-      E::decode(x.v[u], xv);
-      E::decode(w.v[u], wv);
+      g.decode(u, gv, c1);
+      x.decode(u, xv, c1);
+      w.decode(u, wv, c1);
 #pragma unroll
       for (int q = 0; q < E::kN; ++q)
         gv[q] = rstd * (gv[q] * wv[q] - fmaf((xv[q] - mean) * rstd, c2, c1));
       if (S::has(u, D)) E::store(gx + S::at(u), gv);
     }
     if (S::has_tail(D))
-      E::put(gx + S::body(D) + threadIdx.x,
-             rstd * (g.t * w.t - fmaf((x.t - mean) * rstd, c2, c1)));
+      E::put(gx + S::body(D) + S::lane(), rstd * (g.t() * w.t() - fmaf((x.t() - mean) * rstd, c2, c1)));
   }
-  if (W) {
-    float* dst = part + (int64_t)blockIdx.x * 2 * (int64_t)D;
+  if (!W) return;
+  float* dst = part + (int64_t)blockIdx.x * 2 * (int64_t)D;
+  auto put = [&](float* to, const float* v, float t) {
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
       if (!S::has(u, D)) continue;
 #pragma unroll
-      for (int q = 0; q < E::kN; q += 4) {
-        Elem<false>::store(dst + S::at(u) + q, gw + u * E::kN + q);
-        Elem<false>::store(dst + D + S::at(u) + q, gb + u * E::kN + q);
-      }
+      for (int q = 0; q < E::kN; q += 4) Elem<false>::store(to + S::at(u) + q, v + u * E::kN + q);
     }
-    if (S::has_tail(D)) {
-      dst[S::body(D) + threadIdx.x] = gw_t;
-      dst[D + S::body(D) + threadIdx.x] = gb_t;
+    if (S::has_tail(D)) to[S::body(D) + S::lane()] = t;
+  };
+  if (R == 1) {
+    put(dst, gw, gw_t);
+    put(dst + D, gb, gb_t);
+    return;
+  }
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    put(comb[sub], half ? gb : gw, half ? gb_t : gw_t);
+    __syncthreads();
+    for (uint32_t c = threadIdx.x; c < D; c += kBwdThreads) {
+      float v = comb[0][c];
+#pragma unroll
+      for (int r = 1; r < (W ? R : 1); ++r) v += comb[r][c];
+      dst[(int64_t)half * D + c] = v;
     }
+    __syncthreads();
   }
 }
 
@@ -290,21 +315,24 @@ __global__ __launch_bounds__(kThreads) void dora_layernorm_fwd_loop(
   }
 }
 
-// grad_x of one row per workgroup: a pass for the two means, a pass to write.
+// Backward of wide rows, where a row's sums and the weight gradient's do not fit
+// one thread's registers: a workgroup per row forms the two means, and a second
+// kernel goes down columns.  Memory is read twice and written once.
 template <bool BF>
-__global__ __launch_bounds__(kThreads) void dora_layernorm_bwd_x_loop(
+__global__ __launch_bounds__(kThreads) void dora_layernorm_bwd_means(
     const void* gy_, int64_t ldg, const void* x_, int64_t ldx, const void* w_, const float* mean_in,
-    const float* rstd_in, void* gx_, int64_t rows, int64_t D) {
+    const float* rstd_in, float2* means, int64_t rows, int64_t D) {
   using E = Elem<BF>;
   using T = typename E::T;
-  __shared__ float lds[2 * kWaves];
-  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+  __shared__ float lds[2][2 * kWaves];
+  int buf = 0;
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, buf ^= 1) {
     const T* gy = reinterpret_cast<const T*>(gy_) + row * ldg;
     const T* x = reinterpret_cast<const T*>(x_) + row * ldx;
     const T* w = reinterpret_cast<const T*>(w_);
-    T* gx = reinterpret_cast<T*>(gx_) + row * D;
     const float mean = mean_in[row], rstd = rstd_in[row];
     float s[2] = {0.f, 0.f};
+#pragma unroll 2
     for (int64_t j = (int64_t)threadIdx.x * E::kN; j < D; j += kThreads * E::kN) {
       float g[E::kN], v[E::kN], wv[E::kN];
       load_part<BF>(gy, j, D, 0.f, g);
@@ -319,46 +347,77 @@ __global__ __launch_bounds__(kThreads) void dora_layernorm_bwd_x_loop(
         s[1] = fmaf(h, (v[q] - mean) * rstd, s[1]);
       }
     }
-    block_sum<kWaves, 2>(s, lds);
-    const float c1 = s[0] / (float)D, c2 = s[1] / (float)D;
-    for (int64_t j = (int64_t)threadIdx.x * E::kN; j < D; j += kThreads * E::kN) {
-      float g[E::kN], v[E::kN], wv[E::kN];
-      load_part<BF>(gy, j, D, 0.f, g);
-      load_part<BF>(x, j, D, mean, v);
-#pragma unroll
-      for (int q = 0; q < E::kN; ++q) wv[q] = 1.f;
-      if (w) load_part<BF>(w, j, D, 0.f, wv);
-#pragma unroll
-      for (int q = 0; q < E::kN; ++q)
-        v[q] = rstd * (fmaf(g[q], wv[q], -c1) - (v[q] - mean) * rstd * c2);
-      store_part<BF>(gx, j, D, v);
-    }
-    __syncthreads();   // lds is written again for the next row
+    block_sum<kWaves, 2>(s, lds[buf]);
+    if (threadIdx.x == 0) means[row] = float2{s[0] / (float)D, s[1] / (float)D};
   }
 }
 
-// Column sums of gy xhat and gy over a block of rows, one thread per column:
-// part[block][0 or 1][column].
+// Columns [blockIdx.x * kThreads * kN, ...) of the rows [blockIdx.y *
+// rows_per_block, ...): grad_x from the rows' means, and the block's sums of gy
+// xhat and gy as part[blockIdx.y][0 or 1][column].
 template <bool BF>
-__global__ __launch_bounds__(kThreads) void dora_layernorm_bwd_w_loop(
-    const void* gy_, int64_t ldg, const void* x_, int64_t ldx, const float* mean_in,
-    const float* rstd_in, float* part, int64_t rows, int64_t D, int64_t rows_per_block) {
+__global__ __launch_bounds__(kThreads) void dora_layernorm_bwd_columns(
+    const void* gy_, int64_t ldg, const void* x_, int64_t ldx, const void* w_, const float* mean_in,
+    const float* rstd_in, const float2* means, void* gx_, float* part, int64_t rows, int64_t D,
+    int64_t rows_per_block) {
   using E = Elem<BF>;
   using T = typename E::T;
-  const int64_t j = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  constexpr int U = 4;   // rows in flight
+  const int64_t j = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * E::kN;
   if (j >= D) return;
+  const T* gy = reinterpret_cast<const T*>(gy_);
+  const T* x = reinterpret_cast<const T*>(x_);
+  T* gx = reinterpret_cast<T*>(gx_);
   const int64_t r0 = (int64_t)blockIdx.y * rows_per_block;
   const int64_t r1 = min(rows, r0 + rows_per_block);
-  float gw = 0.f, gb = 0.f;
-  for (int64_t r = r0; r < r1; ++r) {
-    const float g = E::get(reinterpret_cast<const T*>(gy_) + r * ldg + j);
-    const float v = E::get(reinterpret_cast<const T*>(x_) + r * ldx + j);
-    gw = fmaf(g, (v - mean_in[r]) * rstd_in[r], gw);
-    gb += g;
+  float w[E::kN], gw[E::kN], gb[E::kN];
+#pragma unroll
+  for (int q = 0; q < E::kN; ++q) w[q] = 1.f, gw[q] = gb[q] = 0.f;
+  if (w_) load_part<BF>(reinterpret_cast<const T*>(w_), j, D, 0.f, w);
+  auto row = [&](int64_t r, float* g, float* v) {
+    const float mean = mean_in[r], rstd = rstd_in[r];
+    const float2 c = gx ? means[r] : float2{0.f, 0.f};
+#pragma unroll
+    for (int q = 0; q < E::kN; ++q) {
+      const float n = (v[q] - mean) * rstd;
+      gw[q] = fmaf(g[q], n, gw[q]);
+      gb[q] += g[q];
+      g[q] = rstd * (g[q] * w[q] - fmaf(n, c.y, c.x));
+    }
+    if (gx) store_part<BF>(gx + r * D, j, D, g);
+  };
+  int64_t r = r0;
+  if (j + E::kN <= D) {
+    for (; r + U <= r1; r += U) {
+      typename E::Vec g[U], v[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        g[u] = E::raw(gy + (r + u) * ldg + j);
+        v[u] = E::raw(x + (r + u) * ldx + j);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float gv[E::kN], xv[E::kN];
+        E::decode(g[u], gv);
+        E::decode(v[u], xv);
+        row(r + u, gv, xv);
+      }
+    }
   }
-  float* dst = part + (int64_t)blockIdx.y * 2 * D;
-  dst[j] = gw;
-  dst[D + j] = gb;
+  for (; r < r1; ++r) {
+    float gv[E::kN], xv[E::kN];
+    load_part<BF>(gy + r * ldg, j, D, 0.f, gv);
+    load_part<BF>(x + r * ldx, j, D, 0.f, xv);
+    row(r, gv, xv);
+  }
+  if (part) {
+    float* dst = part + (int64_t)blockIdx.y * 2 * D;
+#pragma unroll
+    for (int q = 0; q < E::kN; q += 4) {
+      store_part<false>(dst, j + q, D, gw + q);
+      store_part<false>(dst + D, j + q, D, gb + q);
+    }
+  }
 }
 
 // grad_weight and grad_bias: the workgroups' partial sums added in order, 64
@@ -403,118 +462,121 @@ int check_shape(const dora_layernorm_shape* s) {
   return DORA_OK;
 }
 
-// Threads that hold a row: kElems elements each, twice that past 16384
-// elements; 0 for rows past 32768, which take the loops over memory.
-int row_threads(int64_t D) {
+// Threads that hold a row in the forward: kElems elements each, twice that past
+// 16384 elements; 0 for rows past 32768 (16384 in float32, where twice kElems
+// elements with their weights spill), which take the loop over memory.
+int row_threads(int64_t D, bool bf) {
   for (int t = 64; t <= 1024; t *= 2)
     if (D <= (int64_t)t * kElems) return t;
-  return D <= 1024 * 2 * kElems ? 1024 : 0;
+  return bf && D <= 1024 * 2 * kElems ? 1024 : 0;
 }
-// Whether the backward's row kernel also sums the weight's gradient: past 16384
-// elements its sums no longer fit beside the row, and gy and x are read again.
-bool fused_sums(int64_t D) { return D <= 1024 * kElems; }
+// Rows that the backward holds in registers beside the weight gradient's sums.
+bool bwd_in_registers(int64_t D) { return D <= kBwdThreads * kElems; }
 
-// Workgroups of the backward, which is also how many partial sums the weight's
-// gradient has.  As many rounds of rows as it takes kCuThreads threads per CU,
-// then the fewest workgroups with that many rounds.
+// Row blocks of the backward, which is also how many partial sums the weight's
+// gradient has.  In registers: one workgroup per CU, or as few as take no more
+// rounds.  Down columns: workgroups enough for four per CU, none under 16 rows.
 constexpr int64_t kCus = 256;
-constexpr int64_t kCuThreads = 1024;
 int64_t bwd_blocks(const dora_layernorm_shape& s) {
   if (s.rows < 1) return 0;
-  const int64_t most =
-      fused_sums(s.width) ? kCus * std::max<int64_t>(1, kCuThreads / row_threads(s.width)) : kCus;
-  const int64_t rounds = (s.rows + most - 1) / most;
-  return (s.rows + rounds - 1) / rounds;
+  if (bwd_in_registers(s.width)) {
+    const int64_t at_once = kBwdThreads / row_threads(s.width, true);
+    const int64_t groups = (s.rows + at_once - 1) / at_once;
+    const int64_t rounds = (groups + kCus - 1) / kCus;
+    return (groups + rounds - 1) / rounds;
+  }
+  const int64_t per = kThreads * (s.dtype == DORA_BF16 ? 8 : 4);
+  const int64_t cols = (s.width + per - 1) / per;
+  const int64_t want = std::max<int64_t>(1, 4 * kCus / cols);
+  const int64_t rows = std::max<int64_t>(16, (s.rows + want - 1) / want);
+  return (s.rows + rows - 1) / rows;
 }
-size_t w_part_bytes(const dora_layernorm_shape& s) {
-  return (size_t)bwd_blocks(s) * 2 * (size_t)s.width * 4;
+size_t part_bytes(const dora_layernorm_shape& s) {
+  return ((size_t)bwd_blocks(s) * 2 * (size_t)s.width * 4 + 15) / 16 * 16;
+}
+// The workspace: the weight gradient's partial sums, then the means of wide rows.
+size_t ws_bytes_for(const dora_layernorm_shape& s) {
+  return part_bytes(s) + (bwd_in_registers(s.width) ? 0 : (size_t)s.rows * sizeof(float2));
 }
 
-// f(threads, vectors) with the kernel's template arguments for rows of at most
-// 16384 elements.
-template <bool BF, typename F>
+// f(threads) with a row kernel's template argument.
+template <typename F>
 hipError_t with_threads(int64_t D, F f) {
   using std::integral_constant;
-  integral_constant<int, kElems / Elem<BF>::kN> nv;
-  switch (row_threads(D)) {
-    case 64: return f(integral_constant<int, 64>(), nv);
-    case 128: return f(integral_constant<int, 128>(), nv);
-    case 256: return f(integral_constant<int, 256>(), nv);
-    case 512: return f(integral_constant<int, 512>(), nv);
-    default: return f(integral_constant<int, 1024>(), nv);
+  switch (row_threads(D, true)) {
+    case 64: return f(integral_constant<int, 64>());
+    case 128: return f(integral_constant<int, 128>());
+    case 256: return f(integral_constant<int, 256>());
+    default: return f(integral_constant<int, 512>());
   }
 }
 
 template <bool BF>
 hipError_t forward(const dora_layernorm_shape& s, const void* x, const void* w, const void* b,
                    void* y, float* mean, float* rstd, hipStream_t st) {
-  constexpr int kWide = 2 * kElems / Elem<BF>::kN;
+  constexpr int NV = kElems / Elem<BF>::kN;
   const dim3 grid((unsigned)std::min(s.rows, kMaxGrid));
   LaunchTimer t("layernorm_fwd", st);
-  if (row_threads(s.width) == 0) {
+  const uint32_t D = (uint32_t)s.width;
+  if (row_threads(D, BF) == 0) {
     hipLaunchKernelGGL((dora_layernorm_fwd_loop<BF>), grid, dim3(kThreads), 0, st, x, s.ld_x, w, b,
                        y, mean, rstd, s.rows, s.width, s.eps);
-  } else if (s.width > 1024 * kElems) {
-    hipLaunchKernelGGL((dora_layernorm_fwd<BF, 1024, kWide>), grid, dim3(1024), 0, st, x, s.ld_x, w,
-                       b, y, mean, rstd, s.rows, (uint32_t)s.width, s.eps);
+  } else if (D > 1024 * kElems) {
+    if constexpr (BF)
+      hipLaunchKernelGGL((dora_layernorm_fwd<BF, 1024, 2 * NV>), grid, dim3(1024), 0, st, x, s.ld_x,
+                         w, b, y, mean, rstd, s.rows, D, s.eps);
+  } else if (D > 512 * kElems) {
+    hipLaunchKernelGGL((dora_layernorm_fwd<BF, 1024, NV>), grid, dim3(1024), 0, st, x, s.ld_x, w, b,
+                       y, mean, rstd, s.rows, D, s.eps);
   } else {
-    return with_threads<BF>(s.width, [&](auto threads, auto nv) {
-      hipLaunchKernelGGL((dora_layernorm_fwd<BF, threads(), nv()>), grid, dim3(threads()), 0, st, x,
-                         s.ld_x, w, b, y, mean, rstd, s.rows, (uint32_t)s.width, s.eps);
+    return with_threads(D, [&](auto threads) {
+      hipLaunchKernelGGL((dora_layernorm_fwd<BF, threads(), NV>), grid, dim3(threads()), 0, st, x,
+                         s.ld_x, w, b, y, mean, rstd, s.rows, D, s.eps);
       return hipGetLastError();
     });
   }
   return hipGetLastError();
 }
 
-// grad_x alone, for rows past the fused kernel's.
-template <bool BF>
-hipError_t backward_x(const dora_layernorm_shape& s, const void* gy, const void* x, const void* w,
-                      const float* mean, const float* rstd, void* gx, hipStream_t st) {
-  constexpr int kWide = 2 * kElems / Elem<BF>::kN;
-  const dim3 grid((unsigned)std::min(s.rows, kMaxGrid));
-  LaunchTimer t("layernorm_bwd_x", st);
-  if (row_threads(s.width) > 0)
-    hipLaunchKernelGGL((dora_layernorm_bwd<BF, 1024, kWide, false>), grid, dim3(1024), 0, st, gy,
-                       s.ld_gy, x, s.ld_x, w, mean, rstd, gx, nullptr, s.rows,
-                       (uint32_t)s.width);
-  else
-    hipLaunchKernelGGL((dora_layernorm_bwd_x_loop<BF>), grid, dim3(kThreads), 0, st, gy, s.ld_gy, x,
-                       s.ld_x, w, mean, rstd, gx, s.rows, s.width);
-  return hipGetLastError();
-}
-
 template <bool BF>
 hipError_t backward(const dora_layernorm_shape& s, const void* gy, const void* x, const void* w,
-                    const float* mean, const float* rstd, void* gx, void* gw, void* gb, float* part,
+                    const float* mean, const float* rstd, void* gx, void* gw, void* gb, void* ws,
                     hipStream_t st) {
+  constexpr int NV = kElems / Elem<BF>::kN;
   const bool sums = gw || gb;
   const int64_t blocks = bwd_blocks(s);
-  if (s.rows > 0 && fused_sums(s.width)) {
+  float* part = sums ? reinterpret_cast<float*>(ws) : nullptr;
+  if (s.rows > 0 && (gx || sums) && bwd_in_registers(s.width)) {
     LaunchTimer t("layernorm_bwd", st);
-    const hipError_t e = with_threads<BF>(s.width, [&](auto threads, auto nv) {
+    const hipError_t e = with_threads(s.width, [&](auto threads) {
       if (sums)
-        hipLaunchKernelGGL((dora_layernorm_bwd<BF, threads(), nv(), true>), dim3((unsigned)blocks),
-                           dim3(threads()), 0, st, gy, s.ld_gy, x, s.ld_x, w, mean, rstd, gx, part,
-                           s.rows, (uint32_t)s.width);
-      else if (gx)
-        hipLaunchKernelGGL((dora_layernorm_bwd<BF, threads(), nv(), false>),
-                           dim3((unsigned)blocks), dim3(threads()), 0, st, gy, s.ld_gy, x, s.ld_x,
-                           w, mean, rstd, gx, part, s.rows, (uint32_t)s.width);
+        hipLaunchKernelGGL((dora_layernorm_bwd<BF, threads(), NV, true>), dim3((unsigned)blocks),
+                           dim3(kBwdThreads), 0, st, gy, s.ld_gy, x, s.ld_x, w, mean, rstd, gx,
+                           part, s.rows, (uint32_t)s.width);
+      else
+        hipLaunchKernelGGL((dora_layernorm_bwd<BF, threads(), NV, false>), dim3((unsigned)blocks),
+                           dim3(kBwdThreads), 0, st, gy, s.ld_gy, x, s.ld_x, w, mean, rstd, gx,
+                           part, s.rows, (uint32_t)s.width);
       return hipGetLastError();
     });
     if (e) return e;
-  } else if (s.rows > 0) {
-    if (gx)
-      if (hipError_t e = backward_x<BF>(s, gy, x, w, mean, rstd, gx, st)) return e;
-    if (sums) {
-      LaunchTimer t("layernorm_bwd_w", st);
-      const unsigned cols = (unsigned)((s.width + kThreads - 1) / kThreads);
-      hipLaunchKernelGGL((dora_layernorm_bwd_w_loop<BF>), dim3(cols, (unsigned)blocks),
-                         dim3(kThreads), 0, st, gy, s.ld_gy, x, s.ld_x, mean, rstd, part, s.rows,
-                         s.width, (s.rows + blocks - 1) / blocks);
+  } else if (s.rows > 0 && (gx || sums)) {
+    float2* means = gx ? reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(ws) + part_bytes(s))
+                       : nullptr;
+    if (gx) {
+      LaunchTimer t("layernorm_bwd_means", st);
+      hipLaunchKernelGGL((dora_layernorm_bwd_means<BF>),
+                         dim3((unsigned)std::min(s.rows, kMaxGrid)), dim3(kThreads), 0, st, gy,
+                         s.ld_gy, x, s.ld_x, w, mean, rstd, means, s.rows, s.width);
       if (hipError_t e = hipGetLastError()) return e;
     }
+    LaunchTimer t("layernorm_bwd_columns", st);
+    const int64_t per = kThreads * Elem<BF>::kN;
+    hipLaunchKernelGGL((dora_layernorm_bwd_columns<BF>),
+                       dim3((unsigned)((s.width + per - 1) / per), (unsigned)blocks),
+                       dim3(kThreads), 0, st, gy, s.ld_gy, x, s.ld_x, w, mean, rstd, means, gx,
+                       part, s.rows, s.width, (s.rows + blocks - 1) / blocks);
+    if (hipError_t e = hipGetLastError()) return e;
   }
   if (!sums) return hipSuccess;
   LaunchTimer t("layernorm_bwd_finish", st);
@@ -533,7 +595,7 @@ extern "C" {
 
 DORA_API size_t dora_layernorm_workspace_bytes(const dora_layernorm_shape* shape) {
   if (!shape || !dtype_ok(*shape) || !shape_ok(*shape)) return 0;
-  return w_part_bytes(*shape);
+  return ws_bytes_for(*shape);
 }
 
 DORA_API int dora_layernorm_forward(const dora_layernorm_shape* shape, const void* x,
@@ -572,14 +634,15 @@ DORA_API int dora_layernorm_backward(const dora_layernorm_shape* shape, const vo
   DORA_CHECK(check_elem(grad_x, e, true));
   DORA_CHECK(check_elem(grad_weight, e, true));
   DORA_CHECK(check_elem(grad_bias, e, true));
-  if (grad_weight || grad_bias) DORA_CHECK(check_ws(ws, ws_bytes, w_part_bytes(s)));
+  // rows held in registers need none for grad_x alone
+  if (grad_weight || grad_bias || (grad_x && !bwd_in_registers(s.width)))
+    DORA_CHECK(check_ws(ws, ws_bytes, ws_bytes_for(s)));
   hipStream_t st = reinterpret_cast<hipStream_t>(hip_stream);
-  float* part = reinterpret_cast<float*>(ws);
   HIP_TRY(s.dtype == DORA_BF16
               ? backward<true>(s, grad_y, x, weight, mean, rstd, grad_x, grad_weight, grad_bias,
-                               part, st)
+                               ws, st)
               : backward<false>(s, grad_y, x, weight, mean, rstd, grad_x, grad_weight, grad_bias,
-                                part, st));
+                                ws, st));
   return DORA_OK;
 }
 

@@ -324,7 +324,7 @@ def dora_layernorm_backward(grad_y, x, weight, mean, rstd, *, need=("x", "weight
             _need(t, nm, dt, shp, dev)
     sh = _lib.DoraLayernormShape(R, D, ld, ldg, code, 0.0, 0, 0)
     nb = 0
-    if grad_weight is not None or grad_bias is not None:
+    if grad_weight is not None or grad_bias is not None or D > 8192:
         nb = _lib.lib().dora_layernorm_workspace_bytes(ctypes.byref(sh))
         if workspace is None:
             workspace = torch.empty(max(nb, 1), dtype=torch.uint8, device=dev)
