@@ -10,21 +10,25 @@ from __future__ import annotations
 
 import ctypes
 import json
+import operator
 
+import numpy as np
 import torch
 
 from . import _lib
 from ._lib import DoraError, FLAG_EXACT_NORM_GRAD, FLAG_SEPARATE_COMPOSE  # noqa: F401
 
+_dtype_of = operator.attrgetter("dtype")
 _DT = {torch.float32: _lib.F32, torch.bfloat16: _lib.BF16}
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(dev):
-    return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
+    # the handle alone: torch.cuda.current_stream builds a Stream object around it (2 us a call)
+    return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 def _need(t, name, dtype=None, shape=None, dev=None):
@@ -248,6 +252,13 @@ def dora_vera_grads(grad_B_eff, B_shared, b, d, *, need=("b", "d"), workspace=No
     return gb, gd
 
 
+def _out(t, name, dtype, shape, dev):
+    """An output the caller gave, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    return _need(t, name, dtype, shape, dev)
+
+
 def _rows(t, name, dtype=None, shape=None, dev=None):
     """Checks a [rows, width] tensor whose rows are contiguous; returns its row stride."""
     if not isinstance(t, torch.Tensor):
@@ -283,15 +294,9 @@ def dora_layernorm(x, weight=None, bias=None, *, eps=1e-5, y=None, mean=None, rs
     for t, nm in ((weight, "weight"), (bias, "bias")):
         if t is not None:
             _need(t, nm, dt, (D,), dev)
-    if y is None:
-        y = torch.empty(R, D, dtype=dt, device=dev)
-    if mean is None:
-        mean = torch.empty(R, dtype=torch.float32, device=dev)
-    if rstd is None:
-        rstd = torch.empty(R, dtype=torch.float32, device=dev)
-    _need(y, "y", dt, (R, D), dev)
-    _need(mean, "mean", torch.float32, (R,), dev)
-    _need(rstd, "rstd", torch.float32, (R,), dev)
+    y = _out(y, "y", dt, (R, D), dev)
+    mean = _out(mean, "mean", torch.float32, (R,), dev)
+    rstd = _out(rstd, "rstd", torch.float32, (R,), dev)
     sh = _lib.DoraLayernormShape(R, D, ld, ld, code, eps, 0, 0)
     _check(_lib.lib().dora_layernorm_forward(ctypes.byref(sh), _ptr(x), _ptr(weight), _ptr(bias),
                                              _ptr(y), _ptr(mean), _ptr(rstd), _stream(dev)),
@@ -312,16 +317,12 @@ def dora_layernorm_backward(grad_y, x, weight, mean, rstd, *, need=("x", "weight
         _need(weight, "weight", dt, (D,), dev)
     _need(mean, "mean", torch.float32, (R,), dev)
     _need(rstd, "rstd", torch.float32, (R,), dev)
-    if "x" in need and grad_x is None:
-        grad_x = torch.empty(R, D, dtype=dt, device=dev)
-    if "weight" in need and grad_weight is None:
-        grad_weight = torch.empty(D, dtype=dt, device=dev)
-    if "bias" in need and grad_bias is None:
-        grad_bias = torch.empty(D, dtype=dt, device=dev)
-    for t, nm, shp in ((grad_x, "grad_x", (R, D)), (grad_weight, "grad_weight", (D,)),
-                       (grad_bias, "grad_bias", (D,))):
-        if t is not None:
-            _need(t, nm, dt, shp, dev)
+    if grad_x is not None or "x" in need:
+        grad_x = _out(grad_x, "grad_x", dt, (R, D), dev)
+    if grad_weight is not None or "weight" in need:
+        grad_weight = _out(grad_weight, "grad_weight", dt, (D,), dev)
+    if grad_bias is not None or "bias" in need:
+        grad_bias = _out(grad_bias, "grad_bias", dt, (D,), dev)
     sh = _lib.DoraLayernormShape(R, D, ld, ldg, code, 0.0, 0, 0)
     nb = 0
     if grad_weight is not None or grad_bias is not None or D > 8192:
@@ -377,9 +378,7 @@ def dora_token_logprob_backward(grad_logp, grad_entropy, logits, targets, lse, e
         if t is not None:
             _need(t, nm, torch.float32, (T,), dev)
     _need(lse, "lse", torch.float32, (T,), dev)
-    if grad_logits is None:
-        grad_logits = torch.empty(T, V, dtype=logits.dtype, device=dev)
-    _need(grad_logits, "grad_logits", logits.dtype, (T, V), dev)
+    grad_logits = _out(grad_logits, "grad_logits", logits.dtype, (T, V), dev)
     sh = _lib.DoraLogprobShape(T, V, ld, _layer_dtype(logits), 0, float(scale), 0)
     _check(_lib.lib().dora_token_logprob_backward(ctypes.byref(sh), _ptr(grad_logp),
                                                   _ptr(grad_entropy), _ptr(logits), _ptr(targets),
@@ -448,25 +447,32 @@ class AdamWPlan:
                 e.master = mst[i].data_ptr()
         self.params, self.device, self.dtype = params, dev, dt
         self.state_bits = 8 if small else 32
+        self.norm_bytes = None   # workspace of the gradients' norm, asked for once
         self._keep = (exp_avg, exp_avg_sq, sc1, sc2, mst)
         self._at = [p.data_ptr() for p in params]
         self._sizes = [p.numel() for p in params]
+        # the table's gradient addresses as an array, written in one go at each step
+        self._grads = np.frombuffer(self.table, dtype=np.int64).reshape(n, -1)[:, 1]
 
     def _take_grads(self, grads):
         """Checks the gradients and notes where they are; returns their dtype."""
+        T = torch.Tensor
         if len(grads) != len(self.params):
             raise ValueError(f"{len(grads)} gradients for {len(self.params)} params")
-        if [p.data_ptr() for p in self.params] != self._at:
+        if list(map(T.data_ptr, self.params)) != self._at:
             raise ValueError("a parameter's storage has changed since the plan was made")
         gdt = grads[0].dtype
         if gdt not in _DT:
             raise ValueError(f"unsupported dtype {gdt}; use float32 or bfloat16")
-        dev = self.device
-        for i, (g, k) in enumerate(zip(grads, self._sizes)):
-            if g.dtype is not gdt or g.device != dev or g.numel() != k or not g.is_contiguous():
-                _need(g, f"grads[{i}]", gdt, None, dev)
-                raise ValueError(f"grads[{i}] has {g.numel()} elements, expected {k}")
-            self.table[i].grad = g.data_ptr()
+        # whole lists at a time: a step may hold hundreds of small tensors
+        if not (all(map(T.is_contiguous, grads)) and list(map(T.numel, grads)) == self._sizes
+                and set(map(_dtype_of, grads)) == {gdt}
+                and set(map(T.get_device, grads)) == {self.device.index}):
+            for i, (g, k) in enumerate(zip(grads, self._sizes)):
+                _need(g, f"grads[{i}]", gdt, None, self.device)
+                if g.numel() != k:
+                    raise ValueError(f"grads[{i}] has {g.numel()} elements, expected {k}")
+        self._grads[:] = list(map(T.data_ptr, grads))
         return gdt
 
 
@@ -479,10 +485,12 @@ def dora_grad_norm(plan, grads, max_norm=1.0, *, workspace=None):
 
 def _grad_norm(plan, gdt, max_norm, workspace):
     L, n = _lib.lib(), len(plan.params)
-    nb = L.dora_grad_norm_workspace_bytes(plan.table, n)
     if workspace is None:
-        workspace = torch.empty(max(nb, 1), dtype=torch.uint8, device=plan.device)
-    norm, factor = torch.empty(2, dtype=torch.float32, device=plan.device).unbind(0)
+        if plan.norm_bytes is None:
+            plan.norm_bytes = L.dora_grad_norm_workspace_bytes(plan.table, n)
+        workspace = torch.empty(max(plan.norm_bytes, 1), dtype=torch.uint8, device=plan.device)
+    norm = torch.empty((), dtype=torch.float32, device=plan.device)
+    factor = torch.empty((), dtype=torch.float32, device=plan.device)
     _check(L.dora_grad_norm(plan.table, n, _DT[gdt], float(max_norm), _ptr(norm), _ptr(factor),
                             _ptr(workspace), workspace.numel() * workspace.element_size(),
                             _stream(plan.device)), "dora_grad_norm")
