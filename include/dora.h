@@ -281,7 +281,7 @@ DORA_API int dora_layernorm_backward(const dora_layernorm_shape* shape, const vo
 #define DORA_LOGPROB_MAX_TOP 64
 typedef struct {
     int64_t  rows;      /* 0 <= rows < 2^31                                          */
-    int64_t  vocab;     /* 1 <= vocab <= 2^24                                        */
+    int64_t  vocab;     /* 1 <= vocab <= 2^23                                        */
     int64_t  ld;        /* row stride of the logits in elements, vocab <= ld < 2^31  */
     int32_t  dtype;     /* dora_dtype of logits and grad_logits                      */
     int32_t  top;       /* alternatives per row, 0 <= top <= min(vocab, 64)          */
@@ -302,7 +302,7 @@ DORA_API size_t dora_token_logprob_workspace_bytes(const dora_logprob_shape* sha
  *   logp     float32 [rows]; entropy, lse float32 [rows], may be NULL
  *   top_logp float32 [rows, top], top_index int64 [rows, top]; needed when top > 0
  * A target outside [0, vocab) (-100, say) marks a row without one: the row is
- * not read, its logp, entropy, lse and top_logp are 0 and its top_index -1.
+ * skipped, its logp, entropy, lse and top_logp are 0 and its top_index -1.
  * Masked logits are -inf (p = 0) or the type's lowest value.  A row with
  * nothing left (all -inf) has lse = logp = top_logp = -inf and entropy 0; a NaN
  * or +inf in a row makes its logp, entropy and lse NaN (a NaN orders above

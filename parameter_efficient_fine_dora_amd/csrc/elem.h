@@ -19,6 +19,9 @@ struct Elem<true> {
   __device__ static float get(const T* p) { return bf16_to_f32(*p); }
   __device__ static void put(T* p, float v) { *p = f32_to_bf16(v); }
   __device__ static Vec raw(const T* p) { return *reinterpret_cast<const Raw*>(p); }
+  __device__ static Vec masked() {   // every element -inf
+    return Vec{0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u};
+  }
   __device__ static void decode(const Vec& v, float* out) {
 #pragma unroll
     for (int d = 0; d < 4; ++d) {
@@ -34,6 +37,10 @@ struct Elem<true> {
     return v;
   }
   __device__ static void store(T* p, const float* in) { *reinterpret_cast<Raw*>(p) = encode(in); }
+  // past the caches, for what is too large to stay in them
+  __device__ static void store_through(T* p, const float* in) {
+    __builtin_nontemporal_store(encode(in), reinterpret_cast<Raw*>(p));
+  }
 };
 
 template <>
@@ -45,6 +52,10 @@ struct Elem<false> {
   __device__ static float get(const T* p) { return *p; }
   __device__ static void put(T* p, float v) { *p = v; }
   __device__ static Vec raw(const T* p) { return *reinterpret_cast<const Raw*>(p); }
+  __device__ static Vec masked() {
+    const float inf = __builtin_huge_valf();
+    return Vec{-inf, -inf, -inf, -inf};
+  }
   __device__ static void decode(const Vec& v, float* out) {
 #pragma unroll
     for (int d = 0; d < 4; ++d) out[d] = v[d];
@@ -52,6 +63,10 @@ struct Elem<false> {
   __device__ static void load(const T* p, float* out) { decode(raw(p), out); }
   __device__ static Vec encode(const float* in) { return Vec{in[0], in[1], in[2], in[3]}; }
   __device__ static void store(T* p, const float* in) { *reinterpret_cast<Raw*>(p) = encode(in); }
+  // past the caches, for what is too large to stay in them
+  __device__ static void store_through(T* p, const float* in) {
+    __builtin_nontemporal_store(encode(in), reinterpret_cast<Raw*>(p));
+  }
 };
 
 // Elements [j, j + kN) of a row of n, absent ones as `fill`.

@@ -27,13 +27,31 @@ constexpr float kCoarseLse = 1024.f;
 
 // A row is read by up to kMaxSplits workgroups, in chunks of at most kMaxChunk
 // elements (their group maxima stay in LDS).
-constexpr int64_t kMaxSplits = 128;
+constexpr int64_t kMaxSplits = 64;
 constexpr int64_t kMaxChunk = 131072;
 constexpr int kMaxTop = DORA_LOGPROB_MAX_TOP;
 
 // Larger of two, NaN if either is (v_maximum3_f32).
 __device__ __forceinline__ float maxnan(float a, float b) {
   return __builtin_elementwise_maximum(a, b);
+}
+
+__device__ __forceinline__ float wave_maxnan(float v) {
+  v = maxnan(v, dpp_move<0xB1>(v));
+  v = maxnan(v, dpp_move<0x4E>(v));
+  v = maxnan(v, dpp_move<0x141>(v));
+  v = maxnan(v, dpp_move<0x140>(v));
+  return maxnan(maxnan(lane_value(v, 0), lane_value(v, 16)),
+                maxnan(lane_value(v, 32), lane_value(v, 48)));
+}
+
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  v = max(v, __float_as_uint(dpp_move<0xB1>(__uint_as_float(v))));
+  v = max(v, __float_as_uint(dpp_move<0x4E>(__uint_as_float(v))));
+  v = max(v, __float_as_uint(dpp_move<0x141>(__uint_as_float(v))));
+  v = max(v, __float_as_uint(dpp_move<0x140>(__uint_as_float(v))));
+  auto at = [&](int lane) { return (uint32_t)__builtin_amdgcn_readlane((int)v, lane); };
+  return max(max(at(0), at(16)), max(at(32), at(48)));
 }
 
 // Whole numbers in the order of the floats: NaN above +inf, -0 equal to +0.
@@ -95,19 +113,23 @@ __device__ __forceinline__ void add_logits(Stat& a, const float* v, float c2) {
   }
 }
 
-// The workgroup's merged statistics, to every thread; `lds` holds kWaves.
-__device__ __forceinline__ Stat block_stat(Stat a, float c2, Stat* lds) {
-  float m = a.m;
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) m = maxnan(m, __shfl_xor(m, off, 64));
-  rescale(a, m, c2);
+// A wave's merged statistics, to every lane.
+__device__ __forceinline__ Stat wave_stat(Stat a, float c2) {
+  rescale(a, wave_maxnan(a.m), c2);
   a.s = wave_sum(a.s);
   a.u = wave_sum(a.u);
+  return a;
+}
+// A workgroup's, to every thread; `lds` holds WAVES.
+template <int WAVES>
+__device__ __forceinline__ Stat block_stat(Stat a, float c2, Stat* lds) {
+  a = wave_stat(a, c2);
+  if (WAVES == 1) return a;
   if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = a;
   __syncthreads();
   a = lds[0];
 #pragma unroll
-  for (int w = 1; w < kWaves; ++w) a = merge(a, lds[w], c2);
+  for (int w = 1; w < WAVES; ++w) a = merge(a, lds[w], c2);
   return a;
 }
 
@@ -132,18 +154,20 @@ __device__ __forceinline__ RowOut row_out(const Stat& a, float at, float scale) 
 // vectors goes to LDS.  The top k elements lie in the k groups that are first by
 // (maximum falling, index rising): an element outside them has k groups before
 // its own, each with an element that comes before it.  The same holds one level
-// up for runs of consecutive groups, one run per thread.  So three rounds of
-// counting ranks suffice, each over few candidates: the k best of 256 runs; the
-// k best groups of those runs; the k best elements of those groups, which are
-// read again (from cache: 64 bytes each).  A candidate below the k-th of the
-// round before is dropped first, which leaves little more than k of them unless
-// many are equal.  Nothing depends on the order or distribution of the logits but
-// the time, and that only through ties.
-constexpr int kListCap = 2048;   // kMaxTop * max(groups per run, elements per group)
+// up for runs of consecutive groups, one run per thread.  So: the k best runs, by
+// bisection over their maxima; the k best groups of those runs and the k best
+// elements of those groups, by counting ranks among the few that are not below
+// the k-th of the step before.  The groups' elements are read again (from cache:
+// 64 bytes each).  Logits of -inf are left out of all this, or a mask would make
+// one long tie of them; where fewer than k others are left the first of them
+// follow in order.
+constexpr uint32_t kNone = 0x007fffffu;   // order_bits(-inf)
+constexpr int kListCap = 2048;            // kMaxTop * max(groups per run, elements per group)
+template <int THREADS>
 struct TopLds {
   uint64_t list[kListCap];
-  uint32_t run[kThreads];     // order bits of the runs' maxima
-  uint32_t chosen[kMaxTop];   // the runs or groups of the round
+  uint32_t run[THREADS];      // order bits of the runs' maxima
+  uint32_t chosen[kMaxTop];   // the groups
   uint32_t count, bound;
 };
 
@@ -154,48 +178,67 @@ __device__ __forceinline__ int rank_in(uint64_t key, const uint64_t* list, int n
   return r;
 }
 
+// Of a wave's 64 N numbers: an x that at least k of them reach, and that either
+// exactly k reach or that is the k-th largest (0 if fewer than k are above 0).
+// Bisection over the bits; a step is N ballots.
+template <int N>
+__device__ __forceinline__ uint32_t kth_largest(const uint32_t* v, int k) {
+  uint32_t x = 0;
+  for (int bit = 31; bit >= 0; --bit) {
+    const uint32_t c = x | (1u << bit);
+    int n = 0;
+#pragma unroll
+    for (int q = 0; q < N; ++q) n += __popcll(__ballot(v[q] >= c));
+    if (n >= k) x = c;
+    if (n == k) break;
+  }
+  return x;
+}
+
+__device__ __forceinline__ uint64_t lanes_below() {
+  return (uint64_t(1) << (threadIdx.x & 63)) - 1;
+}
+
 // Keys of the k first elements of row[0, n), in order, to put(rank, key);
 // n >= k.  `group` holds the maxima of groups of G elements.
-template <bool BF, typename Put>
+template <bool BF, int THREADS, typename Put>
 __device__ void select_top(const typename Elem<BF>::T* row, int64_t n, const float* group, int k,
                            Put put) {
-  __shared__ TopLds t;
-  constexpr int G = 4 * Elem<BF>::kN;
-  const int tid = threadIdx.x;
+  constexpr int G = 4 * Elem<BF>::kN, W = THREADS / 64;
+  __shared__ TopLds<THREADS> t;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int ng = (int)((n + G - 1) / G);
-  const int run = (ng + kThreads - 1) / kThreads;   // groups per run
-  const int runs = (ng + run - 1) / run;
-  // runs
+  const int run = (ng + THREADS - 1) / THREADS;   // groups per run
   const int g0 = tid * run, g1 = min(ng, g0 + run);
   uint32_t best = 0;
   for (int g = g0; g < g1; ++g) best = max(best, order_bits(group[g]));
   t.run[tid] = best;
-  if (tid == 0) {
-    t.count = 0;
-    t.bound = 0;
-  }
+  if (tid == 0) t.count = 0;
   __syncthreads();
-  int r = 0;
-#pragma unroll 4
-  for (int i = 0; i < kThreads; i += 4) {
-    const u32x4 o = *reinterpret_cast<const u32x4*>(&t.run[i]);
+  // the k best runs, ties by index; every wave finds the same
+  uint32_t v[W];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) r += (o[q] > best || (o[q] == best && i + q < tid)) ? 1 : 0;
+  for (int q = 0; q < W; ++q) v[q] = t.run[q * 64 + lane];
+  const uint32_t x = max(kth_largest<W>(v, k), kNone + 1);
+  int above = 0, before = 0;
+#pragma unroll
+  for (int q = 0; q < W; ++q) {
+    above += __popcll(__ballot(v[q] > x));
+    const uint64_t same = __ballot(v[q] == x);
+    before += q < wave ? __popcll(same) : q == wave ? __popcll(same & lanes_below()) : 0;
   }
-  const bool in = tid < runs && r < k;
-  if (in && r == k - 1) t.bound = best;
-  __syncthreads();
-  // groups of the chosen runs
-  const uint32_t bound = t.bound;
-  if (in) {
+  if (best > x || (best == x && before < k - above)) {
     for (int g = g0; g < g1; ++g) {
       const uint32_t o = order_bits(group[g]);
-      if (o >= bound) t.list[atomicAdd(&t.count, 1u)] = ((uint64_t)o << 32) | (uint32_t)~(uint32_t)g;
+      if (o >= x) t.list[atomicAdd(&t.count, 1u)] = ((uint64_t)o << 32) | (uint32_t)~(uint32_t)g;
     }
   }
   __syncthreads();
+  // the k best groups of those runs
   int m = (int)t.count;
-  for (int i = tid; i < m; i += kThreads) {
+  if (tid == 0) t.bound = x;
+  __syncthreads();
+  for (int i = tid; i < m; i += THREADS) {
     const uint64_t key = t.list[i];
     const int rank = rank_in(key, t.list, m);
     if (rank < k) t.chosen[rank] = ~(uint32_t)key;
@@ -203,11 +246,11 @@ __device__ void select_top(const typename Elem<BF>::T* row, int64_t n, const flo
   }
   const int picked = min(m, k);
   __syncthreads();
-  // elements of the chosen groups
-  const uint32_t least = m >= k ? t.bound : 0u;
+  const uint32_t least = t.bound;
   if (tid == 0) t.count = 0;
   __syncthreads();
-  for (int i = tid; i < picked * G; i += kThreads) {
+  // their k best elements
+  for (int i = tid; i < picked * G; i += THREADS) {
     const int64_t j = (int64_t)t.chosen[i / G] * G + i % G;
     if (j < n) {
       const uint64_t key = order_key(Elem<BF>::get(row + j), (uint32_t)j);
@@ -216,30 +259,57 @@ __device__ void select_top(const typename Elem<BF>::T* row, int64_t n, const flo
   }
   __syncthreads();
   m = (int)t.count;
-  for (int i = tid; i < m; i += kThreads) {
+  for (int i = tid; i < m; i += THREADS) {
     const uint64_t key = t.list[i];
     const int rank = rank_in(key, t.list, m);
     if (rank < k) put(rank, key);
   }
+  // masked ones to make up the number
+  if (wave == 0) {
+    for (int64_t j0 = 0; m < k && j0 < n; j0 += 64) {
+      const bool masked = j0 + lane < n && Elem<BF>::get(row + j0 + lane) == kNegInf;
+      const uint64_t mask = __ballot(masked);
+      const int rank = m + __popcll(mask & lanes_below());
+      if (masked && rank < k) put(rank, order_key(kNegInf, (uint32_t)(j0 + lane)));
+      m += __popcll(mask);
+    }
+  }
 }
 
 // Chunk blockIdx.x of a row (or, with one chunk, the whole row and its results).
-// Loads are kU vectors ahead of the arithmetic; per element the loop costs a
-// subtraction, two products, an exponential, a maximum and two sums.
-template <bool BF, bool TOP, bool SPLIT>
-__global__ __launch_bounds__(kThreads) void dora_logprob_fwd(
+// kU vectors per thread are loaded before the first is used; per element the loop
+// costs a subtraction, two products, an exponential, two maxima and two sums.
+template <bool BF, int THREADS, bool TOP, bool SPLIT>
+__global__ __launch_bounds__(THREADS) void dora_logprob_fwd(
     const void* logits, int64_t ld, const int64_t* targets, float* logp, float* entropy, float* lse,
     float* top_logp, int64_t* top_index, Stat* part, uint64_t* part_top, int64_t rows, int64_t V,
     int64_t chunk, int top, float scale) {
   using E = Elem<BF>;
   using T = typename E::T;
-  constexpr int kStep = kThreads * E::kN;
+  constexpr int kStep = THREADS * E::kN;
   extern __shared__ float group[];
-  __shared__ Stat lds[kWaves];
+  __shared__ Stat lds[THREADS / 64];
   const float c2 = scale * kLog2e;
   const int64_t lo = (int64_t)blockIdx.x * chunk;
   const int64_t n = min(V - lo, chunk);
   for (int64_t row = blockIdx.y; row < rows; row += gridDim.y) {
+    const T* z = reinterpret_cast<const T*>(logits) + row * ld + lo;
+    const int64_t own = (int64_t)threadIdx.x * E::kN;
+    typename E::Vec raw[kU];
+    auto load = [&](int64_t j0) {
+      if (n - j0 >= kStep * kU) {
+#pragma unroll
+        for (int u = 0; u < kU; ++u) raw[u] = E::raw(z + j0 + u * kStep + own);
+      } else {
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          const int64_t j = j0 + u * kStep + own;
+          raw[u] = E::masked();
+          if (j + E::kN <= n) raw[u] = E::raw(z + j);
+        }
+      }
+    };
+    load(0);   // in flight while the target is looked up
     const int64_t y = targets[row];
     if (y < 0 || y >= V) {
       if (SPLIT) continue;   // the join writes its zeros
@@ -254,36 +324,43 @@ __global__ __launch_bounds__(kThreads) void dora_logprob_fwd(
       }
       continue;
     }
-    const T* z = reinterpret_cast<const T*>(logits) + row * ld;
     const float at = SPLIT ? 0.f : E::get(z + y);
-    z += lo;
     Stat a = empty_stat();
     auto group_max = [&](const float* v, int64_t j) {
       float m = v[0];
 #pragma unroll
       for (int q = 1; q < E::kN; ++q) m = maxnan(m, v[q]);
-      m = maxnan(m, __shfl_xor(m, 1, 64));
-      m = maxnan(m, __shfl_xor(m, 2, 64));
+      m = maxnan(m, dpp_move<0xB1>(m));
+      m = maxnan(m, dpp_move<0x4E>(m));
       if ((threadIdx.x & 3) == 0 && j < n) group[j / (4 * E::kN)] = m;
     };
-    int64_t j = (int64_t)threadIdx.x * E::kN;
-    int64_t left = n;
-    for (; left >= kStep * kU; left -= kStep * kU, j += kStep * kU) {
-      float v[kU][E::kN];
+    for (int64_t j0 = 0;;) {
+      if (n - j0 >= kStep * kU) {
+        float v[kU][E::kN];
 #pragma unroll
-      for (int u = 0; u < kU; ++u) E::load(z + j + u * kStep, v[u]);
+        for (int u = 0; u < kU; ++u) E::decode(raw[u], v[u]);
+        if (TOP) {
 #pragma unroll
-      for (int u = 0; u < kU; ++u)
-        if (TOP) group_max(v[u], j + u * kStep);
-      add_logits<kU * E::kN>(a, &v[0][0], c2);
+          for (int u = 0; u < kU; ++u) group_max(v[u], j0 + u * kStep + own);
+        }
+        add_logits<kU * E::kN>(a, &v[0][0], c2);
+      } else {
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          const int64_t j = j0 + u * kStep + own;
+          if (j0 + u * kStep >= n) break;
+          float v[E::kN];
+          E::decode(raw[u], v);
+          if (j < n && j + E::kN > n) load_part<BF>(z, j, n, kNegInf, v);
+          if (TOP) group_max(v, j);
+          add_logits<E::kN>(a, v, c2);
+        }
+      }
+      j0 += kStep * kU;
+      if (j0 >= n) break;
+      load(j0);
     }
-    for (; left > 0; left -= kStep, j += kStep) {
-      float v[E::kN];
-      load_part<BF>(z, j, n, kNegInf, v);
-      if (TOP) group_max(v, j);
-      add_logits<E::kN>(a, v, c2);
-    }
-    a = block_stat(a, c2, lds);   // its barrier also completes the group maxima
+    a = block_stat<THREADS / 64>(a, c2, lds);
     RowOut out;
     if (SPLIT) {
       if (threadIdx.x == 0) part[row * gridDim.x + blockIdx.x] = a;
@@ -296,11 +373,12 @@ __global__ __launch_bounds__(kThreads) void dora_logprob_fwd(
       }
     }
     if constexpr (TOP) {
+      __syncthreads();   // the group maxima are complete
       const int k = (int)min((int64_t)top, n);
       uint64_t* mine = SPLIT ? part_top + (row * gridDim.x + blockIdx.x) * top : nullptr;
       if (SPLIT && k < top && (int)threadIdx.x >= k && (int)threadIdx.x < top)
         mine[threadIdx.x] = 0;   // a chunk shorter than the list
-      select_top<BF>(z, n, group, k, [&](int rank, uint64_t key) {
+      select_top<BF, THREADS>(z, n, group, k, [&](int rank, uint64_t key) {
         const uint32_t index = ~(uint32_t)key;
         if (SPLIT) {
           mine[rank] = (key & 0xffffffff00000000ull) | (uint32_t)~(index + (uint32_t)lo);
@@ -315,26 +393,46 @@ __global__ __launch_bounds__(kThreads) void dora_logprob_fwd(
   }
 }
 
-// Joins the chunks of a row: their statistics in order, and the first k of their
-// sorted lists.  A key below the k-th best of the lists' heads (where there are k
-// lists) or below any list's last is out; at most kMaxTop^2 remain.
-constexpr int kJoinCap = kMaxTop * kMaxTop;
+// Joins the chunks of a row: their statistics, and the first k of their sorted
+// lists.  Every wave takes up to 128 of the lists' foremost keys; what is below
+// the k-th of those, or below the last of any one list, is out, and the rest is
+// ranked.  The dynamic LDS holds all keys (at most kMaxSplits kMaxTop), which
+// many equal logits may leave.
+static_assert(kMaxSplits == 64, "a list per lane");
 template <bool BF, bool TOP>
 __global__ __launch_bounds__(kThreads) void dora_logprob_join(
     const void* logits, int64_t ld, const int64_t* targets, const Stat* part,
     const uint64_t* part_top, int splits, float* logp, float* entropy, float* lse, float* top_logp,
     int64_t* top_index, int64_t rows, int64_t V, int top, float scale) {
   using E = Elem<BF>;
-  __shared__ Stat stats[kMaxSplits];
-  __shared__ uint64_t heads[TOP ? kMaxSplits : 1];
-  __shared__ uint64_t list[TOP ? kJoinCap : 1];
+  extern __shared__ uint64_t list[];
   __shared__ uint32_t count;
-  __shared__ unsigned long long bound;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 63;
   const float c2 = scale * kLog2e;
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
     const int64_t y = targets[row];
-    if (y < 0 || y >= V) {
+    const Stat* stats = part + row * splits;
+    const uint64_t* lists = TOP ? part_top + row * splits * top : nullptr;
+    Stat a = empty_stat();
+    uint32_t front[2] = {0, 0};
+    uint64_t last = 0;
+    const bool live = y >= 0 && y < V;
+    if (live) {
+      if (lane < splits) a = stats[lane];
+      if (TOP) {
+        // the front: the first `deep` keys of every list
+        const int deep = min(top, max(1, 128 / splits));
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int i = lane + 64 * q;
+          if (i < splits * deep)
+            front[q] = (uint32_t)(lists[(int64_t)(i / deep) * top + i % deep] >> 32);
+        }
+        if (lane < splits) last = lists[(int64_t)lane * top + top - 1];
+      }
+    }
+    if (tid == 0) count = 0;
+    if (!live) {
       if (tid == 0) {
         logp[row] = 0.f;
         if (entropy) entropy[row] = 0.f;
@@ -347,33 +445,19 @@ __global__ __launch_bounds__(kThreads) void dora_logprob_join(
       continue;
     }
     const float at = E::get(reinterpret_cast<const typename E::T*>(logits) + row * ld + y);
-    const uint64_t* lists = TOP ? part_top + row * splits * top : nullptr;
-    if (tid < splits) {
-      stats[tid] = part[row * splits + tid];
-      if (TOP) heads[tid] = lists[(int64_t)tid * top];
-    }
-    if (tid == 0) {
-      count = 0;
-      bound = 0;
-    }
-    __syncthreads();
-    Stat a = stats[0];
-    for (int i = 1; i < splits; ++i) a = merge(a, stats[i], c2);
-    const RowOut out = row_out(a, at, scale);
+    const RowOut out = row_out(wave_stat(a, c2), at, scale);
     if (tid == 0) {
       logp[row] = out.logp;
       if (entropy) entropy[row] = out.entropy;
       if (lse) lse[row] = out.lse;
     }
     if (TOP) {
-      if (tid < splits) {
-        const uint64_t last = lists[(int64_t)tid * top + top - 1];
-        atomicMax(&bound, (unsigned long long)last);
-        if (splits >= top && rank_in(heads[tid], heads, splits) == top - 1)
-          atomicMax(&bound, (unsigned long long)heads[tid]);
-      }
-      __syncthreads();
-      const uint64_t least = max((uint64_t)bound, (uint64_t)1);   // 0 pads short lists
+      __syncthreads();   // count is 0
+      const uint32_t x = kth_largest<2>(front, top);
+      const uint32_t hi = wave_max((uint32_t)(last >> 32));
+      const uint32_t low = wave_max((uint32_t)(last >> 32) == hi ? (uint32_t)last : 0u);
+      // at least 1: keys of 0 pad short lists
+      const uint64_t least = max(max((uint64_t)x << 32, ((uint64_t)hi << 32) | low), (uint64_t)1);
       for (int i = tid; i < splits * top; i += kThreads) {
         const uint64_t key = lists[i];
         if (key >= least) list[atomicAdd(&count, 1u)] = key;
@@ -389,63 +473,95 @@ __global__ __launch_bounds__(kThreads) void dora_logprob_join(
           top_logp[row * top + rank] = out.none ? kNegInf : (v - out.ref) * scale - out.log_s;
         }
       }
+      __syncthreads();
     }
-    __syncthreads();
   }
 }
 
-template <bool BF>
+// Gradient of a row's chunk blockIdx.x of kBwdChunk elements.  The logits are
+// loaded before the row's scalars are known; one exponential per element and no
+// reduction, so memory bounds it.  THROUGH: the gradient does not fit the
+// last-level cache and is stored past it (4096 x 131072 bf16: 326 us against
+// 340, 6.2 TB/s; where it fits, its reader finds it there).
+constexpr int kBwdU = 4;
+template <bool BF, bool THROUGH>
 __global__ __launch_bounds__(kThreads) void dora_logprob_bwd(
     const float* g_logp, const float* g_entropy, const void* logits, int64_t ld,
     const int64_t* targets, const float* lse, const float* entropy, void* grad, int64_t rows,
     int64_t V, float scale) {
   using E = Elem<BF>;
   using T = typename E::T;
+  constexpr int kStep = kThreads * E::kN;
   __shared__ Stat lds[kWaves];
-  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
-  __syncthreads();   // the previous row's reductions have been read
-  const T* z = reinterpret_cast<const T*>(logits) + row * ld;
-  T* gz = reinterpret_cast<T*>(grad) + row * V;
-  const int64_t y = targets[row];
-  bool zero = y < 0 || y >= V;
-  float ref = 0.f, log_s = 0.f;
-  if (!zero) {
-    log_s = lse[row];
-    if (!(fabsf(log_s) <= kCoarseLse)) {
+  const int64_t j0 = (int64_t)blockIdx.x * kStep * kBwdU + threadIdx.x * E::kN;
+  auto store = [&](T* gz, int64_t j, const float* v) {
+    if (THROUGH && j + E::kN <= V)
+      E::store_through(gz + j, v);
+    else
+      store_part<BF>(gz, j, V, v);
+  };
+  for (int64_t row = blockIdx.y; row < rows; row += gridDim.y) {
+    const T* z = reinterpret_cast<const T*>(logits) + row * ld;
+    T* gz = reinterpret_cast<T*>(grad) + row * V;
+    const int64_t y = targets[row];
+    if (y < 0 || y >= V) {
+      float o[E::kN] = {};
+#pragma unroll
+      for (int u = 0; u < kBwdU; ++u) store(gz, j0 + u * kStep, o);
+      continue;
+    }
+    typename E::Vec raw[kBwdU];
+#pragma unroll
+    for (int u = 0; u < kBwdU; ++u)
+      if (j0 + u * kStep + E::kN <= V) raw[u] = E::raw(z + j0 + u * kStep);
+    float ref = 0.f, log_s = lse[row];
+    bool zero = false;
+    if (!(fabsf(log_s) <= kCoarseLse)) {   // the same for the whole workgroup
       Stat st = empty_stat();
-      for (int64_t j = (int64_t)threadIdx.x * E::kN; j < V; j += kThreads * E::kN) {
+      for (int64_t j = (int64_t)threadIdx.x * E::kN; j < V; j += kStep) {
         float v[E::kN];
         load_part<BF>(z, j, V, kNegInf, v);
         add_logits<E::kN>(st, v, scale * kLog2e);
       }
-      const RowOut r = row_out(block_stat(st, scale * kLog2e, lds), 0.f, scale);
+      const RowOut r = row_out(block_stat<kWaves>(st, scale * kLog2e, lds), 0.f, scale);
       zero = r.none;
       ref = r.ref;
       log_s = r.log_s;
+      __syncthreads();   // lds is written again for the next row
     }
-  }
-  const float a = g_logp ? g_logp[row] : 0.f;
-  const float b = g_entropy ? g_entropy[row] : 0.f;
-  const float H = g_entropy ? entropy[row] : 0.f;
-  for (int64_t j = (int64_t)threadIdx.x * E::kN; j < V; j += kThreads * E::kN) {
-    float v[E::kN], o[E::kN];
-    load_part<BF>(z, j, V, kNegInf, v);
+    const float a = zero || !g_logp ? 0.f : g_logp[row];
+    const float b = zero || !g_entropy ? 0.f : g_entropy[row];
+    const float H = g_entropy ? entropy[row] : 0.f;
 #pragma unroll
-    for (int q = 0; q < E::kN; ++q) {
-      const float d = fmaf(v[q] - ref, scale, -log_s);
-      const float p = exp2f(d * kLog2e);
-      const float inner = p > 0.f ? d + H : 0.f;
-      float g = -p * fmaf(b, inner, a);
-      if (j + q == y) g += a;
-      o[q] = zero ? 0.f : g * scale;
+    for (int u = 0; u < kBwdU; ++u) {
+      const int64_t j = j0 + u * kStep;
+      if (j >= V) break;
+      float v[E::kN];
+      if (j + E::kN <= V)
+        E::decode(raw[u], v);
+      else
+        load_part<BF>(z, j, V, kNegInf, v);
+#pragma unroll
+      for (int q = 0; q < E::kN; ++q) {
+        const float d = fmaf(v[q] - ref, scale, -log_s);
+        const float p = __builtin_amdgcn_exp2f(d * kLog2e);
+        // p (log p + H) is 0 where p is; d is NaN where a row is lost
+        const float inner = p > 0.f ? d + H : 0.f;
+        v[q] = -p * fmaf(b, inner, a) * scale;
+        if (zero) v[q] = 0.f;
+      }
+      if (y >= j && y < j + E::kN) {
+#pragma unroll
+        for (int q = 0; q < E::kN; ++q)
+          if (j + q == y) v[q] = fmaf(a, scale, v[q]);
+      }
+      store(gz, j, v);
     }
-    store_part<BF>(gz, j, V, o);
-  }
   }
 }
 
 constexpr int64_t kLimit = int64_t(1) << 31;
-constexpr int64_t kMaxVocab = kMaxSplits * kMaxChunk;   // 2^24
+constexpr int64_t kMaxVocab = kMaxSplits * kMaxChunk;   // 2^23
 
 bool shape_ok(const dora_logprob_shape& s) {
   return s.rows >= 0 && s.rows < kLimit && s.vocab >= 1 && s.vocab <= kMaxVocab && s.ld >= s.vocab &&
@@ -463,28 +579,30 @@ int check_shape(const dora_logprob_shape* s) {
 
 // How many workgroups read a row.  With rows enough to give every CU a few
 // workgroups each row is one workgroup's; below that rows are cut until about
-// kWantBlocks workgroups run, no chunk under kMinChunk elements.
+// kWantBlocks workgroups run, no chunk under kU vectors a thread.
 constexpr int64_t kWantBlocks = 1024;
-constexpr int64_t kMinChunk = 4096;
 struct Plan {
   int64_t chunk, splits;
   size_t stat_bytes, top_bytes;
 };
 Plan plan(const dora_logprob_shape& s) {
   Plan p;
-  const int64_t most = std::min(kMaxSplits, std::max<int64_t>(1, s.vocab / kMinChunk));
+  const int64_t unit = kThreads * kU * (s.dtype == DORA_BF16 ? 8 : 4);
+  const int64_t most = std::min(kMaxSplits, std::max<int64_t>(1, s.vocab / unit));
   const int64_t want = std::max<int64_t>(1, kWantBlocks / std::max<int64_t>(1, s.rows));
   const int64_t least = (s.vocab + kMaxChunk - 1) / kMaxChunk;
   const int64_t n = std::max(least, std::min(want, most));
-  p.chunk = std::min(kMaxChunk, ((s.vocab + n - 1) / n + 2047) / 2048 * 2048);
+  p.chunk = std::min(kMaxChunk, ((s.vocab + n - 1) / n + unit - 1) / unit * unit);
   p.splits = (s.vocab + p.chunk - 1) / p.chunk;
   const int64_t parts = p.splits > 1 ? s.rows * p.splits : 0;
   p.stat_bytes = (size_t)((parts * (int64_t)sizeof(Stat) + 15) / 16 * 16);
   p.top_bytes = (size_t)(parts * s.top * 8);
   return p;
 }
+// Short rows are one wave's: no barriers, and four times the rows in flight.
+constexpr int64_t kWaveVocab = 4096;
 
-template <bool BF, bool TOP, bool SPLIT>
+template <bool BF, int THREADS, bool TOP, bool SPLIT>
 hipError_t launch_fwd(const dora_logprob_shape& s, const Plan& p, const void* logits,
                       const int64_t* targets, float* logp, float* entropy, float* lse,
                       float* top_logp, int64_t* top_index, Stat* part, uint64_t* part_top,
@@ -495,8 +613,8 @@ hipError_t launch_fwd(const dora_logprob_shape& s, const Plan& p, const void* lo
                             : 0;
   {
     LaunchTimer t("logprob_fwd", st);
-    hipLaunchKernelGGL((dora_logprob_fwd<BF, TOP, SPLIT>), dim3((unsigned)p.splits, rows),
-                       dim3(kThreads), groups, st, logits, s.ld, targets, logp, entropy, lse,
+    hipLaunchKernelGGL((dora_logprob_fwd<BF, THREADS, TOP, SPLIT>), dim3((unsigned)p.splits, rows),
+                       dim3(THREADS), groups, st, logits, s.ld, targets, logp, entropy, lse,
                        top_logp, top_index, part, part_top, s.rows, s.vocab, p.chunk, (int)s.top,
                        s.scale);
     if (hipError_t e = hipGetLastError()) return e;
@@ -504,8 +622,9 @@ hipError_t launch_fwd(const dora_logprob_shape& s, const Plan& p, const void* lo
   if (!SPLIT) return hipSuccess;
   LaunchTimer t("logprob_join", st);
   hipLaunchKernelGGL((dora_logprob_join<BF, TOP>), dim3((unsigned)std::min(s.rows, kMaxGrid)),
-                     dim3(kThreads), 0, st, logits, s.ld, targets, part, part_top, (int)p.splits,
-                     logp, entropy, lse, top_logp, top_index, s.rows, s.vocab, (int)s.top, s.scale);
+                     dim3(kThreads), TOP ? (size_t)(p.splits * s.top * 8) : 0, st, logits, s.ld,
+                     targets, part, part_top, (int)p.splits, logp, entropy, lse, top_logp,
+                     top_index, s.rows, s.vocab, (int)s.top, s.scale);
   return hipGetLastError();
 }
 
@@ -520,9 +639,12 @@ hipError_t forward(const dora_logprob_shape& s, const void* logits, const int64_
   auto go = [&](auto fn) {
     return fn(s, p, logits, targets, logp, entropy, lse, top_logp, top_index, part, part_top, st);
   };
+  constexpr int N = kThreads;
   if (p.splits > 1)
-    return s.top > 0 ? go(launch_fwd<BF, true, true>) : go(launch_fwd<BF, false, true>);
-  return s.top > 0 ? go(launch_fwd<BF, true, false>) : go(launch_fwd<BF, false, false>);
+    return s.top > 0 ? go(launch_fwd<BF, N, true, true>) : go(launch_fwd<BF, N, false, true>);
+  if (s.vocab <= kWaveVocab)
+    return s.top > 0 ? go(launch_fwd<BF, 64, true, false>) : go(launch_fwd<BF, 64, false, false>);
+  return s.top > 0 ? go(launch_fwd<BF, N, true, false>) : go(launch_fwd<BF, N, false, false>);
 }
 
 template <bool BF>
@@ -530,8 +652,17 @@ hipError_t backward(const dora_logprob_shape& s, const float* g_logp, const floa
                     const void* logits, const int64_t* targets, const float* lse,
                     const float* entropy, void* grad, hipStream_t st) {
   LaunchTimer t("logprob_bwd", st);
-  hipLaunchKernelGGL((dora_logprob_bwd<BF>), dim3((unsigned)std::min(s.rows, kMaxGrid)), dim3(kThreads),
-                     0, st, g_logp, g_entropy, logits, s.ld, targets, lse, entropy, grad, s.rows, s.vocab, s.scale);
+  const int64_t per = kThreads * Elem<BF>::kN * kBwdU;
+  const dim3 grid((unsigned)((s.vocab + per - 1) / per),
+                  (unsigned)std::min<int64_t>(s.rows, 65535));
+  constexpr double kLastLevel = 256.0 * (1 << 20);
+  if ((double)s.rows * (double)s.vocab * sizeof(typename Elem<BF>::T) > kLastLevel)
+    hipLaunchKernelGGL((dora_logprob_bwd<BF, true>), grid, dim3(kThreads), 0, st, g_logp, g_entropy,
+                       logits, s.ld, targets, lse, entropy, grad, s.rows, s.vocab, s.scale);
+  else
+    hipLaunchKernelGGL((dora_logprob_bwd<BF, false>), grid, dim3(kThreads), 0, st, g_logp,
+                       g_entropy, logits, s.ld, targets, lse, entropy, grad, s.rows, s.vocab,
+                       s.scale);
   return hipGetLastError();
 }
 
