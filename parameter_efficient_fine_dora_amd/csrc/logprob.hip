@@ -478,52 +478,63 @@ __global__ __launch_bounds__(kThreads) void dora_logprob_join(
   }
 }
 
-// Gradient of a row's chunk blockIdx.x of kBwdChunk elements.  The logits are
+// Gradient of a row's chunk blockIdx.x of kBwdU vectors per thread.  The logits are
 // loaded before the row's scalars are known; one exponential per element and no
 // reduction, so memory bounds it.  THROUGH: the gradient does not fit the
-// last-level cache and is stored past it (4096 x 131072 bf16: 326 us against
-// 340, 6.2 TB/s; where it fits, its reader finds it there).
-constexpr int kBwdU = 4;
-template <bool BF, bool THROUGH>
-__global__ __launch_bounds__(kThreads) void dora_logprob_bwd(
+// last-level cache and is stored past it (4096 x 131072 bf16: 330 us against
+// 346, 6.1 TB/s; where it fits, its reader finds it there).
+constexpr int kBwdU = 2;
+template <bool BF, int THREADS, bool THROUGH>
+__global__ __launch_bounds__(THREADS) void dora_logprob_bwd(
     const float* g_logp, const float* g_entropy, const void* logits, int64_t ld,
     const int64_t* targets, const float* lse, const float* entropy, void* grad, int64_t rows,
-    int64_t V, float scale) {
+    int V, float scale) {
   using E = Elem<BF>;
   using T = typename E::T;
-  constexpr int kStep = kThreads * E::kN;
-  __shared__ Stat lds[kWaves];
-  const int64_t j0 = (int64_t)blockIdx.x * kStep * kBwdU + threadIdx.x * E::kN;
-  auto store = [&](T* gz, int64_t j, const float* v) {
-    if (THROUGH && j + E::kN <= V)
-      E::store_through(gz + j, v);
-    else
-      store_part<BF>(gz, j, V, v);
-  };
+  constexpr int kStep = THREADS * E::kN;
+  __shared__ Stat lds[THREADS / 64];
   for (int64_t row = blockIdx.y; row < rows; row += gridDim.y) {
     const T* z = reinterpret_cast<const T*>(logits) + row * ld;
     T* gz = reinterpret_cast<T*>(grad) + row * V;
+    // the gradient's vectors lie on 16-byte boundaries; the first may start
+    // before the row
+    const int off = (int)(reinterpret_cast<uintptr_t>(gz) % 16 / sizeof(T));
+    const int j0 = (int)(blockIdx.x * kStep * kBwdU + threadIdx.x * E::kN) - off;
+    const uint32_t fits = V >= E::kN ? V - E::kN + 1 : 0;
+    auto whole = [&](int j) { return (uint32_t)j < fits; };
+    auto store = [&](int j, const float* v) {
+      if (whole(j)) {
+        if (THROUGH)
+          E::store_through(gz + j, v);
+        else
+          E::store(gz + j, v);
+      } else {
+#pragma unroll
+        for (int q = 0; q < E::kN; ++q)
+          if (j + q >= 0 && j + q < V) E::put(gz + j + q, v[q]);
+      }
+    };
     const int64_t y = targets[row];
     if (y < 0 || y >= V) {
       float o[E::kN] = {};
 #pragma unroll
-      for (int u = 0; u < kBwdU; ++u) store(gz, j0 + u * kStep, o);
+      for (int u = 0; u < kBwdU; ++u) store(j0 + u * kStep, o);
       continue;
     }
     typename E::Vec raw[kBwdU];
 #pragma unroll
     for (int u = 0; u < kBwdU; ++u)
-      if (j0 + u * kStep + E::kN <= V) raw[u] = E::raw(z + j0 + u * kStep);
+      if (whole(j0 + u * kStep)) raw[u] = E::raw(z + j0 + u * kStep);
     float ref = 0.f, log_s = lse[row];
     bool zero = false;
     if (!(fabsf(log_s) <= kCoarseLse)) {   // the same for the whole workgroup
       Stat st = empty_stat();
-      for (int64_t j = (int64_t)threadIdx.x * E::kN; j < V; j += kStep) {
+      for (int j = (int)threadIdx.x * E::kN; j < V; j += kStep) {
         float v[E::kN];
         load_part<BF>(z, j, V, kNegInf, v);
         add_logits<E::kN>(st, v, scale * kLog2e);
       }
-      const RowOut r = row_out(block_stat<kWaves>(st, scale * kLog2e, lds), 0.f, scale);
+      const RowOut r = row_out(block_stat<THREADS / 64>(st, scale * kLog2e, lds), 0.f, scale);
       zero = r.none;
       ref = r.ref;
       log_s = r.log_s;
@@ -534,13 +545,16 @@ __global__ __launch_bounds__(kThreads) void dora_logprob_bwd(
     const float H = g_entropy ? entropy[row] : 0.f;
 #pragma unroll
     for (int u = 0; u < kBwdU; ++u) {
-      const int64_t j = j0 + u * kStep;
+      const int j = j0 + u * kStep;
       if (j >= V) break;
       float v[E::kN];
-      if (j + E::kN <= V)
+      if (whole(j)) {
         E::decode(raw[u], v);
-      else
-        load_part<BF>(z, j, V, kNegInf, v);
+      } else {
+#pragma unroll
+        for (int q = 0; q < E::kN; ++q)
+          v[q] = j + q >= 0 && j + q < V ? E::get(z + j + q) : kNegInf;
+      }
 #pragma unroll
       for (int q = 0; q < E::kN; ++q) {
         const float d = fmaf(v[q] - ref, scale, -log_s);
@@ -550,12 +564,13 @@ __global__ __launch_bounds__(kThreads) void dora_logprob_bwd(
         v[q] = -p * fmaf(b, inner, a) * scale;
         if (zero) v[q] = 0.f;
       }
-      if (y >= j && y < j + E::kN) {
+      const int hit = (int)y - j;
+      if ((uint32_t)hit < (uint32_t)E::kN) {
 #pragma unroll
         for (int q = 0; q < E::kN; ++q)
-          if (j + q == y) v[q] = fmaf(a, scale, v[q]);
+          if (q == hit) v[q] = fmaf(a, scale, v[q]);
       }
-      store(gz, j, v);
+      store(j, v);
     }
   }
 }
@@ -652,18 +667,20 @@ hipError_t backward(const dora_logprob_shape& s, const float* g_logp, const floa
                     const void* logits, const int64_t* targets, const float* lse,
                     const float* entropy, void* grad, hipStream_t st) {
   LaunchTimer t("logprob_bwd", st);
-  const int64_t per = kThreads * Elem<BF>::kN * kBwdU;
-  const dim3 grid((unsigned)((s.vocab + per - 1) / per),
-                  (unsigned)std::min<int64_t>(s.rows, 65535));
+  auto launch = [&](auto kernel, int threads) {
+    const int64_t per = (int64_t)threads * Elem<BF>::kN * kBwdU;
+    hipLaunchKernelGGL(kernel,   // a row may take one vector more than its elements fill
+                       dim3((unsigned)((s.vocab + Elem<BF>::kN - 1 + per - 1) / per),
+                            (unsigned)std::min<int64_t>(s.rows, 65535)),
+                       dim3(threads), 0, st, g_logp, g_entropy, logits, s.ld, targets, lse, entropy,
+                       grad, s.rows, (int)s.vocab, s.scale);
+    return hipGetLastError();
+  };
   constexpr double kLastLevel = 256.0 * (1 << 20);
   if ((double)s.rows * (double)s.vocab * sizeof(typename Elem<BF>::T) > kLastLevel)
-    hipLaunchKernelGGL((dora_logprob_bwd<BF, true>), grid, dim3(kThreads), 0, st, g_logp, g_entropy,
-                       logits, s.ld, targets, lse, entropy, grad, s.rows, s.vocab, s.scale);
-  else
-    hipLaunchKernelGGL((dora_logprob_bwd<BF, false>), grid, dim3(kThreads), 0, st, g_logp,
-                       g_entropy, logits, s.ld, targets, lse, entropy, grad, s.rows, s.vocab,
-                       s.scale);
-  return hipGetLastError();
+    return launch(dora_logprob_bwd<BF, kThreads, true>, kThreads);
+  if (s.vocab <= kWaveVocab) return launch(dora_logprob_bwd<BF, 64, false>, 64);
+  return launch(dora_logprob_bwd<BF, kThreads, false>, kThreads);
 }
 
 }  // namespace
