@@ -337,7 +337,7 @@ DORA_API int dora_token_logprob_backward(const dora_logprob_shape* shape, const 
  *   exp_avg     int8 c,  value = exp_avg_scale c |c| / 127^2
  *   exp_avg_sq  uint8 u, its square root = exp_avg_sq_scale (u / 255)^2
  * with the block's largest magnitude as scale and codes rounded to nearest
- * even; a nonzero second moment keeps u >= 1.  Squared codes spend their steps
+ * even; a second moment of 2^-126 or more keeps u >= 1.  Squared codes spend their steps
  * on the small values: a step is 1.6% of a value at the block's largest and 16%
  * at a hundredth of it.
  */

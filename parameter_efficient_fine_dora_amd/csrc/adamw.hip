@@ -3,6 +3,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "../../include/dora.h"
 #include "elem.h"
@@ -14,27 +15,43 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kVec = 8;                          // elements per thread and step
-constexpr int kChunk = kThreads * kVec * 2;      // elements per workgroup
+constexpr int kU = 2;                            // steps of a workgroup, all loaded first
+constexpr int kChunk = kThreads * kVec * kU;     // elements per workgroup
 constexpr int kGroup = DORA_STATE_BLOCK / kVec;  // lanes that share an 8-bit block
 static_assert(kGroup == 16, "an 8-bit block is one 16-lane row of a wave");
-static_assert(kChunk % DORA_STATE_BLOCK == 0, "workgroups start at 8-bit blocks");
+static_assert(kThreads * kVec % DORA_STATE_BLOCK == 0, "steps start at 8-bit blocks");
 
-// The tensors of a launch travel in the kernel's arguments (under 4 KB), so a
-// call needs no device table and no copy.  first[i] is the first workgroup of
-// tensor i; workgroups past the last tensor do not exist.
-constexpr int kMaxTensors = 54;
-struct StepArgs {
-  dora_adamw_tensor t[kMaxTensors];
-  uint32_t first[kMaxTensors];
-  int count;
+// The tensors of a launch travel in the kernel's arguments (under 4 KB, with as
+// many tensors as fit), so a call needs no device table and no copy.  first[i]
+// is the first workgroup of tensor i; workgroups past the last tensor do not
+// exist.
+struct StepNumbers {
   float beta1, beta2, c1, c2;   // c = 1 - beta
   float eps, decay;             // decay = 1 - lr weight_decay
   float step_size, inv_root;    // lr / (1 - beta1^t), 1 / sqrt(1 - beta2^t)
   const float* grad_scale;
+  int count;
 };
-static_assert(sizeof(StepArgs) <= 4096, "kernel arguments");
+template <bool MASTER, bool S8>
+struct StepArgs {
+  static constexpr int kMax =
+      (4096 - (int)sizeof(StepNumbers) - 8) / (8 * (5 + (S8 ? 2 : 0) + (MASTER ? 1 : 0)) + 4);
+  StepNumbers h;
+  int64_t n[kMax];
+  void* param[kMax];
+  const void* grad[kMax];
+  void* exp_avg[kMax];
+  void* exp_avg_sq[kMax];
+  float* exp_avg_scale[S8 ? kMax : 1];
+  float* exp_avg_sq_scale[S8 ? kMax : 1];
+  float* master[MASTER ? kMax : 1];
+  uint32_t first[kMax];
+};
+static_assert(sizeof(StepArgs<true, true>) <= 4096 && sizeof(StepArgs<true, false>) <= 4096 &&
+                  sizeof(StepArgs<false, true>) <= 4096 && sizeof(StepArgs<false, false>) <= 4096,
+              "kernel arguments");
 
-constexpr int kMaxGrads = 160;
+constexpr int kMaxGrads = 200;
 struct NormArgs {
   const void* g[kMaxGrads];
   int64_t n[kMaxGrads];
@@ -43,17 +60,15 @@ struct NormArgs {
 };
 static_assert(sizeof(NormArgs) <= 4096, "kernel arguments");
 
-// Index of the tensor that workgroup b belongs to: the last with first <= b.
+// The tensor that workgroup b belongs to, the last with first <= b: every lane
+// compares some, one ballot counts.
 __device__ __forceinline__ int tensor_of(const uint32_t* first, int count, uint32_t b) {
-  int lo = 0, hi = count - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (first[mid] <= b)
-      lo = mid;
-    else
-      hi = mid - 1;
+  int n = 0;
+  for (int i = 0; i < count; i += 64) {
+    const int k = i + (int)(threadIdx.x & 63);
+    n += __popcll(__ballot(k < count && first[min(k, count - 1)] <= b));
   }
-  return lo;
+  return n - 1;
 }
 
 template <bool BF>
@@ -91,101 +106,154 @@ __device__ __forceinline__ void store_codes(void* p, int64_t i, int64_t n, u32x2
     if (i + k < n) q[k] = (uint8_t)(v[k >> 2] >> (8 * (k & 3)));
 }
 
-// Signed codes: value = scale c |c| / 127^2.  Unsigned: scale (u / 255)^2.
+// Signed codes: value = scale c |c| / 127^2, read as c + 128 (one conversion
+// from a byte).  Unsigned: scale (u / 255)^2.
+constexpr uint32_t kFlip = 0x80808080u;
 template <bool SIGNED>
 __device__ __forceinline__ void decode8(u32x2 codes, float scale, float* out) {
   const float unit = scale * (SIGNED ? 1.f / (127.f * 127.f) : 1.f / (255.f * 255.f));
 #pragma unroll
   for (int k = 0; k < kVec; ++k) {
-    const uint32_t byte = (codes[k >> 2] >> (8 * (k & 3))) & 0xffu;
-    const float c = SIGNED ? (float)(int8_t)byte : (float)byte;
-    out[k] = SIGNED ? c * fabsf(c) * unit : c * c * unit;
+    const uint32_t word = codes[k >> 2] ^ (SIGNED ? kFlip : 0u);
+    const float byte = (float)((word >> (8 * (k & 3))) & 0xffu);
+    const float c = SIGNED ? byte - 128.f : byte;
+    out[k] = c * fabsf(c) * unit;
   }
 }
 
-// Largest magnitude of an 8-bit block, held by 16 lanes of 8.  Compared as
-// whole numbers: a NaN is above every number and is kept.
+// Largest magnitude of an 8-bit block, held by 16 lanes of 8; a NaN is kept.
+__device__ __forceinline__ float maxnan(float a, float b) {
+  return __builtin_elementwise_maximum(a, b);
+}
 __device__ __forceinline__ float block_scale(const float* v) {
-  uint32_t m = 0;
+  float m = fabsf(v[0]);
 #pragma unroll
-  for (int k = 0; k < kVec; ++k) m = max(m, __float_as_uint(v[k]) & 0x7fffffffu);
-#pragma unroll
-  for (int off = kGroup / 2; off > 0; off >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, off, 64));
-  return __uint_as_float(m);
+  for (int k = 1; k < kVec; ++k) m = maxnan(m, fabsf(v[k]));
+  m = maxnan(m, dpp_move<0xB1>(m));
+  m = maxnan(m, dpp_move<0x4E>(m));
+  m = maxnan(m, dpp_move<0x141>(m));
+  return maxnan(m, dpp_move<0x140>(m));
 }
 
-// Codes of eight values, |c| = round(most sqrt(|v| / scale)).  A block whose
-// scale is not finite keeps that scale and codes of 0: all its values read back
-// as NaN.
+// Codes of eight values, |c| = most sqrt(|v| / scale) rounded to nearest even by
+// the conversion that puts a float into a byte (v_cvt_pk_u8_f32, which clamps to
+// 0 .. 255; signed codes go through c + 128).  Reciprocal and root are the
+// hardware's, 1 ulp each: far below the half step that rounding to a code costs.
+// Scales outside their range are divided by.  A block whose scale is not finite
+// keeps that scale and codes of 0: its values read back as NaN.
 template <bool SIGNED>
 __device__ __forceinline__ u32x2 encode8(const float* v, float scale) {
-  const float most = SIGNED ? 127.f : 255.f;
-  const bool ok = scale > 0.f && scale < __builtin_huge_valf();
-  // the smallest scales have no finite reciprocal
-  const float inv = 1.f / scale;
-  const bool tiny = !(inv < __builtin_huge_valf());
+  constexpr float most = SIGNED ? 127.f : 255.f;
+  const bool usual = scale > 0x1p-100f && scale < 0x1p100f;
+  const float inv = usual ? __builtin_amdgcn_rcpf(scale) : 0.f;
   u32x2 codes = {0u, 0u};
+  auto put = [&](int k, float root) {
+    float f;
+    if (SIGNED)
+      f = fmaf(most, copysignf(root, v[k]), 128.f);
+    else   // a nonzero value keeps code 1
+      f = fmaxf(most * root, __builtin_amdgcn_fmed3f(v[k] * 3e38f, 0.f, 1.f));
+    codes[k >> 2] = __builtin_amdgcn_cvt_pk_u8_f32(f, k & 3, codes[k >> 2]);
+  };
 #pragma unroll
-  for (int k = 0; k < kVec; ++k) {
-    const float share = tiny ? fabsf(v[k]) / scale : fabsf(v[k]) * inv;
-    float c = rintf(most * sqrtf(share));
-    c = fminf(c, most);
-    if (!SIGNED && v[k] > 0.f) c = fmaxf(c, 1.f);
-    int code = ok ? (int)c : 0;
-    if (SIGNED && v[k] < 0.f) code = -code;
-    codes[k >> 2] |= ((uint32_t)code & 0xffu) << (8 * (k & 3));
+  for (int k = 0; k < kVec; ++k) put(k, __builtin_amdgcn_sqrtf(fabsf(v[k]) * inv));
+  if (SIGNED) codes ^= kFlip;
+  if (!usual) {
+    codes = u32x2{0u, 0u};
+    if (scale > 0.f && scale < __builtin_huge_valf()) {
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) put(k, sqrtf(fabsf(v[k]) / scale));
+      if (SIGNED) codes ^= kFlip;
+    }
   }
   return codes;
 }
 
 // ---- the step -------------------------------------------------------------------
+// Eight elements: the moments, their root (into r) and the parameter.  Division
+// by the root is a product with the hardware's reciprocal (1 ulp).
+__device__ __forceinline__ void update8(const StepNumbers& h, float gs, const float* g, float* p,
+                                        float* m, float* v, float* r) {
+#pragma unroll
+  for (int k = 0; k < kVec; ++k) {
+    const float gk = g[k] * gs;
+    m[k] = fmaf(h.beta1, m[k], h.c1 * gk);
+    v[k] = fmaf(h.beta2, v[k], h.c2 * gk * gk);
+    r[k] = __builtin_amdgcn_sqrtf(v[k]);
+    const float inv = __builtin_amdgcn_rcpf(fmaf(r[k], h.inv_root, h.eps));
+    p[k] = fmaf(-h.step_size, m[k] * inv, p[k] * h.decay);
+  }
+}
+
 template <bool PBF, bool GBF, bool MASTER, bool S8>
-__global__ __launch_bounds__(kThreads) void dora_adamw_kernel(const StepArgs a) {
-  const int ti = tensor_of(a.first, a.count, blockIdx.x);
-  const dora_adamw_tensor& t = a.t[ti];
-  const int64_t n = t.n;
-  const float gs = a.grad_scale ? *a.grad_scale : 1.f;
-  const int64_t base = (int64_t)(blockIdx.x - a.first[ti]) * kChunk + threadIdx.x * kVec;
-  for (int64_t i = base; i < base + kChunk; i += kThreads * kVec) {
-    // an 8-bit block's 16 lanes stay together: those past the end carry zeros
-    const int64_t block = i / DORA_STATE_BLOCK;
-    if (i >= n && (!S8 || block * DORA_STATE_BLOCK >= n)) break;
-    float p[kVec], g[kVec], m[kVec], v[kVec], r[kVec];
-    if (MASTER)
-      load8<false>(t.master, i, n, p);
-    else
-      load8<PBF>(t.param, i, n, p);
-    load8<GBF>(t.grad, i, n, g);
+__global__ __launch_bounds__(kThreads) void dora_adamw_kernel(const StepArgs<MASTER, S8> a) {
+  const int t = __builtin_amdgcn_readfirstlane(tensor_of(a.first, a.h.count, blockIdx.x));
+  const int64_t n = a.n[t];
+  const float gs = a.h.grad_scale ? *a.h.grad_scale : 1.f;
+  const int64_t start = (int64_t)(blockIdx.x - a.first[t]) * kChunk;
+  const int64_t base = start + threadIdx.x * kVec;
+  void* param = a.param[t];
+  const void* grad = a.grad[t];
+  void* exp_avg = a.exp_avg[t];
+  void* exp_avg_sq = a.exp_avg_sq[t];
+  float* ms = S8 ? a.exp_avg_scale[t] : nullptr;
+  float* vs = S8 ? a.exp_avg_sq_scale[t] : nullptr;
+  void* weight = MASTER ? (void*)a.master[t] : param;
+  struct In {
+    float p[kVec], g[kVec], m[kVec], v[kVec];
+    u32x2 mc, vc;
+    float msc, vsc;
+  };
+  auto load = [&](In& x, int64_t i, int64_t n) {
+    load8<PBF && !MASTER>(weight, i, n, x.p);
+    load8<GBF>(grad, i, n, x.g);
     if (S8) {
-      decode8<true>(load_codes(t.exp_avg, i, n), t.exp_avg_scale[block], m);
-      decode8<false>(load_codes(t.exp_avg_sq, i, n), t.exp_avg_sq_scale[block], r);
-#pragma unroll
-      for (int k = 0; k < kVec; ++k) v[k] = r[k] * r[k];
+      x.mc = load_codes(exp_avg, i, n);
+      x.vc = load_codes(exp_avg_sq, i, n);
+      x.msc = ms[i / DORA_STATE_BLOCK];
+      x.vsc = vs[i / DORA_STATE_BLOCK];
     } else {
-      load8<false>(t.exp_avg, i, n, m);
-      load8<false>(t.exp_avg_sq, i, n, v);
+      load8<false>(exp_avg, i, n, x.m);
+      load8<false>(exp_avg_sq, i, n, x.v);
     }
-#pragma unroll
-    for (int k = 0; k < kVec; ++k) {
-      const float gk = g[k] * gs;
-      m[k] = fmaf(a.beta1, m[k], a.c1 * gk);
-      v[k] = fmaf(a.beta2, v[k], a.c2 * gk * gk);
-      r[k] = sqrtf(v[k]);
-      p[k] = fmaf(-a.step_size, m[k] / fmaf(r[k], a.inv_root, a.eps), p[k] * a.decay);
-    }
-    if (MASTER) store8<false>(t.master, i, n, p);
-    store8<PBF>(t.param, i, n, p);
+  };
+  auto step = [&](In& x, int64_t i, int64_t n) {
+    float r[kVec];
     if (S8) {
-      const float ms = block_scale(m), rs = block_scale(r);
-      store_codes(t.exp_avg, i, n, encode8<true>(m, ms));
-      store_codes(t.exp_avg_sq, i, n, encode8<false>(r, rs));
+      decode8<true>(x.mc, x.msc, x.m);
+      decode8<false>(x.vc, x.vsc, x.v);
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) x.v[k] *= x.v[k];
+    }
+    update8(a.h, gs, x.g, x.p, x.m, x.v, r);
+    if (MASTER) store8<false>(weight, i, n, x.p);
+    store8<PBF>(param, i, n, x.p);
+    if (S8) {
+      const float m_scale = block_scale(x.m), v_scale = block_scale(r);
+      store_codes(exp_avg, i, n, encode8<true>(x.m, m_scale));
+      store_codes(exp_avg_sq, i, n, encode8<false>(r, v_scale));
       if ((threadIdx.x & (kGroup - 1)) == 0) {
-        t.exp_avg_scale[block] = ms;
-        t.exp_avg_sq_scale[block] = rs;
+        ms[i / DORA_STATE_BLOCK] = m_scale;
+        vs[i / DORA_STATE_BLOCK] = v_scale;
       }
     } else {
-      store8<false>(t.exp_avg, i, n, m);
-      store8<false>(t.exp_avg_sq, i, n, v);
+      store8<false>(exp_avg, i, n, x.m);
+      store8<false>(exp_avg_sq, i, n, x.v);
+    }
+  };
+  if (start + kChunk <= n) {
+    In x[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) load(x[u], base + u * kThreads * kVec, INT64_MAX);
+#pragma unroll
+    for (int u = 0; u < kU; ++u) step(x[u], base + u * kThreads * kVec, INT64_MAX);
+  } else {
+    // an 8-bit block's 16 lanes stay together: those past the end carry zeros
+    const int64_t last = S8 ? (n + DORA_STATE_BLOCK - 1) / DORA_STATE_BLOCK * DORA_STATE_BLOCK : n;
+    for (int64_t i = base; i < last && i < base + kChunk; i += kThreads * kVec) {
+      In x;
+      load(x, i, n);
+      step(x, i, n);
     }
   }
 }
@@ -204,16 +272,19 @@ __device__ __forceinline__ double block_sum_f64(double v, double* lds) {
 template <bool GBF>
 __global__ __launch_bounds__(kThreads) void dora_grad_norm_parts(const NormArgs a, double* part) {
   __shared__ double lds[kThreads / 64];
-  const int ti = tensor_of(a.first, a.count, blockIdx.x);
-  const int64_t n = a.n[ti];
-  const int64_t base = (int64_t)(blockIdx.x - a.first[ti]) * kChunk + threadIdx.x * kVec;
-  double sum = 0.0;
-  for (int64_t i = base; i < base + kChunk && i < n; i += kThreads * kVec) {
-    float g[kVec];
-    load8<GBF>(a.g[ti], i, n, g);
+  const int t = __builtin_amdgcn_readfirstlane(tensor_of(a.first, a.count, blockIdx.x));
+  const int64_t n = a.n[t];
+  const int64_t start = (int64_t)(blockIdx.x - a.first[t]) * kChunk;
+  const int64_t base = start + threadIdx.x * kVec;
+  float g[kU][kVec];
+  const int64_t limit = start + kChunk <= n ? INT64_MAX : n;
 #pragma unroll
-    for (int k = 0; k < kVec; ++k) sum = fma((double)g[k], (double)g[k], sum);
-  }
+  for (int u = 0; u < kU; ++u) load8<GBF>(a.g[t], base + u * kThreads * kVec, limit, g[u]);
+  double sum = 0.0;
+#pragma unroll
+  for (int u = 0; u < kU; ++u)
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) sum = fma((double)g[u][k], (double)g[u][k], sum);
   sum = block_sum_f64(sum, lds);
   if (threadIdx.x == 0) part[blockIdx.x] = sum;
 }
@@ -284,31 +355,57 @@ int check_tensors(const dora_adamw_tensor* t, int64_t count) {
 // runs of at most this many workgroups.
 constexpr int64_t kMaxGrid = int64_t(1) << 23;
 
-template <bool PBF, bool GBF, bool MASTER>
-void launch_step(const StepArgs& a, unsigned blocks, int bits, hipStream_t st) {
-  if (bits == 8)
-    hipLaunchKernelGGL((dora_adamw_kernel<PBF, GBF, MASTER, true>), dim3(blocks), dim3(kThreads), 0,
-                       st, a);
-  else
-    hipLaunchKernelGGL((dora_adamw_kernel<PBF, GBF, MASTER, false>), dim3(blocks), dim3(kThreads),
-                       0, st, a);
+template <bool PBF, bool GBF, bool MASTER, bool S8>
+hipError_t run_step(const dora_adamw_tensor* tensors, int64_t count, const StepNumbers& h,
+                    hipStream_t st) {
+  using Args = StepArgs<MASTER, S8>;
+  Args a;
+  a.h = h;
+  int k = 0;
+  int64_t blocks = 0;
+  auto flush = [&]() -> hipError_t {
+    if (k == 0) return hipSuccess;
+    a.h.count = k;
+    LaunchTimer timer("adamw", st);
+    hipLaunchKernelGGL((dora_adamw_kernel<PBF, GBF, MASTER, S8>), dim3((unsigned)blocks),
+                       dim3(kThreads), 0, st, a);
+    k = 0;
+    blocks = 0;
+    return hipGetLastError();
+  };
+  for (int64_t i = 0; i < count; ++i) {
+    const dora_adamw_tensor& t = tensors[i];
+    const int64_t c = chunks(t.n);
+    if (c == 0) continue;
+    if (k == Args::kMax || blocks + c > kMaxGrid)
+      if (hipError_t e = flush()) return e;
+    a.n[k] = t.n;
+    a.param[k] = t.param;
+    a.grad[k] = t.grad;
+    a.exp_avg[k] = t.exp_avg;
+    a.exp_avg_sq[k] = t.exp_avg_sq;
+    if (S8) {
+      a.exp_avg_scale[k] = t.exp_avg_scale;
+      a.exp_avg_sq_scale[k] = t.exp_avg_sq_scale;
+    }
+    if (MASTER) a.master[k] = t.master;
+    a.first[k++] = (uint32_t)blocks;
+    blocks += c;
+  }
+  return flush();
 }
 
-hipError_t run_step(const StepArgs& a, int64_t blocks, const dora_adamw_options& o, bool master,
-                    hipStream_t st) {
-  LaunchTimer timer("adamw", st);
-  const unsigned b = (unsigned)blocks;
-  const bool gbf = o.grad_dtype == DORA_BF16;
-  if (o.param_dtype == DORA_F32)
-    gbf ? launch_step<false, true, false>(a, b, o.state_bits, st)
-        : launch_step<false, false, false>(a, b, o.state_bits, st);
-  else if (master)
-    gbf ? launch_step<true, true, true>(a, b, o.state_bits, st)
-        : launch_step<true, false, true>(a, b, o.state_bits, st);
-  else
-    gbf ? launch_step<true, true, false>(a, b, o.state_bits, st)
-        : launch_step<true, false, false>(a, b, o.state_bits, st);
-  return hipGetLastError();
+// The step for the types of a call: a float32 parameter is its own master.
+hipError_t step_for(const dora_adamw_tensor* t, int64_t n, const dora_adamw_options& o, bool master,
+                    const StepNumbers& h, hipStream_t st) {
+  const bool gbf = o.grad_dtype == DORA_BF16, s8 = o.state_bits == 8;
+  auto pick = [&](auto pbf, auto mst) {
+    constexpr bool P = decltype(pbf)::value, M = decltype(mst)::value;
+    if (s8) return gbf ? run_step<P, true, M, true>(t, n, h, st) : run_step<P, false, M, true>(t, n, h, st);
+    return gbf ? run_step<P, true, M, false>(t, n, h, st) : run_step<P, false, M, false>(t, n, h, st);
+  };
+  if (o.param_dtype == DORA_F32) return pick(std::false_type(), std::false_type());
+  return master ? pick(std::true_type(), std::true_type()) : pick(std::true_type(), std::false_type());
 }
 
 bool options_ok(const dora_adamw_options& o) {
@@ -351,32 +448,18 @@ DORA_API int dora_adamw_step(const dora_adamw_tensor* tensors, int64_t count,
     DORA_CHECK(check_elem(t.master, 4, true));
   }
   if (master && o.param_dtype != DORA_BF16) return DORA_ERR_DTYPE;
-  StepArgs a;
-  a.beta1 = (float)o.beta1;
-  a.beta2 = (float)o.beta2;
-  a.c1 = (float)(1.0 - o.beta1);
-  a.c2 = (float)(1.0 - o.beta2);
-  a.eps = (float)o.eps;
-  a.decay = (float)(1.0 - o.lr * o.weight_decay);
-  a.step_size = (float)(o.lr / (1.0 - std::pow(o.beta1, (double)o.step)));
-  a.inv_root = (float)(1.0 / std::sqrt(1.0 - std::pow(o.beta2, (double)o.step)));
-  a.grad_scale = o.grad_scale;
-  a.count = 0;
-  int64_t blocks = 0;
-  hipStream_t st = reinterpret_cast<hipStream_t>(hip_stream);
-  for (int64_t i = 0; i < count; ++i) {
-    const int64_t c = chunks(tensors[i].n);
-    if (c == 0) continue;
-    if (a.count == kMaxTensors || blocks + c > kMaxGrid) {
-      HIP_TRY(run_step(a, blocks, o, master, st));
-      a.count = 0;
-      blocks = 0;
-    }
-    a.t[a.count] = tensors[i];
-    a.first[a.count++] = (uint32_t)blocks;
-    blocks += c;
-  }
-  if (a.count > 0) HIP_TRY(run_step(a, blocks, o, master, st));
+  StepNumbers h;
+  h.beta1 = (float)o.beta1;
+  h.beta2 = (float)o.beta2;
+  h.c1 = (float)(1.0 - o.beta1);
+  h.c2 = (float)(1.0 - o.beta2);
+  h.eps = (float)o.eps;
+  h.decay = (float)(1.0 - o.lr * o.weight_decay);
+  h.step_size = (float)(o.lr / (1.0 - std::pow(o.beta1, (double)o.step)));
+  h.inv_root = (float)(1.0 / std::sqrt(1.0 - std::pow(o.beta2, (double)o.step)));
+  h.grad_scale = o.grad_scale;
+  h.count = 0;
+  HIP_TRY(step_for(tensors, count, o, master, h, reinterpret_cast<hipStream_t>(hip_stream)));
   return DORA_OK;
 }
 
