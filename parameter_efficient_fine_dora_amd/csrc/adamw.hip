@@ -14,12 +14,11 @@ namespace dora {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kVec = 8;                          // elements per thread and step
-constexpr int kU = 2;                            // steps of a workgroup, all loaded first
-constexpr int kChunk = kThreads * kVec * kU;     // elements per workgroup
+constexpr int kChunk = 2048;                     // elements of a step's workgroup
+constexpr int kVec = 8;                          // elements per thread where states have 8 bits
 constexpr int kGroup = DORA_STATE_BLOCK / kVec;  // lanes that share an 8-bit block
 static_assert(kGroup == 16, "an 8-bit block is one 16-lane row of a wave");
-static_assert(kThreads * kVec % DORA_STATE_BLOCK == 0, "steps start at 8-bit blocks");
+static_assert(kChunk % DORA_STATE_BLOCK == 0, "workgroups start at 8-bit blocks");
 
 // The tensors of a launch travel in the kernel's arguments (under 4 KB, with as
 // many tensors as fit), so a call needs no device table and no copy.  first[i]
@@ -51,6 +50,7 @@ static_assert(sizeof(StepArgs<true, true>) <= 4096 && sizeof(StepArgs<true, fals
                   sizeof(StepArgs<false, true>) <= 4096 && sizeof(StepArgs<false, false>) <= 4096,
               "kernel arguments");
 
+constexpr int kNormChunk = 16384;   // elements of a workgroup of the norm, all loaded first
 constexpr int kMaxGrads = 200;
 struct NormArgs {
   const void* g[kMaxGrads];
@@ -71,34 +71,74 @@ __device__ __forceinline__ int tensor_of(const uint32_t* first, int count, uint3
   return n - 1;
 }
 
-template <bool BF>
-__device__ __forceinline__ void load8(const void* p, int64_t i, int64_t n, float* out) {
-  const typename Elem<BF>::T* q = reinterpret_cast<const typename Elem<BF>::T*>(p);
+// A step touches every byte once and the next one comes a whole forward and
+// backward later, so loads and stores go past the caches (37.8M float32
+// elements with float32 states: 181 us against 201, 5.8 TB/s).  That asks for
+// accesses that fill their lines: with float32 states a thread takes four
+// elements (16 bytes of each such array), not eight.
+
+// N elements (4 or 8) of an array from element i on, by 16-byte accesses (8 bytes
+// for four bf16).  ALL: none is absent.
+template <bool BF, int N, bool ALL>
+__device__ __forceinline__ void load_n(const void* p, int64_t i, int64_t n, float* out) {
+  using E = Elem<BF>;
+  const typename E::T* q = reinterpret_cast<const typename E::T*>(p) + i;
+  if (ALL || i + N <= n) {
+    if constexpr (N >= E::kN) {
 #pragma unroll
-  for (int k = 0; k < kVec; k += Elem<BF>::kN) load_part<BF>(q, i + k, n, 0.f, out + k);
+      for (int k = 0; k < N; k += E::kN) E::decode(E::raw_past(q + k), out + k);
+    } else {
+      typedef u32x2 Half __attribute__((aligned(2)));
+      const u32x2 v = __builtin_nontemporal_load(reinterpret_cast<const Half*>(q));
+#pragma unroll
+      for (int d = 0; d < 2; ++d) {
+        out[2 * d] = bf_lo(v[d]);
+        out[2 * d + 1] = bf_hi(v[d]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; ++k) out[k] = i + k < n ? E::get(q + k) : 0.f;
+  }
 }
-template <bool BF>
-__device__ __forceinline__ void store8(void* p, int64_t i, int64_t n, const float* in) {
-  typename Elem<BF>::T* q = reinterpret_cast<typename Elem<BF>::T*>(p);
+template <bool BF, int N, bool ALL>
+__device__ __forceinline__ void store_n(void* p, int64_t i, int64_t n, const float* in) {
+  using E = Elem<BF>;
+  typename E::T* q = reinterpret_cast<typename E::T*>(p) + i;
+  if (ALL || i + N <= n) {
+    if constexpr (N >= E::kN) {
 #pragma unroll
-  for (int k = 0; k < kVec; k += Elem<BF>::kN) store_part<BF>(q, i + k, n, in + k);
+      for (int k = 0; k < N; k += E::kN) E::store_through(q + k, in + k);
+    } else {
+      typedef u32x2 Half __attribute__((aligned(2)));
+      const u32x2 v = {pack_bf16x2(in[0], in[1]), pack_bf16x2(in[2], in[3])};
+      __builtin_nontemporal_store(v, reinterpret_cast<Half*>(q));
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      if (i + k < n) E::put(q + k, in[k]);
+  }
 }
 
 // Eight codes; absent ones are 0 and are not stored.
 typedef u32x2 CodesRaw __attribute__((aligned(1)));
+template <bool ALL>
 __device__ __forceinline__ u32x2 load_codes(const void* p, int64_t i, int64_t n) {
   const uint8_t* q = reinterpret_cast<const uint8_t*>(p) + i;
-  if (i + kVec <= n) return *reinterpret_cast<const CodesRaw*>(q);
+  if (ALL || i + kVec <= n)
+    return __builtin_nontemporal_load(reinterpret_cast<const CodesRaw*>(q));
   u32x2 v = {0u, 0u};
 #pragma unroll
   for (int k = 0; k < kVec; ++k)
     if (i + k < n) v[k >> 2] |= (uint32_t)q[k] << (8 * (k & 3));
   return v;
 }
+template <bool ALL>
 __device__ __forceinline__ void store_codes(void* p, int64_t i, int64_t n, u32x2 v) {
   uint8_t* q = reinterpret_cast<uint8_t*>(p) + i;
-  if (i + kVec <= n) {
-    *reinterpret_cast<CodesRaw*>(q) = v;
+  if (ALL || i + kVec <= n) {
+    __builtin_nontemporal_store(v, reinterpret_cast<CodesRaw*>(q));
     return;
   }
 #pragma unroll
@@ -170,12 +210,13 @@ __device__ __forceinline__ u32x2 encode8(const float* v, float scale) {
 }
 
 // ---- the step -------------------------------------------------------------------
-// Eight elements: the moments, their root (into r) and the parameter.  Division
-// by the root is a product with the hardware's reciprocal (1 ulp).
-__device__ __forceinline__ void update8(const StepNumbers& h, float gs, const float* g, float* p,
-                                        float* m, float* v, float* r) {
+// N elements: the moments, their root (into r) and the parameter.  Division by
+// the root is a product with the hardware's reciprocal (1 ulp).
+template <int N>
+__device__ __forceinline__ void update(const StepNumbers& h, float gs, const float* g, float* p,
+                                       float* m, float* v, float* r) {
 #pragma unroll
-  for (int k = 0; k < kVec; ++k) {
+  for (int k = 0; k < N; ++k) {
     const float gk = g[k] * gs;
     m[k] = fmaf(h.beta1, m[k], h.c1 * gk);
     v[k] = fmaf(h.beta2, v[k], h.c2 * gk * gk);
@@ -186,75 +227,55 @@ __device__ __forceinline__ void update8(const StepNumbers& h, float gs, const fl
 }
 
 template <bool PBF, bool GBF, bool MASTER, bool S8>
-__global__ __launch_bounds__(kThreads) void dora_adamw_kernel(const StepArgs<MASTER, S8> a) {
+__global__ __launch_bounds__(kChunk / (S8 ? 8 : 4)) void dora_adamw_kernel(
+    const StepArgs<MASTER, S8> a) {
+  constexpr int N = S8 ? kVec : 4;
   const int t = __builtin_amdgcn_readfirstlane(tensor_of(a.first, a.h.count, blockIdx.x));
   const int64_t n = a.n[t];
-  const float gs = a.h.grad_scale ? *a.h.grad_scale : 1.f;
   const int64_t start = (int64_t)(blockIdx.x - a.first[t]) * kChunk;
-  const int64_t base = start + threadIdx.x * kVec;
-  void* param = a.param[t];
-  const void* grad = a.grad[t];
-  void* exp_avg = a.exp_avg[t];
-  void* exp_avg_sq = a.exp_avg_sq[t];
-  float* ms = S8 ? a.exp_avg_scale[t] : nullptr;
-  float* vs = S8 ? a.exp_avg_sq_scale[t] : nullptr;
-  void* weight = MASTER ? (void*)a.master[t] : param;
-  struct In {
-    float p[kVec], g[kVec], m[kVec], v[kVec];
-    u32x2 mc, vc;
-    float msc, vsc;
-  };
-  auto load = [&](In& x, int64_t i, int64_t n) {
-    load8<PBF && !MASTER>(weight, i, n, x.p);
-    load8<GBF>(grad, i, n, x.g);
-    if (S8) {
-      x.mc = load_codes(exp_avg, i, n);
-      x.vc = load_codes(exp_avg_sq, i, n);
-      x.msc = ms[i / DORA_STATE_BLOCK];
-      x.vsc = vs[i / DORA_STATE_BLOCK];
-    } else {
-      load8<false>(exp_avg, i, n, x.m);
-      load8<false>(exp_avg_sq, i, n, x.v);
-    }
-  };
-  auto step = [&](In& x, int64_t i, int64_t n) {
-    float r[kVec];
-    if (S8) {
-      decode8<true>(x.mc, x.msc, x.m);
-      decode8<false>(x.vc, x.vsc, x.v);
+  const int64_t i = start + threadIdx.x * N;
+  const float gs = a.h.grad_scale ? *a.h.grad_scale : 1.f;
+  void* weight = MASTER ? (void*)a.master[t] : a.param[t];
+  auto step = [&](auto all) {
+    constexpr bool ALL = decltype(all)::value;
+    float p[N], g[N], m[N], v[N], r[N];
+    load_n<PBF && !MASTER, N, ALL>(weight, i, n, p);
+    load_n<GBF, N, ALL>(a.grad[t], i, n, g);
+    if constexpr (S8) {
+      const int64_t block = i / DORA_STATE_BLOCK;
+      const u32x2 mc = load_codes<ALL>(a.exp_avg[t], i, n);
+      const u32x2 vc = load_codes<ALL>(a.exp_avg_sq[t], i, n);
+      decode8<true>(mc, a.exp_avg_scale[t][block], m);
+      decode8<false>(vc, a.exp_avg_sq_scale[t][block], v);
 #pragma unroll
-      for (int k = 0; k < kVec; ++k) x.v[k] *= x.v[k];
+      for (int k = 0; k < N; ++k) v[k] *= v[k];
+    } else {
+      load_n<false, N, ALL>(a.exp_avg[t], i, n, m);
+      load_n<false, N, ALL>(a.exp_avg_sq[t], i, n, v);
     }
-    update8(a.h, gs, x.g, x.p, x.m, x.v, r);
-    if (MASTER) store8<false>(weight, i, n, x.p);
-    store8<PBF>(param, i, n, x.p);
-    if (S8) {
-      const float m_scale = block_scale(x.m), v_scale = block_scale(r);
-      store_codes(exp_avg, i, n, encode8<true>(x.m, m_scale));
-      store_codes(exp_avg_sq, i, n, encode8<false>(r, v_scale));
+    update<N>(a.h, gs, g, p, m, v, r);
+    if (MASTER) store_n<false, N, ALL>(weight, i, n, p);
+    store_n<PBF, N, ALL>(a.param[t], i, n, p);
+    if constexpr (S8) {
+      const int64_t block = i / DORA_STATE_BLOCK;
+      const float ms = block_scale(m), vs = block_scale(r);
+      store_codes<ALL>(a.exp_avg[t], i, n, encode8<true>(m, ms));
+      store_codes<ALL>(a.exp_avg_sq[t], i, n, encode8<false>(r, vs));
       if ((threadIdx.x & (kGroup - 1)) == 0) {
-        ms[i / DORA_STATE_BLOCK] = m_scale;
-        vs[i / DORA_STATE_BLOCK] = v_scale;
+        a.exp_avg_scale[t][block] = ms;
+        a.exp_avg_sq_scale[t][block] = vs;
       }
     } else {
-      store8<false>(exp_avg, i, n, x.m);
-      store8<false>(exp_avg_sq, i, n, x.v);
+      store_n<false, N, ALL>(a.exp_avg[t], i, n, m);
+      store_n<false, N, ALL>(a.exp_avg_sq[t], i, n, v);
     }
   };
   if (start + kChunk <= n) {
-    In x[kU];
-#pragma unroll
-    for (int u = 0; u < kU; ++u) load(x[u], base + u * kThreads * kVec, INT64_MAX);
-#pragma unroll
-    for (int u = 0; u < kU; ++u) step(x[u], base + u * kThreads * kVec, INT64_MAX);
+    step(std::true_type());
   } else {
     // an 8-bit block's 16 lanes stay together: those past the end carry zeros
     const int64_t last = S8 ? (n + DORA_STATE_BLOCK - 1) / DORA_STATE_BLOCK * DORA_STATE_BLOCK : n;
-    for (int64_t i = base; i < last && i < base + kChunk; i += kThreads * kVec) {
-      In x;
-      load(x, i, n);
-      step(x, i, n);
-    }
+    if (i < last) step(std::false_type());
   }
 }
 
@@ -269,22 +290,38 @@ __device__ __forceinline__ double block_sum_f64(double v, double* lds) {
   return v;
 }
 
+// One workgroup's elements, squared and summed in float64 (a float32 square
+// passes the type's range from 1.8e19 on).
 template <bool GBF>
 __global__ __launch_bounds__(kThreads) void dora_grad_norm_parts(const NormArgs a, double* part) {
   __shared__ double lds[kThreads / 64];
+  using E = Elem<GBF>;
+  using T = typename E::T;
   const int t = __builtin_amdgcn_readfirstlane(tensor_of(a.first, a.count, blockIdx.x));
   const int64_t n = a.n[t];
-  const int64_t start = (int64_t)(blockIdx.x - a.first[t]) * kChunk;
-  const int64_t base = start + threadIdx.x * kVec;
-  float g[kU][kVec];
-  const int64_t limit = start + kChunk <= n ? INT64_MAX : n;
-#pragma unroll
-  for (int u = 0; u < kU; ++u) load8<GBF>(a.g[t], base + u * kThreads * kVec, limit, g[u]);
+  const int64_t start = (int64_t)(blockIdx.x - a.first[t]) * kNormChunk;
+  const T* g = reinterpret_cast<const T*>(a.g[t]) + start;
   double sum = 0.0;
+  constexpr int kLoads = kNormChunk / kThreads / E::kN;
+  if (start + kNormChunk <= n) {
+    typename E::Vec raw[kLoads];
 #pragma unroll
-  for (int u = 0; u < kU; ++u)
+    for (int u = 0; u < kLoads; ++u) raw[u] = E::raw(g + (u * kThreads + threadIdx.x) * E::kN);
 #pragma unroll
-    for (int k = 0; k < kVec; ++k) sum = fma((double)g[u][k], (double)g[u][k], sum);
+    for (int u = 0; u < kLoads; ++u) {
+      float v[E::kN];
+      E::decode(raw[u], v);
+#pragma unroll
+      for (int k = 0; k < E::kN; ++k) sum = fma((double)v[k], (double)v[k], sum);
+    }
+  } else {
+    for (int64_t i = threadIdx.x * E::kN; i < n - start; i += kThreads * E::kN) {
+      float v[E::kN];
+      load_part<GBF>(g, i, n - start, 0.f, v);
+#pragma unroll
+      for (int k = 0; k < E::kN; ++k) sum = fma((double)v[k], (double)v[k], sum);
+    }
+  }
   sum = block_sum_f64(sum, lds);
   if (threadIdx.x == 0) part[blockIdx.x] = sum;
 }
@@ -313,11 +350,11 @@ __global__ __launch_bounds__(kThreads) void dora_state_values(const void* codes,
   const int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * kVec;
   if (i >= n) return;
   float v[kVec];
-  decode8<!SECOND>(load_codes(codes, i, n), scales[i / DORA_STATE_BLOCK], v);
+  decode8<!SECOND>(load_codes<false>(codes, i, n), scales[i / DORA_STATE_BLOCK], v);
 #pragma unroll
   for (int k = 0; k < kVec; ++k)
     if (SECOND) v[k] *= v[k];
-  store8<BF>(out, i, n, v);
+  store_n<BF, kVec, false>(out, i, n, v);
 }
 
 template <bool SECOND>
@@ -327,12 +364,12 @@ __global__ __launch_bounds__(kThreads) void dora_state_codes(const float* values
   const int64_t block = i / DORA_STATE_BLOCK;
   if (block * DORA_STATE_BLOCK >= n) return;
   float v[kVec];
-  load8<false>(values, i, n, v);
+  load_n<false, kVec, false>(values, i, n, v);
 #pragma unroll
   for (int k = 0; k < kVec; ++k)
     if (SECOND) v[k] = sqrtf(v[k]);
   const float s = block_scale(v);
-  store_codes(codes, i, n, encode8<!SECOND>(v, s));
+  store_codes<false>(codes, i, n, encode8<!SECOND>(v, s));
   if ((threadIdx.x & (kGroup - 1)) == 0) scales[block] = s;
 }
 
@@ -340,6 +377,7 @@ __global__ __launch_bounds__(kThreads) void dora_state_codes(const float* values
 constexpr int64_t kMaxElems = int64_t(1) << 34;
 
 int64_t chunks(int64_t n) { return (n + kChunk - 1) / kChunk; }
+int64_t norm_chunks(int64_t n) { return (n + kNormChunk - 1) / kNormChunk; }
 bool dtype_ok(int dt) { return dt == DORA_F32 || dt == DORA_BF16; }
 size_t esize(int dt) { return dt == DORA_BF16 ? 2 : 4; }
 
@@ -367,8 +405,8 @@ hipError_t run_step(const dora_adamw_tensor* tensors, int64_t count, const StepN
     if (k == 0) return hipSuccess;
     a.h.count = k;
     LaunchTimer timer("adamw", st);
-    hipLaunchKernelGGL((dora_adamw_kernel<PBF, GBF, MASTER, S8>), dim3((unsigned)blocks),
-                       dim3(kThreads), 0, st, a);
+    hipLaunchKernelGGL((dora_adamw_kernel<PBF, GBF, MASTER, S8>),
+                       dim3((unsigned)blocks), dim3(kChunk / (S8 ? 8 : 4)), 0, st, a);
     k = 0;
     blocks = 0;
     return hipGetLastError();
@@ -466,7 +504,7 @@ DORA_API int dora_adamw_step(const dora_adamw_tensor* tensors, int64_t count,
 DORA_API size_t dora_grad_norm_workspace_bytes(const dora_adamw_tensor* tensors, int64_t count) {
   if (check_tensors(tensors, count) != DORA_OK) return 0;
   int64_t parts = 0;
-  for (int64_t i = 0; i < count; ++i) parts += chunks(tensors[i].n);
+  for (int64_t i = 0; i < count; ++i) parts += norm_chunks(tensors[i].n);
   return (size_t)parts * sizeof(double);
 }
 
@@ -501,7 +539,7 @@ DORA_API int dora_grad_norm(const dora_adamw_tensor* tensors, int64_t count, int
     return hipGetLastError();
   };
   for (int64_t i = 0; i < count; ++i) {
-    const int64_t c = chunks(tensors[i].n);
+    const int64_t c = norm_chunks(tensors[i].n);
     if (c == 0) continue;
     if (a.count == kMaxGrads || blocks + c > kMaxGrid) HIP_TRY(flush());
     a.g[a.count] = tensors[i].grad;

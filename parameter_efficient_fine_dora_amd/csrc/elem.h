@@ -19,6 +19,9 @@ struct Elem<true> {
   __device__ static float get(const T* p) { return bf16_to_f32(*p); }
   __device__ static void put(T* p, float v) { *p = f32_to_bf16(v); }
   __device__ static Vec raw(const T* p) { return *reinterpret_cast<const Raw*>(p); }
+  __device__ static Vec raw_past(const T* p) {   // past the caches
+    return __builtin_nontemporal_load(reinterpret_cast<const Raw*>(p));
+  }
   __device__ static Vec masked() {   // every element -inf
     return Vec{0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u};
   }
@@ -52,6 +55,9 @@ struct Elem<false> {
   __device__ static float get(const T* p) { return *p; }
   __device__ static void put(T* p, float v) { *p = v; }
   __device__ static Vec raw(const T* p) { return *reinterpret_cast<const Raw*>(p); }
+  __device__ static Vec raw_past(const T* p) {   // past the caches
+    return __builtin_nontemporal_load(reinterpret_cast<const Raw*>(p));
+  }
   __device__ static Vec masked() {
     const float inf = __builtin_huge_valf();
     return Vec{-inf, -inf, -inf, -inf};
