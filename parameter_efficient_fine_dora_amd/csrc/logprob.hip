@@ -279,7 +279,9 @@ __device__ void select_top(const typename Elem<BF>::T* row, int64_t n, const flo
 // Chunk blockIdx.x of a row (or, with one chunk, the whole row and its results).
 // kU vectors per thread are loaded before the first is used; per element the loop
 // costs a subtraction, two products, an exponential, two maxima and two sums.
-template <bool BF, int THREADS, bool TOP, bool SPLIT>
+// PAST: the logits do not fit the last-level cache and are loaded past it
+// (3584 x 131072 bf16: 159 us against 177, 5.9 TB/s).
+template <bool BF, int THREADS, bool TOP, bool SPLIT, bool PAST>
 __global__ __launch_bounds__(THREADS) void dora_logprob_fwd(
     const void* logits, int64_t ld, const int64_t* targets, float* logp, float* entropy, float* lse,
     float* top_logp, int64_t* top_index, Stat* part, uint64_t* part_top, int64_t rows, int64_t V,
@@ -299,7 +301,10 @@ __global__ __launch_bounds__(THREADS) void dora_logprob_fwd(
     auto load = [&](int64_t j0) {
       if (n - j0 >= kStep * kU) {
 #pragma unroll
-        for (int u = 0; u < kU; ++u) raw[u] = E::raw(z + j0 + u * kStep + own);
+        for (int u = 0; u < kU; ++u) {
+          const T* at = z + j0 + u * kStep + own;
+          raw[u] = PAST ? E::raw_past(at) : E::raw(at);
+        }
       } else {
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
@@ -614,10 +619,17 @@ Plan plan(const dora_logprob_shape& s) {
   p.top_bytes = (size_t)(parts * s.top * 8);
   return p;
 }
+// Whether a call's logits pass the last-level cache.
+template <bool BF>
+bool past_last_level(const dora_logprob_shape& s) {
+  constexpr double kLastLevel = 256.0 * (1 << 20);
+  return (double)s.rows * (double)s.vocab * sizeof(typename Elem<BF>::T) > kLastLevel;
+}
+
 // Short rows are one wave's: no barriers, and four times the rows in flight.
 constexpr int64_t kWaveVocab = 4096;
 
-template <bool BF, int THREADS, bool TOP, bool SPLIT>
+template <bool BF, int THREADS, bool TOP, bool SPLIT, bool PAST>
 hipError_t launch_fwd(const dora_logprob_shape& s, const Plan& p, const void* logits,
                       const int64_t* targets, float* logp, float* entropy, float* lse,
                       float* top_logp, int64_t* top_index, Stat* part, uint64_t* part_top,
@@ -628,7 +640,7 @@ hipError_t launch_fwd(const dora_logprob_shape& s, const Plan& p, const void* lo
                             : 0;
   {
     LaunchTimer t("logprob_fwd", st);
-    hipLaunchKernelGGL((dora_logprob_fwd<BF, THREADS, TOP, SPLIT>), dim3((unsigned)p.splits, rows),
+    hipLaunchKernelGGL((dora_logprob_fwd<BF, THREADS, TOP, SPLIT, PAST>), dim3((unsigned)p.splits, rows),
                        dim3(THREADS), groups, st, logits, s.ld, targets, logp, entropy, lse,
                        top_logp, top_index, part, part_top, s.rows, s.vocab, p.chunk, (int)s.top,
                        s.scale);
@@ -655,11 +667,20 @@ hipError_t forward(const dora_logprob_shape& s, const void* logits, const int64_
     return fn(s, p, logits, targets, logp, entropy, lse, top_logp, top_index, part, part_top, st);
   };
   constexpr int N = kThreads;
+  const bool top = s.top > 0;
+  if (p.splits > 1 && past_last_level<BF>(s))
+    return top ? go(launch_fwd<BF, N, true, true, true>) : go(launch_fwd<BF, N, false, true, true>);
   if (p.splits > 1)
-    return s.top > 0 ? go(launch_fwd<BF, N, true, true>) : go(launch_fwd<BF, N, false, true>);
+    return top ? go(launch_fwd<BF, N, true, true, false>)
+               : go(launch_fwd<BF, N, false, true, false>);
   if (s.vocab <= kWaveVocab)
-    return s.top > 0 ? go(launch_fwd<BF, 64, true, false>) : go(launch_fwd<BF, 64, false, false>);
-  return s.top > 0 ? go(launch_fwd<BF, N, true, false>) : go(launch_fwd<BF, N, false, false>);
+    return top ? go(launch_fwd<BF, 64, true, false, false>)
+               : go(launch_fwd<BF, 64, false, false, false>);
+  if (past_last_level<BF>(s))
+    return top ? go(launch_fwd<BF, N, true, false, true>)
+               : go(launch_fwd<BF, N, false, false, true>);
+  return top ? go(launch_fwd<BF, N, true, false, false>)
+             : go(launch_fwd<BF, N, false, false, false>);
 }
 
 template <bool BF>
@@ -676,9 +697,7 @@ hipError_t backward(const dora_logprob_shape& s, const float* g_logp, const floa
                        grad, s.rows, (int)s.vocab, s.scale);
     return hipGetLastError();
   };
-  constexpr double kLastLevel = 256.0 * (1 << 20);
-  if ((double)s.rows * (double)s.vocab * sizeof(typename Elem<BF>::T) > kLastLevel)
-    return launch(dora_logprob_bwd<BF, kThreads, true>, kThreads);
+  if (past_last_level<BF>(s)) return launch(dora_logprob_bwd<BF, kThreads, true>, kThreads);
   if (s.vocab <= kWaveVocab) return launch(dora_logprob_bwd<BF, 64, false>, 64);
   return launch(dora_logprob_bwd<BF, kThreads, false>, kThreads);
 }
