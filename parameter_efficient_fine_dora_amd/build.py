@@ -1,4 +1,5 @@
-"""Build libdora.so (HIP, gfx950) in-tree with hipcc.
+"""Build libdora.so (HIP, gfx950) with hipcc and the compiled Python binding _bind.so with the
+host compiler, both in-tree.
 
     python -m parameter_efficient_fine_dora_amd.build
 
@@ -12,12 +13,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libdora.so")
+BIND = os.path.join(HERE, "_bind.so")   # csrc/bind.cpp
 SOURCES = ["api.hip", "gemm.hip", "gram.hip", "rowwise.hip", "small.hip", "probe.hip", "noalloc.hip",
            "layernorm.hip", "logprob.hip", "adamw.hip"]
 HEADERS = ["common.h", "kernels.h", "entry.h", "elem.h"]
@@ -41,6 +44,19 @@ def compile_flags() -> list[str]:
     ]
 
 
+def bind_command(out: str) -> list[str]:
+    """csrc/bind.cpp against torch's headers and libraries (which the process has loaded before)."""
+    import torch
+    from torch.utils import cpp_extension
+    inc = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"]]
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    return [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+            "-fvisibility=hidden", "-Wall",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            *(f"-I{p}" for p in inc), os.path.join(CSRC, "bind.cpp"), "-o", out, f"-L{lib}",
+            "-lc10", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
+
+
 def _run(cmd: list[str]) -> tuple[int, str]:
     p = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
     out = "\n".join(l for l in p.stdout.splitlines()
@@ -56,6 +72,7 @@ def build(verbose: bool = False, jobs: int | None = None) -> str:
         obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
         objs.append(obj)
         cmds.append([cc, *compile_flags(), "-c", os.path.join(CSRC, src), "-o", obj])
+    cmds.append(bind_command(BIND + ".tmp"))
     jobs = jobs or min(len(cmds), max(1, (os.cpu_count() or 2) // 2))
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
         results = list(ex.map(_run, cmds))
@@ -65,13 +82,14 @@ def build(verbose: bool = False, jobs: int | None = None) -> str:
             if out.strip():
                 print(out, file=sys.stderr)
         if rc:
-            raise RuntimeError(f"hipcc failed ({rc}) on {cmd[-3]}")
+            raise RuntimeError(f"{os.path.basename(cmd[0])} failed ({rc}): {' '.join(cmd)}")
     tmp = LIB + ".tmp"
     rc, out = _run([cc, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp])
     if rc:
         print(out, file=sys.stderr)
         raise RuntimeError("link of libdora.so failed")
     os.replace(tmp, LIB)
+    os.replace(BIND + ".tmp", BIND)
     return LIB
 
 

@@ -10,15 +10,12 @@ from __future__ import annotations
 
 import ctypes
 import json
-import operator
 
-import numpy as np
 import torch
 
 from . import _lib
 from ._lib import DoraError, FLAG_EXACT_NORM_GRAD, FLAG_SEPARATE_COMPOSE  # noqa: F401
 
-_dtype_of = operator.attrgetter("dtype")
 _DT = {torch.float32: _lib.F32, torch.bfloat16: _lib.BF16}
 
 
@@ -29,6 +26,33 @@ def _ptr(t):
 def _stream(dev):
     # the handle alone: torch.cuda.current_stream builds a Stream object around it (2 us a call)
     return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
+_bind = None
+
+
+def _compiled():
+    """The compiled short way of the small calls (csrc/bind.cpp), with the library's addresses.
+    Its functions return None where the checked way below has to look closer."""
+    global _bind
+    if _bind is None:
+        try:
+            from . import _bind as mod
+        except ImportError as e:
+            raise ImportError("_bind.so is missing: build it with "
+                              "`python -m parameter_efficient_fine_dora_amd.build`") from e
+        L = _lib.lib()
+        mod.init(*(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in (
+            "dora_layernorm_forward", "dora_layernorm_backward", "dora_layernorm_workspace_bytes",
+            "dora_token_logprob_forward", "dora_token_logprob_backward",
+            "dora_token_logprob_workspace_bytes", "dora_grad_norm", "dora_adamw_step",
+            "dora_adamw_dequantize")))
+        _bind = mod
+    return _bind
+
+
+def _on_gpu(t):
+    return isinstance(t, torch.Tensor) and t.is_cuda
 
 
 def _need(t, name, dtype=None, shape=None, dev=None):
@@ -287,6 +311,10 @@ def dora_layernorm(x, weight=None, bias=None, *, eps=1e-5, y=None, mean=None, rs
 
     Returns (y, mean, rstd); mean and rstd are float32 [rows], for the backward.
     """
+    if y is None and mean is None and rstd is None and _on_gpu(x):
+        out = _compiled().layernorm(x, weight, bias, float(eps), _stream(x.device))
+        if out is not None:
+            return out
     ld = _rows(x, "x")
     dev, dt = x.device, x.dtype
     R, D = x.shape
@@ -308,6 +336,12 @@ def dora_layernorm_backward(grad_y, x, weight, mean, rstd, *, need=("x", "weight
                             grad_x=None, grad_weight=None, grad_bias=None, workspace=None):
     """Layer norm backward.  Returns (grad_x, grad_weight, grad_bias), layer dtype; entries not
     in ``need`` are None."""
+    if (grad_x is None and grad_weight is None and grad_bias is None and workspace is None
+            and _on_gpu(x)):
+        out = _compiled().layernorm_backward(grad_y, x, weight, mean, rstd, "x" in need,
+                                             "weight" in need, "bias" in need, _stream(x.device))
+        if out is not None:
+            return out
     ld = _rows(x, "x")
     dev, dt = x.device, x.dtype
     R, D = x.shape
@@ -344,6 +378,11 @@ def dora_token_logprob(logits, targets, *, scale=1.0, top=0, workspace=None):
     ``top`` likeliest tokens of each row, float32 and int64 [rows, top] (None for top = 0).  Rows
     whose target lies outside [0, vocab) are skipped: zeros, and top_index -1.
     """
+    if workspace is None and _on_gpu(logits):
+        out = _compiled().token_logprob(logits, targets, float(scale), int(top),
+                                        _stream(logits.device))
+        if out is not None:
+            return out
     ld = _rows(logits, "logits")
     dev = logits.device
     T, V = logits.shape
@@ -370,6 +409,11 @@ def dora_token_logprob_backward(grad_logp, grad_entropy, logits, targets, lse, e
                                 grad_logits=None):
     """Gradient of dora_token_logprob's logp and entropy (either gradient may be None) with respect
     to the logits, [rows, vocab] in their dtype; lse and entropy as it returned them."""
+    if grad_logits is None and _on_gpu(logits):
+        out = _compiled().token_logprob_backward(grad_logp, grad_entropy, logits, targets, lse,
+                                                 entropy, float(scale), _stream(logits.device))
+        if out is not None:
+            return out
     ld = _rows(logits, "logits")
     dev = logits.device
     T, V = logits.shape
@@ -449,49 +493,48 @@ class AdamWPlan:
         self.state_bits = 8 if small else 32
         self.norm_bytes = None   # workspace of the gradients' norm, asked for once
         self._keep = (exp_avg, exp_avg_sq, sc1, sc2, mst)
-        self._at = [p.data_ptr() for p in params]
-        self._sizes = [p.numel() for p in params]
-        # the table's gradient addresses as an array, written in one go at each step
-        self._grads = np.frombuffer(self.table, dtype=np.int64).reshape(n, -1)[:, 1]
+        self._address = ctypes.addressof(self.table)
 
     def _take_grads(self, grads):
-        """Checks the gradients and notes where they are; returns their dtype."""
-        T = torch.Tensor
+        """Checks the gradients and notes where they are; returns their dtype's code."""
+        grads = grads if isinstance(grads, list) else list(grads)
+        code = _compiled().take_grads(self.params, grads, self._address, self.device.index)
+        if code is not None:
+            return code
         if len(grads) != len(self.params):
             raise ValueError(f"{len(grads)} gradients for {len(self.params)} params")
-        if list(map(T.data_ptr, self.params)) != self._at:
+        if [p.data_ptr() for p in self.params] != [e.param or 0 for e in self.table]:
             raise ValueError("a parameter's storage has changed since the plan was made")
-        gdt = grads[0].dtype
-        if gdt not in _DT:
+        gdt = grads[0].dtype if isinstance(grads[0], torch.Tensor) else None
+        if gdt is not None and gdt not in _DT:
             raise ValueError(f"unsupported dtype {gdt}; use float32 or bfloat16")
-        # whole lists at a time: a step may hold hundreds of small tensors
-        if not (all(map(T.is_contiguous, grads)) and list(map(T.numel, grads)) == self._sizes
-                and set(map(_dtype_of, grads)) == {gdt}
-                and set(map(T.get_device, grads)) == {self.device.index}):
-            for i, (g, k) in enumerate(zip(grads, self._sizes)):
-                _need(g, f"grads[{i}]", gdt, None, self.device)
-                if g.numel() != k:
-                    raise ValueError(f"grads[{i}] has {g.numel()} elements, expected {k}")
-        self._grads[:] = list(map(T.data_ptr, grads))
-        return gdt
+        for i, (g, e) in enumerate(zip(grads, self.table)):
+            _need(g, f"grads[{i}]", gdt, None, self.device)
+            if g.numel() != e.n:
+                raise ValueError(f"grads[{i}] has {g.numel()} elements, expected {e.n}")
+            e.grad = g.data_ptr()
+        return _DT[gdt]
 
 
 def dora_grad_norm(plan, grads, max_norm=1.0, *, workspace=None):
     """Global norm of the gradients of a plan's params and the factor min(1, max_norm / (norm +
     1e-6)) that clips them to ``max_norm``: two float32 scalars on the device."""
-    gdt = plan._take_grads(grads)
-    return _grad_norm(plan, gdt, max_norm, workspace)
+    return _grad_norm(plan, plan._take_grads(grads), max_norm, workspace)
 
 
-def _grad_norm(plan, gdt, max_norm, workspace):
+def _grad_norm(plan, code, max_norm, workspace):
     L, n = _lib.lib(), len(plan.params)
     if workspace is None:
         if plan.norm_bytes is None:
             plan.norm_bytes = L.dora_grad_norm_workspace_bytes(plan.table, n)
+        out = _compiled().grad_norm(plan._address, n, code, float(max_norm), plan.norm_bytes,
+                                    plan.params[0], _stream(plan.device))
+        if out is not None:
+            return out
         workspace = torch.empty(max(plan.norm_bytes, 1), dtype=torch.uint8, device=plan.device)
     norm = torch.empty((), dtype=torch.float32, device=plan.device)
     factor = torch.empty((), dtype=torch.float32, device=plan.device)
-    _check(L.dora_grad_norm(plan.table, n, _DT[gdt], float(max_norm), _ptr(norm), _ptr(factor),
+    _check(L.dora_grad_norm(plan.table, n, code, float(max_norm), _ptr(norm), _ptr(factor),
                             _ptr(workspace), workspace.numel() * workspace.element_size(),
                             _stream(plan.device)), "dora_grad_norm")
     return norm, factor
@@ -507,17 +550,16 @@ def dora_adamw(plan, grads, *, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_de
     """
     if max_norm is not None and grad_scale is not None:
         raise ValueError("max_norm and grad_scale exclude each other")
-    gdt = plan._take_grads(grads)
+    code = plan._take_grads(grads)
     norm = None
     if max_norm is not None:
-        norm, grad_scale = _grad_norm(plan, gdt, max_norm, workspace)
+        norm, grad_scale = _grad_norm(plan, code, max_norm, workspace)
     elif grad_scale is not None:
         _need(grad_scale, "grad_scale", torch.float32, None, plan.device)
-    o = _lib.DoraAdamwOptions(plan.param_code, _DT[gdt], plan.state_bits, 0, int(step), float(lr),
-                              float(betas[0]), float(betas[1]), float(eps), float(weight_decay),
-                              _ptr(grad_scale))
-    _check(_lib.lib().dora_adamw_step(plan.table, len(plan.params), ctypes.byref(o),
-                                      _stream(plan.device)), "dora_adamw_step")
+    _check(_compiled().adamw_step(plan._address, len(plan.params), plan.param_code, code,
+                                  plan.state_bits, int(step), float(lr), float(betas[0]),
+                                  float(betas[1]), float(eps), float(weight_decay), grad_scale,
+                                  _stream(plan.device)), "dora_adamw_step")
     return norm
 
 
@@ -529,6 +571,10 @@ def _second_moment(codes):
 
 def dora_adamw_dequantize(codes, scales, *, dtype=torch.float32):
     """The values of 8-bit states: exp_avg of int8 codes, exp_avg_sq of uint8 codes."""
+    if _on_gpu(codes) and dtype in _DT:
+        out = _compiled().dequantize(codes, scales, dtype == torch.bfloat16, _stream(codes.device))
+        if out is not None:
+            return out
     _need(codes, "codes")
     second = _second_moment(codes)
     n = codes.numel()

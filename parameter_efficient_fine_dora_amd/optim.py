@@ -61,7 +61,7 @@ class AdamW(torch.optim.Optimizer):
         if kept is not None:
             plan, were = kept
             if (len(plan.params) == len(params) and all(a is b for a, b in zip(plan.params, params))
-                    and plan._at == [p.data_ptr() for p in params]
+                    and [e.param for e in plan.table] == [p.data_ptr() or None for p in params]
                     and all(a is b for k in lists for a, b in zip(lists[k], were[k]))):
                 return plan
         plan = ops.AdamWPlan(params, lists["exp_avg"], lists["exp_avg_sq"], masters=lists.get("masters"),
