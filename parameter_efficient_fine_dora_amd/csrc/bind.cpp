@@ -202,6 +202,58 @@ PyObject* token_logprob_backward(PyObject*, PyObject* const* args, Py_ssize_t n)
   END_HANDLE_TH_ERRORS
 }
 
+// make_table(params, exp_avg, exp_avg_sq, exp_avg_scales, exp_avg_sq_scales, masters, table
+// address): fills the table of an AdamW step from lists of tensors (the last three lists may be
+// None; without scales the moments are float32, with them int8 and uint8).  Returns the
+// parameters' dtype code, or None unless all are contiguous, on one device, of their types and
+// sizes.
+PyObject* make_table(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 7 || !PyList_Check(args[0])) Py_RETURN_NONE;
+  const Py_ssize_t count = PyList_GET_SIZE(args[0]);
+  for (int i = 1; i < 6; ++i)
+    if (!(i > 2 && args[i] == Py_None) &&
+        !(PyList_Check(args[i]) && PyList_GET_SIZE(args[i]) == count))
+      Py_RETURN_NONE;
+  const bool small = args[3] != Py_None;
+  if (small != (args[4] != Py_None)) Py_RETURN_NONE;
+  auto* table = static_cast<dora_adamw_tensor*>(PyLong_AsVoidPtr(args[6]));
+  const at::Tensor* first = nullptr;
+  for (Py_ssize_t i = 0; i < count; ++i) {
+    bool ok = true;
+    const at::Tensor* t[6] = {};
+    for (int k = 0; k < 6; ++k)
+      if (args[k] != Py_None) t[k] = tensor(PyList_GET_ITEM(args[k], i), ok);
+    if (!ok || !t[0]) Py_RETURN_NONE;
+    if (!first) first = t[0];
+    const int64_t size = t[0]->numel(), blocks = (size + DORA_STATE_BLOCK - 1) / DORA_STATE_BLOCK;
+    if (!t[0]->is_cuda() || t[0]->scalar_type() != first->scalar_type()) Py_RETURN_NONE;
+    const at::ScalarType types[6] = {first->scalar_type(), small ? at::kChar : at::kFloat,
+                                     small ? at::kByte : at::kFloat, at::kFloat, at::kFloat,
+                                     at::kFloat};
+    for (int k = 0; k < 6; ++k) {
+      if (args[k] == Py_None) continue;
+      const int64_t need = k == 3 || k == 4 ? blocks : size;
+      if (!t[k] || t[k]->scalar_type() != types[k] || t[k]->numel() != need ||
+          !t[k]->is_contiguous() || t[k]->device() != first->device())
+        Py_RETURN_NONE;
+    }
+    dora_adamw_tensor& e = table[i];
+    auto at = [&](int k) { return t[k] ? t[k]->data_ptr() : nullptr; };
+    e.param = at(0);
+    e.exp_avg = at(1);
+    e.exp_avg_sq = at(2);
+    e.exp_avg_scale = static_cast<float*>(at(3));
+    e.exp_avg_sq_scale = static_cast<float*>(at(4));
+    e.master = static_cast<float*>(at(5));
+    e.n = size;
+  }
+  const int code = first ? dtype_code(first->scalar_type()) : -1;
+  if (code < 0 || (args[5] != Py_None && code != DORA_BF16)) Py_RETURN_NONE;
+  return PyLong_FromLong(code);
+  END_HANDLE_TH_ERRORS
+}
+
 // take_grads(params, grads, table address, device index): notes the gradients'
 // addresses in the table.  Returns their dtype code, or None unless every
 // parameter is where the table has it and every gradient is contiguous, of its
@@ -316,9 +368,9 @@ PyObject* init(PyObject*, PyObject* const* args, Py_ssize_t n) {
 #define FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FAST(layernorm),     FAST(layernorm_backward),
                          FAST(token_logprob), FAST(token_logprob_backward),
-                         FAST(take_grads),    FAST(grad_norm),
-                         FAST(adamw_step),    FAST(dequantize),
-                         FAST(init),
+                         FAST(make_table),    FAST(take_grads),
+                         FAST(grad_norm),     FAST(adamw_step),
+                         FAST(dequantize),    FAST(init),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_bind", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

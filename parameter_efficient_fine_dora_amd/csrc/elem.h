@@ -15,6 +15,8 @@ struct Elem<true> {
   using T = uint16_t;
   static constexpr int kN = 8;
   using Vec = u32x4;
+  using Word = uint32_t;   // 32 bits of a vector; its element q
+  __device__ static float from_word(Word w, int q) { return (q & 1) ? bf_hi(w) : bf_lo(w); }
   typedef Vec Raw __attribute__((aligned(2)));
   __device__ static float get(const T* p) { return bf16_to_f32(*p); }
   __device__ static void put(T* p, float v) { *p = f32_to_bf16(v); }
@@ -51,6 +53,8 @@ struct Elem<false> {
   using T = float;
   static constexpr int kN = 4;
   using Vec = f32x4;
+  using Word = float;
+  __device__ static float from_word(Word w, int) { return w; }
   typedef Vec Raw __attribute__((aligned(4)));
   __device__ static float get(const T* p) { return *p; }
   __device__ static void put(T* p, float v) { *p = v; }

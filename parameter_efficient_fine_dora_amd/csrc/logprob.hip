@@ -89,13 +89,6 @@ __device__ __forceinline__ void rescale(Stat& a, float m, float c2) {
   a.s *= f;
   a.m = m;
 }
-__device__ __forceinline__ Stat merge(Stat a, Stat b, float c2) {
-  const float m = maxnan(a.m, b.m);
-  rescale(a, m, c2);
-  rescale(b, m, c2);
-  return {m, a.s + b.s, a.u + b.u};
-}
-
 template <int N>
 __device__ __forceinline__ void add_logits(Stat& a, const float* v, float c2) {
   float m = v[0];
@@ -127,10 +120,18 @@ __device__ __forceinline__ Stat block_stat(Stat a, float c2, Stat* lds) {
   if (WAVES == 1) return a;
   if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = a;
   __syncthreads();
-  a = lds[0];
+  float m = lds[0].m;
 #pragma unroll
-  for (int w = 1; w < WAVES; ++w) a = merge(a, lds[w], c2);
-  return a;
+  for (int w = 1; w < WAVES; ++w) m = maxnan(m, lds[w].m);
+  Stat sum = {m, 0.f, 0.f};
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) {
+    Stat b = lds[w];
+    rescale(b, m, c2);
+    sum.s += b.s;
+    sum.u += b.u;
+  }
+  return sum;
 }
 
 // One row's results from its statistics.
@@ -165,26 +166,32 @@ constexpr uint32_t kNone = 0x007fffffu;   // order_bits(-inf)
 constexpr int kListCap = 2048;            // kMaxTop * max(groups per run, elements per group)
 template <int THREADS>
 struct TopLds {
-  uint64_t list[kListCap];
+  __align__(16) uint64_t list[kListCap];
   uint32_t run[THREADS];      // order bits of the runs' maxima
   uint32_t chosen[kMaxTop];   // the groups
   uint32_t count, bound;
 };
 
+typedef uint64_t u64x2 __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ int rank_in(uint64_t key, const uint64_t* list, int n) {
-  int r = 0;
+  int r = 0, i = 0;
 #pragma unroll 4
-  for (int i = 0; i < n; ++i) r += list[i] > key ? 1 : 0;
+  for (; i + 2 <= n; i += 2) {
+    const u64x2 v = *reinterpret_cast<const u64x2*>(list + i);
+    r += (v[0] > key ? 1 : 0) + (v[1] > key ? 1 : 0);
+  }
+  if (i < n) r += list[i] > key ? 1 : 0;
   return r;
 }
 
 // Of a wave's 64 N numbers: an x that at least k of them reach, and that either
 // exactly k reach or that is the k-th largest (0 if fewer than k are above 0).
-// Bisection over the bits; a step is N ballots.
-template <int N>
+// Bisection over the bits; a step is N ballots.  Stopped at bit LAST, x is
+// rounded down: more than k may reach it.
+template <int N, int LAST = 0>
 __device__ __forceinline__ uint32_t kth_largest(const uint32_t* v, int k) {
   uint32_t x = 0;
-  for (int bit = 31; bit >= 0; --bit) {
+  for (int bit = 31; bit >= LAST; --bit) {
     const uint32_t c = x | (1u << bit);
     int n = 0;
 #pragma unroll
@@ -199,13 +206,34 @@ __device__ __forceinline__ uint64_t lanes_below() {
   return (uint64_t(1) << (threadIdx.x & 63)) - 1;
 }
 
+// The listed keys by rank, and masked logits to make up the number.
+template <bool BF, int THREADS, typename Put>
+__device__ __forceinline__ void rank_list(const typename Elem<BF>::T* row, int64_t n, int k,
+                                          TopLds<THREADS>& t, Put put) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  int m = (int)t.count;
+  for (int i = tid; i < m; i += THREADS) {
+    const uint64_t key = t.list[i];
+    const int rank = rank_in(key, t.list, m);
+    if (rank < k) put(rank, key);
+  }
+  if (tid < 64) {
+    for (int64_t j0 = 0; m < k && j0 < n; j0 += 64) {
+      const bool masked = j0 + lane < n && Elem<BF>::get(row + j0 + lane) == kNegInf;
+      const uint64_t mask = __ballot(masked);
+      const int rank = m + __popcll(mask & lanes_below());
+      if (masked && rank < k) put(rank, order_key(kNegInf, (uint32_t)(j0 + lane)));
+      m += __popcll(mask);
+    }
+  }
+}
+
 // Keys of the k first elements of row[0, n), in order, to put(rank, key);
 // n >= k.  `group` holds the maxima of groups of G elements.
 template <bool BF, int THREADS, typename Put>
 __device__ void select_top(const typename Elem<BF>::T* row, int64_t n, const float* group, int k,
-                           Put put) {
+                           TopLds<THREADS>& t, Put put) {
   constexpr int G = 4 * Elem<BF>::kN, W = THREADS / 64;
-  __shared__ TopLds<THREADS> t;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int ng = (int)((n + G - 1) / G);
   const int run = (ng + THREADS - 1) / THREADS;   // groups per run
@@ -258,30 +286,82 @@ __device__ void select_top(const typename Elem<BF>::T* row, int64_t n, const flo
     }
   }
   __syncthreads();
-  m = (int)t.count;
-  for (int i = tid; i < m; i += THREADS) {
-    const uint64_t key = t.list[i];
-    const int rank = rank_in(key, t.list, m);
-    if (rank < k) put(rank, key);
+  rank_list<BF, THREADS>(row, n, k, t, put);
+}
+
+// The same for a chunk that the threads still hold in `raw` (U vectors each, absent
+// elements -inf), `most` being the largest of a thread's.  Every wave whose lanes
+// all hold elements finds its q-th largest maximum, q = k / (number of such waves)
+// rounded up: the least of these is reached by k elements at least, and what
+// reaches it is ranked.  Returns false where that is more than kHeldCap (ties, or
+// the largest close together), which select_top then settles.
+constexpr uint32_t kHeldCap = 512;
+template <bool BF, int THREADS, int U, typename Put>
+__device__ bool select_held(const typename Elem<BF>::Vec* raw, float most,
+                            const typename Elem<BF>::T* row, int64_t n, int k, TopLds<THREADS>& t,
+                            Put put) {
+  using E = Elem<BF>;
+  constexpr int kBits = U * E::kN;
+  static_assert(kBits <= 32, "a bit per element");
+  const int tid = threadIdx.x, wave = tid >> 6;
+  const int full = max(1, min(THREADS / 64, (int)(n / E::kN) / 64));
+  if (wave < full) {
+    const uint32_t own = order_bits(most);
+    // 16 bits are all a bf16 has; 20 of a float32 round down by 2^-11 at most
+    const uint32_t x = kth_largest<1, BF ? 16 : 12>(&own, (k + full - 1) / full);
+    if ((tid & 63) == 0) t.run[wave] = x;
   }
-  // masked ones to make up the number
-  if (wave == 0) {
-    for (int64_t j0 = 0; m < k && j0 < n; j0 += 64) {
-      const bool masked = j0 + lane < n && Elem<BF>::get(row + j0 + lane) == kNegInf;
-      const uint64_t mask = __ballot(masked);
-      const int rank = m + __popcll(mask & lanes_below());
-      if (masked && rank < k) put(rank, order_key(kNegInf, (uint32_t)(j0 + lane)));
-      m += __popcll(mask);
+  if (tid == 0) t.count = 0;
+  __syncthreads();
+  uint32_t x = t.run[0];
+  for (int w = 1; w < full; ++w) x = min(x, t.run[w]);
+  const float least = order_value(max(x, kNone + 1));
+  uint32_t hits = 0;   // a bit per element; a NaN too
+  if (!(most < least)) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float z[E::kN];
+      E::decode(raw[u], z);
+#pragma unroll
+      for (int q = 0; q < E::kN; ++q) hits |= (z[q] < least ? 0u : 1u) << (u * E::kN + q);
     }
   }
+  // places in the list: the wave's lanes one after the other, one atomic per wave
+  const int mine = __popc(hits);
+  int before = 0, all = 0;
+#pragma unroll
+  for (int b = 0; b < 6; ++b) {
+    const uint64_t m = __ballot((mine >> b) & 1);
+    before += __popcll(m & lanes_below()) << b;
+    all += __popcll(m) << b;
+  }
+  uint32_t slot = 0;
+  if ((tid & 63) == 0 && all > 0) slot = atomicAdd(&t.count, (uint32_t)all);
+  slot = (uint32_t)__builtin_amdgcn_readfirstlane((int)slot) + before;
+  for (; hits; hits &= hits - 1, ++slot) {
+    const int bit = __ffs(hits) - 1;
+    typename E::Word word = raw[0][0];   // the element's 32 bits, picked in registers
+#pragma unroll
+    for (int i = 1; i < 4 * U; ++i) word = bit * 4 / E::kN == i ? raw[i / 4][i % 4] : word;
+    const uint32_t j = (uint32_t)((bit / E::kN * THREADS + tid) * E::kN + bit % E::kN);
+    if (slot < kHeldCap) t.list[slot] = order_key(E::from_word(word, bit), j);
+  }
+  __syncthreads();
+  if (t.count > kHeldCap) return false;
+  rank_list<BF, THREADS>(row, n, k, t, put);
+  return true;
 }
 
 // Chunk blockIdx.x of a row (or, with one chunk, the whole row and its results).
 // kU vectors per thread are loaded before the first is used; per element the loop
 // costs a subtraction, two products, an exponential, two maxima and two sums.
-// PAST: the logits do not fit the last-level cache and are loaded past it
+// TOP: 0 without alternatives; kGroups through the group maxima; kHeld for chunks
+// of one batch, which are still in registers when their statistics are known (one
+// kernel for both would keep one workgroup less per SIMD: 141 us against 119 at
+// 2048 x 131072 bf16, top 20).  PAST: the logits do not fit the last-level cache and are loaded past it
 // (3584 x 131072 bf16: 159 us against 177, 5.9 TB/s).
-template <bool BF, int THREADS, bool TOP, bool SPLIT, bool PAST>
+constexpr int kGroups = 1, kHeld = 2;
+template <bool BF, int THREADS, int TOP, bool SPLIT, bool PAST>
 __global__ __launch_bounds__(THREADS) void dora_logprob_fwd(
     const void* logits, int64_t ld, const int64_t* targets, float* logp, float* entropy, float* lse,
     float* top_logp, int64_t* top_index, Stat* part, uint64_t* part_top, int64_t rows, int64_t V,
@@ -346,7 +426,9 @@ __global__ __launch_bounds__(THREADS) void dora_logprob_fwd(
         for (int u = 0; u < kU; ++u) E::decode(raw[u], v[u]);
         if (TOP) {
 #pragma unroll
-          for (int u = 0; u < kU; ++u) group_max(v[u], j0 + u * kStep + own);
+          for (int u = 0; u < kU; ++u) {
+            if (TOP == kGroups) group_max(v[u], j0 + u * kStep + own);
+          }
         }
         add_logits<kU * E::kN>(a, &v[0][0], c2);
       } else {
@@ -356,8 +438,11 @@ __global__ __launch_bounds__(THREADS) void dora_logprob_fwd(
           if (j0 + u * kStep >= n) break;
           float v[E::kN];
           E::decode(raw[u], v);
-          if (j < n && j + E::kN > n) load_part<BF>(z, j, n, kNegInf, v);
-          if (TOP) group_max(v, j);
+          if (j < n && j + E::kN > n) {
+            load_part<BF>(z, j, n, kNegInf, v);
+            raw[u] = E::encode(v);
+          }
+          if (TOP == kGroups) group_max(v, j);
           add_logits<E::kN>(a, v, c2);
         }
       }
@@ -365,6 +450,7 @@ __global__ __launch_bounds__(THREADS) void dora_logprob_fwd(
       if (j0 >= n) break;
       load(j0);
     }
+    const float most = a.m;
     a = block_stat<THREADS / 64>(a, c2, lds);
     RowOut out;
     if (SPLIT) {
@@ -378,12 +464,12 @@ __global__ __launch_bounds__(THREADS) void dora_logprob_fwd(
       }
     }
     if constexpr (TOP) {
-      __syncthreads();   // the group maxima are complete
+      __shared__ TopLds<THREADS> lists;
       const int k = (int)min((int64_t)top, n);
       uint64_t* mine = SPLIT ? part_top + (row * gridDim.x + blockIdx.x) * top : nullptr;
       if (SPLIT && k < top && (int)threadIdx.x >= k && (int)threadIdx.x < top)
         mine[threadIdx.x] = 0;   // a chunk shorter than the list
-      select_top<BF, THREADS>(z, n, group, k, [&](int rank, uint64_t key) {
+      auto put = [&](int rank, uint64_t key) {
         const uint32_t index = ~(uint32_t)key;
         if (SPLIT) {
           mine[rank] = (key & 0xffffffff00000000ull) | (uint32_t)~(index + (uint32_t)lo);
@@ -392,7 +478,23 @@ __global__ __launch_bounds__(THREADS) void dora_logprob_fwd(
           top_index[row * top + rank] = index;
           top_logp[row * top + rank] = out.none ? kNegInf : (v - out.ref) * scale - out.log_s;
         }
-      });
+      };
+      bool done = false;
+      if constexpr (TOP == kHeld) {
+        done = select_held<BF, THREADS, kU>(raw, most, z, n, k, lists, put);
+        if (!done) {
+#pragma unroll
+          for (int u = 0; u < kU; ++u) {
+            float v[E::kN];
+            E::decode(raw[u], v);
+            group_max(v, u * kStep + own);
+          }
+        }
+      }
+      if (!done) {
+        __syncthreads();   // the group maxima are complete
+        select_top<BF, THREADS>(z, n, group, k, lists, put);
+      }
     }
     __syncthreads();   // LDS is written again for the next row
   }
@@ -410,7 +512,7 @@ __global__ __launch_bounds__(kThreads) void dora_logprob_join(
     const uint64_t* part_top, int splits, float* logp, float* entropy, float* lse, float* top_logp,
     int64_t* top_index, int64_t rows, int64_t V, int top, float scale) {
   using E = Elem<BF>;
-  extern __shared__ uint64_t list[];
+  extern __shared__ __align__(16) uint64_t list[];
   __shared__ uint32_t count;
   const int tid = threadIdx.x, lane = tid & 63;
   const float c2 = scale * kLog2e;
@@ -420,7 +522,7 @@ __global__ __launch_bounds__(kThreads) void dora_logprob_join(
     const uint64_t* lists = TOP ? part_top + row * splits * top : nullptr;
     Stat a = empty_stat();
     uint32_t front[2] = {0, 0};
-    uint64_t last = 0;
+    uint64_t last = 0, early[2] = {0, 0};   // this thread's first keys
     const bool live = y >= 0 && y < V;
     if (live) {
       if (lane < splits) a = stats[lane];
@@ -434,6 +536,9 @@ __global__ __launch_bounds__(kThreads) void dora_logprob_join(
             front[q] = (uint32_t)(lists[(int64_t)(i / deep) * top + i % deep] >> 32);
         }
         if (lane < splits) last = lists[(int64_t)lane * top + top - 1];
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          if (tid + q * kThreads < splits * top) early[q] = lists[tid + q * kThreads];
       }
     }
     if (tid == 0) count = 0;
@@ -458,12 +563,15 @@ __global__ __launch_bounds__(kThreads) void dora_logprob_join(
     }
     if (TOP) {
       __syncthreads();   // count is 0
-      const uint32_t x = kth_largest<2>(front, top);
+      const uint32_t x = kth_largest<2, 12>(front, top);
       const uint32_t hi = wave_max((uint32_t)(last >> 32));
       const uint32_t low = wave_max((uint32_t)(last >> 32) == hi ? (uint32_t)last : 0u);
       // at least 1: keys of 0 pad short lists
       const uint64_t least = max(max((uint64_t)x << 32, ((uint64_t)hi << 32) | low), (uint64_t)1);
-      for (int i = tid; i < splits * top; i += kThreads) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        if (early[q] >= least) list[atomicAdd(&count, 1u)] = early[q];
+      for (int i = tid + 2 * kThreads; i < splits * top; i += kThreads) {
         const uint64_t key = lists[i];
         if (key >= least) list[atomicAdd(&count, 1u)] = key;
       }
@@ -629,7 +737,7 @@ bool past_last_level(const dora_logprob_shape& s) {
 // Short rows are one wave's: no barriers, and four times the rows in flight.
 constexpr int64_t kWaveVocab = 4096;
 
-template <bool BF, int THREADS, bool TOP, bool SPLIT, bool PAST>
+template <bool BF, int THREADS, int TOP, bool SPLIT, bool PAST>
 hipError_t launch_fwd(const dora_logprob_shape& s, const Plan& p, const void* logits,
                       const int64_t* targets, float* logp, float* entropy, float* lse,
                       float* top_logp, int64_t* top_index, Stat* part, uint64_t* part_top,
@@ -648,7 +756,7 @@ hipError_t launch_fwd(const dora_logprob_shape& s, const Plan& p, const void* lo
   }
   if (!SPLIT) return hipSuccess;
   LaunchTimer t("logprob_join", st);
-  hipLaunchKernelGGL((dora_logprob_join<BF, TOP>), dim3((unsigned)std::min(s.rows, kMaxGrid)),
+  hipLaunchKernelGGL((dora_logprob_join<BF, (TOP > 0)>), dim3((unsigned)std::min(s.rows, kMaxGrid)),
                      dim3(kThreads), TOP ? (size_t)(p.splits * s.top * 8) : 0, st, logits, s.ld,
                      targets, part, part_top, (int)p.splits, logp, entropy, lse, top_logp,
                      top_index, s.rows, s.vocab, (int)s.top, s.scale);
@@ -667,20 +775,25 @@ hipError_t forward(const dora_logprob_shape& s, const void* logits, const int64_
     return fn(s, p, logits, targets, logp, entropy, lse, top_logp, top_index, part, part_top, st);
   };
   constexpr int N = kThreads;
-  const bool top = s.top > 0;
-  if (p.splits > 1 && past_last_level<BF>(s))
-    return top ? go(launch_fwd<BF, N, true, true, true>) : go(launch_fwd<BF, N, false, true, true>);
-  if (p.splits > 1)
-    return top ? go(launch_fwd<BF, N, true, true, false>)
-               : go(launch_fwd<BF, N, false, true, false>);
-  if (s.vocab <= kWaveVocab)
-    return top ? go(launch_fwd<BF, 64, true, false, false>)
-               : go(launch_fwd<BF, 64, false, false, false>);
-  if (past_last_level<BF>(s))
-    return top ? go(launch_fwd<BF, N, true, false, true>)
-               : go(launch_fwd<BF, N, false, false, true>);
-  return top ? go(launch_fwd<BF, N, true, false, false>)
-             : go(launch_fwd<BF, N, false, false, false>);
+  const bool top = s.top > 0, past = past_last_level<BF>(s);
+  const int64_t batch = N * kU * Elem<BF>::kN;
+  if (p.splits > 1) {
+    if (top && p.chunk <= batch) return go(launch_fwd<BF, N, kHeld, true, false>);
+    if (top)
+      return past ? go(launch_fwd<BF, N, kGroups, true, true>)
+                  : go(launch_fwd<BF, N, kGroups, true, false>);
+    return past ? go(launch_fwd<BF, N, 0, true, true>) : go(launch_fwd<BF, N, 0, true, false>);
+  }
+  if (s.vocab <= kWaveVocab) {
+    if (!top) return go(launch_fwd<BF, 64, 0, false, false>);
+    return s.vocab <= batch / 4 ? go(launch_fwd<BF, 64, kHeld, false, false>)
+                                : go(launch_fwd<BF, 64, kGroups, false, false>);
+  }
+  if (top && s.vocab <= batch) return go(launch_fwd<BF, N, kHeld, false, false>);
+  if (top)
+    return past ? go(launch_fwd<BF, N, kGroups, false, true>)
+                : go(launch_fwd<BF, N, kGroups, false, false>);
+  return past ? go(launch_fwd<BF, N, 0, false, true>) : go(launch_fwd<BF, N, 0, false, false>);
 }
 
 template <bool BF>

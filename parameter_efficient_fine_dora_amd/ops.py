@@ -451,49 +451,50 @@ class AdamWPlan:
             raise ValueError("params is empty")
         n = len(params)
         small = exp_avg_scales is not None or exp_avg_sq_scales is not None
-        if small and (exp_avg_scales is None or exp_avg_sq_scales is None):
-            raise ValueError("8-bit states need exp_avg_scales and exp_avg_sq_scales")
-        sc1 = list(exp_avg_scales) if small else [None] * n
-        sc2 = list(exp_avg_sq_scales) if small else [None] * n
-        mst = list(masters) if masters is not None else [None] * n
-        for nm, lst in (("exp_avg", exp_avg), ("exp_avg_sq", exp_avg_sq), ("masters", mst),
-                        ("exp_avg_scales", sc1), ("exp_avg_sq_scales", sc2)):
-            if len(lst) != n:
-                raise ValueError(f"{nm} has {len(lst)} tensors, expected {n}")
-        _need(params[0], "params[0]")
-        dev, dt = params[0].device, params[0].dtype
-        self.param_code = _layer_dtype(params[0])
-        if masters is not None and dt != torch.bfloat16:
-            raise ValueError("masters go with bfloat16 params")
+        sc1 = None if exp_avg_scales is None else list(exp_avg_scales)
+        sc2 = None if exp_avg_sq_scales is None else list(exp_avg_sq_scales)
+        mst = None if masters is None else list(masters)
         self.table = (_lib.DoraAdamwTensor * n)()
-        for i in range(n):
-            p = _need(params[i], f"params[{i}]", dt, None, dev)
-            k = p.numel()
-            one = torch.int8 if small else torch.float32
-            two = torch.uint8 if small else torch.float32
-            for t, nm, tdt, size in ((exp_avg[i], "exp_avg", one, k),
-                                     (exp_avg_sq[i], "exp_avg_sq", two, k),
-                                     (sc1[i], "exp_avg_scales", torch.float32, -(-k // _lib.STATE_BLOCK)),
-                                     (sc2[i], "exp_avg_sq_scales", torch.float32, -(-k // _lib.STATE_BLOCK)),
-                                     (mst[i], "masters", torch.float32, k)):
-                if t is None and ((nm == "masters" and masters is None)
-                                  or (nm.endswith("scales") and not small)):
-                    continue
-                _need(t, f"{nm}[{i}]", tdt, None, dev)
-                if t.numel() != size:
-                    raise ValueError(f"{nm}[{i}] has {t.numel()} elements, expected {size}")
-            e = self.table[i]
-            e.param, e.n = p.data_ptr(), k
-            e.exp_avg, e.exp_avg_sq = exp_avg[i].data_ptr(), exp_avg_sq[i].data_ptr()
-            if small:
-                e.exp_avg_scale, e.exp_avg_sq_scale = sc1[i].data_ptr(), sc2[i].data_ptr()
-            if masters is not None:
-                e.master = mst[i].data_ptr()
-        self.params, self.device, self.dtype = params, dev, dt
+        self._address = ctypes.addressof(self.table)
+        code = _compiled().make_table(params, exp_avg, exp_avg_sq, sc1, sc2, mst, self._address)
+        if code is None:
+            code = self._checked_table(params, exp_avg, exp_avg_sq, sc1, sc2, mst)
+        self.param_code = code
+        self.params, self.device, self.dtype = params, params[0].device, params[0].dtype
         self.state_bits = 8 if small else 32
         self.norm_bytes = None   # workspace of the gradients' norm, asked for once
         self._keep = (exp_avg, exp_avg_sq, sc1, sc2, mst)
-        self._address = ctypes.addressof(self.table)
+
+    def _checked_table(self, params, exp_avg, exp_avg_sq, sc1, sc2, mst):
+        """Fills the table tensor by tensor and says what is wrong."""
+        n, small = len(params), sc1 is not None
+        if small != (sc2 is not None):
+            raise ValueError("8-bit states need exp_avg_scales and exp_avg_sq_scales")
+        lists = [("exp_avg", exp_avg, torch.int8 if small else torch.float32, False),
+                 ("exp_avg_sq", exp_avg_sq, torch.uint8 if small else torch.float32, False),
+                 ("exp_avg_scale", sc1, torch.float32, True),
+                 ("exp_avg_sq_scale", sc2, torch.float32, True),
+                 ("master", mst, torch.float32, False)]
+        for nm, lst, _, _ in lists:
+            if lst is not None and len(lst) != n:
+                raise ValueError(f"{nm} has {len(lst)} tensors, expected {n}")
+        _need(params[0], "params[0]")
+        dev, dt = params[0].device, params[0].dtype
+        code = _layer_dtype(params[0])
+        if mst is not None and dt != torch.bfloat16:
+            raise ValueError("masters go with bfloat16 params")
+        for i, (e, p) in enumerate(zip(self.table, params)):
+            k = _need(p, f"params[{i}]", dt, None, dev).numel()
+            e.param, e.n = p.data_ptr(), k
+            for nm, lst, tdt, per_block in lists:
+                if lst is None:
+                    continue
+                t = _need(lst[i], f"{nm}[{i}]", tdt, None, dev)
+                size = -(-k // _lib.STATE_BLOCK) if per_block else k
+                if t.numel() != size:
+                    raise ValueError(f"{nm}[{i}] has {t.numel()} elements, expected {size}")
+                setattr(e, nm, t.data_ptr())
+        return code
 
     def _take_grads(self, grads):
         """Checks the gradients and notes where they are; returns their dtype's code."""

@@ -282,3 +282,28 @@ def test_side_stream_and_graph(ops):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, want))
         assert all(torch.equal(a, b) for a, b in zip(step(), want))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,V,top", [(3, 1500, 20), (5, 2048, 64), (2, 2049, 64), (3, 6000, 33),
+                                     (2, 8192, 64), (40, 8193, 5), (1100, 4100, 7), (1050, 9000, 64)])
+def test_top_of_every_arrangement(ops, T, V, top, dtype):
+    """Rows of one wave, of one workgroup and cut into chunks, each held in registers or streamed:
+    random rows, constant ones (every element a tie), one whose largest lie together at its end,
+    and rows of few distinct values with most of them masked."""
+    say("arrangements", T, V, top, dtype)
+    z, y = logits(T, V, DT[dtype], 7 * V + T)
+    z[0] = 1.5
+    if T > 1:
+        z[1] = torch.linspace(-4, 4, V, device="cuda").to(DT[dtype])
+    if T > 2:
+        z[2] = (torch.arange(V, device="cuda") % 3).to(DT[dtype])
+        z[2, torch.arange(V, device="cuda") % 50 != 0] = NEG
+    rows = sorted({0, min(1, T - 1), min(2, T - 1), T // 2, T - 1})
+    got = ops.dora_token_logprob(z, y, top=top)
+    want = ref.token_logprob(download(z[rows].contiguous()), y[rows].cpu().numpy(), 1.0, top)
+    assert np.array_equal(got[4][rows].cpu().numpy(), want[4])
+    base = V / 256 + 64
+    low = np.where(np.isfinite(want[3]), np.abs(want[3]), 0.0)
+    held(download(got[3][rows]), want[3], U * (base + 8 * (low + np.log(V))), "top_logp")
+    held(download(got[1][rows]), want[1], U * base * (1 + 2 * np.log(V)), "entropy")
