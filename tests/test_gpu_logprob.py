@@ -307,3 +307,26 @@ def test_top_of_every_arrangement(ops, T, V, top, dtype):
     low = np.where(np.isfinite(want[3]), np.abs(want[3]), 0.0)
     held(download(got[3][rows]), want[3], U * (base + 8 * (low + np.log(V))), "top_logp")
     held(download(got[1][rows]), want[1], U * base * (1 + 2 * np.log(V)), "entropy")
+
+
+@pytest.mark.parametrize("T,V", [(1030, 50257), (6, 50257), (1100, 8193), (3, 16385), (1500, 3001)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_rows_bits_do_not_depend_on_its_address(ops, T, V, dtype):
+    """Rows of an odd vocabulary start at every alignment; equal rows give equal bits, wherever
+    the first of them starts."""
+    say("addresses", T, V, dtype)
+    one = (torch.randn(V, device="cuda") * 3).to(DT[dtype])
+    y = torch.full((T,), 11, device="cuda")
+    ga = torch.full((T,), 0.5, device="cuda")
+    seen = []
+    for start in (0, 1, 2):
+        buf = torch.full((T * V + 8,), float("nan"), dtype=DT[dtype], device="cuda")
+        z = buf[start:start + T * V].view(T, V)
+        z[:] = one
+        got = ops.dora_token_logprob(z, y, top=4)
+        g = ops.dora_token_logprob_backward(ga, ga, z, y, got[2], got[1])
+        for t in (*got, g):
+            assert torch.equal(t, t[:1].expand_as(t))
+        seen.append([t[0].clone() for t in (*got, g)])
+    for later in seen[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(seen[0], later))
