@@ -1,5 +1,5 @@
-"""ctypes view of libdora.so (include/dora.h).  No torch here: loading and the
-host-only entry points work without a GPU."""
+"""ctypes view of libdora.so (include/dora.h, include/dora_finetune.h).  No torch here: loading
+and the host-only entry points work without a GPU."""
 from __future__ import annotations
 
 import ctypes

@@ -5,9 +5,9 @@
 #include <cstdint>
 #include <type_traits>
 
-#include "../../include/dora.h"
+#include "../../include/dora_finetune.h"
+#include "checks.h"
 #include "elem.h"
-#include "entry.h"
 #include "kernels.h"
 
 namespace dora {

@@ -324,6 +324,17 @@ int check_ptr(const void* p, bool empty) {
   return aligned(p) ? DORA_OK : DORA_ERR_ALIGN;
 }
 
+#define DORA_CHECK(expr)          \
+  do {                            \
+    const int rc_ = (expr);       \
+    if (rc_ != DORA_OK) return rc_; \
+  } while (0)
+
+#define HIP_TRY(expr)                                 \
+  do {                                                \
+    if ((expr) != hipSuccess) return DORA_ERR_HIP;    \
+  } while (0)
+
 uint8_t* at(void* ws, size_t off) { return reinterpret_cast<uint8_t*>(ws) + off; }
 
 void give_scratch(GemmProblem& g, void* ws, const Layout& L) {

@@ -12,7 +12,7 @@
 
 #include <cstring>
 
-#include "../../include/dora.h"
+#include "../../include/dora_finetune.h"
 
 namespace {
 

@@ -4,9 +4,9 @@
 #include <cmath>
 #include <cstdint>
 
-#include "../../include/dora.h"
+#include "../../include/dora_finetune.h"
+#include "checks.h"
 #include "elem.h"
-#include "entry.h"
 #include "kernels.h"
 
 namespace dora {

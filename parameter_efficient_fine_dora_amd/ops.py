@@ -441,7 +441,8 @@ class AdamWPlan:
     masters        float32 copies of bf16 parameters, or None
 
     The plan refers to the tensors (they stay alive with it) and writes through them.  A parameter
-    whose storage was exchanged since (``p.data = ...``) is an error at the next step.
+    whose storage was exchanged since (``p.data = ...``) is an error at the next step; moments,
+    scales and masters keep the storage they had when the plan was made.
     """
 
     def __init__(self, params, exp_avg, exp_avg_sq, *, masters=None, exp_avg_scales=None,
@@ -556,7 +557,8 @@ def dora_adamw(plan, grads, *, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_de
     if max_norm is not None:
         norm, grad_scale = _grad_norm(plan, code, max_norm, workspace)
     elif grad_scale is not None:
-        _need(grad_scale, "grad_scale", torch.float32, None, plan.device)
+        if _need(grad_scale, "grad_scale", torch.float32, None, plan.device).numel() != 1:
+            raise ValueError("grad_scale must be one number")
     _check(_compiled().adamw_step(plan._address, len(plan.params), plan.param_code, code,
                                   plan.state_bits, int(step), float(lr), float(betas[0]),
                                   float(betas[1]), float(eps), float(weight_decay), grad_scale,

@@ -2,6 +2,7 @@
 header lays them out, arguments refused before anything is enqueued, workspace sizes."""
 import ctypes
 import os
+import re
 
 import pytest
 
@@ -10,6 +11,17 @@ from parameter_efficient_fine_dora_amd import _lib
 pytestmark = pytest.mark.skipif(not os.path.exists(_lib.LIB_PATH), reason="libdora.so not built")
 E = _lib.ERR_CODE
 FAKE = 0x10000   # never dereferenced: every call here is refused
+
+
+HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include",
+                      "dora_finetune.h")
+
+
+def test_library_exports_and_binds_every_declared_symbol():
+    names = re.findall(r"DORA_API\s+[\w\s\*]+?\b(dora_\w+)\s*\(", open(HEADER).read())
+    assert len(names) == 11
+    for name in names:
+        assert hasattr(_lib.lib(), name) and name in _lib._SIGS, name
 
 
 def test_structs_match_the_header():

@@ -349,3 +349,11 @@ def test_side_stream_and_graph(ops):
         d = fresh()
         step(d, d.plan())
         assert all(torch.equal(x, y) for x, y in zip(bits(d), want[0]))
+
+
+def test_grad_scale_is_one_number(ops):
+    p, s = torch.zeros(8, device="cuda"), torch.zeros(8, device="cuda")
+    plan = ops.AdamWPlan([p], [s], [s.clone()])
+    for bad in (s[:0], s[:2]):
+        with pytest.raises(ValueError, match="one number"):
+            ops.dora_adamw(plan, [s], step=1, lr=1e-3, grad_scale=bad)
