@@ -738,7 +738,7 @@ int check_shape(const dora_logprob_shape* s) {
 
 // How many workgroups read a row.  With rows enough to give every CU a few
 // workgroups each row is one workgroup's; below that rows are cut until about
-// kWantBlocks workgroups run, no chunk under kU vectors a thread.
+// kWantBlocks workgroups run, down to chunks of one batch (kU vectors a thread).
 constexpr int64_t kWantBlocks = 1024;
 struct Plan {
   int64_t chunk, splits;
@@ -747,7 +747,9 @@ struct Plan {
 Plan plan(const dora_logprob_shape& s) {
   Plan p;
   const int64_t unit = kThreads * kU * (s.dtype == DORA_BF16 ? 8 : 4);
-  const int64_t most = std::min(kMaxSplits, std::max<int64_t>(1, s.vocab / unit));
+  // rows of under two batches are not worth the join
+  const int64_t batches = s.vocab < 2 * unit ? 1 : (s.vocab + unit - 1) / unit;
+  const int64_t most = std::min(kMaxSplits, batches);
   const int64_t want = std::max<int64_t>(1, kWantBlocks / std::max<int64_t>(1, s.rows));
   const int64_t least = (s.vocab + kMaxChunk - 1) / kMaxChunk;
   const int64_t n = std::max(least, std::min(want, most));
