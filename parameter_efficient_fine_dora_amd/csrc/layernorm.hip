@@ -19,9 +19,10 @@ constexpr int64_t kMaxGrid = int64_t(1) << 21;
 
 // ---- rows that fit a workgroup's registers --------------------------------------
 // A row is held by as many waves as take kElems elements (or, past 16384 elements,
-// twice that) of it per thread, in 16-byte vectors that the threads take in turn.  Memory is read once; mean and centred squares are sums over registers.
-// What a width leaves past its last whole vector, at most 7 elements, is one
-// more scalar of the first threads.  Vectors stay as they were loaded and are
+// twice that) of it per thread, in 16-byte vectors that the threads take in turn.
+// Memory is read once; mean and centred squares are sums over registers.  What a
+// width leaves past its last whole vector, at most 7 elements, is one more scalar
+// of the first threads.  Vectors stay as they were loaded and are
 // decoded where they are used: registers, not arithmetic, limit how many rows a
 // CU has in flight.
 constexpr int kElems = 16;
@@ -189,9 +190,11 @@ __global__ __launch_bounds__(bwd_rows(BF, THREADS) * THREADS) void dora_layernor
     g = g_next;
     x = x_next;
     if (first + stride < rows) fetch(row + stride);
-    float s[2];   // absent elements have gy = 0
+    // absent elements have x = gy = 0 and take 0 for their mean: (0 - mean) rstd may
+    // be infinite
+    float s[2];
     {
-      const float n = (x.t() - mean) * rstd, h = g.t() * w.t();
+      const float n = (x.t() - (S::has_tail(D) ? mean : 0.f)) * rstd, h = g.t() * w.t();
       gw_t = fmaf(g.t(), n, gw_t);
       gb_t += g.t();
       s[0] = h;
@@ -203,9 +206,10 @@ __global__ __launch_bounds__(bwd_rows(BF, THREADS) * THREADS) void dora_layernor
       g.decode(u, gv, s[0]);
       x.decode(u, xv, s[0]);
       w.decode(u, wv, s[0]);
+      const float mu = S::has(u, D) ? mean : 0.f;
 #pragma unroll
       for (int q = 0; q < E::kN; ++q) {
-        const float n = (xv[q] - mean) * rstd, h = gv[q] * wv[q];
+        const float n = (xv[q] - mu) * rstd, h = gv[q] * wv[q];
         if (W) {
           gw[u * E::kN + q] = fmaf(gv[q], n, gw[u * E::kN + q]);
           gb[u * E::kN + q] += gv[q];

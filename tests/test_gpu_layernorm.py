@@ -226,3 +226,24 @@ def test_side_stream_and_graph(ops):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b_) for a, b_ in zip(out, want))
         assert all(torch.equal(a, b_) for a, b_ in zip(step(), want))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("width", [1, 5, 70, 1001, 5121, 8200])
+def test_gradient_of_constant_rows_whose_mean_times_rstd_overflows(ops, width, dtype):
+    """Sums of 2^114 are exact, so xhat is 0 and the formula leaves the centred gradient; what a
+    row's width leaves of the last threads must not bring in 0 - mean."""
+    dt = {"bf16": torch.bfloat16, "f32": torch.float32}[dtype]
+    x = torch.full((3, width), 2.0 ** 114, dtype=dt, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(width)
+    gy = torch.randn(3, width, device="cuda", generator=gen).to(dt)
+    _, mean, rstd = ops.dora_layernorm(x, None, None, eps=1e-12)
+    assert torch.equal(mean, x[:, 0].float())
+    gx, gw, gb = ops.dora_layernorm_backward(gy, x, None, mean, rstd)
+    assert torch.count_nonzero(gw) == 0
+    g = gy.double()
+    want = rstd.double()[:, None] * (g - g.mean(1, keepdim=True))
+    # float32 sums of terms below 6, then one rounding to the type (half a unit in the last place)
+    half = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -24
+    assert ((gx.double() - want).abs() <= want.abs() * half + 2e-5 * rstd.double()[:, None]).all()
+    assert ((gb.double() - g.sum(0)).abs() <= g.sum(0).abs() * half + 2e-6).all()
