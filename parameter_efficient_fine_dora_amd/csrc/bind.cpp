@@ -153,6 +153,7 @@ PyObject* token_logprob(PyObject*, PyObject* const* args, Py_ssize_t n) {
   s.dtype = dtype_code(z->scalar_type());
   s.scale = (float)PyFloat_AS_DOUBLE(args[2]);
   const long top = PyLong_AsLong(args[3]);
+  if (top == -1 && PyErr_Occurred()) PyErr_Clear();
   if (top < 0 || top > DORA_LOGPROB_MAX_TOP || !vector_ok(y, s.rows, at::kLong, *z)) Py_RETURN_NONE;
   s.top = (int32_t)top;
   const auto f32 = z->options().dtype(at::kFloat);
@@ -302,13 +303,15 @@ PyObject* grad_norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// adamw_step(table address, count, param code, grad code, state bits, step, lr, beta1, beta2, eps,
-// weight_decay, grad_scale or None, stream) -> the return code
+// adamw_step(table address, params, param code, grad code, state bits, step, lr, beta1, beta2, eps,
+// weight_decay, grad_scale or None, stream) -> the return code.  The parameters' versions go up, so
+// that a backward pass which saved one of them from before the step is refused.
 PyObject* adamw_step(PyObject*, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  bool ok = n == 13;
+  bool ok = n == 13 && PyList_Check(args[1]);
   const at::Tensor* scale = ok ? tensor(args[11], ok) : nullptr;
   if (!ok) Py_RETURN_NONE;
+  const Py_ssize_t count = PyList_GET_SIZE(args[1]);
   dora_adamw_options o = {};
   o.param_dtype = (int32_t)PyLong_AsLong(args[2]);
   o.grad_dtype = (int32_t)PyLong_AsLong(args[3]);
@@ -321,8 +324,13 @@ PyObject* adamw_step(PyObject*, PyObject* const* args, Py_ssize_t n) {
   o.weight_decay = PyFloat_AsDouble(args[10]);
   o.grad_scale = floats(scale);
   if (PyErr_Occurred()) return nullptr;
-  return PyLong_FromLong(g_api.adamw_step(static_cast<dora_adamw_tensor*>(PyLong_AsVoidPtr(args[0])),
-                                          PyLong_AsLongLong(args[1]), &o, stream_of(args[12])));
+  const int rc = g_api.adamw_step(static_cast<dora_adamw_tensor*>(PyLong_AsVoidPtr(args[0])), count,
+                                  &o, stream_of(args[12]));
+  for (Py_ssize_t i = 0; rc == DORA_OK && i < count; ++i) {
+    const at::Tensor* p = tensor(PyList_GET_ITEM(args[1], i), ok);
+    if (p && !p->is_inference()) p->unsafeGetTensorImpl()->bump_version();
+  }
+  return PyLong_FromLong(rc);
   END_HANDLE_TH_ERRORS
 }
 

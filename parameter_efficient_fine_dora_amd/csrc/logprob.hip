@@ -362,8 +362,8 @@ __device__ bool select_held(const typename Elem<BF>::Vec* raw, float most,
 // TOP: 0 without alternatives; kGroups through the group maxima; kHeld for chunks
 // of one batch, which are still in registers when their statistics are known (one
 // kernel for both would keep one workgroup less per SIMD: 141 us against 119 at
-// 2048 x 131072 bf16, top 20).  PAST: the logits do not fit the last-level cache and are loaded past it
-// (3584 x 131072 bf16: 159 us against 177, 5.9 TB/s).
+// 2048 x 131072 bf16, top 20).  PAST: the logits do not fit the last-level cache
+// and are loaded past it (3584 x 131072 bf16: 159 us against 177, 5.9 TB/s).
 constexpr int kGroups = 1, kHeld = 2;
 template <bool BF, int THREADS, int TOP, bool SPLIT, bool PAST>
 __global__ __launch_bounds__(THREADS) void dora_logprob_fwd(

@@ -10,6 +10,7 @@ from __future__ import annotations
 import math
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import ops
 
@@ -126,6 +127,14 @@ class DVoRALinear(torch.nn.Module):
         return y.reshape(*lead, y.shape[-1])
 
 
+def _as_rows(x):
+    """x as [rows, width], copied if rows are not contiguous or overlap (a broadcast input's)."""
+    x2 = x.reshape(-1, x.shape[-1])
+    if x2.stride(1) != 1 or (x2.shape[0] > 1 and x2.stride(0) < x2.shape[1]):
+        x2 = x2.contiguous()
+    return x2
+
+
 class LayerNormFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, eps):
@@ -134,6 +143,7 @@ class LayerNormFunction(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, gy):
         x, weight, mean, rstd = ctx.saved_tensors
         need = tuple(n for n, k in (("x", 0), ("weight", 1), ("bias", 2)) if ctx.needs_input_grad[k])
@@ -154,9 +164,7 @@ class LayerNorm(torch.nn.Module):
         self.eps = float(eps)
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
-        x2 = x.reshape(-1, x.shape[-1])
-        if x2.stride(-1) != 1:
-            x2 = x2.contiguous()
+        x2 = _as_rows(x)
         return LayerNormFunction.apply(x2, self.weight, self.bias, self.eps).reshape(x.shape)
 
 
@@ -173,6 +181,7 @@ class TokenLogProbFunction(torch.autograd.Function):
         return logp, entropy, top_logp, top_index
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, g_logp, g_entropy, _g_top, _g_index):
         if g_logp is None and g_entropy is None:
             return None, None, None, None
@@ -191,9 +200,7 @@ def token_logprob(logits: torch.Tensor, targets: torch.Tensor, *, scale: float =
     give zeros and no gradient.
     """
     lead = targets.shape
-    z = logits.reshape(-1, logits.shape[-1])
-    if z.stride(-1) != 1:
-        z = z.contiguous()
+    z = _as_rows(logits)
     logp, entropy, top_logp, top_index = TokenLogProbFunction.apply(z, targets.reshape(-1).contiguous(),
                                                                     float(scale), int(top))
     if top:

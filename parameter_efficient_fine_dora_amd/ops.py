@@ -387,7 +387,8 @@ def dora_token_logprob(logits, targets, *, scale=1.0, top=0, workspace=None):
     dev = logits.device
     T, V = logits.shape
     _need(targets, "targets", torch.int64, (T,), dev)
-    sh = _lib.DoraLogprobShape(T, V, ld, _layer_dtype(logits), int(top), float(scale), 0)
+    top = int(top) if 0 <= top <= _lib.LOGPROB_MAX_TOP else -1   # ctypes would cut a larger number
+    sh = _lib.DoraLogprobShape(T, V, ld, _layer_dtype(logits), top, float(scale), 0)
     logp, entropy, lse = torch.empty(3, T, dtype=torch.float32, device=dev).unbind(0)
     top_logp = top_index = None
     if top > 0:
@@ -559,7 +560,7 @@ def dora_adamw(plan, grads, *, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_de
     elif grad_scale is not None:
         if _need(grad_scale, "grad_scale", torch.float32, None, plan.device).numel() != 1:
             raise ValueError("grad_scale must be one number")
-    _check(_compiled().adamw_step(plan._address, len(plan.params), plan.param_code, code,
+    _check(_compiled().adamw_step(plan._address, plan.params, plan.param_code, code,
                                   plan.state_bits, int(step), float(lr), float(betas[0]),
                                   float(betas[1]), float(eps), float(weight_decay), grad_scale,
                                   _stream(plan.device)), "dora_adamw_step")
