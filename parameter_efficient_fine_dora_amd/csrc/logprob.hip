@@ -1,5 +1,13 @@
 // Log probabilities of given tokens under rows of logits, with the entropy and
-// the top alternatives of each row, and their gradient.
+// the top alternatives of each row, and their gradient.  With m the row's maximum,
+// d_j = scale (z_j - m), s = sum exp(d_j) and u = sum d_j exp(d_j):
+//   logp = d_y - log s,  entropy H = log s - u / s,  lse = scale m + log s
+//   grad z_j = scale (a ([j = y] - p_j) - b p_j (log p_j + H)), p_j = exp(d_j) / s
+// for gradients a of logp and b of entropy.  Statistics are float32.  Memory
+// bounds long calls: the forward reads the logits once (4096 x 131072 bf16, an
+// eighth of the rows skipped: 145 us, 6.5 TB/s), the gradient reads and writes
+// them once (318 us, 6.3 TB/s).  Few rows are bound by latency: one of 131072
+// bf16 with its top 20 takes 7 us and 4 us for the join.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
