@@ -41,7 +41,8 @@ struct Elem<true> {
     for (int d = 0; d < 4; ++d) v[d] = pack_bf16x2(in[2 * d], in[2 * d + 1]);
     return v;
   }
-  __device__ static void store(T* p, const float* in) { *reinterpret_cast<Raw*>(p) = encode(in); }
+  __device__ static void store_raw(T* p, Vec v) { *reinterpret_cast<Raw*>(p) = v; }
+  __device__ static void store(T* p, const float* in) { store_raw(p, encode(in)); }
   // past the caches, for what is too large to stay in them
   __device__ static void store_through(T* p, const float* in) {
     __builtin_nontemporal_store(encode(in), reinterpret_cast<Raw*>(p));
@@ -72,7 +73,8 @@ struct Elem<false> {
   }
   __device__ static void load(const T* p, float* out) { decode(raw(p), out); }
   __device__ static Vec encode(const float* in) { return Vec{in[0], in[1], in[2], in[3]}; }
-  __device__ static void store(T* p, const float* in) { *reinterpret_cast<Raw*>(p) = encode(in); }
+  __device__ static void store_raw(T* p, Vec v) { *reinterpret_cast<Raw*>(p) = v; }
+  __device__ static void store(T* p, const float* in) { store_raw(p, encode(in)); }
   // past the caches, for what is too large to stay in them
   __device__ static void store_through(T* p, const float* in) {
     __builtin_nontemporal_store(encode(in), reinterpret_cast<Raw*>(p));

@@ -150,7 +150,7 @@ __global__ __launch_bounds__(THREADS) void dora_layernorm_fwd(
 // R rows at a time, THREADS threads to a row.  Every thread keeps the sums of its
 // own columns in registers over all its rows, and at the end the R rows' threads
 // add theirs through LDS: part[blockIdx.x][0 or 1][column], as few partial sums as
-// there are CUs.  The next row is loaded before this row's reduction.  A row
+// there are CUs.  The next rows are loaded before this row's reduction.  A row
 // costs a CU about 20 operations an element, half of what memory takes, and
 // waits twice for its reductions: several rows at a time fill those gaps.
 constexpr int kMaxBwdThreads = 512;   // of a row
@@ -158,7 +158,13 @@ constexpr int bwd_rows(bool bf, int threads) {
   // rows of one or two waves leave sums of 12 rows to add for little: 8 waves
   return (bf && threads > 128 ? 12 : 8) * 64 / threads;
 }
-template <bool BF, int THREADS, int NV, bool W>
+// Rows fetched ahead: two where one row's waves leave registers for it (4096 x 8192
+// bf16: 45 us against 47 with one or three; float32 loses, 1031 x 5121 21 us
+// against 20).
+constexpr int bwd_ahead(bool bf, int threads) {
+  return bf && threads > 384 ? 2 : 1;
+}
+template <bool BF, int THREADS, int NV, bool W, bool GX>
 __global__ __launch_bounds__(bwd_rows(BF, THREADS) * THREADS) void dora_layernorm_bwd(
     const void* gy_, int64_t ldg, const void* x_, int64_t ldx, const void* w_, const float* mean_in,
     const float* rstd_in, void* gx_, float* part, int64_t rows, uint32_t D) {
@@ -170,36 +176,39 @@ __global__ __launch_bounds__(bwd_rows(BF, THREADS) * THREADS) void dora_layernor
   __shared__ float lds[2][R][2 * kWaves];
   __shared__ __align__(16) float comb[W && R > 1 ? R : 1][W && R > 1 ? THREADS * NV * E::kN : 4];
   const int sub = __builtin_amdgcn_readfirstlane((int)threadIdx.x / THREADS);   // per wave
-  S w, g, x, g_next, x_next;
-  float mean_next = 0.f, rstd_next = 0.f;
+  constexpr int kAhead = bwd_ahead(BF, THREADS);
+  // vectors that every thread has, from the narrowest row of so many threads
+  constexpr int kFull = (THREADS / 64 - 1) * 64 * kElems / (THREADS * E::kN);
+  S w, g, x, g_next[kAhead], x_next[kAhead];
+  float mean_next[kAhead], rstd_next[kAhead];
   float gw[NV * E::kN], gb[NV * E::kN], gw_t = 0.f, gb_t = 0.f;
 #pragma unroll
   for (int i = 0; i < NV * E::kN; ++i) gw[i] = gb[i] = 0.f;
   const int64_t stride = (int64_t)gridDim.x * R;
   // rows past the last load as zeros, which add nothing
-  auto fetch = [&](int64_t row) {
+  auto fetch = [&](int64_t row, int slot) {
     const bool valid = row < rows;
     const int64_t at = valid ? row : 0;
     const uint32_t n = valid ? D : 0;
-    g_next.load(reinterpret_cast<const T*>(gy_) + at * ldg, n);
-    x_next.load(reinterpret_cast<const T*>(x_) + at * ldx, n);
-    mean_next = valid ? mean_in[row] : 0.f;
-    rstd_next = valid ? rstd_in[row] : 0.f;
+    g_next[slot].load(reinterpret_cast<const T*>(gy_) + at * ldg, n);
+    x_next[slot].load(reinterpret_cast<const T*>(x_) + at * ldx, n);
+    mean_next[slot] = valid ? mean_in[row] : 0.f;
+    rstd_next[slot] = valid ? rstd_in[row] : 0.f;
   };
   int64_t row = (int64_t)blockIdx.x * R + sub;
-  fetch(row);
+#pragma unroll
+  for (int slot = 0; slot < kAhead; ++slot) fetch(row + slot * stride, slot);
   if (w_)
     w.load(reinterpret_cast<const T*>(w_), D);
   else
     w.fill(1.f);
   int buf = 0;
-  // every thread of the workgroup takes the same number of turns
-  for (int64_t first = (int64_t)blockIdx.x * R; first < rows;
-       first += stride, row += stride, buf ^= 1) {
-    const float mean = mean_next, rstd = rstd_next;
-    g = g_next;
-    x = x_next;
-    if (first + stride < rows) fetch(row + stride);
+  int64_t first = (int64_t)blockIdx.x * R;
+  auto turn = [&](int slot, bool all) {   // all: every wave has a row
+    const float mean = mean_next[slot], rstd = rstd_next[slot];
+    g = g_next[slot];
+    x = x_next[slot];
+    if (first + kAhead * stride < rows) fetch(row + kAhead * stride, slot);
     // absent elements have x = gy = 0 and take 0 for their mean: (0 - mean) rstd may
     // be infinite
     float s[2];
@@ -216,7 +225,7 @@ __global__ __launch_bounds__(bwd_rows(BF, THREADS) * THREADS) void dora_layernor
       g.decode(u, gv, s[0]);
       x.decode(u, xv, s[0]);
       w.decode(u, wv, s[0]);
-      const float mu = S::has(u, D) ? mean : 0.f;
+      const float mu = u < kFull || S::has(u, D) ? mean : 0.f;
 #pragma unroll
       for (int q = 0; q < E::kN; ++q) {
         const float n = (xv[q] - mu) * rstd, h = gv[q] * wv[q];
@@ -228,12 +237,16 @@ __global__ __launch_bounds__(bwd_rows(BF, THREADS) * THREADS) void dora_layernor
         s[1] = fmaf(h, n, s[1]);
       }
     }
-    if (!gx_) continue;
+    if (!GX) return;
     group_sum<kWaves, 2>(s, lds[buf][sub], threadIdx.x % THREADS);
-    if (row >= rows) continue;
+    if (!all && row >= rows) return;
     const float c2 = s[1] / (float)D;
     float c1 = s[0] / (float)D;
     T* gx = reinterpret_cast<T*>(gx_) + row * D;
+    if (S::has_tail(D))
+      E::put(gx + S::body(D) + S::lane(),
+             rstd * (g.t() * w.t() - fmaf((x.t() - mean) * rstd, c2, c1)));
+    typename E::Vec zeroth;
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
       float gv[E::kN], xv[E::kN], wv[E::kN];
@@ -243,11 +256,37 @@ __global__ __launch_bounds__(bwd_rows(BF, THREADS) * THREADS) void dora_layernor
 #pragma unroll
       for (int q = 0; q < E::kN; ++q)
         gv[q] = rstd * (gv[q] * wv[q] - fmaf((xv[q] - mean) * rstd, c2, c1));
-      if (S::has(u, D)) E::store(gx + S::at(u), gv);
+      typename E::Vec out = E::encode(gv);
+      if (u == 0) zeroth = out;
+      if (kFull > 0) {
+        // stores without a branch: a thread that lacks the vector repeats its first
+        const bool in = u < kFull || S::has(u, D);
+#pragma unroll
+        for (int d = 0; d < 4; ++d) out[d] = in ? out[d] : zeroth[d];
+        E::store_raw(gx + (in ? S::at(u) : S::at(0)), out);
+      } else if (S::has(u, D)) {
+        E::store_raw(gx + S::at(u), out);
+      }
     }
-    if (S::has_tail(D))
-      E::put(gx + S::body(D) + S::lane(), rstd * (g.t() * w.t() - fmaf((x.t() - mean) * rstd, c2, c1)));
+  };
+  // Every thread of the workgroup takes the same number of turns.  Where all have a
+  // row no branch skips a vector's store: the wait for the next row's loads then
+  // counts the stores behind them, instead of waiting for those too (4096 x 8192
+  // bf16: 45 us against 50).
+  static_assert(R == 1 || kAhead == 1, "a last turn without rows for all");
+  bool more = first + R <= rows;
+  while (more) {
+#pragma unroll
+    for (int slot = 0; slot < kAhead; ++slot) {
+      turn(slot, true);
+      first += stride;
+      row += stride;
+      buf ^= 1;
+      more = first + R <= rows;
+      if (!more) break;
+    }
   }
+  if (R > 1 && first < rows) turn(0, false);
   if (!W) return;
   float* dst = part + (int64_t)blockIdx.x * 2 * (int64_t)D;
   auto put = [&](float* to, const float* v, float t) {
@@ -585,15 +624,14 @@ hipError_t backward(const dora_layernorm_shape& s, const void* gy, const void* x
     LaunchTimer t("layernorm_bwd", st);
     const hipError_t e = with_any_threads(row_threads(s.width), [&](auto threads) {
       const dim3 block(bwd_rows(BF, threads()) * threads());
-      if (sums)
-        hipLaunchKernelGGL((dora_layernorm_bwd<BF, threads(), NV, true>), dim3((unsigned)blocks),
-                           block, 0, st, gy, s.ld_gy, x, s.ld_x, w, mean, rstd, gx,
-                           part, s.rows, (uint32_t)s.width);
-      else
-        hipLaunchKernelGGL((dora_layernorm_bwd<BF, threads(), NV, false>), dim3((unsigned)blocks),
-                           block, 0, st, gy, s.ld_gy, x, s.ld_x, w, mean, rstd, gx,
-                           part, s.rows, (uint32_t)s.width);
-      return hipGetLastError();
+      auto launch = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), block, 0, st, gy, s.ld_gy, x, s.ld_x, w,
+                           mean, rstd, gx, part, s.rows, (uint32_t)s.width);
+        return hipGetLastError();
+      };
+      if (!gx) return launch(dora_layernorm_bwd<BF, threads(), NV, true, false>);
+      return sums ? launch(dora_layernorm_bwd<BF, threads(), NV, true, true>)
+                  : launch(dora_layernorm_bwd<BF, threads(), NV, false, true>);
     });
     if (e) return e;
   } else if (s.rows > 0 && (gx || sums)) {
