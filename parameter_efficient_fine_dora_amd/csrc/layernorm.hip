@@ -28,8 +28,8 @@ namespace {
 constexpr int64_t kMaxGrid = int64_t(1) << 21;
 
 // ---- rows that fit a workgroup's registers --------------------------------------
-// A row is held by as many waves as take kElems elements (or, past 16384 elements,
-// twice that) of it per thread, in 16-byte vectors that the threads take in turn.
+// A row is held by as many waves as take kElems elements (wide rows: twice that) of
+// it per thread, in 16-byte vectors that the threads take in turn.
 // Memory is read once; mean and centred squares are sums over registers.  What a
 // width leaves past its last whole vector, at most 7 elements, is one more scalar
 // of the first threads.  Vectors stay as they were loaded and are
@@ -147,38 +147,41 @@ __global__ __launch_bounds__(THREADS) void dora_layernorm_fwd(
 
 // grad_x, and with W the workgroup's share of grad_weight and grad_bias.  A
 // workgroup is a CU's: as many waves as its registers hold (bf16 12, float32 8),
-// R rows at a time, THREADS threads to a row.  Every thread keeps the sums of its
+// R rows at a time, THREADS threads to a row.  bf16 rows past 8192 elements are one
+// row of 5 to 8 waves that hold twice as much (2048 x 16384: 49 us against 81 in two
+// passes); float32 ones would spill.  Every thread keeps the sums of its
 // own columns in registers over all its rows, and at the end the R rows' threads
 // add theirs through LDS: part[blockIdx.x][0 or 1][column], as few partial sums as
 // there are CUs.  The next rows are loaded before this row's reduction.  A row
 // costs a CU about 20 operations an element, half of what memory takes, and
 // waits twice for its reductions: several rows at a time fill those gaps.
 constexpr int kMaxBwdThreads = 512;   // of a row
-constexpr int bwd_rows(bool bf, int threads) {
+constexpr int bwd_rows(bool bf, int threads, bool wide) {
   // rows of one or two waves leave sums of 12 rows to add for little: 8 waves
-  return (bf && threads > 128 ? 12 : 8) * 64 / threads;
+  return wide ? 1 : (bf && threads > 128 ? 12 : 8) * 64 / threads;
 }
 // Rows fetched ahead: two where one row's waves leave registers for it (4096 x 8192
 // bf16: 45 us against 47 with one or three; float32 loses, 1031 x 5121 21 us
 // against 20).
-constexpr int bwd_ahead(bool bf, int threads) {
-  return bf && threads > 384 ? 2 : 1;
+constexpr int bwd_ahead(bool bf, int threads, bool wide) {
+  return bf && !wide && threads > 384 ? 2 : 1;
 }
 template <bool BF, int THREADS, int NV, bool W, bool GX>
-__global__ __launch_bounds__(bwd_rows(BF, THREADS) * THREADS) void dora_layernorm_bwd(
+__global__ __launch_bounds__(bwd_rows(BF, THREADS, NV * Elem<BF>::kN > kElems) * THREADS) void dora_layernorm_bwd(
     const void* gy_, int64_t ldg, const void* x_, int64_t ldx, const void* w_, const float* mean_in,
     const float* rstd_in, void* gx_, float* part, int64_t rows, uint32_t D) {
   using E = Elem<BF>;
   using T = typename E::T;
   using S = Share<BF, THREADS, NV>;
-  constexpr int R = bwd_rows(BF, THREADS);
+  constexpr bool kWide = NV * E::kN > kElems;
+  constexpr int R = bwd_rows(BF, THREADS, kWide);
   constexpr int kWaves = THREADS / 64;
   __shared__ float lds[2][R][2 * kWaves];
   __shared__ __align__(16) float comb[W && R > 1 ? R : 1][W && R > 1 ? THREADS * NV * E::kN : 4];
   const int sub = __builtin_amdgcn_readfirstlane((int)threadIdx.x / THREADS);   // per wave
-  constexpr int kAhead = bwd_ahead(BF, THREADS);
+  constexpr int kAhead = bwd_ahead(BF, THREADS, kWide);
   // vectors that every thread has, from the narrowest row of so many threads
-  constexpr int kFull = (THREADS / 64 - 1) * 64 * kElems / (THREADS * E::kN);
+  constexpr int kFull = (THREADS - 64) * NV / THREADS;
   S w, g, x, g_next[kAhead], x_next[kAhead];
   float mean_next[kAhead], rstd_next[kAhead];
   float gw[NV * E::kN], gb[NV * E::kN], gw_t = 0.f, gb_t = 0.f;
@@ -370,7 +373,7 @@ __global__ __launch_bounds__(kThreads) void dora_layernorm_fwd_loop(
   }
 }
 
-// Backward of wide rows, where a row's sums and the weight gradient's do not fit
+// Backward of still wider rows, where a row's sums and the weight gradient's do not fit
 // one thread's registers: a workgroup per row forms the two means, and a second
 // kernel goes down columns.  Memory is read twice and written once.
 template <bool BF>
@@ -518,9 +521,13 @@ int check_shape(const dora_layernorm_shape* s) {
   return DORA_OK;
 }
 
-// Threads that hold a row of up to 8192 elements: whole waves, kElems elements a
-// thread.
-int row_threads(int64_t D) { return (int)((D + 64 * kElems - 1) / (64 * kElems)) * 64; }
+// Threads that hold a row of the backward: whole waves, kElems elements a thread, or
+// twice that for wide rows (bf16 only: float32 ones spill).
+bool bwd_wide(int64_t D) { return D > kMaxBwdThreads * kElems; }
+int row_threads(int64_t D) {
+  const int64_t per = 64 * kElems * (bwd_wide(D) ? 2 : 1);
+  return (int)((D + per - 1) / per) * 64;
+}
 // The forward's threads: powers of two, whose idle lanes are waves more in flight
 // (2048 x 6144 bf16: 13.1 us against 13.6).
 int fwd_threads(int64_t D) {
@@ -532,7 +539,9 @@ int fwd_threads(int64_t D) {
 // (in float32 that many, with their weights, spill); beyond, it loops over memory.
 int64_t fwd_most(bool bf) { return (bf ? 2 : 1) * 1024 * kElems; }
 // Rows that the backward holds in registers beside the weight gradient's sums.
-bool bwd_in_registers(int64_t D) { return D <= kMaxBwdThreads * kElems; }
+bool bwd_in_registers(const dora_layernorm_shape& s) {
+  return s.width <= kMaxBwdThreads * kElems * (s.dtype == DORA_BF16 ? 2 : 1);
+}
 
 // Row blocks of the backward, which is also how many partial sums the weight's
 // gradient has.  In registers: one workgroup per CU, or as few as take no more
@@ -541,8 +550,8 @@ constexpr int64_t kCus = 256;
 int64_t bwd_blocks(const dora_layernorm_shape& s) {
   if (s.rows < 1) return 0;
   const bool bf = s.dtype == DORA_BF16;
-  if (bwd_in_registers(s.width)) {
-    const int64_t at_once = bwd_rows(bf, row_threads(s.width));
+  if (bwd_in_registers(s)) {
+    const int64_t at_once = bwd_rows(bf, row_threads(s.width), bwd_wide(s.width));
     const int64_t groups = (s.rows + at_once - 1) / at_once;
     const int64_t rounds = (groups + kCus - 1) / kCus;
     return (groups + rounds - 1) / rounds;
@@ -558,7 +567,7 @@ size_t part_bytes(const dora_layernorm_shape& s) {
 }
 // The workspace: the weight gradient's partial sums, then the means of wide rows.
 size_t ws_bytes_for(const dora_layernorm_shape& s) {
-  return part_bytes(s) + (bwd_in_registers(s.width) ? 0 : (size_t)s.rows * sizeof(float2));
+  return part_bytes(s) + (bwd_in_registers(s) ? 0 : (size_t)s.rows * sizeof(float2));
 }
 
 // f(threads) with a row kernel's template argument.
@@ -620,18 +629,25 @@ hipError_t backward(const dora_layernorm_shape& s, const void* gy, const void* x
   const bool sums = gw || gb;
   const int64_t blocks = bwd_blocks(s);
   float* part = sums ? reinterpret_cast<float*>(ws) : nullptr;
-  if (s.rows > 0 && (gx || sums) && bwd_in_registers(s.width)) {
+  if (s.rows > 0 && (gx || sums) && bwd_in_registers(s)) {
     LaunchTimer t("layernorm_bwd", st);
+    auto launch = [&](auto kernel, int threads) {
+      hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(threads), 0, st, gy, s.ld_gy, x,
+                         s.ld_x, w, mean, rstd, gx, part, s.rows, (uint32_t)s.width);
+      return hipGetLastError();
+    };
+    auto pick = [&](auto threads, auto vectors) {
+      constexpr int T = threads(), V = vectors();
+      constexpr int block = bwd_rows(BF, T, V > NV) * T;
+      if (!gx) return launch(dora_layernorm_bwd<BF, T, V, true, false>, block);
+      return sums ? launch(dora_layernorm_bwd<BF, T, V, true, true>, block)
+                  : launch(dora_layernorm_bwd<BF, T, V, false, true>, block);
+    };
     const hipError_t e = with_any_threads(row_threads(s.width), [&](auto threads) {
-      const dim3 block(bwd_rows(BF, threads()) * threads());
-      auto launch = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), block, 0, st, gy, s.ld_gy, x, s.ld_x, w,
-                           mean, rstd, gx, part, s.rows, (uint32_t)s.width);
-        return hipGetLastError();
-      };
-      if (!gx) return launch(dora_layernorm_bwd<BF, threads(), NV, true, false>);
-      return sums ? launch(dora_layernorm_bwd<BF, threads(), NV, true, true>)
-                  : launch(dora_layernorm_bwd<BF, threads(), NV, false, true>);
+      using std::integral_constant;
+      if constexpr (BF && threads() >= 320)
+        if (bwd_wide(s.width)) return pick(threads, integral_constant<int, 2 * NV>());
+      return pick(threads, integral_constant<int, NV>());
     });
     if (e) return e;
   } else if (s.rows > 0 && (gx || sums)) {
@@ -709,7 +725,7 @@ DORA_API int dora_layernorm_backward(const dora_layernorm_shape* shape, const vo
   DORA_CHECK(check_elem(grad_weight, e, true));
   DORA_CHECK(check_elem(grad_bias, e, true));
   // rows held in registers need none for grad_x alone
-  if (grad_weight || grad_bias || (grad_x && !bwd_in_registers(s.width)))
+  if (grad_weight || grad_bias || (grad_x && !bwd_in_registers(s)))
     DORA_CHECK(check_ws(ws, ws_bytes, ws_bytes_for(s)));
   hipStream_t st = reinterpret_cast<hipStream_t>(hip_stream);
   HIP_TRY(s.dtype == DORA_BF16

@@ -247,3 +247,26 @@ def test_gradient_of_constant_rows_whose_mean_times_rstd_overflows(ops, width, d
     half = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -24
     assert ((gx.double() - want).abs() <= want.abs() * half + 2e-5 * rstd.double()[:, None]).all()
     assert ((gb.double() - g.sum(0)).abs() <= g.sum(0).abs() * half + 2e-6).all()
+
+
+@pytest.mark.parametrize("rows,width", [(3, 8200), (300, 9001), (7, 10240), (5, 10241), (261, 12289),
+                                        (2, 14336), (6, 14337), (300, 16383), (520, 16384), (4, 16385)])
+def test_wide_bf16_rows(ops, rows, width):
+    test_forward_and_backward(ops, rows, width, "bf16")
+
+
+@pytest.mark.parametrize("width", [40, 200, 1031, 2300, 5121, 7168, 8192, 9001, 16384, 20000])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_gradients_alone_have_the_bits_they_have_together(ops, width, dtype):
+    """Any subset of the three gradients, rows that do not fill a workgroup's last turn."""
+    for rows in (1, 5, 2049):
+        if rows * width > 1 << 25:
+            continue
+        say("layernorm", rows, width, dtype)
+        x, gy, w, _ = make(rows, width, DT[dtype], rows + width, False, True)
+        _, mean, rstd = ops.dora_layernorm(x, w, None)
+        full = ops.dora_layernorm_backward(gy, x, w, mean, rstd)
+        for need in (("x",), ("weight",), ("bias",), ("weight", "bias"), ("x", "bias")):
+            got = ops.dora_layernorm_backward(gy, x, w, mean, rstd, need=need)
+            for name, a, b in zip(("x", "weight", "bias"), got, full):
+                assert a is None if name not in need else torch.equal(a, b), (rows, need, name)
