@@ -7,8 +7,8 @@
 // All sums are float32 in an order that depends on sizes alone; results are
 // rounded once, to the tensors' type.  Memory bounds both directions where rows
 // are many: the forward reads and writes each element once (2048 x 6144 bf16: 10
-// us, 5.0 TB/s), the backward reads two and writes one (4096 x 8192 bf16: 42 us,
-// 5.2 TB/s with its partial sums, and 5 us to add those; 1031 x 5121 float32: 15
+// us, 5.0 TB/s), the backward reads two and writes one (4096 x 8192 bf16: 36 us,
+// 6.0 TB/s with its partial sums, and 5 us to add those; 1031 x 5121 float32: 15
 // and 4 us).  One row of 8192 is a launch's latency, 3 us.
 #include <algorithm>
 #include <cmath>
@@ -375,7 +375,8 @@ __global__ __launch_bounds__(kThreads) void dora_layernorm_fwd_loop(
 
 // Backward of still wider rows, where a row's sums and the weight gradient's do not fit
 // one thread's registers: a workgroup per row forms the two means, and a second
-// kernel goes down columns.  Memory is read twice and written once.
+// kernel goes down columns.  Memory is read twice and written once (1024 x 27648
+// bf16: 66 us, 4.3 TB/s).
 template <bool BF>
 __global__ __launch_bounds__(kThreads) void dora_layernorm_bwd_means(
     const void* gy_, int64_t ldg, const void* x_, int64_t ldx, const void* w_, const float* mean_in,
@@ -383,6 +384,7 @@ __global__ __launch_bounds__(kThreads) void dora_layernorm_bwd_means(
   using E = Elem<BF>;
   using T = typename E::T;
   __shared__ float lds[2][2 * kWaves];
+  constexpr int kU = 4, kStep = kThreads * E::kN;   // vectors in flight, and apart
   int buf = 0;
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, buf ^= 1) {
     const T* gy = reinterpret_cast<const T*>(gy_) + row * ldg;
@@ -390,20 +392,41 @@ __global__ __launch_bounds__(kThreads) void dora_layernorm_bwd_means(
     const T* w = reinterpret_cast<const T*>(w_);
     const float mean = mean_in[row], rstd = rstd_in[row];
     float s[2] = {0.f, 0.f};
-#pragma unroll 2
-    for (int64_t j = (int64_t)threadIdx.x * E::kN; j < D; j += kThreads * E::kN) {
-      float g[E::kN], v[E::kN], wv[E::kN];
-      load_part<BF>(gy, j, D, 0.f, g);
-      load_part<BF>(x, j, D, mean, v);
-#pragma unroll
-      for (int q = 0; q < E::kN; ++q) wv[q] = 1.f;
-      if (w) load_part<BF>(w, j, D, 0.f, wv);
+    auto add = [&](const float* g, const float* v, const float* wv) {
 #pragma unroll
       for (int q = 0; q < E::kN; ++q) {
         const float h = g[q] * wv[q];
         s[0] += h;
         s[1] = fmaf(h, (v[q] - mean) * rstd, s[1]);
       }
+    };
+    float wv[E::kN];
+#pragma unroll
+    for (int q = 0; q < E::kN; ++q) wv[q] = 1.f;
+    int64_t j = (int64_t)threadIdx.x * E::kN;
+    for (int64_t end = kU * kStep; end <= D; end += kU * kStep, j += kU * kStep) {
+      typename E::Vec g[kU], v[kU], wr[kU];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        if (w) wr[u] = E::raw(w + j + u * kStep);
+        g[u] = E::raw(gy + j + u * kStep);
+        v[u] = E::raw(x + j + u * kStep);
+      }
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        float gv[E::kN], xv[E::kN];
+        E::decode(g[u], gv);
+        E::decode(v[u], xv);
+        if (w) E::decode(wr[u], wv);
+        add(gv, xv, wv);
+      }
+    }
+    for (; j < D; j += kStep) {
+      float gv[E::kN], xv[E::kN];
+      load_part<BF>(gy, j, D, 0.f, gv);
+      load_part<BF>(x, j, D, mean, xv);
+      if (w) load_part<BF>(w, j, D, 0.f, wv);
+      add(gv, xv, wv);
     }
     block_sum<kWaves, 2>(s, lds[buf]);
     if (threadIdx.x == 0) means[row] = float2{s[0] / (float)D, s[1] / (float)D};
