@@ -218,43 +218,48 @@ PyObject* token_logprob_backward(PyObject*, PyObject* const* args, Py_ssize_t n)
   END_HANDLE_TH_ERRORS
 }
 
-// make_table(params, exp_avg, exp_avg_sq, exp_avg_scales, exp_avg_sq_scales, masters, table
-// address): fills the table of an AdamW step from lists of tensors (the last three lists may be
-// None; without scales the moments are float32, with them int8 and uint8).  Returns the
-// parameters' dtype code, or None unless all are contiguous, on one device, of their types and
-// sizes.
-PyObject* make_table(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  HANDLE_TH_ERRORS
-  if (n != 7 || !PyList_Check(args[0])) Py_RETURN_NONE;
-  const Py_ssize_t count = PyList_GET_SIZE(args[0]);
-  for (int i = 1; i < 6; ++i)
-    if (!(i > 2 && args[i] == Py_None) &&
-        !(PyList_Check(args[i]) && PyList_GET_SIZE(args[i]) == count))
-      Py_RETURN_NONE;
-  const bool small = args[3] != Py_None;
-  if (small != (args[4] != Py_None)) Py_RETURN_NONE;
-  auto* table = static_cast<dora_adamw_tensor*>(PyLong_AsVoidPtr(args[6]));
-  const at::Tensor* first = nullptr;
-  for (Py_ssize_t i = 0; i < count; ++i) {
+// The lists of an AdamW step: params, exp_avg, exp_avg_sq, exp_avg_scales, exp_avg_sq_scales,
+// masters (the last three may be None; without scales the moments are float32, with them int8 and
+// uint8).
+struct Lists {
+  PyObject* const* list;   // kCount of them
+  static constexpr int kCount = 6;
+  Py_ssize_t count = 0;
+  bool small = false;
+  const at::Tensor* first = nullptr;   // the first param
+
+  explicit Lists(PyObject* const* args) : list(args) {}
+  bool open() {
+    if (!PyList_Check(list[0])) return false;
+    count = PyList_GET_SIZE(list[0]);
+    for (int i = 1; i < kCount; ++i)
+      if (!(i > 2 && list[i] == Py_None) &&
+          !(PyList_Check(list[i]) && PyList_GET_SIZE(list[i]) == count))
+        return false;
+    small = list[3] != Py_None;
+    return small == (list[4] != Py_None);
+  }
+  // Tensor i as the table's entry (its gradient left out); false unless all are contiguous, on
+  // one device, of their types and sizes.
+  bool entry(Py_ssize_t i, dora_adamw_tensor& e) {
     bool ok = true;
-    const at::Tensor* t[6] = {};
-    for (int k = 0; k < 6; ++k)
-      if (args[k] != Py_None) t[k] = tensor(PyList_GET_ITEM(args[k], i), ok);
-    if (!ok || !t[0]) Py_RETURN_NONE;
+    const at::Tensor* t[kCount] = {};
+    for (int k = 0; k < kCount; ++k)
+      if (list[k] != Py_None) t[k] = tensor(PyList_GET_ITEM(list[k], i), ok);
+    if (!ok || !t[0]) return false;
     if (!first) first = t[0];
     const int64_t size = t[0]->numel(), blocks = (size + DORA_STATE_BLOCK - 1) / DORA_STATE_BLOCK;
-    if (!t[0]->is_cuda() || t[0]->scalar_type() != first->scalar_type()) Py_RETURN_NONE;
-    const at::ScalarType types[6] = {first->scalar_type(), small ? at::kChar : at::kFloat,
-                                     small ? at::kByte : at::kFloat, at::kFloat, at::kFloat,
-                                     at::kFloat};
-    for (int k = 0; k < 6; ++k) {
-      if (args[k] == Py_None) continue;
+    if (!t[0]->is_cuda() || t[0]->scalar_type() != first->scalar_type()) return false;
+    const at::ScalarType types[kCount] = {first->scalar_type(), small ? at::kChar : at::kFloat,
+                                          small ? at::kByte : at::kFloat, at::kFloat, at::kFloat,
+                                          at::kFloat};
+    for (int k = 0; k < kCount; ++k) {
+      if (list[k] == Py_None) continue;
       const int64_t need = k == 3 || k == 4 ? blocks : size;
       if (!t[k] || t[k]->scalar_type() != types[k] || t[k]->numel() != need ||
           !t[k]->is_contiguous() || t[k]->device() != first->device())
-        Py_RETURN_NONE;
+        return false;
     }
-    dora_adamw_tensor& e = table[i];
     auto at = [&](int k) { return t[k] ? t[k]->data_ptr() : nullptr; };
     e.param = at(0);
     e.exp_avg = at(1);
@@ -263,33 +268,62 @@ PyObject* make_table(PyObject*, PyObject* const* args, Py_ssize_t n) {
     e.exp_avg_sq_scale = static_cast<float*>(at(4));
     e.master = static_cast<float*>(at(5));
     e.n = size;
+    return true;
   }
-  const int code = first ? dtype_code(first->scalar_type()) : -1;
+  // Whether tensor i still is what the table's entry says.
+  bool same(Py_ssize_t i, const dora_adamw_tensor& e) {
+    dora_adamw_tensor now = {};
+    return entry(i, now) && now.param == e.param && now.exp_avg == e.exp_avg &&
+           now.exp_avg_sq == e.exp_avg_sq && now.exp_avg_scale == e.exp_avg_scale &&
+           now.exp_avg_sq_scale == e.exp_avg_sq_scale && now.master == e.master && now.n == e.n;
+  }
+};
+
+// make_table(the six lists, table address): fills the table.  Returns the parameters' dtype code,
+// or None where the lists are not what they should be.
+PyObject* make_table(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  Lists lists(args);
+  if (n != Lists::kCount + 1 || !lists.open()) Py_RETURN_NONE;
+  auto* table = static_cast<dora_adamw_tensor*>(PyLong_AsVoidPtr(args[6]));
+  for (Py_ssize_t i = 0; i < lists.count; ++i)
+    if (!lists.entry(i, table[i])) Py_RETURN_NONE;
+  const int code = lists.first ? dtype_code(lists.first->scalar_type()) : -1;
   if (code < 0 || (args[5] != Py_None && code != DORA_BF16)) Py_RETURN_NONE;
   return PyLong_FromLong(code);
   END_HANDLE_TH_ERRORS
 }
 
-// take_grads(params, grads, table address, device index): notes the gradients'
-// addresses in the table.  Returns their dtype code, or None unless every
-// parameter is where the table has it and every gradient is contiguous, of its
-// size, of one type and on the device.
+// same_table(the six lists, table address) -> whether every tensor is where the table has it.
+PyObject* same_table(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  Lists lists(args);
+  if (n != Lists::kCount + 1 || !lists.open()) Py_RETURN_FALSE;
+  const auto* table = static_cast<dora_adamw_tensor*>(PyLong_AsVoidPtr(args[6]));
+  for (Py_ssize_t i = 0; i < lists.count; ++i)
+    if (!lists.same(i, table[i])) Py_RETURN_FALSE;
+  Py_RETURN_TRUE;
+  END_HANDLE_TH_ERRORS
+}
+
+// take_grads(the six lists, table address, grads, device index): notes the gradients' addresses in
+// the table.  Returns their dtype code, or None unless every tensor is where the table has it and
+// every gradient is contiguous, of its size, of one type and on the device.
 PyObject* take_grads(PyObject*, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  if (n != 4 || !PyList_Check(args[0]) || !PyList_Check(args[1])) Py_RETURN_NONE;
-  const Py_ssize_t count = PyList_GET_SIZE(args[0]);
-  if (count < 1 || PyList_GET_SIZE(args[1]) != count) Py_RETURN_NONE;
-  auto* table = static_cast<dora_adamw_tensor*>(PyLong_AsVoidPtr(args[2]));
-  const long device = PyLong_AsLong(args[3]);
+  Lists lists(args);
+  if (n != Lists::kCount + 3 || !lists.open() || !PyList_Check(args[7])) Py_RETURN_NONE;
+  if (lists.count < 1 || PyList_GET_SIZE(args[7]) != lists.count) Py_RETURN_NONE;
+  auto* table = static_cast<dora_adamw_tensor*>(PyLong_AsVoidPtr(args[6]));
+  const long device = PyLong_AsLong(args[8]);
   int code = -1;
-  for (Py_ssize_t i = 0; i < count; ++i) {
+  for (Py_ssize_t i = 0; i < lists.count; ++i) {
     bool ok = true;
-    const at::Tensor* p = tensor(PyList_GET_ITEM(args[0], i), ok);
-    const at::Tensor* g = tensor(PyList_GET_ITEM(args[1], i), ok);
-    if (!p || !g || !g->is_cuda()) Py_RETURN_NONE;
+    const at::Tensor* g = tensor(PyList_GET_ITEM(args[7], i), ok);
+    if (!g || !g->is_cuda()) Py_RETURN_NONE;
     const int c = dtype_code(g->scalar_type());
     if (i == 0) code = c;
-    if (c < 0 || c != code || p->data_ptr() != table[i].param || g->numel() != table[i].n ||
+    if (c < 0 || c != code || !lists.same(i, table[i]) || g->numel() != table[i].n ||
         !g->is_contiguous() || g->get_device() != device)
       Py_RETURN_NONE;
     table[i].grad = g->const_data_ptr();
@@ -393,10 +427,10 @@ PyObject* init(PyObject*, PyObject* const* args, Py_ssize_t n) {
 #define FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FAST(layernorm),     FAST(layernorm_backward),
                          FAST(token_logprob), FAST(token_logprob_backward),
-                         FAST(make_table),    FAST(take_grads),
-                         FAST(grad_norm),     FAST(adamw_step),
-                         FAST(dequantize),    FAST(init),
-                         {nullptr, nullptr, 0, nullptr}};
+                         FAST(make_table),    FAST(same_table),
+                         FAST(take_grads),    FAST(grad_norm),
+                         FAST(adamw_step),    FAST(dequantize),
+                         FAST(init),          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_bind", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 

@@ -441,10 +441,12 @@ class AdamWPlan:
                    [ceil(n / 128)] each
     masters        float32 copies of bf16 parameters, or None
 
-    The plan refers to the tensors (they stay alive with it) and writes through them.  A parameter
-    whose storage was exchanged since (``p.data = ...``) is an error at the next step; moments,
-    scales and masters keep the storage they had when the plan was made.
+    The plan refers to the tensors (they stay alive with it) and writes through them.  A tensor
+    whose storage was exchanged since (``p.data = ...``, ``exp_avg.data = ...``) is an error at the
+    next step: the table has the old address.
     """
+
+    _STATE_FIELDS = ("exp_avg", "exp_avg_sq", "exp_avg_scale", "exp_avg_sq_scale", "master")
 
     def __init__(self, params, exp_avg, exp_avg_sq, *, masters=None, exp_avg_scales=None,
                  exp_avg_sq_scales=None):
@@ -458,17 +460,18 @@ class AdamWPlan:
         mst = None if masters is None else list(masters)
         self.table = (_lib.DoraAdamwTensor * n)()
         self._address = ctypes.addressof(self.table)
-        code = _compiled().make_table(params, exp_avg, exp_avg_sq, sc1, sc2, mst, self._address)
+        self._lists = (params, exp_avg, exp_avg_sq, sc1, sc2, mst)
+        code = _compiled().make_table(*self._lists, self._address)
         if code is None:
-            code = self._checked_table(params, exp_avg, exp_avg_sq, sc1, sc2, mst)
+            code = self._checked_table(self.table, *self._lists)
         self.param_code = code
         self.params, self.device, self.dtype = params, params[0].device, params[0].dtype
         self.state_bits = 8 if small else 32
         self.norm_bytes = None   # workspace of the gradients' norm, asked for once
-        self._keep = (exp_avg, exp_avg_sq, sc1, sc2, mst)
 
-    def _checked_table(self, params, exp_avg, exp_avg_sq, sc1, sc2, mst):
-        """Fills the table tensor by tensor and says what is wrong."""
+    @staticmethod
+    def _checked_table(table, params, exp_avg, exp_avg_sq, sc1, sc2, mst):
+        """Fills a table tensor by tensor and says what is wrong."""
         n, small = len(params), sc1 is not None
         if small != (sc2 is not None):
             raise ValueError("8-bit states need exp_avg_scales and exp_avg_sq_scales")
@@ -485,7 +488,7 @@ class AdamWPlan:
         code = _layer_dtype(params[0])
         if mst is not None and dt != torch.bfloat16:
             raise ValueError("masters go with bfloat16 params")
-        for i, (e, p) in enumerate(zip(self.table, params)):
+        for i, (e, p) in enumerate(zip(table, params)):
             k = _need(p, f"params[{i}]", dt, None, dev).numel()
             e.param, e.n = p.data_ptr(), k
             for nm, lst, tdt, per_block in lists:
@@ -498,16 +501,33 @@ class AdamWPlan:
                 setattr(e, nm, t.data_ptr())
         return code
 
+    def unchanged(self):
+        """Whether every tensor still has the storage it had when the plan was made."""
+        return (self.params[0].dtype == self.dtype
+                and _compiled().same_table(*self._lists, self._address))
+
+    def _check_storage(self):
+        """Says which tensor has another storage than the table's, or another type or size."""
+        if [p.data_ptr() for p in self.params] != [e.param or 0 for e in self.table]:
+            raise ValueError("a parameter's storage has changed since the plan was made")
+        for nm, lst in zip(self._STATE_FIELDS, self._lists[1:]):
+            for i, (t, e) in enumerate(zip(lst or (), self.table)):
+                if t.data_ptr() != (getattr(e, nm) or 0):
+                    raise ValueError(f"{nm}[{i}]'s storage has changed since the plan was made")
+        now = (_lib.DoraAdamwTensor * len(self.params))()
+        code = self._checked_table(now, *self._lists)
+        if code != self.param_code or [e.n for e in now] != [e.n for e in self.table]:
+            raise ValueError("a parameter's type or size has changed since the plan was made")
+
     def _take_grads(self, grads):
         """Checks the gradients and notes where they are; returns their dtype's code."""
         grads = grads if isinstance(grads, list) else list(grads)
-        code = _compiled().take_grads(self.params, grads, self._address, self.device.index)
-        if code is not None:
+        code = _compiled().take_grads(*self._lists, self._address, grads, self.device.index)
+        if code is not None and self.params[0].dtype == self.dtype:
             return code
         if len(grads) != len(self.params):
             raise ValueError(f"{len(grads)} gradients for {len(self.params)} params")
-        if [p.data_ptr() for p in self.params] != [e.param or 0 for e in self.table]:
-            raise ValueError("a parameter's storage has changed since the plan was made")
+        self._check_storage()
         gdt = grads[0].dtype if isinstance(grads[0], torch.Tensor) else None
         if gdt is not None and gdt not in _DT:
             raise ValueError(f"unsupported dtype {gdt}; use float32 or bfloat16")

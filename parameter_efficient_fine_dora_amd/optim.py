@@ -48,7 +48,8 @@ class AdamW(torch.optim.Optimizer):
         return s
 
     def _plan(self, slot, params):
-        """The plan of these parameters, made anew when one of their tensors is another."""
+        """The plan of these parameters, made anew when one of their tensors or its storage is
+        another."""
         states = [self._state_of(p) for p in params]
         small = self.state_bits == 8
         lists = dict(exp_avg=[s["exp_avg"] for s in states], exp_avg_sq=[s["exp_avg_sq"] for s in states])
@@ -61,8 +62,8 @@ class AdamW(torch.optim.Optimizer):
         if kept is not None:
             plan, were = kept
             if (len(plan.params) == len(params) and all(a is b for a, b in zip(plan.params, params))
-                    and [e.param for e in plan.table] == [p.data_ptr() or None for p in params]
-                    and all(a is b for k in lists for a, b in zip(lists[k], were[k]))):
+                    and all(a is b for k in lists for a, b in zip(lists[k], were[k]))
+                    and plan.unchanged()):
                 return plan
         plan = ops.AdamWPlan(params, lists["exp_avg"], lists["exp_avg_sq"], masters=lists.get("masters"),
                              exp_avg_scales=lists.get("exp_avg_scales"),

@@ -1,0 +1,91 @@
+"""Edges of the fine-tuning operators that their own test files leave out."""
+from __future__ import annotations
+
+import copy
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ops():
+    assert torch.cuda.is_available(), "GPU tests need a HIP device"
+    from parameter_efficient_fine_dora_amd import ops as _ops, _lib
+    _lib.lib()
+    return _ops
+
+
+def models(n, dtype, sizes=(1, 40, 700)):
+    torch.manual_seed(2)
+    first = torch.nn.ParameterList([torch.nn.Parameter(torch.randn(k, 3, device="cuda").to(dtype))
+                                    for k in sizes])
+    return [copy.deepcopy(first) for _ in range(n)]
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_states_moved_to_the_host_and_back(ops, bits):
+    """The usual way to free the GPU between steps: ``state.data = ...`` there and back.  The steps
+    after it are those of an optimizer that was left alone."""
+    from parameter_efficient_fine_dora_amd import optim
+    a, b = models(2, torch.bfloat16)
+    oa, ob = (optim.AdamW(m.parameters(), lr=1e-2, state_bits=bits, master=True) for m in (a, b))
+    for step in range(4):
+        for p, q in zip(a, b):
+            p.grad = torch.randn(p.shape, device="cuda").to(p.dtype)
+            q.grad = p.grad.clone()
+        if step >= 1:
+            for p in a:
+                for t in oa.state[p].values():
+                    if isinstance(t, torch.Tensor):
+                        t.data = t.data.cpu()
+            for p in a:
+                for t in oa.state[p].values():
+                    if isinstance(t, torch.Tensor):
+                        t.data = t.data.clone().cuda()
+        oa.step()
+        ob.step()
+    for p, q in zip(a, b):
+        assert torch.equal(p, q)
+        for k, v in oa.state[p].items():
+            assert v == ob.state[q][k] if k == "step" else torch.equal(v, ob.state[q][k]), k
+
+
+@pytest.mark.parametrize("name", ["exp_avg", "exp_avg_sq", "exp_avg_scale", "exp_avg_sq_scale", "master"])
+def test_a_plan_refuses_tensors_that_moved(ops, name):
+    p = torch.randn(300, device="cuda").bfloat16()
+    t = dict(exp_avg=torch.zeros(300, dtype=torch.int8, device="cuda"),
+             exp_avg_sq=torch.zeros(300, dtype=torch.uint8, device="cuda"),
+             exp_avg_scale=torch.zeros(3, device="cuda"), exp_avg_sq_scale=torch.zeros(3, device="cuda"),
+             master=p.float())
+    plan = ops.AdamWPlan([p], [t["exp_avg"]], [t["exp_avg_sq"]], masters=[t["master"]],
+                         exp_avg_scales=[t["exp_avg_scale"]], exp_avg_sq_scales=[t["exp_avg_sq_scale"]])
+    g = [torch.ones_like(p)]
+    ops.dora_adamw(plan, g, step=1, lr=1e-3)
+    assert plan.unchanged()
+    before = p.clone()
+    old = t[name].data                               # the old storage stays alive: addresses differ
+    t[name].data = old.clone()
+    assert not plan.unchanged()
+    with pytest.raises(ValueError, match=rf"{name}\[0\]'s storage has changed"):
+        ops.dora_adamw(plan, g, step=2, lr=1e-3)
+    with pytest.raises(ValueError, match="storage has changed"):
+        ops.dora_grad_norm(plan, g)
+    t[name].data = old[:2]                           # where it was, but shorter
+    with pytest.raises(ValueError, match="elements, expected"):
+        ops.dora_adamw(plan, g, step=2, lr=1e-3)
+    assert torch.equal(p, before)
+    t[name].data = old
+    ops.dora_adamw(plan, g, step=2, lr=1e-3)
+    assert not torch.equal(p, before)
+
+
+def test_a_plan_refuses_a_param_of_another_type(ops):
+    p, s = torch.zeros(64, device="cuda"), torch.zeros(32, device="cuda")
+    p.data = p.data[:32]
+    plan = ops.AdamWPlan([p], [s], [s.clone()])
+    p.data = p.data.view(torch.bfloat16)[:32]        # the same address and size
+    assert not plan.unchanged()
+    with pytest.raises(ValueError, match="type or size"):
+        ops.dora_adamw(plan, [s], step=1, lr=1e-3)

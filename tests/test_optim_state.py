@@ -1,0 +1,68 @@
+"""The optimizer's bookkeeping on the host: which plans it keeps, what its state follows.  The
+operators are replaced by a recorder, so no GPU is needed."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from parameter_efficient_fine_dora_amd import _lib, ops, optim
+
+
+class Plan:
+    """Notes the addresses of a step's tensors, as ops.AdamWPlan does."""
+    made = []
+
+    def __init__(self, params, exp_avg, exp_avg_sq, **more):
+        self.params = list(params)
+        self.lists = [self.params, list(exp_avg), list(exp_avg_sq)]
+        self.lists += [list(v) for v in more.values() if v is not None]
+        self.more = {k: v for k, v in more.items() if v is not None}
+        self.table = (_lib.DoraAdamwTensor * len(self.params))()
+        for e, p in zip(self.table, self.params):
+            e.param = p.data_ptr()
+        self.addresses = self.where()
+        Plan.made.append(self)
+
+    def where(self):
+        return [[t.data_ptr() for t in lst] for lst in self.lists]
+
+    def unchanged(self):
+        return self.addresses == self.where()
+
+
+@pytest.fixture(autouse=True)
+def recorder(monkeypatch):
+    """Steps as (plan, step, parameters) instead of launches."""
+    steps = []
+    Plan.made = []
+    monkeypatch.setattr(ops, "AdamWPlan", Plan)
+    monkeypatch.setattr(ops, "dora_adamw", lambda plan, grads, **kw: steps.append((plan, kw)))
+    monkeypatch.setattr(ops, "dora_grad_norm", lambda plan, grads, most: (torch.tensor(1.0),) * 2)
+    return steps
+
+
+def params(*sizes, dtype=torch.bfloat16):
+    out = [torch.nn.Parameter(torch.randn(n).to(dtype)) for n in sizes]
+    for p in out:
+        p.grad = torch.ones_like(p)
+    return out
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_state_whose_storage_was_exchanged_makes_the_plan_anew(recorder, bits):
+    """What moving states to the host and back does: the tensor objects stay, their memory does not."""
+    ps = params(300, 5)
+    opt = optim.AdamW(ps, state_bits=bits, master=True)
+    opt.step()
+    opt.step()
+    assert len(Plan.made) == 1                       # kept while nothing changes
+    made = 1
+    for name in [k for k in opt.state[ps[0]] if k != "step"]:
+        state = opt.state[ps[0]]
+        state[name].data = state[name].data.clone()
+        opt.step()
+        made += 1
+        assert len(Plan.made) == made, name
+        plan = recorder[-1][0]
+        assert any(state[name] is t for lst in plan.lists for t in lst)
+        assert plan.unchanged()
