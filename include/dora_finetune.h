@@ -161,7 +161,8 @@ typedef struct {
  *   m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2
  *   p = p (1 - lr weight_decay)
  *       - lr / (1 - beta1^step) m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
- * in float32 from the stored states; param and states are rounded once, the
+ * in float32 from the stored states; param and states are rounded once (so a
+ * decay below float32's spacing at 1 still counts beside an update), the
  * parameter from the moments before their rounding.  A NaN or infinite gradient
  * makes its own element NaN (with 8-bit states: the moments of its block).
  * Pointers and hyperparameters are kernel arguments: a captured graph replays

@@ -3,8 +3,11 @@ from __future__ import annotations
 
 import copy
 
+import numpy as np
 import pytest
 import torch
+
+from oracle import finetune as ref
 
 pytestmark = pytest.mark.gpu
 
@@ -89,3 +92,30 @@ def test_a_plan_refuses_a_param_of_another_type(ops):
     assert not plan.unchanged()
     with pytest.raises(ValueError, match="type or size"):
         ops.dora_adamw(plan, [s], step=1, lr=1e-3)
+
+
+@pytest.mark.parametrize("lr,decay", [(1e-4, 0.01), (1e-5, 0.01), (1e-6, 0.01), (1e-6, 0.0), (1e-2, 0.1)])
+def test_a_small_decay_is_not_rounded_away(ops, lr, decay):
+    """The end of a schedule: lr weight_decay near or below float32's spacing at 1.
+
+    The parameter is rounded once: half a last place (2^-24 |p|) beside the update's own error (24
+    roundings of it) and, from lr weight_decay = 2^-10 on, 2^-15 of the decay.  Updates are normal
+    with a deviation of seven last places or more, so their roundings go evenly to either side: the
+    mean over n parameters of the relative error then deviates by at most 2^-24 / sqrt(3 n), and five
+    of those hold a bias."""
+    n = 1 << 18
+    rng = np.random.default_rng(7)
+    p0 = (rng.uniform(0.5, 2.0, n) * rng.choice([-1, 1], n)).astype(np.float32)
+    m0 = rng.standard_normal(n).astype(np.float32)
+    p, m = torch.from_numpy(p0).cuda(), torch.from_numpy(m0).cuda()
+    ops.dora_adamw(ops.AdamWPlan([p], [m], [torch.ones_like(p)]), [torch.zeros_like(p)], step=1000,
+                   lr=lr, weight_decay=decay)
+    want, _, _ = ref.adamw(p0, np.zeros(n), m0, np.ones(n), step=1000, lr=lr, beta1=0.9, beta2=0.999,
+                           eps=1e-8, weight_decay=decay)
+    off = p.cpu().numpy().astype(np.float64) - want
+    coarse = 2.0 ** -15 * lr * decay if lr * decay >= 2.0 ** -10 else 0.0
+    bar = (2.0 ** -24 + coarse) * np.abs(want) + 2.0 ** -24 * lr * (24 * np.abs(m0)
+                                                                    + 2 * decay * np.abs(p0))
+    assert (np.abs(off) <= bar).all(), float((np.abs(off) - bar).max())
+    if not coarse:
+        assert abs((off / want).mean()) <= 5 * 2.0 ** -24 / np.sqrt(3 * n)
