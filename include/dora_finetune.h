@@ -164,7 +164,9 @@ typedef struct {
  * in float32 from the stored states; param and states are rounded once (so a
  * decay below float32's spacing at 1 still counts beside an update), the
  * parameter from the moments before their rounding.  A NaN or infinite gradient
- * makes its own element NaN (with 8-bit states: the moments of its block).
+ * makes its own element NaN (with 8-bit states: the moments of its block).  With
+ * eps = 0 an element whose second moment float32 cannot hold (under 2^-149) is
+ * infinite, or NaN where the first moment is 0 too.
  * Pointers and hyperparameters are kernel arguments: a captured graph replays
  * the values of the call that was captured.
  */

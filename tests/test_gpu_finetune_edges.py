@@ -119,3 +119,34 @@ def test_a_small_decay_is_not_rounded_away(ops, lr, decay):
     assert (np.abs(off) <= bar).all(), float((np.abs(off) - bar).max())
     if not coarse:
         assert abs((off / want).mean()) <= 5 * 2.0 ** -24 / np.sqrt(3 * n)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("step", [1, 3, 1000])
+@pytest.mark.parametrize("eps", [0.0, 1e-30, 1e-18, 1e-15, 1e-12, 1e-8])
+def test_tiny_gradients_with_a_small_eps(ops, eps, step, bits):
+    """Second moments down to 2^-126 and below, where a root that is lost would make the update
+    infinite.
+
+    Bars: an update is 24 roundings of it and half a last place of the parameter (2^-24 |p|), and its
+    root is off by what a denormal second moment is: the step to the stored v is 2^-149, and three of
+    them (products and sum) over 2 v relative.  8-bit states start from zero, so that nothing is read
+    from their codes."""
+    mag = np.repeat([1e-10, 1e-15, 1e-17, 3e-18, 1e-18, 1e-19, 1e-20], 64)
+    n = mag.size
+    rng = np.random.default_rng(3)
+    g = (mag * rng.uniform(0.5, 2.0, n) * rng.choice([-1, 1], n)).astype(np.float32)
+    p = torch.zeros(n, device="cuda")
+    if bits == 8:
+        m, v = torch.zeros(n, dtype=torch.int8, device="cuda"), torch.zeros(n, dtype=torch.uint8, device="cuda")
+        sc = [torch.zeros(-(-n // 128), device="cuda") for _ in range(2)]
+        plan = ops.AdamWPlan([p], [m], [v], exp_avg_scales=sc[:1], exp_avg_sq_scales=sc[1:])
+    else:
+        plan = ops.AdamWPlan([p], [torch.zeros_like(p)], [torch.zeros_like(p)])
+    ops.dora_adamw(plan, [torch.from_numpy(g).cuda()], step=step, lr=1e-2, eps=eps, weight_decay=0.0)
+    want, _, v = ref.adamw(np.zeros(n), g, np.zeros(n), np.zeros(n), step=step, lr=1e-2, beta1=0.9,
+                           beta2=0.999, eps=eps, weight_decay=0.0)
+    got = p.cpu().numpy().astype(np.float64)
+    bar = np.abs(want) * (25 * 2.0 ** -24 + 3 * 2.0 ** -149 / (2 * v))
+    bad = ~(np.abs(got - want) <= bar)
+    assert not bad.any(), (int(bad.sum()), got[bad][:4], want[bad][:4])
