@@ -23,7 +23,7 @@ LIB = os.path.join(HERE, "libdora.so")
 BIND = os.path.join(HERE, "_bind.so")   # csrc/bind.cpp
 SOURCES = ["api.hip", "gemm.hip", "gram.hip", "rowwise.hip", "small.hip", "probe.hip", "noalloc.hip",
            "layernorm.hip", "logprob.hip", "adamw.hip"]
-HEADERS = ["common.h", "kernels.h", "entry.h", "elem.h", "checks.h"]
+HEADERS = ["common.h", "kernels.h", "entry.h", "elem.h", "checks.h", "launch_cut.h"]
 ARCH = "gfx950"
 
 

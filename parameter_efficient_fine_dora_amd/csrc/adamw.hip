@@ -17,6 +17,7 @@
 #include "checks.h"
 #include "elem.h"
 #include "kernels.h"
+#include "launch_cut.h"
 
 namespace dora {
 namespace {
@@ -409,7 +410,6 @@ __global__ __launch_bounds__(kThreads) void dora_state_codes(const float* values
 // ---- host -----------------------------------------------------------------------
 constexpr int64_t kMaxElems = int64_t(1) << 34;
 
-int64_t chunks(int64_t n) { return (n + kChunk - 1) / kChunk; }
 int64_t norm_chunks(int64_t n) { return (n + kNormChunk - 1) / kNormChunk; }
 bool dtype_ok(int dt) { return dt == DORA_F32 || dt == DORA_BF16; }
 size_t esize(int dt) { return dt == DORA_BF16 ? 2 : 4; }
@@ -422,48 +422,41 @@ int check_tensors(const dora_adamw_tensor* t, int64_t count) {
   return DORA_OK;
 }
 
-// HIP holds the threads of a launch below 2^32: a call's tensors are cut into
-// runs of at most this many workgroups.
-constexpr int64_t kMaxGrid = int64_t(1) << 23;
-
 template <bool PBF, bool GBF, bool MASTER, bool S8>
 hipError_t run_step(const dora_adamw_tensor* tensors, int64_t count, const StepNumbers& h,
                     hipStream_t st) {
   using Args = StepArgs<MASTER, S8>;
+  constexpr int threads = kChunk / (S8 ? 8 : 4);
   Args a;
   a.h = h;
-  int k = 0;
-  int64_t blocks = 0;
-  auto flush = [&]() -> hipError_t {
-    if (k == 0) return hipSuccess;
-    a.h.count = k;
-    LaunchTimer timer("adamw", st);
-    hipLaunchKernelGGL((dora_adamw_kernel<PBF, GBF, MASTER, S8>),
-                       dim3((unsigned)blocks), dim3(kChunk / (S8 ? 8 : 4)), 0, st, a);
-    k = 0;
-    blocks = 0;
-    return hipGetLastError();
+  // the byte that element `at` of an array of so many bytes an element starts at
+  auto from = [](auto* p, int64_t at, int bytes) {
+    using P = decltype(p);
+    return reinterpret_cast<P>((uintptr_t)p + (uintptr_t)at * bytes);
   };
-  for (int64_t i = 0; i < count; ++i) {
-    const dora_adamw_tensor& t = tensors[i];
-    const int64_t c = chunks(t.n);
-    if (c == 0) continue;
-    if (k == Args::kMax || blocks + c > kMaxGrid)
-      if (hipError_t e = flush()) return e;
-    a.n[k] = t.n;
-    a.param[k] = t.param;
-    a.grad[k] = t.grad;
-    a.exp_avg[k] = t.exp_avg;
-    a.exp_avg_sq[k] = t.exp_avg_sq;
-    if (S8) {
-      a.exp_avg_scale[k] = t.exp_avg_scale;
-      a.exp_avg_sq_scale[k] = t.exp_avg_sq_scale;
-    }
-    if (MASTER) a.master[k] = t.master;
-    a.first[k++] = (uint32_t)blocks;
-    blocks += c;
-  }
-  return flush();
+  return cut_launches<hipError_t>(
+      count, kChunk, Args::kMax, launch_blocks(threads), [&](int64_t i) { return tensors[i].n; },
+      [&](int k, int64_t i, int64_t at, int64_t n, int64_t block) {
+        const dora_adamw_tensor& t = tensors[i];
+        a.n[k] = n;
+        a.param[k] = from(t.param, at, PBF ? 2 : 4);
+        a.grad[k] = from(t.grad, at, GBF ? 2 : 4);
+        a.exp_avg[k] = from(t.exp_avg, at, S8 ? 1 : 4);
+        a.exp_avg_sq[k] = from(t.exp_avg_sq, at, S8 ? 1 : 4);
+        if (S8) {   // pieces start at 8-bit blocks
+          a.exp_avg_scale[k] = t.exp_avg_scale + at / DORA_STATE_BLOCK;
+          a.exp_avg_sq_scale[k] = t.exp_avg_sq_scale + at / DORA_STATE_BLOCK;
+        }
+        if (MASTER) a.master[k] = t.master + at;
+        a.first[k] = (uint32_t)block;
+      },
+      [&](int pieces, int64_t blocks) {
+        a.h.count = pieces;
+        LaunchTimer timer("adamw", st);
+        hipLaunchKernelGGL((dora_adamw_kernel<PBF, GBF, MASTER, S8>), dim3((unsigned)blocks),
+                           dim3(threads), 0, st, a);
+        return hipGetLastError();
+      });
 }
 
 // The step for the types of a call: a float32 parameter is its own master.
@@ -485,7 +478,8 @@ bool options_ok(const dora_adamw_options& o) {
          o.beta1 < 1 && o.beta2 >= 0 && o.beta2 < 1 && o.step >= 1;
 }
 
-static_assert(kMaxElems / kChunk <= kMaxGrid, "one tensor fits one launch");
+static_assert(kMaxElems / (kThreads * kVec) <= launch_blocks(kThreads),
+              "the conversions' elements fit one launch");
 
 }  // namespace
 }  // namespace dora
@@ -560,33 +554,28 @@ DORA_API int dora_grad_norm(const dora_adamw_tensor* tensors, int64_t count, int
   DORA_CHECK(check_ws(ws, ws_bytes, dora_grad_norm_workspace_bytes(tensors, count)));
   hipStream_t st = reinterpret_cast<hipStream_t>(hip_stream);
   double* part = reinterpret_cast<double*>(ws);
-  int64_t done = 0, blocks = 0;
+  int64_t done = 0;
   NormArgs a;
-  a.count = 0;
-  auto flush = [&]() -> hipError_t {
-    if (a.count == 0) return hipSuccess;
-    LaunchTimer timer("grad_norm", st);
-    if (grad_dtype == DORA_BF16)
-      hipLaunchKernelGGL((dora_grad_norm_parts<true>), dim3((unsigned)blocks), dim3(kThreads), 0,
-                         st, a, part + done);
-    else
-      hipLaunchKernelGGL((dora_grad_norm_parts<false>), dim3((unsigned)blocks), dim3(kThreads), 0,
-                         st, a, part + done);
-    done += blocks;
-    blocks = 0;
-    a.count = 0;
-    return hipGetLastError();
-  };
-  for (int64_t i = 0; i < count; ++i) {
-    const int64_t c = norm_chunks(tensors[i].n);
-    if (c == 0) continue;
-    if (a.count == kMaxGrads || blocks + c > kMaxGrid) HIP_TRY(flush());
-    a.g[a.count] = tensors[i].grad;
-    a.n[a.count] = tensors[i].n;
-    a.first[a.count++] = (uint32_t)blocks;
-    blocks += c;
-  }
-  HIP_TRY(flush());
+  HIP_TRY(cut_launches<hipError_t>(
+      count, kNormChunk, kMaxGrads, launch_blocks(kThreads),
+      [&](int64_t i) { return tensors[i].n; },
+      [&](int k, int64_t i, int64_t at, int64_t n, int64_t block) {
+        a.g[k] = reinterpret_cast<const uint8_t*>(tensors[i].grad) + at * esize(grad_dtype);
+        a.n[k] = n;
+        a.first[k] = (uint32_t)block;
+      },
+      [&](int pieces, int64_t blocks) {
+        a.count = pieces;
+        LaunchTimer timer("grad_norm", st);
+        if (grad_dtype == DORA_BF16)
+          hipLaunchKernelGGL((dora_grad_norm_parts<true>), dim3((unsigned)blocks), dim3(kThreads), 0,
+                             st, a, part + done);
+        else
+          hipLaunchKernelGGL((dora_grad_norm_parts<false>), dim3((unsigned)blocks), dim3(kThreads), 0,
+                             st, a, part + done);
+        done += blocks;
+        return hipGetLastError();
+      }));
   LaunchTimer timer("grad_norm_finish", st);
   hipLaunchKernelGGL(dora_grad_norm_finish, dim3(1), dim3(1024), 0, st, part, done, max_norm, norm,
                      scale);

@@ -150,3 +150,32 @@ def test_tiny_gradients_with_a_small_eps(ops, eps, step, bits):
     bar = np.abs(want) * (25 * 2.0 ** -24 + 3 * 2.0 ** -149 / (2 * v))
     bad = ~(np.abs(got - want) <= bar)
     assert not bad.any(), (int(bad.sum()), got[bad][:4], want[bad][:4])
+
+
+def test_a_step_of_the_most_elements_a_tensor_may_have(ops):
+    """2^34 - 1 elements: more workgroups than one launch takes."""
+    n = (1 << 34) - 1
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < n * 12 + (4 << 30):
+        pytest.skip("needs 210 GB of free device memory")
+    p, g = (torch.zeros(n, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    m, v = (torch.zeros(n, device="cuda") for _ in range(2))
+    cuts = [slice(0, 4096), slice((1 << 33) - 5000, (1 << 33) + 5000), slice(n - 5000, n)]
+    small = []
+    for c in cuts:
+        k = c.stop - c.start
+        p[c], g[c] = torch.randn(k, device="cuda"), torch.randn(k, device="cuda")
+        m[c], v[c] = torch.randn(k, device="cuda"), torch.rand(k, device="cuda")
+        small.append([t[c].clone() for t in (p, g, m, v)])
+    plan = ops.AdamWPlan([p], [m], [v])
+    ops.dora_adamw(plan, [g], step=3, lr=1e-2)
+    ops.dora_adamw(ops.AdamWPlan([s[0] for s in small], [s[2] for s in small], [s[3] for s in small]),
+                   [s[1] for s in small], step=3, lr=1e-2)
+    for c, s in zip(cuts, small):
+        for t, want in zip((p, m, v), (s[0], s[2], s[3])):
+            assert torch.equal(t[c], want)
+    norm, _ = ops.dora_grad_norm(plan, [g])
+    want = sum(float(s[1].double().square().sum()) for s in small) ** 0.5
+    assert abs(float(norm) - want) <= 2 * 2.0 ** -24 * want
+    del p, g, m, v, plan
+    torch.cuda.empty_cache()
