@@ -195,11 +195,13 @@ def token_logprob(logits: torch.Tensor, targets: torch.Tensor, *, scale: float =
     """Log probability of each target under softmax(scale * logits) and the entropy of that
     distribution, differentiable in the logits; with ``top`` > 0 also the likeliest tokens.
 
-    logits [..., vocab], targets int64 [...].  Returns (logp, entropy, top_logp, top_index), the
-    first two float32 [...], the others [..., top] or None.  Targets outside [0, vocab) (-100, say)
-    give zeros and no gradient.
+    logits [..., vocab], targets int64 [...] of the same leading shape.  Returns (logp, entropy,
+    top_logp, top_index), the first two float32 [...], the others [..., top] or None.  Targets
+    outside [0, vocab) (-100, say) give zeros and no gradient.
     """
     lead = targets.shape
+    if logits.dim() < 1 or logits.shape[:-1] != lead:
+        raise ValueError(f"targets have shape {tuple(lead)}, expected {tuple(logits.shape[:-1])}")
     z = _as_rows(logits)
     logp, entropy, top_logp, top_index = TokenLogProbFunction.apply(z, targets.reshape(-1).contiguous(),
                                                                     float(scale), int(top))
