@@ -30,6 +30,14 @@ class AdamW(torch.optim.Optimizer):
         self.grad_norm = None
         self._plans = {}
 
+    def __getstate__(self):   # copies and pickles: torch's own parts, and the options
+        return {**super().__getstate__(), "state_bits": self.state_bits, "master": self.master,
+                "max_norm": self.max_norm}
+
+    def __setstate__(self, state):
+        super().__setstate__(state)
+        self.grad_norm, self._plans = None, {}
+
     def _state_of(self, p):
         s = self.state[p]
         if not s:

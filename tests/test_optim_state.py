@@ -2,6 +2,9 @@
 operators are replaced by a recorder, so no GPU is needed."""
 from __future__ import annotations
 
+import copy
+import pickle
+
 import pytest
 import torch
 
@@ -66,3 +69,22 @@ def test_a_state_whose_storage_was_exchanged_makes_the_plan_anew(recorder, bits)
         plan = recorder[-1][0]
         assert any(state[name] is t for lst in plan.lists for t in lst)
         assert plan.unchanged()
+
+
+@pytest.mark.parametrize("how", ["deepcopy", "pickle"])
+def test_a_copy_steps_as_the_original(recorder, how):
+    """torch keeps an optimizer's defaults, state and groups alone; the options have to come along."""
+    ps = params(300, 5)
+    opt = optim.AdamW(ps, state_bits=8, master=True, max_norm=0.5)
+    opt.step()
+    twin = copy.deepcopy(opt) if how == "deepcopy" else pickle.loads(pickle.dumps(opt))
+    assert (twin.state_bits, twin.master, twin.max_norm) == (8, True, 0.5)
+    mine = twin.param_groups[0]["params"]
+    assert all(a is not b and torch.equal(a, b) for a, b in zip(mine, ps))
+    for p in mine:
+        p.grad = torch.ones_like(p)
+    twin.step()
+    plan, kw = recorder[-1]
+    assert all(a is b for a, b in zip(plan.params, mine)) and kw["step"] == 2
+    assert set(plan.more) == {"masters", "exp_avg_scales", "exp_avg_sq_scales"}
+    assert opt.state[ps[0]]["step"] == 1
