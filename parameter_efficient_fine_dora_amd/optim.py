@@ -114,13 +114,30 @@ class AdamW(torch.optim.Optimizer):
         self._plans = {k: v for k, v in self._plans.items() if k in used}
         return loss
 
+    @staticmethod
+    def _check_loadable(state_dict):
+        """Refuses a checkpoint of an update that this one is not."""
+        for group in state_dict["param_groups"]:
+            for k in ("amsgrad", "maximize"):
+                if group.get(k):
+                    raise ValueError(f"a checkpoint with {k} is not supported")
+            if not group.get("decoupled_weight_decay", True) and group.get("weight_decay"):
+                raise ValueError("a checkpoint without decoupled weight decay is not supported")
+
     def load_state_dict(self, state_dict):
+        """Loads a checkpoint of this class, or of torch's AdamW (without amsgrad and maximize)."""
+        self._check_loadable(state_dict)
         super().load_state_dict(state_dict)
         # torch casts floating state to the parameter's dtype; moments, codes and scales keep theirs
+        # (all floating state here is float32), and step counts are numbers here
         ids = [i for g in state_dict["param_groups"] for i in g["params"]]
         mine = [p for g in self.param_groups for p in g["params"]]
         for i, p in zip(ids, mine):
             for k, v in state_dict["state"].get(i, {}).items():
-                self.state[p][k] = (v.detach().clone(memory_format=torch.contiguous_format).to(p.device)
-                                    if isinstance(v, torch.Tensor) else v)
+                if k == "step":
+                    v = int(v)
+                elif isinstance(v, torch.Tensor):
+                    v = v.detach().clone(memory_format=torch.contiguous_format).to(
+                        p.device, torch.float32 if v.is_floating_point() else None)
+                self.state[p][k] = v
         self._plans = {}

@@ -88,3 +88,42 @@ def test_a_copy_steps_as_the_original(recorder, how):
     assert all(a is b for a, b in zip(plan.params, mine)) and kw["step"] == 2
     assert set(plan.more) == {"masters", "exp_avg_scales", "exp_avg_sq_scales"}
     assert opt.state[ps[0]]["step"] == 1
+
+
+def checkpoint(ps, cls=torch.optim.AdamW, **kw):
+    twins = [torch.nn.Parameter(p.detach().clone()) for p in ps]
+    for p in twins:
+        p.grad = torch.ones_like(p)
+    opt = cls(twins, lr=1e-3, **kw)
+    for _ in range(3):
+        opt.step()
+    return opt.state_dict()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_torchs_checkpoint_keeps_one_call_for_a_group(recorder, dtype):
+    """Its step counts are tensors, one per parameter, and its moments have the parameters' type."""
+    ps = params(300, 5, dtype=dtype)
+    opt = optim.AdamW(ps)
+    saved = checkpoint(ps)
+    opt.load_state_dict(saved)
+    for p, s in zip(ps, saved["state"].values()):
+        mine = opt.state[p]
+        assert type(mine["step"]) is int and mine["step"] == 3
+        for k in ("exp_avg", "exp_avg_sq"):
+            assert mine[k].dtype == torch.float32 and torch.equal(mine[k], s[k].float())
+    opt.step()
+    assert len(recorder) == 1 and recorder[0][1]["step"] == 4 and len(recorder[0][0].params) == 2
+
+
+@pytest.mark.parametrize("cls,kw,word", [
+    (torch.optim.AdamW, dict(amsgrad=True), "amsgrad"), (torch.optim.AdamW, dict(maximize=True), "maximize"),
+    (torch.optim.Adam, dict(weight_decay=0.1), "decoupled")])
+def test_a_checkpoint_of_another_update_is_refused(cls, kw, word):
+    ps = params(30)
+    opt = optim.AdamW(ps, lr=0.5)
+    with pytest.raises(ValueError, match=word):
+        opt.load_state_dict(checkpoint(ps, cls, **kw))
+    assert not opt.state and opt.param_groups[0]["lr"] == 0.5
+    opt.load_state_dict(checkpoint(ps, torch.optim.Adam))       # without decay it is the same update
+    assert opt.state[ps[0]]["step"] == 3
