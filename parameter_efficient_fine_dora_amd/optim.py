@@ -114,15 +114,26 @@ class AdamW(torch.optim.Optimizer):
         self._plans = {k: v for k, v in self._plans.items() if k in used}
         return loss
 
-    @staticmethod
-    def _check_loadable(state_dict):
-        """Refuses a checkpoint of an update that this one is not."""
+    def _check_loadable(self, state_dict):
+        """Refuses a checkpoint of an update that this one is not, and moments that it cannot use."""
         for group in state_dict["param_groups"]:
             for k in ("amsgrad", "maximize"):
                 if group.get(k):
                     raise ValueError(f"a checkpoint with {k} is not supported")
             if not group.get("decoupled_weight_decay", True) and group.get("weight_decay"):
                 raise ValueError("a checkpoint without decoupled weight decay is not supported")
+        need = ["step", "exp_avg", "exp_avg_sq"]
+        if self.state_bits == 8:
+            need += ["exp_avg_scale", "exp_avg_sq_scale"]
+        for i, s in state_dict["state"].items():
+            if s and isinstance(s.get("exp_avg"), torch.Tensor):
+                bits = 32 if s["exp_avg"].is_floating_point() else 8
+                if bits != self.state_bits:
+                    raise ValueError(f"the checkpoint has moments of {bits} bits, this optimizer "
+                                     f"state_bits={self.state_bits}")
+            lacks = [k for k in need if k not in s] if s else []
+            if lacks:
+                raise ValueError(f"the checkpoint's state of parameter {i} lacks {', '.join(lacks)}")
 
     def load_state_dict(self, state_dict):
         """Loads a checkpoint of this class, or of torch's AdamW (without amsgrad and maximize)."""

@@ -127,3 +127,28 @@ def test_a_checkpoint_of_another_update_is_refused(cls, kw, word):
     assert not opt.state and opt.param_groups[0]["lr"] == 0.5
     opt.load_state_dict(checkpoint(ps, torch.optim.Adam))       # without decay it is the same update
     assert opt.state[ps[0]]["step"] == 3
+
+
+@pytest.mark.parametrize("saved,bits", [(32, 8), (8, 32)])
+def test_moments_of_the_other_width_are_refused_by_name(recorder, saved, bits):
+    ps = params(300, 5)
+    other = optim.AdamW(ps, state_bits=saved)
+    other.step()
+    opt = optim.AdamW(ps, state_bits=bits, lr=0.5)
+    with pytest.raises(ValueError, match=f"moments of {saved} bits.*state_bits={bits}"):
+        opt.load_state_dict(other.state_dict())
+    assert not opt.state and opt.param_groups[0]["lr"] == 0.5
+    opt.step()
+
+
+def test_moments_that_are_incomplete_are_refused(recorder):
+    ps = params(300, 5)
+    opt = optim.AdamW(ps, state_bits=8)
+    opt.step()
+    saved = copy.deepcopy(opt.state_dict())
+    del saved["state"][1]["exp_avg_sq_scale"]
+    with pytest.raises(ValueError, match="exp_avg_sq_scale"):
+        optim.AdamW(ps, state_bits=8).load_state_dict(saved)
+    with pytest.raises(ValueError, match="exp_avg"):
+        optim.AdamW(ps).load_state_dict(torch.optim.SGD(ps, lr=0.1, momentum=0.9).state_dict()
+                                        | dict(state={0: dict(momentum_buffer=torch.ones(300))}))
