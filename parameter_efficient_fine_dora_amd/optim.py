@@ -12,7 +12,8 @@ class AdamW(torch.optim.Optimizer):
 
     state_bits  32: float32 moments; 8: 8-bit codes with a scale per 128 elements (about 2 bytes a
                 parameter for both moments instead of 8)
-    master      keep a float32 copy of every bf16 parameter and update that
+    master      keep a float32 copy of every bf16 parameter and update that; made from the parameter
+                where a loaded state has none, and dropped from one where it is not wanted
     max_norm    clip the gradients of all groups together by their global norm; ``step`` then leaves
                 the norm in ``grad_norm`` (a float32 scalar on the device).  Needs parameters of one
                 dtype.
@@ -51,9 +52,15 @@ class AdamW(torch.optim.Optimizer):
                 s["exp_avg_sq_scale"] = torch.zeros(blocks, dtype=torch.float32, device=p.device)
             else:
                 s["exp_avg"], s["exp_avg_sq"] = zero, torch.zeros_like(zero)
-            if self.master and p.dtype == torch.bfloat16:
+        if self._has_master(p):
+            if "master" not in s:
                 s["master"] = p.detach().float().contiguous()
+        else:
+            s.pop("master", None)
         return s
+
+    def _has_master(self, p):
+        return self.master and p.dtype == torch.bfloat16
 
     def _plan(self, slot, params):
         """The plan of these parameters, made anew when one of their tensors or its storage is
@@ -64,7 +71,7 @@ class AdamW(torch.optim.Optimizer):
         if small:
             lists["exp_avg_scales"] = [s["exp_avg_scale"] for s in states]
             lists["exp_avg_sq_scales"] = [s["exp_avg_sq_scale"] for s in states]
-        if "master" in states[0]:
+        if self._has_master(params[0]):
             lists["masters"] = [s["master"] for s in states]
         kept = self._plans.get(slot)
         if kept is not None:

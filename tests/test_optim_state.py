@@ -152,3 +152,47 @@ def test_moments_that_are_incomplete_are_refused(recorder):
     with pytest.raises(ValueError, match="exp_avg"):
         optim.AdamW(ps).load_state_dict(torch.optim.SGD(ps, lr=0.1, momentum=0.9).state_dict()
                                         | dict(state={0: dict(momentum_buffer=torch.ones(300))}))
+
+
+def test_masters_follow_the_option_and_not_the_checkpoint(recorder):
+    """Made from the parameters where the checkpoint has none, left out where they are not wanted."""
+    for saved, wanted in ((False, True), (True, False), (True, True)):
+        ps = params(300, 5)
+        other = optim.AdamW(ps, master=saved)
+        other.step()
+        opt = optim.AdamW(ps, master=wanted)
+        opt.load_state_dict(other.state_dict())
+        opt.step()
+        plan = recorder[-1][0]
+        assert ("masters" in plan.more) == wanted
+        assert all(("master" in opt.state[p]) == wanted for p in ps)
+        if wanted:
+            for p, w in zip(ps, plan.more["masters"]):
+                assert w.dtype == torch.float32 and torch.equal(w, p.detach().float())
+
+
+def test_a_parameter_without_a_master_among_others_that_have_one(recorder):
+    """One joins after a checkpoint was loaded; the plan of the norm takes both."""
+    ps = params(300, 5)
+    saved = optim.AdamW(ps)
+    saved.step()
+    state = copy.deepcopy(saved.state_dict())
+    del state["state"][0]
+    opt = optim.AdamW(ps, master=True, max_norm=1.0)
+    opt.load_state_dict(state)
+    opt.step()
+    assert all(len(p.more["masters"]) == len(p.params) for p in Plan.made if "masters" in p.more)
+    assert [set(opt.state[p]) for p in ps] == [{"step", "exp_avg", "exp_avg_sq", "master"}] * 2
+
+
+def test_a_master_goes_with_its_parameters_type(recorder):
+    p, = params(300)
+    opt = optim.AdamW([p], master=True)
+    opt.step()
+    for dtype in (torch.float32, torch.bfloat16):
+        p.grad = None
+        p.data = torch.randn(300).to(dtype)
+        p.grad = torch.ones_like(p)
+        opt.step()
+        assert ("masters" in recorder[-1][0].more) == (dtype == torch.bfloat16)
+    assert torch.equal(opt.state[p]["master"], p.detach().float())
