@@ -34,6 +34,9 @@ typedef struct {
     uint32_t reserved;  /* must be 0                                                */
 } dora_layernorm_shape;
 
+/* The widest rows whose grad_x alone dora_layernorm_backward forms without a workspace. */
+#define DORA_LAYERNORM_NO_WS_WIDTH(dtype) ((dtype) == DORA_BF16 ? 16384 : 8192)
+
 /* Bytes of workspace dora_layernorm_backward needs (0: invalid shape or nothing to reduce). */
 DORA_API size_t dora_layernorm_workspace_bytes(const dora_layernorm_shape* shape);
 
@@ -57,7 +60,7 @@ DORA_API int dora_layernorm_forward(const dora_layernorm_shape* shape, const voi
  *   grad_x [rows, width] contiguous, grad_weight, grad_bias [width], layer
  *   dtype; each may be NULL to skip it.
  *   ws  workspace of dora_layernorm_workspace_bytes(shape); may be NULL for
- *       grad_x alone where width <= 8192
+ *       grad_x alone where width <= DORA_LAYERNORM_NO_WS_WIDTH(dtype)
  */
 DORA_API int dora_layernorm_backward(const dora_layernorm_shape* shape, const void* grad_y,
                                      const void* x, const void* weight, const float* mean,

@@ -18,6 +18,7 @@ ERR_CODE = {v: k for k, v in ERR.items()}
 NOALLOC_SCRATCH_BYTES = 64 << 20   # DORA_NOALLOC_SCRATCH_BYTES
 LOGPROB_MAX_TOP = 64               # DORA_LOGPROB_MAX_TOP
 STATE_BLOCK = 128                  # DORA_STATE_BLOCK
+LAYERNORM_NO_WS_WIDTH = {F32: 8192, BF16: 16384}   # DORA_LAYERNORM_NO_WS_WIDTH
 
 
 class DoraShape(ctypes.Structure):

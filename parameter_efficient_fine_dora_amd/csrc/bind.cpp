@@ -141,7 +141,8 @@ PyObject* layernorm_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (args[5] == Py_True) gx = at::empty({s.rows, s.width}, x->options());
   if (args[6] == Py_True) gw = at::empty({s.width}, x->options());
   if (args[7] == Py_True) gb = at::empty({s.width}, x->options());
-  const size_t need = g_api.layernorm_workspace_bytes(&s);
+  const bool alone = !gw.defined() && !gb.defined() && s.width <= DORA_LAYERNORM_NO_WS_WIDTH(s.dtype);
+  const size_t need = alone ? 0 : g_api.layernorm_workspace_bytes(&s);
   if (need) ws = at::empty({(int64_t)need}, x->options().dtype(at::kByte));
   auto out = [](const at::Tensor& o) { return o.defined() ? o.mutable_data_ptr() : nullptr; };
   if (g_api.layernorm_backward(&s, gy->const_data_ptr(), x->const_data_ptr(), ptr(w), floats(mean),

@@ -565,6 +565,9 @@ int64_t fwd_most(bool bf) { return (bf ? 2 : 1) * 1024 * kElems; }
 bool bwd_in_registers(const dora_layernorm_shape& s) {
   return s.width <= kMaxBwdThreads * kElems * (s.dtype == DORA_BF16 ? 2 : 1);
 }
+static_assert(DORA_LAYERNORM_NO_WS_WIDTH(DORA_F32) == kMaxBwdThreads * kElems &&
+                  DORA_LAYERNORM_NO_WS_WIDTH(DORA_BF16) == 2 * kMaxBwdThreads * kElems,
+              "rows held in registers need no workspace for grad_x alone");
 
 // Row blocks of the backward, which is also how many partial sums the weight's
 // gradient has.  In registers: one workgroup per CU, or as few as take no more

@@ -359,7 +359,7 @@ def dora_layernorm_backward(grad_y, x, weight, mean, rstd, *, need=("x", "weight
         grad_bias = _out(grad_bias, "grad_bias", dt, (D,), dev)
     sh = _lib.DoraLayernormShape(R, D, ld, ldg, code, 0.0, 0, 0)
     nb = 0
-    if grad_weight is not None or grad_bias is not None or D > 8192:
+    if grad_weight is not None or grad_bias is not None or D > _lib.LAYERNORM_NO_WS_WIDTH[code]:
         nb = _lib.lib().dora_layernorm_workspace_bytes(ctypes.byref(sh))
         if workspace is None:
             workspace = torch.empty(max(nb, 1), dtype=torch.uint8, device=dev)

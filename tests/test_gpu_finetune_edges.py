@@ -179,3 +179,20 @@ def test_a_step_of_the_most_elements_a_tensor_may_have(ops):
     assert abs(float(norm) - want) <= 2 * 2.0 ** -24 * want
     del p, g, m, v, plan
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype,width", [("bf16", 8192), ("bf16", 16384), ("f32", 8192), ("f32", 100)])
+@pytest.mark.parametrize("compiled", [True, False])
+def test_grad_x_alone_allocates_nothing_else(ops, dtype, width, compiled):
+    """Frozen norms: no workspace where the header says that none is needed."""
+    x = torch.randn(1024, width, device="cuda").to({"bf16": torch.bfloat16, "f32": torch.float32}[dtype])
+    gy, w = torch.randn_like(x), torch.ones(width, device="cuda", dtype=x.dtype)
+    _, mean, rstd = ops.dora_layernorm(x, w)
+    out = None if compiled else torch.empty_like(x)     # an output given: the checked way
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    gx, gw, gb = ops.dora_layernorm_backward(gy, x, w, mean, rstd, need=("x",), grad_x=out)
+    peak = torch.cuda.max_memory_allocated() - before
+    assert gw is None and gb is None
+    assert peak == (x.numel() * x.element_size() if compiled else 0), peak
