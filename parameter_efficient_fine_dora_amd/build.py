@@ -58,7 +58,10 @@ def bind_command(out: str) -> list[str]:
 
 
 def _run(cmd: list[str]) -> tuple[int, str]:
-    p = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+    try:
+        p = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+    except OSError as e:   # a compiler that is not there fails its own command only
+        return 127, str(e)
     out = "\n".join(l for l in p.stdout.splitlines()
                     if "packed-fp32-ops' is not a recognized feature" not in l)
     return p.returncode, out
@@ -72,25 +75,40 @@ def build(verbose: bool = False, jobs: int | None = None) -> str:
         obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
         objs.append(obj)
         cmds.append([cc, *compile_flags(), "-c", os.path.join(CSRC, src), "-o", obj])
-    cmds.append(bind_command(BIND + ".tmp"))
+    binding = _bind_command()
+    cmds += [binding] if binding else []
     jobs = jobs or min(len(cmds), max(1, (os.cpu_count() or 2) // 2))
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
         results = list(ex.map(_run, cmds))
-    for cmd, (rc, out) in zip(cmds, results):
+
+    def check(cmd, rc, out):
         if verbose or rc:
             print(" ".join(cmd), file=sys.stderr)
             if out.strip():
                 print(out, file=sys.stderr)
         if rc:
             raise RuntimeError(f"{os.path.basename(cmd[0])} failed ({rc}): {' '.join(cmd)}")
+
+    for cmd, (rc, out) in zip(cmds[:len(objs)], results):
+        check(cmd, rc, out)
     tmp = LIB + ".tmp"
     rc, out = _run([cc, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp])
     if rc:
         print(out, file=sys.stderr)
         raise RuntimeError("link of libdora.so failed")
-    os.replace(tmp, LIB)
-    os.replace(BIND + ".tmp", BIND)
+    os.replace(tmp, LIB)   # whatever becomes of the Python binding
+    if binding:
+        check(binding, *results[-1])
+        os.replace(BIND + ".tmp", BIND)
     return LIB
+
+
+def _bind_command() -> list[str] | None:
+    try:
+        return bind_command(BIND + ".tmp")
+    except ImportError as e:
+        print(f"_bind.so is not built: {e} (libdora.so does not need it)", file=sys.stderr)
+        return None
 
 
 if __name__ == "__main__":
