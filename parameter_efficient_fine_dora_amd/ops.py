@@ -306,6 +306,12 @@ def _rows(t, name, dtype=None, shape=None, dev=None):
     return t.stride(0)
 
 
+def _given_ws(workspace, dev):
+    """Bytes of a workspace that the caller gave: contiguous, on the tensors' device."""
+    _need(workspace, "workspace", None, None, dev)
+    return workspace.numel() * workspace.element_size()
+
+
 def dora_layernorm(x, weight=None, bias=None, *, eps=1e-5, y=None, mean=None, rstd=None):
     """Layer norm over the rows of x [rows, width] (rows contiguous, any row stride).
 
@@ -363,7 +369,7 @@ def dora_layernorm_backward(grad_y, x, weight, mean, rstd, *, need=("x", "weight
         nb = _lib.lib().dora_layernorm_workspace_bytes(ctypes.byref(sh))
         if workspace is None:
             workspace = torch.empty(max(nb, 1), dtype=torch.uint8, device=dev)
-        nb = workspace.numel() * workspace.element_size()
+        nb = _given_ws(workspace, dev)
     _check(_lib.lib().dora_layernorm_backward(ctypes.byref(sh), _ptr(grad_y), _ptr(x), _ptr(weight),
                                               _ptr(mean), _ptr(rstd), _ptr(grad_x),
                                               _ptr(grad_weight), _ptr(grad_bias), _ptr(workspace),
@@ -398,7 +404,7 @@ def dora_token_logprob(logits, targets, *, scale=1.0, top=0, workspace=None):
     if nb and workspace is None:
         workspace = torch.empty(nb, dtype=torch.uint8, device=dev)
     if workspace is not None:
-        nb = workspace.numel() * workspace.element_size()
+        nb = _given_ws(workspace, dev)
     _check(_lib.lib().dora_token_logprob_forward(ctypes.byref(sh), _ptr(logits), _ptr(targets),
                                                  _ptr(logp), _ptr(entropy), _ptr(lse),
                                                  _ptr(top_logp), _ptr(top_index), _ptr(workspace),
@@ -558,7 +564,7 @@ def _grad_norm(plan, code, max_norm, workspace):
     norm = torch.empty((), dtype=torch.float32, device=plan.device)
     factor = torch.empty((), dtype=torch.float32, device=plan.device)
     _check(L.dora_grad_norm(plan.table, n, code, float(max_norm), _ptr(norm), _ptr(factor),
-                            _ptr(workspace), workspace.numel() * workspace.element_size(),
+                            _ptr(workspace), _given_ws(workspace, plan.device),
                             _stream(plan.device)), "dora_grad_norm")
     return norm, factor
 

@@ -196,3 +196,27 @@ def test_grad_x_alone_allocates_nothing_else(ops, dtype, width, compiled):
     peak = torch.cuda.max_memory_allocated() - before
     assert gw is None and gb is None
     assert peak == (x.numel() * x.element_size() if compiled else 0), peak
+
+
+@pytest.mark.parametrize("ws,match", [("host", "workspace must be a device"),
+                                      ("expanded", "workspace must be contiguous"),
+                                      ("strided", "workspace must be contiguous")])
+def test_workspaces_the_kernels_cannot_write_are_refused(ops, ws, match):
+    """One in host memory, and ones whose elements are not as many bytes of memory."""
+    size = 1 << 20
+    w = {"host": lambda: torch.empty(size, dtype=torch.uint8),
+         "expanded": lambda: torch.empty(1, dtype=torch.uint8, device="cuda").expand(size),
+         "strided": lambda: torch.empty(2 * size, dtype=torch.uint8, device="cuda")[::2]}[ws]()
+    x = torch.randn(4, 32, device="cuda")
+    _, mean, rstd = ops.dora_layernorm(x)
+    with pytest.raises(ValueError, match=match):
+        ops.dora_layernorm_backward(x, x, None, mean, rstd, workspace=w)
+    z, y = torch.randn(1, 100000, device="cuda"), torch.zeros(1, dtype=torch.int64, device="cuda")
+    with pytest.raises(ValueError, match=match):
+        ops.dora_token_logprob(z, y, workspace=w)
+    p, s = torch.zeros(64, device="cuda"), torch.zeros(64, device="cuda")
+    plan = ops.AdamWPlan([p], [s], [s.clone()])
+    with pytest.raises(ValueError, match=match):
+        ops.dora_grad_norm(plan, [s], workspace=w)
+    with pytest.raises(ValueError, match=match):
+        ops.dora_adamw(plan, [s], step=1, lr=1e-3, max_norm=1.0, workspace=w)
