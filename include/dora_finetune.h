@@ -110,7 +110,8 @@ DORA_API int dora_token_logprob_forward(const dora_logprob_shape* shape, const v
  *   grad_logp, grad_entropy  float32 [rows], each may be NULL (taken as 0)
  *   lse, entropy             as written by the forward (entropy may be NULL
  *                            when grad_entropy is)
- *   grad_logits              [rows, vocab] contiguous, layer dtype
+ *   grad_logits              [rows, vocab] contiguous, layer dtype; must not
+ *                            overlap logits (a row may be read again)
  * Rows without a target and rows with nothing left get zeros.  shape->top is
  * not used.
  */

@@ -306,6 +306,19 @@ def _rows(t, name, dtype=None, shape=None, dev=None):
     return t.stride(0)
 
 
+def _apart(out, name, rows, of):
+    """Refuses a contiguous output that shares memory with an input of rows."""
+    if not out.numel():
+        return
+    size, (R, D) = rows.element_size(), rows.shape
+    lo = out.data_ptr() - rows.data_ptr()
+    hi = lo + out.numel() * out.element_size()
+    step = rows.stride(0) * size if R > 1 else D * size
+    first = max(0, (lo - D * size) // step + 1)     # the first row that ends past the output's start
+    if first < R and first * step < hi:
+        raise ValueError(f"{name} must not overlap {of}")
+
+
 def _given_ws(workspace, dev):
     """Bytes of a workspace that the caller gave: contiguous, on the tensors' device."""
     _need(workspace, "workspace", None, None, dev)
@@ -430,6 +443,7 @@ def dora_token_logprob_backward(grad_logp, grad_entropy, logits, targets, lse, e
             _need(t, nm, torch.float32, (T,), dev)
     _need(lse, "lse", torch.float32, (T,), dev)
     grad_logits = _out(grad_logits, "grad_logits", logits.dtype, (T, V), dev)
+    _apart(grad_logits, "grad_logits", logits, "logits")
     sh = _lib.DoraLogprobShape(T, V, ld, _layer_dtype(logits), 0, float(scale), 0)
     _check(_lib.lib().dora_token_logprob_backward(ctypes.byref(sh), _ptr(grad_logp),
                                                   _ptr(grad_entropy), _ptr(logits), _ptr(targets),

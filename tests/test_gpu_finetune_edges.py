@@ -220,3 +220,30 @@ def test_workspaces_the_kernels_cannot_write_are_refused(ops, ws, match):
         ops.dora_grad_norm(plan, [s], workspace=w)
     with pytest.raises(ValueError, match=match):
         ops.dora_adamw(plan, [s], step=1, lr=1e-3, max_norm=1.0, workspace=w)
+
+
+def test_a_logits_gradient_over_the_logits_is_refused(ops):
+    """Rows of a large normaliser are read again while other workgroups write their gradient."""
+    buf = torch.randn(40, 128, device="cuda")
+    y = torch.zeros(4, dtype=torch.int64, device="cuda")
+    for z, g in ((buf[:4], buf[:4]), (buf[:4], buf[3:7]), (buf[1:5], buf[:4]),
+                 (buf[:8:2], buf[1:5]), (buf[:4, :64], buf.view(-1)[60:60 + 256].view(4, 64)),
+                 (buf[:4, :64], buf.view(-1)[64:64 + 256].view(4, 64))):
+        lse = torch.zeros(4, device="cuda")
+        with pytest.raises(ValueError, match="must not overlap"):
+            ops.dora_token_logprob_backward(lse, None, z, y, lse, None, grad_logits=g)
+    small = torch.randn(4, 128, device="cuda")
+    _, _, lse, _, _ = ops.dora_token_logprob(small, y)
+    want = ops.dora_token_logprob_backward(lse, None, small, y, lse, None)
+    for z, g in ((buf[:4], buf[4:8]), (buf[4:8], buf[:4])):      # beside each other
+        z.copy_(small)
+        assert torch.equal(ops.dora_token_logprob_backward(lse, None, z, y, lse, None, grad_logits=g), want)
+    z = buf[0:40:10, :16]                                        # between two rows
+    z.copy_(small[:, :16])
+    g = buf.view(-1)[128:128 + 64].view(4, 16)
+    _, _, lse, _, _ = ops.dora_token_logprob(z, y)
+    want = ops.dora_token_logprob_backward(lse, None, z, y, lse, None)
+    assert torch.equal(ops.dora_token_logprob_backward(lse, None, z, y, lse, None, grad_logits=g), want)
+    empty = torch.empty(0, 8, device="cuda")
+    none = torch.empty(0, device="cuda")
+    ops.dora_token_logprob_backward(none, None, empty, y[:0], none, None, grad_logits=empty)
