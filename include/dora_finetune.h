@@ -160,7 +160,7 @@ typedef struct {
 
 /*
  * AdamW on `count` tensors (`tensors` is a host array of device pointers, read
- * during the call only):
+ * during the call only; no two of the arrays that are written may overlap):
  *   g = grad_scale grad
  *   m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2
  *   p = p (1 - lr weight_decay)

@@ -10,7 +10,10 @@
 
 #include <ATen/ATen.h>
 
+#include <algorithm>
 #include <cstring>
+#include <utility>
+#include <vector>
 
 #include "../../include/dora_finetune.h"
 
@@ -280,6 +283,30 @@ struct Lists {
   }
 };
 
+// Whether any two of the arrays that a step on these tensors writes share memory.
+bool overlapping(const dora_adamw_tensor* table, Py_ssize_t count, int param_bytes, bool small) {
+  std::vector<std::pair<const char*, const char*>> written;
+  written.reserve((size_t)count * 6);
+  for (Py_ssize_t i = 0; i < count; ++i) {
+    const dora_adamw_tensor& e = table[i];
+    const int64_t blocks = (e.n + DORA_STATE_BLOCK - 1) / DORA_STATE_BLOCK;
+    auto add = [&](const void* p, int64_t bytes) {
+      const char* at = static_cast<const char*>(p);
+      if (at && bytes > 0) written.emplace_back(at, at + bytes);
+    };
+    add(e.param, e.n * param_bytes);
+    add(e.exp_avg, e.n * (small ? 1 : 4));
+    add(e.exp_avg_sq, e.n * (small ? 1 : 4));
+    add(e.exp_avg_scale, blocks * 4);
+    add(e.exp_avg_sq_scale, blocks * 4);
+    add(e.master, e.n * 4);
+  }
+  std::sort(written.begin(), written.end());
+  for (size_t i = 1; i < written.size(); ++i)
+    if (written[i].first < written[i - 1].second) return true;
+  return false;
+}
+
 // make_table(the six lists, table address): fills the table.  Returns the parameters' dtype code,
 // or None where the lists are not what they should be.
 PyObject* make_table(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -291,6 +318,7 @@ PyObject* make_table(PyObject*, PyObject* const* args, Py_ssize_t n) {
     if (!lists.entry(i, table[i])) Py_RETURN_NONE;
   const int code = lists.first ? dtype_code(lists.first->scalar_type()) : -1;
   if (code < 0 || (args[5] != Py_None && code != DORA_BF16)) Py_RETURN_NONE;
+  if (overlapping(table, lists.count, code == DORA_BF16 ? 2 : 4, lists.small)) Py_RETURN_NONE;
   return PyLong_FromLong(code);
   END_HANDLE_TH_ERRORS
 }

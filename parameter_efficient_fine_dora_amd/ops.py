@@ -519,6 +519,12 @@ class AdamWPlan:
                 if t.numel() != size:
                     raise ValueError(f"{nm}[{i}] has {t.numel()} elements, expected {size}")
                 setattr(e, nm, t.data_ptr())
+        written = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), f"{nm}[{i}]")
+                         for nm, lst in [("params", params)] + [x[:2] for x in lists] if lst is not None
+                         for i, t in enumerate(lst) if t.numel())
+        for a, b in zip(written, written[1:]):
+            if b[0] < a[1]:
+                raise ValueError(f"{a[2]} and {b[2]} share memory: a step writes both")
         return code
 
     def unchanged(self):

@@ -247,3 +247,27 @@ def test_a_logits_gradient_over_the_logits_is_refused(ops):
     empty = torch.empty(0, 8, device="cuda")
     none = torch.empty(0, device="cuda")
     ops.dora_token_logprob_backward(none, None, empty, y[:0], none, None, grad_logits=empty)
+
+
+def test_tensors_of_a_plan_that_share_memory_are_refused(ops):
+    """A step's workgroups would write the same elements, in any order."""
+    buf = torch.zeros(1000, device="cuda")
+    a, b = buf[:100], buf[100:200]
+    m = [torch.zeros(100, device="cuda") for _ in range(4)]
+    ops.AdamWPlan([a, b], m[:2], m[2:])                                  # side by side
+    for bad, match in ((([a, a], m[:2], m[2:]), "params"), (([a, buf[99:199]], m[:2], m[2:]), "params"),
+                       (([a, b], [m[0]] * 2, m[2:]), "exp_avg"), (([a, b], m[:2], [m[2], m[1]]), "exp_avg"),
+                       (([a], [m[0]], [m[0]]), "exp_avg_sq")):
+        with pytest.raises(ValueError, match=match + ".*share memory|share memory.*" + match):
+            ops.AdamWPlan(*bad)
+    p = [torch.zeros(100, device="cuda").bfloat16() for _ in range(2)]
+    with pytest.raises(ValueError, match="master.*share memory"):
+        ops.AdamWPlan(p, m[:2], m[2:], masters=[buf[:100], buf[50:150]])
+    ops.AdamWPlan(p, m[:2], m[2:], masters=[a, b])
+    c, d = (torch.zeros(100, dtype=t, device="cuda") for t in (torch.int8, torch.uint8))
+    s = torch.zeros(2, device="cuda")
+    with pytest.raises(ValueError, match="scale.*share memory"):
+        ops.AdamWPlan([a], [c], [d], exp_avg_scales=[s[:1]], exp_avg_sq_scales=[s[:1]])
+    ops.AdamWPlan([a], [c], [d], exp_avg_scales=[s[:1]], exp_avg_sq_scales=[s[1:]])
+    none = torch.zeros(0, device="cuda")
+    ops.AdamWPlan([none, none], [none, none], [none, none])
