@@ -274,12 +274,26 @@ struct Lists {
     e.n = size;
     return true;
   }
-  // Whether tensor i still is what the table's entry says.
+  // Whether tensor i still is what the table's entry says (the same address is the same device).
   bool same(Py_ssize_t i, const dora_adamw_tensor& e) {
-    dora_adamw_tensor now = {};
-    return entry(i, now) && now.param == e.param && now.exp_avg == e.exp_avg &&
-           now.exp_avg_sq == e.exp_avg_sq && now.exp_avg_scale == e.exp_avg_scale &&
-           now.exp_avg_sq_scale == e.exp_avg_sq_scale && now.master == e.master && now.n == e.n;
+    const void* at[kCount] = {e.param,         e.exp_avg,          e.exp_avg_sq,
+                              e.exp_avg_scale, e.exp_avg_sq_scale, e.master};
+    const int64_t blocks = (e.n + DORA_STATE_BLOCK - 1) / DORA_STATE_BLOCK;
+    for (int k = 0; k < kCount; ++k) {
+      if (list[k] == Py_None) continue;
+      PyObject* o = PyList_GET_ITEM(list[k], i);
+      if (!THPVariable_Check(o)) return false;
+      const at::Tensor& t = THPVariable_Unpack(o);
+      if (!first) first = &t;
+      const at::ScalarType type = k == 0              ? first->scalar_type()
+                                  : small && k == 1 ? at::kChar
+                                  : small && k == 2 ? at::kByte
+                                                    : at::kFloat;
+      if (t.const_data_ptr() != at[k] || t.numel() != (k == 3 || k == 4 ? blocks : e.n) ||
+          t.scalar_type() != type || !t.is_contiguous())
+        return false;
+    }
+    return true;
   }
 };
 
