@@ -75,7 +75,7 @@ typedef struct {
     int64_t  ld;        /* row stride of the logits in elements, vocab <= ld < 2^31  */
     int32_t  dtype;     /* dora_dtype of logits and grad_logits                      */
     int32_t  top;       /* alternatives per row, 0 <= top <= min(vocab, 64)          */
-    float    scale;     /* multiplies the logits (1 / temperature); finite and > 0   */
+    float    scale;     /* multiplies the logits (1 / temperature), 0 < scale < 2^127 */
     uint32_t reserved;  /* must be 0                                                 */
 } dora_logprob_shape;
 

@@ -738,7 +738,8 @@ bool dtype_ok(const dora_logprob_shape& s) { return s.dtype == DORA_F32 || s.dty
 
 int check_shape(const dora_logprob_shape* s) {
   if (!s) return DORA_ERR_NULL;
-  if (s->reserved != 0 || !std::isfinite(s->scale) || s->scale <= 0.f) return DORA_ERR_FLAGS;
+  // (the kernels work with scale log2(e), which passes float32's range from 1.4 2^127 on)
+  if (s->reserved != 0 || !(s->scale > 0.f && s->scale < 0x1p127f)) return DORA_ERR_FLAGS;
   if (!dtype_ok(*s)) return DORA_ERR_DTYPE;
   if (!shape_ok(*s)) return DORA_ERR_SHAPE;
   return DORA_OK;

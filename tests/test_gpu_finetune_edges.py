@@ -271,3 +271,21 @@ def test_tensors_of_a_plan_that_share_memory_are_refused(ops):
     ops.AdamWPlan([a], [c], [d], exp_avg_scales=[s[:1]], exp_avg_sq_scales=[s[1:]])
     none = torch.zeros(0, device="cuda")
     ops.AdamWPlan([none, none], [none, none], [none, none])
+
+
+@pytest.mark.parametrize("scale", [1.7e38, 1e30, 1e-30, 1e-45])
+def test_extreme_scales(ops, scale):
+    """Greedy and flat limits: a row's likeliest tokens share it evenly, or all tokens do.  A few
+    float32 roundings of numbers of order one; a subnormal scale's own spacing for its gradient."""
+    z = torch.tensor([[0.0, 1.0, 1.0, -3.0], [0.0, 0.0, 0.0, float("-inf")]], device="cuda")
+    y = torch.tensor([1, 0], device="cuda")
+    logp, H, lse, best, index = ops.dora_token_logprob(z, y, scale=scale, top=2)
+    n = torch.tensor([2.0 if scale > 1 else 4.0, 3.0], device="cuda")
+    assert torch.allclose(logp, -n.log(), rtol=1e-6) and torch.allclose(H, n.log(), rtol=1e-6)
+    assert index.tolist() == [[1, 2], [0, 1]] and torch.allclose(best, -n.log()[:, None], rtol=1e-6)
+    g = ops.dora_token_logprob_backward(torch.ones_like(logp), None, z, y, lse, None, scale=scale)
+    live = (z == 1) | (z == 0) & (n[:, None] == 3) if scale > 1 else z > -4
+    want = torch.where(live, -1.0 / n[:, None], 0.0).double()
+    want[[0, 1], y] += 1.0
+    unit = float(torch.tensor(scale, dtype=torch.float32))
+    assert ((g.double() - want * unit).abs() <= 1e-6 * unit + 2.0 ** -149).all()
