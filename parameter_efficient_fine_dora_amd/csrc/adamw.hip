@@ -5,9 +5,9 @@
 // in float32, from the moments before their rounding; the parameter is rounded
 // once (its master copy, if it has one, is float32).  Memory bounds all of it: a
 // step moves 22 bytes an element for bf16 with float32 moments (28 with a master)
-// and 10 with 8-bit moments.  151M bf16 with 8-bit moments: 254 us (6.0 TB/s), their
-// values as bf16 79 us each (5.7 TB/s); 29M bf16 with masters: 140 us (5.9 TB/s),
-// their norm 16 us and 5 us to add its parts.
+// and 10 with 8-bit moments.  151M bf16 with 8-bit moments: 239 us (6.4 TB/s), their
+// values as bf16 75 us each (6.1 TB/s); 29M bf16 with masters: 140 us (5.9 TB/s),
+// their norm 15 us and 5 us to add its parts.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -189,8 +189,9 @@ __device__ __forceinline__ float block_scale(const float* v) {
 // the conversion that puts a float into a byte (v_cvt_pk_u8_f32, which clamps to
 // 0 .. 255; signed codes go through c + 128).  Reciprocal and root are the
 // hardware's, 1 ulp each: far below the half step that rounding to a code costs.
-// (Correctly rounded ones here and in the step give the same codes but for 4 in a
-// million, and a step of 151M elements with its moments' values 514 us against 393.)
+// (With correctly rounded ones, here and in the step, as many codes differ from
+// those of a plain float32 form, 3 or 4 in a million, and 151M elements with their
+// moments' values take 514 us against 393.)
 // Scales outside their range are divided by.  A block whose scale is not finite
 // keeps that scale and codes of 0: its values read back as NaN.
 template <bool SIGNED>

@@ -6,10 +6,11 @@
 //   grad_weight = sum over rows of grad_y xhat, grad_bias = sum of grad_y
 // All sums are float32 in an order that depends on sizes alone; results are
 // rounded once, to the tensors' type.  Memory bounds both directions where rows
-// are many: the forward reads and writes each element once (2048 x 6144 bf16: 10
-// us, 5.0 TB/s), the backward reads two and writes one (4096 x 8192 bf16: 36 us,
-// 6.0 TB/s with its partial sums, and 5 us to add those; 1031 x 5121 float32: 15
-// and 4 us).  One row of 8192 is a launch's latency, 3 us.
+// are many: the forward reads and writes each element once (2048 x 6144 bf16: 10.7
+// us a pass, 4.7 TB/s), the backward reads two and writes one (4096 x 8192 bf16: 35
+// us, 6.2 TB/s with its partial sums, and 5 us to add those; 1031 x 5121 float32:
+// 15 and 4 us; grad_x alone, with neither: 34 and 12 us a pass).  One row of 8192 is
+// a launch's latency, 3 us.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -161,8 +162,9 @@ constexpr int bwd_rows(bool bf, int threads, bool wide) {
   return wide ? 1 : (bf && threads > 128 ? 12 : 8) * 64 / threads;
 }
 // Rows fetched ahead: two where one row's waves leave registers for it (4096 x 8192
-// bf16: 45 us against 47 with one or three; float32 loses, 1031 x 5121 21 us
-// against 20).
+// bf16: 53.5 us against 54.7 with one where the GPU is waited for after every pass,
+// 43.9 against 43.3 among others; three take longer, and float32 loses with two,
+// 1031 x 5121 21 us against 20).
 constexpr int bwd_ahead(bool bf, int threads, bool wide) {
   return bf && !wide && threads > 384 ? 2 : 1;
 }
@@ -552,7 +554,7 @@ int row_threads(int64_t D) {
   return (int)((D + per - 1) / per) * 64;
 }
 // The forward's threads: powers of two, whose idle lanes are waves more in flight
-// (2048 x 6144 bf16: 13.1 us against 13.6).
+// (2048 x 6144 bf16: 10.7 us a pass against 11.3).
 int fwd_threads(int64_t D) {
   int t = 64;
   while ((int64_t)t * kElems < D) t *= 2;

@@ -3,10 +3,12 @@
 // d_j = scale (z_j - m), s = sum exp(d_j) and u = sum d_j exp(d_j):
 //   logp = d_y - log s,  entropy H = log s - u / s,  lse = scale m + log s
 //   grad z_j = scale (a ([j = y] - p_j) - b p_j (log p_j + H)), p_j = exp(d_j) / s
-// for gradients a of logp and b of entropy.  Statistics are float32.  Memory
-// bounds long calls: the forward reads the logits once (4096 x 131072 bf16, an
-// eighth of the rows skipped: 145 us, 6.5 TB/s), the gradient reads and writes
-// them once (318 us, 6.3 TB/s).  Few rows are bound by latency: one of 131072
+// for gradients a of logp and b of entropy.  Statistics are float32, with the
+// hardware's exponential (1 ulp) of a difference times the rounded scale log2(e): over
+// 4096 rows of 131072 the results are 1.2e-7 off float64's, those of a plain float32
+// form 6e-8.  Memory bounds long calls: the forward reads the logits once (4096 x 131072 bf16, an eighth of the rows
+// skipped: 146 us, 6.4 TB/s), the gradient reads and writes them once (317 us, 6.3
+// TB/s).  Few rows are bound by latency: one of 131072
 // bf16 with its top 20 takes 7 us and 4 us for the join.
 #include <algorithm>
 #include <cmath>
@@ -371,7 +373,7 @@ __device__ bool select_held(const typename Elem<BF>::Vec* raw, float most,
 // of one batch, which are still in registers when their statistics are known (one
 // kernel for both would keep one workgroup less per SIMD: 141 us against 119 at
 // 2048 x 131072 bf16, top 20).  PAST: the logits do not fit the last-level cache
-// and are loaded past it (3584 x 131072 bf16: 159 us against 177, 5.9 TB/s).
+// and are loaded past it (3584 x 131072 bf16: 147 us a pass against 172, 6.4 TB/s).
 constexpr int kGroups = 1, kHeld = 2;
 template <bool BF, int THREADS, int TOP, bool SPLIT, bool PAST>
 __global__ __launch_bounds__(THREADS) void dora_logprob_fwd(
@@ -633,8 +635,10 @@ __global__ __launch_bounds__(kThreads) void dora_logprob_join(
 // Gradient of a row's chunk blockIdx.x of kBwdU vectors per thread.  The logits are
 // loaded before the row's scalars are known; one exponential per element and no
 // reduction, so memory bounds it.  THROUGH: the gradient does not fit the
-// last-level cache and is stored past it (4096 x 131072 bf16: 330 us against
-// 346, 6.1 TB/s; where it fits, its reader finds it there).
+// last-level cache and is stored past it (4096 x 131072 bf16: 319 us a pass against
+// 336, 6.3 TB/s; where it fits, its reader finds it there).  A row whose lse is too
+// coarse is read again by each of its workgroups (1024 x 131072 bf16, all rows such:
+// 1.1 ms against 0.1).
 constexpr int kBwdU = 2;
 template <bool BF, int THREADS, bool THROUGH>
 __global__ __launch_bounds__(THREADS) void dora_logprob_bwd(
