@@ -1,5 +1,5 @@
-"""ctypes view of libdora.so (include/dora.h, include/dora_finetune.h).  No torch here: loading
-and the host-only entry points work without a GPU."""
+"""ctypes view of libdora.so (include/dora.h, include/dora_finetune.h, include/dora_posttrain.h).
+No torch here: loading and the host-only entry points work without a GPU."""
 from __future__ import annotations
 
 import ctypes
@@ -19,6 +19,8 @@ NOALLOC_SCRATCH_BYTES = 64 << 20   # DORA_NOALLOC_SCRATCH_BYTES
 LOGPROB_MAX_TOP = 64               # DORA_LOGPROB_MAX_TOP
 STATE_BLOCK = 128                  # DORA_STATE_BLOCK
 LAYERNORM_NO_WS_WIDTH = {F32: 8192, BF16: 16384}   # DORA_LAYERNORM_NO_WS_WIDTH
+PREFERENCE_KIND = {"sigmoid": 0, "hinge": 1, "square": 2}   # dora_preference_kind
+POLICY_REDUCE = {"token": 0, "sequence": 1}                 # dora_policy_reduce
 
 
 class DoraShape(ctypes.Structure):
@@ -62,6 +64,28 @@ class DoraAdamwOptions(ctypes.Structure):
     ]
 
 
+class DoraTokenBatch(ctypes.Structure):
+    _fields_ = [
+        ("tokens", ctypes.c_int64), ("sequences", ctypes.c_int64), ("length", ctypes.c_int64),
+        ("offsets", ctypes.c_void_p), ("mask", ctypes.c_void_p),
+    ]
+
+
+class DoraPreferenceOptions(ctypes.Structure):
+    _fields_ = [
+        ("kind", ctypes.c_int32), ("normalize", ctypes.c_int32), ("beta", ctypes.c_double),
+        ("margin", ctypes.c_double), ("smoothing", ctypes.c_double),
+    ]
+
+
+class DoraPolicyOptions(ctypes.Structure):
+    _fields_ = [
+        ("clip_low", ctypes.c_double), ("clip_high", ctypes.c_double), ("dual_clip", ctypes.c_double),
+        ("kl_coef", ctypes.c_double), ("denominator", ctypes.c_double), ("reduce", ctypes.c_int32),
+        ("per_sequence", ctypes.c_int32),
+    ]
+
+
 class DoraError(RuntimeError):
     def __init__(self, code: int, what: str):
         self.code = code
@@ -98,6 +122,19 @@ _SIGS = {
                             _vp]),
     "dora_adamw_dequantize": (_i, [_vp, _vp, ctypes.c_int64, _i, _vp, ctypes.c_int32, _vp]),
     "dora_adamw_quantize": (_i, [_vp, ctypes.c_int64, _i, _vp, _vp, _vp]),
+    "dora_preference_workspace_bytes": (_sz, [ctypes.POINTER(DoraTokenBatch)]),
+    "dora_preference_forward": (_i, [ctypes.POINTER(DoraTokenBatch),
+                                     ctypes.POINTER(DoraPreferenceOptions), ctypes.c_int64, _vp, _vp,
+                                     _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "dora_preference_backward": (_i, [ctypes.POINTER(DoraTokenBatch),
+                                      ctypes.POINTER(DoraPreferenceOptions), ctypes.c_int64, _vp, _vp,
+                                      _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "dora_policy_workspace_bytes": (_sz, [ctypes.POINTER(DoraTokenBatch),
+                                          ctypes.POINTER(DoraPolicyOptions)]),
+    "dora_policy_forward": (_i, [ctypes.POINTER(DoraTokenBatch), ctypes.POINTER(DoraPolicyOptions),
+                                 _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "dora_policy_backward": (_i, [ctypes.POINTER(DoraTokenBatch), ctypes.POINTER(DoraPolicyOptions),
+                                  _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "dora_strerror": (ctypes.c_char_p, [_i]),
     "dora_timing_enable": (_i, [_i]),
     "dora_timing_collect": (_i, [ctypes.c_char_p, _sz]),

@@ -1,5 +1,5 @@
-"""DoRA and DVoRA linear layers, layer norm and token log probabilities on top of the C ABI
-(autograd glue only).
+"""DoRA and DVoRA linear layers, layer norm, token log probabilities and the losses on them on top of
+the C ABI (autograd glue only).
 
 Forward saves norm, xs = s (x A^T) and y for the backward; the norm is
 detached there (DoRA reading notes, Sec. 3.4).  DVoRA (Sec. 3.5) runs the same
@@ -208,3 +208,95 @@ def token_logprob(logits: torch.Tensor, targets: torch.Tensor, *, scale: float =
     if top:
         top_logp, top_index = top_logp.reshape(*lead, top), top_index.reshape(*lead, top)
     return logp.reshape(lead), entropy.reshape(lead), top_logp, top_index
+
+
+def _constants(**tensors):
+    """Refuses tensors that want a gradient which these losses do not form."""
+    for name, t in tensors.items():
+        if t is not None and t.requires_grad:
+            raise ValueError(f"{name} is a constant of this loss: detach it")
+
+
+def _contiguous(*tensors):
+    return [None if t is None else t.contiguous() for t in tensors]
+
+
+class PreferenceLossFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logp, ref_logp, chosen, rejected, mask, offsets, how):
+        loss, score, logit, count = ops.dora_preference_loss(logp, chosen, rejected, ref_logp=ref_logp,
+                                                             mask=mask, offsets=offsets, **how)
+        ctx.shape, ctx.how = logp.shape, how
+        ctx.save_for_backward(logit, count, chosen, rejected, mask, offsets)
+        ctx.mark_non_differentiable(score)
+        return loss, score
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, g_loss, _g_score):
+        logit, count, chosen, rejected, mask, offsets = ctx.saved_tensors
+        g = ops.dora_preference_loss_backward(g_loss.contiguous(), logit, count, chosen, rejected,
+                                              shape=ctx.shape, mask=mask, offsets=offsets, **ctx.how)
+        return g, None, None, None, None, None, None
+
+
+def preference_loss(logp: torch.Tensor, chosen: torch.Tensor, rejected: torch.Tensor, *, ref_logp=None,
+                    mask=None, offsets=None, kind: str = "sigmoid", beta: float = 0.1,
+                    margin: float = 0.0, smoothing: float = 0.0, normalize: bool = False):
+    """Loss of pairs of sequences, the first of which is preferred, differentiable in ``logp``.
+
+    logp, ref_logp: token log probabilities as ``token_logprob`` gives them, float32 [sequences,
+    length] or, with ``offsets`` (int64 [sequences + 1]), packed [tokens]; chosen, rejected: int64
+    [pairs], the sequences of each pair.  ``mask`` (bool) tells the tokens that count, ``normalize``
+    takes means over them instead of sums.  ``kind`` is sigmoid (with ``smoothing``, the share of
+    labels taken to be wrong), hinge or square.
+
+    Returns (loss, score): float32 [pairs], and float32 [sequences] without gradient, beta times a
+    sequence's log ratio.
+    """
+    _constants(ref_logp=ref_logp)
+    how = dict(kind=kind, beta=beta, margin=margin, smoothing=smoothing, normalize=normalize)
+    logp, ref_logp, chosen, rejected, mask, offsets = _contiguous(logp, ref_logp, chosen, rejected,
+                                                                  mask, offsets)
+    return PreferenceLossFunction.apply(logp, ref_logp, chosen, rejected, mask, offsets, how)
+
+
+class PolicyLossFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logp, old_logp, advantages, ref_logp, mask, offsets, how):
+        loss, stats, weight = ops.dora_policy_loss(logp, old_logp, advantages, ref_logp=ref_logp,
+                                                   mask=mask, offsets=offsets, **how)
+        ctx.how = how
+        ctx.save_for_backward(weight, logp, old_logp, advantages, ref_logp, mask, offsets)
+        ctx.mark_non_differentiable(stats)
+        return loss, stats
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, g_loss, _g_stats):
+        weight, logp, old_logp, advantages, ref_logp, mask, offsets = ctx.saved_tensors
+        g = ops.dora_policy_loss_backward(g_loss.contiguous(), weight, logp, old_logp, advantages,
+                                          ref_logp=ref_logp, mask=mask, offsets=offsets, **ctx.how)
+        return g, None, None, None, None, None, None
+
+
+def policy_loss(logp: torch.Tensor, old_logp: torch.Tensor, advantages: torch.Tensor, *, ref_logp=None,
+                mask=None, offsets=None, clip=(0.2, 0.2), dual_clip=None, kl_coef: float = 0.0,
+                reduce: str = "token", denominator=None):
+    """Clipped policy loss on token log probabilities, differentiable in ``logp``.
+
+    logp, old_logp, ref_logp: float32 [sequences, length] or, with ``offsets`` (int64 [sequences +
+    1]), packed [tokens]; advantages: float32, of logp's shape or [sequences].  ``mask`` (bool) tells
+    the tokens that count.  The ratio exp(logp - old_logp) is bounded by 1 - clip[0] and 1 + clip[1]
+    (and by ``dual_clip`` where the advantage is negative); ``kl_coef`` weighs the divergence
+    exp(d) - 1 - d, d = ref_logp - logp.  ``reduce`` is token (mean over tokens) or sequence (mean
+    over sequences of their means); ``denominator`` replaces the number that is divided by.
+
+    Returns (loss, stats): a scalar, and float32 [4] without gradient: mean divergence, share of
+    tokens held by a bound, mean ratio, number of counted tokens.
+    """
+    _constants(old_logp=old_logp, advantages=advantages, ref_logp=ref_logp)
+    how = dict(clip=clip, dual_clip=dual_clip, kl_coef=kl_coef, reduce=reduce, denominator=denominator)
+    logp, old_logp, advantages, ref_logp, mask, offsets = _contiguous(logp, old_logp, advantages,
+                                                                      ref_logp, mask, offsets)
+    return PolicyLossFunction.apply(logp, old_logp, advantages, ref_logp, mask, offsets, how)

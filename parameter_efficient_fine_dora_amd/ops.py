@@ -452,6 +452,183 @@ def dora_token_logprob_backward(grad_logp, grad_entropy, logits, targets, lse, e
     return grad_logits
 
 
+def _token_batch(shape, dev, mask, offsets):
+    """The sequences of tensors [sequences, length], or of one [tokens] with offsets."""
+    if offsets is None:
+        if len(shape) != 2:
+            raise ValueError(f"log probabilities have shape {tuple(shape)}: two dimensions, or one "
+                             "with offsets, are expected")
+        S, length = shape
+        tokens = S * length
+    else:
+        if len(shape) != 1:
+            raise ValueError(f"log probabilities have shape {tuple(shape)}: one dimension is "
+                             "expected with offsets")
+        _need(offsets, "offsets", torch.int64, None, dev)
+        if offsets.dim() != 1 or offsets.numel() < 1:
+            raise ValueError(f"offsets have shape {tuple(offsets.shape)}, expected (sequences + 1,)")
+        tokens, S, length = shape[0], offsets.numel() - 1, 0
+    if mask is not None:
+        _need(mask, "mask", torch.bool, shape, dev)
+    return _lib.DoraTokenBatch(tokens, S, length, _ptr(offsets), _ptr(mask))
+
+
+def _choice(value, name, of):
+    if value not in of:
+        raise ValueError(f"{name} is {value!r}, expected one of {', '.join(of)}")
+    return of[value]
+
+
+def _preference_options(kind, beta, margin, smoothing, normalize):
+    return _lib.DoraPreferenceOptions(_choice(kind, "kind", _lib.PREFERENCE_KIND), int(bool(normalize)),
+                                      float(beta), float(margin), float(smoothing))
+
+
+def _some_ws(nbytes, dev, workspace):
+    """A workspace of at least `nbytes`, the caller's if there is one; its address and size."""
+    if workspace is None:
+        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
+    return workspace, _given_ws(workspace, dev)
+
+
+def dora_preference_loss(logp, chosen, rejected, *, ref_logp=None, mask=None, offsets=None,
+                         kind="sigmoid", beta=0.1, margin=0.0, smoothing=0.0, normalize=False,
+                         workspace=None):
+    """Losses of pairs of sequences by their summed log probabilities, relative to a reference's.
+
+    logp, ref_logp   float32 [sequences, length], or [tokens] with ``offsets`` (int64
+                     [sequences + 1]: sequence s has tokens offsets[s] to offsets[s + 1])
+    chosen, rejected int64 [pairs]: the sequences of each pair, the preferred one first
+    mask             bool, of logp's shape: the tokens that count
+    kind             sigmoid, hinge or square; ``smoothing`` is the sigmoid's share of wrong labels
+    normalize        means over a sequence's counted tokens instead of sums
+
+    Returns (loss, score, logit, count): float32 [pairs], [sequences], [pairs], [sequences]; score
+    is beta times a sequence's sum, logit the difference of two scores less ``margin``.
+    """
+    _need(logp, "logp", torch.float32)
+    dev, shape = logp.device, logp.shape
+    batch = _token_batch(shape, dev, mask, offsets)
+    if ref_logp is not None:
+        _need(ref_logp, "ref_logp", torch.float32, shape, dev)
+    P, S = _pairs(chosen, rejected, dev), batch.sequences
+    how = _preference_options(kind, beta, margin, smoothing, normalize)
+    loss, logit = torch.empty(2, P, dtype=torch.float32, device=dev).unbind(0)
+    score, count = torch.empty(2, S, dtype=torch.float32, device=dev).unbind(0)
+    L = _lib.lib()
+    ws, nb = _some_ws(L.dora_preference_workspace_bytes(ctypes.byref(batch)), dev, workspace)
+    _check(L.dora_preference_forward(ctypes.byref(batch), ctypes.byref(how), P, _ptr(logp),
+                                     _ptr(ref_logp), _ptr(chosen), _ptr(rejected), _ptr(loss),
+                                     _ptr(score), _ptr(logit), _ptr(count), _ptr(ws), nb,
+                                     _stream(dev)), "dora_preference_forward")
+    return loss, score, logit, count
+
+
+def _pairs(chosen, rejected, dev):
+    _need(chosen, "chosen", torch.int64, None, dev)
+    if chosen.dim() != 1:
+        raise ValueError(f"chosen must have one dimension, has {chosen.dim()}")
+    _need(rejected, "rejected", torch.int64, chosen.shape, dev)
+    return chosen.numel()
+
+
+def dora_preference_loss_backward(grad_loss, logit, count, chosen, rejected, *, shape, mask=None,
+                                  offsets=None, kind="sigmoid", beta=0.1, margin=0.0, smoothing=0.0,
+                                  normalize=False, grad_logp=None, workspace=None):
+    """Gradient of dora_preference_loss's losses with respect to logp (of ``shape``), float32;
+    logit and count as it returned them."""
+    _need(logit, "logit", torch.float32)
+    dev, shape = logit.device, tuple(shape)
+    batch = _token_batch(shape, dev, mask, offsets)
+    P = _pairs(chosen, rejected, dev)
+    _need(logit, "logit", torch.float32, (P,), dev)
+    _need(grad_loss, "grad_loss", torch.float32, (P,), dev)
+    _need(count, "count", torch.float32, (batch.sequences,), dev)
+    how = _preference_options(kind, beta, margin, smoothing, normalize)
+    grad_logp = _out(grad_logp, "grad_logp", torch.float32, shape, dev)
+    L = _lib.lib()
+    ws, nb = _some_ws(L.dora_preference_workspace_bytes(ctypes.byref(batch)), dev, workspace)
+    _check(L.dora_preference_backward(ctypes.byref(batch), ctypes.byref(how), P, _ptr(grad_loss),
+                                      _ptr(logit), _ptr(count), _ptr(chosen), _ptr(rejected),
+                                      _ptr(grad_logp), _ptr(ws), nb, _stream(dev)),
+           "dora_preference_backward")
+    return grad_logp
+
+
+def _policy_arguments(logp, old_logp, advantages, ref_logp, mask, offsets, clip, dual_clip, kl_coef,
+                      reduce, denominator):
+    """Checks what both directions of the policy loss take; returns the batch and the options."""
+    _need(logp, "logp", torch.float32)
+    dev, shape = logp.device, logp.shape
+    batch = _token_batch(shape, dev, mask, offsets)
+    _need(old_logp, "old_logp", torch.float32, shape, dev)
+    if ref_logp is not None:
+        _need(ref_logp, "ref_logp", torch.float32, shape, dev)
+    elif kl_coef:
+        raise ValueError("kl_coef needs ref_logp")
+    # one advantage a token where the shapes agree, else one a sequence
+    each = isinstance(advantages, torch.Tensor) and advantages.shape == shape
+    _need(advantages, "advantages", torch.float32, shape if each else (batch.sequences,), dev)
+    if denominator is not None and not denominator > 0:
+        raise ValueError(f"denominator is {denominator}, expected more than 0")
+    return batch, _lib.DoraPolicyOptions(
+        float(clip[0]), float(clip[1]), float("inf") if dual_clip is None else float(dual_clip),
+        float(kl_coef), 0.0 if denominator is None else float(denominator),
+        _choice(reduce, "reduce", _lib.POLICY_REDUCE), int(not each))
+
+
+def dora_policy_loss(logp, old_logp, advantages, *, ref_logp=None, mask=None, offsets=None,
+                     clip=(0.2, 0.2), dual_clip=None, kl_coef=0.0, reduce="token", denominator=None,
+                     workspace=None):
+    """Clipped policy loss of tokens, with ``kl_coef`` times their divergence from a reference.
+
+    logp, old_logp, ref_logp   float32 [sequences, length], or [tokens] with ``offsets`` (int64
+                     [sequences + 1])
+    advantages       float32, one a token (logp's shape) or one a sequence ([sequences])
+    mask             bool, of logp's shape: the tokens that count
+    clip             the ratio's bounds are 1 - clip[0] and 1 + clip[1]; ``dual_clip`` bounds it from
+                     above where the advantage is negative
+    reduce           token: sum over tokens / their number; sequence: mean over the sequences of
+                     their means.  ``denominator`` takes the place of the number.
+
+    Returns (loss, stats, weight): a float32 scalar; float32 [4], the counted tokens' mean
+    divergence, the share of them held by a bound, their mean ratio and their number; the factor of
+    each sequence's tokens in the loss, float32 [sequences] or [1], for the backward.
+    """
+    batch, how = _policy_arguments(logp, old_logp, advantages, ref_logp, mask, offsets, clip,
+                                   dual_clip, kl_coef, reduce, denominator)
+    dev = logp.device
+    loss = torch.empty((), dtype=torch.float32, device=dev)
+    stats = torch.empty(4, dtype=torch.float32, device=dev)
+    weight = torch.empty(batch.sequences if how.reduce else 1, dtype=torch.float32, device=dev)
+    L = _lib.lib()
+    nb = L.dora_policy_workspace_bytes(ctypes.byref(batch), ctypes.byref(how))
+    ws, nb = _some_ws(nb, dev, workspace)
+    _check(L.dora_policy_forward(ctypes.byref(batch), ctypes.byref(how), _ptr(logp), _ptr(old_logp),
+                                 _ptr(ref_logp), _ptr(advantages), _ptr(loss), _ptr(stats),
+                                 _ptr(weight), _ptr(ws), nb, _stream(dev)), "dora_policy_forward")
+    return loss, stats, weight
+
+
+def dora_policy_loss_backward(grad_loss, weight, logp, old_logp, advantages, *, ref_logp=None,
+                              mask=None, offsets=None, clip=(0.2, 0.2), dual_clip=None, kl_coef=0.0,
+                              reduce="token", denominator=None, grad_logp=None):
+    """Gradient of dora_policy_loss's loss with respect to logp, float32 of its shape; grad_loss is a
+    float32 scalar on the device, weight as the forward returned it."""
+    batch, how = _policy_arguments(logp, old_logp, advantages, ref_logp, mask, offsets, clip,
+                                   dual_clip, kl_coef, reduce, denominator)
+    dev = logp.device
+    if _need(grad_loss, "grad_loss", torch.float32, None, dev).numel() != 1:
+        raise ValueError("grad_loss must be one number")
+    _need(weight, "weight", torch.float32, (batch.sequences if how.reduce else 1,), dev)
+    grad_logp = _out(grad_logp, "grad_logp", torch.float32, logp.shape, dev)
+    _check(_lib.lib().dora_policy_backward(ctypes.byref(batch), ctypes.byref(how), _ptr(grad_loss),
+                                           _ptr(weight), _ptr(logp), _ptr(old_logp), _ptr(ref_logp),
+                                           _ptr(advantages), _ptr(grad_logp), _stream(dev)),
+           "dora_policy_backward")
+    return grad_logp
+
+
 class AdamWPlan:
     """The tensors of an AdamW step, checked once and kept for the steps that follow.
 
