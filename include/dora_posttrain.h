@@ -134,6 +134,83 @@ DORA_API int dora_policy_backward(const dora_token_batch* batch, const dora_poli
                                   const float* old_logp, const float* ref_logp,
                                   const float* advantages, float* grad_logp, void* hip_stream);
 
+/*
+ * Newton-Schulz iteration towards the nearest (semi-)orthogonal matrix:
+ *   X <- X / (|X|_F + eps), then for each step k
+ *   X <- a_k X + (b_k S + c_k S^2) X,  S = X X^T (X^T X for a tall X: the same X)
+ * Singular values s of X become those of the composed polynomials
+ * s (a + b s^2 + c s^4); (3.4445, -4.7750, 2.0315) five times takes nearly all of
+ * them to between 0.7 and 1.2.
+ */
+typedef struct {
+    const double* coefficients;  /* host [steps][3]: a, b, c; finite, and such that singular
+                                    values, Q and S stay below 2^30 (else DORA_ERR_FLAGS)    */
+    int32_t       steps;         /* 1 <= steps <= 16                                          */
+    uint32_t      reserved;      /* must be 0                                                 */
+    double        eps;           /* 2^-100 <= eps, finite as a float32                        */
+} dora_newton_schulz;
+
+typedef struct {
+    const void* x;     /* [rows, cols] contiguous                                             */
+    void*       out;   /* [rows, cols] contiguous; may be x itself, must not overlap otherwise */
+    int64_t     rows;  /* >= 0; the longer of both at most 2^20, the shorter at most 16384    */
+    int64_t     cols;
+} dora_matrix;
+
+typedef struct {
+    dora_newton_schulz iteration;
+    int32_t  dtype;      /* dora_dtype of x and out                                           */
+    uint32_t reserved;   /* must be 0                                                         */
+} dora_orthogonalize_options;
+
+/*
+ * out = the iteration's last X for each of `count` matrices (`matrices` and the
+ * coefficients are host arrays, read during the call only).  Matrices of any sizes
+ * share launches; the workspace holds about 4 bytes (bf16) or 16 (float32) an
+ * element and 20 n^2 for a shorter side of n.  Sums are float32, and float32
+ * results have float32's precision.  A matrix of zeros stays zero; one with a NaN
+ * or an infinity becomes NaN throughout, the others of the call do not.
+ */
+DORA_API size_t dora_orthogonalize_workspace_bytes(const dora_matrix* matrices, int64_t count,
+                                                   const dora_orthogonalize_options* options);
+DORA_API int dora_orthogonalize(const dora_matrix* matrices, int64_t count,
+                                const dora_orthogonalize_options* options, void* ws,
+                                size_t ws_bytes, void* hip_stream);
+
+typedef struct {
+    void*       param;     /* [rows, cols], param_dtype: read and written                     */
+    const void* grad;      /* [rows, cols], grad_dtype                                        */
+    float*      momentum;  /* [rows, cols]                                                    */
+    float*      master;    /* float32 [rows, cols] copy of a bf16 param, or NULL; where given
+                              it is the value that is updated and param becomes its rounding.
+                              All tensors of a call have one or none does.                    */
+    int64_t     rows, cols;
+    double      scale;     /* of this tensor's update, finite                                 */
+} dora_muon_tensor;
+
+typedef struct {
+    dora_newton_schulz iteration;
+    int32_t  param_dtype;   /* dora_dtype of every param                                      */
+    int32_t  grad_dtype;    /* dora_dtype of every grad                                       */
+    int32_t  nesterov;      /* 0 or 1                                                         */
+    uint32_t reserved;      /* must be 0                                                      */
+    double   lr, momentum, weight_decay;   /* finite; 0 <= momentum < 1                       */
+} dora_muon_options;
+
+/*
+ * A step on `count` matrices with orthogonalised updates (no two of the arrays
+ * that are written may overlap):
+ *   m = momentum m + (1 - momentum) grad
+ *   u = momentum m + (1 - momentum) grad with nesterov, else m
+ *   p = p (1 - lr weight_decay) - lr scale X(u),  X(u) the iteration's last X from u
+ * m, u and the update are float32; p is rounded once.
+ */
+DORA_API size_t dora_muon_workspace_bytes(const dora_muon_tensor* tensors, int64_t count,
+                                          const dora_muon_options* options);
+DORA_API int dora_muon_step(const dora_muon_tensor* tensors, int64_t count,
+                            const dora_muon_options* options, void* ws, size_t ws_bytes,
+                            void* hip_stream);
+
 #ifdef __cplusplus
 }
 #endif

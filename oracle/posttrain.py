@@ -126,3 +126,26 @@ def policy_loss(logp, old, adv, where, ref=None, mask=None, clip=(0.2, 0.2), dua
             factor[a:b] = w
     stats = np.array([*(terms[live][:, 2:].sum(0) / max(total, 1)), total])
     return math.fsum(factor[live] * terms[live][:, 0]), stats, weight, np.where(live, factor * terms[:, 1], 0.0)
+
+
+def orthogonalize(x, coefficients, eps=1e-7):
+    """The iteration's last X of one matrix."""
+    x = np.asarray(x, np.float64)
+    with np.errstate(invalid="ignore", over="ignore"):
+        x = x / (np.sqrt((x * x).sum()) + eps)
+        for a, b, c in coefficients:
+            if x.shape[0] <= x.shape[1]:
+                s = x @ x.T
+                x = a * x + (b * s + c * (s @ s)) @ x
+            else:
+                s = x.T @ x
+                x = a * x + x @ (b * s + c * (s @ s))
+    return x
+
+
+def muon_step(p, g, m, lr, momentum, nesterov, weight_decay, coefficients, eps, factor):
+    """(p, m) after a step."""
+    p, g, m = (np.asarray(t, np.float64) for t in (p, g, m))
+    m = momentum * m + (1 - momentum) * g
+    u = momentum * m + (1 - momentum) * g if nesterov else m
+    return p * (1 - lr * weight_decay) - lr * factor * orthogonalize(u, coefficients, eps), m

@@ -86,6 +86,42 @@ class DoraPolicyOptions(ctypes.Structure):
     ]
 
 
+class DoraNewtonSchulz(ctypes.Structure):
+    _fields_ = [
+        ("coefficients", ctypes.c_void_p), ("steps", ctypes.c_int32), ("reserved", ctypes.c_uint32),
+        ("eps", ctypes.c_double),
+    ]
+
+
+class DoraMatrix(ctypes.Structure):
+    _fields_ = [
+        ("x", ctypes.c_void_p), ("out", ctypes.c_void_p), ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+    ]
+
+
+class DoraOrthogonalizeOptions(ctypes.Structure):
+    _fields_ = [
+        ("iteration", DoraNewtonSchulz), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_uint32),
+    ]
+
+
+class DoraMuonTensor(ctypes.Structure):
+    _fields_ = [
+        ("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("momentum", ctypes.c_void_p),
+        ("master", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+        ("scale", ctypes.c_double),
+    ]
+
+
+class DoraMuonOptions(ctypes.Structure):
+    _fields_ = [
+        ("iteration", DoraNewtonSchulz), ("param_dtype", ctypes.c_int32),
+        ("grad_dtype", ctypes.c_int32), ("nesterov", ctypes.c_int32), ("reserved", ctypes.c_uint32),
+        ("lr", ctypes.c_double), ("momentum", ctypes.c_double), ("weight_decay", ctypes.c_double),
+    ]
+
+
 class DoraError(RuntimeError):
     def __init__(self, code: int, what: str):
         self.code = code
@@ -135,6 +171,12 @@ _SIGS = {
                                  _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "dora_policy_backward": (_i, [ctypes.POINTER(DoraTokenBatch), ctypes.POINTER(DoraPolicyOptions),
                                   _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "dora_orthogonalize_workspace_bytes": (_sz, [_vp, ctypes.c_int64,
+                                                 ctypes.POINTER(DoraOrthogonalizeOptions)]),
+    "dora_orthogonalize": (_i, [_vp, ctypes.c_int64, ctypes.POINTER(DoraOrthogonalizeOptions), _vp, _sz,
+                                _vp]),
+    "dora_muon_workspace_bytes": (_sz, [_vp, ctypes.c_int64, ctypes.POINTER(DoraMuonOptions)]),
+    "dora_muon_step": (_i, [_vp, ctypes.c_int64, ctypes.POINTER(DoraMuonOptions), _vp, _sz, _vp]),
     "dora_strerror": (ctypes.c_char_p, [_i]),
     "dora_timing_enable": (_i, [_i]),
     "dora_timing_collect": (_i, [ctypes.c_char_p, _sz]),

@@ -1,0 +1,1293 @@
+// Orthogonalised updates: X_0 = X / (|X|_F + eps), then for each step
+//   X <- P X,  P = a + b S + c S^2,  S = X X^T   (n x n, n the shorter side of X, m the longer).
+//
+// Everything between the first S and the last product stays n x n.  The P of all steps are
+// polynomials of the first S, so they commute, and
+//   S <- P S P,  Q <- P Q,  X_last = Q X_0
+// replace two products with X in every step (4 n^2 m flops each way round) by one half of one
+// (S is symmetric) and one at the end; adapters have n of 16 to 400 against m of thousands.  The
+// n x n products are symmetric too: only tiles on and above the diagonal are computed.
+//
+// Precision.  A step multiplies small singular values by a (3.4445 as usually chosen), so five
+// steps raise an error in S of E (relative to |X|_F^2) to |b/a| sum_j prod_{i<j} a_i^2 E = 3e4 E in
+// the directions below 2^-9 of the norm.  All n x n matrices are therefore held as two half
+// precision numbers, hi + lo (22 bits or more: the hi product and both cross products go through
+// the matrix cores, the lo lo product is below 2^-22), scaled by powers of two into half's range;
+// sums are float32.  For bf16 results that is enough.  For float32 results the product Q X is
+// formed before the factor passes 1024 (after three of five usual steps), and S anew from it.
+// A bf16 X is one half precision number exactly (its bits below 2^-38 of its largest element are
+// left out), a float32 X is hi + lo.
+//
+// Layout.  A "pair" row holds blocks of 32 columns: 32 hi, then 32 lo, so that the 128 bytes that
+// a stage copies of a row are the hi and lo of 32 columns; a "single" row holds 64 columns there.
+// X is kept in both orders, [n, m] for S and [m, n] for Q X: then both operands of every product
+// are contiguous along what is summed over, and one loop serves them all.
+//
+// Many matrices share a launch: a step on the adapters of a model is 20 launches whatever their
+// number, and small matrices fill the chip together.
+#include <algorithm>
+#include <cmath>
+#include <type_traits>
+#include <vector>
+
+#include "../../include/dora_posttrain.h"
+#include "checks.h"
+#include "elem.h"
+#include "kernels.h"
+#include "launch_cut.h"
+
+namespace dora {
+namespace {
+
+typedef _Float16 f16;
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+typedef __amdgpu_buffer_rsrc_t Rsrc;
+
+constexpr int kThreads = 256;
+constexpr int kRowBytes = 128;       // of a row in one stage
+constexpr int kPairBlock = 32;       // columns of a pair row's block
+constexpr int kPad = 128;            // the long side is padded to whole tiles of either size
+constexpr int kMaxGroups = 12;
+constexpr int kMaxMatrices = 48;     // of one launch that needs their addresses
+constexpr int kMaxBlocks = 1024;     // workgroups that look for one matrix's largest element
+constexpr int kMaxSplits = 32;
+
+// ---- matrices of one size ---------------------------------------------------------------
+// Offsets are bytes from a matrix's own part of the workspace.
+struct Group {
+  int n, m;            // shorter and longer side
+  int nt, mt;          // padded
+  int count;           // matrices
+  int first;           // the first one's number
+  uint32_t from;       // the launch's first workgroup of this group
+  int splits;          // of the sum over m
+  int blocks;          // partial maxima
+  int64_t base, stride;
+  int64_t xk, xt;      // X as [n, m] and [m, n]
+  int64_t xk2, xt2;    // the same of the product formed on the way
+  int64_t sq[5];       // n x n pairs: S, P, P S, and Q twice
+  int64_t part;        // partial sums of S, float32
+  int64_t most, scale; // partial maxima; the factor on X
+  bool tall;           // rows are the longer side
+};
+struct Groups {
+  int count;
+  Group g[kMaxGroups];
+};
+
+__host__ __device__ inline int tri(int t) { return t * (t + 1) / 2; }
+
+// Tile t of the upper triangle of nt x nt tiles, row by row.
+__device__ __forceinline__ void tri_tile(int t, int nt, int& ti, int& tj) {
+  int row = 0;
+  while (t >= nt - row) {
+    t -= nt - row;
+    ++row;
+  }
+  ti = row;
+  tj = row + t;
+}
+__device__ __forceinline__ int diagonal_tile(int t, int nt) { return t * nt - t * (t - 1) / 2; }
+
+// Neighbouring tiles on one XCD: workgroups go round the eight of them.
+__device__ __forceinline__ uint32_t by_xcd(uint32_t id, uint32_t total) {
+  const uint32_t each = total / 8, more = total % 8, x = id % 8, i = id / 8;
+  return x * each + min(x, more) + i;
+}
+__device__ __forceinline__ int group_of(const Groups& a, uint32_t id) {
+  int g = 0;
+  while (g + 1 < a.count && id >= a.g[g + 1].from) ++g;
+  return __builtin_amdgcn_readfirstlane(g);
+}
+
+// ---- the product loop ---------------------------------------------------------------------
+__device__ __forceinline__ Rsrc rsrc(const void* base, int64_t bytes) {
+  const uint64_t a = reinterpret_cast<uint64_t>(base);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)a);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
+  const int n = __builtin_amdgcn_readfirstlane((int)min(bytes, (int64_t)0x7fffffff));
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(((uint64_t)hi << 32) | lo),
+                                           (short)0, n, 0x00020000);
+}
+// s_waitcnt vmcnt(N), the other counters left open.
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
+}
+__device__ __forceinline__ void barrier_nofence() { asm volatile("s_barrier" ::: "memory"); }
+__device__ __forceinline__ int swz(int row) { return (row & 7) ^ ((row >> 3) & 7); }
+
+// One operand of a tile: T rows of `ld` bytes, `wrap` stages along them (a longer sum starts
+// again at the first).
+struct Side {
+  const uint8_t* p;
+  int64_t ld;
+  int wrap;
+};
+
+// A T x T tile of A B^T over the stages [k0, k0 + steps): four waves, each a quarter.  acc[i][j]
+// are 32 x 32 blocks; in block (i, j) a lane has row lane % 32 of A's side and, as element
+// 4 g + e, column 8 g + 4 (lane / 32) + e of B's.
+//
+// PAIR: three products of every hi + lo pair of fragments, 12 matrix instructions to 8 fragments
+// read from LDS at T = 128 (single: 4 to 4).  RING stages are in flight.
+template <int T, int RING, bool PAIR>
+struct Product {
+  static constexpr int kB = T / 64;                       // blocks of a wave along a side
+  static constexpr int kStage = 2 * T * kRowBytes;
+  static constexpr int kCopies = 2 * T / 8 / 4;           // of a wave and stage, 8 rows each
+  static constexpr int kLds = RING * kStage;
+
+  __device__ static __forceinline__ void run(uint8_t* sm, const Side& a, const Side& b, int k0,
+                                             int steps, f32x16 (&acc)[kB][kB]) {
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const Rsrc ra = rsrc(a.p, T * a.ld), rb = rsrc(b.p, T * b.ld);
+    uint32_t off[kCopies];
+#pragma unroll
+    for (int q = 0; q < kCopies; ++q) {
+      const int row = (wave + 4 * q) * 8 + (lane >> 3);   // of both sides, A's first
+      const int64_t ld = row < T ? a.ld : b.ld;
+      off[q] = (uint32_t)((row & (T - 1)) * ld) + (uint32_t)(((lane & 7) ^ swz(row)) << 4);
+    }
+    int ka = k0 % a.wrap, kb = k0 % b.wrap;
+    auto issue = [&](int slot) {
+      uint8_t* dst = sm + slot * kStage;
+#pragma unroll
+      for (int q = 0; q < kCopies; ++q) {
+        const bool first = (4 * q) * 8 < T;   // a copy's rows are all of one side
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            first ? ra : rb, (__attribute__((address_space(3))) void*)(dst + (wave + 4 * q) * 1024),
+            16, (int)off[q], (first ? ka : kb) * kRowBytes, 0, 0);
+      }
+      if (++ka == a.wrap) ka = 0;
+      if (++kb == b.wrap) kb = 0;
+    };
+#pragma unroll
+    for (int i = 0; i < kB; ++i)
+#pragma unroll
+      for (int j = 0; j < kB; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+    const int pre = min(RING, steps);
+    for (int s = 0; s < pre; ++s) issue(s);
+    const int rowa = (wave & 1) * (T / 2) + (lane & 31);
+    const int rowb = T + (wave >> 1) * (T / 2) + (lane & 31);
+    int slot = 0;
+    for (int s = 0; s < steps; ++s) {
+      // the stage has landed once only the copies of the stages behind it are in flight
+      const int later = min(RING - 1, steps - 1 - s);
+      if (RING > 3 && later >= 3) wait_vm<3 * kCopies>();
+      else if (RING > 2 && later == 2) wait_vm<2 * kCopies>();
+      else if (later >= 1) wait_vm<kCopies>();
+      else wait_vm<0>();
+      barrier_nofence();
+      const uint8_t* src = sm + slot * kStage;
+      auto frag = [&](int row, int chunk) {
+        return *reinterpret_cast<const f16x8*>(src + row * kRowBytes + ((chunk ^ swz(row)) << 4));
+      };
+      constexpr int kSub = PAIR ? 2 : 4;
+#pragma unroll
+      for (int u = 0; u < kSub; ++u) {
+        const int ch = u * 2 + (lane >> 5);
+        f16x8 fa[kB], fb[kB], la[kB], lb[kB];
+#pragma unroll
+        for (int i = 0; i < kB; ++i) {
+          fa[i] = frag(rowa + 32 * i, ch);
+          fb[i] = frag(rowb + 32 * i, ch);
+          if (PAIR) {
+            la[i] = frag(rowa + 32 * i, ch + 4);
+            lb[i] = frag(rowb + 32 * i, ch + 4);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kB; ++i)
+#pragma unroll
+          for (int j = 0; j < kB; ++j) {
+            if (PAIR) {
+              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fb[j], la[i], acc[i][j], 0, 0, 0);
+              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(lb[j], fa[i], acc[i][j], 0, 0, 0);
+            }
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fb[j], fa[i], acc[i][j], 0, 0, 0);
+          }
+      }
+      barrier_nofence();   // every wave has read the slot before it is filled again
+      if (s + RING < steps) issue(slot);
+      if (++slot == RING) slot = 0;
+    }
+  }
+
+  // Calls fn(row, column, values of four columns) for every group of four that this lane has.
+  template <typename Fn>
+  __device__ static __forceinline__ void each(const f32x16 (&acc)[kB][kB], Fn fn) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int i = 0; i < kB; ++i)
+#pragma unroll
+      for (int j = 0; j < kB; ++j)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          fn((wave & 1) * (T / 2) + 32 * i + (lane & 31),
+             (wave >> 1) * (T / 2) + 32 * j + 8 * g + 4 * (lane >> 5),
+             f32x4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2],
+                   acc[i][j][4 * g + 3]});
+  }
+};
+
+// ---- pairs ----------------------------------------------------------------------------------
+__device__ __forceinline__ int64_t pair_at(int64_t k) { return (k >> 5) * 64 + (k & 31); }
+
+__device__ __forceinline__ void split(float v, f16& hi, f16& lo) {
+  hi = (f16)v;
+  lo = (f16)(v - (float)hi);
+}
+// Columns [k, k + 4) of a pair row.
+__device__ __forceinline__ void store_pair4(f16* row, int64_t k, const f32x4& v) {
+  f16x4 h, l;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    f16 a, b;
+    split(v[e], a, b);
+    h[e] = a;
+    l[e] = b;
+  }
+  f16* p = row + pair_at(k);
+  *reinterpret_cast<f16x4*>(p) = h;
+  *reinterpret_cast<f16x4*>(p + kPairBlock) = l;
+}
+__device__ __forceinline__ f32x4 load_pair4(const f16* row, int64_t k) {
+  const f16* p = row + pair_at(k);
+  const f16x4 h = *reinterpret_cast<const f16x4*>(p);
+  const f16x4 l = *reinterpret_cast<const f16x4*>(p + kPairBlock);
+  f32x4 v;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = (float)h[e] + (float)l[e];
+  return v;
+}
+// The same four values at their mirrored places: column k of four rows.
+__device__ __forceinline__ void store_pair_mirror(f16* rows, int64_t ld, int64_t k, const f32x4& v) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    f16 a, b;
+    split(v[e], a, b);
+    f16* p = rows + e * ld + pair_at(k);
+    p[0] = a;
+    p[kPairBlock] = b;
+  }
+}
+
+// ---- X into half precision --------------------------------------------------------------------
+// Where a matrix's elements come from.  MOMENT: u = mu m + (1 - mu) g of the gradient in `x` and
+// the momentum (already moved on where `moved`), or the momentum itself without nesterov.
+struct Source {
+  const void* x;
+  float* moment;
+};
+struct Sources {
+  Groups groups;
+  int count;                       // matrices of this launch
+  int first;                       // number of the first
+  uint32_t from[kMaxMatrices];     // their first workgroups
+  Source s[kMaxMatrices];
+  float mu, nu;                    // momentum's factor, 1 - that
+  int nesterov;
+};
+
+__device__ __forceinline__ int matrix_of(const uint32_t* from, int count, uint32_t id) {
+  int lo = 0, hi = count;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (id >= from[mid]) lo = mid;
+    else hi = mid;
+  }
+  return __builtin_amdgcn_readfirstlane(lo);
+}
+__device__ __forceinline__ int group_of_matrix(const Groups& a, int matrix) {
+  int g = 0;
+  while (g + 1 < a.count && matrix >= a.g[g + 1].first) ++g;
+  return __builtin_amdgcn_readfirstlane(g);
+}
+__device__ __forceinline__ float moved(float m, float g, float mu, float nu) {
+  return fmaf(mu, m, nu * g);
+}
+__device__ __forceinline__ float update_of(float m, float g, const Sources& a) {
+  return a.nesterov ? fmaf(a.mu, m, a.nu * g) : m;
+}
+
+constexpr int kVec = 8;
+
+template <bool BF>
+__device__ __forceinline__ void load8(const void* p, int64_t i, int64_t n, float* v) {
+  using E = Elem<BF>;
+  const typename E::T* x = reinterpret_cast<const typename E::T*>(p);
+#pragma unroll
+  for (int q = 0; q < kVec; q += E::kN) load_part<BF>(x, i + q, n, 0.f, v + q);
+}
+
+// The largest magnitude of a matrix's part, as bits (NaN above infinity above numbers), and the
+// momentum moved on: one pass over gradient and momentum, bound by memory.
+template <bool BF, bool MOMENT>
+__global__ __launch_bounds__(kThreads) void dora_orthogonal_most(const Sources a, uint8_t* ws) {
+  __shared__ uint32_t lds[kThreads / 64];
+  const int u = matrix_of(a.from, a.count, blockIdx.x);
+  const Group& g = a.groups.g[group_of_matrix(a.groups, a.first + u)];
+  const int64_t n = (int64_t)g.n * g.m;
+  const int block = blockIdx.x - a.from[u];
+  const Source s = a.s[u];
+  uint32_t most = 0;
+  for (int64_t i = ((int64_t)block * kThreads + threadIdx.x) * kVec; i < n;
+       i += (int64_t)g.blocks * kThreads * kVec) {
+    float v[kVec];
+    load8<BF>(s.x, i, n, v);
+    if (MOMENT) {
+      float m[kVec];
+      load8<false>(s.moment, i, n, m);
+#pragma unroll
+      for (int q = 0; q < kVec; ++q) {
+        m[q] = moved(m[q], v[q], a.mu, a.nu);
+        v[q] = update_of(m[q], v[q], a);
+      }
+      store_part<false>(s.moment, i, n, m);
+      store_part<false>(s.moment, i + 4, n, m + 4);
+    }
+#pragma unroll
+    for (int q = 0; q < kVec; ++q) most = max(most, __float_as_uint(v[q]) & 0x7fffffffu);
+  }
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) most = max(most, (uint32_t)__shfl_xor((int)most, off, 64));
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = most;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int w = 1; w < kThreads / 64; ++w) most = max(most, lds[w]);
+    uint8_t* own = ws + g.base + (int64_t)(a.first + u - g.first) * g.stride;
+    reinterpret_cast<uint32_t*>(own + g.most)[block] = most;
+  }
+}
+
+// The power of two that takes a matrix's largest magnitude to [2^14, 2^15): half precision holds
+// 2^16 - 32 at most and whole steps of 2^-24.  0 for a matrix of zeros, infinities or NaN (whose
+// results are NaN throughout).
+__device__ __forceinline__ int exponent_of(const uint32_t* most, int blocks, uint32_t* lds) {
+  uint32_t v = 0;
+  for (int i = threadIdx.x; i < blocks; i += kThreads) v = max(v, most[i]);
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, off, 64));
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+  __syncthreads();
+  v = lds[0];
+#pragma unroll
+  for (int w = 1; w < kThreads / 64; ++w) v = max(v, lds[w]);
+  if (v == 0 || v >= 0x7f800000u) return 0;
+  const int e = v >> 23 ? (int)(v >> 23) - 127 : 31 - __builtin_clz(v) - 149;
+  return 14 - e;
+}
+
+// A 64 x 64 block of the padded matrix into both orders, through LDS for the turned one; zeros
+// where the matrix ends.  Memory bounds it: what is read is 2 to 6 bytes an element, written 4 (one
+// number, two orders) or 8.
+template <bool BF, bool MOMENT, bool PAIR>
+__global__ __launch_bounds__(kThreads) void dora_orthogonal_halves(const Sources a, uint8_t* ws) {
+  constexpr int kE = 64;
+  __shared__ uint32_t tile[kE][kE + 1];
+  __shared__ uint32_t lds[kThreads / 64];
+  const int u = matrix_of(a.from, a.count, blockIdx.x);
+  const Group& g = a.groups.g[group_of_matrix(a.groups, a.first + u)];
+  uint8_t* own = ws + g.base + (int64_t)(a.first + u - g.first) * g.stride;
+  const int rows = g.tall ? g.m : g.n, cols = g.tall ? g.n : g.m;
+  const int prows = g.tall ? g.mt : g.nt, pcols = g.tall ? g.nt : g.mt;
+  const int across = pcols / kE, block = blockIdx.x - a.from[u];
+  const int r0 = block / across * kE, c0 = block % across * kE;
+  const int e = exponent_of(reinterpret_cast<const uint32_t*>(own + g.most), g.blocks, lds);
+  const Source s = a.s[u];
+  f16* straight = reinterpret_cast<f16*>(own + (g.tall ? g.xt : g.xk));   // [prows, pcols]
+  f16* turned = reinterpret_cast<f16*>(own + (g.tall ? g.xk : g.xt));     // [pcols, prows]
+  auto put = [&](f16* row, int64_t k, const f16* h, const f16* l) {
+    f16* p = row + (PAIR ? pair_at(k) : k);
+    *reinterpret_cast<f16x8*>(p) = *reinterpret_cast<const f16x8*>(h);
+    if (PAIR) *reinterpret_cast<f16x8*>(p + kPairBlock) = *reinterpret_cast<const f16x8*>(l);
+  };
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const int r = threadIdx.x / 8 + 32 * half, c = threadIdx.x % 8 * kVec;
+    float v[kVec] = {};
+    if (r0 + r < rows && c0 + c < cols) {
+      const int64_t i = (int64_t)(r0 + r) * cols + c0 + c;
+      const int64_t stop = (int64_t)(r0 + r + 1) * cols;   // the row's end: zeros behind it
+      load8<BF>(s.x, i, stop, v);
+      if (MOMENT) {
+        float m[kVec];
+        load8<false>(s.moment, i, stop, m);
+#pragma unroll
+        for (int q = 0; q < kVec; ++q) v[q] = update_of(m[q], v[q], a);
+      }
+    }
+    __attribute__((aligned(16))) f16 h[kVec], l[kVec];
+#pragma unroll
+    for (int q = 0; q < kVec; ++q) {
+      split(ldexpf(v[q], e), h[q], l[q]);
+      tile[r][c + q] = (uint32_t)__builtin_bit_cast(uint16_t, h[q]) |
+                       (uint32_t)__builtin_bit_cast(uint16_t, l[q]) << 16;
+    }
+    put(straight + (int64_t)(r0 + r) * pcols * (PAIR ? 2 : 1), c0 + c, h, l);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const int c = threadIdx.x / 8 + 32 * half, r = threadIdx.x % 8 * kVec;
+    __attribute__((aligned(16))) f16 h[kVec], l[kVec];
+#pragma unroll
+    for (int q = 0; q < kVec; ++q) {
+      const uint32_t w = tile[r + q][c];
+      h[q] = __builtin_bit_cast(f16, (uint16_t)w);
+      l[q] = __builtin_bit_cast(f16, (uint16_t)(w >> 16));
+    }
+    put(turned + (int64_t)(c0 + c) * prows * (PAIR ? 2 : 1), r0 + r, h, l);
+  }
+}
+
+// ---- n x n products ---------------------------------------------------------------------------
+// Partial sums of S = X X^T over a part of m, float32.
+template <int T, int RING, bool PAIR>
+__global__ __launch_bounds__(kThreads) void dora_orthogonal_gram(const Groups a, uint32_t total,
+                                                                 bool second, uint8_t* ws) {
+  using P = Product<T, RING, PAIR>;
+  __shared__ __attribute__((aligned(1024))) uint8_t sm[P::kLds];
+  const uint32_t id = by_xcd(blockIdx.x, total);
+  const Group& g = a.g[group_of(a, id)];
+  const int nt = g.nt / T, tiles = tri(nt);
+  int rest = (int)(id - g.from);
+  const int split = rest % g.splits;
+  rest /= g.splits;
+  const int t = rest % tiles, u = rest / tiles;
+  int ti, tj;
+  tri_tile(t, nt, ti, tj);
+  uint8_t* own = ws + g.base + (int64_t)u * g.stride;
+  const int64_t ld = (int64_t)g.mt * (PAIR ? 4 : 2);
+  const int stages = (int)(ld / kRowBytes);
+  const int k0 = (int)((int64_t)stages * split / g.splits);
+  const int k1 = (int)((int64_t)stages * (split + 1) / g.splits);
+  const uint8_t* x = own + (second ? g.xk2 : g.xk);
+  f32x16 acc[P::kB][P::kB];
+  P::run(sm, Side{x + ti * T * ld, ld, stages}, Side{x + tj * T * ld, ld, stages}, k0, k1 - k0, acc);
+  float* out = reinterpret_cast<float*>(own + g.part) + ((int64_t)t * g.splits + split) * T * T;
+  P::each(acc, [&](int i, int j, const f32x4& v) {
+    *reinterpret_cast<f32x4*>(out + i * T + j) = v;
+  });
+}
+
+// Adds S's partial sums in order, and makes it a pair.  `unit` 0: X is normalised here: the factor
+// 1 / (|X| + eps) comes from the trace, which every workgroup adds up for itself in the same order
+// (n numbers a split, from L2).  Otherwise the factor is `unit`.
+template <int T>
+__global__ __launch_bounds__(kThreads) void dora_orthogonal_gather(const Groups a, float eps,
+                                                                   float unit, float to,
+                                                                   uint8_t* ws) {
+  constexpr int kE = 32, kSide = T / kE;
+  __shared__ float tile[kE][kE + 1];
+  __shared__ float lds[kThreads / 64];
+  __shared__ uint32_t lds_most[kThreads / 64];
+  const uint32_t id = blockIdx.x;
+  const Group& g = a.g[group_of(a, id)];
+  const int nt = g.nt / T, tiles = tri(nt);
+  int rest = (int)(id - g.from);
+  const int piece = rest % (kSide * kSide);
+  rest /= kSide * kSide;
+  const int t = rest % tiles, u = rest / tiles;
+  int ti, tj;
+  tri_tile(t, nt, ti, tj);
+  uint8_t* own = ws + g.base + (int64_t)u * g.stride;
+  const float* part = reinterpret_cast<const float*>(own + g.part);
+  float r = unit;
+  if (unit == 0.f) {
+    float sum[1] = {0.f};
+    for (int i = threadIdx.x; i < g.n; i += kThreads) {
+      const float* d = part + (int64_t)diagonal_tile(i / T, nt) * g.splits * T * T + (i % T) * (T + 1);
+      for (int s = 0; s < g.splits; ++s) sum[0] += d[(int64_t)s * T * T];
+    }
+    block_sum<kThreads / 64, 1>(sum, lds);
+    const int e = exponent_of(reinterpret_cast<const uint32_t*>(own + g.most), g.blocks, lds_most);
+    r = 1.f / (sqrtf(sum[0]) + ldexpf(eps, e));
+  }
+  if (piece == 0 && t == 0 && threadIdx.x == 0) *reinterpret_cast<float*>(own + g.scale) = r;
+  const int pi = piece / kSide * kE, pj = piece % kSide * kE;
+  if (ti == tj && pj < pi) return;   // (the same for the whole workgroup)
+  const int i = threadIdx.x / 8, j = threadIdx.x % 8 * 4;
+  const float* p = part + (int64_t)t * g.splits * T * T + (pi + i) * T + pj + j;
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  for (int s = 0; s < g.splits; ++s) v += *reinterpret_cast<const f32x4*>(p + (int64_t)s * T * T);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) v[q] = v[q] * r * r * to;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) tile[i][j + q] = v[q];
+  __syncthreads();
+  const bool diagonal = ti == tj && pi == pj;
+  if (diagonal) {   // the upper half's values on both sides
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (j + q < i) v[q] = tile[j + q][i];
+  }
+  f16* s = reinterpret_cast<f16*>(own + g.sq[0]);
+  const int64_t ld = 2 * (int64_t)g.nt;
+  const int64_t row = (int64_t)ti * T + pi, col = (int64_t)tj * T + pj;
+  store_pair4(s + (row + i) * ld, col + j, v);
+  if (diagonal) return;
+  f32x4 w;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) w[q] = tile[j + q][i];
+  store_pair4(s + (col + i) * ld, row + j, w);
+}
+
+// A symmetric product of two n x n pairs, or of two such products of one launch (`both`).
+//   POLY: out = alpha (left right) + beta left + gamma 1, left and right both S
+//   otherwise out = alpha (left right)
+// `flat`: out's rows hold all hi, then all lo, as the last product wants them.
+struct Square {
+  int left, right, out;      // of sq
+  float alpha, beta, gamma;
+  int flat;
+};
+struct Squares {
+  Groups groups;
+  uint32_t total, half;      // workgroups; where the second product starts (total: there is none)
+  Square q[2];
+};
+template <int T, int RING, bool POLY>
+__global__ __launch_bounds__(kThreads) void dora_orthogonal_square(const Squares a, uint8_t* ws) {
+  using P = Product<T, RING, true>;
+  __shared__ __attribute__((aligned(1024))) uint8_t sm[P::kLds];
+  uint32_t id = by_xcd(blockIdx.x, a.total);
+  const Square& q = a.q[id >= a.half ? 1 : 0];
+  if (id >= a.half) id -= a.half;
+  const Group& g = a.groups.g[group_of(a.groups, id)];
+  const int nt = g.nt / T, tiles = tri(nt);
+  const int rest = (int)(id - g.from);
+  const int t = rest % tiles, u = rest / tiles;
+  int ti, tj;
+  tri_tile(t, nt, ti, tj);
+  uint8_t* own = ws + g.base + (int64_t)u * g.stride;
+  const int64_t ld = (int64_t)g.nt * 4;
+  const int stages = (int)(ld / kRowBytes);
+  const uint8_t* left = own + g.sq[q.left];
+  f32x16 acc[P::kB][P::kB];
+  P::run(sm, Side{left + (int64_t)ti * T * ld, ld, stages},
+         Side{own + g.sq[q.right] + (int64_t)tj * T * ld, ld, stages}, 0, stages, acc);
+  f16* out = reinterpret_cast<f16*>(own + g.sq[q.out]);
+  const int64_t le = ld / 2;
+  P::each(acc, [&](int ii, int jj, f32x4 v) {
+    const int i = ti * T + ii, j = tj * T + jj;
+    if (ti == tj && jj + 3 < ii) return;   // below the diagonal: the mirror of what is above
+    v *= q.alpha;
+    if (POLY) {
+      const f32x4 s = load_pair4(reinterpret_cast<const f16*>(left) + (int64_t)i * le, j);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[e] = fmaf(q.beta, s[e], v[e]);
+        if (i == j + e && i < g.n) v[e] += q.gamma;
+      }
+    }
+    if (q.flat) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (ti == tj && jj + e < ii) continue;
+        f16 h, l;
+        split(v[e], h, l);
+        f16* at = out + (int64_t)i * le + j + e;
+        f16* mirror = out + (int64_t)(j + e) * le + i;
+        at[0] = mirror[0] = h;
+        at[g.nt] = mirror[g.nt] = l;
+      }
+      return;
+    }
+    if (ti == tj && jj < ii + 1) {   // the four across the diagonal, one by one
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (jj + e < ii) continue;
+        f16 h, l;
+        split(v[e], h, l);
+        f16* at = out + (int64_t)i * le + pair_at(j + e);
+        f16* mirror = out + (int64_t)(j + e) * le + pair_at(i);
+        at[0] = mirror[0] = h;
+        at[kPairBlock] = mirror[kPairBlock] = l;
+      }
+      return;
+    }
+    store_pair4(out + (int64_t)i * le, j, v);
+    store_pair_mirror(out + (int64_t)j * le, le, i, v);
+  });
+}
+
+// ---- Q X ----------------------------------------------------------------------------------------
+// Where a matrix's result goes: `out`, or the parameter (and its master) that it updates.
+struct Sink {
+  void* out;
+  float* master;
+  float rate;          // lr times the matrix's own factor
+};
+struct Sinks {
+  Groups groups;       // `from`: unused
+  int count, first;
+  uint32_t total;
+  uint32_t from[kMaxMatrices];
+  Sink s[kMaxMatrices];
+  int q;               // which of sq is Q
+  float unit;          // 1 / Q's factor
+  bool second;         // the X formed on the way
+  float decay, rest;   // 1 - lr weight_decay and what its rounding leaves
+};
+enum Result { kOut, kParam, kMaster };
+
+template <int T, int RING, bool PAIR>
+__device__ __forceinline__ void last_product(uint8_t* sm, const Group& g, uint8_t* own, int q,
+                                             bool second, int64_t row0, int64_t col0,
+                                             f32x16 (&acc)[T / 64][T / 64]) {
+  // Q's rows are pairs where X's are; else all hi and then all lo against X twice
+  const int64_t ld_q = (int64_t)g.nt * 4, ld_x = (int64_t)g.nt * (PAIR ? 4 : 2);
+  const int sq = (int)(ld_q / kRowBytes), sx = (int)(ld_x / kRowBytes);
+  const uint8_t* x = own + (second ? g.xt2 : g.xt);
+  const uint8_t* qp = own + g.sq[q];
+  const Side qs = {qp + (g.tall ? col0 : row0) * ld_q, ld_q, sq};
+  const Side xs = {x + (g.tall ? row0 : col0) * ld_x, ld_x, sx};
+  Product<T, RING, PAIR>::run(sm, g.tall ? xs : qs, g.tall ? qs : xs, 0, sq, acc);
+}
+
+template <int T, int RING, bool PAIR, bool BF, Result WHAT>
+__global__ __launch_bounds__(kThreads) void dora_orthogonal_apply(const Sinks a, uint8_t* ws) {
+  using P = Product<T, RING, PAIR>;
+  __shared__ __attribute__((aligned(1024))) uint8_t sm[P::kLds];
+  using E = Elem<BF>;
+  const uint32_t id = by_xcd(blockIdx.x, a.total);
+  const int u = matrix_of(a.from, a.count, id);
+  const Group& g = a.groups.g[group_of_matrix(a.groups, a.first + u)];
+  uint8_t* own = ws + g.base + (int64_t)(a.first + u - g.first) * g.stride;
+  const int rows = g.tall ? g.m : g.n, cols = g.tall ? g.n : g.m;
+  const int down = ((g.tall ? g.m : g.n) + T - 1) / T, across = (cols + T - 1) / T;
+  const int t = (int)(id - a.from[u]);
+  // the tiles that share rows or columns of the long side next to each other
+  const int64_t row0 = (int64_t)(g.tall ? t / across : t % down) * T;
+  const int64_t col0 = (int64_t)(g.tall ? t % across : t / down) * T;
+  f32x16 acc[P::kB][P::kB];
+  last_product<T, RING, PAIR>(sm, g, own, a.q, a.second, row0, col0, acc);
+  const Sink s = a.s[u];
+  const float r = *reinterpret_cast<const float*>(own + g.scale) * a.unit *
+                  (WHAT == kOut ? 1.f : -s.rate);
+  typename E::T* out = reinterpret_cast<typename E::T*>(s.out);
+  P::each(acc, [&](int ii, int jj, f32x4 v) {
+    const int64_t i = row0 + ii, j = col0 + jj;
+    if (i >= rows || j >= cols) return;
+    const int64_t at = i * cols + j;
+    const int here = (int)min((int64_t)4, cols - j);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (e >= here) break;
+      float x = v[e] * r;
+      if (WHAT != kOut) {
+        const float p = WHAT == kMaster ? s.master[at + e] : E::get(out + at + e);
+        x = fmaf(p, a.decay, fmaf(p, a.rest, x));
+        if (WHAT == kMaster) s.master[at + e] = x;
+      }
+      E::put(out + at + e, x);
+    }
+  });
+}
+
+// Q X as pairs in both orders, in place of X from here on.
+template <int T, int RING, bool PAIR>
+__global__ __launch_bounds__(kThreads) void dora_orthogonal_between(const Groups a, uint32_t total,
+                                                                    int q, float unit, bool second,
+                                                                    uint8_t* ws) {
+  using P = Product<T, RING, PAIR>;
+  __shared__ __attribute__((aligned(1024))) uint8_t sm[P::kLds];
+  const uint32_t id = by_xcd(blockIdx.x, total);
+  Group g = a.g[group_of(a, id)];
+  const int down = g.nt / T, tiles = down * (g.mt / T);
+  const int rest = (int)(id - g.from);
+  const int t = rest % tiles, u = rest / tiles;
+  uint8_t* own = ws + g.base + (int64_t)u * g.stride;
+  g.tall = false;   // rows are n's whatever the matrix's order
+  const int64_t row0 = (int64_t)(t % down) * T, col0 = (int64_t)(t / down) * T;
+  f32x16 acc[P::kB][P::kB];
+  last_product<T, RING, PAIR>(sm, g, own, q, second, row0, col0, acc);
+  const float r = *reinterpret_cast<const float*>(own + g.scale) * unit;
+  f16* xk = reinterpret_cast<f16*>(own + (second ? g.xk : g.xk2));
+  f16* xt = reinterpret_cast<f16*>(own + (second ? g.xt : g.xt2));
+  P::each(acc, [&](int ii, int jj, f32x4 v) {
+    v *= r;
+    store_pair4(xk + (row0 + ii) * 2 * g.mt, col0 + jj, v);
+    store_pair_mirror(xt + (col0 + jj) * 2 * g.nt, 2 * g.nt, row0 + ii, v);
+  });
+}
+
+static_assert(sizeof(Sinks) <= 4000 && sizeof(Sources) <= 4000 && sizeof(Squares) <= 4000,
+              "kernel arguments");
+
+// ---- host: the iteration's numbers ------------------------------------------------------------
+constexpr int kMaxSteps = 16;
+
+double largest(double l, double (*f)(double, const double*), const double* abc, double q1, double q2) {
+  double m = std::max(std::fabs(f(0.0, abc)), std::fabs(f(l, abc)));
+  for (double x : {q1, q2})
+    if (x > 0 && x < l) m = std::max(m, std::fabs(f(x, abc)));
+  return m;
+}
+double p_of(double x, const double* k) { return k[0] + x * (k[1] + x * k[2]); }
+double r_of(double x, const double* k) { return x * p_of(x, k); }
+double s_of(double x, const double* k) { return x * p_of(x, k) * p_of(x, k); }
+// Real roots of u + v x + w x^2 (NaN, which no comparison takes, where there are none).
+void roots(double u, double v, double w, double* x) {
+  if (w == 0) {
+    x[0] = x[1] = -u / v;
+    return;
+  }
+  const double d = std::sqrt(v * v - 4 * u * w);
+  x[0] = (-v + d) / (2 * w);
+  x[1] = (-v - d) / (2 * w);
+}
+
+// Powers of two that keep every matrix inside half precision: its eigenvalues are polynomials of
+// those of the first S, which lie in [0, 1], so their bounds are known beforehand, and no entry of a
+// symmetric matrix is larger than its largest eigenvalue.
+struct Numbers {
+  int steps;
+  double abc[kMaxSteps][3];
+  int s[kMaxSteps + 1], p[kMaxSteps], r[kMaxSteps], q[kMaxSteps];   // exponents
+  int x[kMaxSteps + 1];
+  bool anew[kMaxSteps + 1];   // Q X is formed before step k, and S anew from it
+  int times;                  // how often
+  bool good;
+};
+int exponent(double bound) {
+  // 2^14 of half precision's 2^16: roundings may pass the bound a little
+  return 14 - (int)std::ceil(std::log2(std::max(bound, 0x1p-24)));
+}
+Numbers numbers(const double* coefficients, int steps, bool exact) {
+  Numbers z = {};
+  z.steps = steps;
+  z.good = false;
+  // the factor on S's rounding up to which Q is kept: results of 8 bits, or of 24
+  const double most = exact ? 1024.0 : 65536.0;
+  double l = 1.0, q = 1.0, grown = 0.0, gain = 1.0;
+  for (int k = 0; k < steps; ++k) {
+    const double* abc = z.abc[k];
+    for (int i = 0; i < 3; ++i) {
+      z.abc[k][i] = coefficients[3 * k + i];
+      if (!std::isfinite(abc[i])) return z;
+    }
+    const double rise = abc[0] != 0 ? std::fabs(abc[1] / abc[0]) * gain : 0.0;
+    if (k > 0 && grown + rise > most) {
+      z.anew[k] = true;
+      ++z.times;
+      grown = 0.0;
+      gain = q = 1.0;
+    }
+    grown += abc[0] != 0 ? std::fabs(abc[1] / abc[0]) * gain : 0.0;
+    gain *= abc[0] * abc[0];
+    double t[2], top;
+    top = -abc[1] / (2 * abc[2]);
+    const double p = largest(l, p_of, abc, top, top);
+    roots(abc[0], 2 * abc[1], 3 * abc[2], t);
+    const double r = largest(l, r_of, abc, t[0], t[1]);
+    roots(abc[0], 3 * abc[1], 5 * abc[2], t);
+    const double next = largest(l, s_of, abc, t[0], t[1]);
+    q *= p;
+    if (!(p < 0x1p30) || !(q < 0x1p30) || !(r < 0x1p30) || !(next < 0x1p30)) return z;
+    z.s[k] = exponent(l);
+    z.x[k] = exponent(std::sqrt(l));
+    z.p[k] = exponent(p);
+    z.r[k] = exponent(r);
+    z.q[k] = exponent(q);
+    l = std::max(next, 0x1p-24);
+    z.s[k + 1] = exponent(l);
+  }
+  z.good = true;
+  return z;
+}
+
+// ---- host: which matrices share launches -------------------------------------------------------
+struct Item {
+  int64_t rows, cols;
+  Source from;
+  Sink to;
+};
+struct Kind {
+  bool pair;      // X is hi + lo
+  int times;      // how often Q X is formed on the way
+};
+struct Pass {
+  int tile;
+  std::vector<int> order;   // items, group by group
+  Groups groups;
+  size_t bytes;
+};
+
+int64_t padded(int64_t v, int to) { return (v + to - 1) / to * to; }
+
+void lay_out(Group& g, const Kind& k, int tile) {
+  g.nt = (int)padded(g.n, tile);
+  g.mt = (int)padded(g.m, kPad);
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t here = at;
+    at += padded(bytes, 256);
+    return here;
+  };
+  const int64_t x = (int64_t)g.nt * g.mt * (k.pair || k.times > 1 ? 4 : 2);
+  g.xk = take(x);
+  g.xt = take(x);
+  g.xk2 = g.xt2 = 0;
+  if (k.times) {
+    g.xk2 = take((int64_t)g.nt * g.mt * 4);
+    g.xt2 = take((int64_t)g.nt * g.mt * 4);
+  }
+  for (int64_t& s : g.sq) s = take((int64_t)g.nt * g.nt * 4);
+  g.part = take((int64_t)tri(g.nt / tile) * g.splits * tile * tile * 4);
+  g.most = take((int64_t)g.blocks * 4);
+  g.scale = take(4);
+  g.stride = at;
+}
+
+// Tiles of 128 where they fill the chip (a CU holds two workgroups of them): 24 matrices of 384
+// and as many again of another shape are 288. Else of 64, which have four times as many.
+constexpr int64_t kEnoughTiles = 256;
+constexpr int64_t kWantSums = 768;   // workgroups of the sums over m
+
+std::vector<Pass> passes(const std::vector<Item>& items, const Kind& kind) {
+  auto small = [](const Item& i) { return std::min(i.rows, i.cols); };
+  std::vector<int> order((size_t)items.size());
+  for (size_t i = 0; i < items.size(); ++i) order[i] = (int)i;
+  order.erase(std::remove_if(order.begin(), order.end(),
+                             [&](int i) { return small(items[i]) == 0; }),
+              order.end());
+  std::stable_sort(order.begin(), order.end(), [&](int a, int b) {
+    const Item &x = items[a], &y = items[b];
+    if (small(x) != small(y)) return small(x) < small(y);
+    return x.rows != y.rows ? x.rows < y.rows : x.cols < y.cols;
+  });
+  std::vector<Pass> out;
+  for (size_t at = 0; at < order.size();) {
+    // matrices of one n choose their tile together
+    size_t same = at;
+    const int64_t n = small(items[order[at]]);
+    while (same < order.size() && small(items[order[same]]) == n) ++same;
+    const int64_t wide = (int64_t)(same - at) * tri((int)((n + 127) / 128));
+    const int tile = n > 64 && wide >= kEnoughTiles ? 128 : 64;
+    while (at < same) {
+      size_t end = at;
+      const Item& one = items[order[at]];
+      while (end < same && items[order[end]].rows == one.rows && items[order[end]].cols == one.cols)
+        ++end;
+      if (out.empty() || out.back().tile != tile || out.back().groups.count == kMaxGroups) {
+        out.emplace_back();
+        out.back().tile = tile;
+        out.back().groups.count = 0;
+      }
+      Pass& p = out.back();
+      Group& g = p.groups.g[p.groups.count++];
+      g = Group{};
+      g.n = (int)n;
+      g.m = (int)std::max(one.rows, one.cols);
+      g.tall = one.rows > one.cols;
+      g.count = (int)(end - at);
+      g.first = (int)p.order.size();
+      p.order.insert(p.order.end(), order.begin() + at, order.begin() + end);
+      at = end;
+    }
+  }
+  for (Pass& p : out) {
+    int64_t tiles = 0;
+    for (int i = 0; i < p.groups.count; ++i) {
+      const Group& g = p.groups.g[i];
+      tiles += (int64_t)g.count * tri((g.n + p.tile - 1) / p.tile);
+    }
+    int64_t base = 0;
+    for (int i = 0; i < p.groups.count; ++i) {
+      Group& g = p.groups.g[i];
+      const int64_t stages = padded(g.m, kPad) / 64;   // at least four to a part
+      g.splits = (int)std::max<int64_t>(
+          1, std::min({kWantSums / std::max<int64_t>(tiles, 1), stages / 4, (int64_t)kMaxSplits}));
+      g.blocks = (int)std::min<int64_t>(kMaxBlocks, ((int64_t)g.n * g.m + 8191) / 8192);
+      lay_out(g, kind, p.tile);
+      g.base = base;
+      base += g.stride * g.count;
+    }
+    p.bytes = (size_t)base;
+  }
+  return out;
+}
+
+// Sets each group's first workgroup and returns their number; size(group): of one matrix.
+template <typename Size>
+int64_t spread(Groups& a, Size size) {
+  int64_t at = 0;
+  for (int i = 0; i < a.count; ++i) {
+    a.g[i].from = (uint32_t)at;
+    at += size(a.g[i]) * a.g[i].count;
+  }
+  return at;
+}
+
+// ---- host: launches ------------------------------------------------------------------------------
+struct Call {
+  bool x_bf, moment, out_bf;
+  Result what;
+  float eps, mu, nu, decay, rest;
+  int nesterov;
+};
+
+// (an argument's type is the kernel's, not what is passed)
+template <typename T>
+struct Identity {
+  using type = T;
+};
+template <typename T>
+using identity_t = typename Identity<T>::type;
+
+template <typename... Args>
+hipError_t launch(const char* label, void (*kernel)(Args...), int64_t blocks, hipStream_t st,
+                  identity_t<Args>... args) {
+  LaunchTimer timer(label, st);
+  hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(kThreads), 0, st, args...);
+  return hipGetLastError();
+}
+
+// Launches over the matrices of a pass whose addresses the kernel takes; fill(slot, item).
+template <typename A, typename Size, typename Fill, typename Go>
+hipError_t by_matrix(const Pass& p, A& a, Size size, Fill fill, Go go) {
+  a.groups = p.groups;
+  const int all = (int)p.order.size();
+  for (int first = 0; first < all;) {
+    int64_t blocks = 0;
+    a.first = first;
+    a.count = 0;
+    for (; first < all && a.count < kMaxMatrices; ++first) {
+      int g = 0;
+      while (g + 1 < p.groups.count && first >= p.groups.g[g + 1].first) ++g;
+      const int64_t n = size(p.groups.g[g]);
+      if (a.count && blocks + n > launch_blocks(kThreads)) break;
+      a.from[a.count] = (uint32_t)blocks;
+      fill(a.count++, p.order[first]);
+      blocks += n;
+    }
+    if (hipError_t e = go(blocks)) return e;
+  }
+  return hipSuccess;
+}
+
+#define ORTHO_TRY(expr)                              \
+  do {                                               \
+    if (hipError_t e_ = (expr)) return e_;           \
+  } while (0)
+
+template <int T>
+struct Engine {
+  static constexpr int kRing = T == 128 ? 2 : 4;
+  const Pass& p;
+  const std::vector<Item>& items;
+  const Numbers& z;
+  const Call& c;
+  bool pair, second = false;
+  uint8_t* ws;
+  hipStream_t st;
+
+  template <bool BF, bool MOMENT>
+  hipError_t halves() {
+    Sources a;
+    a.mu = c.mu;
+    a.nu = c.nu;
+    a.nesterov = c.nesterov;
+    auto fill = [&](int slot, int item) { a.s[slot] = items[item].from; };
+    ORTHO_TRY(by_matrix(p, a, [](const Group& g) { return (int64_t)g.blocks; }, fill,
+                        [&](int64_t blocks) {
+                          return launch("orthogonal_most", dora_orthogonal_most<BF, MOMENT>, blocks,
+                                        st, a, ws);
+                        }));
+    auto kernel = pair ? dora_orthogonal_halves<BF, MOMENT, true> : dora_orthogonal_halves<BF, MOMENT, false>;
+    return by_matrix(p, a, [](const Group& g) { return (int64_t)(g.nt / 64) * (g.mt / 64); }, fill,
+                     [&](int64_t blocks) {
+                       return launch("orthogonal_halves", kernel, blocks, st, a, ws);
+                     });
+  }
+  hipError_t start() {
+    if (c.moment) return c.x_bf ? halves<true, true>() : halves<false, true>();
+    return c.x_bf ? halves<true, false>() : halves<false, false>();
+  }
+  hipError_t gram(float unit, int to) {
+    Groups a = p.groups;
+    int64_t blocks = spread(a, [](const Group& g) { return (int64_t)tri(g.nt / T) * g.splits; });
+    auto kernel = pair ? dora_orthogonal_gram<T, kRing, true> : dora_orthogonal_gram<T, kRing, false>;
+    ORTHO_TRY(launch("orthogonal_gram", kernel, blocks, st, a, (uint32_t)blocks, second, ws));
+    blocks = spread(a, [](const Group& g) { return (int64_t)tri(g.nt / T) * (T / 32) * (T / 32); });
+    return launch("orthogonal_gather", dora_orthogonal_gather<T>, blocks, st, a, c.eps, unit,
+                  std::ldexp(1.f, to), ws);
+  }
+  template <bool POLY>
+  hipError_t squares(Square one, const Square* two = nullptr) {
+    Squares a;
+    a.groups = p.groups;
+    const int64_t blocks = spread(a.groups, [](const Group& g) { return (int64_t)tri(g.nt / T); });
+    a.half = (uint32_t)blocks;
+    a.total = (uint32_t)(two ? 2 * blocks : blocks);
+    a.q[0] = one;
+    a.q[1] = two ? *two : one;
+    return launch(POLY ? "orthogonal_poly" : "orthogonal_square",
+                  dora_orthogonal_square<T, kRing, POLY>, a.total, st, a, ws);
+  }
+  hipError_t between(int q, int e) {
+    Groups a = p.groups;
+    const int64_t blocks =
+        spread(a, [](const Group& g) { return (int64_t)(g.nt / T) * (g.mt / T); });
+    auto kernel = pair ? dora_orthogonal_between<T, kRing, true> : dora_orthogonal_between<T, kRing, false>;
+    ORTHO_TRY(launch("orthogonal_between", kernel, blocks, st, a, (uint32_t)blocks, q,
+                     std::ldexp(1.f, e), second, ws));
+    pair = true;
+    second = !second;
+    return hipSuccess;
+  }
+  template <bool PAIR, bool BF, Result WHAT>
+  hipError_t apply(int q, int e) {
+    Sinks a;
+    a.q = q;
+    a.unit = std::ldexp(1.f, -e);
+    a.second = second;
+    a.decay = c.decay;
+    a.rest = c.rest;
+    auto size = [](const Group& g) { return (int64_t)((g.n + T - 1) / T) * ((g.m + T - 1) / T); };
+    auto fill = [&](int slot, int item) { a.s[slot] = items[item].to; };
+    return by_matrix(p, a, size, fill, [&](int64_t blocks) {
+      a.total = (uint32_t)blocks;
+      return launch("orthogonal_apply", dora_orthogonal_apply<T, kRing, PAIR, BF, WHAT>, blocks, st,
+                    a, ws);
+    });
+  }
+  template <bool PAIR>
+  hipError_t finish(int q, int e) {
+    if (c.what == kMaster) return apply<PAIR, true, kMaster>(q, e);
+    if (c.what == kParam)
+      return c.out_bf ? apply<PAIR, true, kParam>(q, e) : apply<PAIR, false, kParam>(q, e);
+    return c.out_bf ? apply<PAIR, true, kOut>(q, e) : apply<PAIR, false, kOut>(q, e);
+  }
+
+  hipError_t run() {
+    ORTHO_TRY(start());
+    ORTHO_TRY(gram(0.f, z.s[0]));
+    constexpr int S = 0, P = 1, R = 2, Qa = 3, Qb = 4;
+    int q = -1, eq = 0;   // Q: P of the first step, so it is written where Q goes
+    auto two = [](int e) { return std::ldexp(1.f, e); };
+    for (int k = 0; k < z.steps; ++k) {
+      if (z.anew[k]) {
+        ORTHO_TRY(between(q, z.x[k] - eq));
+        ORTHO_TRY(gram(two(-z.x[k]), z.s[k]));
+        q = -1;
+      }
+      const bool last = k + 1 == z.steps || z.anew[k + 1];   // Q meets X next
+      const int flat = last && !pair;
+      const int pi = q < 0 ? Qa : P;
+      const double* abc = z.abc[k];
+      Square poly = {S, S, pi, (float)std::ldexp(abc[2], z.p[k] - 2 * z.s[k]),
+                     (float)std::ldexp(abc[1], z.p[k] - z.s[k]), (float)std::ldexp(abc[0], z.p[k]),
+                     q < 0 ? flat : 0};
+      ORTHO_TRY(squares<true>(poly));
+      const Square ps = {pi, S, R, two(z.r[k] - z.p[k] - z.s[k]), 0.f, 0.f, 0};
+      if (q < 0) {
+        q = Qa;
+        eq = z.p[k];
+        if (!last) ORTHO_TRY(squares<false>(ps));
+      } else {
+        const int to = q == Qa ? Qb : Qa;
+        const Square pq = {P, q, to, two(z.q[k] - z.p[k] - eq), 0.f, 0.f, flat};
+        ORTHO_TRY(squares<false>(pq, last ? nullptr : &ps));
+        q = to;
+        eq = z.q[k];
+      }
+      if (!last)
+        ORTHO_TRY(squares<false>(Square{pi, R, S, two(z.s[k + 1] - z.p[k] - z.r[k]), 0.f, 0.f, 0}));
+    }
+    return pair ? finish<true>(q, eq) : finish<false>(q, eq);
+  }
+};
+
+hipError_t run_all(const std::vector<Item>& items, const Kind& kind, const Numbers& z, const Call& c,
+                   void* ws, hipStream_t st) {
+  for (const Pass& p : passes(items, kind)) {
+    uint8_t* w = reinterpret_cast<uint8_t*>(ws);
+    if (p.tile == 128) {
+      Engine<128> e{p, items, z, c, kind.pair, false, w, st};
+      ORTHO_TRY(e.run());
+    } else {
+      Engine<64> e{p, items, z, c, kind.pair, false, w, st};
+      ORTHO_TRY(e.run());
+    }
+  }
+  return hipSuccess;
+}
+
+size_t bytes_of(const std::vector<Item>& items, const Kind& kind) {
+  size_t most = 0;
+  for (const Pass& p : passes(items, kind)) most = std::max(most, p.bytes);
+  return most;
+}
+
+// ---- host: arguments -----------------------------------------------------------------------------
+bool dtype_ok(int dt) { return dt == DORA_F32 || dt == DORA_BF16; }
+size_t esize(int dt) { return dt == DORA_BF16 ? 2 : 4; }
+
+constexpr int64_t kMaxLong = int64_t(1) << 20, kMaxShort = 16384;
+constexpr int64_t kMaxCount = int64_t(1) << 20;
+
+bool sides_ok(int64_t rows, int64_t cols) {
+  return rows >= 0 && cols >= 0 && std::max(rows, cols) <= kMaxLong &&
+         std::min(rows, cols) <= kMaxShort;
+}
+
+int check_iteration(const dora_newton_schulz* o, bool exact, Numbers& z) {
+  if (!(o->eps >= 0x1p-100) || !std::isfinite(o->eps) || !std::isfinite((float)o->eps) || o->steps < 1 ||
+      o->steps > kMaxSteps)
+    return DORA_ERR_FLAGS;
+  if (!o->coefficients) return DORA_ERR_NULL;
+  z = numbers(o->coefficients, o->steps, exact);
+  return z.good ? DORA_OK : DORA_ERR_FLAGS;
+}
+
+// What a call's types say of the precision: float32 results or states need it, bf16 ones do not.
+struct Setup {
+  Numbers z;
+  Kind kind;
+  std::vector<Item> items;
+};
+
+int set_up(const dora_orthogonalize_options* o, const dora_matrix* a, int64_t count, Setup& s) {
+  if (!o) return DORA_ERR_NULL;
+  if (!dtype_ok(o->dtype)) return DORA_ERR_DTYPE;
+  if (o->reserved != 0) return DORA_ERR_FLAGS;
+  const bool exact = o->dtype == DORA_F32;
+  DORA_CHECK(check_iteration(&o->iteration, exact, s.z));
+  if (count < 0 || count >= kMaxCount) return DORA_ERR_SHAPE;
+  if (count > 0 && !a) return DORA_ERR_NULL;
+  s.kind = {exact, s.z.times};
+  s.items.resize((size_t)count);
+  for (int64_t i = 0; i < count; ++i) {
+    if (!sides_ok(a[i].rows, a[i].cols)) return DORA_ERR_SHAPE;
+    s.items[i] = {a[i].rows, a[i].cols, {a[i].x, nullptr}, {a[i].out, nullptr, 0.f}};
+  }
+  return DORA_OK;
+}
+
+int set_up(const dora_muon_options* o, const dora_muon_tensor* a, int64_t count, Setup& s, bool& master) {
+  if (!o) return DORA_ERR_NULL;
+  if (!dtype_ok(o->param_dtype) || !dtype_ok(o->grad_dtype)) return DORA_ERR_DTYPE;
+  if (o->reserved != 0 || (o->nesterov != 0 && o->nesterov != 1) || !std::isfinite(o->lr) ||
+      !std::isfinite(o->weight_decay) || !(o->momentum >= 0 && o->momentum < 1))
+    return DORA_ERR_FLAGS;
+  if (count < 0 || count >= kMaxCount) return DORA_ERR_SHAPE;
+  if (count > 0 && !a) return DORA_ERR_NULL;
+  bool any = false;
+  master = false;
+  s.items.resize((size_t)count);
+  for (int64_t i = 0; i < count; ++i) {
+    if (!sides_ok(a[i].rows, a[i].cols)) return DORA_ERR_SHAPE;
+    if (!std::isfinite(a[i].scale)) return DORA_ERR_FLAGS;
+    s.items[i] = {a[i].rows, a[i].cols, {a[i].grad, a[i].momentum},
+                  {a[i].param, a[i].master, (float)(o->lr * a[i].scale)}};
+    if (a[i].rows == 0 || a[i].cols == 0) continue;
+    if (!any) master = a[i].master != nullptr;
+    any = true;
+    if ((a[i].master != nullptr) != master) return DORA_ERR_NULL;
+  }
+  if (master && o->param_dtype != DORA_BF16) return DORA_ERR_DTYPE;
+  const bool exact = master || o->param_dtype == DORA_F32;
+  DORA_CHECK(check_iteration(&o->iteration, exact, s.z));
+  s.kind = {true, s.z.times};
+  return DORA_OK;
+}
+
+}  // namespace
+}  // namespace dora
+
+using namespace dora;
+
+extern "C" {
+
+DORA_API size_t dora_orthogonalize_workspace_bytes(const dora_matrix* matrices, int64_t count,
+                                                   const dora_orthogonalize_options* options) {
+  try {
+    Setup s;
+    return set_up(options, matrices, count, s) == DORA_OK ? bytes_of(s.items, s.kind) : 0;
+  } catch (...) {   // no memory on the host
+    return 0;
+  }
+}
+
+DORA_API int dora_orthogonalize(const dora_matrix* matrices, int64_t count,
+                                const dora_orthogonalize_options* options, void* ws, size_t ws_bytes,
+                                void* hip_stream) {
+  try {
+    Setup s;
+    DORA_CHECK(set_up(options, matrices, count, s));
+    const size_t e = esize(options->dtype);
+    for (int64_t i = 0; i < count; ++i) {
+      const bool none = matrices[i].rows == 0 || matrices[i].cols == 0;
+      DORA_CHECK(check_elem(matrices[i].x, e, none));
+      DORA_CHECK(check_elem(matrices[i].out, e, none));
+    }
+    DORA_CHECK(check_ws(ws, ws_bytes, bytes_of(s.items, s.kind)));
+    Call c = {};
+    c.x_bf = c.out_bf = options->dtype == DORA_BF16;
+    c.what = kOut;
+    c.eps = (float)options->iteration.eps;
+    HIP_TRY(run_all(s.items, s.kind, s.z, c, ws, reinterpret_cast<hipStream_t>(hip_stream)));
+    return DORA_OK;
+  } catch (...) {
+    return DORA_ERR_HIP;
+  }
+}
+
+DORA_API size_t dora_muon_workspace_bytes(const dora_muon_tensor* tensors, int64_t count,
+                                          const dora_muon_options* options) {
+  try {
+    Setup s;
+    bool master;
+    return set_up(options, tensors, count, s, master) == DORA_OK ? bytes_of(s.items, s.kind) : 0;
+  } catch (...) {
+    return 0;
+  }
+}
+
+DORA_API int dora_muon_step(const dora_muon_tensor* tensors, int64_t count,
+                            const dora_muon_options* options, void* ws, size_t ws_bytes,
+                            void* hip_stream) {
+  try {
+    Setup s;
+    bool master;
+    DORA_CHECK(set_up(options, tensors, count, s, master));
+    const dora_muon_options& o = *options;
+    for (int64_t i = 0; i < count; ++i) {
+      const dora_muon_tensor& t = tensors[i];
+      const bool none = t.rows == 0 || t.cols == 0;
+      DORA_CHECK(check_elem(t.param, esize(o.param_dtype), none));
+      DORA_CHECK(check_elem(t.grad, esize(o.grad_dtype), none));
+      DORA_CHECK(check_elem(t.momentum, 4, none));
+      DORA_CHECK(check_elem(t.master, 4, true));
+    }
+    DORA_CHECK(check_ws(ws, ws_bytes, bytes_of(s.items, s.kind)));
+    Call c = {};
+    c.x_bf = o.grad_dtype == DORA_BF16;
+    c.out_bf = o.param_dtype == DORA_BF16;
+    c.moment = true;
+    c.what = master ? kMaster : kParam;
+    c.eps = (float)o.iteration.eps;
+    c.mu = (float)o.momentum;
+    c.nu = (float)(1.0 - o.momentum);
+    c.nesterov = o.nesterov;
+    // what float32 loses of 1 - lr weight_decay beside 1 is added apart
+    const double decay = o.lr * o.weight_decay;
+    c.decay = (float)(1.0 - decay);
+    c.rest = (float)(1.0 - decay - (double)c.decay);
+    HIP_TRY(run_all(s.items, s.kind, s.z, c, ws, reinterpret_cast<hipStream_t>(hip_stream)));
+    return DORA_OK;
+  } catch (...) {
+    return DORA_ERR_HIP;
+  }
+}
+
+}  // extern "C"

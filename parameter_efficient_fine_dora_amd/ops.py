@@ -790,6 +790,178 @@ def dora_adamw(plan, grads, *, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_de
     return norm
 
 
+# Newton-Schulz coefficients that take singular values from 2e-3 to 1 to within [0.68, 1.13]
+NEWTON_SCHULZ = ((3.4445, -4.7750, 2.0315),) * 5
+
+
+def _iteration(coefficients, eps):
+    """The iteration's struct, and the array of coefficients that it points to."""
+    flat = [float(v) for abc in coefficients for v in abc]
+    if any(len(abc) != 3 for abc in coefficients):
+        raise ValueError("coefficients are (a, b, c) for each step")
+    array = (ctypes.c_double * max(len(flat), 1))(*flat)
+    steps = len(flat) // 3
+    return _lib.DoraNewtonSchulz(ctypes.addressof(array), steps, 0, float(eps)), array
+
+
+def dora_orthogonalize(x, *, coefficients=NEWTON_SCHULZ, eps=1e-7, out=None, workspace=None):
+    """The orthogonalised matrix (or matrices) of ``x`` by Newton-Schulz products: x / (|x| + eps),
+    then a x + (b s + c s^2) x with s = x x^T for each (a, b, c) of ``coefficients``.
+
+    x: a contiguous [rows, cols] tensor, a stack [count, rows, cols], or a list of matrices of any
+    sizes, bf16 or float32.  Returns the same kind; ``out`` may be x itself.
+    """
+    many = isinstance(x, (list, tuple))
+    xs = list(x) if many else [x]
+    outs = [None] * len(xs) if out is None else list(out) if many else [out]
+    if len(outs) != len(xs):
+        raise ValueError(f"out has {len(outs)} tensors, expected {len(xs)}")
+    if not xs:
+        return []
+    _need(xs[0], "x[0]" if many else "x")
+    dev, dt = xs[0].device, xs[0].dtype
+    code = _layer_dtype(xs[0])
+    counts = []
+    for i, t in enumerate(xs):
+        name = f"x[{i}]" if many else "x"
+        _need(t, name, dt, None, dev)
+        if t.dim() not in ((2,) if many else (2, 3)):
+            raise ValueError(f"{name} has {t.dim()} dimensions, expected a matrix"
+                             + ("" if many else " or a stack of them"))
+        outs[i] = _out(outs[i], "out", dt, t.shape, dev)
+        if outs[i].data_ptr() != t.data_ptr():
+            _disjoint(outs[i], t, "out", name)
+        counts.append(t.shape[0] if t.dim() == 3 else 1)
+    table = (_lib.DoraMatrix * max(sum(counts), 1))()
+    size, at = xs[0].element_size(), 0
+    for t, o, k in zip(xs, outs, counts):
+        rows, cols = t.shape[-2:]
+        a, b = t.data_ptr(), o.data_ptr()
+        for j in range(k):
+            e = table[at]
+            e.x, e.out, e.rows, e.cols = a + j * rows * cols * size, b + j * rows * cols * size, rows, cols
+            at += 1
+    iteration, _held = _iteration(coefficients, eps)
+    how = _lib.DoraOrthogonalizeOptions(iteration, code, 0)
+    L = _lib.lib()
+    nb = L.dora_orthogonalize_workspace_bytes(table, at, ctypes.byref(how))
+    ws, nb = _some_ws(nb, dev, workspace)
+    _check(L.dora_orthogonalize(table, at, ctypes.byref(how), _ptr(ws), nb, _stream(dev)),
+           "dora_orthogonalize")
+    return outs if many else outs[0]
+
+
+def _disjoint(a, b, name, other):
+    if a.numel() and b.numel():
+        lo, hi = a.data_ptr(), a.data_ptr() + a.numel() * a.element_size()
+        if lo < b.data_ptr() + b.numel() * b.element_size() and b.data_ptr() < hi:
+            raise ValueError(f"{name} must not overlap {other}")
+
+
+class MuonPlan:
+    """The matrices of a step with orthogonalised updates, checked once and kept for the steps that
+    follow.
+
+    params     contiguous matrices of one dtype (bf16 or float32) on one device
+    momenta    float32 tensors of their shapes
+    masters    float32 copies of bf16 parameters, or None
+
+    The plan refers to the tensors and writes through them.  A tensor whose storage was exchanged
+    since is an error at the next step.
+    """
+
+    def __init__(self, params, momenta, *, masters=None):
+        self.params, self.momenta = list(params), list(momenta)
+        self.masters = None if masters is None else list(masters)
+        if not self.params:
+            raise ValueError("params is empty")
+        _need(self.params[0], "params[0]")
+        self.device, self.dtype = self.params[0].device, self.params[0].dtype
+        self.param_code = _layer_dtype(self.params[0])
+        if self.masters is not None and self.dtype != torch.bfloat16:
+            raise ValueError("masters go with bfloat16 params")
+        lists = [("momenta", self.momenta), ("masters", self.masters)]
+        for nm, lst in lists:
+            if lst is not None and len(lst) != len(self.params):
+                raise ValueError(f"{nm} has {len(lst)} tensors, expected {len(self.params)}")
+        self.table = (_lib.DoraMuonTensor * len(self.params))()
+        written = []
+        for i, (e, p) in enumerate(zip(self.table, self.params)):
+            _need(p, f"params[{i}]", self.dtype, None, self.device)
+            if p.dim() != 2:
+                raise ValueError(f"params[{i}] has {p.dim()} dimensions, expected a matrix")
+            e.rows, e.cols = p.shape
+            e.param = p.data_ptr()
+            written.append((p, f"params[{i}]"))
+            for nm, lst in lists:
+                if lst is not None:
+                    _need(lst[i], f"{nm}[{i}]", torch.float32, p.shape, self.device)
+                    written.append((lst[i], f"{nm}[{i}]"))
+            e.momentum = self.momenta[i].data_ptr()
+            e.master = None if self.masters is None else self.masters[i].data_ptr()
+        spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), nm)
+                       for t, nm in written if t.numel())
+        for a, b in zip(spans, spans[1:]):
+            if b[0] < a[1]:
+                raise ValueError(f"{a[2]} and {b[2]} share memory: a step writes both")
+        self._bytes = {}
+
+    def unchanged(self):
+        """Whether every tensor still has the storage it had when the plan was made."""
+        masters = self.masters or [None] * len(self.params)
+        return all(p.data_ptr() == (e.param or 0) and p.dtype == self.dtype
+                   and p.shape == (e.rows, e.cols) and m.data_ptr() == (e.momentum or 0)
+                   and (w is None or w.data_ptr() == (e.master or 0))
+                   and p.is_contiguous() and m.is_contiguous() and m.shape == p.shape
+                   for e, p, m, w in zip(self.table, self.params, self.momenta, masters))
+
+
+def update_factor(adjust, rows, cols):
+    """The factor on an orthogonalised update: "rms" 0.2 sqrt(max(rows, cols)), which gives it the
+    root mean square of AdamW's; "spectral" sqrt(max(1, rows / cols)); or a number."""
+    if adjust == "rms":
+        return 0.2 * max(rows, cols) ** 0.5
+    if adjust == "spectral":
+        return max(1.0, rows / max(cols, 1)) ** 0.5
+    if isinstance(adjust, str):
+        raise ValueError(f"adjust is {adjust!r}, expected rms, spectral or a number")
+    return float(adjust)
+
+
+def dora_muon(plan, grads, *, lr, momentum=0.95, nesterov=True, weight_decay=0.0,
+              coefficients=NEWTON_SCHULZ, eps=1e-7, adjust="rms", workspace=None):
+    """One step with orthogonalised updates on the matrices of a plan, in place:
+    m = momentum m + (1 - momentum) g, u = momentum m + (1 - momentum) g (m without ``nesterov``),
+    p = p (1 - lr weight_decay) - lr update_factor(adjust) orthogonalised(u).
+
+    ``grads``: one contiguous tensor per parameter, all bf16 or all float32.
+    """
+    grads = list(grads)
+    if len(grads) != len(plan.params):
+        raise ValueError(f"{len(grads)} gradients for {len(plan.params)} params")
+    if not plan.unchanged():
+        raise ValueError("a tensor's storage has changed since the plan was made")
+    gdt = grads[0].dtype if isinstance(grads[0], torch.Tensor) else None
+    if gdt is not None and gdt not in _DT:
+        raise ValueError(f"unsupported dtype {gdt}; use float32 or bfloat16")
+    for i, (g, p, e) in enumerate(zip(grads, plan.params, plan.table)):
+        e.grad = _need(g, f"grads[{i}]", gdt, p.shape, plan.device).data_ptr()
+        e.scale = update_factor(adjust, e.rows, e.cols)
+    iteration, _held = _iteration(coefficients, eps)
+    how = _lib.DoraMuonOptions(iteration, plan.param_code, _DT[gdt], int(bool(nesterov)), 0, float(lr),
+                               float(momentum), float(weight_decay))
+    L, n = _lib.lib(), len(plan.params)
+    if workspace is None:
+        key = tuple(_held)
+        if key not in plan._bytes:   # depends on the sizes, which a plan keeps, and the coefficients
+            plan._bytes = {key: L.dora_muon_workspace_bytes(plan.table, n, ctypes.byref(how))}
+        workspace = torch.empty(max(plan._bytes[key], 1), dtype=torch.uint8, device=plan.device)
+    _check(L.dora_muon_step(plan.table, n, ctypes.byref(how), _ptr(workspace),
+                            _given_ws(workspace, plan.device), _stream(plan.device)), "dora_muon_step")
+    # a backward pass that saved a parameter from before the step is refused
+    torch.autograd.graph.increment_version([p for p in plan.params if not p.is_inference()])
+
+
 def _second_moment(codes):
     if codes.dtype not in (torch.int8, torch.uint8):
         raise ValueError(f"codes have dtype {codes.dtype}, expected int8 (exp_avg) or uint8 (exp_avg_sq)")

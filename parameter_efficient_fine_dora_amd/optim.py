@@ -1,5 +1,6 @@
-"""AdamW for the adapters on top of the C ABI: every tensor of a parameter group in a few launches,
-with moments in float32 or in 8-bit codes, float32 master weights and gradient clipping."""
+"""Optimizers for the adapters on top of the C ABI, every tensor of a parameter group in a few
+launches: AdamW with moments in float32 or in 8-bit codes, float32 master weights and gradient
+clipping, and Muon, whose updates of matrices are orthogonalised."""
 from __future__ import annotations
 
 import torch
@@ -157,5 +158,112 @@ class AdamW(torch.optim.Optimizer):
                 elif isinstance(v, torch.Tensor):
                     v = v.detach().clone(memory_format=torch.contiguous_format).to(
                         p.device, torch.float32 if v.is_floating_point() else None)
+                self.state[p][k] = v
+        self._plans = {}
+
+
+class Muon(torch.optim.Optimizer):
+    """Steps whose updates of matrices are orthogonalised, on contiguous bf16 or float32 device
+    parameters of two dimensions (an adapter's A and B; vectors go to ``AdamW``).
+
+    The gradient's running mean (``momentum``, with a look ahead where ``nesterov``) is taken towards
+    the nearest orthogonal matrix by Newton-Schulz steps (``coefficients``, ``eps``; see
+    ``ops.dora_orthogonalize``) and scaled as ``adjust`` says (``ops.update_factor``).
+
+    master      keep a float32 copy of every bf16 parameter and update that; made from the parameter
+                where a loaded state has none, and dropped from one where it is not wanted
+
+    Hyperparameters are read at each step, so schedulers work; they are kernel arguments, so a
+    captured graph repeats the captured step's.
+    """
+
+    def __init__(self, params, lr=1e-3, momentum=0.95, weight_decay=0.0, *, nesterov=True,
+                 coefficients=ops.NEWTON_SCHULZ, eps=1e-7, adjust="rms", master=False):
+        super().__init__(params, dict(lr=lr, momentum=momentum, weight_decay=weight_decay,
+                                      nesterov=nesterov, eps=eps, adjust=adjust,
+                                      coefficients=tuple(tuple(map(float, abc)) for abc in coefficients)))
+        self.master = bool(master)
+        self._plans = {}
+
+    def add_param_group(self, param_group):
+        super().add_param_group(param_group)
+        group = self.param_groups[-1]
+        bad = [tuple(p.shape) for p in group["params"] if p.dim() != 2]
+        if bad:
+            self.param_groups.pop()
+            raise ValueError(f"a parameter of shape {bad[0]} is not a matrix")
+        ops.update_factor(group["adjust"], 1, 1)   # says what is wrong with it
+
+    def __getstate__(self):   # copies and pickles: torch's own parts, and the option
+        return {**super().__getstate__(), "master": self.master}
+
+    def __setstate__(self, state):
+        super().__setstate__(state)
+        self._plans = {}
+
+    def _state_of(self, p):
+        s = self.state[p]
+        if "momentum_buffer" not in s:
+            s["momentum_buffer"] = torch.zeros_like(p, dtype=torch.float32,
+                                                    memory_format=torch.contiguous_format)
+        if self.master and p.dtype == torch.bfloat16:
+            if "master" not in s:
+                s["master"] = p.detach().float().contiguous()
+        else:
+            s.pop("master", None)
+        return s
+
+    def _plan(self, slot, params):
+        """The plan of these parameters, made anew when one of their tensors or its storage is
+        another."""
+        states = [self._state_of(p) for p in params]
+        momenta = [s["momentum_buffer"] for s in states]
+        masters = [s["master"] for s in states] if "master" in states[0] else None
+
+        def same(a, b):
+            return a is b or (a is not None and b is not None and len(a) == len(b)
+                              and all(x is y for x, y in zip(a, b)))
+
+        plan = self._plans.get(slot)
+        if not (plan is not None and same(plan.params, params) and same(plan.momenta, momenta)
+                and same(plan.masters, masters) and plan.unchanged()):
+            plan = ops.MuonPlan(params, momenta, masters=masters)
+        return plan
+
+    @torch.no_grad()
+    def step(self, closure=None):
+        loss = None
+        if closure is not None:
+            with torch.enable_grad():
+                loss = closure()
+        buckets = {}   # one call each: a group's parameters of one dtype and device
+        for gi, group in enumerate(self.param_groups):
+            for p in group["params"]:
+                if p.grad is not None:
+                    buckets.setdefault((gi, p.dtype, p.grad.dtype, p.device), []).append(p)
+        plans = {}
+        for slot, params in buckets.items():
+            group = self.param_groups[slot[0]]
+            plans[slot] = self._plan(slot, params)
+            ops.dora_muon(plans[slot], [p.grad.contiguous() for p in params], lr=group["lr"],
+                          momentum=group["momentum"], nesterov=group["nesterov"],
+                          weight_decay=group["weight_decay"], coefficients=group["coefficients"],
+                          eps=group["eps"], adjust=group["adjust"])
+        self._plans = plans
+        return loss
+
+    def load_state_dict(self, state_dict):
+        """Loads a checkpoint of this class."""
+        for i, s in state_dict["state"].items():
+            if s and "momentum_buffer" not in s:
+                raise ValueError(f"the checkpoint's state of parameter {i} lacks momentum_buffer")
+        super().load_state_dict(state_dict)
+        # torch casts floating state to the parameter's dtype; all of it is float32 here
+        ids = [i for g in state_dict["param_groups"] for i in g["params"]]
+        mine = [p for g in self.param_groups for p in g["params"]]
+        for i, p in zip(ids, mine):
+            for k, v in state_dict["state"].get(i, {}).items():
+                if isinstance(v, torch.Tensor):
+                    v = v.detach().clone(memory_format=torch.contiguous_format).to(p.device, torch.float32)
                 self.state[p][k] = v
         self._plans = {}

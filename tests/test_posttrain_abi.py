@@ -153,3 +153,138 @@ def test_workspaces():
     assert pref_backward(b=batch(0, 0, 0), pairs=0, args=[None] * 6, ws=None, nb=0) == 0
     assert policy_backward(b=batch(0, 3, 0), args=[None] * 7) == 0
     assert pref_forward(b=batch(0, 0, 0), pairs=0, args=[None] * 8, ws=None, nb=0) == 0
+
+
+def iteration(coefficients=((3.4445, -4.7750, 2.0315),) * 5, steps=None, eps=1e-7, reserved=0):
+    flat = (ctypes.c_double * (3 * len(coefficients) or 1))(*[v for abc in coefficients for v in abc])
+    z = _lib.DoraNewtonSchulz(ctypes.addressof(flat), len(coefficients) if steps is None else steps, reserved,
+                              eps)
+    z.held = flat
+    return z
+
+
+def matrices(*sizes, x=FAKE, out=FAKE):
+    t = (_lib.DoraMatrix * max(len(sizes), 1))()
+    for e, (rows, cols) in zip(t, sizes):
+        e.x, e.out, e.rows, e.cols = x, out, rows, cols
+    return t
+
+
+def ortho(t=None, n=1, dtype=_lib.F32, reserved=0, ws=FAKE, nb=1 << 50, **kw):
+    z = iteration(**kw)
+    o = _lib.DoraOrthogonalizeOptions(z, dtype, reserved)
+    t = matrices((6, 8)) if t is None else t
+    return (_lib.lib().dora_orthogonalize(t, n, ctypes.byref(o), ws, nb, None),
+            _lib.lib().dora_orthogonalize_workspace_bytes(t, n, ctypes.byref(o)))
+
+
+def test_matrix_structs_are_the_headers():
+    assert ctypes.sizeof(_lib.DoraNewtonSchulz) == 24 and ctypes.sizeof(_lib.DoraMatrix) == 32
+    assert ctypes.sizeof(_lib.DoraOrthogonalizeOptions) == 32
+    assert ctypes.sizeof(_lib.DoraMuonTensor) == 56
+    assert ctypes.sizeof(_lib.DoraMuonOptions) == 64 and _lib.DoraMuonOptions.lr.offset == 40
+
+
+DIVERGES = ((30.0, 2.0, 3.0),) * 9
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dtype=2), "DORA_ERR_DTYPE"), (dict(reserved=1), "DORA_ERR_FLAGS"),
+    (dict(steps=0), "DORA_ERR_FLAGS"), (dict(steps=17), "DORA_ERR_FLAGS"), (dict(steps=-1), "DORA_ERR_FLAGS"),
+    (dict(eps=0.0), "DORA_ERR_FLAGS"), (dict(eps=-1.0), "DORA_ERR_FLAGS"), (dict(eps=NAN), "DORA_ERR_FLAGS"),
+    (dict(eps=1e39), "DORA_ERR_FLAGS"), (dict(eps=2.0 ** -101), "DORA_ERR_FLAGS"),
+    (dict(coefficients=((NAN, 1.0, 1.0),)), "DORA_ERR_FLAGS"),
+    (dict(coefficients=((INF, 1.0, 1.0),)), "DORA_ERR_FLAGS"),
+    (dict(coefficients=DIVERGES), "DORA_ERR_FLAGS"),
+    (dict(coefficients=((1e20, 0.0, 0.0),)), "DORA_ERR_FLAGS"),
+    (dict(t=matrices((-1, 8))), "DORA_ERR_SHAPE"), (dict(t=matrices((6, -8))), "DORA_ERR_SHAPE"),
+    (dict(t=matrices((6, (1 << 20) + 1))), "DORA_ERR_SHAPE"),
+    (dict(t=matrices((16385, 16385))), "DORA_ERR_SHAPE"),
+    (dict(n=-1), "DORA_ERR_SHAPE"), (dict(n=1 << 20), "DORA_ERR_SHAPE"),
+])
+def test_orthogonalize_refused(kw, code):
+    assert ortho(**kw) == (E[code], 0)
+
+
+def test_orthogonalize_pointers_and_workspace():
+    _, need = ortho()
+    assert need > 0
+    assert ortho(ws=None)[0] == E["DORA_ERR_NULL"] and ortho(ws=FAKE + 8)[0] == E["DORA_ERR_ALIGN"]
+    assert ortho(nb=need - 1)[0] == E["DORA_ERR_WORKSPACE"]
+    for kw in (dict(x=None), dict(out=None)):
+        assert ortho(t=matrices((6, 8), **kw))[0] == E["DORA_ERR_NULL"]
+    for kw in (dict(x=FAKE + 2), dict(out=FAKE + 2)):
+        assert ortho(t=matrices((6, 8), **kw))[0] == E["DORA_ERR_ALIGN"]
+    assert ortho(t=matrices((6, 8), x=FAKE + 1), dtype=_lib.BF16)[0] == E["DORA_ERR_ALIGN"]
+    # nothing to do
+    assert ortho(n=0) == (0, 0)
+    assert ortho(t=matrices((0, 8), (5, 0), x=None, out=None), n=2) == (0, 0)
+    z = iteration()
+    o = _lib.DoraOrthogonalizeOptions(z, _lib.F32, 0)
+    L = _lib.lib()
+    assert L.dora_orthogonalize(None, 1, ctypes.byref(o), FAKE, HUGE, None) == E["DORA_ERR_NULL"]
+    assert L.dora_orthogonalize(matrices((6, 8)), 1, None, FAKE, HUGE, None) == E["DORA_ERR_NULL"]
+    o.iteration.coefficients = None
+    assert L.dora_orthogonalize(matrices((6, 8)), 1, ctypes.byref(o), FAKE, HUGE, None) == E["DORA_ERR_NULL"]
+
+
+def test_workspaces_follow_the_matrices():
+    one = ortho(t=matrices((64, 2048)), dtype=_lib.BF16)[1]
+    many = ortho(t=matrices(*[(64, 2048)] * 40), n=40, dtype=_lib.BF16)[1]
+    assert many <= 40 * one
+    # 4 bytes an element and 20 n^2, and what rounding up to tiles adds
+    assert ortho(t=matrices((1024, 8192)), dtype=_lib.BF16)[1] <= 1.3 * (4 * 1024 * 8192 + 20 * 1024 ** 2)
+    assert ortho(t=matrices((1024, 8192)))[1] <= 1.3 * (16 * 1024 * 8192 + 20 * 1024 ** 2)
+
+
+def muon(n=1, nb=1 << 50, ws=FAKE, coefficients=None, tensor=None, **kw):
+    z = iteration(**({} if coefficients is None else dict(coefficients=coefficients)))
+    o = _lib.DoraMuonOptions(z, _lib.F32, _lib.F32, 1, 0, 1e-3, 0.95, 0.0)
+    for k, v in kw.items():
+        setattr(o, k, v)
+    t = (_lib.DoraMuonTensor * max(n, 1))()
+    for e in t:
+        e.param = e.grad = e.momentum = FAKE
+        e.rows, e.cols, e.scale = 6, 8, 1.0
+        for k, v in (tensor or {}).items():
+            setattr(e, k, v)
+    rc = _lib.lib().dora_muon_step(t, n, ctypes.byref(o), ws, nb, None)
+    return rc, _lib.lib().dora_muon_workspace_bytes(t, n, ctypes.byref(o))
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(param_dtype=3), "DORA_ERR_DTYPE"), (dict(grad_dtype=-1), "DORA_ERR_DTYPE"),
+    (dict(nesterov=2), "DORA_ERR_FLAGS"), (dict(reserved=1), "DORA_ERR_FLAGS"),
+    (dict(lr=NAN), "DORA_ERR_FLAGS"), (dict(lr=INF), "DORA_ERR_FLAGS"), (dict(momentum=1.0), "DORA_ERR_FLAGS"),
+    (dict(momentum=-0.1), "DORA_ERR_FLAGS"), (dict(momentum=NAN), "DORA_ERR_FLAGS"),
+    (dict(weight_decay=INF), "DORA_ERR_FLAGS"), (dict(coefficients=DIVERGES), "DORA_ERR_FLAGS"),
+    (dict(tensor=dict(scale=NAN)), "DORA_ERR_FLAGS"), (dict(tensor=dict(rows=-1)), "DORA_ERR_SHAPE"),
+    (dict(tensor=dict(master=FAKE)), "DORA_ERR_DTYPE"), (dict(n=-1), "DORA_ERR_SHAPE"),
+])
+def test_muon_refused(kw, code):
+    assert muon(**kw) == (E[code], 0)
+
+
+def test_muon_pointers_and_workspace():
+    _, need = muon()
+    assert muon(nb=need - 1)[0] == E["DORA_ERR_WORKSPACE"] and muon(ws=None)[0] == E["DORA_ERR_NULL"]
+    for k in ("param", "grad", "momentum"):
+        assert muon(tensor={k: None})[0] == E["DORA_ERR_NULL"], k
+        assert muon(tensor={k: FAKE + 2})[0] == E["DORA_ERR_ALIGN"], k
+    assert muon(param_dtype=_lib.BF16, tensor=dict(master=FAKE + 2))[0] == E["DORA_ERR_ALIGN"]
+    assert muon(n=0) == (0, 0)
+    assert muon(tensor=dict(rows=0, param=None, grad=None, momentum=None)) == (0, 0)
+    # a float32 parameter's product is formed on the way and kept beside X, a bf16 one's is not
+    assert muon(tensor=dict(rows=512, cols=4096))[1] > 1.5 * muon(tensor=dict(rows=512, cols=4096),
+                                                                   param_dtype=_lib.BF16)[1]
+
+
+def test_a_master_for_some_tensors_only_is_refused():
+    z = iteration()
+    o = _lib.DoraMuonOptions(z, _lib.BF16, _lib.BF16, 1, 0, 1e-3, 0.95, 0.0)
+    t = (_lib.DoraMuonTensor * 2)()
+    for e in t:
+        e.param = e.grad = e.momentum = FAKE
+        e.rows, e.cols, e.scale = 6, 8, 1.0
+    t[1].master = FAKE
+    assert _lib.lib().dora_muon_step(t, 2, ctypes.byref(o), FAKE, HUGE, None) == E["DORA_ERR_NULL"]
