@@ -47,7 +47,6 @@ typedef __amdgpu_buffer_rsrc_t Rsrc;
 constexpr int kThreads = 256;
 constexpr int kRowBytes = 128;       // of a row in one stage
 constexpr int kPairBlock = 32;       // columns of a pair row's block
-constexpr int kPad = 128;            // the long side is padded to whole tiles of either size
 constexpr int kMaxGroups = 12;
 constexpr int kMaxMatrices = 48;     // of one launch that needs their addresses
 constexpr int kMaxBlocks = 1024;     // workgroups that look for one matrix's largest element
@@ -57,7 +56,8 @@ constexpr int kMaxSplits = 32;
 // Offsets are bytes from a matrix's own part of the workspace.
 struct Group {
   int n, m;            // shorter and longer side
-  int nt, mt;          // padded
+  int ne;              // n in whole blocks of 64: what sums over n run to
+  int nt, mt;          // padded to tiles
   int count;           // matrices
   int first;           // the first one's number
   uint32_t from;       // the launch's first workgroup of this group
@@ -218,6 +218,51 @@ struct Product {
     }
   }
 
+  // The tile in LDS, for results that leave in whole rows (or columns) of it: a lane's four columns
+  // of 32 different rows would be 8 bytes here and there.  Groups of four columns are swizzled by
+  // the row, so that rows and columns are read without bank conflicts.
+  __device__ static __forceinline__ float* at(float* tile, int r, int c) {
+    return tile + r * T + (((c >> 2) ^ ((r ^ (r >> 3)) & (T / 4 - 1))) << 2) + (c & 3);
+  }
+  __device__ static __forceinline__ float* stage(uint8_t* sm, const f32x16 (&acc)[kB][kB]) {
+    static_assert(T * T * 4 <= kLds, "the tile fits where the stages were");
+    float* tile = reinterpret_cast<float*>(sm);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int i = 0; i < kB; ++i)
+#pragma unroll
+      for (int j = 0; j < kB; ++j)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          *reinterpret_cast<f32x4*>(at(tile, (wave & 1) * (T / 2) + 32 * i + (lane & 31),
+                                       (wave >> 1) * (T / 2) + 32 * j + 8 * g + 4 * (lane >> 5))) =
+              f32x4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2],
+                    acc[i][j][4 * g + 3]};
+    __syncthreads();
+    return tile;
+  }
+  // Eight columns of a row, and eight rows of a column.
+  __device__ static __forceinline__ void row8(float* tile, int r, int c, float* v) {
+#pragma unroll
+    for (int q = 0; q < 8; q += 4) {
+      const f32x4 x = *reinterpret_cast<const f32x4*>(at(tile, r, c + q));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[q + e] = x[e];
+    }
+  }
+  __device__ static __forceinline__ void column8(float* tile, int r, int c, float* v) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[q] = *at(tile, r + q, c);
+  }
+  // Calls fn(line, first of eight) for all of the tile's lines.
+  template <typename Fn>
+  __device__ static __forceinline__ void lines(Fn fn) {
+#pragma unroll
+    for (int i = 0; i < T * T / 8 / kThreads; ++i) {
+      const int x = i * kThreads + threadIdx.x;
+      fn(x / (T / 8), x % (T / 8) * 8);
+    }
+  }
   // Calls fn(row, column, values of four columns) for every group of four that this lane has.
   template <typename Fn>
   __device__ static __forceinline__ void each(const f32x16 (&acc)[kB][kB], Fn fn) {
@@ -242,39 +287,28 @@ __device__ __forceinline__ void split(float v, f16& hi, f16& lo) {
   hi = (f16)v;
   lo = (f16)(v - (float)hi);
 }
-// Columns [k, k + 4) of a pair row.
-__device__ __forceinline__ void store_pair4(f16* row, int64_t k, const f32x4& v) {
-  f16x4 h, l;
+// Columns [k, k + N) of a pair row; of a flat one, whose lo begin at `lo`.
+template <int N>
+__device__ __forceinline__ void store_pair(f16* row, int64_t k, const float* v, int64_t lo = 0) {
+  typedef _Float16 V __attribute__((ext_vector_type(N)));
+  V h, l;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
+  for (int e = 0; e < N; ++e) {
     f16 a, b;
     split(v[e], a, b);
     h[e] = a;
     l[e] = b;
   }
-  f16* p = row + pair_at(k);
-  *reinterpret_cast<f16x4*>(p) = h;
-  *reinterpret_cast<f16x4*>(p + kPairBlock) = l;
+  f16* p = row + (lo ? k : pair_at(k));
+  *reinterpret_cast<V*>(p) = h;
+  *reinterpret_cast<V*>(p + (lo ? lo : kPairBlock)) = l;
 }
-__device__ __forceinline__ f32x4 load_pair4(const f16* row, int64_t k) {
+__device__ __forceinline__ void load_pair8(const f16* row, int64_t k, float* v) {
   const f16* p = row + pair_at(k);
-  const f16x4 h = *reinterpret_cast<const f16x4*>(p);
-  const f16x4 l = *reinterpret_cast<const f16x4*>(p + kPairBlock);
-  f32x4 v;
+  const f16x8 h = *reinterpret_cast<const f16x8*>(p);
+  const f16x8 l = *reinterpret_cast<const f16x8*>(p + kPairBlock);
 #pragma unroll
-  for (int e = 0; e < 4; ++e) v[e] = (float)h[e] + (float)l[e];
-  return v;
-}
-// The same four values at their mirrored places: column k of four rows.
-__device__ __forceinline__ void store_pair_mirror(f16* rows, int64_t ld, int64_t k, const f32x4& v) {
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    f16 a, b;
-    split(v[e], a, b);
-    f16* p = rows + e * ld + pair_at(k);
-    p[0] = a;
-    p[kPairBlock] = b;
-  }
+  for (int e = 0; e < 8; ++e) v[e] = (float)h[e] + (float)l[e];
 }
 
 // ---- X into half precision --------------------------------------------------------------------
@@ -456,7 +490,7 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_gram(const Groups a,
   __shared__ __attribute__((aligned(1024))) uint8_t sm[P::kLds];
   const uint32_t id = by_xcd(blockIdx.x, total);
   const Group& g = a.g[group_of(a, id)];
-  const int nt = g.nt / T, tiles = tri(nt);
+  const int nt = (g.n + T - 1) / T, tiles = tri(nt);
   int rest = (int)(id - g.from);
   const int split = rest % g.splits;
   rest /= g.splits;
@@ -465,7 +499,7 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_gram(const Groups a,
   tri_tile(t, nt, ti, tj);
   uint8_t* own = ws + g.base + (int64_t)u * g.stride;
   const int64_t ld = (int64_t)g.mt * (PAIR ? 4 : 2);
-  const int stages = (int)(ld / kRowBytes);
+  const int stages = (g.m + 63) / 64 * (PAIR ? 2 : 1);
   const int k0 = (int)((int64_t)stages * split / g.splits);
   const int k1 = (int)((int64_t)stages * (split + 1) / g.splits);
   const uint8_t* x = own + (second ? g.xk2 : g.xk);
@@ -490,7 +524,7 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_gather(const Groups 
   __shared__ uint32_t lds_most[kThreads / 64];
   const uint32_t id = blockIdx.x;
   const Group& g = a.g[group_of(a, id)];
-  const int nt = g.nt / T, tiles = tri(nt);
+  const int nt = (g.n + T - 1) / T, tiles = tri(nt);
   int rest = (int)(id - g.from);
   const int piece = rest % (kSide * kSide);
   rest /= kSide * kSide;
@@ -515,10 +549,11 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_gather(const Groups 
   if (ti == tj && pj < pi) return;   // (the same for the whole workgroup)
   const int i = threadIdx.x / 8, j = threadIdx.x % 8 * 4;
   const float* p = part + (int64_t)t * g.splits * T * T + (pi + i) * T + pj + j;
-  f32x4 v = {0.f, 0.f, 0.f, 0.f};
-  for (int s = 0; s < g.splits; ++s) v += *reinterpret_cast<const f32x4*>(p + (int64_t)s * T * T);
+  f32x4 x = {0.f, 0.f, 0.f, 0.f};
+  for (int s = 0; s < g.splits; ++s) x += *reinterpret_cast<const f32x4*>(p + (int64_t)s * T * T);
+  float v[4], w[4];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) v[q] = v[q] * r * r * to;
+  for (int q = 0; q < 4; ++q) v[q] = x[q] * r * r * to;
 #pragma unroll
   for (int q = 0; q < 4; ++q) tile[i][j + q] = v[q];
   __syncthreads();
@@ -531,12 +566,11 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_gather(const Groups 
   f16* s = reinterpret_cast<f16*>(own + g.sq[0]);
   const int64_t ld = 2 * (int64_t)g.nt;
   const int64_t row = (int64_t)ti * T + pi, col = (int64_t)tj * T + pj;
-  store_pair4(s + (row + i) * ld, col + j, v);
+  store_pair<4>(s + (row + i) * ld, col + j, v);
   if (diagonal) return;
-  f32x4 w;
 #pragma unroll
   for (int q = 0; q < 4; ++q) w[q] = tile[j + q][i];
-  store_pair4(s + (col + i) * ld, row + j, w);
+  store_pair<4>(s + (col + i) * ld, row + j, w);
 }
 
 // A symmetric product of two n x n pairs, or of two such products of one launch (`both`).
@@ -561,60 +595,52 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_square(const Squares
   const Square& q = a.q[id >= a.half ? 1 : 0];
   if (id >= a.half) id -= a.half;
   const Group& g = a.groups.g[group_of(a.groups, id)];
-  const int nt = g.nt / T, tiles = tri(nt);
+  const int nt = (g.n + T - 1) / T, tiles = tri(nt);
   const int rest = (int)(id - g.from);
   const int t = rest % tiles, u = rest / tiles;
   int ti, tj;
   tri_tile(t, nt, ti, tj);
   uint8_t* own = ws + g.base + (int64_t)u * g.stride;
-  const int64_t ld = (int64_t)g.nt * 4;
-  const int stages = (int)(ld / kRowBytes);
+  const int64_t ld = (int64_t)g.nt * 4, le = ld / 2;
+  const int stages = g.ne / kPairBlock;
   const uint8_t* left = own + g.sq[q.left];
+  const int64_t i0 = (int64_t)ti * T, j0 = (int64_t)tj * T;
   f32x16 acc[P::kB][P::kB];
-  P::run(sm, Side{left + (int64_t)ti * T * ld, ld, stages},
-         Side{own + g.sq[q.right] + (int64_t)tj * T * ld, ld, stages}, 0, stages, acc);
+  P::run(sm, Side{left + i0 * ld, ld, stages}, Side{own + g.sq[q.right] + j0 * ld, ld, stages}, 0,
+         stages, acc);
+  float* tile = P::stage(sm, acc);
   f16* out = reinterpret_cast<f16*>(own + g.sq[q.out]);
-  const int64_t le = ld / 2;
-  P::each(acc, [&](int ii, int jj, f32x4 v) {
-    const int i = ti * T + ii, j = tj * T + jj;
-    if (ti == tj && jj + 3 < ii) return;   // below the diagonal: the mirror of what is above
-    v *= q.alpha;
-    if (POLY) {
-      const f32x4 s = load_pair4(reinterpret_cast<const f16*>(left) + (int64_t)i * le, j);
+  // columns [j, j + 8) of row i
+  auto put = [&](int64_t i, int64_t j, float* v) {
+    if (j >= g.ne) return;   // padding that nothing reads (and where a flat row's lo lie)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < 8; ++e) v[e] *= q.alpha;
+    if (POLY) {
+      float s[8];
+      load_pair8(reinterpret_cast<const f16*>(left) + i * le, j, s);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
         v[e] = fmaf(q.beta, s[e], v[e]);
         if (i == j + e && i < g.n) v[e] += q.gamma;
       }
     }
-    if (q.flat) {
+    store_pair<8>(out + i * le, j, v, q.flat ? g.ne : 0);
+  };
+  P::lines([&](int r, int c) {
+    float v[8];
+    P::row8(tile, r, c, v);
+    if (ti == tj && c < r) {   // below the diagonal what is above it, so that it stays symmetric
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (ti == tj && jj + e < ii) continue;
-        f16 h, l;
-        split(v[e], h, l);
-        f16* at = out + (int64_t)i * le + j + e;
-        f16* mirror = out + (int64_t)(j + e) * le + i;
-        at[0] = mirror[0] = h;
-        at[g.nt] = mirror[g.nt] = l;
-      }
-      return;
+      for (int e = 0; e < 8; ++e)
+        if (c + e < r) v[e] = *P::at(tile, c + e, r);
     }
-    if (ti == tj && jj < ii + 1) {   // the four across the diagonal, one by one
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (jj + e < ii) continue;
-        f16 h, l;
-        split(v[e], h, l);
-        f16* at = out + (int64_t)i * le + pair_at(j + e);
-        f16* mirror = out + (int64_t)(j + e) * le + pair_at(i);
-        at[0] = mirror[0] = h;
-        at[kPairBlock] = mirror[kPairBlock] = l;
-      }
-      return;
-    }
-    store_pair4(out + (int64_t)i * le, j, v);
-    store_pair_mirror(out + (int64_t)j * le, le, i, v);
+    put(i0 + r, j0 + c, v);
+  });
+  if (ti == tj) return;
+  P::lines([&](int c, int r) {
+    float v[8];
+    P::column8(tile, r, c, v);
+    put(j0 + c, i0 + r, v);
   });
 }
 
@@ -640,16 +666,16 @@ enum Result { kOut, kParam, kMaster };
 
 template <int T, int RING, bool PAIR>
 __device__ __forceinline__ void last_product(uint8_t* sm, const Group& g, uint8_t* own, int q,
-                                             bool second, int64_t row0, int64_t col0,
+                                             bool second, bool tall, int64_t row0, int64_t col0,
                                              f32x16 (&acc)[T / 64][T / 64]) {
   // Q's rows are pairs where X's are; else all hi and then all lo against X twice
   const int64_t ld_q = (int64_t)g.nt * 4, ld_x = (int64_t)g.nt * (PAIR ? 4 : 2);
-  const int sq = (int)(ld_q / kRowBytes), sx = (int)(ld_x / kRowBytes);
+  const int sq = g.ne / kPairBlock, sx = PAIR ? sq : sq / 2;
   const uint8_t* x = own + (second ? g.xt2 : g.xt);
   const uint8_t* qp = own + g.sq[q];
-  const Side qs = {qp + (g.tall ? col0 : row0) * ld_q, ld_q, sq};
-  const Side xs = {x + (g.tall ? row0 : col0) * ld_x, ld_x, sx};
-  Product<T, RING, PAIR>::run(sm, g.tall ? xs : qs, g.tall ? qs : xs, 0, sq, acc);
+  const Side qs = {qp + (tall ? col0 : row0) * ld_q, ld_q, sq};
+  const Side xs = {x + (tall ? row0 : col0) * ld_x, ld_x, sx};
+  Product<T, RING, PAIR>::run(sm, tall ? xs : qs, tall ? qs : xs, 0, sq, acc);
 }
 
 template <int T, int RING, bool PAIR, bool BF, Result WHAT>
@@ -661,34 +687,41 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_apply(const Sinks a,
   const int u = matrix_of(a.from, a.count, id);
   const Group& g = a.groups.g[group_of_matrix(a.groups, a.first + u)];
   uint8_t* own = ws + g.base + (int64_t)(a.first + u - g.first) * g.stride;
-  const int rows = g.tall ? g.m : g.n, cols = g.tall ? g.n : g.m;
-  const int down = ((g.tall ? g.m : g.n) + T - 1) / T, across = (cols + T - 1) / T;
+  const bool tall = g.tall;
+  const int rows = tall ? g.m : g.n, cols = tall ? g.n : g.m;
+  const int down = (rows + T - 1) / T, across = (cols + T - 1) / T;
   const int t = (int)(id - a.from[u]);
-  // the tiles that share rows or columns of the long side next to each other
-  const int64_t row0 = (int64_t)(g.tall ? t / across : t % down) * T;
-  const int64_t col0 = (int64_t)(g.tall ? t % across : t / down) * T;
+  // tiles that share X's columns next to each other
+  const int64_t row0 = (int64_t)(tall ? t / across : t % down) * T;
+  const int64_t col0 = (int64_t)(tall ? t % across : t / down) * T;
   f32x16 acc[P::kB][P::kB];
-  last_product<T, RING, PAIR>(sm, g, own, a.q, a.second, row0, col0, acc);
+  last_product<T, RING, PAIR>(sm, g, own, a.q, a.second, tall, row0, col0, acc);
+  float* tile = P::stage(sm, acc);
   const Sink s = a.s[u];
-  const float r = *reinterpret_cast<const float*>(own + g.scale) * a.unit *
+  const float f = *reinterpret_cast<const float*>(own + g.scale) * a.unit *
                   (WHAT == kOut ? 1.f : -s.rate);
   typename E::T* out = reinterpret_cast<typename E::T*>(s.out);
-  P::each(acc, [&](int ii, int jj, f32x4 v) {
-    const int64_t i = row0 + ii, j = col0 + jj;
+  P::lines([&](int r, int c) {
+    const int64_t i = row0 + r, j = col0 + c;
     if (i >= rows || j >= cols) return;
-    const int64_t at = i * cols + j;
-    const int here = (int)min((int64_t)4, cols - j);
+    float v[8];
+    P::row8(tile, r, c, v);
+    const int64_t at = i * cols + j, stop = (i + 1) * cols;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (e >= here) break;
-      float x = v[e] * r;
-      if (WHAT != kOut) {
-        const float p = WHAT == kMaster ? s.master[at + e] : E::get(out + at + e);
-        x = fmaf(p, a.decay, fmaf(p, a.rest, x));
-        if (WHAT == kMaster) s.master[at + e] = x;
+    for (int e = 0; e < 8; ++e) v[e] *= f;
+    if (WHAT != kOut) {
+      float p[8];
+      if (WHAT == kMaster) load8<false>(s.master, at, stop, p);
+      else load8<BF>(out, at, stop, p);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = fmaf(p[e], a.decay, fmaf(p[e], a.rest, v[e]));
+      if (WHAT == kMaster) {
+        store_part<false>(s.master, at, stop, v);
+        store_part<false>(s.master, at + 4, stop, v + 4);
       }
-      E::put(out + at + e, x);
     }
+#pragma unroll
+    for (int e = 0; e < 8; e += E::kN) store_part<BF>(out, at + e, stop, v + e);
   });
 }
 
@@ -700,22 +733,31 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_between(const Groups
   using P = Product<T, RING, PAIR>;
   __shared__ __attribute__((aligned(1024))) uint8_t sm[P::kLds];
   const uint32_t id = by_xcd(blockIdx.x, total);
-  Group g = a.g[group_of(a, id)];
-  const int down = g.nt / T, tiles = down * (g.mt / T);
+  const Group& g = a.g[group_of(a, id)];
+  const int down = (g.n + T - 1) / T, tiles = down * ((g.m + T - 1) / T);
   const int rest = (int)(id - g.from);
   const int t = rest % tiles, u = rest / tiles;
   uint8_t* own = ws + g.base + (int64_t)u * g.stride;
-  g.tall = false;   // rows are n's whatever the matrix's order
   const int64_t row0 = (int64_t)(t % down) * T, col0 = (int64_t)(t / down) * T;
   f32x16 acc[P::kB][P::kB];
-  last_product<T, RING, PAIR>(sm, g, own, q, second, row0, col0, acc);
-  const float r = *reinterpret_cast<const float*>(own + g.scale) * unit;
+  last_product<T, RING, PAIR>(sm, g, own, q, second, false, row0, col0, acc);
+  float* tile = P::stage(sm, acc);
+  const float f = *reinterpret_cast<const float*>(own + g.scale) * unit;
   f16* xk = reinterpret_cast<f16*>(own + (second ? g.xk : g.xk2));
   f16* xt = reinterpret_cast<f16*>(own + (second ? g.xt : g.xt2));
-  P::each(acc, [&](int ii, int jj, f32x4 v) {
-    v *= r;
-    store_pair4(xk + (row0 + ii) * 2 * g.mt, col0 + jj, v);
-    store_pair_mirror(xt + (col0 + jj) * 2 * g.nt, 2 * g.nt, row0 + ii, v);
+  P::lines([&](int r, int c) {
+    float v[8];
+    P::row8(tile, r, c, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= f;
+    store_pair<8>(xk + (row0 + r) * 2 * g.mt, col0 + c, v);
+  });
+  P::lines([&](int c, int r) {
+    float v[8];
+    P::column8(tile, r, c, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= f;
+    store_pair<8>(xt + (col0 + c) * 2 * g.nt, row0 + r, v);
   });
 }
 
@@ -815,17 +857,20 @@ struct Kind {
   int times;      // how often Q X is formed on the way
 };
 struct Pass {
-  int tile;
+  bool small;               // n <= 64 throughout
+  int gram, square, apply;  // tiles
   std::vector<int> order;   // items, group by group
   Groups groups;
   size_t bytes;
 };
 
 int64_t padded(int64_t v, int to) { return (v + to - 1) / to * to; }
+int tiles(int v, int tile) { return (v + tile - 1) / tile; }
 
-void lay_out(Group& g, const Kind& k, int tile) {
-  g.nt = (int)padded(g.n, tile);
-  g.mt = (int)padded(g.m, kPad);
+void lay_out(Group& g, const Kind& k, int gram) {
+  g.ne = (int)padded(g.n, 64);
+  g.nt = g.n <= 64 ? 64 : (int)padded(g.n, 128);
+  g.mt = (int)padded(g.m, 128);
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     const int64_t here = at;
@@ -841,24 +886,23 @@ void lay_out(Group& g, const Kind& k, int tile) {
     g.xt2 = take((int64_t)g.nt * g.mt * 4);
   }
   for (int64_t& s : g.sq) s = take((int64_t)g.nt * g.nt * 4);
-  g.part = take((int64_t)tri(g.nt / tile) * g.splits * tile * tile * 4);
+  g.part = take((int64_t)tri(tiles(g.n, gram)) * g.splits * gram * gram * 4);
   g.most = take((int64_t)g.blocks * 4);
   g.scale = take(4);
   g.stride = at;
 }
 
-// Tiles of 128 where they fill the chip (a CU holds two workgroups of them): 24 matrices of 384
-// and as many again of another shape are 288. Else of 64, which have four times as many.
-constexpr int64_t kEnoughTiles = 256;
+// Tiles of 128 read half of what tiles of 64 read for the same products, and are taken where they
+// fill the chip (these numbers: of workgroups).
+constexpr int64_t kEnough = 256;
 constexpr int64_t kWantSums = 768;   // workgroups of the sums over m
 
 std::vector<Pass> passes(const std::vector<Item>& items, const Kind& kind) {
   auto small = [](const Item& i) { return std::min(i.rows, i.cols); };
-  std::vector<int> order((size_t)items.size());
-  for (size_t i = 0; i < items.size(); ++i) order[i] = (int)i;
-  order.erase(std::remove_if(order.begin(), order.end(),
-                             [&](int i) { return small(items[i]) == 0; }),
-              order.end());
+  std::vector<int> order;
+  order.reserve(items.size());
+  for (size_t i = 0; i < items.size(); ++i)
+    if (small(items[i]) > 0) order.push_back((int)i);
   std::stable_sort(order.begin(), order.end(), [&](int a, int b) {
     const Item &x = items[a], &y = items[b];
     if (small(x) != small(y)) return small(x) < small(y);
@@ -866,48 +910,51 @@ std::vector<Pass> passes(const std::vector<Item>& items, const Kind& kind) {
   });
   std::vector<Pass> out;
   for (size_t at = 0; at < order.size();) {
-    // matrices of one n choose their tile together
-    size_t same = at;
-    const int64_t n = small(items[order[at]]);
-    while (same < order.size() && small(items[order[same]]) == n) ++same;
-    const int64_t wide = (int64_t)(same - at) * tri((int)((n + 127) / 128));
-    const int tile = n > 64 && wide >= kEnoughTiles ? 128 : 64;
-    while (at < same) {
-      size_t end = at;
-      const Item& one = items[order[at]];
-      while (end < same && items[order[end]].rows == one.rows && items[order[end]].cols == one.cols)
-        ++end;
-      if (out.empty() || out.back().tile != tile || out.back().groups.count == kMaxGroups) {
-        out.emplace_back();
-        out.back().tile = tile;
-        out.back().groups.count = 0;
-      }
-      Pass& p = out.back();
-      Group& g = p.groups.g[p.groups.count++];
-      g = Group{};
-      g.n = (int)n;
-      g.m = (int)std::max(one.rows, one.cols);
-      g.tall = one.rows > one.cols;
-      g.count = (int)(end - at);
-      g.first = (int)p.order.size();
-      p.order.insert(p.order.end(), order.begin() + at, order.begin() + end);
-      at = end;
+    const Item& one = items[order[at]];
+    size_t end = at;
+    while (end < order.size() && items[order[end]].rows == one.rows && items[order[end]].cols == one.cols)
+      ++end;
+    const bool low = small(one) <= 64;
+    if (out.empty() || out.back().small != low || out.back().groups.count == kMaxGroups) {
+      out.emplace_back();
+      out.back().small = low;
+      out.back().groups.count = 0;
     }
+    Pass& p = out.back();
+    Group& g = p.groups.g[p.groups.count++];
+    g = Group{};
+    g.n = (int)small(one);
+    g.m = (int)std::max(one.rows, one.cols);
+    g.tall = one.rows > one.cols;
+    g.count = (int)(end - at);
+    g.first = (int)p.order.size();
+    p.order.insert(p.order.end(), order.begin() + at, order.begin() + end);
+    at = end;
   }
   for (Pass& p : out) {
-    int64_t tiles = 0;
+    int64_t squares = 0, across = 0, parts = 0;   // workgroups with tiles of 128
     for (int i = 0; i < p.groups.count; ++i) {
       const Group& g = p.groups.g[i];
-      tiles += (int64_t)g.count * tri((g.n + p.tile - 1) / p.tile);
+      const int64_t t = (int64_t)g.count * tri(tiles(g.n, 128));
+      squares += t;
+      parts += t * std::min<int64_t>(tiles(g.m, 256), kMaxSplits);
+      across += (int64_t)g.count * tiles(g.n, 128) * tiles(g.m, 128);
     }
+    p.gram = !p.small && parts >= kEnough ? 128 : 64;
+    p.square = !p.small && squares >= kEnough ? 128 : 64;
+    p.apply = !p.small && across >= kEnough ? 128 : 64;
+    int64_t sums = 0;
+    for (int i = 0; i < p.groups.count; ++i)
+      sums += (int64_t)p.groups.g[i].count * tri(tiles(p.groups.g[i].n, p.gram));
     int64_t base = 0;
     for (int i = 0; i < p.groups.count; ++i) {
       Group& g = p.groups.g[i];
-      const int64_t stages = padded(g.m, kPad) / 64;   // at least four to a part
+      const int64_t stages = tiles(g.m, 64);   // at least four to a part
       g.splits = (int)std::max<int64_t>(
-          1, std::min({kWantSums / std::max<int64_t>(tiles, 1), stages / 4, (int64_t)kMaxSplits}));
+          1, std::min({tiles(kWantSums, (int)std::min<int64_t>(sums, kWantSums)), (int)(stages / 4),
+                       kMaxSplits}));
       g.blocks = (int)std::min<int64_t>(kMaxBlocks, ((int64_t)g.n * g.m + 8191) / 8192);
-      lay_out(g, kind, p.tile);
+      lay_out(g, kind, p.gram);
       g.base = base;
       base += g.stride * g.count;
     }
@@ -979,14 +1026,24 @@ hipError_t by_matrix(const Pass& p, A& a, Size size, Fill fill, Go go) {
     if (hipError_t e_ = (expr)) return e_;           \
   } while (0)
 
-template <int T>
+// Stages in flight: two of a 128 tile (64 KB) leave room for a second workgroup on the CU.
+constexpr int ring(int tile) { return tile == 128 ? 2 : 4; }
+
+template <typename Fn>
+hipError_t by_tile(int tile, Fn fn) {
+  return tile == 128 ? fn(std::integral_constant<int, 128>()) : fn(std::integral_constant<int, 64>());
+}
+template <typename Fn>
+hipError_t by_flag(bool flag, Fn fn) {
+  return flag ? fn(std::true_type()) : fn(std::false_type());
+}
+
 struct Engine {
-  static constexpr int kRing = T == 128 ? 2 : 4;
   const Pass& p;
   const std::vector<Item>& items;
   const Numbers& z;
   const Call& c;
-  bool pair, second = false;
+  bool pair, second;
   uint8_t* ws;
   hipStream_t st;
 
@@ -1013,38 +1070,49 @@ struct Engine {
     return c.x_bf ? halves<true, false>() : halves<false, false>();
   }
   hipError_t gram(float unit, int to) {
-    Groups a = p.groups;
-    int64_t blocks = spread(a, [](const Group& g) { return (int64_t)tri(g.nt / T) * g.splits; });
-    auto kernel = pair ? dora_orthogonal_gram<T, kRing, true> : dora_orthogonal_gram<T, kRing, false>;
-    ORTHO_TRY(launch("orthogonal_gram", kernel, blocks, st, a, (uint32_t)blocks, second, ws));
-    blocks = spread(a, [](const Group& g) { return (int64_t)tri(g.nt / T) * (T / 32) * (T / 32); });
-    return launch("orthogonal_gather", dora_orthogonal_gather<T>, blocks, st, a, c.eps, unit,
-                  std::ldexp(1.f, to), ws);
+    return by_tile(p.gram, [&](auto tile) {
+      constexpr int T = decltype(tile)::value;
+      Groups a = p.groups;
+      int64_t blocks = spread(a, [](const Group& g) { return (int64_t)tri(tiles(g.n, T)) * g.splits; });
+      auto kernel = pair ? dora_orthogonal_gram<T, ring(T), true> : dora_orthogonal_gram<T, ring(T), false>;
+      ORTHO_TRY(launch("orthogonal_gram", kernel, blocks, st, a, (uint32_t)blocks, second, ws));
+      blocks = spread(a, [](const Group& g) {
+        return (int64_t)tri(tiles(g.n, T)) * (T / 32) * (T / 32);
+      });
+      return launch("orthogonal_gather", dora_orthogonal_gather<T>, blocks, st, a, c.eps, unit,
+                    std::ldexp(1.f, to), ws);
+    });
   }
   template <bool POLY>
   hipError_t squares(Square one, const Square* two = nullptr) {
-    Squares a;
-    a.groups = p.groups;
-    const int64_t blocks = spread(a.groups, [](const Group& g) { return (int64_t)tri(g.nt / T); });
-    a.half = (uint32_t)blocks;
-    a.total = (uint32_t)(two ? 2 * blocks : blocks);
-    a.q[0] = one;
-    a.q[1] = two ? *two : one;
-    return launch(POLY ? "orthogonal_poly" : "orthogonal_square",
-                  dora_orthogonal_square<T, kRing, POLY>, a.total, st, a, ws);
+    return by_tile(p.square, [&](auto tile) {
+      constexpr int T = decltype(tile)::value;
+      Squares a;
+      a.groups = p.groups;
+      const int64_t blocks = spread(a.groups, [](const Group& g) { return (int64_t)tri(tiles(g.n, T)); });
+      a.half = (uint32_t)blocks;
+      a.total = (uint32_t)(two ? 2 * blocks : blocks);
+      a.q[0] = one;
+      a.q[1] = two ? *two : one;
+      return launch(POLY ? "orthogonal_poly" : "orthogonal_square",
+                    dora_orthogonal_square<T, ring(T), POLY>, a.total, st, a, ws);
+    });
   }
   hipError_t between(int q, int e) {
-    Groups a = p.groups;
-    const int64_t blocks =
-        spread(a, [](const Group& g) { return (int64_t)(g.nt / T) * (g.mt / T); });
-    auto kernel = pair ? dora_orthogonal_between<T, kRing, true> : dora_orthogonal_between<T, kRing, false>;
-    ORTHO_TRY(launch("orthogonal_between", kernel, blocks, st, a, (uint32_t)blocks, q,
-                     std::ldexp(1.f, e), second, ws));
+    ORTHO_TRY(by_tile(p.apply, [&](auto tile) {
+      constexpr int T = decltype(tile)::value;
+      Groups a = p.groups;
+      const int64_t blocks =
+          spread(a, [](const Group& g) { return (int64_t)tiles(g.n, T) * tiles(g.m, T); });
+      auto kernel = pair ? dora_orthogonal_between<T, ring(T), true> : dora_orthogonal_between<T, ring(T), false>;
+      return launch("orthogonal_between", kernel, blocks, st, a, (uint32_t)blocks, q,
+                    std::ldexp(1.f, e), second, ws);
+    }));
     pair = true;
     second = !second;
     return hipSuccess;
   }
-  template <bool PAIR, bool BF, Result WHAT>
+  template <bool BF, Result WHAT>
   hipError_t apply(int q, int e) {
     Sinks a;
     a.q = q;
@@ -1052,20 +1120,24 @@ struct Engine {
     a.second = second;
     a.decay = c.decay;
     a.rest = c.rest;
-    auto size = [](const Group& g) { return (int64_t)((g.n + T - 1) / T) * ((g.m + T - 1) / T); };
     auto fill = [&](int slot, int item) { a.s[slot] = items[item].to; };
-    return by_matrix(p, a, size, fill, [&](int64_t blocks) {
-      a.total = (uint32_t)blocks;
-      return launch("orthogonal_apply", dora_orthogonal_apply<T, kRing, PAIR, BF, WHAT>, blocks, st,
-                    a, ws);
+    return by_tile(p.apply, [&](auto tile) {
+      return by_flag(pair, [&](auto pair_) {
+        constexpr int T = decltype(tile)::value;
+        auto size = [](const Group& g) { return (int64_t)tiles(g.n, T) * tiles(g.m, T); };
+        return by_matrix(p, a, size, fill, [&](int64_t blocks) {
+          a.total = (uint32_t)blocks;
+          return launch("orthogonal_apply",
+                        dora_orthogonal_apply<T, ring(T), decltype(pair_)::value, BF, WHAT>, blocks,
+                        st, a, ws);
+        });
+      });
     });
   }
-  template <bool PAIR>
   hipError_t finish(int q, int e) {
-    if (c.what == kMaster) return apply<PAIR, true, kMaster>(q, e);
-    if (c.what == kParam)
-      return c.out_bf ? apply<PAIR, true, kParam>(q, e) : apply<PAIR, false, kParam>(q, e);
-    return c.out_bf ? apply<PAIR, true, kOut>(q, e) : apply<PAIR, false, kOut>(q, e);
+    if (c.what == kMaster) return apply<true, kMaster>(q, e);
+    if (c.what == kParam) return c.out_bf ? apply<true, kParam>(q, e) : apply<false, kParam>(q, e);
+    return c.out_bf ? apply<true, kOut>(q, e) : apply<false, kOut>(q, e);
   }
 
   hipError_t run() {
@@ -1103,21 +1175,15 @@ struct Engine {
       if (!last)
         ORTHO_TRY(squares<false>(Square{pi, R, S, two(z.s[k + 1] - z.p[k] - z.r[k]), 0.f, 0.f, 0}));
     }
-    return pair ? finish<true>(q, eq) : finish<false>(q, eq);
+    return finish(q, eq);
   }
 };
 
 hipError_t run_all(const std::vector<Item>& items, const Kind& kind, const Numbers& z, const Call& c,
                    void* ws, hipStream_t st) {
   for (const Pass& p : passes(items, kind)) {
-    uint8_t* w = reinterpret_cast<uint8_t*>(ws);
-    if (p.tile == 128) {
-      Engine<128> e{p, items, z, c, kind.pair, false, w, st};
-      ORTHO_TRY(e.run());
-    } else {
-      Engine<64> e{p, items, z, c, kind.pair, false, w, st};
-      ORTHO_TRY(e.run());
-    }
+    Engine e{p, items, z, c, kind.pair, false, reinterpret_cast<uint8_t*>(ws), st};
+    ORTHO_TRY(e.run());
   }
   return hipSuccess;
 }
