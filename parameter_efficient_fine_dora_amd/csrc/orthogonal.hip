@@ -45,10 +45,12 @@ typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 typedef __amdgpu_buffer_rsrc_t Rsrc;
 
 constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
 constexpr int kRowBytes = 128;       // of a row in one stage
 constexpr int kPairBlock = 32;       // columns of a pair row's block
 constexpr int kMaxGroups = 12;
 constexpr int kMaxMatrices = 48;     // of one launch that needs their addresses
+constexpr int kMaxSteps = 16;
 constexpr int kMaxBlocks = 1024;     // workgroups that look for one matrix's largest element
 constexpr int kMaxSplits = 32;
 
@@ -67,7 +69,7 @@ struct Group {
   int64_t xk, xt;      // X as [n, m] and [m, n]
   int64_t xk2, xt2;    // the same of the product formed on the way
   int64_t sq[5];       // n x n pairs: S, P, P S, and Q twice
-  int64_t part;        // partial sums of S, float32
+  int64_t part, trace; // partial sums of S and of its trace, float32
   int64_t most, scale; // partial maxima; the factor on X
   bool tall;           // rows are the longer side
 };
@@ -88,7 +90,6 @@ __device__ __forceinline__ void tri_tile(int t, int nt, int& ti, int& tj) {
   ti = row;
   tj = row + t;
 }
-__device__ __forceinline__ int diagonal_tile(int t, int nt) { return t * nt - t * (t - 1) / 2; }
 
 // Neighbouring tiles on one XCD: workgroups go round the eight of them.
 __device__ __forceinline__ uint32_t by_xcd(uint32_t id, uint32_t total) {
@@ -126,17 +127,19 @@ struct Side {
   int wrap;
 };
 
-// A T x T tile of A B^T over the stages [k0, k0 + steps): four waves, each a quarter.  acc[i][j]
+// A T x T tile of A B^T over the stages [k0, k0 + steps): each of four waves has a quarter, of eight
+// waves two share one, each half of every stage (stage() adds them).  acc[i][j]
 // are 32 x 32 blocks; in block (i, j) a lane has row lane % 32 of A's side and, as element
 // 4 g + e, column 8 g + 4 (lane / 32) + e of B's.
 //
 // PAIR: three products of every hi + lo pair of fragments, 12 matrix instructions to 8 fragments
 // read from LDS at T = 128 (single: 4 to 4).  RING stages are in flight.
-template <int T, int RING, bool PAIR>
+template <int T, int RING, bool PAIR, int WAVES = 4>
 struct Product {
   static constexpr int kB = T / 64;                       // blocks of a wave along a side
   static constexpr int kStage = 2 * T * kRowBytes;
-  static constexpr int kCopies = 2 * T / 8 / 4;           // of a wave and stage, 8 rows each
+  static constexpr int kCopies = 2 * T / 8 / WAVES;       // of a wave and stage, 8 rows each
+  static constexpr int kHalves = WAVES / 4;               // waves that share a quarter
   static constexpr int kLds = RING * kStage;
 
   __device__ static __forceinline__ void run(uint8_t* sm, const Side& a, const Side& b, int k0,
@@ -147,7 +150,7 @@ struct Product {
     uint32_t off[kCopies];
 #pragma unroll
     for (int q = 0; q < kCopies; ++q) {
-      const int row = (wave + 4 * q) * 8 + (lane >> 3);   // of both sides, A's first
+      const int row = (wave + WAVES * q) * 8 + (lane >> 3);   // of both sides, A's first
       const int64_t ld = row < T ? a.ld : b.ld;
       off[q] = (uint32_t)((row & (T - 1)) * ld) + (uint32_t)(((lane & 7) ^ swz(row)) << 4);
     }
@@ -156,9 +159,10 @@ struct Product {
       uint8_t* dst = sm + slot * kStage;
 #pragma unroll
       for (int q = 0; q < kCopies; ++q) {
-        const bool first = (4 * q) * 8 < T;   // a copy's rows are all of one side
+        const bool first = WAVES * q * 8 < T;   // a copy's rows are all of one side
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            first ? ra : rb, (__attribute__((address_space(3))) void*)(dst + (wave + 4 * q) * 1024),
+            first ? ra : rb,
+            (__attribute__((address_space(3))) void*)(dst + (wave + WAVES * q) * 1024),
             16, (int)off[q], (first ? ka : kb) * kRowBytes, 0, 0);
       }
       if (++ka == a.wrap) ka = 0;
@@ -173,7 +177,8 @@ struct Product {
     const int pre = min(RING, steps);
     for (int s = 0; s < pre; ++s) issue(s);
     const int rowa = (wave & 1) * (T / 2) + (lane & 31);
-    const int rowb = T + (wave >> 1) * (T / 2) + (lane & 31);
+    const int rowb = T + ((wave >> 1) & 1) * (T / 2) + (lane & 31);
+    const int half = wave >> 2;   // which of its quarter's sums a wave takes
     int slot = 0;
     for (int s = 0; s < steps; ++s) {
       // the stage has landed once only the copies of the stages behind it are in flight
@@ -187,31 +192,35 @@ struct Product {
       auto frag = [&](int row, int chunk) {
         return *reinterpret_cast<const f16x8*>(src + row * kRowBytes + ((chunk ^ swz(row)) << 4));
       };
-      constexpr int kSub = PAIR ? 2 : 4;
+      // all of the wave's fragments first: the later ones arrive while the first are multiplied
+      constexpr int kSub = (PAIR ? 2 : 4) / kHalves;
+      f16x8 fa[kSub][kB], fb[kSub][kB], la[kSub][kB], lb[kSub][kB];
 #pragma unroll
       for (int u = 0; u < kSub; ++u) {
-        const int ch = u * 2 + (lane >> 5);
-        f16x8 fa[kB], fb[kB], la[kB], lb[kB];
+        const int ch = (u + half * kSub) * 2 + (lane >> 5);
 #pragma unroll
         for (int i = 0; i < kB; ++i) {
-          fa[i] = frag(rowa + 32 * i, ch);
-          fb[i] = frag(rowb + 32 * i, ch);
+          fa[u][i] = frag(rowa + 32 * i, ch);
+          fb[u][i] = frag(rowb + 32 * i, ch);
           if (PAIR) {
-            la[i] = frag(rowa + 32 * i, ch + 4);
-            lb[i] = frag(rowb + 32 * i, ch + 4);
+            la[u][i] = frag(rowa + 32 * i, ch + 4);
+            lb[u][i] = frag(rowb + 32 * i, ch + 4);
           }
         }
+      }
+#pragma unroll
+      for (int u = 0; u < kSub; ++u)
 #pragma unroll
         for (int i = 0; i < kB; ++i)
 #pragma unroll
           for (int j = 0; j < kB; ++j) {
+            auto& c = acc[i][j];
             if (PAIR) {
-              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fb[j], la[i], acc[i][j], 0, 0, 0);
-              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(lb[j], fa[i], acc[i][j], 0, 0, 0);
+              c = __builtin_amdgcn_mfma_f32_32x32x16_f16(fb[u][j], la[u][i], c, 0, 0, 0);
+              c = __builtin_amdgcn_mfma_f32_32x32x16_f16(lb[u][j], fa[u][i], c, 0, 0, 0);
             }
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fb[j], fa[i], acc[i][j], 0, 0, 0);
+            c = __builtin_amdgcn_mfma_f32_32x32x16_f16(fb[u][j], fa[u][i], c, 0, 0, 0);
           }
-      }
       barrier_nofence();   // every wave has read the slot before it is filled again
       if (s + RING < steps) issue(slot);
       if (++slot == RING) slot = 0;
@@ -227,18 +236,15 @@ struct Product {
   __device__ static __forceinline__ float* stage(uint8_t* sm, const f32x16 (&acc)[kB][kB]) {
     static_assert(T * T * 4 <= kLds, "the tile fits where the stages were");
     float* tile = reinterpret_cast<float*>(sm);
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
-    for (int i = 0; i < kB; ++i)
-#pragma unroll
-      for (int j = 0; j < kB; ++j)
-#pragma unroll
-        for (int g = 0; g < 4; ++g)
-          *reinterpret_cast<f32x4*>(at(tile, (wave & 1) * (T / 2) + 32 * i + (lane & 31),
-                                       (wave >> 1) * (T / 2) + 32 * j + 8 * g + 4 * (lane >> 5))) =
-              f32x4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2],
-                    acc[i][j][4 * g + 3]};
-    __syncthreads();
+    for (int half = 0; half < kHalves; ++half) {
+      if (kHalves == 1 || (int)threadIdx.x / 256 == half)
+        each(acc, [&](int r, int c, f32x4 v) {
+          f32x4* p = reinterpret_cast<f32x4*>(at(tile, r, c));
+          *p = half ? *p + v : v;
+        });
+      __syncthreads();
+    }
     return tile;
   }
   // Eight columns of a row, and eight rows of a column.
@@ -258,8 +264,8 @@ struct Product {
   template <typename Fn>
   __device__ static __forceinline__ void lines(Fn fn) {
 #pragma unroll
-    for (int i = 0; i < T * T / 8 / kThreads; ++i) {
-      const int x = i * kThreads + threadIdx.x;
+    for (int i = 0; i < T * T / 8 / (WAVES * 64); ++i) {
+      const int x = i * WAVES * 64 + threadIdx.x;
       fn(x / (T / 8), x % (T / 8) * 8);
     }
   }
@@ -274,7 +280,7 @@ struct Product {
 #pragma unroll
         for (int g = 0; g < 4; ++g)
           fn((wave & 1) * (T / 2) + 32 * i + (lane & 31),
-             (wave >> 1) * (T / 2) + 32 * j + 8 * g + 4 * (lane >> 5),
+             ((wave >> 1) & 1) * (T / 2) + 32 * j + 8 * g + 4 * (lane >> 5),
              f32x4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2],
                    acc[i][j][4 * g + 3]});
   }
@@ -509,11 +515,20 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_gram(const Groups a,
   P::each(acc, [&](int i, int j, const f32x4& v) {
     *reinterpret_cast<f32x4*>(out + i * T + j) = v;
   });
+  if (ti != tj) return;
+  float sum = 0.f;
+  P::each(acc, [&](int i, int j, const f32x4& v) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum += i == j + e ? v[e] : 0.f;
+  });
+  sum = wave_sum(sum);
+  if ((threadIdx.x & 63) == 0)
+    reinterpret_cast<float*>(own + g.trace)[(ti * g.splits + split) * kWaves + threadIdx.x / 64] = sum;
 }
 
 // Adds S's partial sums in order, and makes it a pair.  `unit` 0: X is normalised here: the factor
 // 1 / (|X| + eps) comes from the trace, which every workgroup adds up for itself in the same order
-// (n numbers a split, from L2).  Otherwise the factor is `unit`.
+// (four numbers for each split of a tile).  Otherwise the factor is `unit`.
 template <int T>
 __global__ __launch_bounds__(kThreads) void dora_orthogonal_gather(const Groups a, float eps,
                                                                    float unit, float to,
@@ -536,10 +551,8 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_gather(const Groups 
   float r = unit;
   if (unit == 0.f) {
     float sum[1] = {0.f};
-    for (int i = threadIdx.x; i < g.n; i += kThreads) {
-      const float* d = part + (int64_t)diagonal_tile(i / T, nt) * g.splits * T * T + (i % T) * (T + 1);
-      for (int s = 0; s < g.splits; ++s) sum[0] += d[(int64_t)s * T * T];
-    }
+    const float* d = reinterpret_cast<const float*>(own + g.trace);
+    for (int i = threadIdx.x; i < nt * g.splits * kWaves; i += kThreads) sum[0] += d[i];
     block_sum<kThreads / 64, 1>(sum, lds);
     const int e = exponent_of(reinterpret_cast<const uint32_t*>(own + g.most), g.blocks, lds_most);
     r = 1.f / (sqrtf(sum[0]) + ldexpf(eps, e));
@@ -587,9 +600,9 @@ struct Squares {
   uint32_t total, half;      // workgroups; where the second product starts (total: there is none)
   Square q[2];
 };
-template <int T, int RING, bool POLY>
-__global__ __launch_bounds__(kThreads) void dora_orthogonal_square(const Squares a, uint8_t* ws) {
-  using P = Product<T, RING, true>;
+template <int T, int RING, int WAVES, bool POLY>
+__global__ __launch_bounds__(WAVES * 64) void dora_orthogonal_square(const Squares a, uint8_t* ws) {
+  using P = Product<T, RING, true, WAVES>;
   __shared__ __attribute__((aligned(1024))) uint8_t sm[P::kLds];
   uint32_t id = by_xcd(blockIdx.x, a.total);
   const Square& q = a.q[id >= a.half ? 1 : 0];
@@ -642,6 +655,175 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_square(const Squares
     P::column8(tile, r, c, v);
     put(j0 + c, i0 + r, v);
   });
+}
+
+// All of a segment's n x n products for n <= 64: one workgroup a matrix, with S, P, P S and Q in
+// LDS.  A product is 12 matrix instructions of each of four waves, and the 14 products of five
+// steps take 11 us where as many launches take 70.
+struct Chain {
+  Groups groups;
+  int steps;
+  float unit, eps, to;                 // as dora_orthogonal_gather's
+  int pair;                            // Q's rows as pairs, or flat
+  float poly[kMaxSteps][3];            // factors of S S, S and 1
+  float ps[kMaxSteps], pq[kMaxSteps], next[kMaxSteps];   // of P S, P Q and P (P S)
+};
+__global__ __launch_bounds__(kThreads) void dora_orthogonal_chain(const Chain a, uint8_t* ws) {
+  constexpr int kN = 64, kLd = kN * 4;   // bytes of a pair row: 16 chunks, swizzled by the row
+  __shared__ __attribute__((aligned(1024))) uint8_t sm[4][kN * kLd];
+  __shared__ float lds[kThreads / 64];
+  __shared__ uint32_t lds_most[kThreads / 64];
+  const Group& g = a.groups.g[group_of(a.groups, blockIdx.x)];
+  uint8_t* own = ws + g.base + (int64_t)(blockIdx.x - g.from) * g.stride;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  float r = a.unit;
+  if (r == 0.f) {
+    float sum[1] = {0.f};
+    const float* d = reinterpret_cast<const float*>(own + g.trace);
+    for (int i = threadIdx.x; i < g.splits * kWaves; i += kThreads) sum[0] += d[i];
+    block_sum<kThreads / 64, 1>(sum, lds);
+    const int e = exponent_of(reinterpret_cast<const uint32_t*>(own + g.most), g.blocks, lds_most);
+    r = 1.f / (sqrtf(sum[0]) + ldexpf(a.eps, e));
+  }
+  if (threadIdx.x == 0) *reinterpret_cast<float*>(own + g.scale) = r;
+  // chunk c (16 bytes) of row i; columns k .. of a pair row lie in chunks of 8
+  auto chunk = [&](int m, int i, int c) { return sm[m] + i * kLd + ((c ^ (i & 15)) << 4); };
+  auto put = [&](int m, int i, int k, const float* v) {   // four columns
+    f16x4 h, l;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      f16 x, y;
+      split(v[e], x, y);
+      h[e] = x;
+      l[e] = y;
+    }
+    const int c = (k >> 5) * 8 + ((k & 31) >> 3);
+    *reinterpret_cast<f16x4*>(chunk(m, i, c) + (k & 4) * 2) = h;
+    *reinterpret_cast<f16x4*>(chunk(m, i, c + 4) + (k & 4) * 2) = l;
+  };
+  auto get = [&](int m, int i, int k, float* v) {
+    const int c = (k >> 5) * 8 + ((k & 31) >> 3);
+    const f16x4 h = *reinterpret_cast<const f16x4*>(chunk(m, i, c) + (k & 4) * 2);
+    const f16x4 l = *reinterpret_cast<const f16x4*>(chunk(m, i, c + 4) + (k & 4) * 2);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = (float)h[e] + (float)l[e];
+  };
+  constexpr int S = 0, P = 1, R = 2, Q = 3;
+  const float* part = reinterpret_cast<const float*>(own + g.part);
+  constexpr int kMine = kN * kN / 4 / kThreads;
+  f32x4 sums[kMine] = {};
+  for (int s = 0; s < g.splits; s += 4) {   // every load of four splits in flight
+    f32x4 w[kMine][4];
+#pragma unroll
+    for (int u = 0; u < kMine; ++u)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        w[u][q] = *reinterpret_cast<const f32x4*>(part + (int64_t)min(s + q, g.splits - 1) * kN * kN +
+                                                  (u * kThreads + threadIdx.x) * 4);
+#pragma unroll
+    for (int u = 0; u < kMine; ++u)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (s + q < g.splits) sums[u] += w[u][q];
+  }
+#pragma unroll
+  for (int u = 0; u < kMine; ++u) {
+    const int x = u * kThreads + threadIdx.x;
+    float v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = sums[u][e] * r * r * a.to;
+    put(S, x / 16, x % 16 * 4, v);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < kMine; ++u) {   // the upper triangle's values on both sides: S is symmetric
+    const int x = u * kThreads + threadIdx.x, i = x / 16, j = x % 16 * 4;
+    if (j >= i) continue;
+    float v[4], o[4];
+    get(S, i, j, v);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      get(S, min(j + e, i), i & ~3, o);
+      if (j + e < i) v[e] = (i & 3) == 0 ? o[0] : (i & 3) == 1 ? o[1] : (i & 3) == 2 ? o[2] : o[3];
+    }
+    put(S, i, j, v);
+  }
+  const int rowa = (wave & 1) * 32 + (lane & 31), rowb = (wave >> 1) * 32 + (lane & 31);
+  auto product = [&](int x, int y, f32x16& acc) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[e] = 0.f;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int c = (u >> 1) * 8 + (u & 1) * 2 + (lane >> 5);
+      const f16x8 fa = *reinterpret_cast<const f16x8*>(chunk(x, rowa, c));
+      const f16x8 la = *reinterpret_cast<const f16x8*>(chunk(x, rowa, c + 4));
+      const f16x8 fb = *reinterpret_cast<const f16x8*>(chunk(y, rowb, c));
+      const f16x8 lb = *reinterpret_cast<const f16x8*>(chunk(y, rowb, c + 4));
+      acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(fb, la, acc, 0, 0, 0);
+      acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(lb, fa, acc, 0, 0, 0);
+      acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(fb, fa, acc, 0, 0, 0);
+    }
+  };
+  // fn(row, first of four columns, values)
+  auto each = [&](const f32x16& acc, auto fn) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float v[4] = {acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]};
+      fn((wave & 1) * 32 + (lane & 31), (wave >> 1) * 32 + 8 * q + 4 * (lane >> 5), v);
+    }
+  };
+  f32x16 x, y;
+  for (int k = 0; k < a.steps; ++k) {
+    const bool last = k + 1 == a.steps;
+    __syncthreads();
+    product(S, S, x);
+    const int p = k == 0 ? Q : P;   // the first P is Q
+    each(x, [&](int i, int j, float* v) {
+      float s[4];
+      get(S, i, j, s);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[e] = fmaf(a.poly[k][1], s[e], v[e] * a.poly[k][0]);
+        if (i == j + e && i < g.n) v[e] += a.poly[k][2];
+      }
+      put(p, i, j, v);
+    });
+    __syncthreads();
+    if (!last) product(p, S, x);
+    if (k > 0) {
+      product(P, Q, y);
+      __syncthreads();   // Q has been read
+      each(y, [&](int i, int j, float* v) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] *= a.pq[k];
+        put(Q, i, j, v);
+      });
+    }
+    if (last) break;
+    each(x, [&](int i, int j, float* v) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] *= a.ps[k];
+      put(R, i, j, v);
+    });
+    __syncthreads();
+    // (k = 0: P is Q, which the products after the next barrier replace)
+    product(p, R, x);
+    each(x, [&](int i, int j, float* v) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] *= a.next[k];
+      put(S, i, j, v);
+    });
+  }
+  __syncthreads();
+  f16* out = reinterpret_cast<f16*>(own + g.sq[0]);
+#pragma unroll
+  for (int u = 0; u < kN * 16 / kThreads; ++u) {
+    const int t = u * kThreads + threadIdx.x, i = t / 16, c = t % 16;
+    const f16x8 v = *reinterpret_cast<const f16x8*>(chunk(Q, i, c));
+    // flat: 32 columns of a block, then the lo 64 columns on
+    const int at = a.pair ? c * 8 : (c >> 3) * 32 + (c & 3) * 8 + ((c & 4) ? kN : 0);
+    *reinterpret_cast<f16x8*>(out + i * 2 * kN + at) = v;
+  }
 }
 
 // ---- Q X ----------------------------------------------------------------------------------------
@@ -761,11 +943,10 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_between(const Groups
   });
 }
 
-static_assert(sizeof(Sinks) <= 4000 && sizeof(Sources) <= 4000 && sizeof(Squares) <= 4000,
+static_assert(sizeof(Sinks) <= 4000 && sizeof(Chain) <= 4000 && sizeof(Sources) <= 4000 && sizeof(Squares) <= 4000,
               "kernel arguments");
 
 // ---- host: the iteration's numbers ------------------------------------------------------------
-constexpr int kMaxSteps = 16;
 
 double largest(double l, double (*f)(double, const double*), const double* abc, double q1, double q2) {
   double m = std::max(std::fabs(f(0.0, abc)), std::fabs(f(l, abc)));
@@ -887,6 +1068,7 @@ void lay_out(Group& g, const Kind& k, int gram) {
   }
   for (int64_t& s : g.sq) s = take((int64_t)g.nt * g.nt * 4);
   g.part = take((int64_t)tri(tiles(g.n, gram)) * g.splits * gram * gram * 4);
+  g.trace = take((int64_t)tiles(g.n, gram) * g.splits * kWaves * 4);
   g.most = take((int64_t)g.blocks * 4);
   g.scale = take(4);
   g.stride = at;
@@ -941,7 +1123,7 @@ std::vector<Pass> passes(const std::vector<Item>& items, const Kind& kind) {
       across += (int64_t)g.count * tiles(g.n, 128) * tiles(g.m, 128);
     }
     p.gram = !p.small && parts >= kEnough ? 128 : 64;
-    p.square = !p.small && squares >= kEnough ? 128 : 64;
+    p.square = !p.small && squares >= kEnough / 2 ? 128 : 64;
     p.apply = !p.small && across >= kEnough ? 128 : 64;
     int64_t sums = 0;
     for (int i = 0; i < p.groups.count; ++i)
@@ -990,11 +1172,11 @@ struct Identity {
 template <typename T>
 using identity_t = typename Identity<T>::type;
 
-template <typename... Args>
+template <int THREADS = kThreads, typename... Args>
 hipError_t launch(const char* label, void (*kernel)(Args...), int64_t blocks, hipStream_t st,
                   identity_t<Args>... args) {
   LaunchTimer timer(label, st);
-  hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(kThreads), 0, st, args...);
+  hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(THREADS), 0, st, args...);
   return hipGetLastError();
 }
 
@@ -1025,6 +1207,9 @@ hipError_t by_matrix(const Pass& p, A& a, Size size, Fill fill, Go go) {
   do {                                               \
     if (hipError_t e_ = (expr)) return e_;           \
   } while (0)
+
+constexpr int kSquareWaves = 8;
+float two(int e) { return std::ldexp(1.f, e); }
 
 // Stages in flight: two of a 128 tile (64 KB) leave room for a second workgroup on the CU.
 constexpr int ring(int tile) { return tile == 128 ? 2 : 4; }
@@ -1069,6 +1254,7 @@ struct Engine {
     if (c.moment) return c.x_bf ? halves<true, true>() : halves<false, true>();
     return c.x_bf ? halves<true, false>() : halves<false, false>();
   }
+  // S of the current X; `unit` as dora_orthogonal_gather takes it
   hipError_t gram(float unit, int to) {
     return by_tile(p.gram, [&](auto tile) {
       constexpr int T = decltype(tile)::value;
@@ -1076,6 +1262,7 @@ struct Engine {
       int64_t blocks = spread(a, [](const Group& g) { return (int64_t)tri(tiles(g.n, T)) * g.splits; });
       auto kernel = pair ? dora_orthogonal_gram<T, ring(T), true> : dora_orthogonal_gram<T, ring(T), false>;
       ORTHO_TRY(launch("orthogonal_gram", kernel, blocks, st, a, (uint32_t)blocks, second, ws));
+      if (p.small) return hipSuccess;   // the chain gathers it
       blocks = spread(a, [](const Group& g) {
         return (int64_t)tri(tiles(g.n, T)) * (T / 32) * (T / 32);
       });
@@ -1094,8 +1281,8 @@ struct Engine {
       a.total = (uint32_t)(two ? 2 * blocks : blocks);
       a.q[0] = one;
       a.q[1] = two ? *two : one;
-      return launch(POLY ? "orthogonal_poly" : "orthogonal_square",
-                    dora_orthogonal_square<T, ring(T), POLY>, a.total, st, a, ws);
+      return launch<kSquareWaves * 64>(POLY ? "orthogonal_poly" : "orthogonal_square",
+                    dora_orthogonal_square<T, ring(T), kSquareWaves, POLY>, a.total, st, a, ws);
     });
   }
   hipError_t between(int q, int e) {
@@ -1140,42 +1327,74 @@ struct Engine {
     return c.out_bf ? apply<true, kOut>(q, e) : apply<false, kOut>(q, e);
   }
 
-  hipError_t run() {
-    ORTHO_TRY(start());
-    ORTHO_TRY(gram(0.f, z.s[0]));
+  // The steps [from, to) between two products with X, from S's partial sums; which of sq is Q and
+  // its exponent in q and e.
+  hipError_t chain(int from, int to, float unit, int& q, int& e) {
+    Chain a;
+    a.groups = p.groups;
+    a.steps = to - from;
+    a.unit = unit;
+    a.eps = c.eps;
+    a.to = two(z.s[from]);
+    a.pair = pair;
+    e = z.p[from];
+    for (int k = from; k < to; ++k) {
+      const int i = k - from;
+      a.poly[i][0] = (float)std::ldexp(z.abc[k][2], z.p[k] - 2 * z.s[k]);
+      a.poly[i][1] = (float)std::ldexp(z.abc[k][1], z.p[k] - z.s[k]);
+      a.poly[i][2] = (float)std::ldexp(z.abc[k][0], z.p[k]);
+      a.ps[i] = two(z.r[k] - z.p[k] - z.s[k]);
+      a.next[i] = two(z.s[k + 1] - z.p[k] - z.r[k]);
+      a.pq[i] = two(z.q[k] - z.p[k] - e);
+      if (i > 0) e = z.q[k];
+    }
+    q = 0;
+    const int64_t blocks = spread(a.groups, [](const Group&) { return (int64_t)1; });
+    return launch("orthogonal_chain", dora_orthogonal_chain, blocks, st, a, ws);
+  }
+  hipError_t products(int from, int to, int& q, int& e) {
     constexpr int S = 0, P = 1, R = 2, Qa = 3, Qb = 4;
-    int q = -1, eq = 0;   // Q: P of the first step, so it is written where Q goes
-    auto two = [](int e) { return std::ldexp(1.f, e); };
-    for (int k = 0; k < z.steps; ++k) {
-      if (z.anew[k]) {
-        ORTHO_TRY(between(q, z.x[k] - eq));
-        ORTHO_TRY(gram(two(-z.x[k]), z.s[k]));
-        q = -1;
-      }
-      const bool last = k + 1 == z.steps || z.anew[k + 1];   // Q meets X next
+    for (int k = from; k < to; ++k) {
+      const bool last = k + 1 == to;   // Q meets X next
       const int flat = last && !pair;
-      const int pi = q < 0 ? Qa : P;
+      const int pi = k == from ? Qa : P;   // the first P is Q
       const double* abc = z.abc[k];
       Square poly = {S, S, pi, (float)std::ldexp(abc[2], z.p[k] - 2 * z.s[k]),
                      (float)std::ldexp(abc[1], z.p[k] - z.s[k]), (float)std::ldexp(abc[0], z.p[k]),
-                     q < 0 ? flat : 0};
+                     k == from ? flat : 0};
       ORTHO_TRY(squares<true>(poly));
       const Square ps = {pi, S, R, two(z.r[k] - z.p[k] - z.s[k]), 0.f, 0.f, 0};
-      if (q < 0) {
+      if (k == from) {
         q = Qa;
-        eq = z.p[k];
+        e = z.p[k];
         if (!last) ORTHO_TRY(squares<false>(ps));
       } else {
-        const int to = q == Qa ? Qb : Qa;
-        const Square pq = {P, q, to, two(z.q[k] - z.p[k] - eq), 0.f, 0.f, flat};
+        const int next = q == Qa ? Qb : Qa;
+        const Square pq = {P, q, next, two(z.q[k] - z.p[k] - e), 0.f, 0.f, flat};
         ORTHO_TRY(squares<false>(pq, last ? nullptr : &ps));
-        q = to;
-        eq = z.q[k];
+        q = next;
+        e = z.q[k];
       }
       if (!last)
         ORTHO_TRY(squares<false>(Square{pi, R, S, two(z.s[k + 1] - z.p[k] - z.r[k]), 0.f, 0.f, 0}));
     }
-    return finish(q, eq);
+    return hipSuccess;
+  }
+
+  hipError_t run() {
+    ORTHO_TRY(start());
+    for (int from = 0; from < z.steps;) {
+      int to = from + 1;
+      while (to < z.steps && !z.anew[to]) ++to;
+      const float unit = from ? two(-z.x[from]) : 0.f;
+      ORTHO_TRY(gram(unit, z.s[from]));
+      int q = 0, e = 0;
+      ORTHO_TRY(p.small ? chain(from, to, unit, q, e) : products(from, to, q, e));
+      if (to == z.steps) return finish(q, e);
+      ORTHO_TRY(between(q, z.x[to] - e));
+      from = to;
+    }
+    return hipSuccess;
   }
 };
 
