@@ -16,7 +16,10 @@
 // sums are float32.  For bf16 results that is enough.  For float32 results the product Q X is
 // formed before the factor passes 1024 (after three of five usual steps), and S anew from it.
 // A bf16 X is one half precision number exactly (its bits below 2^-38 of its largest element are
-// left out), a float32 X is hi + lo.
+// left out), a float32 X is hi + lo.  The update of a bf16 parameter is held as two bf16 numbers
+// instead, 16 bits: what is lost is 2^-18 of X, raised 485 times in the worst case, and half a step
+// of the parameter is 2^-8 of it; half precision would need X's largest element first, which is
+// another pass over gradient and momentum.
 //
 // Layout.  A "pair" row holds blocks of 32 columns: 32 hi, then 32 lo, so that the 128 bytes that
 // a stage copies of a row are the hi and lo of 32 columns; a "single" row holds 64 columns there.
@@ -80,7 +83,30 @@ struct Groups {
 
 __host__ __device__ inline int tri(int t) { return t * (t + 1) / 2; }
 
-// Tile t of the upper triangle of nt x nt tiles, row by row.
+// Tile t of the upper triangle of nt x nt tiles: bands of eight rows, column by column, so that
+// neighbours share both their rows and their columns (each XCD has an eighth of the tiles).
+__device__ __forceinline__ void band_tile(int t, int nt, int& ti, int& tj) {
+  constexpr int kBand = 8;
+  int r0 = 0, high = min(nt, kBand);
+  while (true) {   // a band has a triangle, then whole columns
+    const int n = tri(high) + high * (nt - r0 - high);
+    if (t < n) break;
+    t -= n;
+    r0 += high;
+    high = min(nt - r0, kBand);
+  }
+  if (t < tri(high)) {
+    int c = 0;
+    while (t > c) t -= ++c;
+    ti = r0 + t;
+    tj = r0 + c;
+  } else {
+    t -= tri(high);
+    ti = r0 + t % high;
+    tj = r0 + high + t / high;
+  }
+}
+// Tile t of the same, row by row.
 __device__ __forceinline__ void tri_tile(int t, int nt, int& ti, int& tj) {
   int row = 0;
   while (t >= nt - row) {
@@ -102,6 +128,24 @@ __device__ __forceinline__ int group_of(const Groups& a, uint32_t id) {
   return __builtin_amdgcn_readfirstlane(g);
 }
 
+// How X's numbers are held: one half precision number, two of them, or two bf16.
+enum Form { kSingle, kPair, kWide };
+template <Form F>
+struct Number {
+  using T = std::conditional_t<F == kWide, __bf16, f16>;
+  static constexpr bool kTwo = F != kSingle;
+};
+typedef short short8 __attribute__((ext_vector_type(8)));
+template <Form F>
+__device__ __forceinline__ f32x16 multiply(short8 a, short8 b, f32x16 c) {
+  if constexpr (F == kWide)
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a),
+                                                  __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
 // ---- the product loop ---------------------------------------------------------------------
 __device__ __forceinline__ Rsrc rsrc(const void* base, int64_t bytes) {
   const uint64_t a = reinterpret_cast<uint64_t>(base);
@@ -116,6 +160,8 @@ template <int N>
 __device__ __forceinline__ void wait_vm() {
   __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
 }
+// LDS reads that are under way have arrived (lgkmcnt 0).
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 __device__ __forceinline__ void barrier_nofence() { asm volatile("s_barrier" ::: "memory"); }
 __device__ __forceinline__ int swz(int row) { return (row & 7) ^ ((row >> 3) & 7); }
 
@@ -134,8 +180,9 @@ struct Side {
 //
 // PAIR: three products of every hi + lo pair of fragments, 12 matrix instructions to 8 fragments
 // read from LDS at T = 128 (single: 4 to 4).  RING stages are in flight.
-template <int T, int RING, bool PAIR, int WAVES = 4>
+template <int T, int RING, Form F, int WAVES = 4>
 struct Product {
+  static constexpr bool PAIR = F != kSingle;
   static constexpr int kB = T / 64;                       // blocks of a wave along a side
   static constexpr int kStage = 2 * T * kRowBytes;
   static constexpr int kCopies = 2 * T / 8 / WAVES;       // of a wave and stage, 8 rows each
@@ -190,11 +237,11 @@ struct Product {
       barrier_nofence();
       const uint8_t* src = sm + slot * kStage;
       auto frag = [&](int row, int chunk) {
-        return *reinterpret_cast<const f16x8*>(src + row * kRowBytes + ((chunk ^ swz(row)) << 4));
+        return *reinterpret_cast<const short8*>(src + row * kRowBytes + ((chunk ^ swz(row)) << 4));
       };
       // all of the wave's fragments first: the later ones arrive while the first are multiplied
       constexpr int kSub = (PAIR ? 2 : 4) / kHalves;
-      f16x8 fa[kSub][kB], fb[kSub][kB], la[kSub][kB], lb[kSub][kB];
+      short8 fa[kSub][kB], fb[kSub][kB], la[kSub][kB], lb[kSub][kB];
 #pragma unroll
       for (int u = 0; u < kSub; ++u) {
         const int ch = (u + half * kSub) * 2 + (lane >> 5);
@@ -216,12 +263,14 @@ struct Product {
           for (int j = 0; j < kB; ++j) {
             auto& c = acc[i][j];
             if (PAIR) {
-              c = __builtin_amdgcn_mfma_f32_32x32x16_f16(fb[u][j], la[u][i], c, 0, 0, 0);
-              c = __builtin_amdgcn_mfma_f32_32x32x16_f16(lb[u][j], fa[u][i], c, 0, 0, 0);
+              c = multiply<F>(fb[u][j], la[u][i], c);
+              c = multiply<F>(lb[u][j], fa[u][i], c);
             }
-            c = __builtin_amdgcn_mfma_f32_32x32x16_f16(fb[u][j], fa[u][i], c, 0, 0, 0);
+            c = multiply<F>(fb[u][j], fa[u][i], c);
           }
-      barrier_nofence();   // every wave has read the slot before it is filled again
+      // every wave has read the slot, and not only asked for it, before it is filled again
+      wait_lds();
+      barrier_nofence();
       if (s + RING < steps) issue(slot);
       if (++slot == RING) slot = 0;
     }
@@ -289,23 +338,24 @@ struct Product {
 // ---- pairs ----------------------------------------------------------------------------------
 __device__ __forceinline__ int64_t pair_at(int64_t k) { return (k >> 5) * 64 + (k & 31); }
 
-__device__ __forceinline__ void split(float v, f16& hi, f16& lo) {
-  hi = (f16)v;
-  lo = (f16)(v - (float)hi);
+template <typename H>
+__device__ __forceinline__ void split(float v, H& hi, H& lo) {
+  hi = (H)v;
+  lo = (H)(v - (float)hi);
 }
 // Columns [k, k + N) of a pair row; of a flat one, whose lo begin at `lo`.
-template <int N>
-__device__ __forceinline__ void store_pair(f16* row, int64_t k, const float* v, int64_t lo = 0) {
-  typedef _Float16 V __attribute__((ext_vector_type(N)));
+template <int N, typename H = f16>
+__device__ __forceinline__ void store_pair(H* row, int64_t k, const float* v, int64_t lo = 0) {
+  typedef H V __attribute__((ext_vector_type(N)));
   V h, l;
 #pragma unroll
   for (int e = 0; e < N; ++e) {
-    f16 a, b;
+    H a, b;
     split(v[e], a, b);
     h[e] = a;
     l[e] = b;
   }
-  f16* p = row + (lo ? k : pair_at(k));
+  H* p = row + (lo ? k : pair_at(k));
   *reinterpret_cast<V*>(p) = h;
   *reinterpret_cast<V*>(p + (lo ? lo : kPairBlock)) = l;
 }
@@ -332,6 +382,7 @@ struct Sources {
   Source s[kMaxMatrices];
   float mu, nu;                    // momentum's factor, 1 - that
   int nesterov;
+  int fixed;                       // kWide: the power of two that X is multiplied by
 };
 
 __device__ __forceinline__ int matrix_of(const uint32_t* from, int count, uint32_t id) {
@@ -426,9 +477,13 @@ __device__ __forceinline__ int exponent_of(const uint32_t* most, int blocks, uin
 
 // A 64 x 64 block of the padded matrix into both orders, through LDS for the turned one; zeros
 // where the matrix ends.  Memory bounds it: what is read is 2 to 6 bytes an element, written 4 (one
-// number, two orders) or 8.
-template <bool BF, bool MOMENT, bool PAIR>
+// number, two orders) or 8.  bf16 holds float32's range, so kWide needs no largest element: the
+// momentum is moved on here too, in the only pass over it.
+template <bool BF, bool MOMENT, Form F>
 __global__ __launch_bounds__(kThreads) void dora_orthogonal_halves(const Sources a, uint8_t* ws) {
+  using H = typename Number<F>::T;
+  constexpr bool PAIR = Number<F>::kTwo;
+  typedef H H8 __attribute__((ext_vector_type(8)));
   constexpr int kE = 64;
   __shared__ uint32_t tile[kE][kE + 1];
   __shared__ uint32_t lds[kThreads / 64];
@@ -439,14 +494,15 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_halves(const Sources
   const int prows = g.tall ? g.mt : g.nt, pcols = g.tall ? g.nt : g.mt;
   const int across = pcols / kE, block = blockIdx.x - a.from[u];
   const int r0 = block / across * kE, c0 = block % across * kE;
-  const int e = exponent_of(reinterpret_cast<const uint32_t*>(own + g.most), g.blocks, lds);
+  const int e = F == kWide ? a.fixed
+                           : exponent_of(reinterpret_cast<const uint32_t*>(own + g.most), g.blocks, lds);
   const Source s = a.s[u];
-  f16* straight = reinterpret_cast<f16*>(own + (g.tall ? g.xt : g.xk));   // [prows, pcols]
-  f16* turned = reinterpret_cast<f16*>(own + (g.tall ? g.xk : g.xt));     // [pcols, prows]
-  auto put = [&](f16* row, int64_t k, const f16* h, const f16* l) {
-    f16* p = row + (PAIR ? pair_at(k) : k);
-    *reinterpret_cast<f16x8*>(p) = *reinterpret_cast<const f16x8*>(h);
-    if (PAIR) *reinterpret_cast<f16x8*>(p + kPairBlock) = *reinterpret_cast<const f16x8*>(l);
+  H* straight = reinterpret_cast<H*>(own + (g.tall ? g.xt : g.xk));   // [prows, pcols]
+  H* turned = reinterpret_cast<H*>(own + (g.tall ? g.xk : g.xt));     // [pcols, prows]
+  auto put = [&](H* row, int64_t k, const H* h, const H* l) {
+    H* p = row + (PAIR ? pair_at(k) : k);
+    *reinterpret_cast<H8*>(p) = *reinterpret_cast<const H8*>(h);
+    if (PAIR) *reinterpret_cast<H8*>(p + kPairBlock) = *reinterpret_cast<const H8*>(l);
   };
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
@@ -459,11 +515,17 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_halves(const Sources
       if (MOMENT) {
         float m[kVec];
         load8<false>(s.moment, i, stop, m);
+        if (F == kWide) {
+#pragma unroll
+          for (int q = 0; q < kVec; ++q) m[q] = moved(m[q], v[q], a.mu, a.nu);
+          store_part<false>(s.moment, i, stop, m);
+          store_part<false>(s.moment, i + 4, stop, m + 4);
+        }
 #pragma unroll
         for (int q = 0; q < kVec; ++q) v[q] = update_of(m[q], v[q], a);
       }
     }
-    __attribute__((aligned(16))) f16 h[kVec], l[kVec];
+    __attribute__((aligned(16))) H h[kVec], l[kVec];
 #pragma unroll
     for (int q = 0; q < kVec; ++q) {
       split(ldexpf(v[q], e), h[q], l[q]);
@@ -476,12 +538,12 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_halves(const Sources
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     const int c = threadIdx.x / 8 + 32 * half, r = threadIdx.x % 8 * kVec;
-    __attribute__((aligned(16))) f16 h[kVec], l[kVec];
+    __attribute__((aligned(16))) H h[kVec], l[kVec];
 #pragma unroll
     for (int q = 0; q < kVec; ++q) {
       const uint32_t w = tile[r + q][c];
-      h[q] = __builtin_bit_cast(f16, (uint16_t)w);
-      l[q] = __builtin_bit_cast(f16, (uint16_t)(w >> 16));
+      h[q] = __builtin_bit_cast(H, (uint16_t)w);
+      l[q] = __builtin_bit_cast(H, (uint16_t)(w >> 16));
     }
     put(turned + (int64_t)(c0 + c) * prows * (PAIR ? 2 : 1), r0 + r, h, l);
   }
@@ -489,10 +551,11 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_halves(const Sources
 
 // ---- n x n products ---------------------------------------------------------------------------
 // Partial sums of S = X X^T over a part of m, float32.
-template <int T, int RING, bool PAIR>
+template <int T, int RING, Form F>
 __global__ __launch_bounds__(kThreads) void dora_orthogonal_gram(const Groups a, uint32_t total,
                                                                  bool second, uint8_t* ws) {
-  using P = Product<T, RING, PAIR>;
+  using P = Product<T, RING, F>;
+  constexpr bool PAIR = P::PAIR;
   __shared__ __attribute__((aligned(1024))) uint8_t sm[P::kLds];
   const uint32_t id = by_xcd(blockIdx.x, total);
   const Group& g = a.g[group_of(a, id)];
@@ -526,13 +589,26 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_gram(const Groups a,
     reinterpret_cast<float*>(own + g.trace)[(ti * g.splits + split) * kWaves + threadIdx.x / 64] = sum;
 }
 
+// What turns X' X'^T into the first S: X' is X times a power of two, kWide's or the one that its
+// largest element asks for.
+struct Unit {
+  float unit;   // the factor on X' where it is known, else 0
+  float eps;
+  int wide, fixed;
+};
+__device__ __forceinline__ float norm_factor(float trace, const Unit& u, const Group& g, uint8_t* own,
+                                             uint32_t* lds) {
+  const int e = u.wide ? u.fixed
+                       : exponent_of(reinterpret_cast<const uint32_t*>(own + g.most), g.blocks, lds);
+  return 1.f / (sqrtf(trace) + ldexpf(u.eps, e));
+}
+
 // Adds S's partial sums in order, and makes it a pair.  `unit` 0: X is normalised here: the factor
 // 1 / (|X| + eps) comes from the trace, which every workgroup adds up for itself in the same order
 // (four numbers for each split of a tile).  Otherwise the factor is `unit`.
 template <int T>
-__global__ __launch_bounds__(kThreads) void dora_orthogonal_gather(const Groups a, float eps,
-                                                                   float unit, float to,
-                                                                   uint8_t* ws) {
+__global__ __launch_bounds__(kThreads) void dora_orthogonal_gather(const Groups a, const Unit unit,
+                                                                   float to, uint8_t* ws) {
   constexpr int kE = 32, kSide = T / kE;
   __shared__ float tile[kE][kE + 1];
   __shared__ float lds[kThreads / 64];
@@ -548,14 +624,13 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_gather(const Groups 
   tri_tile(t, nt, ti, tj);
   uint8_t* own = ws + g.base + (int64_t)u * g.stride;
   const float* part = reinterpret_cast<const float*>(own + g.part);
-  float r = unit;
-  if (unit == 0.f) {
+  float r = unit.unit;
+  if (r == 0.f) {
     float sum[1] = {0.f};
     const float* d = reinterpret_cast<const float*>(own + g.trace);
     for (int i = threadIdx.x; i < nt * g.splits * kWaves; i += kThreads) sum[0] += d[i];
     block_sum<kThreads / 64, 1>(sum, lds);
-    const int e = exponent_of(reinterpret_cast<const uint32_t*>(own + g.most), g.blocks, lds_most);
-    r = 1.f / (sqrtf(sum[0]) + ldexpf(eps, e));
+    r = norm_factor(sum[0], unit, g, own, lds_most);
   }
   if (piece == 0 && t == 0 && threadIdx.x == 0) *reinterpret_cast<float*>(own + g.scale) = r;
   const int pi = piece / kSide * kE, pj = piece % kSide * kE;
@@ -589,11 +664,11 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_gather(const Groups 
 // A symmetric product of two n x n pairs, or of two such products of one launch (`both`).
 //   POLY: out = alpha (left right) + beta left + gamma 1, left and right both S
 //   otherwise out = alpha (left right)
-// `flat`: out's rows hold all hi, then all lo, as the last product wants them.
+// `form`: as X's form wants Q: kSingle: all hi of a row, then all lo; kWide: pairs of bf16.
 struct Square {
   int left, right, out;      // of sq
   float alpha, beta, gamma;
-  int flat;
+  int form;
 };
 struct Squares {
   Groups groups;
@@ -602,7 +677,7 @@ struct Squares {
 };
 template <int T, int RING, int WAVES, bool POLY>
 __global__ __launch_bounds__(WAVES * 64) void dora_orthogonal_square(const Squares a, uint8_t* ws) {
-  using P = Product<T, RING, true, WAVES>;
+  using P = Product<T, RING, kPair, WAVES>;
   __shared__ __attribute__((aligned(1024))) uint8_t sm[P::kLds];
   uint32_t id = by_xcd(blockIdx.x, a.total);
   const Square& q = a.q[id >= a.half ? 1 : 0];
@@ -612,7 +687,7 @@ __global__ __launch_bounds__(WAVES * 64) void dora_orthogonal_square(const Squar
   const int rest = (int)(id - g.from);
   const int t = rest % tiles, u = rest / tiles;
   int ti, tj;
-  tri_tile(t, nt, ti, tj);
+  band_tile(t, nt, ti, tj);
   uint8_t* own = ws + g.base + (int64_t)u * g.stride;
   const int64_t ld = (int64_t)g.nt * 4, le = ld / 2;
   const int stages = g.ne / kPairBlock;
@@ -637,7 +712,8 @@ __global__ __launch_bounds__(WAVES * 64) void dora_orthogonal_square(const Squar
         if (i == j + e && i < g.n) v[e] += q.gamma;
       }
     }
-    store_pair<8>(out + i * le, j, v, q.flat ? g.ne : 0);
+    if (q.form == kWide) store_pair<8>(reinterpret_cast<__bf16*>(out) + i * le, j, v);
+    else store_pair<8>(out + i * le, j, v, q.form == kSingle ? g.ne : 0);
   };
   P::lines([&](int r, int c) {
     float v[8];
@@ -663,8 +739,9 @@ __global__ __launch_bounds__(WAVES * 64) void dora_orthogonal_square(const Squar
 struct Chain {
   Groups groups;
   int steps;
-  float unit, eps, to;                 // as dora_orthogonal_gather's
-  int pair;                            // Q's rows as pairs, or flat
+  Unit unit;                           // as dora_orthogonal_gather's
+  float to;
+  int form;                            // X's, which says how Q is wanted
   float poly[kMaxSteps][3];            // factors of S S, S and 1
   float ps[kMaxSteps], pq[kMaxSteps], next[kMaxSteps];   // of P S, P Q and P (P S)
 };
@@ -676,14 +753,13 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_chain(const Chain a,
   const Group& g = a.groups.g[group_of(a.groups, blockIdx.x)];
   uint8_t* own = ws + g.base + (int64_t)(blockIdx.x - g.from) * g.stride;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  float r = a.unit;
+  float r = a.unit.unit;
   if (r == 0.f) {
     float sum[1] = {0.f};
     const float* d = reinterpret_cast<const float*>(own + g.trace);
     for (int i = threadIdx.x; i < g.splits * kWaves; i += kThreads) sum[0] += d[i];
     block_sum<kThreads / 64, 1>(sum, lds);
-    const int e = exponent_of(reinterpret_cast<const uint32_t*>(own + g.most), g.blocks, lds_most);
-    r = 1.f / (sqrtf(sum[0]) + ldexpf(a.eps, e));
+    r = norm_factor(sum[0], a.unit, g, own, lds_most);
   }
   if (threadIdx.x == 0) *reinterpret_cast<float*>(own + g.scale) = r;
   // chunk c (16 bytes) of row i; columns k .. of a pair row lie in chunks of 8
@@ -815,13 +891,24 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_chain(const Chain a,
     });
   }
   __syncthreads();
+  if (a.form == kWide) {
+    __bf16* out = reinterpret_cast<__bf16*>(own + g.sq[0]);
+#pragma unroll
+    for (int u = 0; u < kMine; ++u) {
+      const int x = u * kThreads + threadIdx.x, i = x / 16, j = x % 16 * 4;
+      float v[4];
+      get(Q, i, j, v);
+      store_pair<4>(out + i * 2 * kN, j, v);
+    }
+    return;
+  }
   f16* out = reinterpret_cast<f16*>(own + g.sq[0]);
 #pragma unroll
   for (int u = 0; u < kN * 16 / kThreads; ++u) {
     const int t = u * kThreads + threadIdx.x, i = t / 16, c = t % 16;
     const f16x8 v = *reinterpret_cast<const f16x8*>(chunk(Q, i, c));
     // flat: 32 columns of a block, then the lo 64 columns on
-    const int at = a.pair ? c * 8 : (c >> 3) * 32 + (c & 3) * 8 + ((c & 4) ? kN : 0);
+    const int at = a.form == kPair ? c * 8 : (c >> 3) * 32 + (c & 3) * 8 + ((c & 4) ? kN : 0);
     *reinterpret_cast<f16x8*>(out + i * 2 * kN + at) = v;
   }
 }
@@ -846,23 +933,24 @@ struct Sinks {
 };
 enum Result { kOut, kParam, kMaster };
 
-template <int T, int RING, bool PAIR>
+template <int T, int RING, Form F>
 __device__ __forceinline__ void last_product(uint8_t* sm, const Group& g, uint8_t* own, int q,
                                              bool second, bool tall, int64_t row0, int64_t col0,
                                              f32x16 (&acc)[T / 64][T / 64]) {
   // Q's rows are pairs where X's are; else all hi and then all lo against X twice
+  constexpr bool PAIR = Number<F>::kTwo;
   const int64_t ld_q = (int64_t)g.nt * 4, ld_x = (int64_t)g.nt * (PAIR ? 4 : 2);
   const int sq = g.ne / kPairBlock, sx = PAIR ? sq : sq / 2;
   const uint8_t* x = own + (second ? g.xt2 : g.xt);
   const uint8_t* qp = own + g.sq[q];
   const Side qs = {qp + (tall ? col0 : row0) * ld_q, ld_q, sq};
   const Side xs = {x + (tall ? row0 : col0) * ld_x, ld_x, sx};
-  Product<T, RING, PAIR>::run(sm, tall ? xs : qs, tall ? qs : xs, 0, sq, acc);
+  Product<T, RING, F>::run(sm, tall ? xs : qs, tall ? qs : xs, 0, sq, acc);
 }
 
-template <int T, int RING, bool PAIR, bool BF, Result WHAT>
+template <int T, int RING, Form F, bool BF, Result WHAT>
 __global__ __launch_bounds__(kThreads) void dora_orthogonal_apply(const Sinks a, uint8_t* ws) {
-  using P = Product<T, RING, PAIR>;
+  using P = Product<T, RING, F>;
   __shared__ __attribute__((aligned(1024))) uint8_t sm[P::kLds];
   using E = Elem<BF>;
   const uint32_t id = by_xcd(blockIdx.x, a.total);
@@ -877,7 +965,7 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_apply(const Sinks a,
   const int64_t row0 = (int64_t)(tall ? t / across : t % down) * T;
   const int64_t col0 = (int64_t)(tall ? t % across : t / down) * T;
   f32x16 acc[P::kB][P::kB];
-  last_product<T, RING, PAIR>(sm, g, own, a.q, a.second, tall, row0, col0, acc);
+  last_product<T, RING, F>(sm, g, own, a.q, a.second, tall, row0, col0, acc);
   float* tile = P::stage(sm, acc);
   const Sink s = a.s[u];
   const float f = *reinterpret_cast<const float*>(own + g.scale) * a.unit *
@@ -908,11 +996,11 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_apply(const Sinks a,
 }
 
 // Q X as pairs in both orders, in place of X from here on.
-template <int T, int RING, bool PAIR>
+template <int T, int RING, Form F>
 __global__ __launch_bounds__(kThreads) void dora_orthogonal_between(const Groups a, uint32_t total,
                                                                     int q, float unit, bool second,
                                                                     uint8_t* ws) {
-  using P = Product<T, RING, PAIR>;
+  using P = Product<T, RING, F>;
   __shared__ __attribute__((aligned(1024))) uint8_t sm[P::kLds];
   const uint32_t id = by_xcd(blockIdx.x, total);
   const Group& g = a.g[group_of(a, id)];
@@ -922,7 +1010,7 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_between(const Groups
   uint8_t* own = ws + g.base + (int64_t)u * g.stride;
   const int64_t row0 = (int64_t)(t % down) * T, col0 = (int64_t)(t / down) * T;
   f32x16 acc[P::kB][P::kB];
-  last_product<T, RING, PAIR>(sm, g, own, q, second, false, row0, col0, acc);
+  last_product<T, RING, F>(sm, g, own, q, second, false, row0, col0, acc);
   float* tile = P::stage(sm, acc);
   const float f = *reinterpret_cast<const float*>(own + g.scale) * unit;
   f16* xk = reinterpret_cast<f16*>(own + (second ? g.xk : g.xk2));
@@ -1034,12 +1122,13 @@ struct Item {
   Sink to;
 };
 struct Kind {
-  bool pair;      // X is hi + lo
+  Form form;      // X's
   int times;      // how often Q X is formed on the way
 };
 struct Pass {
   bool small;               // n <= 64 throughout
   int gram, square, apply;  // tiles
+  bool few;                 // fewer tiles of the n x n products than two for each CU
   std::vector<int> order;   // items, group by group
   Groups groups;
   size_t bytes;
@@ -1058,7 +1147,7 @@ void lay_out(Group& g, const Kind& k, int gram) {
     at += padded(bytes, 256);
     return here;
   };
-  const int64_t x = (int64_t)g.nt * g.mt * (k.pair || k.times > 1 ? 4 : 2);
+  const int64_t x = (int64_t)g.nt * g.mt * (k.form != kSingle || k.times > 1 ? 4 : 2);
   g.xk = take(x);
   g.xt = take(x);
   g.xk2 = g.xt2 = 0;
@@ -1115,15 +1204,18 @@ std::vector<Pass> passes(const std::vector<Item>& items, const Kind& kind) {
   }
   for (Pass& p : out) {
     int64_t squares = 0, across = 0, parts = 0;   // workgroups with tiles of 128
+    int64_t small_squares = 0;                    // and of 64
     for (int i = 0; i < p.groups.count; ++i) {
       const Group& g = p.groups.g[i];
       const int64_t t = (int64_t)g.count * tri(tiles(g.n, 128));
       squares += t;
+      small_squares += (int64_t)g.count * tri(tiles(g.n, 64));
       parts += t * std::min<int64_t>(tiles(g.m, 256), kMaxSplits);
       across += (int64_t)g.count * tiles(g.n, 128) * tiles(g.m, 128);
     }
     p.gram = !p.small && parts >= kEnough ? 128 : 64;
-    p.square = !p.small && squares >= kEnough / 2 ? 128 : 64;
+    p.square = squares >= 2 * kEnough ? 128 : 64;
+    p.few = small_squares < 2 * kEnough;
     p.apply = !p.small && across >= kEnough ? 128 : 64;
     int64_t sums = 0;
     for (int i = 0; i < p.groups.count; ++i)
@@ -1162,6 +1254,7 @@ struct Call {
   Result what;
   float eps, mu, nu, decay, rest;
   int nesterov;
+  int fixed;   // kWide: X's power of two
 };
 
 // (an argument's type is the kernel's, not what is passed)
@@ -1208,7 +1301,6 @@ hipError_t by_matrix(const Pass& p, A& a, Size size, Fill fill, Go go) {
     if (hipError_t e_ = (expr)) return e_;           \
   } while (0)
 
-constexpr int kSquareWaves = 8;
 float two(int e) { return std::ldexp(1.f, e); }
 
 // Stages in flight: two of a 128 tile (64 KB) leave room for a second workgroup on the CU.
@@ -1218,72 +1310,90 @@ template <typename Fn>
 hipError_t by_tile(int tile, Fn fn) {
   return tile == 128 ? fn(std::integral_constant<int, 128>()) : fn(std::integral_constant<int, 64>());
 }
-template <typename Fn>
-hipError_t by_flag(bool flag, Fn fn) {
-  return flag ? fn(std::true_type()) : fn(std::false_type());
-}
-
 struct Engine {
   const Pass& p;
   const std::vector<Item>& items;
   const Numbers& z;
   const Call& c;
-  bool pair, second;
+  Form form;     // of the current X, and which of the two it is
+  bool second;
   uint8_t* ws;
   hipStream_t st;
 
-  template <bool BF, bool MOMENT>
+  template <bool BF, bool MOMENT, Form... FORMS>
   hipError_t halves() {
     Sources a;
     a.mu = c.mu;
     a.nu = c.nu;
     a.nesterov = c.nesterov;
+    a.fixed = c.fixed;
     auto fill = [&](int slot, int item) { a.s[slot] = items[item].from; };
-    ORTHO_TRY(by_matrix(p, a, [](const Group& g) { return (int64_t)g.blocks; }, fill,
-                        [&](int64_t blocks) {
-                          return launch("orthogonal_most", dora_orthogonal_most<BF, MOMENT>, blocks,
-                                        st, a, ws);
-                        }));
-    auto kernel = pair ? dora_orthogonal_halves<BF, MOMENT, true> : dora_orthogonal_halves<BF, MOMENT, false>;
-    return by_matrix(p, a, [](const Group& g) { return (int64_t)(g.nt / 64) * (g.mt / 64); }, fill,
-                     [&](int64_t blocks) {
-                       return launch("orthogonal_halves", kernel, blocks, st, a, ws);
-                     });
+    if (form != kWide)
+      ORTHO_TRY(by_matrix(p, a, [](const Group& g) { return (int64_t)g.blocks; }, fill,
+                          [&](int64_t blocks) {
+                            return launch("orthogonal_most", dora_orthogonal_most<BF, MOMENT>, blocks,
+                                          st, a, ws);
+                          }));
+    return by_form<FORMS...>([&](auto f) {
+      return by_matrix(p, a, [](const Group& g) { return (int64_t)(g.nt / 64) * (g.mt / 64); }, fill,
+                       [&](int64_t blocks) {
+                         return launch("orthogonal_halves",
+                                       dora_orthogonal_halves<BF, MOMENT, decltype(f)::value>, blocks,
+                                       st, a, ws);
+                       });
+    });
   }
   hipError_t start() {
-    if (c.moment) return c.x_bf ? halves<true, true>() : halves<false, true>();
-    return c.x_bf ? halves<true, false>() : halves<false, false>();
+    if (c.moment) return c.x_bf ? halves<true, true, kPair, kWide>() : halves<false, true, kPair, kWide>();
+    return c.x_bf ? halves<true, false, kSingle>() : halves<false, false, kPair>();
   }
+  Unit unit_of(float unit) const { return {unit, c.eps, form == kWide, c.fixed}; }
+  // fn with X's form, one of FORMS, as a constant
+  template <Form... FORMS, typename Fn>
+  hipError_t by_form(Fn fn) const {
+    hipError_t e = hipErrorInvalidValue;
+    (void)((form == FORMS && (e = fn(std::integral_constant<Form, FORMS>()), true)) || ...);
+    return e;
+  }
+
   // S of the current X; `unit` as dora_orthogonal_gather takes it
   hipError_t gram(float unit, int to) {
     return by_tile(p.gram, [&](auto tile) {
       constexpr int T = decltype(tile)::value;
       Groups a = p.groups;
       int64_t blocks = spread(a, [](const Group& g) { return (int64_t)tri(tiles(g.n, T)) * g.splits; });
-      auto kernel = pair ? dora_orthogonal_gram<T, ring(T), true> : dora_orthogonal_gram<T, ring(T), false>;
-      ORTHO_TRY(launch("orthogonal_gram", kernel, blocks, st, a, (uint32_t)blocks, second, ws));
+      ORTHO_TRY((by_form<kSingle, kPair, kWide>([&](auto f) {
+        return launch("orthogonal_gram", dora_orthogonal_gram<T, ring(T), decltype(f)::value>, blocks,
+                      st, a, (uint32_t)blocks, second, ws);
+      })));
       if (p.small) return hipSuccess;   // the chain gathers it
       blocks = spread(a, [](const Group& g) {
         return (int64_t)tri(tiles(g.n, T)) * (T / 32) * (T / 32);
       });
-      return launch("orthogonal_gather", dora_orthogonal_gather<T>, blocks, st, a, c.eps, unit,
-                    std::ldexp(1.f, to), ws);
+      return launch("orthogonal_gather", dora_orthogonal_gather<T>, blocks, st, a,
+                    unit_of(unit), two(to), ws);
     });
   }
+  template <bool POLY, int T, int RING, int WAVES>
+  hipError_t squares_on(const Square& one, const Square* two) {
+    Squares a;
+    a.groups = p.groups;
+    const int64_t blocks = spread(a.groups, [](const Group& g) { return (int64_t)tri(tiles(g.n, T)); });
+    a.half = (uint32_t)blocks;
+    a.total = (uint32_t)(two ? 2 * blocks : blocks);
+    a.q[0] = one;
+    a.q[1] = two ? *two : one;
+    return launch<WAVES * 64>(POLY ? "orthogonal_poly" : "orthogonal_square",
+                              dora_orthogonal_square<T, RING, WAVES, POLY>, a.total, st, a, ws);
+  }
+  // Tiles of 64 in two stages (32 KB) lie five to a CU: 48 matrices of 384 take 24 us a product, with
+  // tiles of 128 30; a matrix of 2048 takes 48 and 58.  From two of the large tiles for each CU on
+  // their half traffic counts (4096: 4.4 ms in all against 6.2).  Few tiles have the CU's SIMDs to
+  // themselves: eight waves (517 columns: 179 us in all, with four 192).
   template <bool POLY>
-  hipError_t squares(Square one, const Square* two = nullptr) {
-    return by_tile(p.square, [&](auto tile) {
-      constexpr int T = decltype(tile)::value;
-      Squares a;
-      a.groups = p.groups;
-      const int64_t blocks = spread(a.groups, [](const Group& g) { return (int64_t)tri(tiles(g.n, T)); });
-      a.half = (uint32_t)blocks;
-      a.total = (uint32_t)(two ? 2 * blocks : blocks);
-      a.q[0] = one;
-      a.q[1] = two ? *two : one;
-      return launch<kSquareWaves * 64>(POLY ? "orthogonal_poly" : "orthogonal_square",
-                    dora_orthogonal_square<T, ring(T), kSquareWaves, POLY>, a.total, st, a, ws);
-    });
+  hipError_t squares(const Square& one, const Square* two = nullptr) {
+    if (p.square == 128) return squares_on<POLY, 128, 2, 8>(one, two);
+    return p.few ? squares_on<POLY, 64, 3, 8>(one, two) : squares_on<POLY, 64, 2, 4>(one, two);
   }
   hipError_t between(int q, int e) {
     ORTHO_TRY(by_tile(p.apply, [&](auto tile) {
@@ -1291,40 +1401,43 @@ struct Engine {
       Groups a = p.groups;
       const int64_t blocks =
           spread(a, [](const Group& g) { return (int64_t)tiles(g.n, T) * tiles(g.m, T); });
-      auto kernel = pair ? dora_orthogonal_between<T, ring(T), true> : dora_orthogonal_between<T, ring(T), false>;
-      return launch("orthogonal_between", kernel, blocks, st, a, (uint32_t)blocks, q,
-                    std::ldexp(1.f, e), second, ws);
+      return by_form<kSingle, kPair, kWide>([&](auto f) {
+        return launch("orthogonal_between", dora_orthogonal_between<T, ring(T), decltype(f)::value>,
+                      blocks, st, a, (uint32_t)blocks, q, two(e), second, ws);
+      });
     }));
-    pair = true;
+    form = kPair;
     second = !second;
     return hipSuccess;
   }
-  template <bool BF, Result WHAT>
+  template <bool BF, Result WHAT, Form... FORMS>
   hipError_t apply(int q, int e) {
     Sinks a;
     a.q = q;
-    a.unit = std::ldexp(1.f, -e);
+    a.unit = two(-e);
     a.second = second;
     a.decay = c.decay;
     a.rest = c.rest;
     auto fill = [&](int slot, int item) { a.s[slot] = items[item].to; };
     return by_tile(p.apply, [&](auto tile) {
-      return by_flag(pair, [&](auto pair_) {
+      return by_form<FORMS...>([&](auto f) {
         constexpr int T = decltype(tile)::value;
         auto size = [](const Group& g) { return (int64_t)tiles(g.n, T) * tiles(g.m, T); };
         return by_matrix(p, a, size, fill, [&](int64_t blocks) {
           a.total = (uint32_t)blocks;
           return launch("orthogonal_apply",
-                        dora_orthogonal_apply<T, ring(T), decltype(pair_)::value, BF, WHAT>, blocks,
+                        dora_orthogonal_apply<T, ring(T), decltype(f)::value, BF, WHAT>, blocks,
                         st, a, ws);
         });
       });
     });
   }
+  // (kPair where X was formed on the way)
   hipError_t finish(int q, int e) {
-    if (c.what == kMaster) return apply<true, kMaster>(q, e);
-    if (c.what == kParam) return c.out_bf ? apply<true, kParam>(q, e) : apply<false, kParam>(q, e);
-    return c.out_bf ? apply<true, kOut>(q, e) : apply<false, kOut>(q, e);
+    if (c.what == kMaster) return apply<true, kMaster, kPair>(q, e);
+    if (c.what == kParam)
+      return c.out_bf ? apply<true, kParam, kWide, kPair>(q, e) : apply<false, kParam, kPair>(q, e);
+    return c.out_bf ? apply<true, kOut, kSingle, kPair>(q, e) : apply<false, kOut, kPair>(q, e);
   }
 
   // The steps [from, to) between two products with X, from S's partial sums; which of sq is Q and
@@ -1333,10 +1446,9 @@ struct Engine {
     Chain a;
     a.groups = p.groups;
     a.steps = to - from;
-    a.unit = unit;
-    a.eps = c.eps;
+    a.unit = unit_of(unit);
     a.to = two(z.s[from]);
-    a.pair = pair;
+    a.form = form;
     e = z.p[from];
     for (int k = from; k < to; ++k) {
       const int i = k - from;
@@ -1356,27 +1468,27 @@ struct Engine {
     constexpr int S = 0, P = 1, R = 2, Qa = 3, Qb = 4;
     for (int k = from; k < to; ++k) {
       const bool last = k + 1 == to;   // Q meets X next
-      const int flat = last && !pair;
+      const int as = last ? form : kPair;
       const int pi = k == from ? Qa : P;   // the first P is Q
       const double* abc = z.abc[k];
       Square poly = {S, S, pi, (float)std::ldexp(abc[2], z.p[k] - 2 * z.s[k]),
                      (float)std::ldexp(abc[1], z.p[k] - z.s[k]), (float)std::ldexp(abc[0], z.p[k]),
-                     k == from ? flat : 0};
+                     k == from ? as : kPair};
       ORTHO_TRY(squares<true>(poly));
-      const Square ps = {pi, S, R, two(z.r[k] - z.p[k] - z.s[k]), 0.f, 0.f, 0};
+      const Square ps = {pi, S, R, two(z.r[k] - z.p[k] - z.s[k]), 0.f, 0.f, kPair};
       if (k == from) {
         q = Qa;
         e = z.p[k];
         if (!last) ORTHO_TRY(squares<false>(ps));
       } else {
         const int next = q == Qa ? Qb : Qa;
-        const Square pq = {P, q, next, two(z.q[k] - z.p[k] - e), 0.f, 0.f, flat};
+        const Square pq = {P, q, next, two(z.q[k] - z.p[k] - e), 0.f, 0.f, as};
         ORTHO_TRY(squares<false>(pq, last ? nullptr : &ps));
         q = next;
         e = z.q[k];
       }
       if (!last)
-        ORTHO_TRY(squares<false>(Square{pi, R, S, two(z.s[k + 1] - z.p[k] - z.r[k]), 0.f, 0.f, 0}));
+        ORTHO_TRY(squares<false>(Square{pi, R, S, two(z.s[k + 1] - z.p[k] - z.r[k]), 0.f, 0.f, kPair}));
     }
     return hipSuccess;
   }
@@ -1401,7 +1513,7 @@ struct Engine {
 hipError_t run_all(const std::vector<Item>& items, const Kind& kind, const Numbers& z, const Call& c,
                    void* ws, hipStream_t st) {
   for (const Pass& p : passes(items, kind)) {
-    Engine e{p, items, z, c, kind.pair, false, reinterpret_cast<uint8_t*>(ws), st};
+    Engine e{p, items, z, c, kind.form, false, reinterpret_cast<uint8_t*>(ws), st};
     ORTHO_TRY(e.run());
   }
   return hipSuccess;
@@ -1449,7 +1561,7 @@ int set_up(const dora_orthogonalize_options* o, const dora_matrix* a, int64_t co
   DORA_CHECK(check_iteration(&o->iteration, exact, s.z));
   if (count < 0 || count >= kMaxCount) return DORA_ERR_SHAPE;
   if (count > 0 && !a) return DORA_ERR_NULL;
-  s.kind = {exact, s.z.times};
+  s.kind = {exact ? kPair : kSingle, s.z.times};
   s.items.resize((size_t)count);
   for (int64_t i = 0; i < count; ++i) {
     if (!sides_ok(a[i].rows, a[i].cols)) return DORA_ERR_SHAPE;
@@ -1482,7 +1594,7 @@ int set_up(const dora_muon_options* o, const dora_muon_tensor* a, int64_t count,
   if (master && o->param_dtype != DORA_BF16) return DORA_ERR_DTYPE;
   const bool exact = master || o->param_dtype == DORA_F32;
   DORA_CHECK(check_iteration(&o->iteration, exact, s.z));
-  s.kind = {true, s.z.times};
+  s.kind = {exact ? kPair : kWide, s.z.times};
   return DORA_OK;
 }
 
@@ -1564,6 +1676,9 @@ DORA_API int dora_muon_step(const dora_muon_tensor* tensors, int64_t count,
     c.mu = (float)o.momentum;
     c.nu = (float)(1.0 - o.momentum);
     c.nesterov = o.nesterov;
+    // eps becomes 2^-40 to 2^-41: where X's squares underflow (|X| under 2^-63) eps is all there is,
+    // and they overflow from |X| = 2^64, 2^104 eps, on
+    c.fixed = -40 - (int)std::ceil(std::log2(o.iteration.eps));
     // what float32 loses of 1 - lr weight_decay beside 1 is added apart
     const double decay = o.lr * o.weight_decay;
     c.decay = (float)(1.0 - decay);
