@@ -338,8 +338,11 @@ struct Product {
 // ---- pairs ----------------------------------------------------------------------------------
 __device__ __forceinline__ int64_t pair_at(int64_t k) { return (k >> 5) * 64 + (k & 31); }
 
+// v is rounded to float32 first, in a register: a product that the compiler rounds to hi in one
+// step (v_fma_mixlo_f16) and to float32 for lo has another hi in one of 4000 cases.
 template <typename H>
 __device__ __forceinline__ void split(float v, H& hi, H& lo) {
+  asm("" : "+v"(v));
   hi = (H)v;
   lo = (H)(v - (float)hi);
 }
