@@ -1,5 +1,5 @@
-// The short way from Python to the layer norm, token log probability and AdamW
-// entry points: checks, output allocation and the call in one compiled step, for
+// The short way from Python to the layer norm, token log probability, AdamW, loss and
+// orthogonalisation entry points: checks, output allocation and the call in one compiled step, for
 // calls whose kernels run a few microseconds (a layer norm of one token: 7 us of
 // host time against 12 through ctypes).  Every function returns None where an
 // argument is not what it expects; the caller then takes the checked way, which
@@ -11,11 +11,13 @@
 #include <ATen/ATen.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstring>
 #include <utility>
 #include <vector>
 
 #include "../../include/dora_finetune.h"
+#include "../../include/dora_posttrain.h"
 
 namespace {
 
@@ -29,6 +31,15 @@ struct Api {
   decltype(&dora_grad_norm) grad_norm;
   decltype(&dora_adamw_step) adamw_step;
   decltype(&dora_adamw_dequantize) dequantize;
+  decltype(&dora_preference_forward) preference_forward;
+  decltype(&dora_preference_backward) preference_backward;
+  decltype(&dora_preference_workspace_bytes) preference_workspace_bytes;
+  decltype(&dora_policy_forward) policy_forward;
+  decltype(&dora_policy_backward) policy_backward;
+  decltype(&dora_policy_workspace_bytes) policy_workspace_bytes;
+  decltype(&dora_orthogonalize) orthogonalize;
+  decltype(&dora_orthogonalize_workspace_bytes) orthogonalize_workspace_bytes;
+  decltype(&dora_muon_step) muon_step;
 };
 Api g_api = {};
 
@@ -91,6 +102,15 @@ PyObject* give(std::initializer_list<const at::Tensor*> out) {
     PyTuple_SET_ITEM(t, i++, o);
   }
   return t;
+}
+
+// The versions of a list's tensors go up by one.
+void raise_versions(PyObject* list) {
+  bool ok = true;
+  for (Py_ssize_t i = 0; i < PyList_GET_SIZE(list); ++i) {
+    const at::Tensor* p = tensor(PyList_GET_ITEM(list, i), ok);
+    if (p && !p->is_inference()) p->unsafeGetTensorImpl()->bump_version();
+  }
 }
 
 // layernorm(x, weight, bias, eps, stream) -> (y, mean, rstd)
@@ -420,10 +440,7 @@ PyObject* adamw_step(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (PyErr_Occurred()) return nullptr;
   const int rc = g_api.adamw_step(static_cast<dora_adamw_tensor*>(PyLong_AsVoidPtr(args[0])), count,
                                   &o, stream_of(args[12]));
-  for (Py_ssize_t i = 0; rc == DORA_OK && i < count; ++i) {
-    const at::Tensor* p = tensor(PyList_GET_ITEM(args[1], i), ok);
-    if (p && !p->is_inference()) p->unsafeGetTensorImpl()->bump_version();
-  }
+  if (rc == DORA_OK) raise_versions(args[1]);
   return PyLong_FromLong(rc);
   END_HANDLE_TH_ERRORS
 }
@@ -451,6 +468,286 @@ PyObject* dequantize(PyObject*, PyObject* const* args, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// The sequences of log probabilities [sequences, length], or [tokens] with offsets; false where
+// shapes, types or devices are not what they should be.
+bool batch_ok(at::IntArrayRef shape, const at::Tensor& like, const at::Tensor* mask,
+              const at::Tensor* offsets, dora_token_batch& b) {
+  if (shape.size() != (offsets ? 1u : 2u)) return false;
+  b = {};
+  if (offsets) {
+    if (offsets->scalar_type() != at::kLong || offsets->dim() != 1 || offsets->size(0) < 1 ||
+        !offsets->is_contiguous() || offsets->device() != like.device())
+      return false;
+    b.tokens = shape[0];
+    b.sequences = offsets->size(0) - 1;
+    b.offsets = offsets->const_data_ptr<int64_t>();
+  } else {
+    b.sequences = shape[0];
+    b.length = shape[1];
+    b.tokens = b.sequences * b.length;
+  }
+  if (mask) {
+    if (mask->scalar_type() != at::kBool || mask->sizes() != shape || !mask->is_contiguous() ||
+        mask->device() != like.device())
+      return false;
+    b.mask = static_cast<const uint8_t*>(mask->const_data_ptr());
+  }
+  return true;
+}
+bool floats_as(const at::Tensor* t, at::IntArrayRef shape, const at::Tensor& like) {
+  return t && t->scalar_type() == at::kFloat && t->sizes() == shape && t->is_contiguous() &&
+         t->device() == like.device();
+}
+bool indices_ok(const at::Tensor* c, const at::Tensor* r, const at::Tensor& like) {
+  return c && c->dim() == 1 && vector_ok(c, c->size(0), at::kLong, like) &&
+         vector_ok(r, c->size(0), at::kLong, like);
+}
+at::Tensor workspace(size_t bytes, const at::Tensor& like) {
+  return at::empty({bytes ? (int64_t)bytes : 1}, like.options().dtype(at::kByte));
+}
+// Tensor arguments args[0 .. N) into t; whether all are tensors or None.
+template <int N>
+bool tensors(PyObject* const* args, const at::Tensor** t) {
+  bool ok = true;
+  for (int i = 0; i < N; ++i) t[i] = tensor(args[i], ok);
+  return ok;
+}
+// Numbers args[0 .. N) into v; whether all are.
+template <int N>
+bool numbers(PyObject* const* args, double* v) {
+  for (int i = 0; i < N; ++i) {
+    if (!PyFloat_Check(args[i])) return false;
+    v[i] = PyFloat_AS_DOUBLE(args[i]);
+  }
+  return true;
+}
+
+// preference_loss(logp, ref_logp, chosen, rejected, mask, offsets, beta, margin, smoothing, kind,
+// normalize, stream) -> (loss, score, logit, count)
+PyObject* preference_loss(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  const at::Tensor* t[6];
+  double v[3];
+  dora_token_batch b;
+  if (n != 12 || !tensors<6>(args, t) || !numbers<3>(args + 6, v) || !PyLong_Check(args[9]) || !t[0] ||
+      !t[0]->is_cuda())
+    Py_RETURN_NONE;
+  const at::Tensor& x = *t[0];
+  if (!floats_as(&x, x.sizes(), x) || (t[1] && !floats_as(t[1], x.sizes(), x)) ||
+      !indices_ok(t[2], t[3], x) || !batch_ok(x.sizes(), x, t[4], t[5], b))
+    Py_RETURN_NONE;
+  const dora_preference_options o = {(int32_t)PyLong_AsLong(args[9]), args[10] == Py_True, v[0], v[1],
+                                     v[2]};
+  const int64_t P = t[2]->size(0), S = b.sequences;
+  const at::Tensor whole = at::empty({2 * (P + S)}, x.options());
+  int64_t from = 0;
+  const at::Tensor loss = take(whole, from, {P}), score = take(whole, from, {S}),
+                   logit = take(whole, from, {P}), count = take(whole, from, {S});
+  const size_t need = g_api.preference_workspace_bytes(&b);
+  const at::Tensor ws = workspace(need, x);
+  if (g_api.preference_forward(&b, &o, P, floats(&x), floats(t[1]), t[2]->const_data_ptr<int64_t>(),
+                               t[3]->const_data_ptr<int64_t>(), floats(loss), floats(score),
+                               floats(logit), floats(count), ws.mutable_data_ptr(), need,
+                               stream_of(args[11])) != DORA_OK)
+    Py_RETURN_NONE;
+  return give({&loss, &score, &logit, &count});
+  END_HANDLE_TH_ERRORS
+}
+
+// preference_loss_backward(grad_loss, logit, count, chosen, rejected, mask, offsets, beta, margin,
+// smoothing, kind, normalize, shape, stream) -> grad_logp
+PyObject* preference_loss_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  const at::Tensor* t[7];
+  double v[3];
+  dora_token_batch b;
+  if (n != 14 || !tensors<7>(args, t) || !numbers<3>(args + 7, v) || !PyLong_Check(args[10]) || !t[1] ||
+      !t[1]->is_cuda() || !PyTuple_Check(args[12]) || PyTuple_GET_SIZE(args[12]) > 2)
+    Py_RETURN_NONE;
+  int64_t dims[2] = {};
+  const size_t rank = (size_t)PyTuple_GET_SIZE(args[12]);
+  for (size_t i = 0; i < rank; ++i) {
+    dims[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(args[12], (Py_ssize_t)i));
+    if (dims[i] < 0) {
+      PyErr_Clear();
+      Py_RETURN_NONE;
+    }
+  }
+  const at::IntArrayRef shape(dims, rank);
+  const at::Tensor& x = *t[1];
+  if (!indices_ok(t[3], t[4], x) || !batch_ok(shape, x, t[5], t[6], b)) Py_RETURN_NONE;
+  const int64_t P = t[3]->size(0);
+  if (!vector_ok(t[0], P, at::kFloat, x) || !vector_ok(&x, P, at::kFloat, x) ||
+      !vector_ok(t[2], b.sequences, at::kFloat, x))
+    Py_RETURN_NONE;
+  const dora_preference_options o = {(int32_t)PyLong_AsLong(args[10]), args[11] == Py_True, v[0], v[1],
+                                     v[2]};
+  const at::Tensor grad = at::empty(shape, x.options());
+  const size_t need = g_api.preference_workspace_bytes(&b);
+  const at::Tensor ws = workspace(need, x);
+  if (g_api.preference_backward(&b, &o, P, floats(t[0]), floats(&x), floats(t[2]),
+                                t[3]->const_data_ptr<int64_t>(), t[4]->const_data_ptr<int64_t>(),
+                                floats(grad), ws.mutable_data_ptr(), need,
+                                stream_of(args[13])) != DORA_OK)
+    Py_RETURN_NONE;
+  return THPVariable_Wrap(grad);
+  END_HANDLE_TH_ERRORS
+}
+
+// The arguments that both directions of the policy loss begin with: logp, old_logp, advantages,
+// ref_logp, mask, offsets, clip_low, clip_high, dual_clip, kl_coef, denominator, reduce.
+struct Policy {
+  const at::Tensor* t[6];
+  dora_token_batch b;
+  dora_policy_options o;
+  static constexpr int kCount = 12;
+  bool read(PyObject* const* args) {
+    double v[5];
+    if (!tensors<6>(args, t) || !numbers<5>(args + 6, v) || !PyLong_Check(args[11]) || !t[0] ||
+        !t[0]->is_cuda())
+      return false;
+    const at::Tensor& x = *t[0];
+    if (!floats_as(&x, x.sizes(), x) || !floats_as(t[1], x.sizes(), x) ||
+        (t[3] && !floats_as(t[3], x.sizes(), x)) || !batch_ok(x.sizes(), x, t[4], t[5], b))
+      return false;
+    const bool each = floats_as(t[2], x.sizes(), x);
+    if (!each && !vector_ok(t[2], b.sequences, at::kFloat, x)) return false;
+    o = {v[0], v[1], v[2], v[3], v[4], (int32_t)PyLong_AsLong(args[11]), !each};
+    return true;
+  }
+  int64_t weights() const { return o.reduce == DORA_REDUCE_SEQUENCE ? b.sequences : 1; }
+};
+
+// policy_loss(..., stream) -> (loss, stats, weight)
+PyObject* policy_loss(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  Policy p;
+  if (n != Policy::kCount + 1 || !p.read(args)) Py_RETURN_NONE;
+  const at::Tensor& x = *p.t[0];
+  const at::Tensor whole = at::empty({5 + p.weights()}, x.options());
+  int64_t from = 0;
+  const at::Tensor loss = take(whole, from, {}), stats = take(whole, from, {4}),
+                   weight = take(whole, from, {p.weights()});
+  const size_t need = g_api.policy_workspace_bytes(&p.b, &p.o);
+  const at::Tensor ws = workspace(need, x);
+  if (g_api.policy_forward(&p.b, &p.o, floats(&x), floats(p.t[1]), floats(p.t[3]), floats(p.t[2]),
+                           floats(loss), floats(stats), floats(weight), ws.mutable_data_ptr(), need,
+                           stream_of(args[Policy::kCount])) != DORA_OK)
+    Py_RETURN_NONE;
+  return give({&loss, &stats, &weight});
+  END_HANDLE_TH_ERRORS
+}
+
+// policy_loss_backward(..., grad_loss, weight, stream) -> grad_logp
+PyObject* policy_loss_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  Policy p;
+  const at::Tensor* g[2];
+  if (n != Policy::kCount + 3 || !p.read(args) || !tensors<2>(args + Policy::kCount, g) || !g[0])
+    Py_RETURN_NONE;
+  const at::Tensor& x = *p.t[0];
+  if (!floats_as(g[0], g[0]->sizes(), x) || g[0]->numel() != 1 ||
+      !vector_ok(g[1], p.weights(), at::kFloat, x))
+    Py_RETURN_NONE;
+  const at::Tensor grad = at::empty(x.sizes(), x.options());
+  if (g_api.policy_backward(&p.b, &p.o, floats(g[0]), floats(g[1]), floats(&x), floats(p.t[1]),
+                            floats(p.t[3]), floats(p.t[2]), floats(grad),
+                            stream_of(args[Policy::kCount + 2])) != DORA_OK)
+    Py_RETURN_NONE;
+  return THPVariable_Wrap(grad);
+  END_HANDLE_TH_ERRORS
+}
+
+// orthogonalize(x, coefficients address, steps, eps, stream) -> a matrix, or a stack of them
+PyObject* orthogonalize(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  const at::Tensor* t[1];
+  double eps[1];
+  if (n != 5 || !tensors<1>(args, t) || !t[0] || !numbers<1>(args + 3, eps)) Py_RETURN_NONE;
+  const at::Tensor& x = *t[0];
+  const int code = dtype_code(x.scalar_type());
+  if (!x.is_cuda() || code < 0 || !x.is_contiguous() || (x.dim() != 2 && x.dim() != 3)) Py_RETURN_NONE;
+  dora_orthogonalize_options o = {};
+  o.iteration.coefficients = static_cast<const double*>(PyLong_AsVoidPtr(args[1]));
+  o.iteration.steps = (int32_t)PyLong_AsLong(args[2]);
+  o.iteration.eps = eps[0];
+  o.dtype = code;
+  const at::Tensor out = at::empty(x.sizes(), x.options());
+  const int64_t rows = x.size(-2), cols = x.size(-1), count = x.dim() == 3 ? x.size(0) : 1;
+  const int64_t bytes = rows * cols * (int64_t)x.element_size();
+  std::vector<dora_matrix> table((size_t)count);
+  const char* a = static_cast<const char*>(x.const_data_ptr());
+  char* b = static_cast<char*>(out.mutable_data_ptr());
+  for (int64_t i = 0; i < count; ++i) table[(size_t)i] = {a + i * bytes, b + i * bytes, rows, cols};
+  const size_t need = g_api.orthogonalize_workspace_bytes(table.data(), count, &o);
+  const at::Tensor ws = workspace(need, x);
+  if (g_api.orthogonalize(table.data(), count, &o, ws.mutable_data_ptr(), need,
+                          stream_of(args[4])) != DORA_OK)
+    Py_RETURN_NONE;
+  return THPVariable_Wrap(out);
+  END_HANDLE_TH_ERRORS
+}
+
+// muon_grads(params, momenta, masters or None, table address, grads, factor): looks at every tensor
+// of a plan, and notes the gradients and scales in the table.  factor: a number, or None for 0.2
+// sqrt(max(rows, cols)).  Returns the gradients' dtype code, or None where something has changed.
+PyObject* muon_grads(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 6 || !PyList_Check(args[0]) || !PyList_Check(args[1]) || !PyList_Check(args[4]))
+    Py_RETURN_NONE;
+  const bool masters = args[2] != Py_None;
+  const Py_ssize_t count = PyList_GET_SIZE(args[0]);
+  if (count < 1 || PyList_GET_SIZE(args[1]) != count || PyList_GET_SIZE(args[4]) != count ||
+      (masters && (!PyList_Check(args[2]) || PyList_GET_SIZE(args[2]) != count)) ||
+      (args[5] != Py_None && !PyFloat_Check(args[5])))
+    Py_RETURN_NONE;
+  auto* table = static_cast<dora_muon_tensor*>(PyLong_AsVoidPtr(args[3]));
+  int code = -1;
+  at::ScalarType type = at::kFloat;
+  for (Py_ssize_t i = 0; i < count; ++i) {
+    dora_muon_tensor& e = table[i];
+    bool ok = true;
+    const at::Tensor* p = tensor(PyList_GET_ITEM(args[0], i), ok);
+    const at::Tensor* m = tensor(PyList_GET_ITEM(args[1], i), ok);
+    const at::Tensor* w = masters ? tensor(PyList_GET_ITEM(args[2], i), ok) : nullptr;
+    const at::Tensor* g = tensor(PyList_GET_ITEM(args[4], i), ok);
+    if (!p || !m || !g || (masters && !w)) Py_RETURN_NONE;
+    if (i == 0) {
+      code = dtype_code(g->scalar_type());
+      type = p->scalar_type();
+    }
+    auto matrix = [&](const at::Tensor& t) {
+      return t.dim() == 2 && t.size(0) == e.rows && t.size(1) == e.cols && t.is_contiguous() &&
+             t.device() == p->device();
+    };
+    if (code < 0 || dtype_code(g->scalar_type()) != code || p->scalar_type() != type || !p->is_cuda() ||
+        !matrix(*p) || !matrix(*g) || !matrix(*m) || m->scalar_type() != at::kFloat ||
+        p->const_data_ptr() != e.param || m->const_data_ptr() != e.momentum ||
+        (w && (!matrix(*w) || w->scalar_type() != at::kFloat || w->const_data_ptr() != e.master)))
+      Py_RETURN_NONE;
+    e.grad = g->const_data_ptr();
+    e.scale = args[5] == Py_None ? 0.2 * std::sqrt((double)std::max(e.rows, e.cols))
+                                 : PyFloat_AS_DOUBLE(args[5]);
+  }
+  return PyLong_FromLong(code);
+  END_HANDLE_TH_ERRORS
+}
+
+// muon_step(table address, params, options address, workspace address, its bytes, stream) -> the
+// return code.  The parameters' versions go up, as adamw_step's.
+PyObject* muon_step(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 6 || !PyList_Check(args[1])) Py_RETURN_NONE;
+  const Py_ssize_t count = PyList_GET_SIZE(args[1]);
+  const size_t bytes = PyLong_AsSize_t(args[4]);
+  const int rc = g_api.muon_step(static_cast<dora_muon_tensor*>(PyLong_AsVoidPtr(args[0])), count,
+                                 static_cast<dora_muon_options*>(PyLong_AsVoidPtr(args[2])),
+                                 PyLong_AsVoidPtr(args[3]), bytes, stream_of(args[5]));
+  if (rc == DORA_OK) raise_versions(args[1]);
+  return PyLong_FromLong(rc);
+  END_HANDLE_TH_ERRORS
+}
+
 // init(addresses of the entry points of Api, in its order)
 PyObject* init(PyObject*, PyObject* const* args, Py_ssize_t n) {
   constexpr Py_ssize_t kCount = sizeof(Api) / sizeof(void*);
@@ -473,7 +770,11 @@ PyMethodDef methods[] = {FAST(layernorm),     FAST(layernorm_backward),
                          FAST(make_table),    FAST(same_table),
                          FAST(take_grads),    FAST(grad_norm),
                          FAST(adamw_step),    FAST(dequantize),
-                         FAST(init),          {nullptr, nullptr, 0, nullptr}};
+                         FAST(preference_loss), FAST(preference_loss_backward),
+                         FAST(policy_loss),   FAST(policy_loss_backward),
+                         FAST(orthogonalize), FAST(muon_grads),
+                         FAST(muon_step),     FAST(init),
+                         {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_bind", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 

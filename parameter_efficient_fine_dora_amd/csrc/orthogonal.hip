@@ -183,6 +183,10 @@ struct Side {
 template <int T, int RING, Form F, int WAVES = 4>
 struct Product {
   static constexpr bool PAIR = F != kSingle;
+  // The cross products are summed apart: a third of the additions to the large sum, whose roundings
+  // the iteration raises (float32 results 1.1e-6 off instead of 1.4e-6 at 1031 x 517, 2.1e-6 instead
+  // of 2.9e-6 at 300 x 300).  A tile of 128 has no registers for it.
+  static constexpr bool kApart = F == kPair && T == 64;
   static constexpr int kB = T / 64;                       // blocks of a wave along a side
   static constexpr int kStage = 2 * T * kRowBytes;
   static constexpr int kCopies = 2 * T / 8 / WAVES;       // of a wave and stage, 8 rows each
@@ -221,6 +225,13 @@ struct Product {
       for (int j = 0; j < kB; ++j)
 #pragma unroll
         for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+    f32x16 low[kApart ? kB : 1][kApart ? kB : 1];   // the cross products
+    if (kApart) {
+#pragma unroll
+      for (int i = 0; i < kB; ++i)
+#pragma unroll
+        for (int j = 0; j < kB; ++j) low[kApart ? i : 0][kApart ? j : 0] = acc[i][j];
+    }
     const int pre = min(RING, steps);
     for (int s = 0; s < pre; ++s) issue(s);
     const int rowa = (wave & 1) * (T / 2) + (lane & 31);
@@ -263,8 +274,9 @@ struct Product {
           for (int j = 0; j < kB; ++j) {
             auto& c = acc[i][j];
             if (PAIR) {
-              c = multiply<F>(fb[u][j], la[u][i], c);
-              c = multiply<F>(lb[u][j], fa[u][i], c);
+              auto& l = kApart ? low[kApart ? i : 0][kApart ? j : 0] : c;
+              l = multiply<F>(fb[u][j], la[u][i], l);
+              l = multiply<F>(lb[u][j], fa[u][i], l);
             }
             c = multiply<F>(fb[u][j], fa[u][i], c);
           }
@@ -273,6 +285,12 @@ struct Product {
       barrier_nofence();
       if (s + RING < steps) issue(slot);
       if (++slot == RING) slot = 0;
+    }
+    if (kApart) {
+#pragma unroll
+      for (int i = 0; i < kB; ++i)
+#pragma unroll
+        for (int j = 0; j < kB; ++j) acc[i][j] += low[kApart ? i : 0][kApart ? j : 0];
     }
   }
 
@@ -640,11 +658,15 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_gather(const Groups 
   if (ti == tj && pj < pi) return;   // (the same for the whole workgroup)
   const int i = threadIdx.x / 8, j = threadIdx.x % 8 * 4;
   const float* p = part + (int64_t)t * g.splits * T * T + (pi + i) * T + pj + j;
-  f32x4 x = {0.f, 0.f, 0.f, 0.f};
-  for (int s = 0; s < g.splits; ++s) x += *reinterpret_cast<const f32x4*>(p + (int64_t)s * T * T);
+  double x[4] = {};
+  for (int s = 0; s < g.splits; ++s) {
+    const f32x4 d = *reinterpret_cast<const f32x4*>(p + (int64_t)s * T * T);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) x[q] += (double)d[q];
+  }
   float v[4], w[4];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) v[q] = x[q] * r * r * to;
+  for (int q = 0; q < 4; ++q) v[q] = (float)x[q] * r * r * to;
 #pragma unroll
   for (int q = 0; q < 4; ++q) tile[i][j + q] = v[q];
   __syncthreads();
@@ -790,7 +812,7 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_chain(const Chain a,
   constexpr int S = 0, P = 1, R = 2, Q = 3;
   const float* part = reinterpret_cast<const float*>(own + g.part);
   constexpr int kMine = kN * kN / 4 / kThreads;
-  f32x4 sums[kMine] = {};
+  double sums[kMine][4] = {};
   for (int s = 0; s < g.splits; s += 4) {   // every load of four splits in flight
     f32x4 w[kMine][4];
 #pragma unroll
@@ -803,14 +825,16 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_chain(const Chain a,
     for (int u = 0; u < kMine; ++u)
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        if (s + q < g.splits) sums[u] += w[u][q];
+        if (s + q < g.splits)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sums[u][e] += (double)w[u][q][e];
   }
 #pragma unroll
   for (int u = 0; u < kMine; ++u) {
     const int x = u * kThreads + threadIdx.x;
     float v[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = sums[u][e] * r * r * a.to;
+    for (int e = 0; e < 4; ++e) v[e] = (float)sums[u][e] * r * r * a.to;
     put(S, x / 16, x % 16 * 4, v);
   }
   __syncthreads();
@@ -831,6 +855,7 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_chain(const Chain a,
   auto product = [&](int x, int y, f32x16& acc) {
 #pragma unroll
     for (int e = 0; e < 16; ++e) acc[e] = 0.f;
+    f32x16 low = acc;
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int c = (u >> 1) * 8 + (u & 1) * 2 + (lane >> 5);
@@ -838,10 +863,11 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_chain(const Chain a,
       const f16x8 la = *reinterpret_cast<const f16x8*>(chunk(x, rowa, c + 4));
       const f16x8 fb = *reinterpret_cast<const f16x8*>(chunk(y, rowb, c));
       const f16x8 lb = *reinterpret_cast<const f16x8*>(chunk(y, rowb, c + 4));
-      acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(fb, la, acc, 0, 0, 0);
-      acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(lb, fa, acc, 0, 0, 0);
+      low = __builtin_amdgcn_mfma_f32_32x32x16_f16(fb, la, low, 0, 0, 0);
+      low = __builtin_amdgcn_mfma_f32_32x32x16_f16(lb, fa, low, 0, 0, 0);
       acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(fb, fa, acc, 0, 0, 0);
     }
+    acc += low;
   };
   // fn(row, first of four columns, values)
   auto each = [&](const f32x16& acc, auto fn) {
@@ -1075,12 +1101,10 @@ int exponent(double bound) {
   // 2^14 of half precision's 2^16: roundings may pass the bound a little
   return 14 - (int)std::ceil(std::log2(std::max(bound, 0x1p-24)));
 }
-Numbers numbers(const double* coefficients, int steps, bool exact) {
+Numbers numbers(const double* coefficients, int steps, double most) {
   Numbers z = {};
   z.steps = steps;
   z.good = false;
-  // the factor on S's rounding up to which Q is kept: results of 8 bits, or of 24
-  const double most = exact ? 1024.0 : 65536.0;
   double l = 1.0, q = 1.0, grown = 0.0, gain = 1.0;
   for (int k = 0; k < steps; ++k) {
     const double* abc = z.abc[k];
@@ -1540,16 +1564,20 @@ bool sides_ok(int64_t rows, int64_t cols) {
          std::min(rows, cols) <= kMaxShort;
 }
 
-int check_iteration(const dora_newton_schulz* o, bool exact, Numbers& z) {
+int check_iteration(const dora_newton_schulz* o, double most, Numbers& z) {
   if (!(o->eps >= 0x1p-100) || !std::isfinite(o->eps) || !std::isfinite((float)o->eps) || o->steps < 1 ||
       o->steps > kMaxSteps)
     return DORA_ERR_FLAGS;
   if (!o->coefficients) return DORA_ERR_NULL;
-  z = numbers(o->coefficients, o->steps, exact);
+  z = numbers(o->coefficients, o->steps, most);
   return z.good ? DORA_OK : DORA_ERR_FLAGS;
 }
 
-// What a call's types say of the precision: float32 results or states need it, bf16 ones do not.
+// The factor on S's rounding up to which Q is kept, by what the result is: float32 matrices (S anew
+// after two of five usual steps, and after four), updates of float32 parameters, of which they are a
+// few percent (after three: each time costs a fifth of the step of 56 rank-64 layers), and bf16
+// (never in five steps).
+constexpr double kMostExact = 20.0, kMostUpdate = 1024.0, kMostBrief = 65536.0;
 struct Setup {
   Numbers z;
   Kind kind;
@@ -1561,7 +1589,7 @@ int set_up(const dora_orthogonalize_options* o, const dora_matrix* a, int64_t co
   if (!dtype_ok(o->dtype)) return DORA_ERR_DTYPE;
   if (o->reserved != 0) return DORA_ERR_FLAGS;
   const bool exact = o->dtype == DORA_F32;
-  DORA_CHECK(check_iteration(&o->iteration, exact, s.z));
+  DORA_CHECK(check_iteration(&o->iteration, exact ? kMostExact : kMostBrief, s.z));
   if (count < 0 || count >= kMaxCount) return DORA_ERR_SHAPE;
   if (count > 0 && !a) return DORA_ERR_NULL;
   s.kind = {exact ? kPair : kSingle, s.z.times};
@@ -1596,7 +1624,7 @@ int set_up(const dora_muon_options* o, const dora_muon_tensor* a, int64_t count,
   }
   if (master && o->param_dtype != DORA_BF16) return DORA_ERR_DTYPE;
   const bool exact = master || o->param_dtype == DORA_F32;
-  DORA_CHECK(check_iteration(&o->iteration, exact, s.z));
+  DORA_CHECK(check_iteration(&o->iteration, exact ? kMostUpdate : kMostBrief, s.z));
   s.kind = {exact ? kPair : kWide, s.z.times};
   return DORA_OK;
 }

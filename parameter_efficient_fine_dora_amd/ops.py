@@ -9,6 +9,7 @@ step of the computation runs in the library's kernels.
 from __future__ import annotations
 
 import ctypes
+import functools
 import json
 
 import torch
@@ -46,7 +47,10 @@ def _compiled():
             "dora_layernorm_forward", "dora_layernorm_backward", "dora_layernorm_workspace_bytes",
             "dora_token_logprob_forward", "dora_token_logprob_backward",
             "dora_token_logprob_workspace_bytes", "dora_grad_norm", "dora_adamw_step",
-            "dora_adamw_dequantize")))
+            "dora_adamw_dequantize", "dora_preference_forward", "dora_preference_backward",
+            "dora_preference_workspace_bytes", "dora_policy_forward", "dora_policy_backward",
+            "dora_policy_workspace_bytes", "dora_orthogonalize",
+            "dora_orthogonalize_workspace_bytes", "dora_muon_step")))
         _bind = mod
     return _bind
 
@@ -506,6 +510,12 @@ def dora_preference_loss(logp, chosen, rejected, *, ref_logp=None, mask=None, of
     Returns (loss, score, logit, count): float32 [pairs], [sequences], [pairs], [sequences]; score
     is beta times a sequence's sum, logit the difference of two scores less ``margin``.
     """
+    if workspace is None and kind in _lib.PREFERENCE_KIND and _on_gpu(logp):
+        out = _compiled().preference_loss(logp, ref_logp, chosen, rejected, mask, offsets, float(beta),
+                                          float(margin), float(smoothing), _lib.PREFERENCE_KIND[kind],
+                                          bool(normalize), _stream(logp.device))
+        if out is not None:
+            return out
     _need(logp, "logp", torch.float32)
     dev, shape = logp.device, logp.shape
     batch = _token_batch(shape, dev, mask, offsets)
@@ -537,8 +547,15 @@ def dora_preference_loss_backward(grad_loss, logit, count, chosen, rejected, *, 
                                   normalize=False, grad_logp=None, workspace=None):
     """Gradient of dora_preference_loss's losses with respect to logp (of ``shape``), float32;
     logit and count as it returned them."""
+    shape = tuple(shape)
+    if grad_logp is None and workspace is None and kind in _lib.PREFERENCE_KIND and _on_gpu(logit):
+        out = _compiled().preference_loss_backward(
+            grad_loss, logit, count, chosen, rejected, mask, offsets, float(beta), float(margin),
+            float(smoothing), _lib.PREFERENCE_KIND[kind], bool(normalize), shape, _stream(logit.device))
+        if out is not None:
+            return out
     _need(logit, "logit", torch.float32)
-    dev, shape = logit.device, tuple(shape)
+    dev = logit.device
     batch = _token_batch(shape, dev, mask, offsets)
     P = _pairs(chosen, rejected, dev)
     _need(logit, "logit", torch.float32, (P,), dev)
@@ -553,6 +570,14 @@ def dora_preference_loss_backward(grad_loss, logit, count, chosen, rejected, *, 
                                       _ptr(grad_logp), _ptr(ws), nb, _stream(dev)),
            "dora_preference_backward")
     return grad_logp
+
+
+def _policy_numbers(clip, dual_clip, kl_coef, reduce, denominator, ref_logp):
+    """The options as the compiled way takes them, or None where they have to be looked at."""
+    if reduce not in _lib.POLICY_REDUCE or (kl_coef and ref_logp is None) or denominator == 0:
+        return None
+    return (float(clip[0]), float(clip[1]), float("inf") if dual_clip is None else float(dual_clip),
+            float(kl_coef), 0.0 if denominator is None else float(denominator), _lib.POLICY_REDUCE[reduce])
 
 
 def _policy_arguments(logp, old_logp, advantages, ref_logp, mask, offsets, clip, dual_clip, kl_coef,
@@ -595,6 +620,12 @@ def dora_policy_loss(logp, old_logp, advantages, *, ref_logp=None, mask=None, of
     divergence, the share of them held by a bound, their mean ratio and their number; the factor of
     each sequence's tokens in the loss, float32 [sequences] or [1], for the backward.
     """
+    if workspace is None and _on_gpu(logp):
+        fast = _policy_numbers(clip, dual_clip, kl_coef, reduce, denominator, ref_logp)
+        out = fast and _compiled().policy_loss(logp, old_logp, advantages, ref_logp, mask, offsets, *fast,
+                                               _stream(logp.device))
+        if out is not None:
+            return out
     batch, how = _policy_arguments(logp, old_logp, advantages, ref_logp, mask, offsets, clip,
                                    dual_clip, kl_coef, reduce, denominator)
     dev = logp.device
@@ -615,6 +646,12 @@ def dora_policy_loss_backward(grad_loss, weight, logp, old_logp, advantages, *, 
                               reduce="token", denominator=None, grad_logp=None):
     """Gradient of dora_policy_loss's loss with respect to logp, float32 of its shape; grad_loss is a
     float32 scalar on the device, weight as the forward returned it."""
+    if grad_logp is None and _on_gpu(logp):
+        fast = _policy_numbers(clip, dual_clip, kl_coef, reduce, denominator, ref_logp)
+        out = fast and _compiled().policy_loss_backward(logp, old_logp, advantages, ref_logp, mask, offsets,
+                                                        *fast, grad_loss, weight, _stream(logp.device))
+        if out is not None:
+            return out
     batch, how = _policy_arguments(logp, old_logp, advantages, ref_logp, mask, offsets, clip,
                                    dual_clip, kl_coef, reduce, denominator)
     dev = logp.device
@@ -794,14 +831,20 @@ def dora_adamw(plan, grads, *, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_de
 NEWTON_SCHULZ = ((3.4445, -4.7750, 2.0315),) * 5
 
 
-def _iteration(coefficients, eps):
-    """The iteration's struct, and the array of coefficients that it points to."""
+@functools.lru_cache(maxsize=16)
+def _coefficients(coefficients):
+    """(array, its address, steps) of ((a, b, c), ...)."""
     flat = [float(v) for abc in coefficients for v in abc]
     if any(len(abc) != 3 for abc in coefficients):
         raise ValueError("coefficients are (a, b, c) for each step")
     array = (ctypes.c_double * max(len(flat), 1))(*flat)
-    steps = len(flat) // 3
-    return _lib.DoraNewtonSchulz(ctypes.addressof(array), steps, 0, float(eps)), array
+    return array, ctypes.addressof(array), len(flat) // 3
+
+
+def _iteration(coefficients, eps):
+    """The iteration's struct, and the array of coefficients that it points to."""
+    array, address, steps = _coefficients(tuple(tuple(abc) for abc in coefficients))
+    return _lib.DoraNewtonSchulz(address, steps, 0, float(eps)), array
 
 
 def dora_orthogonalize(x, *, coefficients=NEWTON_SCHULZ, eps=1e-7, out=None, workspace=None):
@@ -811,6 +854,11 @@ def dora_orthogonalize(x, *, coefficients=NEWTON_SCHULZ, eps=1e-7, out=None, wor
     x: a contiguous [rows, cols] tensor, a stack [count, rows, cols], or a list of matrices of any
     sizes, bf16 or float32.  Returns the same kind; ``out`` may be x itself.
     """
+    if out is None and workspace is None and _on_gpu(x):
+        _held, address, steps = _coefficients(tuple(tuple(abc) for abc in coefficients))
+        out = _compiled().orthogonalize(x, address, steps, float(eps), _stream(x.device))
+        if out is not None:
+            return out
     many = isinstance(x, (list, tuple))
     xs = list(x) if many else [x]
     outs = [None] * len(xs) if out is None else list(out) if many else [out]
@@ -904,7 +952,8 @@ class MuonPlan:
         for a, b in zip(spans, spans[1:]):
             if b[0] < a[1]:
                 raise ValueError(f"{a[2]} and {b[2]} share memory: a step writes both")
-        self._bytes = {}
+        self._address = ctypes.addressof(self.table)
+        self._bytes = {}   # of workspace, for the coefficients of the last step
 
     def unchanged(self):
         """Whether every tensor still has the storage it had when the plan was made."""
@@ -914,6 +963,21 @@ class MuonPlan:
                    and (w is None or w.data_ptr() == (e.master or 0))
                    and p.is_contiguous() and m.is_contiguous() and m.shape == p.shape
                    for e, p, m, w in zip(self.table, self.params, self.momenta, masters))
+
+
+    def _take_grads(self, grads, adjust):
+        """Checks the gradients and notes them and their updates' factors; returns their dtype's code."""
+        if len(grads) != len(self.params):
+            raise ValueError(f"{len(grads)} gradients for {len(self.params)} params")
+        if not self.unchanged():
+            raise ValueError("a tensor's storage has changed since the plan was made")
+        gdt = grads[0].dtype if isinstance(grads[0], torch.Tensor) else None
+        if gdt is not None and gdt not in _DT:
+            raise ValueError(f"unsupported dtype {gdt}; use float32 or bfloat16")
+        for i, (g, p, e) in enumerate(zip(grads, self.params, self.table)):
+            e.grad = _need(g, f"grads[{i}]", gdt, p.shape, self.device).data_ptr()
+            e.scale = update_factor(adjust, e.rows, e.cols)
+        return _DT[gdt]
 
 
 def update_factor(adjust, rows, cols):
@@ -936,19 +1000,15 @@ def dora_muon(plan, grads, *, lr, momentum=0.95, nesterov=True, weight_decay=0.0
 
     ``grads``: one contiguous tensor per parameter, all bf16 or all float32.
     """
-    grads = list(grads)
-    if len(grads) != len(plan.params):
-        raise ValueError(f"{len(grads)} gradients for {len(plan.params)} params")
-    if not plan.unchanged():
-        raise ValueError("a tensor's storage has changed since the plan was made")
-    gdt = grads[0].dtype if isinstance(grads[0], torch.Tensor) else None
-    if gdt is not None and gdt not in _DT:
-        raise ValueError(f"unsupported dtype {gdt}; use float32 or bfloat16")
-    for i, (g, p, e) in enumerate(zip(grads, plan.params, plan.table)):
-        e.grad = _need(g, f"grads[{i}]", gdt, p.shape, plan.device).data_ptr()
-        e.scale = update_factor(adjust, e.rows, e.cols)
+    grads = grads if isinstance(grads, list) else list(grads)
+    code = None
+    if adjust != "spectral":
+        factor = None if adjust == "rms" else update_factor(adjust, 1, 1)
+        code = _compiled().muon_grads(plan.params, plan.momenta, plan.masters, plan._address, grads, factor)
+    if code is None or plan.params[0].dtype != plan.dtype:
+        code = plan._take_grads(grads, adjust)
     iteration, _held = _iteration(coefficients, eps)
-    how = _lib.DoraMuonOptions(iteration, plan.param_code, _DT[gdt], int(bool(nesterov)), 0, float(lr),
+    how = _lib.DoraMuonOptions(iteration, plan.param_code, code, int(bool(nesterov)), 0, float(lr),
                                float(momentum), float(weight_decay))
     L, n = _lib.lib(), len(plan.params)
     if workspace is None:
@@ -956,10 +1016,10 @@ def dora_muon(plan, grads, *, lr, momentum=0.95, nesterov=True, weight_decay=0.0
         if key not in plan._bytes:   # depends on the sizes, which a plan keeps, and the coefficients
             plan._bytes = {key: L.dora_muon_workspace_bytes(plan.table, n, ctypes.byref(how))}
         workspace = torch.empty(max(plan._bytes[key], 1), dtype=torch.uint8, device=plan.device)
-    _check(L.dora_muon_step(plan.table, n, ctypes.byref(how), _ptr(workspace),
-                            _given_ws(workspace, plan.device), _stream(plan.device)), "dora_muon_step")
-    # a backward pass that saved a parameter from before the step is refused
-    torch.autograd.graph.increment_version([p for p in plan.params if not p.is_inference()])
+    # (the parameters' versions go up: a backward pass that saved one from before is refused)
+    _check(_compiled().muon_step(plan._address, plan.params, ctypes.addressof(how), workspace.data_ptr(),
+                                 _given_ws(workspace, plan.device), _stream(plan.device)),
+           "dora_muon_step")
 
 
 def _second_moment(codes):
