@@ -7,8 +7,7 @@
 // writes four.  Memory bounds large batches, launches small ones.  The terms are
 // float64: whether a bound holds a ratio must not depend on a float32 rounding beside
 // the bound (the slope jumps there), the loss is a small difference of large sums, and
-// exp(d) - 1 - d cancels.  Two float64 exponentials a token still take less time than
-// its bytes.
+// exp(d) - 1 - d cancels.
 #include <algorithm>
 #include <cmath>
 
@@ -32,10 +31,36 @@ struct Term {
   double loss, slope, kl, held, ratio;
 };
 
+// exp(x) = 2^n (1 + q) with x = n log 2 + r, |r| <= 0.35, and q the Taylor sum to r^10 / 10!: what is
+// left out is under 0.35^11 / 11! = 2.4e-13 of the result, a thousandth of a float32 rounding and
+// less.  (Memory should bound these kernels: the library's exponentials, exact to the last bit of
+// float64, took 14 us of 1M tokens' sums where these take 9.)
+struct Exponential {
+  double q, two;   // two: 2^n
+  __device__ __forceinline__ explicit Exponential(double x) {
+    x = x > 1100.0 ? 1100.0 : x < -1100.0 ? -1100.0 : x;   // 0 and infinity; NaN stays
+    const double n = __builtin_rint(x * 1.4426950408889634);
+    const double r = fma(n, -0.6931471805599453, x);
+    double p = 1.0 / 3628800.0;
+    p = fma(p, r, 1.0 / 362880.0);
+    p = fma(p, r, 1.0 / 40320.0);
+    p = fma(p, r, 1.0 / 5040.0);
+    p = fma(p, r, 1.0 / 720.0);
+    p = fma(p, r, 1.0 / 120.0);
+    p = fma(p, r, 1.0 / 24.0);
+    p = fma(p, r, 1.0 / 6.0);
+    p = fma(p, r, 0.5);
+    q = fma(p * r, r, r);
+    two = ldexp(1.0, (int)n);
+  }
+  __device__ __forceinline__ double value() const { return fma(q, two, two); }
+  __device__ __forceinline__ double less_one() const { return fma(q, two, two - 1.0); }
+};
+
 __device__ __forceinline__ Term term(const Tokens& k, float logp, float old, float ref, float adv) {
   Term x;
   const double a = adv;
-  x.ratio = exp((double)logp - (double)old);
+  x.ratio = Exponential((double)logp - (double)old).value();
   const bool over = a > 0.0 ? x.ratio > k.high : a < 0.0 && x.ratio > k.dual;
   const bool under = a < 0.0 && x.ratio < k.low;
   const double bounded = over ? (a > 0.0 ? k.high : k.dual) : under ? k.low : x.ratio;
@@ -45,7 +70,7 @@ __device__ __forceinline__ Term term(const Tokens& k, float logp, float old, flo
   x.slope = over || under || (a == 0.0 && x.ratio > k.high) ? 0.0 : -a * x.ratio;
   x.kl = 0.0;
   if (k.ref) {
-    const double d = (double)ref - (double)logp, e = expm1(d);
+    const double d = (double)ref - (double)logp, e = Exponential(d).less_one();
     x.kl = e - d;
     if (k.kl_coef > 0.0) {
       x.loss += k.kl_coef * x.kl;
@@ -75,15 +100,18 @@ struct Four {
 
 constexpr int kTotals = 5;   // loss, counted, kl, held, ratio
 
-// Sums over chunks, a wave each; SEQ: also the loss and count of each sequence.
+// Sums over chunks, a wave each, and their totals by workgroup; SEQ: also the loss and count of each
+// sequence.
 template <bool SEQ, bool PER>
 __global__ __launch_bounds__(kThreads) void dora_policy_sums(const Batch b, const Parts parts,
                                                              int64_t chunk, const Tokens k,
                                                              double* totals) {
-  const int64_t w = wave_id(), c0 = w * chunk;
-  if (c0 >= b.tokens) return;
+  __shared__ double lds[kWaves][kTotals];
+  const int64_t w = wave_id(), c0 = min(w * chunk, b.tokens);
   const int64_t c1 = min(c0 + chunk, b.tokens);
   const int lane = threadIdx.x & 63;
+  Four x;   // loads are under way while the sequence is looked for, and a round ahead
+  x.load(b, k, c0 + lane * 4, !PER);
   Cursor at = cursor_at(b, c0);
   Pair64 sum = {0.0, 0.0};
   double all[kTotals] = {};
@@ -94,8 +122,8 @@ __global__ __launch_bounds__(kThreads) void dora_policy_sums(const Batch b, cons
   };
   for (int64_t r0 = c0; r0 < c1; r0 += kRound) {
     const int64_t t = r0 + lane * 4, r1 = min(r0 + kRound, c1);
-    Four x;
-    x.load(b, k, t, !PER);
+    Four ahead;
+    if (r1 < c1) ahead.load(b, k, t + kRound, !PER);
     // tokens of no sequence do not count; the others get their sequence's advantage
     bool real[4] = {};
     Cursor look = at;
@@ -126,30 +154,35 @@ __global__ __launch_bounds__(kThreads) void dora_policy_sums(const Batch b, cons
         all[4] += v.ratio;
       }
     }
-    if (!SEQ) {
-      at = look;
-      continue;
-    }
-    through_round(
-        b, at, r0, r1, c1,
-        [&](int64_t, int64_t from, int64_t to) {
+    if (SEQ)
+      through_round(
+          b, at, r0, r1, c1,
+          [&](int64_t, int64_t from, int64_t to) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            if (real[q] && t + q >= from && t + q < to) {
-              sum.v += loss[q];
-              sum.n += 1.0;
+            for (int q = 0; q < 4; ++q) {
+              if (real[q] && t + q >= from && t + q < to) {
+                sum.v += loss[q];
+                sum.n += 1.0;
+              }
             }
-          }
-        },
-        [&](int64_t s, bool began) { give(began ? parts.own + s : parts.head + w); });
+          },
+          [&](int64_t s, bool began) { give(began ? parts.own + s : parts.head + w); });
+    at = look;
+    x = ahead;
   }
-  if (SEQ && b.inside(at.s)) give(at.began ? parts.tail + w : parts.head + w);
+  if (SEQ && c0 < c1 && b.inside(at.s)) give(at.began ? parts.tail + w : parts.head + w);
 #pragma unroll
   for (int i = 0; i < kTotals; ++i) {
     const double v = wave_sum64(all[i]);
-    if (lane == 0) totals[w * kTotals + i] = v;
+    if (lane == 0) lds[threadIdx.x >> 6][i] = v;
+  }
+  __syncthreads();
+  if (threadIdx.x < kTotals) {
+    const int i = threadIdx.x;
+    totals[(int64_t)blockIdx.x * kTotals + i] = (lds[0][i] + lds[1][i]) + (lds[2][i] + lds[3][i]);
   }
 }
+static_assert(kWaves == 4, "four waves' totals are added");
 
 // Each sequence's mean and count, in place of its sums, a wave per sequence.
 __global__ __launch_bounds__(kThreads) void dora_policy_join(const Batch b, const Parts parts,
@@ -161,33 +194,30 @@ __global__ __launch_bounds__(kThreads) void dora_policy_join(const Batch b, cons
   }
 }
 
+// Sums of N values over the workgroup's 16 waves, to every thread.
 template <int N>
 __device__ __forceinline__ void finish_sum(double* v, double* lds) {
-  constexpr int kW = kFinish / 64;
+  static_assert(kFinish == 16 * 64, "a row of 16 lanes has a wave's sum each");
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     v[i] = wave_sum64(v[i]);
-    if ((threadIdx.x & 63) == 0) lds[(threadIdx.x >> 6) * N + i] = v[i];
+    if ((threadIdx.x & 63) == 0) lds[i * 16 + (threadIdx.x >> 6)] = v[i];
   }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    v[i] = 0.0;
-#pragma unroll 1
-    for (int w = 0; w < kW; ++w) v[i] += lds[w * N + i];
-  }
+  for (int i = 0; i < N; ++i) v[i] = lane_value64(row_sum64(lds[i * 16 + (threadIdx.x & 15)]), 0);
   __syncthreads();
 }
 
 // The loss, the statistics and the factors, by one workgroup.
 template <bool SEQ>
 __global__ __launch_bounds__(kFinish) void dora_policy_finish(int64_t sequences, const Pair64* means,
-                                                              const double* totals, int64_t chunks,
+                                                              const double* totals, int64_t groups,
                                                               double denominator, float* loss,
                                                               float* stats, float* weight) {
   __shared__ double lds[kFinish / 64 * kTotals];
   double all[kTotals] = {};
-  for (int64_t c = threadIdx.x; c < chunks; c += kFinish) {
+  for (int64_t c = threadIdx.x; c < groups; c += kFinish) {
 #pragma unroll
     for (int i = 0; i < kTotals; ++i) all[i] += totals[c * kTotals + i];
   }
@@ -225,11 +255,13 @@ __global__ __launch_bounds__(kThreads) void dora_policy_grad(const Batch b, int6
   if (c0 >= b.tokens) return;
   const int64_t c1 = min(c0 + chunk, b.tokens);
   const double g = *grad_loss, flat = SEQ ? 0.0 : g * (double)*weight;
+  Four x;
+  x.load(b, k, c0 + (threadIdx.x & 63) * 4, !PER);
   Cursor at = cursor_at(b, c0);
   for (int64_t r0 = c0; r0 < c1; r0 += kRound) {
     const int64_t t = r0 + (threadIdx.x & 63) * 4;
-    Four x;
-    x.load(b, k, t, !PER);
+    Four ahead;
+    if (r0 + kRound < c1) ahead.load(b, k, t + kRound, !PER);
     bool real[4] = {};
     double factor[4] = {};
     through_round(
@@ -253,10 +285,15 @@ __global__ __launch_bounds__(kThreads) void dora_policy_grad(const Batch b, int6
       if (real[q])
         out[q] = (float)(factor[q] * term(k, x.logp[q], x.old[q], x.ref[q], x.adv[q]).slope);
     store_part<false>(grad, t, b.tokens, out);
+    x = ahead;
   }
 }
 
 // ---- host ---------------------------------------------------------------------------
+unsigned wave_grid(int64_t waves) {
+  return (unsigned)std::min<int64_t>((waves + kWaves - 1) / kWaves, int64_t(1) << 20);
+}
+
 struct Layout {
   int64_t chunk, chunks;
   size_t tail, own, totals, bytes;
@@ -270,7 +307,7 @@ Layout layout(const dora_token_batch& b, const dora_policy_options& o) {
   l.tail = (size_t)l.chunks * part;
   l.own = l.tail + (size_t)l.chunks * part;
   l.totals = l.own + (size_t)b.sequences * part;
-  l.bytes = l.totals + (size_t)l.chunks * kTotals * sizeof(double);
+  l.bytes = l.totals + (size_t)wave_grid(l.chunks) * kTotals * sizeof(double);
   return l;
 }
 
@@ -287,10 +324,6 @@ int check_options(const dora_policy_options* o) {
 Tokens tokens_of(const dora_policy_options& o, const float* logp, const float* old, const float* ref,
                  const float* adv) {
   return {logp, old, ref, adv, 1.0 - o.clip_low, 1.0 + o.clip_high, o.dual_clip, o.kl_coef};
-}
-
-unsigned wave_grid(int64_t waves) {
-  return (unsigned)std::min<int64_t>((waves + kWaves - 1) / kWaves, int64_t(1) << 20);
 }
 
 // fn(sequence?, per-sequence advantages?) with both as constants.
@@ -357,8 +390,8 @@ DORA_API int dora_policy_forward(const dora_token_batch* batch, const dora_polic
   }
   LaunchTimer timer("policy_finish", st);
   auto finish = seq ? dora_policy_finish<true> : dora_policy_finish<false>;
-  hipLaunchKernelGGL(finish, dim3(1), dim3(kFinish), 0, st, b.sequences, parts.own, totals, l.chunks,
-                     options->denominator, loss, stats, weight);
+  hipLaunchKernelGGL(finish, dim3(1), dim3(kFinish), 0, st, b.sequences, parts.own, totals,
+                     (int64_t)(none ? 0 : wave_grid(l.chunks)), options->denominator, loss, stats, weight);
   HIP_TRY(hipGetLastError());
   return DORA_OK;
 }

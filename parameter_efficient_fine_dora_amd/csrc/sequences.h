@@ -25,14 +25,19 @@ struct Batch {
     return o < 0 ? 0 : o > tokens ? tokens : o;
   }
   // The sequence of token t: the last one that starts at t or before, -1 before the
-  // first.  `sequences` behind the last.
+  // first.  `sequences` behind the last.  A whole wave looks for one t: 64 starts at a
+  // time, so that 4096 sequences are two loads one after the other (of a wave's 5 us
+  // on 256 tokens a search by halves of 512 took more than half).
   __device__ __forceinline__ int64_t sequence_of(int64_t t) const {
     if (!offsets) return length > 0 ? t / length : sequences;
     int64_t lo = -1, hi = sequences + 1;   // start(lo) <= t < start(hi)
     while (hi - lo > 1) {
-      const int64_t mid = lo + (hi - lo) / 2;
-      if (start(mid) <= t) lo = mid;
-      else hi = mid;
+      const int64_t step = (hi - lo + 63) / 64;
+      const int64_t at = lo + (int64_t)((threadIdx.x & 63) + 1) * step;
+      // lanes at hi or behind it count as behind t
+      const int n = __popcll(__ballot(at < hi && start(at) <= t));
+      lo += n * step;
+      hi = min(hi, lo + step);
     }
     return lo;
   }
@@ -65,10 +70,26 @@ __device__ __forceinline__ void load4(const float* p, int64_t t, int64_t n, floa
   load_part<false>(p, t, n, 0.f, v);
 }
 
+// Sum over a wave to every lane, in a fixed order, as wave_sum for float32.
+template <int CTRL>
+__device__ __forceinline__ double dpp_move64(double v) {
+  return __hiloint2double(__builtin_amdgcn_update_dpp(0, __double2hiint(v), CTRL, 0xf, 0xf, true),
+                          __builtin_amdgcn_update_dpp(0, __double2loint(v), CTRL, 0xf, 0xf, true));
+}
+__device__ __forceinline__ double lane_value64(double v, int lane) {
+  return __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(v), lane),
+                          __builtin_amdgcn_readlane(__double2loint(v), lane));
+}
+// Sums over rows of 16 lanes, to each of their lanes.
+__device__ __forceinline__ double row_sum64(double v) {
+  v += dpp_move64<0xB1>(v);    // quad_perm 1,0,3,2
+  v += dpp_move64<0x4E>(v);    // quad_perm 2,3,0,1
+  v += dpp_move64<0x141>(v);   // row_half_mirror: the other quad of eight lanes
+  return v + dpp_move64<0x140>(v);   // row_mirror: the other half of sixteen
+}
 __device__ __forceinline__ double wave_sum64(double v) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
-  return v;
+  v = row_sum64(v);
+  return (lane_value64(v, 0) + lane_value64(v, 16)) + (lane_value64(v, 32) + lane_value64(v, 48));
 }
 
 // Two sums over (part of) a sequence.
