@@ -255,13 +255,12 @@ __global__ __launch_bounds__(kThreads) void dora_policy_grad(const Batch b, int6
   if (c0 >= b.tokens) return;
   const int64_t c1 = min(c0 + chunk, b.tokens);
   const double g = *grad_loss, flat = SEQ ? 0.0 : g * (double)*weight;
-  Four x;
+  Four x;   // under way while the sequence is looked for
   x.load(b, k, c0 + (threadIdx.x & 63) * 4, !PER);
   Cursor at = cursor_at(b, c0);
   for (int64_t r0 = c0; r0 < c1; r0 += kRound) {
     const int64_t t = r0 + (threadIdx.x & 63) * 4;
-    Four ahead;
-    if (r0 + kRound < c1) ahead.load(b, k, t + kRound, !PER);
+    if (r0 > c0) x.load(b, k, t, !PER);
     bool real[4] = {};
     double factor[4] = {};
     through_round(
@@ -285,7 +284,6 @@ __global__ __launch_bounds__(kThreads) void dora_policy_grad(const Batch b, int6
       if (real[q])
         out[q] = (float)(factor[q] * term(k, x.logp[q], x.old[q], x.ref[q], x.adv[q]).slope);
     store_part<false>(grad, t, b.tokens, out);
-    x = ahead;
   }
 }
 
@@ -302,8 +300,8 @@ Layout layout(const dora_token_batch& b, const dora_policy_options& o) {
   Layout l;
   const bool seq = o.reduce == DORA_REDUCE_SEQUENCE;
   const size_t part = seq ? sizeof(Pair64) : 0;
-  l.chunk = chunk_of(b.tokens);
-  l.chunks = chunks_of(b.tokens);
+  l.chunk = chunk_of(b.tokens, kMostSums);
+  l.chunks = chunks_of(b.tokens, kMostSums);
   l.tail = (size_t)l.chunks * part;
   l.own = l.tail + (size_t)l.chunks * part;
   l.totals = l.own + (size_t)b.sequences * part;
@@ -416,10 +414,10 @@ DORA_API int dora_policy_backward(const dora_token_batch* batch, const dora_poli
   hipStream_t st = reinterpret_cast<hipStream_t>(hip_stream);
   LaunchTimer timer("policy_grad", st);
   const Tokens k = tokens_of(*options, logp, old_logp, ref_logp, advantages);
-  const int64_t chunk = chunk_of(b.tokens);
+  const int64_t chunk = chunk_of(b.tokens, kMostGrads);
   by_options(*options, [&](auto seq_, auto per_) {
     hipLaunchKernelGGL((dora_policy_grad<decltype(seq_)::value, decltype(per_)::value>),
-                       dim3(wave_grid(chunks_of(b.tokens))), dim3(kThreads), 0, st, b, chunk, k,
+                       dim3(wave_grid(chunks_of(b.tokens, kMostGrads))), dim3(kThreads), 0, st, b, chunk, k,
                        grad_loss, weight, grad_logp);
   });
   HIP_TRY(hipGetLastError());

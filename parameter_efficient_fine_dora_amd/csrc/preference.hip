@@ -194,8 +194,8 @@ struct Layout {
 };
 Layout layout(const dora_token_batch& b) {
   Layout l;
-  l.chunk = chunk_of(b.tokens);
-  l.chunks = chunks_of(b.tokens);
+  l.chunk = chunk_of(b.tokens, kMostSums);
+  l.chunks = chunks_of(b.tokens, kMostSums);
   l.head = 0;
   l.tail = l.head + (size_t)l.chunks * sizeof(Pair64);
   l.own = l.tail + (size_t)l.chunks * sizeof(Pair64);
@@ -310,8 +310,8 @@ DORA_API int dora_preference_backward(const dora_token_batch* batch,
   }
   LaunchTimer timer("preference_grad", st);
   auto kernel = known ? dora_preference_grad<true> : dora_preference_grad<false>;
-  hipLaunchKernelGGL(kernel, dim3(wave_grid(l.chunks)), dim3(kThreads), 0, st, b, l.chunk, p, coef,
-                     grad_logp);
+  hipLaunchKernelGGL(kernel, dim3(wave_grid(chunks_of(b.tokens, kMostGrads))), dim3(kThreads), 0, st, b,
+                     chunk_of(b.tokens, kMostGrads), p, coef, grad_logp);
   HIP_TRY(hipGetLastError());
   return DORA_OK;
 }
