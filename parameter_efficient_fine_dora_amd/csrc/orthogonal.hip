@@ -23,8 +23,8 @@
 //
 // Layout.  A "pair" row holds blocks of 32 columns: 32 hi, then 32 lo, so that the 128 bytes that
 // a stage copies of a row are the hi and lo of 32 columns; a "single" row holds 64 columns there.
-// X is kept in both orders, [n, m] for S and [m, n] for Q X: then both operands of every product
-// are contiguous along what is summed over, and one loop serves them all.
+// X stays in its own order: where the sum runs down its rows (S of a tall matrix, Q X of a wide
+// one) its numbers are turned as they are read from LDS.
 //
 // Many matrices share a launch: a step on the adapters of a model is 20 launches whatever their
 // number, and small matrices fill the chip together.
@@ -69,8 +69,7 @@ struct Group {
   int splits;          // of the sum over m
   int blocks;          // partial maxima
   int64_t base, stride;
-  int64_t xk, xt;      // X as [n, m] and [m, n]
-  int64_t xk2, xt2;    // the same of the product formed on the way
+  int64_t x, x2;       // X in its own order, and the product formed on the way
   int64_t sq[5];       // n x n pairs: S, P, P S, and Q twice
   int64_t part, trace; // partial sums of S and of its trace, float32
   int64_t most, scale; // partial maxima; the factor on X
@@ -165,12 +164,146 @@ __device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)"
 __device__ __forceinline__ void barrier_nofence() { asm volatile("s_barrier" ::: "memory"); }
 __device__ __forceinline__ int swz(int row) { return (row & 7) ^ ((row >> 3) & 7); }
 
-// One operand of a tile: T rows of `ld` bytes, `wrap` stages along them (a longer sum starts
-// again at the first).
+// One operand of a tile.  Straight: T rows of `ld` bytes, along which the sum runs.  Turned: the sum
+// runs down rows of `ld` bytes, of which the tile has T columns, from p on.  A sum that is longer
+// than the operand starts again at its first stage after `wrap`.
 struct Side {
   const uint8_t* p;
   int64_t ld;
   int wrap;
+};
+
+typedef short short4_ __attribute__((ext_vector_type(4)));
+// N fragments of 8 numbers along the sum, read from LDS rows that run across it: each 16 lanes of
+// ds_read_b64_tr_b16 take four rows of 16 numbers, and each lane is left with a column's four.  at[i]
+// is the lane's first address, LOW and HIGH the offsets of the first and the second four rows.  The
+// wait stands in the same block: the compiler takes the registers as written at once.
+template <int LOW, int HIGH>
+__device__ __forceinline__ void read_turned(const uint32_t (&at)[1], short4_ (&x)[1][2]) {
+  asm volatile(
+      "ds_read_b64_tr_b16 %0, %2 offset:%3\n\t"
+      "ds_read_b64_tr_b16 %1, %2 offset:%4\n\t"
+      "s_waitcnt lgkmcnt(0)"
+      : "=&v"(x[0][0]), "=&v"(x[0][1])
+      : "v"(at[0]), "n"(LOW), "n"(HIGH)
+      : "memory");
+}
+template <int LOW, int HIGH>
+__device__ __forceinline__ void read_turned(const uint32_t (&at)[2], short4_ (&x)[2][2]) {
+  asm volatile(
+      "ds_read_b64_tr_b16 %0, %4 offset:%6\n\t"
+      "ds_read_b64_tr_b16 %1, %4 offset:%7\n\t"
+      "ds_read_b64_tr_b16 %2, %5 offset:%6\n\t"
+      "ds_read_b64_tr_b16 %3, %5 offset:%7\n\t"
+      "s_waitcnt lgkmcnt(0)"
+      : "=&v"(x[0][0]), "=&v"(x[0][1]), "=&v"(x[1][0]), "=&v"(x[1][1])
+      : "v"(at[0]), "v"(at[1]), "n"(LOW), "n"(HIGH)
+      : "memory");
+}
+template <int LOW, int HIGH>
+__device__ __forceinline__ void read_turned(const uint32_t (&at)[4], short4_ (&x)[4][2]) {
+  asm volatile(
+      "ds_read_b64_tr_b16 %0, %8 offset:%12\n\t"
+      "ds_read_b64_tr_b16 %1, %8 offset:%13\n\t"
+      "ds_read_b64_tr_b16 %2, %9 offset:%12\n\t"
+      "ds_read_b64_tr_b16 %3, %9 offset:%13\n\t"
+      "ds_read_b64_tr_b16 %4, %10 offset:%12\n\t"
+      "ds_read_b64_tr_b16 %5, %10 offset:%13\n\t"
+      "ds_read_b64_tr_b16 %6, %11 offset:%12\n\t"
+      "ds_read_b64_tr_b16 %7, %11 offset:%13\n\t"
+      "s_waitcnt lgkmcnt(0)"
+      : "=&v"(x[0][0]), "=&v"(x[0][1]), "=&v"(x[1][0]), "=&v"(x[1][1]), "=&v"(x[2][0]), "=&v"(x[2][1]),
+        "=&v"(x[3][0]), "=&v"(x[3][1])
+      : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "n"(LOW), "n"(HIGH)
+      : "memory");
+}
+
+// A side's part of a stage in LDS: T rows of 128 bytes, or, turned, kDeep rows of T numbers (pairs:
+// T hi and T lo in blocks).  16-byte chunks are swizzled by the row, so that reads meet no bank twice.
+template <int T, Form F, bool TURNED, int WAVES>
+struct Operand {
+  static constexpr bool PAIR = F != kSingle;
+  static constexpr int kB = T / 64;
+  static constexpr int kBytes = T * kRowBytes;
+  static constexpr int kCopies = kBytes / 1024 / WAVES;      // of a wave and stage, 1 KB each
+  static constexpr int kDeep = PAIR ? 32 : 64;               // rows of a turned stage
+  static constexpr int kAcross = TURNED ? T * (PAIR ? 4 : 2) : kRowBytes;   // bytes of a row in LDS
+  static constexpr int kChunks = kAcross / 16;
+  static constexpr int kReads = kB * (PAIR ? 2 : 1);         // fragments of a 16-deep step
+
+  const uint8_t* p;
+  int64_t ld;
+  int wrap, k;
+  Rsrc rs;
+  uint32_t off[kCopies];
+  uint32_t at[kReads];   // turned: the lane's pieces, from the side's start in a stage
+
+  __device__ static __forceinline__ int swizzle(int row) {
+    // turned: four rows of 16 columns (two chunks of each) are read at once
+    return TURNED ? (kChunks >= 16 ? 4 : 2) * (row & 3) : swz(row);
+  }
+  __device__ __forceinline__ void start(const Side& s, int k0, int quarter) {
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    p = s.p;
+    ld = s.ld;
+    wrap = s.wrap;
+    k = k0 % wrap;
+    if (!TURNED) rs = rsrc(p, T * ld);
+#pragma unroll
+    for (int q = 0; q < kCopies; ++q) {
+      const int chunk = (wave + WAVES * q) * 64 + lane, row = chunk / kChunks;
+      off[q] = (uint32_t)(row * ld) + (uint32_t)(((chunk % kChunks) ^ swizzle(row)) << 4);
+    }
+    if (TURNED) {
+      const int g = lane >> 4, j = (lane >> 2) & 3, q = lane & 3;
+      const int row = 8 * (g >> 1) + j;   // of the first four; (row & 3) is j in all of them
+#pragma unroll
+      for (int i = 0; i < kReads; ++i) {
+        const int c = quarter * (T / 2) + 32 * (i % kB) + 16 * (g & 1) + 4 * q;
+        const int chunk = PAIR ? (c >> 5) * 8 + (i / kB) * 4 + ((c & 31) >> 3) : c >> 3;
+        at[i] = row * kAcross + ((chunk ^ swizzle(row)) << 4) + ((c >> 2) & 1) * 8;
+      }
+    }
+  }
+  __device__ __forceinline__ void issue(uint8_t* dst) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (TURNED) rs = rsrc(p + (int64_t)k * kDeep * ld, kDeep * ld);
+#pragma unroll
+    for (int q = 0; q < kCopies; ++q)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rs, (__attribute__((address_space(3))) void*)(dst + (wave + WAVES * q) * 1024), 16,
+          (int)off[q], TURNED ? 0 : k * kRowBytes, 0, 0);
+    if (++k == wrap) k = 0;
+  }
+  // The hi (and lo) fragments of this wave's blocks for the 16-deep step u of a stage.
+  template <int U>
+  __device__ __forceinline__ void read(const uint8_t* src, int quarter, int first, short8 (&hi)[kB],
+                                       short8 (&lo)[kB]) const {
+    if constexpr (TURNED) {
+      const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t*)src;
+      uint32_t from[kReads];
+      short4_ x[kReads][2];
+#pragma unroll
+      for (int i = 0; i < kReads; ++i) from[i] = base + at[i];
+      read_turned<U * 16 * kAcross, (U * 16 + 4) * kAcross>(from, x);
+#pragma unroll
+      for (int i = 0; i < kB; ++i) {
+        hi[i] = __builtin_shufflevector(x[i][0], x[i][1], 0, 1, 2, 3, 4, 5, 6, 7);
+        if constexpr (PAIR)
+          lo[i] = __builtin_shufflevector(x[kB + i][0], x[kB + i][1], 0, 1, 2, 3, 4, 5, 6, 7);
+      }
+    } else {
+      const int lane = threadIdx.x & 63, chunk = (first + U) * 2 + (lane >> 5);
+#pragma unroll
+      for (int i = 0; i < kB; ++i) {
+        const int row = quarter * (T / 2) + 32 * i + (lane & 31);
+        const uint8_t* r = src + row * kRowBytes;
+        hi[i] = *reinterpret_cast<const short8*>(r + ((chunk ^ swz(row)) << 4));
+        if constexpr (PAIR) lo[i] = *reinterpret_cast<const short8*>(r + (((chunk + 4) ^ swz(row)) << 4));
+      }
+    }
+  }
 };
 
 // A T x T tile of A B^T over the stages [k0, k0 + steps): each of four waves has a quarter, of eight
@@ -189,35 +322,25 @@ struct Product {
   static constexpr bool kApart = F == kPair && T == 64;
   static constexpr int kB = T / 64;                       // blocks of a wave along a side
   static constexpr int kStage = 2 * T * kRowBytes;
-  static constexpr int kCopies = 2 * T / 8 / WAVES;       // of a wave and stage, 8 rows each
+  static constexpr int kCopies = kStage / 1024 / WAVES;   // of a wave and stage
   static constexpr int kHalves = WAVES / 4;               // waves that share a quarter
   static constexpr int kLds = RING * kStage;
 
-  __device__ static __forceinline__ void run(uint8_t* sm, const Side& a, const Side& b, int k0,
+  // TA, TB: that side is turned
+  template <bool TA = false, bool TB = false>
+  __device__ static __forceinline__ void run(uint8_t* sm, const Side& sa, const Side& sb, int k0,
                                              int steps, f32x16 (&acc)[kB][kB]) {
-    const int lane = threadIdx.x & 63;
+    static_assert(kHalves == 1 || (!TA && !TB), "halves of a stage are of straight sides");
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const Rsrc ra = rsrc(a.p, T * a.ld), rb = rsrc(b.p, T * b.ld);
-    uint32_t off[kCopies];
-#pragma unroll
-    for (int q = 0; q < kCopies; ++q) {
-      const int row = (wave + WAVES * q) * 8 + (lane >> 3);   // of both sides, A's first
-      const int64_t ld = row < T ? a.ld : b.ld;
-      off[q] = (uint32_t)((row & (T - 1)) * ld) + (uint32_t)(((lane & 7) ^ swz(row)) << 4);
-    }
-    int ka = k0 % a.wrap, kb = k0 % b.wrap;
+    const int quarter_a = wave & 1, quarter_b = (wave >> 1) & 1;
+    Operand<T, F, TA, WAVES> a;
+    Operand<T, F, TB, WAVES> b;
+    a.start(sa, k0, quarter_a);
+    b.start(sb, k0, quarter_b);
     auto issue = [&](int slot) {
       uint8_t* dst = sm + slot * kStage;
-#pragma unroll
-      for (int q = 0; q < kCopies; ++q) {
-        const bool first = WAVES * q * 8 < T;   // a copy's rows are all of one side
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            first ? ra : rb,
-            (__attribute__((address_space(3))) void*)(dst + (wave + WAVES * q) * 1024),
-            16, (int)off[q], (first ? ka : kb) * kRowBytes, 0, 0);
-      }
-      if (++ka == a.wrap) ka = 0;
-      if (++kb == b.wrap) kb = 0;
+      a.issue(dst);
+      b.issue(dst + a.kBytes);
     };
 #pragma unroll
     for (int i = 0; i < kB; ++i)
@@ -234,9 +357,8 @@ struct Product {
     }
     const int pre = min(RING, steps);
     for (int s = 0; s < pre; ++s) issue(s);
-    const int rowa = (wave & 1) * (T / 2) + (lane & 31);
-    const int rowb = T + ((wave >> 1) & 1) * (T / 2) + (lane & 31);
-    const int half = wave >> 2;   // which of its quarter's sums a wave takes
+    constexpr int kSub = (PAIR ? 2 : 4) / kHalves;
+    const int first = (wave >> 2) * kSub;   // the 16-deep steps of a stage that this wave takes
     int slot = 0;
     for (int s = 0; s < steps; ++s) {
       // the stage has landed once only the copies of the stages behind it are in flight
@@ -247,39 +369,30 @@ struct Product {
       else wait_vm<0>();
       barrier_nofence();
       const uint8_t* src = sm + slot * kStage;
-      auto frag = [&](int row, int chunk) {
-        return *reinterpret_cast<const short8*>(src + row * kRowBytes + ((chunk ^ swz(row)) << 4));
-      };
-      // all of the wave's fragments first: the later ones arrive while the first are multiplied
-      constexpr int kSub = (PAIR ? 2 : 4) / kHalves;
-      short8 fa[kSub][kB], fb[kSub][kB], la[kSub][kB], lb[kSub][kB];
-#pragma unroll
-      for (int u = 0; u < kSub; ++u) {
-        const int ch = (u + half * kSub) * 2 + (lane >> 5);
-#pragma unroll
-        for (int i = 0; i < kB; ++i) {
-          fa[u][i] = frag(rowa + 32 * i, ch);
-          fb[u][i] = frag(rowb + 32 * i, ch);
-          if (PAIR) {
-            la[u][i] = frag(rowa + 32 * i, ch + 4);
-            lb[u][i] = frag(rowb + 32 * i, ch + 4);
-          }
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < kSub; ++u)
+      auto step = [&](auto number) {
+        constexpr int U = decltype(number)::value;
+        short8 fa[kB], la[kB], fb[kB], lb[kB];
+        a.template read<U>(src, quarter_a, first, fa, la);
+        b.template read<U>(src + a.kBytes, quarter_b, first, fb, lb);
 #pragma unroll
         for (int i = 0; i < kB; ++i)
 #pragma unroll
           for (int j = 0; j < kB; ++j) {
             auto& c = acc[i][j];
-            if (PAIR) {
+            if constexpr (PAIR) {
               auto& l = kApart ? low[kApart ? i : 0][kApart ? j : 0] : c;
-              l = multiply<F>(fb[u][j], la[u][i], l);
-              l = multiply<F>(lb[u][j], fa[u][i], l);
+              l = multiply<F>(fb[j], la[i], l);
+              l = multiply<F>(lb[j], fa[i], l);
             }
-            c = multiply<F>(fb[u][j], fa[u][i], c);
+            c = multiply<F>(fb[j], fa[i], c);
           }
+      };
+      step(std::integral_constant<int, 0>());
+      if constexpr (kSub > 1) step(std::integral_constant<int, 1>());
+      if constexpr (kSub > 2) {
+        step(std::integral_constant<int, 2>());
+        step(std::integral_constant<int, 3>());
+      }
       // every wave has read the slot, and not only asked for it, before it is filled again
       wait_lds();
       barrier_nofence();
@@ -496,77 +609,63 @@ __device__ __forceinline__ int exponent_of(const uint32_t* most, int blocks, uin
   return 14 - e;
 }
 
-// A 64 x 64 block of the padded matrix into both orders, through LDS for the turned one; zeros
-// where the matrix ends.  Memory bounds it: what is read is 2 to 6 bytes an element, written 4 (one
-// number, two orders) or 8.  bf16 holds float32's range, so kWide needs no largest element: the
-// momentum is moved on here too, in the only pass over it.
+// The padded matrix as half precision numbers, zeros where the matrix ends: a thread takes eight
+// columns.  Memory bounds it: 2 to 6 bytes an element are read, 2 or 4 written.  bf16 holds float32's
+// range, so kWide needs no largest element: the momentum is moved on here too, in the only pass over
+// it.
+constexpr int kPiece = 4096;   // elements of a workgroup
 template <bool BF, bool MOMENT, Form F>
 __global__ __launch_bounds__(kThreads) void dora_orthogonal_halves(const Sources a, uint8_t* ws) {
   using H = typename Number<F>::T;
   constexpr bool PAIR = Number<F>::kTwo;
   typedef H H8 __attribute__((ext_vector_type(8)));
-  constexpr int kE = 64;
-  __shared__ uint32_t tile[kE][kE + 1];
   __shared__ uint32_t lds[kThreads / 64];
   const int u = matrix_of(a.from, a.count, blockIdx.x);
   const Group& g = a.groups.g[group_of_matrix(a.groups, a.first + u)];
   uint8_t* own = ws + g.base + (int64_t)(a.first + u - g.first) * g.stride;
   const int rows = g.tall ? g.m : g.n, cols = g.tall ? g.n : g.m;
-  const int prows = g.tall ? g.mt : g.nt, pcols = g.tall ? g.nt : g.mt;
-  const int across = pcols / kE, block = blockIdx.x - a.from[u];
-  const int r0 = block / across * kE, c0 = block % across * kE;
+  const int pcols = g.tall ? g.nt : g.mt;
+  const int64_t all = (int64_t)g.nt * g.mt;
   const int e = F == kWide ? a.fixed
                            : exponent_of(reinterpret_cast<const uint32_t*>(own + g.most), g.blocks, lds);
   const Source s = a.s[u];
-  H* straight = reinterpret_cast<H*>(own + (g.tall ? g.xt : g.xk));   // [prows, pcols]
-  H* turned = reinterpret_cast<H*>(own + (g.tall ? g.xk : g.xt));     // [pcols, prows]
-  auto put = [&](H* row, int64_t k, const H* h, const H* l) {
-    H* p = row + (PAIR ? pair_at(k) : k);
-    *reinterpret_cast<H8*>(p) = *reinterpret_cast<const H8*>(h);
-    if (PAIR) *reinterpret_cast<H8*>(p + kPairBlock) = *reinterpret_cast<const H8*>(l);
-  };
+  H* out = reinterpret_cast<H*>(own + g.x);
+  const int64_t first = (int64_t)(blockIdx.x - a.from[u]) * kPiece, row0 = first / pcols;
+  const uint32_t col0 = (uint32_t)(first - row0 * pcols);
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    const int r = threadIdx.x / 8 + 32 * half, c = threadIdx.x % 8 * kVec;
+  for (int i = 0; i < kPiece / kVec / kThreads; ++i) {
+    const uint32_t on = col0 + (i * kThreads + threadIdx.x) * kVec, down = on / (uint32_t)pcols;
+    const int64_t r = row0 + down, at = first + (on - col0);
+    const int c = (int)(on - down * (uint32_t)pcols);
+    if (at >= all) break;
     float v[kVec] = {};
-    if (r0 + r < rows && c0 + c < cols) {
-      const int64_t i = (int64_t)(r0 + r) * cols + c0 + c;
-      const int64_t stop = (int64_t)(r0 + r + 1) * cols;   // the row's end: zeros behind it
-      load8<BF>(s.x, i, stop, v);
+    if (r < rows && c < cols) {
+      const int64_t from = r * cols + c, stop = (r + 1) * cols;   // the row's end: zeros behind it
+      load8<BF>(s.x, from, stop, v);
       if (MOMENT) {
         float m[kVec];
-        load8<false>(s.moment, i, stop, m);
+        load8<false>(s.moment, from, stop, m);
         if (F == kWide) {
 #pragma unroll
           for (int q = 0; q < kVec; ++q) m[q] = moved(m[q], v[q], a.mu, a.nu);
-          store_part<false>(s.moment, i, stop, m);
-          store_part<false>(s.moment, i + 4, stop, m + 4);
+          store_part<false>(s.moment, from, stop, m);
+          store_part<false>(s.moment, from + 4, stop, m + 4);
         }
 #pragma unroll
         for (int q = 0; q < kVec; ++q) v[q] = update_of(m[q], v[q], a);
       }
     }
-    __attribute__((aligned(16))) H h[kVec], l[kVec];
+    H8 h, l;
 #pragma unroll
     for (int q = 0; q < kVec; ++q) {
-      split(ldexpf(v[q], e), h[q], l[q]);
-      tile[r][c + q] = (uint32_t)__builtin_bit_cast(uint16_t, h[q]) |
-                       (uint32_t)__builtin_bit_cast(uint16_t, l[q]) << 16;
+      H x, y;
+      split(ldexpf(v[q], e), x, y);
+      h[q] = x;
+      l[q] = y;
     }
-    put(straight + (int64_t)(r0 + r) * pcols * (PAIR ? 2 : 1), c0 + c, h, l);
-  }
-  __syncthreads();
-#pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    const int c = threadIdx.x / 8 + 32 * half, r = threadIdx.x % 8 * kVec;
-    __attribute__((aligned(16))) H h[kVec], l[kVec];
-#pragma unroll
-    for (int q = 0; q < kVec; ++q) {
-      const uint32_t w = tile[r + q][c];
-      h[q] = __builtin_bit_cast(H, (uint16_t)w);
-      l[q] = __builtin_bit_cast(H, (uint16_t)(w >> 16));
-    }
-    put(turned + (int64_t)(c0 + c) * prows * (PAIR ? 2 : 1), r0 + r, h, l);
+    H* p = out + (PAIR ? r * pcols * 2 + pair_at(c) : at);
+    *reinterpret_cast<H8*>(p) = h;
+    if (PAIR) *reinterpret_cast<H8*>(p + kPairBlock) = l;
   }
 }
 
@@ -588,13 +687,18 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_gram(const Groups a,
   int ti, tj;
   tri_tile(t, nt, ti, tj);
   uint8_t* own = ws + g.base + (int64_t)u * g.stride;
-  const int64_t ld = (int64_t)g.mt * (PAIR ? 4 : 2);
+  constexpr int kSize = PAIR ? 4 : 2;   // bytes of a number
+  const int64_t ld = (int64_t)(g.tall ? g.nt : g.mt) * kSize;
   const int stages = (g.m + 63) / 64 * (PAIR ? 2 : 1);
   const int k0 = (int)((int64_t)stages * split / g.splits);
   const int k1 = (int)((int64_t)stages * (split + 1) / g.splits);
-  const uint8_t* x = own + (second ? g.xk2 : g.xk);
+  const uint8_t* x = own + (second ? g.x2 : g.x);
   f32x16 acc[P::kB][P::kB];
-  P::run(sm, Side{x + ti * T * ld, ld, stages}, Side{x + tj * T * ld, ld, stages}, k0, k1 - k0, acc);
+  if (g.tall)
+    P::template run<true, true>(sm, Side{x + ti * T * kSize, ld, stages},
+                                Side{x + tj * T * kSize, ld, stages}, k0, k1 - k0, acc);
+  else
+    P::run(sm, Side{x + ti * T * ld, ld, stages}, Side{x + tj * T * ld, ld, stages}, k0, k1 - k0, acc);
   float* out = reinterpret_cast<float*>(own + g.part) + ((int64_t)t * g.splits + split) * T * T;
   P::each(acc, [&](int i, int j, const f32x4& v) {
     *reinterpret_cast<f32x4*>(out + i * T + j) = v;
@@ -962,19 +1066,24 @@ struct Sinks {
 };
 enum Result { kOut, kParam, kMaster };
 
+// A tile of Q X, or of X Q for a tall X, at (row0, col0) of X.
 template <int T, int RING, Form F>
 __device__ __forceinline__ void last_product(uint8_t* sm, const Group& g, uint8_t* own, int q,
-                                             bool second, bool tall, int64_t row0, int64_t col0,
+                                             bool second, int64_t row0, int64_t col0,
                                              f32x16 (&acc)[T / 64][T / 64]) {
   // Q's rows are pairs where X's are; else all hi and then all lo against X twice
   constexpr bool PAIR = Number<F>::kTwo;
-  const int64_t ld_q = (int64_t)g.nt * 4, ld_x = (int64_t)g.nt * (PAIR ? 4 : 2);
+  constexpr int kSize = PAIR ? 4 : 2;
+  using P = Product<T, RING, F>;
+  const int64_t ld_q = (int64_t)g.nt * 4, ld_x = (int64_t)(g.tall ? g.nt : g.mt) * kSize;
   const int sq = g.ne / kPairBlock, sx = PAIR ? sq : sq / 2;
-  const uint8_t* x = own + (second ? g.xt2 : g.xt);
+  const uint8_t* x = own + (second ? g.x2 : g.x);
   const uint8_t* qp = own + g.sq[q];
-  const Side qs = {qp + (tall ? col0 : row0) * ld_q, ld_q, sq};
-  const Side xs = {x + (tall ? row0 : col0) * ld_x, ld_x, sx};
-  Product<T, RING, F>::run(sm, tall ? xs : qs, tall ? qs : xs, 0, sq, acc);
+  if (g.tall)
+    P::run(sm, Side{x + row0 * ld_x, ld_x, sx}, Side{qp + col0 * ld_q, ld_q, sq}, 0, sq, acc);
+  else
+    P::template run<false, true>(sm, Side{qp + row0 * ld_q, ld_q, sq},
+                                 Side{x + col0 * kSize, ld_x, sx}, 0, sq, acc);
 }
 
 template <int T, int RING, Form F, bool BF, Result WHAT>
@@ -994,7 +1103,7 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_apply(const Sinks a,
   const int64_t row0 = (int64_t)(tall ? t / across : t % down) * T;
   const int64_t col0 = (int64_t)(tall ? t % across : t / down) * T;
   f32x16 acc[P::kB][P::kB];
-  last_product<T, RING, F>(sm, g, own, a.q, a.second, tall, row0, col0, acc);
+  last_product<T, RING, F>(sm, g, own, a.q, a.second, row0, col0, acc);
   float* tile = P::stage(sm, acc);
   const Sink s = a.s[u];
   const float f = *reinterpret_cast<const float*>(own + g.scale) * a.unit *
@@ -1024,7 +1133,7 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_apply(const Sinks a,
   });
 }
 
-// Q X as pairs in both orders, in place of X from here on.
+// Q X as pairs, in place of X from here on.
 template <int T, int RING, Form F>
 __global__ __launch_bounds__(kThreads) void dora_orthogonal_between(const Groups a, uint32_t total,
                                                                     int q, float unit, bool second,
@@ -1033,30 +1142,24 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_between(const Groups
   __shared__ __attribute__((aligned(1024))) uint8_t sm[P::kLds];
   const uint32_t id = by_xcd(blockIdx.x, total);
   const Group& g = a.g[group_of(a, id)];
-  const int down = (g.n + T - 1) / T, tiles = down * ((g.m + T - 1) / T);
+  const int down = ((g.tall ? g.m : g.n) + T - 1) / T, across = ((g.tall ? g.n : g.m) + T - 1) / T;
   const int rest = (int)(id - g.from);
-  const int t = rest % tiles, u = rest / tiles;
+  const int t = rest % (down * across), u = rest / (down * across);
   uint8_t* own = ws + g.base + (int64_t)u * g.stride;
-  const int64_t row0 = (int64_t)(t % down) * T, col0 = (int64_t)(t / down) * T;
+  const int64_t row0 = (int64_t)(g.tall ? t / across : t % down) * T;
+  const int64_t col0 = (int64_t)(g.tall ? t % across : t / down) * T;
   f32x16 acc[P::kB][P::kB];
-  last_product<T, RING, F>(sm, g, own, q, second, false, row0, col0, acc);
+  last_product<T, RING, F>(sm, g, own, q, second, row0, col0, acc);
   float* tile = P::stage(sm, acc);
   const float f = *reinterpret_cast<const float*>(own + g.scale) * unit;
-  f16* xk = reinterpret_cast<f16*>(own + (second ? g.xk : g.xk2));
-  f16* xt = reinterpret_cast<f16*>(own + (second ? g.xt : g.xt2));
+  f16* x = reinterpret_cast<f16*>(own + (second ? g.x : g.x2));
+  const int64_t ld = 2 * (int64_t)(g.tall ? g.nt : g.mt);
   P::lines([&](int r, int c) {
     float v[8];
     P::row8(tile, r, c, v);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] *= f;
-    store_pair<8>(xk + (row0 + r) * 2 * g.mt, col0 + c, v);
-  });
-  P::lines([&](int c, int r) {
-    float v[8];
-    P::column8(tile, r, c, v);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] *= f;
-    store_pair<8>(xt + (col0 + c) * 2 * g.nt, row0 + r, v);
+    store_pair<8>(x + (row0 + r) * ld, col0 + c, v);
   });
 }
 
@@ -1174,14 +1277,8 @@ void lay_out(Group& g, const Kind& k, int gram) {
     at += padded(bytes, 256);
     return here;
   };
-  const int64_t x = (int64_t)g.nt * g.mt * (k.form != kSingle || k.times > 1 ? 4 : 2);
-  g.xk = take(x);
-  g.xt = take(x);
-  g.xk2 = g.xt2 = 0;
-  if (k.times) {
-    g.xk2 = take((int64_t)g.nt * g.mt * 4);
-    g.xt2 = take((int64_t)g.nt * g.mt * 4);
-  }
+  g.x = take((int64_t)g.nt * g.mt * (k.form != kSingle || k.times > 1 ? 4 : 2));
+  g.x2 = k.times ? take((int64_t)g.nt * g.mt * 4) : 0;
   for (int64_t& s : g.sq) s = take((int64_t)g.nt * g.nt * 4);
   g.part = take((int64_t)tri(tiles(g.n, gram)) * g.splits * gram * gram * 4);
   g.trace = take((int64_t)tiles(g.n, gram) * g.splits * kWaves * 4);
@@ -1362,7 +1459,7 @@ struct Engine {
                                           st, a, ws);
                           }));
     return by_form<FORMS...>([&](auto f) {
-      return by_matrix(p, a, [](const Group& g) { return (int64_t)(g.nt / 64) * (g.mt / 64); }, fill,
+      return by_matrix(p, a, [](const Group& g) { return ((int64_t)g.nt * g.mt + kPiece - 1) / kPiece; }, fill,
                        [&](int64_t blocks) {
                          return launch("orthogonal_halves",
                                        dora_orthogonal_halves<BF, MOMENT, decltype(f)::value>, blocks,
