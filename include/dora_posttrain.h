@@ -152,7 +152,8 @@ typedef struct {
 
 typedef struct {
     const void* x;     /* [rows, cols] contiguous                                             */
-    void*       out;   /* [rows, cols] contiguous; may be x itself, must not overlap otherwise */
+    void*       out;   /* [rows, cols] contiguous; may be its own x, must overlap no other array
+                          of the call                                                        */
     int64_t     rows;  /* >= 0; the longer of both at most 2^20, the shorter at most 16384    */
     int64_t     cols;
 } dora_matrix;
@@ -166,8 +167,8 @@ typedef struct {
 /*
  * out = the iteration's last X for each of `count` matrices (`matrices` and the
  * coefficients are host arrays, read during the call only).  Matrices of any sizes
- * share launches; the workspace holds about 4 bytes (bf16) or 16 (float32) an
- * element and 20 n^2 for a shorter side of n.  Sums are float32, and float32
+ * share launches; the workspace holds 2 bytes (bf16) or 8 (float32) an element, 20 n^2
+ * for a shorter side of n, and partial sums; sides are padded to 128.  Sums are float32, and float32
  * results have float32's precision.  A matrix of zeros stays zero; one with a NaN
  * or an infinity becomes NaN throughout, the others of the call do not.
  */
@@ -198,12 +199,16 @@ typedef struct {
 } dora_muon_options;
 
 /*
- * A step on `count` matrices with orthogonalised updates (no two of the arrays
- * that are written may overlap):
+ * A step on `count` matrices with orthogonalised updates (no array that is written
+ * may overlap another one of the call):
  *   m = momentum m + (1 - momentum) grad
  *   u = momentum m + (1 - momentum) grad with nesterov, else m
  *   p = p (1 - lr weight_decay) - lr scale X(u),  X(u) the iteration's last X from u
- * m, u and the update are float32; p is rounded once.
+ * m and the update are float32; p is rounded once.  u is taken to 22 bits, to 16 for bf16
+ * parameters without masters, and from |u| = 2^104 eps on the latter become NaN.  A NaN or an
+ * infinity in a gradient makes its own element of m, and its own matrix, NaN.  The workspace holds 4
+ * (bf16 parameters without masters) or 8 bytes an element beside what dora_orthogonalize's holds
+ * for n.
  */
 DORA_API size_t dora_muon_workspace_bytes(const dora_muon_tensor* tensors, int64_t count,
                                           const dora_muon_options* options);

@@ -9,6 +9,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ATen.h>
+#include <c10/core/DeviceGuard.h>
 
 #include <algorithm>
 #include <cmath>
@@ -538,6 +539,7 @@ PyObject* preference_loss(PyObject*, PyObject* const* args, Py_ssize_t n) {
     Py_RETURN_NONE;
   const dora_preference_options o = {(int32_t)PyLong_AsLong(args[9]), args[10] == Py_True, v[0], v[1],
                                      v[2]};
+  const c10::DeviceGuard on(x.device());   // (the null stream is the current device's)
   const int64_t P = t[2]->size(0), S = b.sequences;
   const at::Tensor whole = at::empty({2 * (P + S)}, x.options());
   int64_t from = 0;
@@ -582,6 +584,7 @@ PyObject* preference_loss_backward(PyObject*, PyObject* const* args, Py_ssize_t 
     Py_RETURN_NONE;
   const dora_preference_options o = {(int32_t)PyLong_AsLong(args[10]), args[11] == Py_True, v[0], v[1],
                                      v[2]};
+  const c10::DeviceGuard on(x.device());
   const at::Tensor grad = at::empty(shape, x.options());
   const size_t need = g_api.preference_workspace_bytes(&b);
   const at::Tensor ws = workspace(need, x);
@@ -624,6 +627,7 @@ PyObject* policy_loss(PyObject*, PyObject* const* args, Py_ssize_t n) {
   Policy p;
   if (n != Policy::kCount + 1 || !p.read(args)) Py_RETURN_NONE;
   const at::Tensor& x = *p.t[0];
+  const c10::DeviceGuard on(x.device());
   const at::Tensor whole = at::empty({5 + p.weights()}, x.options());
   int64_t from = 0;
   const at::Tensor loss = take(whole, from, {}), stats = take(whole, from, {4}),
@@ -649,6 +653,7 @@ PyObject* policy_loss_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (!floats_as(g[0], g[0]->sizes(), x) || g[0]->numel() != 1 ||
       !vector_ok(g[1], p.weights(), at::kFloat, x))
     Py_RETURN_NONE;
+  const c10::DeviceGuard on(x.device());
   const at::Tensor grad = at::empty(x.sizes(), x.options());
   if (g_api.policy_backward(&p.b, &p.o, floats(g[0]), floats(g[1]), floats(&x), floats(p.t[1]),
                             floats(p.t[3]), floats(p.t[2]), floats(grad),
@@ -672,6 +677,7 @@ PyObject* orthogonalize(PyObject*, PyObject* const* args, Py_ssize_t n) {
   o.iteration.steps = (int32_t)PyLong_AsLong(args[2]);
   o.iteration.eps = eps[0];
   o.dtype = code;
+  const c10::DeviceGuard on(x.device());
   const at::Tensor out = at::empty(x.sizes(), x.options());
   const int64_t rows = x.size(-2), cols = x.size(-1), count = x.dim() == 3 ? x.size(0) : 1;
   const int64_t bytes = rows * cols * (int64_t)x.element_size();
@@ -740,6 +746,10 @@ PyObject* muon_step(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (n != 6 || !PyList_Check(args[1])) Py_RETURN_NONE;
   const Py_ssize_t count = PyList_GET_SIZE(args[1]);
   const size_t bytes = PyLong_AsSize_t(args[4]);
+  bool ok = count > 0;
+  const at::Tensor* one = ok ? tensor(PyList_GET_ITEM(args[1], 0), ok) : nullptr;
+  if (!one) Py_RETURN_NONE;
+  const c10::DeviceGuard on(one->device());
   const int rc = g_api.muon_step(static_cast<dora_muon_tensor*>(PyLong_AsVoidPtr(args[0])), count,
                                  static_cast<dora_muon_options*>(PyLong_AsVoidPtr(args[2])),
                                  PyLong_AsVoidPtr(args[3]), bytes, stream_of(args[5]));

@@ -527,10 +527,11 @@ def dora_preference_loss(logp, chosen, rejected, *, ref_logp=None, mask=None, of
     score, count = torch.empty(2, S, dtype=torch.float32, device=dev).unbind(0)
     L = _lib.lib()
     ws, nb = _some_ws(L.dora_preference_workspace_bytes(ctypes.byref(batch)), dev, workspace)
-    _check(L.dora_preference_forward(ctypes.byref(batch), ctypes.byref(how), P, _ptr(logp),
-                                     _ptr(ref_logp), _ptr(chosen), _ptr(rejected), _ptr(loss),
-                                     _ptr(score), _ptr(logit), _ptr(count), _ptr(ws), nb,
-                                     _stream(dev)), "dora_preference_forward")
+    with torch.cuda.device(dev):   # (the null stream is the current device's)
+        _check(L.dora_preference_forward(ctypes.byref(batch), ctypes.byref(how), P, _ptr(logp),
+                                         _ptr(ref_logp), _ptr(chosen), _ptr(rejected), _ptr(loss),
+                                         _ptr(score), _ptr(logit), _ptr(count), _ptr(ws), nb,
+                                         _stream(dev)), "dora_preference_forward")
     return loss, score, logit, count
 
 
@@ -565,10 +566,11 @@ def dora_preference_loss_backward(grad_loss, logit, count, chosen, rejected, *, 
     grad_logp = _out(grad_logp, "grad_logp", torch.float32, shape, dev)
     L = _lib.lib()
     ws, nb = _some_ws(L.dora_preference_workspace_bytes(ctypes.byref(batch)), dev, workspace)
-    _check(L.dora_preference_backward(ctypes.byref(batch), ctypes.byref(how), P, _ptr(grad_loss),
-                                      _ptr(logit), _ptr(count), _ptr(chosen), _ptr(rejected),
-                                      _ptr(grad_logp), _ptr(ws), nb, _stream(dev)),
-           "dora_preference_backward")
+    with torch.cuda.device(dev):   # (the null stream is the current device's)
+        _check(L.dora_preference_backward(ctypes.byref(batch), ctypes.byref(how), P, _ptr(grad_loss),
+                                          _ptr(logit), _ptr(count), _ptr(chosen), _ptr(rejected),
+                                          _ptr(grad_logp), _ptr(ws), nb, _stream(dev)),
+               "dora_preference_backward")
     return grad_logp
 
 
@@ -635,9 +637,10 @@ def dora_policy_loss(logp, old_logp, advantages, *, ref_logp=None, mask=None, of
     L = _lib.lib()
     nb = L.dora_policy_workspace_bytes(ctypes.byref(batch), ctypes.byref(how))
     ws, nb = _some_ws(nb, dev, workspace)
-    _check(L.dora_policy_forward(ctypes.byref(batch), ctypes.byref(how), _ptr(logp), _ptr(old_logp),
-                                 _ptr(ref_logp), _ptr(advantages), _ptr(loss), _ptr(stats),
-                                 _ptr(weight), _ptr(ws), nb, _stream(dev)), "dora_policy_forward")
+    with torch.cuda.device(dev):   # (the null stream is the current device's)
+        _check(L.dora_policy_forward(ctypes.byref(batch), ctypes.byref(how), _ptr(logp), _ptr(old_logp),
+                                     _ptr(ref_logp), _ptr(advantages), _ptr(loss), _ptr(stats),
+                                     _ptr(weight), _ptr(ws), nb, _stream(dev)), "dora_policy_forward")
     return loss, stats, weight
 
 
@@ -659,10 +662,11 @@ def dora_policy_loss_backward(grad_loss, weight, logp, old_logp, advantages, *, 
         raise ValueError("grad_loss must be one number")
     _need(weight, "weight", torch.float32, (batch.sequences if how.reduce else 1,), dev)
     grad_logp = _out(grad_logp, "grad_logp", torch.float32, logp.shape, dev)
-    _check(_lib.lib().dora_policy_backward(ctypes.byref(batch), ctypes.byref(how), _ptr(grad_loss),
-                                           _ptr(weight), _ptr(logp), _ptr(old_logp), _ptr(ref_logp),
-                                           _ptr(advantages), _ptr(grad_logp), _stream(dev)),
-           "dora_policy_backward")
+    with torch.cuda.device(dev):   # (the null stream is the current device's)
+        _check(_lib.lib().dora_policy_backward(ctypes.byref(batch), ctypes.byref(how), _ptr(grad_loss),
+                                               _ptr(weight), _ptr(logp), _ptr(old_logp), _ptr(ref_logp),
+                                               _ptr(advantages), _ptr(grad_logp), _stream(dev)),
+               "dora_policy_backward")
     return grad_logp
 
 
@@ -877,9 +881,9 @@ def dora_orthogonalize(x, *, coefficients=NEWTON_SCHULZ, eps=1e-7, out=None, wor
             raise ValueError(f"{name} has {t.dim()} dimensions, expected a matrix"
                              + ("" if many else " or a stack of them"))
         outs[i] = _out(outs[i], "out", dt, t.shape, dev)
-        if outs[i].data_ptr() != t.data_ptr():
-            _disjoint(outs[i], t, "out", name)
         counts.append(t.shape[0] if t.dim() == 3 else 1)
+    if out is not None:
+        _disjoint(outs, xs)
     table = (_lib.DoraMatrix * max(sum(counts), 1))()
     size, at = xs[0].element_size(), 0
     for t, o, k in zip(xs, outs, counts):
@@ -894,16 +898,27 @@ def dora_orthogonalize(x, *, coefficients=NEWTON_SCHULZ, eps=1e-7, out=None, wor
     L = _lib.lib()
     nb = L.dora_orthogonalize_workspace_bytes(table, at, ctypes.byref(how))
     ws, nb = _some_ws(nb, dev, workspace)
-    _check(L.dora_orthogonalize(table, at, ctypes.byref(how), _ptr(ws), nb, _stream(dev)),
-           "dora_orthogonalize")
+    with torch.cuda.device(dev):   # (the null stream is the current device's)
+        _check(L.dora_orthogonalize(table, at, ctypes.byref(how), _ptr(ws), nb, _stream(dev)),
+               "dora_orthogonalize")
     return outs if many else outs[0]
 
 
-def _disjoint(a, b, name, other):
-    if a.numel() and b.numel():
-        lo, hi = a.data_ptr(), a.data_ptr() + a.numel() * a.element_size()
-        if lo < b.data_ptr() + b.numel() * b.element_size() and b.data_ptr() < hi:
-            raise ValueError(f"{name} must not overlap {other}")
+def _disjoint(outs, xs):
+    """Refuses outputs that share memory with each other or with an input that is not their own:
+    matrices are worked on in any order."""
+    spans = []   # (first byte, end, whether it is written)
+    for o, x in zip(outs, xs):
+        if o.numel():
+            size, a, b = o.numel() * o.element_size(), o.data_ptr(), x.data_ptr()
+            spans.append((a, a + size, True))
+            if a != b:
+                spans.append((b, b + size, False))
+    end = written = 0
+    for lo, hi, write in sorted(spans):
+        if lo < (end if write else written):
+            raise ValueError("out must not overlap: a matrix may take its own x's place, and no other")
+        end, written = max(end, hi), max(written, hi if write else 0)
 
 
 class MuonPlan:

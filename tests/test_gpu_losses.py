@@ -316,6 +316,52 @@ def test_more_tokens_than_one_round_a_wave(ops):
     assert not grad[:5].any() and not grad[at[-1]:].any() and not pg[:5].any() and not pg[at[-1]:].any()
 
 
+def test_more_than_2_32_tokens(ops):
+    """Token numbers pass 2^32; the sequences' log ratios are 1/4 a token, and every fourth is masked."""
+    n = 2 ** 32 + 5003
+    at = [3, 2 ** 31 + 9, 2 ** 32 - 1, 2 ** 32 + 1, 2 ** 32 + 4999]
+    off = torch.tensor(at, device="cuda")
+    logp = torch.full((n,), -0.5, device="cuda")
+    old = torch.full((n,), -0.75, device="cuda")
+    mask = torch.ones(n, dtype=torch.bool, device="cuda")
+    mask[::4] = False
+    live = [b - a - ((b + 3) // 4 - (a + 3) // 4) for a, b in zip(at, at[1:])]
+    c, r = torch.tensor([0, 2], device="cuda"), torch.tensor([1, 3], device="cuda")
+    loss, score, logit, count = ops.dora_preference_loss(logp, c, r, ref_logp=old, mask=mask, offsets=off,
+                                                         beta=1e-9)
+    near(score, [0.25e-9 * v for v in live])
+    near(count, live)
+    gl = torch.ones(2, device="cuda")
+    g = ops.dora_preference_loss_backward(gl, logit, count, c, r, shape=(n,), mask=mask, offsets=off, beta=1e-9)
+    slope = [1e-9 / (1 + math.exp(float(h))) for h in logit]
+
+    def ends(g, values):
+        """The first and last counted tokens of each sequence, and those around them."""
+        for s, v in enumerate(values):
+            for t in {*range(at[s], at[s] + 5), *range(at[s + 1] - 5, at[s + 1])}:
+                if at[s] <= t < at[s + 1]:
+                    near(g[t], v if t % 4 else 0.0)
+        assert not g[:at[0]].any() and not g[at[-1]:].any()
+        # what a sequence holds beside its value and zero would change these
+        total = sum(float(p.double().sum()) for p in g.split(2 ** 30))
+        each = [v * k for v, k in zip(values, live)]
+        assert abs(total - sum(each)) <= 1e-6 * sum(abs(v) for v in each)
+
+    ends(g, [-slope[0], slope[0], -slope[1], slope[1]])
+    del g
+    adv = torch.tensor([1.0, -1.0, 0.5, 2.0], device="cuda")
+    rho = math.exp(0.25)
+    gain = [1.2, -rho, 0.6, 2.4]   # of 1 + 0.2, and the ratio itself for the negative advantage
+    one = torch.ones((), device="cuda")
+    for reduce in ("token", "sequence"):
+        value, stats, w = ops.dora_policy_loss(logp, old, adv, mask=mask, offsets=off, reduce=reduce)
+        by = [1 / sum(live)] * 4 if reduce == "token" else [0.25 / k for k in live]
+        near(value, -sum(a * k * f for a, k, f in zip(gain, live, by)), 10.0)
+        g = ops.dora_policy_loss_backward(one, w, logp, old, adv, mask=mask, offsets=off, reduce=reduce)
+        w = w.expand(4).tolist()
+        ends(g, [0.0, rho * w[1], 0.0, 0.0])
+
+
 def test_offsets_that_are_wrong_touch_nothing_else(ops):
     """Decreasing, negative and too large offsets: any numbers, but none outside the tensors."""
     room = torch.full((3000,), 7.0, device="cuda")
@@ -404,6 +450,21 @@ def test_same_bits_again_on_another_stream_and_from_a_graph(ops):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) for x, y in zip(held, want)), k
+
+
+@pytest.mark.skipif(torch.cuda.device_count() < 2, reason="needs a second GPU")
+def test_another_device_than_the_current_one(ops):
+    def run(device):
+        logp = torch.linspace(-3, -1, 80, device=device).view(4, 20)
+        adv = torch.linspace(-1, 1, 4, device=device)
+        c, r = torch.tensor([0, 2], device=device), torch.tensor([1, 3], device=device)
+        a = ops.dora_preference_loss(logp, c, r)
+        b = ops.dora_policy_loss(logp, logp - 0.1, adv)
+        one = torch.ones((), device=device)
+        return [*a, *b, ops.dora_preference_loss_backward(a[0], a[2], a[3], c, r, shape=(4, 20)),
+                ops.dora_policy_loss_backward(one, b[2], logp, logp - 0.1, adv)]
+
+    assert all(torch.equal(x.cpu(), y.cpu()) for x, y in zip(run("cuda:0"), run("cuda:1")))
 
 
 def test_through_autograd(ops):
