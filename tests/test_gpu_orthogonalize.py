@@ -3,8 +3,9 @@
 Tolerances.  A rounding E of the first S (relative to its Frobenius norm, which is at most 1) changes
 a singular value's result by at most R E of itself, R = sum_j |b_j / a_j| prod_{i<j} a_i^2 over the
 steps until S is formed anew: 3.02e4 for the usual five (bf16 results), 213 for three of them and 18
-for the remaining two (updates of float32 parameters), 18 for two, two and one (float32 matrices).  E is taken as 2^-22: two roundings of 22 or more bits (S as
-hi + lo, the lo lo product left out), and float32 sums, whose errors are independent.
+for the remaining two (updates of float32 parameters), 18 for two, two and one (float32 matrices).  E
+is taken as 2^-22: two roundings of 22 or more bits (S as hi + lo, the lo lo product left out), and
+float32 sums, whose errors are independent.
 
 X itself is held as hi + lo too: half precision's half step is 2^-11 of a number, so what hi leaves is
 2^-11 of it and what lo leaves 2^-22 of it, in norm 2^-22 |X| and |X| = 1 after the first division.
