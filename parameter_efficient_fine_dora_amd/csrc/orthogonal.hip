@@ -52,7 +52,7 @@ constexpr int kWaves = kThreads / 64;
 constexpr int kRowBytes = 128;       // of a row in one stage
 constexpr int kPairBlock = 32;       // columns of a pair row's block
 constexpr int kMaxGroups = 12;
-constexpr int kMaxMatrices = 48;     // of one launch that needs their addresses
+constexpr int kMaxMatrices = 120;    // of one launch that needs their addresses
 constexpr int kMaxSteps = 16;
 constexpr int kMaxBlocks = 1024;     // workgroups that look for one matrix's largest element
 constexpr int kMaxSplits = 32;
@@ -66,11 +66,12 @@ struct Group {
   int count;           // matrices
   int first;           // the first one's number
   uint32_t from;       // the launch's first workgroup of this group
+  int each, begin;     // where addresses are taken: workgroups of a matrix, the launch's first one
   int splits;          // of the sum over m
   int blocks;          // partial maxima
   int64_t base, stride;
   int64_t x, x2;       // X in its own order, and the product formed on the way
-  int64_t sq[5];       // n x n pairs: S, P, P S, and Q twice
+  int64_t sq;          // five n x n pairs: S, P, P S, and Q twice
   int64_t part, trace; // partial sums of S and of its trace, float32
   int64_t most, scale; // partial maxima; the factor on X
   bool tall;           // rows are the longer side
@@ -79,6 +80,9 @@ struct Groups {
   int count;
   Group g[kMaxGroups];
 };
+__device__ __forceinline__ uint8_t* square_of(const Group& g, uint8_t* own, int i) {
+  return own + g.sq + (int64_t)i * g.nt * g.nt * 4;
+}
 
 __host__ __device__ inline int tri(int t) { return t * (t + 1) / 2; }
 
@@ -510,28 +514,25 @@ struct Source {
 };
 struct Sources {
   Groups groups;
-  int count;                       // matrices of this launch
-  int first;                       // number of the first
-  uint32_t from[kMaxMatrices];     // their first workgroups
+  int first;                       // number of the launch's first matrix
   Source s[kMaxMatrices];
   float mu, nu;                    // momentum's factor, 1 - that
   int nesterov;
   int fixed;                       // kWide: the power of two that X is multiplied by
 };
 
-__device__ __forceinline__ int matrix_of(const uint32_t* from, int count, uint32_t id) {
-  int lo = 0, hi = count;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (id >= from[mid]) lo = mid;
-    else hi = mid;
-  }
-  return __builtin_amdgcn_readfirstlane(lo);
-}
-__device__ __forceinline__ int group_of_matrix(const Groups& a, int matrix) {
-  int g = 0;
-  while (g + 1 < a.count && matrix >= a.g[g + 1].first) ++g;
-  return __builtin_amdgcn_readfirstlane(g);
+// Which matrix a workgroup of a launch with addresses works on.
+struct Where {
+  const Group& g;
+  int slot;      // of the launch's addresses
+  int piece;     // of the matrix's workgroups
+  uint8_t* own;
+};
+__device__ __forceinline__ Where where(const Groups& a, int first, uint32_t id, uint8_t* ws) {
+  const Group& g = a.g[group_of(a, id)];
+  const int u = (int)(id - g.from) / g.each, matrix = g.begin + u;
+  return {g, __builtin_amdgcn_readfirstlane(matrix - first), (int)(id - g.from) - u * g.each,
+          ws + g.base + (int64_t)(matrix - g.first) * g.stride};
 }
 __device__ __forceinline__ float moved(float m, float g, float mu, float nu) {
   return fmaf(mu, m, nu * g);
@@ -555,11 +556,11 @@ __device__ __forceinline__ void load8(const void* p, int64_t i, int64_t n, float
 template <bool BF, bool MOMENT>
 __global__ __launch_bounds__(kThreads) void dora_orthogonal_most(const Sources a, uint8_t* ws) {
   __shared__ uint32_t lds[kThreads / 64];
-  const int u = matrix_of(a.from, a.count, blockIdx.x);
-  const Group& g = a.groups.g[group_of_matrix(a.groups, a.first + u)];
+  const Where at = where(a.groups, a.first, blockIdx.x, ws);
+  const Group& g = at.g;
   const int64_t n = (int64_t)g.n * g.m;
-  const int block = blockIdx.x - a.from[u];
-  const Source s = a.s[u];
+  const int block = at.piece;
+  const Source s = a.s[at.slot];
   uint32_t most = 0;
   for (int64_t i = ((int64_t)block * kThreads + threadIdx.x) * kVec; i < n;
        i += (int64_t)g.blocks * kThreads * kVec) {
@@ -586,8 +587,7 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_most(const Sources a
   if (threadIdx.x == 0) {
 #pragma unroll
     for (int w = 1; w < kThreads / 64; ++w) most = max(most, lds[w]);
-    uint8_t* own = ws + g.base + (int64_t)(a.first + u - g.first) * g.stride;
-    reinterpret_cast<uint32_t*>(own + g.most)[block] = most;
+    reinterpret_cast<uint32_t*>(at.own + g.most)[block] = most;
   }
 }
 
@@ -620,17 +620,17 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_halves(const Sources
   constexpr bool PAIR = Number<F>::kTwo;
   typedef H H8 __attribute__((ext_vector_type(8)));
   __shared__ uint32_t lds[kThreads / 64];
-  const int u = matrix_of(a.from, a.count, blockIdx.x);
-  const Group& g = a.groups.g[group_of_matrix(a.groups, a.first + u)];
-  uint8_t* own = ws + g.base + (int64_t)(a.first + u - g.first) * g.stride;
+  const Where here = where(a.groups, a.first, blockIdx.x, ws);
+  const Group& g = here.g;
+  uint8_t* own = here.own;
   const int rows = g.tall ? g.m : g.n, cols = g.tall ? g.n : g.m;
   const int pcols = g.tall ? g.nt : g.mt;
   const int64_t all = (int64_t)g.nt * g.mt;
   const int e = F == kWide ? a.fixed
                            : exponent_of(reinterpret_cast<const uint32_t*>(own + g.most), g.blocks, lds);
-  const Source s = a.s[u];
+  const Source s = a.s[here.slot];
   H* out = reinterpret_cast<H*>(own + g.x);
-  const int64_t first = (int64_t)(blockIdx.x - a.from[u]) * kPiece, row0 = first / pcols;
+  const int64_t first = (int64_t)here.piece * kPiece, row0 = first / pcols;
   const uint32_t col0 = (uint32_t)(first - row0 * pcols);
 #pragma unroll
   for (int i = 0; i < kPiece / kVec / kThreads; ++i) {
@@ -714,6 +714,297 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_gram(const Groups a,
     reinterpret_cast<float*>(own + g.trace)[(ti * g.splits + split) * kWaves + threadIdx.x / 64] = sum;
 }
 
+// ---- n <= 64: S while X is written or taken further -----------------------------------------------
+// A block of 64 of the longer side is all that S's sum needs of it, and fits a workgroup's LDS.
+
+// A wave's quarter of S, 32 x 32, summed over blocks in LDS (`TURNED`: their rows run across the sum).
+template <Form F, bool TURNED>
+struct Sums {
+  using Side64 = Operand<64, F, TURNED, kWaves>;
+  static constexpr bool PAIR = F != kSingle;
+  static constexpr int kStages = PAIR ? 2 : 1, kBytes = Side64::kBytes;   // of a block
+  static constexpr int kBlock = kStages * kBytes;
+  Side64 a, b;
+  f32x16 acc, low;
+
+  __device__ __forceinline__ Sums() {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const Side none = {nullptr, 0, 1};
+    a.start(none, 0, wave & 1);
+    b.start(none, 0, wave >> 1);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[e] = low[e] = 0.f;
+  }
+  // Where eight columns of a row of X begin in a block; a pair's lo lie kLo chunks on.
+  __device__ static __forceinline__ uint8_t* at(uint8_t* block, int row, int c, int lo) {
+    if constexpr (TURNED) {
+      const int chunk = PAIR ? (c >> 5) * 8 + ((c & 31) >> 3) + lo : c >> 3;
+      return block + row * Side64::kAcross + ((chunk ^ Side64::swizzle(row)) << 4);
+    } else {
+      const int chunk = PAIR ? ((c & 31) >> 3) + lo : c >> 3;
+      return block + (PAIR ? (c >> 5) * kBytes : 0) + row * kRowBytes + ((chunk ^ swz(row)) << 4);
+    }
+  }
+  __device__ __forceinline__ void add(const uint8_t* block) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    auto step = [&](const uint8_t* src, auto number) {
+      constexpr int U = decltype(number)::value;
+      short8 fa[1], la[1], fb[1], lb[1];
+      a.template read<U>(src, wave & 1, 0, fa, la);
+      b.template read<U>(src, wave >> 1, 0, fb, lb);
+      if constexpr (PAIR) {
+        low = multiply<F>(fb[0], la[0], low);
+        low = multiply<F>(lb[0], fa[0], low);
+      }
+      acc = multiply<F>(fb[0], fa[0], acc);
+    };
+#pragma unroll
+    for (int s = 0; s < kStages; ++s) {
+      step(block + s * kBytes, std::integral_constant<int, 0>());
+      step(block + s * kBytes, std::integral_constant<int, 1>());
+    }
+    if constexpr (!PAIR) {
+      step(block, std::integral_constant<int, 2>());
+      step(block, std::integral_constant<int, 3>());
+    }
+  }
+  // The partial sums and this wave's part of their trace, as dora_orthogonal_gram leaves them.
+  __device__ __forceinline__ void give(const Group& g, uint8_t* own, int split) {
+    using P = Product<64, 4, F>;
+    const f32x16 all[1][1] = {{acc + low}};
+    float* out = reinterpret_cast<float*>(own + g.part) + (int64_t)split * 64 * 64;
+    float sum = 0.f;
+    P::each(all, [&](int i, int j, const f32x4& v) {
+      *reinterpret_cast<f32x4*>(out + i * 64 + j) = v;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum += i == j + e ? v[e] : 0.f;
+    });
+    sum = wave_sum(sum);
+    if ((threadIdx.x & 63) == 0)
+      reinterpret_cast<float*>(own + g.trace)[split * kWaves + threadIdx.x / 64] = sum;
+  }
+};
+
+// X as halves (see dora_orthogonal_halves) and the sums of S over it in one pass: X is written, but
+// not read again for S.  The numbers of the next block are under way while this one is multiplied.
+template <bool BF, bool MOMENT, Form F>
+__global__ __launch_bounds__(kThreads) void dora_orthogonal_first(const Sources a, uint8_t* ws) {
+  using H = typename Number<F>::T;
+  constexpr bool PAIR = Number<F>::kTwo;
+  typedef H H8 __attribute__((ext_vector_type(8)));
+  constexpr int kBlock = Sums<F, false>::kBlock, kMine = 64 * 64 / kVec / kThreads;
+  __shared__ __attribute__((aligned(1024))) uint8_t sm[2][kBlock];
+  __shared__ uint32_t lds[kThreads / 64];
+  const Where here = where(a.groups, a.first, blockIdx.x, ws);
+  const Group& g = here.g;
+  const Source s = a.s[here.slot];
+  const int e = F == kWide ? a.fixed
+                           : exponent_of(reinterpret_cast<const uint32_t*>(here.own + g.most), g.blocks, lds);
+  const int rows = g.tall ? g.m : g.n, cols = g.tall ? g.n : g.m, pcols = g.tall ? g.nt : g.mt;
+  const int blocks = (g.m + 63) / 64;
+  const int k0 = (int)((int64_t)blocks * here.piece / g.splits);
+  const int k1 = (int)((int64_t)blocks * (here.piece + 1) / g.splits);
+  H* out = reinterpret_cast<H*>(here.own + g.x);
+  auto run = [&](auto tall) {
+    constexpr bool TALL = decltype(tall)::value;
+    Sums<F, TALL> sums;
+    float v[kMine][kVec], m[MOMENT ? kMine : 1][kVec];
+    auto place = [&](int k, int i, int& r, int& c, int64_t& r_all, int64_t& c_all) {
+      r = (i * kThreads + (int)threadIdx.x) / 8;
+      c = (int)threadIdx.x % 8 * kVec;
+      r_all = r + (TALL ? (int64_t)k * 64 : 0);
+      c_all = c + (TALL ? 0 : (int64_t)k * 64);
+      return r_all < rows && c_all < cols;
+    };
+    auto load = [&](int k) {
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        int r, c;
+        int64_t ra, ca;
+#pragma unroll
+        for (int q = 0; q < kVec; ++q) v[i][q] = m[MOMENT ? i : 0][q] = 0.f;
+        if (!place(k, i, r, c, ra, ca)) continue;
+        load8<BF>(s.x, ra * cols + ca, (ra + 1) * cols, v[i]);
+        if (MOMENT) load8<false>(s.moment, ra * cols + ca, (ra + 1) * cols, m[MOMENT ? i : 0]);
+      }
+    };
+    load(k0);
+    for (int k = k0; k < k1; ++k) {
+      uint8_t* block = sm[(k - k0) & 1];
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        int r, c;
+        int64_t ra, ca;
+        const bool real = place(k, i, r, c, ra, ca);
+        if (MOMENT) {
+          float* mo = m[MOMENT ? i : 0];
+          if (F == kWide) {
+#pragma unroll
+            for (int q = 0; q < kVec; ++q) mo[q] = moved(mo[q], v[i][q], a.mu, a.nu);
+            if (real) {
+              store_part<false>(s.moment, ra * cols + ca, (ra + 1) * cols, mo);
+              store_part<false>(s.moment, ra * cols + ca + 4, (ra + 1) * cols, mo + 4);
+            }
+          }
+#pragma unroll
+          for (int q = 0; q < kVec; ++q) v[i][q] = update_of(mo[q], v[i][q], a);
+        }
+        H8 h, l;
+#pragma unroll
+        for (int q = 0; q < kVec; ++q) {
+          // (behind a row's end are zeros, and update_of of the zeros of gradient and momentum)
+          H x, y;
+          split(ldexpf(v[i][q], e), x, y);
+          h[q] = x;
+          l[q] = y;
+        }
+        H* to = out + (PAIR ? ra * pcols * 2 + pair_at(ca) : ra * pcols + ca);
+        *reinterpret_cast<H8*>(to) = h;
+        *reinterpret_cast<H8*>(sums.at(block, r, c, 0)) = h;
+        if (PAIR) {
+          *reinterpret_cast<H8*>(to + kPairBlock) = l;
+          *reinterpret_cast<H8*>(sums.at(block, r, c, 4)) = l;
+        }
+      }
+      if (k + 1 < k1) load(k + 1);
+      wait_lds();
+      barrier_nofence();
+      sums.add(block);   // (the other block is written next, this one behind another barrier)
+      wait_lds();
+    }
+    sums.give(g, here.own, here.piece);
+  };
+  if (g.tall) run(std::true_type());
+  else run(std::false_type());
+}
+
+// Y = Q_k .. Q_1 X for a block of 64 of X's longer side, with each product rounded to a pair: what
+// was formed from it before is the same to the bit, whoever forms it again.
+constexpr int kMostQ = 3;
+struct Turns {
+  float unit[kMostQ];   // of each product; the first one's times X's own
+};
+constexpr int kHalfBlock = 64 * kRowBytes, kPairs = 2 * kHalfBlock;   // bytes of a block's half, and of it
+
+// 32 rows of Q, 16 columns each.
+struct Rows {
+  short8 h[4], l[4];
+  __device__ __forceinline__ void load(const Group& g, uint8_t* own, int number, int first) {
+    const int lane = threadIdx.x & 63;
+    const f16* q = reinterpret_cast<const f16*>(square_of(g, own, number)) + (first + (lane & 31)) * 128;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const f16* p = q + pair_at(u * 16 + (lane >> 5) * 8);
+      h[u] = *reinterpret_cast<const short8*>(p);
+      l[u] = *reinterpret_cast<const short8*>(p + kPairBlock);
+    }
+  }
+};
+// A quarter of Q times a block in LDS: a lane has a row of Q and, as element 4 g + e, column 8 g + 4
+// (lane / 32) + e of the block; ACROSS: a column of the block and these rows of Q.
+template <bool ACROSS, bool TURNED>
+__device__ __forceinline__ f32x16 quarter_of(const Rows& q, const Operand<64, kPair, TURNED, kWaves>& x,
+                                             const uint8_t* block, int quarter) {
+  f32x16 acc, low;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) acc[e] = low[e] = 0.f;
+  auto step = [&](auto number) {
+    constexpr int U = decltype(number)::value;
+    short8 h[1], l[1];
+    x.template read<U % 2>(block + U / 2 * kHalfBlock, quarter, 0, h, l);
+    low = ACROSS ? multiply<kPair>(q.l[U], h[0], low) : multiply<kPair>(h[0], q.l[U], low);
+    low = ACROSS ? multiply<kPair>(q.h[U], l[0], low) : multiply<kPair>(l[0], q.h[U], low);
+    acc = ACROSS ? multiply<kPair>(q.h[U], h[0], acc) : multiply<kPair>(h[0], q.h[U], acc);
+  };
+  step(std::integral_constant<int, 0>());
+  step(std::integral_constant<int, 1>());
+  step(std::integral_constant<int, 2>());
+  step(std::integral_constant<int, 3>());
+  return acc + low;
+}
+// Puts a quarter of Y into a block: its sum is to run down the rows (TURNED) or along them.
+template <bool TURNED>
+__device__ __forceinline__ void keep_quarter(uint8_t* block, const f32x16& acc, float f, int qa, int qb) {
+  const int lane = threadIdx.x & 63, i = qa * 32 + (lane & 31);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    f16x4 h, l;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      f16 hi, lo;
+      split(acc[4 * c + e] * f, hi, lo);
+      h[e] = hi;
+      l[e] = lo;
+    }
+    const int at = qb * 32 + c * 8;
+    *reinterpret_cast<f16x4*>(Sums<kPair, TURNED>::at(block, i, at, 0) + (lane >> 5) * 8) = h;
+    *reinterpret_cast<f16x4*>(Sums<kPair, TURNED>::at(block, i, at, 4) + (lane >> 5) * 8) = l;
+  }
+}
+// Copies block k of X, two stages of 32 of n.
+template <bool TALL>
+__device__ __forceinline__ void issue_block(Operand<64, kPair, !TALL, kWaves>& x, const uint8_t* from,
+                                            int64_t ld, int64_t k, uint8_t* to) {
+  x.p = from + k * 64 * (TALL ? ld : 4);
+  if (TALL) x.rs = rsrc(x.p, 64 * ld);
+  x.issue(to);
+  x.issue(to + kHalfBlock);
+}
+
+// S anew after QS segments: the sums of Y Y^T, in one pass over X; Y is not kept.
+template <int QS>
+__global__ __launch_bounds__(kThreads) void dora_orthogonal_fold(const Groups a, uint32_t total,
+                                                                 const Turns turns, uint8_t* ws) {
+  constexpr int kRing = 3;
+  __shared__ __attribute__((aligned(1024))) uint8_t sm[kRing][kPairs];
+  __shared__ __attribute__((aligned(1024))) uint8_t made[QS][kPairs];
+  const uint32_t id = by_xcd(blockIdx.x, total);
+  const Group& g = a.g[group_of(a, id)];
+  const int rest = (int)(id - g.from), part = rest % g.splits;
+  uint8_t* own = ws + g.base + (int64_t)(rest / g.splits) * g.stride;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), qa = wave & 1, qb = wave >> 1;
+  const int64_t ld = (int64_t)(g.tall ? g.nt : g.mt) * 4;
+  const int blocks = (g.m + 63) / 64;
+  const int k0 = (int)((int64_t)blocks * part / g.splits);
+  const int k1 = (int)((int64_t)blocks * (part + 1) / g.splits);
+  const float f = *reinterpret_cast<const float*>(own + g.scale) * turns.unit[0];
+  Rows q[QS];
+#pragma unroll
+  for (int i = 0; i < QS; ++i) q[i].load(g, own, i, qa * 32);
+  auto run = [&](auto tall) {
+    constexpr bool TALL = decltype(tall)::value;
+    Sums<kPair, false> sums;
+    Operand<64, kPair, !TALL, kWaves> x;
+    x.start(Side{own + g.x, ld, 2}, 0, qb);
+    Operand<64, kPair, true, kWaves> y;   // Y of all but the last segment
+    y.start(Side{nullptr, 0, 1}, 0, qb);
+    constexpr int kCopies = 2 * x.kCopies;
+    for (int k = k0; k < min(k0 + kRing, k1); ++k) issue_block<TALL>(x, own + g.x, ld, k, sm[(k - k0) % kRing]);
+    for (int k = k0; k < k1; ++k) {
+      const int later = min(kRing - 1, k1 - 1 - k);
+      if (later == 2) wait_vm<2 * kCopies>();
+      else if (later == 1) wait_vm<kCopies>();
+      else wait_vm<0>();
+      barrier_nofence();   // also: Y of the block before has been read
+      uint8_t* src = sm[(k - k0) % kRing];
+      keep_quarter<QS == 2>(made[0], quarter_of<false>(q[0], x, src, qb), f, qa, qb);
+      wait_lds();
+      barrier_nofence();   // Y is there, and the block of X has been read
+      if (k + kRing < k1) issue_block<TALL>(x, own + g.x, ld, k + kRing, src);
+      if (QS == 2) {
+        keep_quarter<false>(made[QS - 1], quarter_of<false>(q[QS - 1], y, made[0], qb), turns.unit[1], qa, qb);
+        wait_lds();
+        barrier_nofence();
+      }
+      sums.add(made[QS - 1]);
+      wait_lds();
+    }
+    sums.give(g, own, part);
+  };
+  if (g.tall) run(std::true_type());
+  else run(std::false_type());
+}
+
 // What turns X' X'^T into the first S: X' is X times a power of two, kWide's or the one that its
 // largest element asks for.
 struct Unit {
@@ -780,7 +1071,7 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_gather(const Groups 
     for (int q = 0; q < 4; ++q)
       if (j + q < i) v[q] = tile[j + q][i];
   }
-  f16* s = reinterpret_cast<f16*>(own + g.sq[0]);
+  f16* s = reinterpret_cast<f16*>(square_of(g, own, 0));
   const int64_t ld = 2 * (int64_t)g.nt;
   const int64_t row = (int64_t)ti * T + pi, col = (int64_t)tj * T + pj;
   store_pair<4>(s + (row + i) * ld, col + j, v);
@@ -820,13 +1111,13 @@ __global__ __launch_bounds__(WAVES * 64) void dora_orthogonal_square(const Squar
   uint8_t* own = ws + g.base + (int64_t)u * g.stride;
   const int64_t ld = (int64_t)g.nt * 4, le = ld / 2;
   const int stages = g.ne / kPairBlock;
-  const uint8_t* left = own + g.sq[q.left];
+  const uint8_t* left = square_of(g, own, q.left);
   const int64_t i0 = (int64_t)ti * T, j0 = (int64_t)tj * T;
   f32x16 acc[P::kB][P::kB];
-  P::run(sm, Side{left + i0 * ld, ld, stages}, Side{own + g.sq[q.right] + j0 * ld, ld, stages}, 0,
+  P::run(sm, Side{left + i0 * ld, ld, stages}, Side{square_of(g, own, q.right) + j0 * ld, ld, stages}, 0,
          stages, acc);
   float* tile = P::stage(sm, acc);
-  f16* out = reinterpret_cast<f16*>(own + g.sq[q.out]);
+  f16* out = reinterpret_cast<f16*>(square_of(g, own, q.out));
   // columns [j, j + 8) of row i
   auto put = [&](int64_t i, int64_t j, float* v) {
     if (j >= g.ne) return;   // padding that nothing reads (and where a flat row's lo lie)
@@ -871,6 +1162,8 @@ struct Chain {
   Unit unit;                           // as dora_orthogonal_gather's
   float to;
   int form;                            // X's, which says how Q is wanted
+  int q;                               // where it is put
+  bool scale;                          // X's factor is put down
   float poly[kMaxSteps][3];            // factors of S S, S and 1
   float ps[kMaxSteps], pq[kMaxSteps], next[kMaxSteps];   // of P S, P Q and P (P S)
 };
@@ -890,7 +1183,7 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_chain(const Chain a,
     block_sum<kThreads / 64, 1>(sum, lds);
     r = norm_factor(sum[0], a.unit, g, own, lds_most);
   }
-  if (threadIdx.x == 0) *reinterpret_cast<float*>(own + g.scale) = r;
+  if (threadIdx.x == 0 && a.scale) *reinterpret_cast<float*>(own + g.scale) = r;
   // chunk c (16 bytes) of row i; columns k .. of a pair row lie in chunks of 8
   auto chunk = [&](int m, int i, int c) { return sm[m] + i * kLd + ((c ^ (i & 15)) << 4); };
   auto put = [&](int m, int i, int k, const float* v) {   // four columns
@@ -1025,7 +1318,7 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_chain(const Chain a,
   }
   __syncthreads();
   if (a.form == kWide) {
-    __bf16* out = reinterpret_cast<__bf16*>(own + g.sq[0]);
+    __bf16* out = reinterpret_cast<__bf16*>(square_of(g, own, a.q));
 #pragma unroll
     for (int u = 0; u < kMine; ++u) {
       const int x = u * kThreads + threadIdx.x, i = x / 16, j = x % 16 * 4;
@@ -1035,7 +1328,7 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_chain(const Chain a,
     }
     return;
   }
-  f16* out = reinterpret_cast<f16*>(own + g.sq[0]);
+  f16* out = reinterpret_cast<f16*>(square_of(g, own, a.q));
 #pragma unroll
   for (int u = 0; u < kN * 16 / kThreads; ++u) {
     const int t = u * kThreads + threadIdx.x, i = t / 16, c = t % 16;
@@ -1051,14 +1344,13 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_chain(const Chain a,
 struct Sink {
   void* out;
   float* master;
-  float rate;          // lr times the matrix's own factor
 };
 struct Sinks {
-  Groups groups;       // `from`: unused
-  int count, first;
+  Groups groups;
+  int first;
   uint32_t total;
-  uint32_t from[kMaxMatrices];
   Sink s[kMaxMatrices];
+  float rate[kMaxMatrices];   // lr times the matrix's own factor
   int q;               // which of sq is Q
   float unit;          // 1 / Q's factor
   bool second;         // the X formed on the way
@@ -1078,7 +1370,7 @@ __device__ __forceinline__ void last_product(uint8_t* sm, const Group& g, uint8_
   const int64_t ld_q = (int64_t)g.nt * 4, ld_x = (int64_t)(g.tall ? g.nt : g.mt) * kSize;
   const int sq = g.ne / kPairBlock, sx = PAIR ? sq : sq / 2;
   const uint8_t* x = own + (second ? g.x2 : g.x);
-  const uint8_t* qp = own + g.sq[q];
+  const uint8_t* qp = square_of(g, own, q);
   if (g.tall)
     P::run(sm, Side{x + row0 * ld_x, ld_x, sx}, Side{qp + col0 * ld_q, ld_q, sq}, 0, sq, acc);
   else
@@ -1086,28 +1378,13 @@ __device__ __forceinline__ void last_product(uint8_t* sm, const Group& g, uint8_
                                  Side{x + col0 * kSize, ld_x, sx}, 0, sq, acc);
 }
 
-template <int T, int RING, Form F, bool BF, Result WHAT>
-__global__ __launch_bounds__(kThreads) void dora_orthogonal_apply(const Sinks a, uint8_t* ws) {
-  using P = Product<T, RING, F>;
-  __shared__ __attribute__((aligned(1024))) uint8_t sm[P::kLds];
+// A tile of the last product in LDS, from (row0, col0) of X on, to where it goes; f: its factor.
+template <typename P, bool BF, Result WHAT>
+__device__ __forceinline__ void put_out(float* tile, const Sinks& a, const Where& here, int64_t row0,
+                                        int64_t col0, int rows, int cols, float f) {
   using E = Elem<BF>;
-  const uint32_t id = by_xcd(blockIdx.x, a.total);
-  const int u = matrix_of(a.from, a.count, id);
-  const Group& g = a.groups.g[group_of_matrix(a.groups, a.first + u)];
-  uint8_t* own = ws + g.base + (int64_t)(a.first + u - g.first) * g.stride;
-  const bool tall = g.tall;
-  const int rows = tall ? g.m : g.n, cols = tall ? g.n : g.m;
-  const int down = (rows + T - 1) / T, across = (cols + T - 1) / T;
-  const int t = (int)(id - a.from[u]);
-  // tiles that share X's columns next to each other
-  const int64_t row0 = (int64_t)(tall ? t / across : t % down) * T;
-  const int64_t col0 = (int64_t)(tall ? t % across : t / down) * T;
-  f32x16 acc[P::kB][P::kB];
-  last_product<T, RING, F>(sm, g, own, a.q, a.second, row0, col0, acc);
-  float* tile = P::stage(sm, acc);
-  const Sink s = a.s[u];
-  const float f = *reinterpret_cast<const float*>(own + g.scale) * a.unit *
-                  (WHAT == kOut ? 1.f : -s.rate);
+  const Sink s = a.s[here.slot];
+  if (WHAT != kOut) f *= -a.rate[here.slot];
   typename E::T* out = reinterpret_cast<typename E::T*>(s.out);
   P::lines([&](int r, int c) {
     const int64_t i = row0 + r, j = col0 + c;
@@ -1131,6 +1408,77 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_apply(const Sinks a,
 #pragma unroll
     for (int e = 0; e < 8; e += E::kN) store_part<BF>(out, at + e, stop, v + e);
   });
+}
+
+template <int T, int RING, Form F, bool BF, Result WHAT>
+__global__ __launch_bounds__(kThreads) void dora_orthogonal_apply(const Sinks a, uint8_t* ws) {
+  using P = Product<T, RING, F>;
+  __shared__ __attribute__((aligned(1024))) uint8_t sm[P::kLds];
+  const uint32_t id = by_xcd(blockIdx.x, a.total);
+  const Where here = where(a.groups, a.first, id, ws);
+  const Group& g = here.g;
+  uint8_t* own = here.own;
+  const bool tall = g.tall;
+  const int rows = tall ? g.m : g.n, cols = tall ? g.n : g.m;
+  const int down = (rows + T - 1) / T, across = (cols + T - 1) / T;
+  const int t = here.piece;
+  // tiles that share X's columns next to each other
+  const int64_t row0 = (int64_t)(tall ? t / across : t % down) * T;
+  const int64_t col0 = (int64_t)(tall ? t % across : t / down) * T;
+  f32x16 acc[P::kB][P::kB];
+  last_product<T, RING, F>(sm, g, own, a.q, a.second, row0, col0, acc);
+  float* tile = P::stage(sm, acc);
+  const float f = *reinterpret_cast<const float*>(own + g.scale) * a.unit;
+  put_out<P, BF, WHAT>(tile, a, here, row0, col0, rows, cols, f);
+}
+
+// The last product after QS - 1 others that were not kept (n <= 64), a block of X a workgroup.
+template <int QS, bool BF, Result WHAT>
+__global__ __launch_bounds__(kThreads) void dora_orthogonal_last(const Sinks a, const Turns turns,
+                                                                 uint8_t* ws) {
+  using P = Product<64, 4, kPair>;
+  __shared__ __attribute__((aligned(1024))) uint8_t sm[kPairs], made[QS - 1][kPairs];
+  const uint32_t id = by_xcd(blockIdx.x, a.total);
+  const Where here = where(a.groups, a.first, id, ws);
+  const Group& g = here.g;
+  uint8_t* own = here.own;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), qa = wave & 1, qb = wave >> 1;
+  const int64_t ld = (int64_t)(g.tall ? g.nt : g.mt) * 4;
+  const float f = *reinterpret_cast<const float*>(own + g.scale) * turns.unit[0];
+  auto run = [&](auto tall) {
+    constexpr bool TALL = decltype(tall)::value;
+    Operand<64, kPair, !TALL, kWaves> x;
+    x.start(Side{own + g.x, ld, 2}, 0, qb);
+    Operand<64, kPair, true, kWaves> y;
+    y.start(Side{nullptr, 0, 1}, 0, qb);
+    issue_block<TALL>(x, own + g.x, ld, here.piece, sm);
+    Rows q[QS];
+#pragma unroll
+    for (int i = 0; i < QS; ++i) q[i].load(g, own, i, qa * 32);
+    wait_vm<0>();
+    barrier_nofence();
+    keep_quarter<true>(made[0], quarter_of<false>(q[0], x, sm, qb), f, qa, qb);
+    wait_lds();
+    barrier_nofence();
+    if (QS == 3) {
+      keep_quarter<true>(made[QS - 2], quarter_of<false>(q[1], y, made[0], qb), turns.unit[1], qa, qb);
+      wait_lds();
+      barrier_nofence();
+    }
+    const f32x16 acc = quarter_of<TALL>(q[QS - 1], y, made[QS - 2], qb);
+    const int lane = threadIdx.x & 63;
+    float* tile = reinterpret_cast<float*>(sm);   // (X has been read)
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      *reinterpret_cast<f32x4*>(P::at(tile, (TALL ? qb : qa) * 32 + (lane & 31),
+                                      (TALL ? qa : qb) * 32 + 8 * c + 4 * (lane >> 5))) =
+          f32x4{acc[4 * c], acc[4 * c + 1], acc[4 * c + 2], acc[4 * c + 3]};
+    __syncthreads();
+    const int64_t on = (int64_t)here.piece * 64;
+    put_out<P, BF, WHAT>(tile, a, here, TALL ? on : 0, TALL ? 0 : on, TALL ? g.m : g.n, TALL ? g.n : g.m, a.unit);
+  };
+  if (g.tall) run(std::true_type());
+  else run(std::false_type());
 }
 
 // Q X as pairs, in place of X from here on.
@@ -1250,10 +1598,13 @@ struct Item {
   int64_t rows, cols;
   Source from;
   Sink to;
+  float rate;
 };
 struct Kind {
   Form form;      // X's
   int times;      // how often Q X is formed on the way
+  // n <= 64: Q X is not kept, but formed again where it is wanted
+  bool folds() const { return form == kPair && times < kMostQ; }
 };
 struct Pass {
   bool small;               // n <= 64 throughout
@@ -1267,7 +1618,7 @@ struct Pass {
 int64_t padded(int64_t v, int to) { return (v + to - 1) / to * to; }
 int tiles(int v, int tile) { return (v + tile - 1) / tile; }
 
-void lay_out(Group& g, const Kind& k, int gram) {
+void lay_out(Group& g, const Kind& k, int gram, bool small) {
   g.ne = (int)padded(g.n, 64);
   g.nt = g.n <= 64 ? 64 : (int)padded(g.n, 128);
   g.mt = (int)padded(g.m, 128);
@@ -1278,8 +1629,8 @@ void lay_out(Group& g, const Kind& k, int gram) {
     return here;
   };
   g.x = take((int64_t)g.nt * g.mt * (k.form != kSingle || k.times > 1 ? 4 : 2));
-  g.x2 = k.times ? take((int64_t)g.nt * g.mt * 4) : 0;
-  for (int64_t& s : g.sq) s = take((int64_t)g.nt * g.nt * 4);
+  g.x2 = k.times && !(small && k.folds()) ? take((int64_t)g.nt * g.mt * 4) : 0;
+  g.sq = take((int64_t)g.nt * g.nt * 4 * 5);
   g.part = take((int64_t)tri(tiles(g.n, gram)) * g.splits * gram * gram * 4);
   g.trace = take((int64_t)tiles(g.n, gram) * g.splits * kWaves * 4);
   g.most = take((int64_t)g.blocks * 4);
@@ -1352,7 +1703,7 @@ std::vector<Pass> passes(const std::vector<Item>& items, const Kind& kind) {
           1, std::min({tiles(kWantSums, (int)std::min<int64_t>(sums, kWantSums)), (int)(stages / 4),
                        kMaxSplits}));
       g.blocks = (int)std::min<int64_t>(kMaxBlocks, ((int64_t)g.n * g.m + 8191) / 8192);
-      lay_out(g, kind, p.gram);
+      lay_out(g, kind, p.gram, p.small);
       g.base = base;
       base += g.stride * g.count;
     }
@@ -1404,16 +1755,18 @@ hipError_t by_matrix(const Pass& p, A& a, Size size, Fill fill, Go go) {
   const int all = (int)p.order.size();
   for (int first = 0; first < all;) {
     int64_t blocks = 0;
+    int slot = 0;
     a.first = first;
-    a.count = 0;
-    for (; first < all && a.count < kMaxMatrices; ++first) {
-      int g = 0;
-      while (g + 1 < p.groups.count && first >= p.groups.g[g + 1].first) ++g;
-      const int64_t n = size(p.groups.g[g]);
-      if (a.count && blocks + n > launch_blocks(kThreads)) break;
-      a.from[a.count] = (uint32_t)blocks;
-      fill(a.count++, p.order[first]);
-      blocks += n;
+    for (int i = 0; i < a.groups.count; ++i) {   // (groups of which it has none get no workgroups)
+      Group& g = a.groups.g[i];
+      g.from = (uint32_t)blocks;
+      g.each = (int)size(g);
+      g.begin = first;
+      for (; first >= g.first && first < g.first + g.count && slot < kMaxMatrices; ++first) {
+        if (slot && blocks + g.each > launch_blocks(kThreads)) break;
+        fill(slot++, p.order[first]);
+        blocks += g.each;
+      }
     }
     if (hipError_t e = go(blocks)) return e;
   }
@@ -1441,8 +1794,13 @@ struct Engine {
   const Call& c;
   Form form;     // of the current X, and which of the two it is
   bool second;
+  bool folds;    // Kind's
   uint8_t* ws;
   hipStream_t st;
+  // Where products are formed again (`folds`): how many there are, their factors, and the exponent
+  // of what they leave.
+  int seen = 0, at = 0;
+  Turns turns = {};
 
   template <bool BF, bool MOMENT, Form... FORMS>
   hipError_t halves() {
@@ -1458,6 +1816,13 @@ struct Engine {
                             return launch("orthogonal_most", dora_orthogonal_most<BF, MOMENT>, blocks,
                                           st, a, ws);
                           }));
+    if (p.small)
+      return by_form<FORMS...>([&](auto f) {
+        return by_matrix(p, a, [](const Group& g) { return (int64_t)g.splits; }, fill, [&](int64_t blocks) {
+          return launch("orthogonal_first", dora_orthogonal_first<BF, MOMENT, decltype(f)::value>, blocks,
+                        st, a, ws);
+        });
+      });
     return by_form<FORMS...>([&](auto f) {
       return by_matrix(p, a, [](const Group& g) { return ((int64_t)g.nt * g.mt + kPiece - 1) / kPiece; }, fill,
                        [&](int64_t blocks) {
@@ -1519,6 +1884,12 @@ struct Engine {
     if (p.square == 128) return squares_on<POLY, 128, 2, 8>(one, two);
     return p.few ? squares_on<POLY, 64, 3, 8>(one, two) : squares_on<POLY, 64, 2, 4>(one, two);
   }
+  hipError_t fold() {
+    Groups a = p.groups;
+    const int64_t blocks = spread(a, [](const Group& g) { return (int64_t)g.splits; });
+    return launch("orthogonal_fold", seen == 1 ? dora_orthogonal_fold<1> : dora_orthogonal_fold<2>, blocks, st, a,
+                  (uint32_t)blocks, turns, ws);
+  }
   hipError_t between(int q, int e) {
     ORTHO_TRY(by_tile(p.apply, [&](auto tile) {
       constexpr int T = decltype(tile)::value;
@@ -1538,11 +1909,22 @@ struct Engine {
   hipError_t apply(int q, int e) {
     Sinks a;
     a.q = q;
-    a.unit = two(-e);
+    a.unit = two(-e - at);
     a.second = second;
     a.decay = c.decay;
     a.rest = c.rest;
-    auto fill = [&](int slot, int item) { a.s[slot] = items[item].to; };
+    auto fill = [&](int slot, int item) {
+      a.s[slot] = items[item].to;
+      a.rate[slot] = items[item].rate;
+    };
+    if constexpr (BF == (WHAT == kMaster))
+      if (seen > 0)
+        return by_matrix(p, a, [](const Group& g) { return (int64_t)tiles(g.m, 64); }, fill, [&](int64_t blocks) {
+          a.total = (uint32_t)blocks;
+          return launch("orthogonal_apply",
+                        seen == 1 ? dora_orthogonal_last<2, BF, WHAT> : dora_orthogonal_last<3, BF, WHAT>,
+                        blocks, st, a, turns, ws);
+        });
     return by_tile(p.apply, [&](auto tile) {
       return by_form<FORMS...>([&](auto f) {
         constexpr int T = decltype(tile)::value;
@@ -1573,6 +1955,8 @@ struct Engine {
     a.unit = unit_of(unit);
     a.to = two(z.s[from]);
     a.form = form;
+    a.q = seen;
+    a.scale = seen == 0;
     e = z.p[from];
     for (int k = from; k < to; ++k) {
       const int i = k - from;
@@ -1623,11 +2007,18 @@ struct Engine {
       int to = from + 1;
       while (to < z.steps && !z.anew[to]) ++to;
       const float unit = from ? two(-z.x[from]) : 0.f;
-      ORTHO_TRY(gram(unit, z.s[from]));
+      // (for n <= 64 the pass that writes X, or takes it on, has formed S)
+      if (!p.small || (from && !folds)) ORTHO_TRY(gram(unit, z.s[from]));
       int q = 0, e = 0;
       ORTHO_TRY(p.small ? chain(from, to, unit, q, e) : products(from, to, q, e));
       if (to == z.steps) return finish(q, e);
-      ORTHO_TRY(between(q, z.x[to] - e));
+      if (folds) {
+        turns.unit[seen++] = two(z.x[to] - e - at);
+        at = z.x[to];
+        ORTHO_TRY(fold());
+      } else {
+        ORTHO_TRY(between(q, z.x[to] - e));
+      }
       from = to;
     }
     return hipSuccess;
@@ -1637,7 +2028,7 @@ struct Engine {
 hipError_t run_all(const std::vector<Item>& items, const Kind& kind, const Numbers& z, const Call& c,
                    void* ws, hipStream_t st) {
   for (const Pass& p : passes(items, kind)) {
-    Engine e{p, items, z, c, kind.form, false, reinterpret_cast<uint8_t*>(ws), st};
+    Engine e{p, items, z, c, kind.form, false, p.small && kind.folds(), reinterpret_cast<uint8_t*>(ws), st};
     ORTHO_TRY(e.run());
   }
   return hipSuccess;
@@ -1693,7 +2084,7 @@ int set_up(const dora_orthogonalize_options* o, const dora_matrix* a, int64_t co
   s.items.resize((size_t)count);
   for (int64_t i = 0; i < count; ++i) {
     if (!sides_ok(a[i].rows, a[i].cols)) return DORA_ERR_SHAPE;
-    s.items[i] = {a[i].rows, a[i].cols, {a[i].x, nullptr}, {a[i].out, nullptr, 0.f}};
+    s.items[i] = {a[i].rows, a[i].cols, {a[i].x, nullptr}, {a[i].out, nullptr}, 0.f};
   }
   return DORA_OK;
 }
@@ -1713,7 +2104,7 @@ int set_up(const dora_muon_options* o, const dora_muon_tensor* a, int64_t count,
     if (!sides_ok(a[i].rows, a[i].cols)) return DORA_ERR_SHAPE;
     if (!std::isfinite(a[i].scale)) return DORA_ERR_FLAGS;
     s.items[i] = {a[i].rows, a[i].cols, {a[i].grad, a[i].momentum},
-                  {a[i].param, a[i].master, (float)(o->lr * a[i].scale)}};
+                  {a[i].param, a[i].master}, (float)(o->lr * a[i].scale)};
     if (a[i].rows == 0 || a[i].cols == 0) continue;
     if (!any) master = a[i].master != nullptr;
     any = true;

@@ -115,6 +115,23 @@ def test_tiles_of_128_and_many_matrices(ops, dtype):
         assert float(d) <= 2 * tolerance(dt, want)
 
 
+def test_more_matrices_than_a_launch_takes(ops):
+    """Launches that begin and end inside runs of equal sizes, each matrix as it is alone."""
+    sizes = [(5, 70)] * 100 + [(70, 5)] * 90 + [(9, 20)] * 55 + [(70, 66)] * 130
+    xs = [matrix(*s, i, torch.bfloat16) for i, s in enumerate(sizes)]
+    got = ops.dora_orthogonalize(xs)
+    for i in (0, 99, 100, 119, 120, 121, 189, 190, 239, 240, 241, 244, 245, 364, 365, 374):
+        want = oracle.orthogonalize(host(xs[i]), STEPS, 1e-7)
+        assert off(got[i], want) <= tolerance(torch.bfloat16, want), i
+    ps, ms = [x.clone() for x in xs], [torch.zeros(x.shape, device="cuda") for x in xs]
+    ops.dora_muon(ops.MuonPlan(ps, ms), xs, lr=1.0, momentum=0.0, adjust=1.0)
+    # the parameter is x and the update x's: their difference is rounded to half a step of at most 1 + |x|
+    for p, x, y in zip(ps, xs, got):
+        want = host(x) - host(y)
+        room = (raised(STEPS, 65536.0) * 2.0 ** -22 + 2 * HALF[torch.bfloat16]) * (np.linalg.norm(host(y)) + np.linalg.norm(host(x)))
+        assert float(np.linalg.norm(host(p) - want)) <= room
+
+
 @pytest.mark.parametrize("dtype", list(DTYPES))
 def test_lists_of_every_size(ops, dtype):
     """More sizes than one pass takes, small and large tiles, empty matrices among them."""
