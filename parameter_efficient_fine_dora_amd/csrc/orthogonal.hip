@@ -444,14 +444,19 @@ struct Product {
 #pragma unroll
     for (int q = 0; q < 8; ++q) v[q] = *at(tile, r + q, c);
   }
-  // Calls fn(line, first of eight) for all of the tile's lines.
+  // Calls fn(line, first of eight) for all of the tile's lines; numbered: fn(which of this thread's, ..).
+  static constexpr int kLines = T * T / 8 / (WAVES * 64);
+  template <typename Fn>
+  __device__ static __forceinline__ void numbered(Fn fn) {
+#pragma unroll
+    for (int i = 0; i < kLines; ++i) {
+      const int x = i * WAVES * 64 + threadIdx.x;
+      fn(i, x / (T / 8), x % (T / 8) * 8);
+    }
+  }
   template <typename Fn>
   __device__ static __forceinline__ void lines(Fn fn) {
-#pragma unroll
-    for (int i = 0; i < T * T / 8 / (WAVES * 64); ++i) {
-      const int x = i * WAVES * 64 + threadIdx.x;
-      fn(x / (T / 8), x % (T / 8) * 8);
-    }
+    numbered([&](int, int r, int c) { fn(r, c); });
   }
   // Calls fn(row, column, values of four columns) for every group of four that this lane has.
   template <typename Fn>
@@ -594,9 +599,12 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_most(const Sources a
 // The power of two that takes a matrix's largest magnitude to [2^14, 2^15): half precision holds
 // 2^16 - 32 at most and whole steps of 2^-24.  0 for a matrix of zeros, infinities or NaN (whose
 // results are NaN throughout).
-__device__ __forceinline__ int exponent_of(const uint32_t* most, int blocks, uint32_t* lds) {
+__device__ __forceinline__ uint32_t most_of(const uint32_t* most, int blocks) {   // a thread's part
   uint32_t v = 0;
   for (int i = threadIdx.x; i < blocks; i += kThreads) v = max(v, most[i]);
+  return v;
+}
+__device__ __forceinline__ int exponent_of(uint32_t v, uint32_t* lds) {
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, off, 64));
   if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
@@ -627,7 +635,7 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_halves(const Sources
   const int pcols = g.tall ? g.nt : g.mt;
   const int64_t all = (int64_t)g.nt * g.mt;
   const int e = F == kWide ? a.fixed
-                           : exponent_of(reinterpret_cast<const uint32_t*>(own + g.most), g.blocks, lds);
+                           : exponent_of(most_of(reinterpret_cast<const uint32_t*>(own + g.most), g.blocks), lds);
   const Source s = a.s[here.slot];
   H* out = reinterpret_cast<H*>(own + g.x);
   const int64_t first = (int64_t)here.piece * kPiece, row0 = first / pcols;
@@ -788,7 +796,7 @@ struct Sums {
 // X as halves (see dora_orthogonal_halves) and the sums of S over it in one pass: X is written, but
 // not read again for S.  The numbers of the next block are under way while this one is multiplied.
 template <bool BF, bool MOMENT, Form F>
-__global__ __launch_bounds__(kThreads) void dora_orthogonal_first(const Sources a, uint8_t* ws) {
+__global__ __launch_bounds__(kThreads, 3) void dora_orthogonal_first(const Sources a, uint8_t* ws) {
   using H = typename Number<F>::T;
   constexpr bool PAIR = Number<F>::kTwo;
   typedef H H8 __attribute__((ext_vector_type(8)));
@@ -799,7 +807,7 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_first(const Sources 
   const Group& g = here.g;
   const Source s = a.s[here.slot];
   const int e = F == kWide ? a.fixed
-                           : exponent_of(reinterpret_cast<const uint32_t*>(here.own + g.most), g.blocks, lds);
+                           : exponent_of(most_of(reinterpret_cast<const uint32_t*>(here.own + g.most), g.blocks), lds);
   const int rows = g.tall ? g.m : g.n, cols = g.tall ? g.n : g.m, pcols = g.tall ? g.nt : g.mt;
   const int blocks = (g.m + 63) / 64;
   const int k0 = (int)((int64_t)blocks * here.piece / g.splits);
@@ -955,7 +963,7 @@ __device__ __forceinline__ void issue_block(Operand<64, kPair, !TALL, kWaves>& x
 template <int QS>
 __global__ __launch_bounds__(kThreads) void dora_orthogonal_fold(const Groups a, uint32_t total,
                                                                  const Turns turns, uint8_t* ws) {
-  constexpr int kRing = 3;
+  constexpr int kRing = 2;   // (48 KB with `made`: three workgroups to a CU)
   __shared__ __attribute__((aligned(1024))) uint8_t sm[kRing][kPairs];
   __shared__ __attribute__((aligned(1024))) uint8_t made[QS][kPairs];
   const uint32_t id = by_xcd(blockIdx.x, total);
@@ -979,14 +987,12 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_fold(const Groups a,
     Operand<64, kPair, true, kWaves> y;   // Y of all but the last segment
     y.start(Side{nullptr, 0, 1}, 0, qb);
     constexpr int kCopies = 2 * x.kCopies;
-    for (int k = k0; k < min(k0 + kRing, k1); ++k) issue_block<TALL>(x, own + g.x, ld, k, sm[(k - k0) % kRing]);
+    for (int k = k0; k < min(k0 + kRing, k1); ++k) issue_block<TALL>(x, own + g.x, ld, k, sm[(k - k0) & 1]);
     for (int k = k0; k < k1; ++k) {
-      const int later = min(kRing - 1, k1 - 1 - k);
-      if (later == 2) wait_vm<2 * kCopies>();
-      else if (later == 1) wait_vm<kCopies>();
+      if (k + 1 < k1) wait_vm<kCopies>();
       else wait_vm<0>();
       barrier_nofence();   // also: Y of the block before has been read
-      uint8_t* src = sm[(k - k0) % kRing];
+      uint8_t* src = sm[(k - k0) & 1];
       keep_quarter<QS == 2>(made[0], quarter_of<false>(q[0], x, src, qb), f, qa, qb);
       wait_lds();
       barrier_nofence();   // Y is there, and the block of X has been read
@@ -1012,10 +1018,8 @@ struct Unit {
   float eps;
   int wide, fixed;
 };
-__device__ __forceinline__ float norm_factor(float trace, const Unit& u, const Group& g, uint8_t* own,
-                                             uint32_t* lds) {
-  const int e = u.wide ? u.fixed
-                       : exponent_of(reinterpret_cast<const uint32_t*>(own + g.most), g.blocks, lds);
+__device__ __forceinline__ float norm_factor(float trace, const Unit& u, uint32_t most, uint32_t* lds) {
+  const int e = u.wide ? u.fixed : exponent_of(most, lds);
   return 1.f / (sqrtf(trace) + ldexpf(u.eps, e));
 }
 
@@ -1046,7 +1050,7 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_gather(const Groups 
     const float* d = reinterpret_cast<const float*>(own + g.trace);
     for (int i = threadIdx.x; i < nt * g.splits * kWaves; i += kThreads) sum[0] += d[i];
     block_sum<kThreads / 64, 1>(sum, lds);
-    r = norm_factor(sum[0], unit, g, own, lds_most);
+    r = norm_factor(sum[0], unit, most_of(reinterpret_cast<const uint32_t*>(own + g.most), g.blocks), lds_most);
   }
   if (piece == 0 && t == 0 && threadIdx.x == 0) *reinterpret_cast<float*>(own + g.scale) = r;
   const int pi = piece / kSide * kE, pj = piece % kSide * kE;
@@ -1164,26 +1168,26 @@ struct Chain {
   int form;                            // X's, which says how Q is wanted
   int q;                               // where it is put
   bool scale;                          // X's factor is put down
-  float poly[kMaxSteps][3];            // factors of S S, S and 1
-  float ps[kMaxSteps], pq[kMaxSteps], next[kMaxSteps];   // of P S, P Q and P (P S)
+  float step[kMaxSteps][6];            // factors of S S, S and 1; of P S, P Q and P (P S)
 };
 __global__ __launch_bounds__(kThreads) void dora_orthogonal_chain(const Chain a, uint8_t* ws) {
   constexpr int kN = 64, kLd = kN * 4;   // bytes of a pair row: 16 chunks, swizzled by the row
-  __shared__ __attribute__((aligned(1024))) uint8_t sm[4][kN * kLd];
+  __shared__ __attribute__((aligned(1024))) uint8_t sm[5][kN * kLd];
   __shared__ float lds[kThreads / 64];
   __shared__ uint32_t lds_most[kThreads / 64];
+  __shared__ float steps[kMaxSteps * 6];
   const Group& g = a.groups.g[group_of(a.groups, blockIdx.x)];
   uint8_t* own = ws + g.base + (int64_t)(blockIdx.x - g.from) * g.stride;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  float r = a.unit.unit;
-  if (r == 0.f) {
-    float sum[1] = {0.f};
-    const float* d = reinterpret_cast<const float*>(own + g.trace);
-    for (int i = threadIdx.x; i < g.splits * kWaves; i += kThreads) sum[0] += d[i];
-    block_sum<kThreads / 64, 1>(sum, lds);
-    r = norm_factor(sum[0], a.unit, g, own, lds_most);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = g.n;
+  // all at once: a step that asks the kernel's arguments for its own waits 3000 cycles for them
+  if ((int)threadIdx.x < a.steps * 6) steps[threadIdx.x] = (&a.step[0][0])[threadIdx.x];
+  float r = a.unit.unit, trace = 0.f;
+  uint32_t most = 0;
+  if (r == 0.f) {   // under way beside the sums
+    static_assert(kMaxSplits * kWaves <= kThreads, "a number of the trace for each thread");
+    if ((int)threadIdx.x < g.splits * kWaves) trace = reinterpret_cast<const float*>(own + g.trace)[threadIdx.x];
+    if (!a.unit.wide) most = most_of(reinterpret_cast<const uint32_t*>(own + g.most), g.blocks);
   }
-  if (threadIdx.x == 0 && a.scale) *reinterpret_cast<float*>(own + g.scale) = r;
   // chunk c (16 bytes) of row i; columns k .. of a pair row lie in chunks of 8
   auto chunk = [&](int m, int i, int c) { return sm[m] + i * kLd + ((c ^ (i & 15)) << 4); };
   auto put = [&](int m, int i, int k, const float* v) {   // four columns
@@ -1206,7 +1210,8 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_chain(const Chain a,
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = (float)h[e] + (float)l[e];
   };
-  constexpr int S = 0, P = 1, R = 2, Q = 3;
+  constexpr int S = 0, P = 1, R = 2;
+  int Q = 3, other = 4;   // where Q is, and where it goes next
   const float* part = reinterpret_cast<const float*>(own + g.part);
   constexpr int kMine = kN * kN / 4 / kThreads;
   double sums[kMine][4] = {};
@@ -1226,6 +1231,12 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_chain(const Chain a,
 #pragma unroll
           for (int e = 0; e < 4; ++e) sums[u][e] += (double)w[u][q][e];
   }
+  if (r == 0.f) {
+    float sum[1] = {trace};
+    block_sum<kThreads / 64, 1>(sum, lds);
+    r = norm_factor(sum[0], a.unit, most, lds_most);
+  }
+  if (threadIdx.x == 0 && a.scale) *reinterpret_cast<float*>(own + g.scale) = r;
 #pragma unroll
   for (int u = 0; u < kMine; ++u) {
     const int x = u * kThreads + threadIdx.x;
@@ -1235,84 +1246,111 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_chain(const Chain a,
     put(S, x / 16, x % 16 * 4, v);
   }
   __syncthreads();
+  // The upper triangle's values on both sides: S is symmetric.  (Every read of LDS before the first
+  // write, here and below: the compiler cannot tell them apart, and would wait for each in turn.)
+  f16 high[kMine][4], deep[kMine][4];
 #pragma unroll
-  for (int u = 0; u < kMine; ++u) {   // the upper triangle's values on both sides: S is symmetric
+  for (int u = 0; u < kMine; ++u) {
     const int x = u * kThreads + threadIdx.x, i = x / 16, j = x % 16 * 4;
-    if (j >= i) continue;
-    float v[4], o[4];
-    get(S, i, j, v);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      get(S, min(j + e, i), i & ~3, o);
-      if (j + e < i) v[e] = (i & 3) == 0 ? o[0] : (i & 3) == 1 ? o[1] : (i & 3) == 2 ? o[2] : o[3];
+      const int row = min(j + e, i), col = max(j + e, i), c = (col >> 5) * 8 + ((col & 31) >> 3);
+      high[u][e] = *reinterpret_cast<const f16*>(chunk(S, row, c) + (col & 7) * 2);
+      deep[u][e] = *reinterpret_cast<const f16*>(chunk(S, row, c + 4) + (col & 7) * 2);
     }
-    put(S, i, j, v);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < kMine; ++u) {
+    const int x = u * kThreads + threadIdx.x, i = x / 16, j = x % 16 * 4, c = (j >> 5) * 8 + ((j & 31) >> 3);
+    *reinterpret_cast<f16x4*>(chunk(S, i, c) + (j & 4) * 2) = f16x4{high[u][0], high[u][1], high[u][2], high[u][3]};
+    *reinterpret_cast<f16x4*>(chunk(S, i, c + 4) + (j & 4) * 2) = f16x4{deep[u][0], deep[u][1], deep[u][2], deep[u][3]};
   }
   const int rowa = (wave & 1) * 32 + (lane & 31), rowb = (wave >> 1) * 32 + (lane & 31);
-  auto product = [&](int x, int y, f32x16& acc) {
-#pragma unroll
-    for (int e = 0; e < 16; ++e) acc[e] = 0.f;
-    f32x16 low = acc;
+  struct Fragments {
+    f16x8 h[4], l[4];
+  };
+  auto fetch = [&](int m, int row, Fragments& f) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int c = (u >> 1) * 8 + (u & 1) * 2 + (lane >> 5);
-      const f16x8 fa = *reinterpret_cast<const f16x8*>(chunk(x, rowa, c));
-      const f16x8 la = *reinterpret_cast<const f16x8*>(chunk(x, rowa, c + 4));
-      const f16x8 fb = *reinterpret_cast<const f16x8*>(chunk(y, rowb, c));
-      const f16x8 lb = *reinterpret_cast<const f16x8*>(chunk(y, rowb, c + 4));
-      low = __builtin_amdgcn_mfma_f32_32x32x16_f16(fb, la, low, 0, 0, 0);
-      low = __builtin_amdgcn_mfma_f32_32x32x16_f16(lb, fa, low, 0, 0, 0);
-      acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(fb, fa, acc, 0, 0, 0);
+      f.h[u] = *reinterpret_cast<const f16x8*>(chunk(m, row, c));
+      f.l[u] = *reinterpret_cast<const f16x8*>(chunk(m, row, c + 4));
     }
-    acc += low;
   };
-  // fn(row, first of four columns, values)
-  auto each = [&](const f32x16& acc, auto fn) {
+  auto product = [&](const Fragments& x, const Fragments& y, f32x16& acc) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      float v[4] = {acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]};
-      fn((wave & 1) * 32 + (lane & 31), (wave >> 1) * 32 + 8 * q + 4 * (lane >> 5), v);
+    for (int e = 0; e < 16; ++e) acc[e] = 0.f;
+    f32x16 low = acc, also = acc;   // three sums that do not wait for each other
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      low = __builtin_amdgcn_mfma_f32_32x32x16_f16(y.h[u], x.l[u], low, 0, 0, 0);
+      also = __builtin_amdgcn_mfma_f32_32x32x16_f16(y.l[u], x.h[u], also, 0, 0, 0);
+      acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(y.h[u], x.h[u], acc, 0, 0, 0);
     }
+    acc += low + also;
+  };
+  // fn(which, row, first of four columns), and also their values
+  auto at_each = [&](auto fn) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) fn(q, (wave & 1) * 32 + (lane & 31), (wave >> 1) * 32 + 8 * q + 4 * (lane >> 5));
+  };
+  auto each = [&](const f32x16& acc, auto fn) {
+    at_each([&](int q, int i, int j) {
+      float v[4] = {acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]};
+      fn(q, i, j, v);
+    });
   };
   f32x16 x, y;
+  Fragments fp, fs, f;   // P's rows, S's other rows, and what else is met
   for (int k = 0; k < a.steps; ++k) {
     const bool last = k + 1 == a.steps;
     __syncthreads();
-    product(S, S, x);
+    float of[6], s[4][4];
+#pragma unroll
+    for (int i = 0; i < 6; ++i) of[i] = steps[k * 6 + i];
+    fetch(S, rowa, f);
+    fetch(S, rowb, fs);
+    at_each([&](int q, int i, int j) { get(S, i, j, s[q]); });
+    product(f, fs, x);
     const int p = k == 0 ? Q : P;   // the first P is Q
-    each(x, [&](int i, int j, float* v) {
-      float s[4];
-      get(S, i, j, s);
+    each(x, [&](int q, int i, int j, float* v) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        v[e] = fmaf(a.poly[k][1], s[e], v[e] * a.poly[k][0]);
-        if (i == j + e && i < g.n) v[e] += a.poly[k][2];
+        v[e] = fmaf(of[1], s[q][e], v[e] * of[0]);
+        if (i == j + e && i < n) v[e] += of[2];
       }
       put(p, i, j, v);
     });
     __syncthreads();
-    if (!last) product(p, S, x);
+    fetch(p, rowa, fp);
     if (k > 0) {
-      product(P, Q, y);
-      __syncthreads();   // Q has been read
-      each(y, [&](int i, int j, float* v) {
+      fetch(Q, rowb, f);
+      product(fp, f, y);
+    }
+    if (!last) product(fp, fs, x);
+    if (k > 0) {
+      each(y, [&](int, int i, int j, float* v) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] *= a.pq[k];
-        put(Q, i, j, v);
+        for (int e = 0; e < 4; ++e) v[e] *= of[4];
+        put(other, i, j, v);
       });
+      const int was = Q;
+      Q = other;
+      other = was;
     }
     if (last) break;
-    each(x, [&](int i, int j, float* v) {
+    each(x, [&](int, int i, int j, float* v) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] *= a.ps[k];
+      for (int e = 0; e < 4; ++e) v[e] *= of[3];
       put(R, i, j, v);
     });
     __syncthreads();
-    // (k = 0: P is Q, which the products after the next barrier replace)
-    product(p, R, x);
-    each(x, [&](int i, int j, float* v) {
+    fetch(R, rowb, f);
+    product(fp, f, x);
+    each(x, [&](int, int i, int j, float* v) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] *= a.next[k];
+      for (int e = 0; e < 4; ++e) v[e] *= of[5];
       put(S, i, j, v);
     });
   }
@@ -1378,15 +1416,23 @@ __device__ __forceinline__ void last_product(uint8_t* sm, const Group& g, uint8_
                                  Side{x + col0 * kSize, ld_x, sx}, 0, sq, acc);
 }
 
+// What eight numbers of a parameter were.
+template <bool BF, Result WHAT>
+__device__ __forceinline__ void was(const Sink& s, int64_t at, int64_t stop, float* p) {
+  if (WHAT == kMaster) load8<false>(s.master, at, stop, p);
+  else load8<BF>(s.out, at, stop, p);
+}
 // A tile of the last product in LDS, from (row0, col0) of X on, to where it goes; f: its factor.
-template <typename P, bool BF, Result WHAT>
+// EARLY: what the parameter was is in `before`.
+template <typename P, bool BF, Result WHAT, bool EARLY>
 __device__ __forceinline__ void put_out(float* tile, const Sinks& a, const Where& here, int64_t row0,
-                                        int64_t col0, int rows, int cols, float f) {
+                                        int64_t col0, int rows, int cols, float f,
+                                        const float (*before)[8]) {
   using E = Elem<BF>;
   const Sink s = a.s[here.slot];
   if (WHAT != kOut) f *= -a.rate[here.slot];
   typename E::T* out = reinterpret_cast<typename E::T*>(s.out);
-  P::lines([&](int r, int c) {
+  P::numbered([&](int n, int r, int c) {
     const int64_t i = row0 + r, j = col0 + c;
     if (i >= rows || j >= cols) return;
     float v[8];
@@ -1396,10 +1442,12 @@ __device__ __forceinline__ void put_out(float* tile, const Sinks& a, const Where
     for (int e = 0; e < 8; ++e) v[e] *= f;
     if (WHAT != kOut) {
       float p[8];
-      if (WHAT == kMaster) load8<false>(s.master, at, stop, p);
-      else load8<BF>(out, at, stop, p);
+      if (!EARLY) was<BF, WHAT>(s, at, stop, p);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = fmaf(p[e], a.decay, fmaf(p[e], a.rest, v[e]));
+      for (int e = 0; e < 8; ++e) {
+        const float x = EARLY ? before[n][e] : p[e];
+        v[e] = fmaf(x, a.decay, fmaf(x, a.rest, v[e]));
+      }
       if (WHAT == kMaster) {
         store_part<false>(s.master, at, stop, v);
         store_part<false>(s.master, at + 4, stop, v + 4);
@@ -1429,7 +1477,7 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_apply(const Sinks a,
   last_product<T, RING, F>(sm, g, own, a.q, a.second, row0, col0, acc);
   float* tile = P::stage(sm, acc);
   const float f = *reinterpret_cast<const float*>(own + g.scale) * a.unit;
-  put_out<P, BF, WHAT>(tile, a, here, row0, col0, rows, cols, f);
+  put_out<P, BF, WHAT, false>(tile, a, here, row0, col0, rows, cols, f, nullptr);
 }
 
 // The last product after QS - 1 others that were not kept (n <= 64), a block of X a workgroup.
@@ -1452,6 +1500,14 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_last(const Sinks a, 
     Operand<64, kPair, true, kWaves> y;
     y.start(Side{nullptr, 0, 1}, 0, qb);
     issue_block<TALL>(x, own + g.x, ld, here.piece, sm);
+    const int64_t on = (int64_t)here.piece * 64, row0 = TALL ? on : 0, col0 = TALL ? 0 : on;
+    const int rows = TALL ? g.m : g.n, cols = TALL ? g.n : g.m;
+    float before[P::kLines][8];
+    if (WHAT != kOut)
+      P::numbered([&](int n, int r, int c) {
+        const int64_t i = row0 + r, j = col0 + c;
+        if (i < rows && j < cols) was<BF, WHAT>(a.s[here.slot], i * cols + j, (i + 1) * cols, before[n]);
+      });
     Rows q[QS];
 #pragma unroll
     for (int i = 0; i < QS; ++i) q[i].load(g, own, i, qa * 32);
@@ -1474,8 +1530,7 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_last(const Sinks a, 
                                       (TALL ? qa : qb) * 32 + 8 * c + 4 * (lane >> 5))) =
           f32x4{acc[4 * c], acc[4 * c + 1], acc[4 * c + 2], acc[4 * c + 3]};
     __syncthreads();
-    const int64_t on = (int64_t)here.piece * 64;
-    put_out<P, BF, WHAT>(tile, a, here, TALL ? on : 0, TALL ? 0 : on, TALL ? g.m : g.n, TALL ? g.n : g.m, a.unit);
+    put_out<P, BF, WHAT, true>(tile, a, here, row0, col0, rows, cols, a.unit, before);
   };
   if (g.tall) run(std::true_type());
   else run(std::false_type());
@@ -1641,7 +1696,8 @@ void lay_out(Group& g, const Kind& k, int gram, bool small) {
 // Tiles of 128 read half of what tiles of 64 read for the same products, and are taken where they
 // fill the chip (these numbers: of workgroups).
 constexpr int64_t kEnough = 256;
-constexpr int64_t kWantSums = 768;   // workgroups of the sums over m
+constexpr int64_t kLeastPart = 4;    // stages of 64 of a part of such a sum
+constexpr int64_t kWantSums = 1024, kWantSmall = 768;   // workgroups of the sums over m
 
 std::vector<Pass> passes(const std::vector<Item>& items, const Kind& kind) {
   auto small = [](const Item& i) { return std::min(i.rows, i.cols); };
@@ -1692,16 +1748,17 @@ std::vector<Pass> passes(const std::vector<Item>& items, const Kind& kind) {
     p.square = squares >= 2 * kEnough ? 128 : 64;
     p.few = small_squares < 2 * kEnough;
     p.apply = !p.small && across >= kEnough ? 128 : 64;
-    int64_t sums = 0;
-    for (int i = 0; i < p.groups.count; ++i)
-      sums += (int64_t)p.groups.g[i].count * tri(tiles(p.groups.g[i].n, p.gram));
+    int64_t stages = 0;   // of 64 of the longer side, for all tiles of S
+    for (int i = 0; i < p.groups.count; ++i) {
+      const Group& g = p.groups.g[i];
+      stages += (int64_t)g.count * tri(tiles(g.n, p.gram)) * tiles(g.m, 64);
+    }
+    const int64_t want = p.small ? kWantSmall : kWantSums;
+    const int64_t part = std::max<int64_t>(kLeastPart, (stages + want - 1) / want);
     int64_t base = 0;
     for (int i = 0; i < p.groups.count; ++i) {
       Group& g = p.groups.g[i];
-      const int64_t stages = tiles(g.m, 64);   // at least four to a part
-      g.splits = (int)std::max<int64_t>(
-          1, std::min({tiles(kWantSums, (int)std::min<int64_t>(sums, kWantSums)), (int)(stages / 4),
-                       kMaxSplits}));
+      g.splits = (int)std::min<int64_t>(std::max<int64_t>(1, tiles(g.m, 64) / part), kMaxSplits);
       g.blocks = (int)std::min<int64_t>(kMaxBlocks, ((int64_t)g.n * g.m + 8191) / 8192);
       lay_out(g, kind, p.gram, p.small);
       g.base = base;
@@ -1960,12 +2017,13 @@ struct Engine {
     e = z.p[from];
     for (int k = from; k < to; ++k) {
       const int i = k - from;
-      a.poly[i][0] = (float)std::ldexp(z.abc[k][2], z.p[k] - 2 * z.s[k]);
-      a.poly[i][1] = (float)std::ldexp(z.abc[k][1], z.p[k] - z.s[k]);
-      a.poly[i][2] = (float)std::ldexp(z.abc[k][0], z.p[k]);
-      a.ps[i] = two(z.r[k] - z.p[k] - z.s[k]);
-      a.next[i] = two(z.s[k + 1] - z.p[k] - z.r[k]);
-      a.pq[i] = two(z.q[k] - z.p[k] - e);
+      float* of = a.step[i];
+      of[0] = (float)std::ldexp(z.abc[k][2], z.p[k] - 2 * z.s[k]);
+      of[1] = (float)std::ldexp(z.abc[k][1], z.p[k] - z.s[k]);
+      of[2] = (float)std::ldexp(z.abc[k][0], z.p[k]);
+      of[3] = two(z.r[k] - z.p[k] - z.s[k]);
+      of[5] = two(z.s[k + 1] - z.p[k] - z.r[k]);
+      of[4] = two(z.q[k] - z.p[k] - e);
       if (i > 0) e = z.q[k];
     }
     q = 0;
