@@ -163,6 +163,16 @@ template <int N>
 __device__ __forceinline__ void wait_vm() {
   __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
 }
+// Waits until at most `later` stages of N copies each are under way; MOST: as many as there can be.
+template <int N, int MOST>
+__device__ __forceinline__ void wait_stages(int later) {
+  if constexpr (MOST == 0) {
+    wait_vm<0>();
+  } else {
+    if (later >= MOST) wait_vm<MOST * N>();
+    else wait_stages<N, MOST - 1>(later);
+  }
+}
 // LDS reads that are under way have arrived (lgkmcnt 0).
 __device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 __device__ __forceinline__ void barrier_nofence() { asm volatile("s_barrier" ::: "memory"); }
@@ -317,7 +327,7 @@ struct Operand {
 //
 // PAIR: three products of every hi + lo pair of fragments, 12 matrix instructions to 8 fragments
 // read from LDS at T = 128 (single: 4 to 4).  RING stages are in flight.
-template <int T, int RING, Form F, int WAVES = 4>
+template <int T, int RING, Form F, int WAVES = 4, int DEEP = 1>
 struct Product {
   static constexpr bool PAIR = F != kSingle;
   // The cross products are summed apart: a third of the additions to the large sum, whose roundings
@@ -364,44 +374,47 @@ struct Product {
     constexpr int kSub = (PAIR ? 2 : 4) / kHalves;
     const int first = (wave >> 2) * kSub;   // the 16-deep steps of a stage that this wave takes
     int slot = 0;
-    for (int s = 0; s < steps; ++s) {
-      // the stage has landed once only the copies of the stages behind it are in flight
-      const int later = min(RING - 1, steps - 1 - s);
-      if (RING > 3 && later >= 3) wait_vm<3 * kCopies>();
-      else if (RING > 2 && later == 2) wait_vm<2 * kCopies>();
-      else if (later >= 1) wait_vm<kCopies>();
-      else wait_vm<0>();
+    for (int s = 0; s < steps; s += DEEP) {
+      // the stages have landed once only the copies of those behind them are in flight
+      wait_stages<kCopies, RING - DEEP>(steps - DEEP - s);
       barrier_nofence();
-      const uint8_t* src = sm + slot * kStage;
-      auto step = [&](auto number) {
-        constexpr int U = decltype(number)::value;
-        short8 fa[kB], la[kB], fb[kB], lb[kB];
-        a.template read<U>(src, quarter_a, first, fa, la);
-        b.template read<U>(src + a.kBytes, quarter_b, first, fb, lb);
 #pragma unroll
-        for (int i = 0; i < kB; ++i)
+      for (int d = 0; d < DEEP; ++d) {
+        if (d > 0 && s + d >= steps) break;
+        const uint8_t* src = sm + (slot + d) * kStage;
+        auto step = [&](auto number) {
+          constexpr int U = decltype(number)::value;
+          short8 fa[kB], la[kB], fb[kB], lb[kB];
+          a.template read<U>(src, quarter_a, first, fa, la);
+          b.template read<U>(src + a.kBytes, quarter_b, first, fb, lb);
 #pragma unroll
-          for (int j = 0; j < kB; ++j) {
-            auto& c = acc[i][j];
-            if constexpr (PAIR) {
-              auto& l = kApart ? low[kApart ? i : 0][kApart ? j : 0] : c;
-              l = multiply<F>(fb[j], la[i], l);
-              l = multiply<F>(lb[j], fa[i], l);
+          for (int i = 0; i < kB; ++i)
+#pragma unroll
+            for (int j = 0; j < kB; ++j) {
+              auto& c = acc[i][j];
+              if constexpr (PAIR) {
+                auto& l = kApart ? low[kApart ? i : 0][kApart ? j : 0] : c;
+                l = multiply<F>(fb[j], la[i], l);
+                l = multiply<F>(lb[j], fa[i], l);
+              }
+              c = multiply<F>(fb[j], fa[i], c);
             }
-            c = multiply<F>(fb[j], fa[i], c);
-          }
-      };
-      step(std::integral_constant<int, 0>());
-      if constexpr (kSub > 1) step(std::integral_constant<int, 1>());
-      if constexpr (kSub > 2) {
-        step(std::integral_constant<int, 2>());
-        step(std::integral_constant<int, 3>());
+        };
+        step(std::integral_constant<int, 0>());
+        if constexpr (kSub > 1) step(std::integral_constant<int, 1>());
+        if constexpr (kSub > 2) {
+          step(std::integral_constant<int, 2>());
+          step(std::integral_constant<int, 3>());
+        }
       }
-      // every wave has read the slot, and not only asked for it, before it is filled again
+      // every wave has read the slots, and not only asked for them, before they are filled again
       wait_lds();
       barrier_nofence();
-      if (s + RING < steps) issue(slot);
-      if (++slot == RING) slot = 0;
+#pragma unroll
+      for (int d = 0; d < DEEP; ++d)
+        if (s + d + RING < steps) issue(slot + d);
+      slot += DEEP;
+      if (slot == RING) slot = 0;
     }
     if (kApart) {
 #pragma unroll
@@ -682,7 +695,7 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_halves(const Sources
 template <int T, int RING, Form F>
 __global__ __launch_bounds__(kThreads) void dora_orthogonal_gram(const Groups a, uint32_t total,
                                                                  bool second, uint8_t* ws) {
-  using P = Product<T, RING, F>;
+  using P = Product<T, RING, F, 4, T == 64 ? 2 : 1>;
   constexpr bool PAIR = P::PAIR;
   __shared__ __attribute__((aligned(1024))) uint8_t sm[P::kLds];
   const uint32_t id = by_xcd(blockIdx.x, total);
@@ -1099,9 +1112,9 @@ struct Squares {
   uint32_t total, half;      // workgroups; where the second product starts (total: there is none)
   Square q[2];
 };
-template <int T, int RING, int WAVES, bool POLY>
+template <int T, int RING, int WAVES, int DEEP, bool POLY>
 __global__ __launch_bounds__(WAVES * 64) void dora_orthogonal_square(const Squares a, uint8_t* ws) {
-  using P = Product<T, RING, kPair, WAVES>;
+  using P = Product<T, RING, kPair, WAVES, DEEP>;
   __shared__ __attribute__((aligned(1024))) uint8_t sm[P::kLds];
   uint32_t id = by_xcd(blockIdx.x, a.total);
   const Square& q = a.q[id >= a.half ? 1 : 0];
@@ -1404,7 +1417,7 @@ __device__ __forceinline__ void last_product(uint8_t* sm, const Group& g, uint8_
   // Q's rows are pairs where X's are; else all hi and then all lo against X twice
   constexpr bool PAIR = Number<F>::kTwo;
   constexpr int kSize = PAIR ? 4 : 2;
-  using P = Product<T, RING, F>;
+  using P = Product<T, RING, F, 4, T == 64 ? 2 : 1>;
   const int64_t ld_q = (int64_t)g.nt * 4, ld_x = (int64_t)(g.tall ? g.nt : g.mt) * kSize;
   const int sq = g.ne / kPairBlock, sx = PAIR ? sq : sq / 2;
   const uint8_t* x = own + (second ? g.x2 : g.x);
@@ -1460,7 +1473,7 @@ __device__ __forceinline__ void put_out(float* tile, const Sinks& a, const Where
 
 template <int T, int RING, Form F, bool BF, Result WHAT>
 __global__ __launch_bounds__(kThreads) void dora_orthogonal_apply(const Sinks a, uint8_t* ws) {
-  using P = Product<T, RING, F>;
+  using P = Product<T, RING, F, 4, T == 64 ? 2 : 1>;
   __shared__ __attribute__((aligned(1024))) uint8_t sm[P::kLds];
   const uint32_t id = by_xcd(blockIdx.x, a.total);
   const Where here = where(a.groups, a.first, id, ws);
@@ -1541,7 +1554,7 @@ template <int T, int RING, Form F>
 __global__ __launch_bounds__(kThreads) void dora_orthogonal_between(const Groups a, uint32_t total,
                                                                     int q, float unit, bool second,
                                                                     uint8_t* ws) {
-  using P = Product<T, RING, F>;
+  using P = Product<T, RING, F, 4, T == 64 ? 2 : 1>;
   __shared__ __attribute__((aligned(1024))) uint8_t sm[P::kLds];
   const uint32_t id = by_xcd(blockIdx.x, total);
   const Group& g = a.g[group_of(a, id)];
@@ -1664,7 +1677,7 @@ struct Kind {
 struct Pass {
   bool small;               // n <= 64 throughout
   int gram, square, apply;  // tiles
-  bool few;                 // fewer tiles of the n x n products than two for each CU
+  int64_t tiles;            // of 64, of an n x n product
   std::vector<int> order;   // items, group by group
   Groups groups;
   size_t bytes;
@@ -1696,6 +1709,7 @@ void lay_out(Group& g, const Kind& k, int gram, bool small) {
 // Tiles of 128 read half of what tiles of 64 read for the same products, and are taken where they
 // fill the chip (these numbers: of workgroups).
 constexpr int64_t kEnough = 256;
+constexpr int64_t kFewTiles = 384;   // of a launch of n x n products
 constexpr int64_t kLeastPart = 4;    // stages of 64 of a part of such a sum
 constexpr int64_t kWantSums = 1024, kWantSmall = 768;   // workgroups of the sums over m
 
@@ -1746,7 +1760,7 @@ std::vector<Pass> passes(const std::vector<Item>& items, const Kind& kind) {
     }
     p.gram = !p.small && parts >= kEnough ? 128 : 64;
     p.square = squares >= 2 * kEnough ? 128 : 64;
-    p.few = small_squares < 2 * kEnough;
+    p.tiles = small_squares;
     p.apply = !p.small && across >= kEnough ? 128 : 64;
     int64_t stages = 0;   // of 64 of the longer side, for all tiles of S
     for (int i = 0; i < p.groups.count; ++i) {
@@ -1920,7 +1934,7 @@ struct Engine {
                     unit_of(unit), two(to), ws);
     });
   }
-  template <bool POLY, int T, int RING, int WAVES>
+  template <bool POLY, int T, int RING, int WAVES, int DEEP>
   hipError_t squares_on(const Square& one, const Square* two) {
     Squares a;
     a.groups = p.groups;
@@ -1930,16 +1944,20 @@ struct Engine {
     a.q[0] = one;
     a.q[1] = two ? *two : one;
     return launch<WAVES * 64>(POLY ? "orthogonal_poly" : "orthogonal_square",
-                              dora_orthogonal_square<T, RING, WAVES, POLY>, a.total, st, a, ws);
+                              dora_orthogonal_square<T, RING, WAVES, DEEP, POLY>, a.total, st, a, ws);
   }
   // Tiles of 64 in two stages (32 KB) lie five to a CU: 48 matrices of 384 take 24 us a product, with
   // tiles of 128 30; a matrix of 2048 takes 48 and 58.  From two of the large tiles for each CU on
   // their half traffic counts (4096: 4.4 ms in all against 6.2).  Few tiles have the CU's SIMDs to
-  // themselves: eight waves (517 columns: 179 us in all, with four 192).
+  // themselves: eight waves, and two stages at a time, since a stage is 750 cycles of waiting for LDS
+  // and for each other (517 columns: 175 us in all, one stage at a time 184, four waves 192; 1536
+  // columns, whose double launches have 600 tiles: 467 us either way; 24 matrices of 384, 504 tiles:
+  // 335 us as here, 355 with eight waves).
   template <bool POLY>
   hipError_t squares(const Square& one, const Square* two = nullptr) {
-    if (p.square == 128) return squares_on<POLY, 128, 2, 8>(one, two);
-    return p.few ? squares_on<POLY, 64, 3, 8>(one, two) : squares_on<POLY, 64, 2, 4>(one, two);
+    if (p.square == 128) return squares_on<POLY, 128, 2, 8, 1>(one, two);
+    return p.tiles * (two ? 2 : 1) <= kFewTiles ? squares_on<POLY, 64, 4, 8, 2>(one, two)
+                                                : squares_on<POLY, 64, 2, 4, 1>(one, two);
   }
   hipError_t fold() {
     Groups a = p.groups;
