@@ -167,9 +167,10 @@ typedef struct {
 /*
  * out = the iteration's last X for each of `count` matrices (`matrices` and the
  * coefficients are host arrays, read during the call only).  Matrices of any sizes
- * share launches; the workspace holds 2 bytes (bf16) or 8 (float32) an element, 20 n^2
- * for a shorter side of n, and partial sums; sides are padded to 128.  Sums are float32, and float32
- * results have float32's precision.  A matrix of zeros stays zero; one with a NaN
+ * share launches; the workspace holds 2 bytes (bf16) or 8 (float32; 4 for a shorter side
+ * n <= 64) an element, 20 n^2, and partial sums; sides are padded to 128 (n <= 64: to
+ * 64).  Sums are float32, and float32 results have float32's precision.  A matrix of
+ * zeros stays zero; one with a NaN
  * or an infinity becomes NaN throughout, the others of the call do not.
  */
 DORA_API size_t dora_orthogonalize_workspace_bytes(const dora_matrix* matrices, int64_t count,
@@ -207,8 +208,8 @@ typedef struct {
  * m and the update are float32; p is rounded once.  u is taken to 22 bits, to 16 for bf16
  * parameters without masters, and from |u| = 2^104 eps on the latter become NaN.  A NaN or an
  * infinity in a gradient makes its own element of m, and its own matrix, NaN.  The workspace holds 4
- * (bf16 parameters without masters) or 8 bytes an element beside what dora_orthogonalize's holds
- * for n.
+ * (bf16 parameters without masters, or n <= 64) or 8 bytes an element beside what
+ * dora_orthogonalize's holds for n.
  */
 DORA_API size_t dora_muon_workspace_bytes(const dora_muon_tensor* tensors, int64_t count,
                                           const dora_muon_options* options);

@@ -13,8 +13,8 @@
 // the directions below 2^-9 of the norm.  All n x n matrices are therefore held as two half
 // precision numbers, hi + lo (22 bits or more: the hi product and both cross products go through
 // the matrix cores, the lo lo product is below 2^-22), scaled by powers of two into half's range;
-// sums are float32.  For bf16 results that is enough.  For float32 results the product Q X is
-// formed before the factor passes 1024 (after three of five usual steps), and S anew from it.
+// sums are float32.  For bf16 results that is enough.  Others form the product Q X on the way, before
+// the factor passes what they allow (kMostExact, kMostUpdate), and S anew from it.
 // A bf16 X is one half precision number exactly (its bits below 2^-38 of its largest element are
 // left out), a float32 X is hi + lo.  The update of a bf16 parameter is held as two bf16 numbers
 // instead, 16 bits: what is lost is 2^-18 of X, raised 485 times in the worst case, and half a step
@@ -26,8 +26,12 @@
 // X stays in its own order: where the sum runs down its rows (S of a tall matrix, Q X of a wide
 // one) its numbers are turned as they are read from LDS.
 //
-// Many matrices share a launch: a step on the adapters of a model is 20 launches whatever their
-// number, and small matrices fill the chip together.
+// Many matrices share a launch: a step on the adapters of a model is 18 launches whatever their
+// number (bf16 parameters, five steps), and small matrices fill the chip together.
+//
+// n <= 64 (most adapters) takes another way: the n x n products of one matrix are one workgroup's, in
+// LDS, S is summed by the pass that writes X, and Q X is not kept on the way but formed again where it
+// is wanted.  Then a step is three launches (six with float32 masters), and memory bounds it.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -55,7 +59,9 @@ constexpr int kMaxGroups = 12;
 constexpr int kMaxMatrices = 120;    // of one launch that needs their addresses
 constexpr int kMaxSteps = 16;
 constexpr int kMaxBlocks = 1024;     // workgroups that look for one matrix's largest element
-constexpr int kMaxSplits = 32;
+// Parts of a sum over m: for n <= 64 one workgroup adds them, which costs 6 us for 64, and few
+// workgroups cost more (16 x 200000: 337 us, with 32 parts 503).
+constexpr int kMaxSplits = 64, kMaxParts = 32;
 
 // ---- matrices of one size ---------------------------------------------------------------
 // Offsets are bytes from a matrix's own part of the workspace.
@@ -326,7 +332,8 @@ struct Operand {
 // 4 g + e, column 8 g + 4 (lane / 32) + e of B's.
 //
 // PAIR: three products of every hi + lo pair of fragments, 12 matrix instructions to 8 fragments
-// read from LDS at T = 128 (single: 4 to 4).  RING stages are in flight.
+// read from LDS at T = 128 (single: 4 to 4).  RING stages are in flight, DEEP of them are taken between
+// two barriers (two of four where T is 64: 300 x 4096 158 us in all, one at a time 165).
 template <int T, int RING, Form F, int WAVES = 4, int DEEP = 1>
 struct Product {
   static constexpr bool PAIR = F != kSingle;
@@ -808,6 +815,9 @@ struct Sums {
 
 // X as halves (see dora_orthogonal_halves) and the sums of S over it in one pass: X is written, but
 // not read again for S.  The numbers of the next block are under way while this one is multiplied.
+// Memory bounds it: 56 layers' 29M elements, 10 bytes each, take 68 us (4.3 TB/s), where the two
+// kernels that n > 64 has took 67 and 42.  Three workgroups to a CU, for which one variant spills two
+// registers (two to a CU: 72 us).
 template <bool BF, bool MOMENT, Form F>
 __global__ __launch_bounds__(kThreads, 3) void dora_orthogonal_first(const Sources a, uint8_t* ws) {
   using H = typename Number<F>::T;
@@ -900,7 +910,9 @@ __global__ __launch_bounds__(kThreads, 3) void dora_orthogonal_first(const Sourc
 }
 
 // Y = Q_k .. Q_1 X for a block of 64 of X's longer side, with each product rounded to a pair: what
-// was formed from it before is the same to the bit, whoever forms it again.
+// was formed from it before is the same to the bit, whoever forms it again.  (One product with the Q
+// of all steps in its place would not be what S was summed from: a matrix of rank 2 came out 2e-4 off
+// instead of 2e-5.)
 constexpr int kMostQ = 3;
 struct Turns {
   float unit[kMostQ];   // of each product; the first one's times X's own
@@ -972,7 +984,10 @@ __device__ __forceinline__ void issue_block(Operand<64, kPair, !TALL, kWaves>& x
   x.issue(to + kHalfBlock);
 }
 
-// S anew after QS segments: the sums of Y Y^T, in one pass over X; Y is not kept.
+// S anew after QS segments: the sums of Y Y^T, in one pass over X; Y is not kept.  56 layers' 29M
+// elements take 39 us, of which reading X alone is 27; a product that is kept and sums of it (as n > 64
+// has) took 56 and 42.  48 KB of LDS put three workgroups on a CU (a ring of three blocks, two
+// workgroups: 61 us).
 template <int QS>
 __global__ __launch_bounds__(kThreads) void dora_orthogonal_fold(const Groups a, uint32_t total,
                                                                  const Turns turns, uint8_t* ws) {
@@ -1171,8 +1186,10 @@ __global__ __launch_bounds__(WAVES * 64) void dora_orthogonal_square(const Squar
 }
 
 // All of a segment's n x n products for n <= 64: one workgroup a matrix, with S, P, P S and Q in
-// LDS.  A product is 12 matrix instructions of each of four waves, and the 14 products of five
-// steps take 11 us where as many launches take 70.
+// LDS.  A product is 12 matrix instructions of each of four waves; waiting for LDS and for each other
+// bounds it (a step of three or four products 2.3 us, the sums' gathering 6), so that all reads of a
+// phase stand before its writes, and P's rows and S's stay in registers for the products that share
+// them.  Five steps take 19 us where as many launches take 75.
 struct Chain {
   Groups groups;
   int steps;
@@ -1493,7 +1510,9 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_apply(const Sinks a,
   put_out<P, BF, WHAT, false>(tile, a, here, row0, col0, rows, cols, f, nullptr);
 }
 
-// The last product after QS - 1 others that were not kept (n <= 64), a block of X a workgroup.
+// The last product after QS - 1 others that were not kept (n <= 64), a block of X a workgroup.  What
+// the parameter was is read before the products: 56 layers' masters take 113 us (14 bytes an element:
+// 3.6 TB/s), 119 when it is read behind them.
 template <int QS, bool BF, Result WHAT>
 __global__ __launch_bounds__(kThreads) void dora_orthogonal_last(const Sinks a, const Turns turns,
                                                                  uint8_t* ws) {
@@ -1707,11 +1726,16 @@ void lay_out(Group& g, const Kind& k, int gram, bool small) {
 }
 
 // Tiles of 128 read half of what tiles of 64 read for the same products, and are taken where they
-// fill the chip (these numbers: of workgroups).
+// fill the chip: this many workgroups (2048 x 6144: 877 us in all, with tiles of 64 for S and Q X 999,
+// 24 matrices of 384 x 8192 503 and 581; with tiles of 128 throughout 1031 x 517 213 instead of 174).
 constexpr int64_t kEnough = 256;
 constexpr int64_t kFewTiles = 384;   // of a launch of n x n products
-constexpr int64_t kLeastPart = 4;    // stages of 64 of a part of such a sum
-constexpr int64_t kWantSums = 1024, kWantSmall = 768;   // workgroups of the sums over m
+// Workgroups of the sums over m, and the least stages of 64 of one's part.  Parts cost their partial
+// sums, few of them leave CUs empty or the last ones waiting: 24 layers' step 1.43 ms, with 768
+// wanted 1.45; four matrices of 384 x 8192 190 us, with parts of four stages 201; with tiles of 64
+// 1031 x 517 172 us, with parts of eight 177.  For n <= 64 three lie on a CU (dora_orthogonal_fold).
+constexpr int64_t kWantSums = 1024, kWantSmall = 768;
+constexpr int64_t kLeastPart = 8, kLeastSmall = 4;
 
 std::vector<Pass> passes(const std::vector<Item>& items, const Kind& kind) {
   auto small = [](const Item& i) { return std::min(i.rows, i.cols); };
@@ -1755,7 +1779,7 @@ std::vector<Pass> passes(const std::vector<Item>& items, const Kind& kind) {
       const int64_t t = (int64_t)g.count * tri(tiles(g.n, 128));
       squares += t;
       small_squares += (int64_t)g.count * tri(tiles(g.n, 64));
-      parts += t * std::min<int64_t>(tiles(g.m, 256), kMaxSplits);
+      parts += t * std::min<int64_t>(tiles(g.m, 256), kMaxParts);
       across += (int64_t)g.count * tiles(g.n, 128) * tiles(g.m, 128);
     }
     p.gram = !p.small && parts >= kEnough ? 128 : 64;
@@ -1768,11 +1792,12 @@ std::vector<Pass> passes(const std::vector<Item>& items, const Kind& kind) {
       stages += (int64_t)g.count * tri(tiles(g.n, p.gram)) * tiles(g.m, 64);
     }
     const int64_t want = p.small ? kWantSmall : kWantSums;
-    const int64_t part = std::max<int64_t>(kLeastPart, (stages + want - 1) / want);
+    const int64_t part = std::max<int64_t>(p.gram == 128 ? kLeastPart : kLeastSmall, (stages + want - 1) / want);
     int64_t base = 0;
     for (int i = 0; i < p.groups.count; ++i) {
       Group& g = p.groups.g[i];
-      g.splits = (int)std::min<int64_t>(std::max<int64_t>(1, tiles(g.m, 64) / part), kMaxSplits);
+      g.splits = (int)std::min<int64_t>(std::max<int64_t>(1, tiles(g.m, 64) / part),
+                                        p.small ? kMaxSplits : kMaxParts);
       g.blocks = (int)std::min<int64_t>(kMaxBlocks, ((int64_t)g.n * g.m + 8191) / 8192);
       lay_out(g, kind, p.gram, p.small);
       g.base = base;

@@ -7,7 +7,9 @@
 // writes four.  Memory bounds large batches, launches small ones.  The terms are
 // float64: whether a bound holds a ratio must not depend on a float32 rounding beside
 // the bound (the slope jumps there), the loss is a small difference of large sums, and
-// exp(d) - 1 - d cancels.
+// exp(d) - 1 - d cancels.  4.2M tokens' gradient takes 17 us (5.2 TB/s, what streams reach here);
+// 1M packed tokens' loss is 12 us of sums, which the exponentials share with memory, and 8 of joining
+// and finishing.
 #include <algorithm>
 #include <cmath>
 
@@ -34,7 +36,7 @@ struct Term {
 // exp(x) = 2^n (1 + q) with x = n log 2 + r, |r| <= 0.35, and q the Taylor sum to r^10 / 10!: what is
 // left out is under 0.35^11 / 11! = 2.4e-13 of the result, a thousandth of a float32 rounding and
 // less.  (Memory should bound these kernels: the library's exponentials, exact to the last bit of
-// float64, took 14 us of 1M tokens' sums where these take 9.)
+// float64, took 5 us more of 1M tokens' sums, 17 against 12.)
 struct Exponential {
   double q, two;   // two: 2^n
   __device__ __forceinline__ explicit Exponential(double x) {
@@ -65,7 +67,7 @@ __device__ __forceinline__ Term term(const Tokens& k, float logp, float old, flo
   const bool under = a < 0.0 && x.ratio < k.low;
   const double bounded = over ? (a > 0.0 ? k.high : k.dual) : under ? k.low : x.ratio;
   x.held = over || under ? 1.0 : 0.0;
-  // an advantage of 0 gives 0 whatever the ratio (an infinite one too)
+  // an advantage of 0 gives 0 whatever the ratio (an infinite one too, where it has an upper bound)
   x.loss = a == 0.0 && x.ratio > k.high ? 0.0 : -a * bounded;
   x.slope = over || under || (a == 0.0 && x.ratio > k.high) ? 0.0 : -a * x.ratio;
   x.kl = 0.0;

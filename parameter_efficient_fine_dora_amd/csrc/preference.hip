@@ -300,7 +300,7 @@ DORA_API int dora_preference_backward(const dora_token_batch* batch,
   hipStream_t st = reinterpret_cast<hipStream_t>(hip_stream);
   const Pairs p = {numbers(*options), no_seq ? 0 : pairs, grad_loss, logit, count, chosen, rejected};
   // Up to 256 pairs are looked through by every wave, four loads one after the other, which is less
-  // than another launch (127 pairs of 2 x 1031 tokens: 4.9 us against 3.4 and 4.4).
+  // than another launch (127 pairs of 2 x 1031 tokens: loss and gradient 19.5 us in all against 22.8).
   const bool known = p.count > 256;
   if (known) {
     LaunchTimer timer("preference_coef", st);

@@ -84,7 +84,7 @@ def matrix(rows, cols, seed, dtype, kind="gradient"):
 
 
 SIZES = [(1, 1), (1, 7), (7, 1), (3, 5), (2, 300), (17, 2057), (16, 4096), (64, 64), (64, 2048), (65, 64),
-         (65, 130), (128, 128), (129, 300), (200, 100), (1031, 517), (300, 4097), (384, 1111)]
+         (65, 130), (128, 128), (129, 300), (200, 100), (1031, 517), (300, 4097), (384, 1111), (9, 140001)]
 
 
 @pytest.mark.parametrize("size", SIZES, ids=lambda s: f"{s[0]}x{s[1]}")
