@@ -1446,18 +1446,26 @@ __device__ __forceinline__ void last_product(uint8_t* sm, const Group& g, uint8_
                                  Side{x + col0 * kSize, ld_x, sx}, 0, sq, acc);
 }
 
-// What eight numbers of a parameter were.
-template <bool BF, Result WHAT>
-__device__ __forceinline__ void was(const Sink& s, int64_t at, int64_t stop, float* p) {
-  if (WHAT == kMaster) load8<false>(s.master, at, stop, p);
-  else load8<BF>(s.out, at, stop, p);
+// What the parameter was where a tile from (row0, col0) of X on will go: read before the products.
+// Behind them each line would wait for its own, since the stores between cannot be told apart from the
+// loads (24 high-rank layers' QX: 457 us, so 472).
+template <typename P, bool BF, Result WHAT>
+__device__ __forceinline__ void read_before(const Sinks& a, const Where& here, int64_t row0, int64_t col0,
+                                            int rows, int cols, float (&before)[P::kLines][8]) {
+  if (WHAT == kOut) return;
+  const Sink s = a.s[here.slot];
+  P::numbered([&](int n, int r, int c) {
+    const int64_t i = row0 + r, j = col0 + c, at = i * cols + j, stop = (i + 1) * cols;
+    if (i >= rows || j >= cols) return;
+    if (WHAT == kMaster) load8<false>(s.master, at, stop, before[n]);
+    else load8<BF>(s.out, at, stop, before[n]);
+  });
 }
-// A tile of the last product in LDS, from (row0, col0) of X on, to where it goes; f: its factor.
-// EARLY: what the parameter was is in `before`.
-template <typename P, bool BF, Result WHAT, bool EARLY>
+// A tile of the last product in LDS to where it goes; f: its factor.
+template <typename P, bool BF, Result WHAT>
 __device__ __forceinline__ void put_out(float* tile, const Sinks& a, const Where& here, int64_t row0,
                                         int64_t col0, int rows, int cols, float f,
-                                        const float (*before)[8]) {
+                                        const float (&before)[P::kLines][8]) {
   using E = Elem<BF>;
   const Sink s = a.s[here.slot];
   if (WHAT != kOut) f *= -a.rate[here.slot];
@@ -1471,13 +1479,8 @@ __device__ __forceinline__ void put_out(float* tile, const Sinks& a, const Where
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] *= f;
     if (WHAT != kOut) {
-      float p[8];
-      if (!EARLY) was<BF, WHAT>(s, at, stop, p);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float x = EARLY ? before[n][e] : p[e];
-        v[e] = fmaf(x, a.decay, fmaf(x, a.rest, v[e]));
-      }
+      for (int e = 0; e < 8; ++e) v[e] = fmaf(before[n][e], a.decay, fmaf(before[n][e], a.rest, v[e]));
       if (WHAT == kMaster) {
         store_part<false>(s.master, at, stop, v);
         store_part<false>(s.master, at + 4, stop, v + 4);
@@ -1503,11 +1506,13 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_apply(const Sinks a,
   // tiles that share X's columns next to each other
   const int64_t row0 = (int64_t)(tall ? t / across : t % down) * T;
   const int64_t col0 = (int64_t)(tall ? t % across : t / down) * T;
+  float before[P::kLines][8];
+  read_before<P, BF, WHAT>(a, here, row0, col0, rows, cols, before);
+  const float f = *reinterpret_cast<const float*>(own + g.scale) * a.unit;
   f32x16 acc[P::kB][P::kB];
   last_product<T, RING, F>(sm, g, own, a.q, a.second, row0, col0, acc);
   float* tile = P::stage(sm, acc);
-  const float f = *reinterpret_cast<const float*>(own + g.scale) * a.unit;
-  put_out<P, BF, WHAT, false>(tile, a, here, row0, col0, rows, cols, f, nullptr);
+  put_out<P, BF, WHAT>(tile, a, here, row0, col0, rows, cols, f, before);
 }
 
 // The last product after QS - 1 others that were not kept (n <= 64), a block of X a workgroup.  What
@@ -1535,11 +1540,7 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_last(const Sinks a, 
     const int64_t on = (int64_t)here.piece * 64, row0 = TALL ? on : 0, col0 = TALL ? 0 : on;
     const int rows = TALL ? g.m : g.n, cols = TALL ? g.n : g.m;
     float before[P::kLines][8];
-    if (WHAT != kOut)
-      P::numbered([&](int n, int r, int c) {
-        const int64_t i = row0 + r, j = col0 + c;
-        if (i < rows && j < cols) was<BF, WHAT>(a.s[here.slot], i * cols + j, (i + 1) * cols, before[n]);
-      });
+    read_before<P, BF, WHAT>(a, here, row0, col0, rows, cols, before);
     Rows q[QS];
 #pragma unroll
     for (int i = 0; i < QS; ++i) q[i].load(g, own, i, qa * 32);
@@ -1562,7 +1563,7 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_last(const Sinks a, 
                                       (TALL ? qa : qb) * 32 + 8 * c + 4 * (lane >> 5))) =
           f32x4{acc[4 * c], acc[4 * c + 1], acc[4 * c + 2], acc[4 * c + 3]};
     __syncthreads();
-    put_out<P, BF, WHAT, true>(tile, a, here, row0, col0, rows, cols, a.unit, before);
+    put_out<P, BF, WHAT>(tile, a, here, row0, col0, rows, cols, a.unit, before);
   };
   if (g.tall) run(std::true_type());
   else run(std::false_type());

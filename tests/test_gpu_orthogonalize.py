@@ -84,7 +84,8 @@ def matrix(rows, cols, seed, dtype, kind="gradient"):
 
 
 SIZES = [(1, 1), (1, 7), (7, 1), (3, 5), (2, 300), (17, 2057), (16, 4096), (64, 64), (64, 2048), (65, 64),
-         (65, 130), (128, 128), (129, 300), (200, 100), (1031, 517), (300, 4097), (384, 1111), (9, 140001)]
+         (65, 130), (128, 128), (129, 300), (200, 100), (1031, 517), (300, 4097), (384, 1111), (9, 140001),
+         (2057, 17), (1000, 64), (300, 2)]
 
 
 @pytest.mark.parametrize("size", SIZES, ids=lambda s: f"{s[0]}x{s[1]}")
@@ -128,7 +129,8 @@ def test_more_matrices_than_a_launch_takes(ops):
     # the parameter is x and the update x's: their difference is rounded to half a step of at most 1 + |x|
     for p, x, y in zip(ps, xs, got):
         want = host(x) - host(y)
-        room = (raised(STEPS, 65536.0) * 2.0 ** -22 + 2 * HALF[torch.bfloat16]) * (np.linalg.norm(host(y)) + np.linalg.norm(host(x)))
+        room = raised(STEPS, 65536.0) * 2.0 ** -22 + 2 * HALF[torch.bfloat16]
+        room *= float(np.linalg.norm(host(y)) + np.linalg.norm(host(x)))
         assert float(np.linalg.norm(host(p) - want)) <= room
 
 
@@ -261,6 +263,32 @@ def test_step(ops, param, grad, nesterov):
             if masters:
                 assert torch.equal(ps[i], masters[i].to(dt))
             rp[i], rm[i] = host(got), host(ms[i])
+
+
+@pytest.mark.parametrize("param", ["bf16", "f32", "master"])
+@pytest.mark.parametrize("steps", [2, 10, 16])
+def test_step_of_few_and_many_products(ops, param, steps):
+    """(2, -3/2, 1/2) raises S's rounding by 3/4 sum 4^i: two steps form S once, ten of them twice, and
+    sixteen three times for float32 parameters."""
+    coefficients = ((2.0, -1.5, 0.5),) * steps
+    dt = torch.float32 if param == "f32" else torch.bfloat16
+    sizes = [(40, 90), (90, 40), (64, 300), (1, 9), (130, 140), (140, 66)]
+    ps = [(0.3 * matrix(*s, i, torch.float32)).to(dt) for i, s in enumerate(sizes)]
+    ms = [torch.zeros(*s, device="cuda") for s in sizes]
+    masters = [p.float() + 1e-4 for p in ps] if param == "master" else None
+    gs = [matrix(*s, 40 + i, torch.float32) for i, s in enumerate(sizes)]
+    was = [host(p) for p in (masters or ps)]
+    ops.dora_muon(ops.MuonPlan(ps, ms, masters=masters), gs, lr=0.03, adjust=1.0, coefficients=coefficients)
+    for i, s in enumerate(sizes):
+        want, _ = oracle.muon_step(was[i], host(gs[i]), np.zeros(s), 0.03, 0.95, True, 0.0, coefficients, 1e-7, 1.0)
+        got = masters[i] if masters else ps[i]
+        moved = float(np.linalg.norm(want - was[i]))
+        exact = param != "bf16"
+        # as in test_step; u is held to 22 bits, to 16 for bf16 parameters: half a step is 2^-18 of it
+        room = moved * raised(coefficients, 1024.0 if exact else 65536.0) * 2.0 ** -22
+        room += 0.03 * 2.0 ** steps * (2.0 ** -22 if exact else 2.0 ** -18)
+        room += HALF[got.dtype] * 1.01 * float(np.linalg.norm(want))
+        assert float(np.linalg.norm(host(got) - want)) <= room, s
 
 
 def test_step_from_zero_parameters(ops):
