@@ -23,6 +23,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kFinish = 1024;
+constexpr int64_t kSmallTokens = 4096, kSmallSequences = 32;   // what one workgroup does alone
 
 struct Tokens {
   const float *logp, *old, *ref, *adv;
@@ -102,14 +103,12 @@ struct Four {
 
 constexpr int kTotals = 5;   // loss, counted, kl, held, ratio
 
-// Sums over chunks, a wave each, and their totals by workgroup; SEQ: also the loss and count of each
+// Sums over chunk w, by a wave: its totals in `totals` (LDS); SEQ: also the loss and count of each
 // sequence.
 template <bool SEQ, bool PER>
-__global__ __launch_bounds__(kThreads) void dora_policy_sums(const Batch b, const Parts parts,
-                                                             int64_t chunk, const Tokens k,
-                                                             double* totals) {
-  __shared__ double lds[kWaves][kTotals];
-  const int64_t w = wave_id(), c0 = min(w * chunk, b.tokens);
+__device__ __forceinline__ void chunk_sums(const Batch& b, const Parts& parts, int64_t chunk, int64_t w,
+                                           const Tokens& k, double* totals) {
+  const int64_t c0 = min(w * chunk, b.tokens);
   const int64_t c1 = min(c0 + chunk, b.tokens);
   const int lane = threadIdx.x & 63;
   Four x;   // loads are under way while the sequence is looked for, and a round ahead
@@ -176,8 +175,16 @@ __global__ __launch_bounds__(kThreads) void dora_policy_sums(const Batch b, cons
 #pragma unroll
   for (int i = 0; i < kTotals; ++i) {
     const double v = wave_sum64(all[i]);
-    if (lane == 0) lds[threadIdx.x >> 6][i] = v;
+    if (lane == 0) totals[i] = v;
   }
+}
+
+template <bool SEQ, bool PER>
+__global__ __launch_bounds__(kThreads) void dora_policy_sums(const Batch b, const Parts parts,
+                                                             int64_t chunk, const Tokens k,
+                                                             double* totals) {
+  __shared__ double lds[kWaves][kTotals];
+  chunk_sums<SEQ, PER>(b, parts, chunk, wave_id(), k, lds[threadIdx.x >> 6]);
   __syncthreads();
   if (threadIdx.x < kTotals) {
     const int i = threadIdx.x;
@@ -187,13 +194,17 @@ __global__ __launch_bounds__(kThreads) void dora_policy_sums(const Batch b, cons
 static_assert(kWaves == 4, "four waves' totals are added");
 
 // Each sequence's mean and count, in place of its sums, a wave per sequence.
-__global__ __launch_bounds__(kThreads) void dora_policy_join(const Batch b, const Parts parts,
-                                                             int64_t chunk) {
-  const int64_t waves = (int64_t)gridDim.x * kWaves;
-  for (int64_t s = wave_id(); s < b.sequences; s += waves) {
+__device__ __forceinline__ void join_means(const Batch& b, const Parts& parts, int64_t chunk, int64_t first,
+                                           int64_t waves) {
+  for (int64_t s = first; s < b.sequences; s += waves) {
     const Pair64 x = join(b, parts, s, chunk);
     if ((threadIdx.x & 63) == 0) parts.own[s] = {x.n > 0.0 ? x.v / x.n : 0.0, x.n};
   }
+}
+
+__global__ __launch_bounds__(kThreads) void dora_policy_join(const Batch b, const Parts parts,
+                                                             int64_t chunk) {
+  join_means(b, parts, chunk, wave_id(), (int64_t)gridDim.x * kWaves);
 }
 
 // Sums of N values over the workgroup's 16 waves, to every thread.
@@ -211,13 +222,14 @@ __device__ __forceinline__ void finish_sum(double* v, double* lds) {
   __syncthreads();
 }
 
-// The loss, the statistics and the factors, by one workgroup.
+// The loss, the statistics and the factors, by one workgroup, from `groups` totals.
+struct Results {
+  double denominator;
+  float *loss, *stats, *weight;
+};
 template <bool SEQ>
-__global__ __launch_bounds__(kFinish) void dora_policy_finish(int64_t sequences, const Pair64* means,
-                                                              const double* totals, int64_t groups,
-                                                              double denominator, float* loss,
-                                                              float* stats, float* weight) {
-  __shared__ double lds[kFinish / 64 * kTotals];
+__device__ __forceinline__ void finish(int64_t sequences, const Pair64* means, const double* totals,
+                                       int64_t groups, const Results& to, double* lds) {
   double all[kTotals] = {};
   for (int64_t c = threadIdx.x; c < groups; c += kFinish) {
 #pragma unroll
@@ -233,20 +245,43 @@ __global__ __launch_bounds__(kFinish) void dora_policy_finish(int64_t sequences,
     }
     finish_sum<2>(sum, lds);
   }
-  const double by = denominator > 0.0 ? denominator : fmax(sum[1], 1.0);
+  const double by = to.denominator > 0.0 ? to.denominator : fmax(sum[1], 1.0);
   if (SEQ) {
     for (int64_t s = threadIdx.x; s < sequences; s += kFinish)
-      weight[s] = means[s].n > 0.0 ? (float)(1.0 / (means[s].n * by)) : 0.f;
+      to.weight[s] = means[s].n > 0.0 ? (float)(1.0 / (means[s].n * by)) : 0.f;
   }
   if (threadIdx.x == 0) {
     const double n = fmax(all[1], 1.0);
-    *loss = (float)(sum[0] / by);
-    if (!SEQ) *weight = (float)(1.0 / by);
-    stats[0] = (float)(all[2] / n);
-    stats[1] = (float)(all[3] / n);
-    stats[2] = (float)(all[4] / n);
-    stats[3] = (float)all[1];
+    *to.loss = (float)(sum[0] / by);
+    if (!SEQ) *to.weight = (float)(1.0 / by);
+    to.stats[0] = (float)(all[2] / n);
+    to.stats[1] = (float)(all[3] / n);
+    to.stats[2] = (float)(all[4] / n);
+    to.stats[3] = (float)all[1];
   }
+}
+template <bool SEQ>
+__global__ __launch_bounds__(kFinish) void dora_policy_finish(int64_t sequences, const Pair64* means,
+                                                              const double* totals, int64_t groups,
+                                                              const Results to) {
+  __shared__ double lds[kFinish / 64 * kTotals];
+  finish<SEQ>(sequences, means, totals, groups, to, lds);
+}
+// All of a small batch's loss by one workgroup, a round a wave: one launch (from Python eight answers of
+// 256 tokens 6.8 us, in two launches 10.1; of 512 8.7 and 10.1; of 1024, two rounds a wave, 12.6 and
+// 9.9; means of 64 sequences of 32 19.8 and 19.2).
+template <bool SEQ, bool PER>
+__global__ __launch_bounds__(kFinish) void dora_policy_small(const Batch b, const Parts parts, int64_t chunk,
+                                                             const Tokens k, const Results to) {
+  __shared__ double totals[kFinish / 64 * kTotals], lds[kFinish / 64 * kTotals];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  chunk_sums<SEQ, PER>(b, parts, chunk, wave, k, totals + wave * kTotals);
+  __syncthreads();   // the workgroup's own writes are there
+  if (SEQ) {
+    join_means(b, parts, chunk, wave, kFinish / 64);
+    __syncthreads();
+  }
+  finish<SEQ>(b.sequences, parts.own, totals, kFinish / 64, to, lds);
 }
 
 template <bool SEQ, bool PER>
@@ -372,9 +407,19 @@ DORA_API int dora_policy_forward(const dora_token_batch* batch, const dora_polic
                        reinterpret_cast<Pair64*>(p + l.own)};
   double* totals = reinterpret_cast<double*>(p + l.totals);
   hipStream_t st = reinterpret_cast<hipStream_t>(hip_stream);
+  const Tokens k = tokens_of(*options, logp, old_logp, ref_logp, advantages);
+  const Results to = {options->denominator, loss, stats, weight};
+  if (b.tokens <= kSmallTokens && (!seq || b.sequences <= kSmallSequences)) {
+    LaunchTimer timer("policy_small", st);
+    by_options(*options, [&](auto seq_, auto per_) {
+      hipLaunchKernelGGL((dora_policy_small<decltype(seq_)::value, decltype(per_)::value>), dim3(1),
+                         dim3(kFinish), 0, st, b, parts, chunk_of(b.tokens, kFinish / 64), k, to);
+    });
+    HIP_TRY(hipGetLastError());
+    return DORA_OK;
+  }
   if (!none) {
     LaunchTimer timer("policy_sums", st);
-    const Tokens k = tokens_of(*options, logp, old_logp, ref_logp, advantages);
     by_options(*options, [&](auto seq_, auto per_) {
       hipLaunchKernelGGL((dora_policy_sums<decltype(seq_)::value, decltype(per_)::value>),
                          dim3(wave_grid(l.chunks)), dim3(kThreads), 0, st, b, parts, l.chunk, k,
@@ -389,9 +434,9 @@ DORA_API int dora_policy_forward(const dora_token_batch* batch, const dora_polic
     HIP_TRY(hipGetLastError());
   }
   LaunchTimer timer("policy_finish", st);
-  auto finish = seq ? dora_policy_finish<true> : dora_policy_finish<false>;
-  hipLaunchKernelGGL(finish, dim3(1), dim3(kFinish), 0, st, b.sequences, parts.own, totals,
-                     (int64_t)(none ? 0 : wave_grid(l.chunks)), options->denominator, loss, stats, weight);
+  auto kernel = seq ? dora_policy_finish<true> : dora_policy_finish<false>;
+  hipLaunchKernelGGL(kernel, dim3(1), dim3(kFinish), 0, st, b.sequences, parts.own, totals,
+                     (int64_t)(none ? 0 : wave_grid(l.chunks)), to);
   HIP_TRY(hipGetLastError());
   return DORA_OK;
 }

@@ -6,7 +6,7 @@
 // Nine bytes a token are read forward (two log probabilities and the mask), one is
 // read and four are written backward, so a large batch is bound by memory and a
 // small one by its launches: two forward (sums of chunks; sequences joined and pairs
-// finished) and one backward, or two (a coefficient per sequence; the tokens).  Scores are
+// finished), or one where a workgroup does both, and one backward, or two (a coefficient per sequence; the tokens).  Scores are
 // differences of sums over thousands of tokens, so sums are float64.
 #include <algorithm>
 #include <cmath>
@@ -20,17 +20,18 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
+constexpr int kSmall = 1024;   // threads of a small batch's workgroup, and what it takes: tokens, and
+constexpr int64_t kSmallTokens = 16384, kSmallRows = 32;   // sequences and pairs together
 
 __device__ __forceinline__ int64_t wave_id() {
   return (int64_t)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 }
 
-// Sums of logp - ref and the counted tokens, a wave per chunk.
+// Sums of logp - ref and the counted tokens of chunk w, by a wave.
 template <bool REF>
-__global__ __launch_bounds__(kThreads) void dora_preference_sums(const Batch b, const Parts parts,
-                                                                 int64_t chunk, const float* logp,
-                                                                 const float* ref) {
-  const int64_t w = wave_id(), c0 = w * chunk;
+__device__ __forceinline__ void chunk_sums(const Batch& b, const Parts& parts, int64_t chunk, int64_t w,
+                                           const float* logp, const float* ref) {
+  const int64_t c0 = w * chunk;
   if (c0 >= b.tokens) return;
   const int64_t c1 = min(c0 + chunk, b.tokens);
   const int lane = threadIdx.x & 63;
@@ -80,23 +81,26 @@ __device__ __forceinline__ double score_of(const Numbers& o, const Pair64& x) {
   return o.beta * (o.normalize ? x.v / fmax(x.n, 1.0) : x.v);
 }
 
-// A wave per sequence writes its score and count, and one per pair the loss.
-__global__ __launch_bounds__(kThreads) void dora_preference_pairs(
-    const Batch b, const Parts parts, int64_t chunk, const Numbers o, int64_t pairs,
-    const int64_t* chosen, const int64_t* rejected, float* loss, float* score, float* logit,
-    float* count) {
+struct Results {
+  int64_t pairs;
+  const int64_t *chosen, *rejected;
+  float *loss, *score, *logit, *count;
+};
+// A wave per sequence writes its score and count, and one per pair the loss: those from `first` on, each
+// `waves`th.
+__device__ __forceinline__ void finish(const Batch& b, const Parts& parts, int64_t chunk, const Numbers& o,
+                                       const Results& to, int64_t first, int64_t waves) {
   const int lane = threadIdx.x & 63;
-  const int64_t waves = (int64_t)gridDim.x * kWaves;
-  for (int64_t w = wave_id(); w < b.sequences + pairs; w += waves) {
+  for (int64_t w = first; w < b.sequences + to.pairs; w += waves) {
     if (w < b.sequences) {
       const Pair64 x = join(b, parts, w, chunk);
       if (lane == 0) {
-        score[w] = (float)score_of(o, x);
-        count[w] = (float)x.n;
+        to.score[w] = (float)score_of(o, x);
+        to.count[w] = (float)x.n;
       }
       continue;
     }
-    const int64_t p = w - b.sequences, c = chosen[p], r = rejected[p];
+    const int64_t p = w - b.sequences, c = to.chosen[p], r = to.rejected[p];
     float out = 0.f, at = 0.f;
     if (b.inside(c) && b.inside(r)) {
       const double h = score_of(o, join(b, parts, c, chunk)) -
@@ -116,10 +120,35 @@ __global__ __launch_bounds__(kThreads) void dora_preference_pairs(
       at = (float)h;
     }
     if (lane == 0) {
-      loss[p] = out;
-      logit[p] = at;
+      to.loss[p] = out;
+      to.logit[p] = at;
     }
   }
+}
+
+template <bool REF>
+__global__ __launch_bounds__(kThreads) void dora_preference_sums(const Batch b, const Parts parts,
+                                                                 int64_t chunk, const float* logp,
+                                                                 const float* ref) {
+  chunk_sums<REF>(b, parts, chunk, wave_id(), logp, ref);
+}
+__global__ __launch_bounds__(kThreads) void dora_preference_pairs(const Batch b, const Parts parts,
+                                                                  int64_t chunk, const Numbers o,
+                                                                  const Results to) {
+  finish(b, parts, chunk, o, to, wave_id(), (int64_t)gridDim.x * kWaves);
+}
+// Both for a small batch by one workgroup, a chunk a wave: one launch (from Python a pair of 512 tokens
+// each 6.3 us, in two launches 10.0; 8 pairs of 1024 7.7 and 10.1; but 4 pairs of 4096 10.4 and 10.3,
+// 32 pairs of 256 15.4 and 10.3).
+template <bool REF>
+__global__ __launch_bounds__(kSmall) void dora_preference_small(const Batch b, const Parts parts,
+                                                                int64_t chunk, const float* logp,
+                                                                const float* ref, const Numbers o,
+                                                                const Results to) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  chunk_sums<REF>(b, parts, chunk, wave, logp, ref);
+  __syncthreads();   // the workgroup's own writes are there
+  finish(b, parts, chunk, o, to, wave, kSmall / 64);
 }
 
 __device__ __forceinline__ double slope_of(const Numbers& o, double h) {
@@ -260,6 +289,17 @@ DORA_API int dora_preference_forward(const dora_token_batch* batch,
   const Batch b = device_batch(*batch);
   const Parts parts = parts_at(l, ws);
   hipStream_t st = reinterpret_cast<hipStream_t>(hip_stream);
+  const Results to = {pairs, chosen, rejected, loss, score, logit, count};
+  if (!none && b.tokens <= kSmallTokens && b.sequences + pairs <= kSmallRows) {
+    if (no_seq && alone) return DORA_OK;
+    const int64_t chunk = chunk_of(b.tokens, kSmall / 64);
+    LaunchTimer timer("preference_small", st);
+    auto kernel = ref_logp ? dora_preference_small<true> : dora_preference_small<false>;
+    hipLaunchKernelGGL(kernel, dim3(1), dim3(kSmall), 0, st, b, parts, chunk, logp, ref_logp, numbers(*options),
+                       to);
+    HIP_TRY(hipGetLastError());
+    return DORA_OK;
+  }
   if (!none && !no_seq) {
     LaunchTimer timer("preference_sums", st);
     auto kernel = ref_logp ? dora_preference_sums<true> : dora_preference_sums<false>;
@@ -270,8 +310,7 @@ DORA_API int dora_preference_forward(const dora_token_batch* batch,
   if (no_seq && alone) return DORA_OK;
   LaunchTimer timer("preference_pairs", st);
   hipLaunchKernelGGL(dora_preference_pairs, dim3(wave_grid(b.sequences + pairs)), dim3(kThreads), 0,
-                     st, b, parts, l.chunk, numbers(*options), pairs, chosen, rejected, loss, score,
-                     logit, count);
+                     st, b, parts, l.chunk, numbers(*options), to);
   HIP_TRY(hipGetLastError());
   return DORA_OK;
 }

@@ -316,6 +316,41 @@ def test_more_tokens_than_one_round_a_wave(ops):
     assert not grad[:5].any() and not grad[at[-1]:].any() and not pg[:5].any() and not pg[at[-1]:].any()
 
 
+@pytest.mark.parametrize("layout", [[16384], [16385], [4096], [4097], [512] * 8, [128] * 32, [1] * 33 + [7],
+                                    [1000] * 16, [700] * 21, [0] * 20 + [4000, 96]], ids=lambda v: f"{len(v)}x{max(v)}")
+def test_batches_of_one_workgroup_and_just_more(ops, layout):
+    """The same sums whichever way they are formed: sequences on both sides of a batch that is not small."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    off = torch.tensor(np.concatenate([[0], np.cumsum(layout)]), device="cuda")
+    n, S, more = int(off[-1]), len(layout), 20000
+    logp, old, ref = (-torch.rand(n + more, device="cuda", generator=g) for _ in range(3))
+    mask = torch.rand(n + more, device="cuda", generator=g) < 0.9
+    adv = torch.randn(S + 1, device="cuda", generator=g)
+    c, r = (torch.randint(0, S, (9,), device="cuda", generator=g) for _ in range(2))
+    big = torch.cat([off, off[-1:] + more])
+    a = ops.dora_preference_loss(logp[:n], c, r, ref_logp=ref[:n], mask=mask[:n], offsets=off)
+    b = ops.dora_preference_loss(logp, c, r, ref_logp=ref, mask=mask, offsets=big)
+    for x, y in zip(a, b):
+        near(x, y[:x.numel()].double().cpu().numpy(), 10.0, half=2 * HALF)
+    how = dict(kl_coef=0.1, reduce="sequence")
+    v, stats, w = ops.dora_policy_loss(logp[:n], old[:n], adv[:S], ref_logp=ref[:n], mask=mask[:n], offsets=off, **how)
+    v2, stats2, w2 = ops.dora_policy_loss(logp, old, adv, ref_logp=ref, mask=mask, offsets=big, **how)
+    some = int((w > 0).sum())
+    near(w * some, (w2[:S] * int((w2 > 0).sum())).double().cpu().numpy(), half=6 * HALF)
+    # token sums are additive: of the batch, of what lies behind it, and of both
+    one = dict(mask=mask[n:], offsets=torch.tensor([0, more], device="cuda"), denominator=1.0, kl_coef=0.1)
+    rest = ops.dora_policy_loss(logp[n:], old[n:], adv[S:], ref_logp=ref[n:], **one)
+    one = dict(denominator=1.0, kl_coef=0.1)
+    part = ops.dora_policy_loss(logp[:n], old[:n], adv[:S], ref_logp=ref[:n], mask=mask[:n], offsets=off, **one)
+    both = ops.dora_policy_loss(logp, old, adv, ref_logp=ref, mask=mask, offsets=big, **one)
+    # three sums, each rounded to float32
+    room = HALF * sum(abs(float(x[0])) for x in (part, rest, both)) + 1e-12 * (n + more)
+    assert abs(float(part[0]) + float(rest[0]) - float(both[0])) <= room
+    assert float(part[1][3]) + float(rest[1][3]) == float(both[1][3]) == int(mask.sum())
+    means = [(float(x[1][0]) * float(x[1][3])) for x in (part, rest, both)]
+    assert abs(means[0] + means[1] - means[2]) <= 6 * HALF * abs(means[2])
+
+
 def test_more_than_2_32_tokens(ops):
     """Token numbers pass 2^32; the sequences' log ratios are 1/4 a token, and every fourth is masked."""
     n = 2 ** 32 + 5003
