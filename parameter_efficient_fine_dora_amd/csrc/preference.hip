@@ -6,8 +6,9 @@
 // Nine bytes a token are read forward (two log probabilities and the mask), one is
 // read and four are written backward, so a large batch is bound by memory and a
 // small one by its launches: two forward (sums of chunks; sequences joined and pairs
-// finished), or one where a workgroup does both, and one backward, or two (a coefficient per sequence; the tokens).  Scores are
-// differences of sums over thousands of tokens, so sums are float64.
+// finished), or one where a workgroup does both, and one backward, or two (a
+// coefficient per sequence; the tokens).  Scores are differences of sums over
+// thousands of tokens, so sums are float64.
 #include <algorithm>
 #include <cmath>
 
