@@ -1697,7 +1697,7 @@ struct Kind {
 struct Pass {
   bool small;               // n <= 64 throughout
   int gram, square, apply;  // tiles
-  int64_t tiles;            // of 64, of an n x n product
+  int64_t tiles, large;     // of 64 and of 128, of an n x n product
   std::vector<int> order;   // items, group by group
   Groups groups;
   size_t bytes;
@@ -1731,6 +1731,7 @@ void lay_out(Group& g, const Kind& k, int gram, bool small) {
 // 24 matrices of 384 x 8192 503 and 581; with tiles of 128 throughout 1031 x 517 213 instead of 174).
 constexpr int64_t kEnough = 256;
 constexpr int64_t kFewTiles = 384;   // of a launch of n x n products
+constexpr int64_t kCus = 256;
 // Workgroups of the sums over m, and the least stages of 64 of one's part.  Parts cost their partial
 // sums, few of them leave CUs empty or the last ones waiting: 24 layers' step 1.43 ms, with 768
 // wanted 1.45; four matrices of 384 x 8192 190 us, with parts of four stages 201; with tiles of 64
@@ -1786,6 +1787,7 @@ std::vector<Pass> passes(const std::vector<Item>& items, const Kind& kind) {
     p.gram = !p.small && parts >= kEnough ? 128 : 64;
     p.square = squares >= 2 * kEnough ? 128 : 64;
     p.tiles = small_squares;
+    p.large = squares;
     p.apply = !p.small && across >= kEnough ? 128 : 64;
     int64_t stages = 0;   // of 64 of the longer side, for all tiles of S
     for (int i = 0; i < p.groups.count; ++i) {
@@ -1974,16 +1976,22 @@ struct Engine {
   }
   // Tiles of 64 in two stages (32 KB) lie five to a CU: 48 matrices of 384 take 24 us a product, with
   // tiles of 128 30; a matrix of 2048 takes 48 and 58.  From two of the large tiles for each CU on
-  // their half traffic counts (4096: 4.4 ms in all against 6.2).  Few tiles have the CU's SIMDs to
-  // themselves: eight waves, and two stages at a time, since a stage is 750 cycles of waiting for LDS
-  // and for each other (517 columns: 175 us in all, one stage at a time 184, four waves 192; 1536
-  // columns, whose double launches have 600 tiles: 467 us either way; 24 matrices of 384, 504 tiles:
-  // 335 us as here, 355 with eight waves).
+  // their half traffic counts (4096 columns: 4.6 ms in all against 5.0, 5000: 7.9 against 10.2).  Fewer
+  // of them are worth it where they leave the fullest CU no more work than tiles of 64 do, one to a CU
+  // in four stages (1800 columns: 604 us against 631, 2600: 1342 against 1427; 2048, where they do not,
+  // 990 against 905; 40 matrices of 384, where it is level: 518 against 515).  Few tiles have the CU's
+  // SIMDs to themselves: eight waves, and two stages at a time, since a stage is 750 cycles of waiting
+  // for LDS and for each other (517 columns: 175 us in all, one stage at a time 184, four waves 192; 1536
+  // columns, whose double launches have 600 tiles: 467 us either way; 24 matrices of 384, 504 tiles: 335
+  // us as here, 355 with eight waves).
   template <bool POLY>
   hipError_t squares(const Square& one, const Square* two = nullptr) {
     if (p.square == 128) return squares_on<POLY, 128, 2, 8, 1>(one, two);
-    return p.tiles * (two ? 2 : 1) <= kFewTiles ? squares_on<POLY, 64, 4, 8, 2>(one, two)
-                                                : squares_on<POLY, 64, 2, 4, 1>(one, two);
+    const int64_t small = p.tiles * (two ? 2 : 1), large = p.large * (two ? 2 : 1);
+    if (small <= kFewTiles) return squares_on<POLY, 64, 4, 8, 2>(one, two);
+    const int64_t each = (small + kCus - 1) / kCus, each_large = (large + kCus - 1) / kCus;
+    return 4 * each_large <= each ? squares_on<POLY, 128, 4, 8, 1>(one, two)
+                                  : squares_on<POLY, 64, 2, 4, 1>(one, two);
   }
   hipError_t fold() {
     Groups a = p.groups;

@@ -116,6 +116,21 @@ def test_tiles_of_128_and_many_matrices(ops, dtype):
         assert float(d) <= 2 * tolerance(dt, want)
 
 
+def test_tiles_by_the_fullest_cu(ops):
+    """Numbers of tiles for which products of one launch, or of two in one, change their tiles."""
+    for count, n in ((40, 333), (13, 600), (1, 1290), (1, 1800)):
+        x = torch.stack([matrix(n, n + 70, i % 3, torch.bfloat16) for i in range(count)])
+        got = ops.dora_orthogonalize(x)
+        for i in {0, count - 1}:
+            want = x[i].double()
+            want /= want.norm() + 1e-7
+            for a, b, c in STEPS:
+                s = want @ want.T
+                want = a * want + (b * s + c * (s @ s)) @ want
+            want = host(want)
+            assert off(got[i], want) <= tolerance(torch.bfloat16, want), (n, off(got[i], want))
+
+
 def test_more_matrices_than_a_launch_takes(ops):
     """Launches that begin and end inside runs of equal sizes, each matrix as it is alone."""
     sizes = [(5, 70)] * 100 + [(70, 5)] * 90 + [(9, 20)] * 55 + [(70, 66)] * 130
