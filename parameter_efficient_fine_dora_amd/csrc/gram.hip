@@ -54,6 +54,8 @@ template <int N>
 __device__ __forceinline__ void wait_vm() {
   __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
 }
+// LDS reads that are under way have arrived (lgkmcnt 0).
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 __device__ __forceinline__ void barrier_nofence() { asm volatile("s_barrier" ::: "memory"); }
 
 // Upper-triangle tile t of an n x n tile grid -> (ti, tj), ti <= tj, row by row.
@@ -135,7 +137,10 @@ __global__ __launch_bounds__(256) void dora_gram_partial(const uint16_t* A, int 
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk)
       acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[kk], fa[kk], acc, 0, 0, 0);
-    barrier_nofence();   // every wave has read the slot before it is refilled
+    // every wave has read the slot, and not only asked for it, before it is refilled: the compiler may
+    // put the last reads' wait, with their matrix instruction, behind the barrier
+    wait_lds();
+    barrier_nofence();
     if (st + kGRing < nst) issue(st + kGRing);
   }
   // acc[v]: row a = lane % 32 of the A-side block, column (v/4)*8 + (lane/32)*4 + v%4
