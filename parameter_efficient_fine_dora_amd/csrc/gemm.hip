@@ -452,6 +452,8 @@ __device__ __forceinline__ float g_row(const void* mag, const float* norm, int m
 }
 
 __device__ __forceinline__ void wait_vmem() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// LDS reads and stores that are under way have arrived (lgkmcnt 0).
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
 // s_waitcnt vmcnt(N) with the other counters left open (gfx9 encoding).
 template <int N>
@@ -711,6 +713,7 @@ __global__ __launch_bounds__(WM * WN * 64) void dora_gemm_bf16(const KArgs p) {
       wait_vmem();                                                                         \
       ca.commit(DORA_A(SB), tid);                                                          \
       cb.commit(DORA_B(SB) + BBASE, tid);                                                  \
+      wait_lds(); /* the stores are in LDS before the barrier, behind which they are read */ \
     }                                                                                      \
   } while (0)
 

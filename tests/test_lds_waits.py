@@ -5,12 +5,13 @@ from __future__ import annotations
 import os
 import re
 import subprocess
+from concurrent.futures import ThreadPoolExecutor
 
 import pytest
 
 from parameter_efficient_fine_dora_amd import build
 
-OWN_BARRIERS = ["gram.hip", "orthogonal.hip"]
+OWN_BARRIERS = ["gemm.hip", "gram.hip", "orthogonal.hip"]
 
 
 def under_way(assembly):
@@ -42,19 +43,31 @@ def test_the_look_finds_what_it_should():
     assert under_way(read + " s_endpgm\n_Z1j:\n s_barrier\n") == (1, [])
 
 
-@pytest.mark.parametrize("source", OWN_BARRIERS)
-def test_no_lds_access_is_under_way_at_a_barrier(source, tmp_path):
-    out = tmp_path / "out.s"
-    cmd = [build.hipcc(), *build.compile_flags(), "--cuda-device-only", "-S",
-           os.path.join(build.CSRC, source), "-o", str(out)]
+@pytest.fixture(scope="module")
+def assembly(tmp_path_factory):
+    """The sources' assembly, compiled side by side (gemm.hip alone takes most of a minute)."""
+    at = tmp_path_factory.mktemp("waits")
+
+    def compiled(source):
+        out = at / (source + ".s")
+        subprocess.run([build.hipcc(), *build.compile_flags(), "--cuda-device-only", "-S",
+                        os.path.join(build.CSRC, source), "-o", str(out)], check=True,
+                       stdout=subprocess.DEVNULL, stderr=subprocess.DEVNULL, timeout=600)
+        return out.read_text()
+
     try:
-        subprocess.run(cmd, check=True, stdout=subprocess.DEVNULL, stderr=subprocess.DEVNULL, timeout=300)
+        with ThreadPoolExecutor(len(OWN_BARRIERS)) as pool:
+            return dict(zip(OWN_BARRIERS, pool.map(compiled, OWN_BARRIERS)))
     except OSError:
         pytest.skip("hipcc not available")
-    barriers, found = under_way(out.read_text())
+
+
+@pytest.mark.parametrize("source", OWN_BARRIERS)
+def test_no_lds_access_is_under_way_at_a_barrier(assembly, source):
+    barriers, found = under_way(assembly[source])
     assert barriers > 0 and not found, found
 
 
 def test_every_source_with_its_own_barrier_is_looked_at():
     own = [s for s in build.SOURCES if '"s_barrier"' in open(os.path.join(build.CSRC, s)).read()]
-    assert set(OWN_BARRIERS) <= set(own)
+    assert set(OWN_BARRIERS) == set(own)
