@@ -105,7 +105,7 @@ DORA_API size_t dora_policy_workspace_bytes(const dora_token_batch* batch,
  * with rho = exp(logp - old_logp), A its advantage and d = ref_logp - logp:
  *   gain = A min(rho, 1 + clip_high)                       for A >= 0
  *          A min(max(rho, 1 - clip_low), dual_clip)        for A < 0
- *   kl   = exp(d) - 1 - d
+ *   kl   = exp(d) - 1 - d, infinite for an infinite d
  *   l    = -gain + kl_coef kl
  *   loss = sum of l over the counted tokens / denominator             (token), or
  *          sum over sequences of the mean of l / denominator          (sequence),

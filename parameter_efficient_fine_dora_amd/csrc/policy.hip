@@ -16,6 +16,7 @@
 #include "checks.h"
 #include "kernels.h"
 #include "sequences.h"
+#include "exponential.h"
 
 namespace dora {
 namespace {
@@ -34,32 +35,6 @@ struct Term {
   double loss, slope, kl, held, ratio;
 };
 
-// exp(x) = 2^n (1 + q) with x = n log 2 + r, |r| <= 0.35, and q the Taylor sum to r^10 / 10!: what is
-// left out is under 0.35^11 / 11! = 2.4e-13 of the result, a thousandth of a float32 rounding and
-// less.  (Memory should bound these kernels: the library's exponentials, exact to the last bit of
-// float64, took 5 us more of 1M tokens' sums, 17 against 12.)
-struct Exponential {
-  double q, two;   // two: 2^n
-  __device__ __forceinline__ explicit Exponential(double x) {
-    x = x > 1100.0 ? 1100.0 : x < -1100.0 ? -1100.0 : x;   // 0 and infinity; NaN stays
-    const double n = __builtin_rint(x * 1.4426950408889634);
-    const double r = fma(n, -0.6931471805599453, x);
-    double p = 1.0 / 3628800.0;
-    p = fma(p, r, 1.0 / 362880.0);
-    p = fma(p, r, 1.0 / 40320.0);
-    p = fma(p, r, 1.0 / 5040.0);
-    p = fma(p, r, 1.0 / 720.0);
-    p = fma(p, r, 1.0 / 120.0);
-    p = fma(p, r, 1.0 / 24.0);
-    p = fma(p, r, 1.0 / 6.0);
-    p = fma(p, r, 0.5);
-    q = fma(p * r, r, r);
-    two = ldexp(1.0, (int)n);
-  }
-  __device__ __forceinline__ double value() const { return fma(q, two, two); }
-  __device__ __forceinline__ double less_one() const { return fma(q, two, two - 1.0); }
-};
-
 __device__ __forceinline__ Term term(const Tokens& k, float logp, float old, float ref, float adv) {
   Term x;
   const double a = adv;
@@ -74,7 +49,7 @@ __device__ __forceinline__ Term term(const Tokens& k, float logp, float old, flo
   x.kl = 0.0;
   if (k.ref) {
     const double d = (double)ref - (double)logp, e = Exponential(d).less_one();
-    x.kl = e - d;
+    x.kl = d > 1100.0 ? e : e - d;   // an infinite d is nothing beside its exponential
     if (k.kl_coef > 0.0) {
       x.loss += k.kl_coef * x.kl;
       x.slope -= k.kl_coef * e;
