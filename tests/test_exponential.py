@@ -5,6 +5,7 @@ import math
 import os
 import shutil
 import subprocess
+from decimal import Decimal, localcontext
 
 import pytest
 
@@ -63,3 +64,18 @@ def test_the_ends(evaluate):
         assert abs(value - math.exp(x)) <= 1e-12 * math.exp(x) + 2.0 ** -1074 and less == -1.0, x
     value, less = evaluate([math.nan])[0]
     assert math.isnan(value) and math.isnan(less)
+
+
+def test_numbers_between(evaluate):
+    """float64's own precision.  With |r| <= 0.3466 and q in [-0.293, 0.414]: q is off by its rounding, 2^-55,
+    by r's, 2^-55, and by the sum's, a fifth of it twice rounded, 2^-56; 1 + q by 2^-53 of itself more, in all
+    under 2^-52.  2^n q + (2^n - 1) raises q's 2^-54 to at most 2 2^-54 / 0.414 (n = 1) and rounds once: under
+    2^-51.  (One log 2 of float64 instead of two parts is 2^-57 n off: 1e-14 at 700; sums to r^10 are 2e-13.)"""
+    xs = [0.0, 1e-300, 1e-17, 1e-9, 1e-3, 0.1, 0.34657, 0.34658, 0.396, 1.0, 1.0397, 10.0, 44.3, 45.1, 100.3, 417.605, 700.1]
+    xs += [-x for x in xs]
+    with localcontext() as c:
+        c.prec = 400   # of 1 + 1e-300, and what is left of it without the 1
+        for x, (value, less) in zip(xs, evaluate(xs)):
+            exp = Decimal(x).exp()
+            assert abs(Decimal(value) - exp) <= Decimal(2.0 ** -52) * exp, x
+            assert abs(Decimal(less) - (exp - 1)) <= Decimal(2.0 ** -51) * abs(exp - 1), x
