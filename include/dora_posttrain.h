@@ -205,11 +205,10 @@ typedef struct {
  *   m = momentum m + (1 - momentum) grad
  *   u = momentum m + (1 - momentum) grad with nesterov, else m
  *   p = p (1 - lr weight_decay) - lr scale X(u),  X(u) the iteration's last X from u
- * m and the update are float32; p is rounded once.  u is taken to 22 bits, to 16 for bf16
- * parameters without masters, and from |u| = 2^104 eps on the latter become NaN.  A NaN or an
- * infinity in a gradient makes its own element of m, and its own matrix, NaN.  The workspace holds 4
- * (bf16 parameters without masters, or n <= 64) or 8 bytes an element beside what
- * dora_orthogonalize's holds for n.
+ * m and the update are float32; p is rounded once.  u is taken to 22 bits of its largest element,
+ * whatever that is.  A NaN or an infinity in a gradient makes its own element of m, and its own
+ * matrix, NaN.  The workspace holds 4 (bf16 parameters without masters, or n <= 64) or 8 bytes an
+ * element beside what dora_orthogonalize's holds for n.
  */
 DORA_API size_t dora_muon_workspace_bytes(const dora_muon_tensor* tensors, int64_t count,
                                           const dora_muon_options* options);

@@ -16,22 +16,22 @@
 // sums are float32.  For bf16 results that is enough.  Others form the product Q X on the way, before
 // the factor passes what they allow (kMostExact, kMostUpdate), and S anew from it.
 // A bf16 X is one half precision number exactly (its bits below 2^-38 of its largest element are
-// left out), a float32 X is hi + lo.  The update of a bf16 parameter is held as two bf16 numbers
-// instead, 16 bits: what is lost is 2^-18 of X, raised 485 times in the worst case, and half a step
-// of the parameter is 2^-8 of it; half precision would need X's largest element first, which is
-// another pass over gradient and momentum.
+// left out), a float32 X and every update are hi + lo, scaled by a power of two that X's largest element
+// asks for, so that any finite X is held to 22 bits.  (That costs a pass over gradient and momentum.
+// Two bf16 numbers, which hold float32's range, would save it for bf16 parameters, 24 rank-384 layers'
+// step 1.42 ms instead of 1.62, but keep 16 bits, raised 485 times, and squares overflow from 2^104 eps on.)
 //
 // Layout.  A "pair" row holds blocks of 32 columns: 32 hi, then 32 lo, so that the 128 bytes that
 // a stage copies of a row are the hi and lo of 32 columns; a "single" row holds 64 columns there.
 // X stays in its own order: where the sum runs down its rows (S of a tall matrix, Q X of a wide
 // one) its numbers are turned as they are read from LDS.
 //
-// Many matrices share a launch: a step on the adapters of a model is 18 launches whatever their
-// number (bf16 parameters, five steps), and small matrices fill the chip together.
+// Many matrices share a launch: a step on the adapters of a model is 19 launches (bf16 parameters, five
+// steps; up to 120 matrices of up to 12 sizes on one side of 64), and small matrices fill the chip together.
 //
 // n <= 64 (most adapters) takes another way: the n x n products of one matrix are one workgroup's, in
 // LDS, S is summed by the pass that writes X, and Q X is not kept on the way but formed again where it
-// is wanted.  Then a step is three launches (six with float32 masters), and memory bounds it.
+// is wanted.  Then a step is four launches (six with float32 masters), and memory bounds it.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -137,22 +137,12 @@ __device__ __forceinline__ int group_of(const Groups& a, uint32_t id) {
   return __builtin_amdgcn_readfirstlane(g);
 }
 
-// How X's numbers are held: one half precision number, two of them, or two bf16.
-enum Form { kSingle, kPair, kWide };
-template <Form F>
-struct Number {
-  using T = std::conditional_t<F == kWide, __bf16, f16>;
-  static constexpr bool kTwo = F != kSingle;
-};
+// How X's numbers are held: one half precision number, or two of them.
+enum Form { kSingle, kPair };
 typedef short short8 __attribute__((ext_vector_type(8)));
-template <Form F>
 __device__ __forceinline__ f32x16 multiply(short8 a, short8 b, f32x16 c) {
-  if constexpr (F == kWide)
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
-                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
-  else
-    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a),
-                                                  __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0,
+                                                0, 0);
 }
 
 // ---- the product loop ---------------------------------------------------------------------
@@ -401,10 +391,10 @@ struct Product {
               auto& c = acc[i][j];
               if constexpr (PAIR) {
                 auto& l = kApart ? low[kApart ? i : 0][kApart ? j : 0] : c;
-                l = multiply<F>(fb[j], la[i], l);
-                l = multiply<F>(lb[j], fa[i], l);
+                l = multiply(fb[j], la[i], l);
+                l = multiply(lb[j], fa[i], l);
               }
-              c = multiply<F>(fb[j], fa[i], c);
+              c = multiply(fb[j], fa[i], c);
             }
         };
         step(std::integral_constant<int, 0>());
@@ -500,25 +490,24 @@ __device__ __forceinline__ int64_t pair_at(int64_t k) { return (k >> 5) * 64 + (
 
 // v is rounded to float32 first, in a register: a product that the compiler rounds to hi in one
 // step (v_fma_mixlo_f16) and to float32 for lo has another hi in one of 4000 cases.
-template <typename H>
-__device__ __forceinline__ void split(float v, H& hi, H& lo) {
+__device__ __forceinline__ void split(float v, f16& hi, f16& lo) {
   asm("" : "+v"(v));
-  hi = (H)v;
-  lo = (H)(v - (float)hi);
+  hi = (f16)v;
+  lo = (f16)(v - (float)hi);
 }
 // Columns [k, k + N) of a pair row; of a flat one, whose lo begin at `lo`.
-template <int N, typename H = f16>
-__device__ __forceinline__ void store_pair(H* row, int64_t k, const float* v, int64_t lo = 0) {
-  typedef H V __attribute__((ext_vector_type(N)));
+template <int N>
+__device__ __forceinline__ void store_pair(f16* row, int64_t k, const float* v, int64_t lo = 0) {
+  typedef f16 V __attribute__((ext_vector_type(N)));
   V h, l;
 #pragma unroll
   for (int e = 0; e < N; ++e) {
-    H a, b;
+    f16 a, b;
     split(v[e], a, b);
     h[e] = a;
     l[e] = b;
   }
-  H* p = row + (lo ? k : pair_at(k));
+  f16* p = row + (lo ? k : pair_at(k));
   *reinterpret_cast<V*>(p) = h;
   *reinterpret_cast<V*>(p + (lo ? lo : kPairBlock)) = l;
 }
@@ -543,7 +532,6 @@ struct Sources {
   Source s[kMaxMatrices];
   float mu, nu;                    // momentum's factor, 1 - that
   int nesterov;
-  int fixed;                       // kWide: the power of two that X is multiplied by
 };
 
 // Which matrix a workgroup of a launch with addresses works on.
@@ -638,15 +626,11 @@ __device__ __forceinline__ int exponent_of(uint32_t v, uint32_t* lds) {
 }
 
 // The padded matrix as half precision numbers, zeros where the matrix ends: a thread takes eight
-// columns.  Memory bounds it: 2 to 6 bytes an element are read, 2 or 4 written.  bf16 holds float32's
-// range, so kWide needs no largest element: the momentum is moved on here too, in the only pass over
-// it.
+// columns.  Memory bounds it: 2 to 6 bytes an element are read, 2 or 4 written.
 constexpr int kPiece = 4096;   // elements of a workgroup
 template <bool BF, bool MOMENT, Form F>
 __global__ __launch_bounds__(kThreads) void dora_orthogonal_halves(const Sources a, uint8_t* ws) {
-  using H = typename Number<F>::T;
-  constexpr bool PAIR = Number<F>::kTwo;
-  typedef H H8 __attribute__((ext_vector_type(8)));
+  constexpr bool PAIR = F == kPair;
   __shared__ uint32_t lds[kThreads / 64];
   const Where here = where(a.groups, a.first, blockIdx.x, ws);
   const Group& g = here.g;
@@ -654,10 +638,9 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_halves(const Sources
   const int rows = g.tall ? g.m : g.n, cols = g.tall ? g.n : g.m;
   const int pcols = g.tall ? g.nt : g.mt;
   const int64_t all = (int64_t)g.nt * g.mt;
-  const int e = F == kWide ? a.fixed
-                           : exponent_of(most_of(reinterpret_cast<const uint32_t*>(own + g.most), g.blocks), lds);
+  const int e = exponent_of(most_of(reinterpret_cast<const uint32_t*>(own + g.most), g.blocks), lds);
   const Source s = a.s[here.slot];
-  H* out = reinterpret_cast<H*>(own + g.x);
+  f16* out = reinterpret_cast<f16*>(own + g.x);
   const int64_t first = (int64_t)here.piece * kPiece, row0 = first / pcols;
   const uint32_t col0 = (uint32_t)(first - row0 * pcols);
 #pragma unroll
@@ -673,27 +656,21 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_halves(const Sources
       if (MOMENT) {
         float m[kVec];
         load8<false>(s.moment, from, stop, m);
-        if (F == kWide) {
-#pragma unroll
-          for (int q = 0; q < kVec; ++q) m[q] = moved(m[q], v[q], a.mu, a.nu);
-          store_part<false>(s.moment, from, stop, m);
-          store_part<false>(s.moment, from + 4, stop, m + 4);
-        }
 #pragma unroll
         for (int q = 0; q < kVec; ++q) v[q] = update_of(m[q], v[q], a);
       }
     }
-    H8 h, l;
+    f16x8 h, l;
 #pragma unroll
     for (int q = 0; q < kVec; ++q) {
-      H x, y;
+      f16 x, y;
       split(ldexpf(v[q], e), x, y);
       h[q] = x;
       l[q] = y;
     }
-    H* p = out + (PAIR ? r * pcols * 2 + pair_at(c) : at);
-    *reinterpret_cast<H8*>(p) = h;
-    if (PAIR) *reinterpret_cast<H8*>(p + kPairBlock) = l;
+    f16* p = out + (PAIR ? r * pcols * 2 + pair_at(c) : at);
+    *reinterpret_cast<f16x8*>(p) = h;
+    if (PAIR) *reinterpret_cast<f16x8*>(p + kPairBlock) = l;
   }
 }
 
@@ -781,10 +758,10 @@ struct Sums {
       a.template read<U>(src, wave & 1, 0, fa, la);
       b.template read<U>(src, wave >> 1, 0, fb, lb);
       if constexpr (PAIR) {
-        low = multiply<F>(fb[0], la[0], low);
-        low = multiply<F>(lb[0], fa[0], low);
+        low = multiply(fb[0], la[0], low);
+        low = multiply(lb[0], fa[0], low);
       }
-      acc = multiply<F>(fb[0], fa[0], acc);
+      acc = multiply(fb[0], fa[0], acc);
     };
 #pragma unroll
     for (int s = 0; s < kStages; ++s) {
@@ -820,22 +797,19 @@ struct Sums {
 // registers (two to a CU: 72 us).
 template <bool BF, bool MOMENT, Form F>
 __global__ __launch_bounds__(kThreads, 3) void dora_orthogonal_first(const Sources a, uint8_t* ws) {
-  using H = typename Number<F>::T;
-  constexpr bool PAIR = Number<F>::kTwo;
-  typedef H H8 __attribute__((ext_vector_type(8)));
+  constexpr bool PAIR = F == kPair;
   constexpr int kBlock = Sums<F, false>::kBlock, kMine = 64 * 64 / kVec / kThreads;
   __shared__ __attribute__((aligned(1024))) uint8_t sm[2][kBlock];
   __shared__ uint32_t lds[kThreads / 64];
   const Where here = where(a.groups, a.first, blockIdx.x, ws);
   const Group& g = here.g;
   const Source s = a.s[here.slot];
-  const int e = F == kWide ? a.fixed
-                           : exponent_of(most_of(reinterpret_cast<const uint32_t*>(here.own + g.most), g.blocks), lds);
+  const int e = exponent_of(most_of(reinterpret_cast<const uint32_t*>(here.own + g.most), g.blocks), lds);
   const int rows = g.tall ? g.m : g.n, cols = g.tall ? g.n : g.m, pcols = g.tall ? g.nt : g.mt;
   const int blocks = (g.m + 63) / 64;
   const int k0 = (int)((int64_t)blocks * here.piece / g.splits);
   const int k1 = (int)((int64_t)blocks * (here.piece + 1) / g.splits);
-  H* out = reinterpret_cast<H*>(here.own + g.x);
+  f16* out = reinterpret_cast<f16*>(here.own + g.x);
   auto run = [&](auto tall) {
     constexpr bool TALL = decltype(tall)::value;
     Sums<F, TALL> sums;
@@ -866,35 +840,26 @@ __global__ __launch_bounds__(kThreads, 3) void dora_orthogonal_first(const Sourc
       for (int i = 0; i < kMine; ++i) {
         int r, c;
         int64_t ra, ca;
-        const bool real = place(k, i, r, c, ra, ca);
+        place(k, i, r, c, ra, ca);
         if (MOMENT) {
-          float* mo = m[MOMENT ? i : 0];
-          if (F == kWide) {
 #pragma unroll
-            for (int q = 0; q < kVec; ++q) mo[q] = moved(mo[q], v[i][q], a.mu, a.nu);
-            if (real) {
-              store_part<false>(s.moment, ra * cols + ca, (ra + 1) * cols, mo);
-              store_part<false>(s.moment, ra * cols + ca + 4, (ra + 1) * cols, mo + 4);
-            }
-          }
-#pragma unroll
-          for (int q = 0; q < kVec; ++q) v[i][q] = update_of(mo[q], v[i][q], a);
+          for (int q = 0; q < kVec; ++q) v[i][q] = update_of(m[MOMENT ? i : 0][q], v[i][q], a);
         }
-        H8 h, l;
+        f16x8 h, l;
 #pragma unroll
         for (int q = 0; q < kVec; ++q) {
           // (behind a row's end are zeros, and update_of of the zeros of gradient and momentum)
-          H x, y;
+          f16 x, y;
           split(ldexpf(v[i][q], e), x, y);
           h[q] = x;
           l[q] = y;
         }
-        H* to = out + (PAIR ? ra * pcols * 2 + pair_at(ca) : ra * pcols + ca);
-        *reinterpret_cast<H8*>(to) = h;
-        *reinterpret_cast<H8*>(sums.at(block, r, c, 0)) = h;
+        f16* to = out + (PAIR ? ra * pcols * 2 + pair_at(ca) : ra * pcols + ca);
+        *reinterpret_cast<f16x8*>(to) = h;
+        *reinterpret_cast<f16x8*>(sums.at(block, r, c, 0)) = h;
         if (PAIR) {
-          *reinterpret_cast<H8*>(to + kPairBlock) = l;
-          *reinterpret_cast<H8*>(sums.at(block, r, c, 4)) = l;
+          *reinterpret_cast<f16x8*>(to + kPairBlock) = l;
+          *reinterpret_cast<f16x8*>(sums.at(block, r, c, 4)) = l;
         }
       }
       if (k + 1 < k1) load(k + 1);
@@ -945,9 +910,9 @@ __device__ __forceinline__ f32x16 quarter_of(const Rows& q, const Operand<64, kP
     constexpr int U = decltype(number)::value;
     short8 h[1], l[1];
     x.template read<U % 2>(block + U / 2 * kHalfBlock, quarter, 0, h, l);
-    low = ACROSS ? multiply<kPair>(q.l[U], h[0], low) : multiply<kPair>(h[0], q.l[U], low);
-    low = ACROSS ? multiply<kPair>(q.h[U], l[0], low) : multiply<kPair>(l[0], q.h[U], low);
-    acc = ACROSS ? multiply<kPair>(q.h[U], h[0], acc) : multiply<kPair>(h[0], q.h[U], acc);
+    low = ACROSS ? multiply(q.l[U], h[0], low) : multiply(h[0], q.l[U], low);
+    low = ACROSS ? multiply(q.h[U], l[0], low) : multiply(l[0], q.h[U], low);
+    acc = ACROSS ? multiply(q.h[U], h[0], acc) : multiply(h[0], q.h[U], acc);
   };
   step(std::integral_constant<int, 0>());
   step(std::integral_constant<int, 1>());
@@ -1039,16 +1004,13 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_fold(const Groups a,
   else run(std::false_type());
 }
 
-// What turns X' X'^T into the first S: X' is X times a power of two, kWide's or the one that its
-// largest element asks for.
+// What turns X' X'^T into the first S: X' is X times the power of two that its largest element asks for.
 struct Unit {
   float unit;   // the factor on X' where it is known, else 0
   float eps;
-  int wide, fixed;
 };
 __device__ __forceinline__ float norm_factor(float trace, const Unit& u, uint32_t most, uint32_t* lds) {
-  const int e = u.wide ? u.fixed : exponent_of(most, lds);
-  return 1.f / (sqrtf(trace) + ldexpf(u.eps, e));
+  return 1.f / (sqrtf(trace) + ldexpf(u.eps, exponent_of(most, lds)));
 }
 
 // Adds S's partial sums in order, and makes it a pair.  `unit` 0: X is normalised here: the factor
@@ -1116,7 +1078,7 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_gather(const Groups 
 // A symmetric product of two n x n pairs, or of two such products of one launch (`both`).
 //   POLY: out = alpha (left right) + beta left + gamma 1, left and right both S
 //   otherwise out = alpha (left right)
-// `form`: as X's form wants Q: kSingle: all hi of a row, then all lo; kWide: pairs of bf16.
+// `form`: as X's form wants Q: kSingle: all hi of a row, then all lo.
 struct Square {
   int left, right, out;      // of sq
   float alpha, beta, gamma;
@@ -1164,8 +1126,7 @@ __global__ __launch_bounds__(WAVES * 64) void dora_orthogonal_square(const Squar
         if (i == j + e && i < g.n) v[e] += q.gamma;
       }
     }
-    if (q.form == kWide) store_pair<8>(reinterpret_cast<__bf16*>(out) + i * le, j, v);
-    else store_pair<8>(out + i * le, j, v, q.form == kSingle ? g.ne : 0);
+    store_pair<8>(out + i * le, j, v, q.form == kSingle ? g.ne : 0);
   };
   P::lines([&](int r, int c) {
     float v[8];
@@ -1216,7 +1177,7 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_chain(const Chain a,
   if (r == 0.f) {   // under way beside the sums
     static_assert(kMaxSplits * kWaves <= kThreads, "a number of the trace for each thread");
     if ((int)threadIdx.x < g.splits * kWaves) trace = reinterpret_cast<const float*>(own + g.trace)[threadIdx.x];
-    if (!a.unit.wide) most = most_of(reinterpret_cast<const uint32_t*>(own + g.most), g.blocks);
+    most = most_of(reinterpret_cast<const uint32_t*>(own + g.most), g.blocks);
   }
   // chunk c (16 bytes) of row i; columns k .. of a pair row lie in chunks of 8
   auto chunk = [&](int m, int i, int c) { return sm[m] + i * kLd + ((c ^ (i & 15)) << 4); };
@@ -1385,17 +1346,6 @@ __global__ __launch_bounds__(kThreads) void dora_orthogonal_chain(const Chain a,
     });
   }
   __syncthreads();
-  if (a.form == kWide) {
-    __bf16* out = reinterpret_cast<__bf16*>(square_of(g, own, a.q));
-#pragma unroll
-    for (int u = 0; u < kMine; ++u) {
-      const int x = u * kThreads + threadIdx.x, i = x / 16, j = x % 16 * 4;
-      float v[4];
-      get(Q, i, j, v);
-      store_pair<4>(out + i * 2 * kN, j, v);
-    }
-    return;
-  }
   f16* out = reinterpret_cast<f16*>(square_of(g, own, a.q));
 #pragma unroll
   for (int u = 0; u < kN * 16 / kThreads; ++u) {
@@ -1432,7 +1382,7 @@ __device__ __forceinline__ void last_product(uint8_t* sm, const Group& g, uint8_
                                              bool second, int64_t row0, int64_t col0,
                                              f32x16 (&acc)[T / 64][T / 64]) {
   // Q's rows are pairs where X's are; else all hi and then all lo against X twice
-  constexpr bool PAIR = Number<F>::kTwo;
+  constexpr bool PAIR = F == kPair;
   constexpr int kSize = PAIR ? 4 : 2;
   using P = Product<T, RING, F, 4, T == 64 ? 2 : 1>;
   const int64_t ld_q = (int64_t)g.nt * 4, ld_x = (int64_t)(g.tall ? g.nt : g.mt) * kSize;
@@ -1828,7 +1778,6 @@ struct Call {
   Result what;
   float eps, mu, nu, decay, rest;
   int nesterov;
-  int fixed;   // kWide: X's power of two
 };
 
 // (an argument's type is the kernel's, not what is passed)
@@ -1901,41 +1850,30 @@ struct Engine {
   int seen = 0, at = 0;
   Turns turns = {};
 
-  template <bool BF, bool MOMENT, Form... FORMS>
+  template <bool BF, bool MOMENT, Form F>
   hipError_t halves() {
     Sources a;
     a.mu = c.mu;
     a.nu = c.nu;
     a.nesterov = c.nesterov;
-    a.fixed = c.fixed;
     auto fill = [&](int slot, int item) { a.s[slot] = items[item].from; };
-    if (form != kWide)
-      ORTHO_TRY(by_matrix(p, a, [](const Group& g) { return (int64_t)g.blocks; }, fill,
-                          [&](int64_t blocks) {
-                            return launch("orthogonal_most", dora_orthogonal_most<BF, MOMENT>, blocks,
-                                          st, a, ws);
-                          }));
+    ORTHO_TRY(by_matrix(p, a, [](const Group& g) { return (int64_t)g.blocks; }, fill, [&](int64_t blocks) {
+      return launch("orthogonal_most", dora_orthogonal_most<BF, MOMENT>, blocks, st, a, ws);
+    }));
     if (p.small)
-      return by_form<FORMS...>([&](auto f) {
-        return by_matrix(p, a, [](const Group& g) { return (int64_t)g.splits; }, fill, [&](int64_t blocks) {
-          return launch("orthogonal_first", dora_orthogonal_first<BF, MOMENT, decltype(f)::value>, blocks,
-                        st, a, ws);
-        });
+      return by_matrix(p, a, [](const Group& g) { return (int64_t)g.splits; }, fill, [&](int64_t blocks) {
+        return launch("orthogonal_first", dora_orthogonal_first<BF, MOMENT, F>, blocks, st, a, ws);
       });
-    return by_form<FORMS...>([&](auto f) {
-      return by_matrix(p, a, [](const Group& g) { return ((int64_t)g.nt * g.mt + kPiece - 1) / kPiece; }, fill,
-                       [&](int64_t blocks) {
-                         return launch("orthogonal_halves",
-                                       dora_orthogonal_halves<BF, MOMENT, decltype(f)::value>, blocks,
-                                       st, a, ws);
-                       });
-    });
+    return by_matrix(p, a, [](const Group& g) { return ((int64_t)g.nt * g.mt + kPiece - 1) / kPiece; }, fill,
+                     [&](int64_t blocks) {
+                       return launch("orthogonal_halves", dora_orthogonal_halves<BF, MOMENT, F>, blocks, st, a, ws);
+                     });
   }
   hipError_t start() {
-    if (c.moment) return c.x_bf ? halves<true, true, kPair, kWide>() : halves<false, true, kPair, kWide>();
+    if (c.moment) return c.x_bf ? halves<true, true, kPair>() : halves<false, true, kPair>();
     return c.x_bf ? halves<true, false, kSingle>() : halves<false, false, kPair>();
   }
-  Unit unit_of(float unit) const { return {unit, c.eps, form == kWide, c.fixed}; }
+  Unit unit_of(float unit) const { return {unit, c.eps}; }
   // fn with X's form, one of FORMS, as a constant
   template <Form... FORMS, typename Fn>
   hipError_t by_form(Fn fn) const {
@@ -1950,7 +1888,7 @@ struct Engine {
       constexpr int T = decltype(tile)::value;
       Groups a = p.groups;
       int64_t blocks = spread(a, [](const Group& g) { return (int64_t)tri(tiles(g.n, T)) * g.splits; });
-      ORTHO_TRY((by_form<kSingle, kPair, kWide>([&](auto f) {
+      ORTHO_TRY((by_form<kSingle, kPair>([&](auto f) {
         return launch("orthogonal_gram", dora_orthogonal_gram<T, ring(T), decltype(f)::value>, blocks,
                       st, a, (uint32_t)blocks, second, ws);
       })));
@@ -2005,7 +1943,7 @@ struct Engine {
       Groups a = p.groups;
       const int64_t blocks =
           spread(a, [](const Group& g) { return (int64_t)tiles(g.n, T) * tiles(g.m, T); });
-      return by_form<kSingle, kPair, kWide>([&](auto f) {
+      return by_form<kSingle, kPair>([&](auto f) {
         return launch("orthogonal_between", dora_orthogonal_between<T, ring(T), decltype(f)::value>,
                       blocks, st, a, (uint32_t)blocks, q, two(e), second, ws);
       });
@@ -2026,7 +1964,7 @@ struct Engine {
       a.s[slot] = items[item].to;
       a.rate[slot] = items[item].rate;
     };
-    if constexpr (BF == (WHAT == kMaster))
+    if constexpr (!BF || WHAT != kOut)   // (bf16 matrices keep what they form)
       if (seen > 0)
         return by_matrix(p, a, [](const Group& g) { return (int64_t)tiles(g.m, 64); }, fill, [&](int64_t blocks) {
           a.total = (uint32_t)blocks;
@@ -2051,7 +1989,7 @@ struct Engine {
   hipError_t finish(int q, int e) {
     if (c.what == kMaster) return apply<true, kMaster, kPair>(q, e);
     if (c.what == kParam)
-      return c.out_bf ? apply<true, kParam, kWide, kPair>(q, e) : apply<false, kParam, kPair>(q, e);
+      return c.out_bf ? apply<true, kParam, kPair>(q, e) : apply<false, kParam, kPair>(q, e);
     return c.out_bf ? apply<true, kOut, kSingle, kPair>(q, e) : apply<false, kOut, kPair>(q, e);
   }
 
@@ -2223,7 +2161,7 @@ int set_up(const dora_muon_options* o, const dora_muon_tensor* a, int64_t count,
   if (master && o->param_dtype != DORA_BF16) return DORA_ERR_DTYPE;
   const bool exact = master || o->param_dtype == DORA_F32;
   DORA_CHECK(check_iteration(&o->iteration, exact ? kMostUpdate : kMostBrief, s.z));
-  s.kind = {exact ? kPair : kWide, s.z.times};
+  s.kind = {kPair, s.z.times};
   return DORA_OK;
 }
 
@@ -2305,9 +2243,6 @@ DORA_API int dora_muon_step(const dora_muon_tensor* tensors, int64_t count,
     c.mu = (float)o.momentum;
     c.nu = (float)(1.0 - o.momentum);
     c.nesterov = o.nesterov;
-    // eps becomes 2^-40 to 2^-41: where X's squares underflow (|X| under 2^-63) eps is all there is,
-    // and they overflow from |X| = 2^64, 2^104 eps, on
-    c.fixed = -40 - (int)std::ceil(std::log2(o.iteration.eps));
     // what float32 loses of 1 - lr weight_decay beside 1 is added apart
     const double decay = o.lr * o.weight_decay;
     c.decay = (float)(1.0 - decay);
