@@ -1027,10 +1027,12 @@ def dora_muon(plan, grads, *, lr, momentum=0.95, nesterov=True, weight_decay=0.0
                                float(momentum), float(weight_decay))
     L, n = _lib.lib(), len(plan.params)
     if workspace is None:
+        # depends on the sizes, which a plan keeps, and the coefficients; 0 where the step will be refused
+        # for another option, which says nothing about the next one
         key = tuple(_held)
-        if key not in plan._bytes:   # depends on the sizes, which a plan keeps, and the coefficients
-            plan._bytes = {key: L.dora_muon_workspace_bytes(plan.table, n, ctypes.byref(how))}
-        workspace = torch.empty(max(plan._bytes[key], 1), dtype=torch.uint8, device=plan.device)
+        nbytes = plan._bytes.get(key) or L.dora_muon_workspace_bytes(plan.table, n, ctypes.byref(how))
+        plan._bytes = {key: nbytes}
+        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=plan.device)
     # (the parameters' versions go up: a backward pass that saved one from before is refused)
     _check(_compiled().muon_step(plan._address, plan.params, ctypes.addressof(how), workspace.data_ptr(),
                                  _given_ws(workspace, plan.device), _stream(plan.device)),

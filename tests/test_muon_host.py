@@ -1,0 +1,80 @@
+"""Muon's bookkeeping on the host: plans on tensors that are only looked at, the compiled step replaced by
+a recorder, so that no GPU is needed."""
+from __future__ import annotations
+
+import ctypes
+import math
+import os
+
+import pytest
+import torch
+
+from parameter_efficient_fine_dora_amd import _lib, ops
+
+pytestmark = pytest.mark.skipif(not os.path.exists(_lib.LIB_PATH), reason="libdora.so not built")
+
+
+class Recorder:
+    """The compiled entry points: notes the workspace that a step got, and refuses what the library's
+    size says is refused."""
+
+    def __init__(self):
+        self.steps = []
+
+    def muon_grads(self, *args):
+        return None
+
+    def muon_step(self, table, params, how, ws, ws_bytes, stream):
+        options = _lib.DoraMuonOptions.from_address(how)
+        entries = (_lib.DoraMuonTensor * len(params)).from_address(table)
+        need = _lib.lib().dora_muon_workspace_bytes(entries, len(params), ctypes.byref(options))
+        self.steps.append((ws_bytes, need))
+        if not need:
+            return _lib.ERR_CODE["DORA_ERR_FLAGS"]
+        return _lib.ERR_CODE["DORA_ERR_WORKSPACE"] if ws_bytes < need else 0
+
+
+@pytest.fixture
+def compiled(monkeypatch):
+    """Host tensors pass for device tensors, and the recorder for the compiled module."""
+    def need(t, name, dtype=None, shape=None, dev=None):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a tensor")
+        if dtype is not None and t.dtype != dtype:
+            raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+        if shape is not None and tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        return t
+
+    recorder = Recorder()
+    monkeypatch.setattr(ops, "_need", need)
+    monkeypatch.setattr(ops, "_compiled", lambda: recorder)
+    monkeypatch.setattr(ops, "_stream", lambda dev: 0)
+    monkeypatch.setattr(ops, "_given_ws", lambda ws, dev: ws.numel())
+    return recorder
+
+
+def plan_of(*sizes, dtype=torch.float32):
+    params = [torch.ones(*s, dtype=dtype) for s in sizes]
+    return ops.MuonPlan(params, [torch.zeros(*s) for s in sizes]), [torch.ones(*s, dtype=dtype) for s in sizes]
+
+
+@pytest.mark.parametrize("bad", [dict(lr=math.nan), dict(lr=math.inf), dict(momentum=1.0), dict(momentum=-0.5),
+                                 dict(eps=0.0), dict(weight_decay=math.inf)], ids=str)
+def test_a_refused_step_spoils_no_later_one(compiled, bad):
+    plan, grads = plan_of((256, 1024))
+    with pytest.raises(_lib.DoraError, match="DORA_ERR_FLAGS"):
+        ops.dora_muon(plan, grads, **dict(dict(lr=0.1), **bad))
+    for _ in range(2):
+        ops.dora_muon(plan, grads, lr=0.1)
+    assert compiled.steps[-1][0] >= compiled.steps[-1][1] > 0
+
+
+def test_other_coefficients_get_their_own_workspace(compiled):
+    plan, grads = plan_of((256, 1024))
+    for steps in (5, 16, 1, 5):
+        ops.dora_muon(plan, grads, lr=0.1, coefficients=((3.4445, -4.7750, 2.0315),) * steps)
+        got, need = compiled.steps[-1]
+        assert got == need > 0
