@@ -254,6 +254,10 @@ class Muon(torch.optim.Optimizer):
 
     def load_state_dict(self, state_dict):
         """Loads a checkpoint of this class."""
+        for i, group in enumerate(state_dict["param_groups"]):
+            lacks = [k for k in self.defaults if k not in group]
+            if lacks:   # another optimizer's: torch would take the group as it is
+                raise ValueError(f"the checkpoint's group {i} lacks {', '.join(lacks)}")
         for i, s in state_dict["state"].items():
             if s and "momentum_buffer" not in s:
                 raise ValueError(f"the checkpoint's state of parameter {i} lacks momentum_buffer")

@@ -9,7 +9,7 @@ import os
 import pytest
 import torch
 
-from parameter_efficient_fine_dora_amd import _lib, ops
+from parameter_efficient_fine_dora_amd import _lib, ops, optim
 
 pytestmark = pytest.mark.skipif(not os.path.exists(_lib.LIB_PATH), reason="libdora.so not built")
 
@@ -78,3 +78,40 @@ def test_other_coefficients_get_their_own_workspace(compiled):
         ops.dora_muon(plan, grads, lr=0.1, coefficients=((3.4445, -4.7750, 2.0315),) * steps)
         got, need = compiled.steps[-1]
         assert got == need > 0
+
+
+def parameters():
+    return [torch.nn.Parameter(torch.ones(6, 8)), torch.nn.Parameter(torch.ones(8, 6))]
+
+
+def others():
+    """Optimizers whose state has a momentum_buffer too."""
+    yield torch.optim.SGD, dict(lr=0.1, momentum=0.9), "eps"
+    if hasattr(torch.optim, "Muon"):
+        yield torch.optim.Muon, dict(lr=0.1), "coefficients"
+
+
+@pytest.mark.parametrize("kind,how,lacks", list(others()), ids=lambda v: getattr(v, "__name__", None))
+def test_another_optimizers_checkpoint_is_refused(kind, how, lacks):
+    theirs = parameters()
+    other = kind(theirs, **how)
+    for p in theirs:
+        p.grad = torch.ones_like(p)
+    other.step()
+    saved = other.state_dict()
+    assert all("momentum_buffer" in s for s in saved["state"].values())
+    opt = optim.Muon(parameters(), lr=0.25, momentum=0.5)
+    before = opt.state_dict()
+    with pytest.raises(ValueError, match=f"group 0 lacks .*{lacks}"):
+        opt.load_state_dict(saved)
+    assert opt.state_dict() == before and opt.param_groups[0]["lr"] == 0.25 and not opt.state
+
+
+def test_its_own_checkpoint_is_loaded():
+    opt, ps = optim.Muon(parameters(), lr=0.25, adjust=1.0), parameters()
+    for p in opt.param_groups[0]["params"]:
+        opt.state[p]["momentum_buffer"] = torch.full(p.shape, 2.0)
+    other = optim.Muon(ps)
+    other.load_state_dict(opt.state_dict())
+    assert other.param_groups[0]["lr"] == 0.25 and other.param_groups[0]["adjust"] == 1.0
+    assert all(torch.equal(other.state[p]["momentum_buffer"], torch.full(p.shape, 2.0)) for p in ps)
