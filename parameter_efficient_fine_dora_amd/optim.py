@@ -188,11 +188,14 @@ class Muon(torch.optim.Optimizer):
     def add_param_group(self, param_group):
         super().add_param_group(param_group)
         group = self.param_groups[-1]
-        bad = [tuple(p.shape) for p in group["params"] if p.dim() != 2]
-        if bad:
+        try:
+            for p in group["params"]:
+                if p.dim() != 2:
+                    raise ValueError(f"a parameter of shape {tuple(p.shape)} is not a matrix")
+            ops.update_factor(group["adjust"], 1, 1)   # says what is wrong with it
+        except (TypeError, ValueError):
             self.param_groups.pop()
-            raise ValueError(f"a parameter of shape {bad[0]} is not a matrix")
-        ops.update_factor(group["adjust"], 1, 1)   # says what is wrong with it
+            raise
 
     def __getstate__(self):   # copies and pickles: torch's own parts, and the option
         return {**super().__getstate__(), "master": self.master}

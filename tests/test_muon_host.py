@@ -115,3 +115,15 @@ def test_its_own_checkpoint_is_loaded():
     other.load_state_dict(opt.state_dict())
     assert other.param_groups[0]["lr"] == 0.25 and other.param_groups[0]["adjust"] == 1.0
     assert all(torch.equal(other.state[p]["momentum_buffer"], torch.full(p.shape, 2.0)) for p in ps)
+
+
+@pytest.mark.parametrize("bad,error", [(dict(adjust="none"), ValueError), (dict(adjust=None), TypeError),
+                                       (dict(adjust=1.0, params=[torch.nn.Parameter(torch.ones(3))]), ValueError)],
+                         ids=["name", "none", "vector"])
+def test_a_refused_group_is_not_kept(bad, error):
+    opt = optim.Muon(parameters())
+    with pytest.raises(error):
+        opt.add_param_group(dict(dict(params=parameters()), **bad))
+    assert len(opt.param_groups) == 1
+    opt.add_param_group(dict(params=parameters(), adjust="spectral"))
+    assert len(opt.param_groups) == 2
