@@ -177,6 +177,9 @@ class Muon(torch.optim.Optimizer):
     captured graph repeats the captured step's.
     """
 
+    # what a checkpoint's groups have to say (torch adds an entry of its own to an optimizer's defaults)
+    _OPTIONS = ("lr", "momentum", "weight_decay", "nesterov", "eps", "adjust", "coefficients")
+
     def __init__(self, params, lr=1e-3, momentum=0.95, weight_decay=0.0, *, nesterov=True,
                  coefficients=ops.NEWTON_SCHULZ, eps=1e-7, adjust="rms", master=False):
         super().__init__(params, dict(lr=lr, momentum=momentum, weight_decay=weight_decay,
@@ -258,7 +261,7 @@ class Muon(torch.optim.Optimizer):
     def load_state_dict(self, state_dict):
         """Loads a checkpoint of this class."""
         for i, group in enumerate(state_dict["param_groups"]):
-            lacks = [k for k in self.defaults if k not in group]
+            lacks = [k for k in self._OPTIONS if k not in group]
             if lacks:   # another optimizer's: torch would take the group as it is
                 raise ValueError(f"the checkpoint's group {i} lacks {', '.join(lacks)}")
         for i, s in state_dict["state"].items():

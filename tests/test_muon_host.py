@@ -112,7 +112,9 @@ def test_its_own_checkpoint_is_loaded():
     for p in opt.param_groups[0]["params"]:
         opt.state[p]["momentum_buffer"] = torch.full(p.shape, 2.0)
     other = optim.Muon(ps)
-    other.load_state_dict(opt.state_dict())
+    for _ in range(2):
+        other.load_state_dict(opt.state_dict())
+    assert set(optim.Muon._OPTIONS) == set(opt.defaults)
     assert other.param_groups[0]["lr"] == 0.25 and other.param_groups[0]["adjust"] == 1.0
     assert all(torch.equal(other.state[p]["momentum_buffer"], torch.full(p.shape, 2.0)) for p in ps)
 
