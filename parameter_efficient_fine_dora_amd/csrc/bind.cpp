@@ -694,13 +694,21 @@ PyObject* orthogonalize(PyObject*, PyObject* const* args, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// muon_grads(params, momenta, masters or None, table address, grads, factor): looks at every tensor
-// of a plan, and notes the gradients and scales in the table.  factor: a number, or None for 0.2
-// sqrt(max(rows, cols)).  Returns the gradients' dtype code, or None where something has changed.
+// muon_grads(params, momenta, masters or None, table address, grads, factor, spans address, their
+// number): looks at every tensor of a plan, and notes the gradients and scales in the table.  factor: a
+// number, or None for 0.2 sqrt(max(rows, cols)); spans: first byte and end of every array that the step
+// writes, in order.  Returns the gradients' dtype code, or None where something has changed or a
+// gradient shares memory with one of them.
 PyObject* muon_grads(PyObject*, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  if (n != 6 || !PyList_Check(args[0]) || !PyList_Check(args[1]) || !PyList_Check(args[4]))
+  if (n != 8 || !PyList_Check(args[0]) || !PyList_Check(args[1]) || !PyList_Check(args[4]))
     Py_RETURN_NONE;
+  struct Span {
+    int64_t from, end;
+  };
+  const Span* spans = static_cast<const Span*>(PyLong_AsVoidPtr(args[6]));
+  const Span* last = spans + PyLong_AsSsize_t(args[7]);
+  if (PyErr_Occurred()) return nullptr;
   const bool masters = args[2] != Py_None;
   const Py_ssize_t count = PyList_GET_SIZE(args[0]);
   if (count < 1 || PyList_GET_SIZE(args[1]) != count || PyList_GET_SIZE(args[4]) != count ||
@@ -731,6 +739,9 @@ PyObject* muon_grads(PyObject*, PyObject* const* args, Py_ssize_t n) {
         p->const_data_ptr() != e.param || m->const_data_ptr() != e.momentum ||
         (w && (!matrix(*w) || w->scalar_type() != at::kFloat || w->const_data_ptr() != e.master)))
       Py_RETURN_NONE;
+    const int64_t from = (int64_t)g->const_data_ptr();
+    const Span* next = std::upper_bound(spans, last, from, [](int64_t at, const Span& s) { return at < s.end; });
+    if (next != last && next->from < from + g->numel() * (int64_t)g->element_size()) Py_RETURN_NONE;
     e.grad = g->const_data_ptr();
     e.scale = args[5] == Py_None ? 0.2 * std::sqrt((double)std::max(e.rows, e.cols))
                                  : PyFloat_AS_DOUBLE(args[5]);

@@ -8,6 +8,7 @@ step of the computation runs in the library's kernels.
 """
 from __future__ import annotations
 
+import bisect
 import ctypes
 import functools
 import json
@@ -967,6 +968,9 @@ class MuonPlan:
         for a, b in zip(spans, spans[1:]):
             if b[0] < a[1]:
                 raise ValueError(f"{a[2]} and {b[2]} share memory: a step writes both")
+        self._written, self._ends = spans, [a[1] for a in spans]   # in order, and apart from each other
+        flat = [v for a in spans for v in a[:2]]
+        self._spans = (ctypes.c_int64 * max(len(flat), 1))(*flat)
         self._address = ctypes.addressof(self.table)
         self._bytes = {}   # of workspace, for the coefficients of the last step
 
@@ -992,6 +996,11 @@ class MuonPlan:
         for i, (g, p, e) in enumerate(zip(grads, self.params, self.table)):
             e.grad = _need(g, f"grads[{i}]", gdt, p.shape, self.device).data_ptr()
             e.scale = update_factor(adjust, e.rows, e.cols)
+            end = g.data_ptr() + g.numel() * g.element_size()
+            for lo, hi, name in self._written[bisect.bisect_right(self._ends, g.data_ptr()):]:
+                if lo >= end:
+                    break
+                raise ValueError(f"grads[{i}] and {name} share memory: a step writes one and reads the other")
         return _DT[gdt]
 
 
@@ -1013,13 +1022,15 @@ def dora_muon(plan, grads, *, lr, momentum=0.95, nesterov=True, weight_decay=0.0
     m = momentum m + (1 - momentum) g, u = momentum m + (1 - momentum) g (m without ``nesterov``),
     p = p (1 - lr weight_decay) - lr update_factor(adjust) orthogonalised(u).
 
-    ``grads``: one contiguous tensor per parameter, all bf16 or all float32.
+    ``grads``: one contiguous tensor per parameter, all bf16 or all float32, none of them over memory that
+    the step writes.
     """
     grads = grads if isinstance(grads, list) else list(grads)
     code = None
     if adjust != "spectral":
         factor = None if adjust == "rms" else update_factor(adjust, 1, 1)
-        code = _compiled().muon_grads(plan.params, plan.momenta, plan.masters, plan._address, grads, factor)
+        code = _compiled().muon_grads(plan.params, plan.momenta, plan.masters, plan._address, grads, factor,
+                                      ctypes.addressof(plan._spans), len(plan._written))
     if code is None or plan.params[0].dtype != plan.dtype:
         code = plan._take_grads(grads, adjust)
     iteration, _held = _iteration(coefficients, eps)

@@ -1,0 +1,48 @@
+"""Gradients of a Muon step over the memory that it writes, in the compiled way and in the checked one."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ops():
+    assert torch.cuda.is_available(), "GPU tests need a HIP device"
+    from parameter_efficient_fine_dora_amd import _lib, ops
+    _lib.lib()
+    return ops
+
+
+@pytest.mark.parametrize("adjust", ["rms", "spectral"])   # (the latter takes the checked way)
+def test_gradients_over_what_a_step_writes_are_refused(ops, adjust):
+    room = torch.randn(1000, device="cuda")
+
+    def cut(at):
+        return room[at:at + 48].view(6, 8)
+
+    plan = ops.MuonPlan([cut(100), cut(300)], [cut(148), cut(500)])
+    for at in (53, 100, 147, 148, 195, 253, 347, 453, 547):
+        was = room.clone()
+        for grads in ([cut(0), cut(at)], [cut(at), cut(0)]):
+            with pytest.raises(ValueError, match="share memory"):
+                ops.dora_muon(plan, grads, lr=0.1, adjust=adjust)
+        assert torch.equal(room, was)
+    for at in (0, 52, 196, 252, 348, 452, 548, 700):
+        ps, ms = [p.clone() for p in plan.params], [m.clone() for m in plan.momenta]
+        g = cut(at).clone()
+        ops.dora_muon(ops.MuonPlan(ps, ms), [g, g], lr=0.1, adjust=adjust)
+        ops.dora_muon(plan, [cut(at), cut(at)], lr=0.1, adjust=adjust)
+        assert all(torch.equal(a, b) for a, b in zip(ps + ms, plan.params + plan.momenta))
+        assert torch.equal(g, cut(at))
+
+
+def test_masters_and_empty_matrices(ops):
+    p, w = torch.ones(6, 8, dtype=torch.bfloat16, device="cuda"), torch.ones(6, 8, device="cuda")
+    plan = ops.MuonPlan([p], [torch.zeros(6, 8, device="cuda")], masters=[w])
+    for g in (p, w):
+        with pytest.raises(ValueError, match="share memory"):
+            ops.dora_muon(plan, [g], lr=0.1)
+    none = torch.ones(0, 8, device="cuda")
+    ops.dora_muon(ops.MuonPlan([none], [none.clone()]), [none], lr=0.1)

@@ -129,3 +129,25 @@ def test_a_refused_group_is_not_kept(bad, error):
     assert len(opt.param_groups) == 1
     opt.add_param_group(dict(params=parameters(), adjust="spectral"))
     assert len(opt.param_groups) == 2
+
+
+def test_gradients_over_what_a_step_writes_are_refused(compiled):
+    """Byte for byte: a gradient may lie right before or behind, and gradients over each other."""
+    room = torch.ones(1000)
+    cut = lambda at, rows=6, cols=8: room[at:at + rows * cols].view(rows, cols)
+    plan = ops.MuonPlan([cut(100), cut(300)], [cut(148), cut(500)])
+    for at in (0, 52, 196, 252, 348, 452, 548, 700):
+        ops.dora_muon(plan, [cut(at), cut(at)], lr=0.1)
+    for at, name in ((53, "params.0"), (100, "params.0"), (147, "params.0"), (148, "momenta.0"), (195, "momenta.0"),
+                     (253, "params.1"), (347, "params.1"), (453, "momenta.1"), (547, "momenta.1")):
+        steps = len(compiled.steps)
+        for grads in ([cut(0), cut(at)], [cut(at), cut(0)]):
+            with pytest.raises(ValueError, match=f"{name}. share memory"):
+                ops.dora_muon(plan, grads, lr=0.1)
+        assert len(compiled.steps) == steps
+    p, w = torch.ones(6, 8, dtype=torch.bfloat16), torch.ones(6, 8)
+    plan = ops.MuonPlan([p], [torch.zeros(6, 8)], masters=[w])
+    with pytest.raises(ValueError, match="masters.0. share memory"):
+        ops.dora_muon(plan, [w], lr=0.1)
+    with pytest.raises(ValueError, match="params.0. share memory"):
+        ops.dora_muon(plan, [p], lr=0.1)
