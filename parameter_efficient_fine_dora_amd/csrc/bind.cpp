@@ -598,12 +598,13 @@ PyObject* preference_loss_backward(PyObject*, PyObject* const* args, Py_ssize_t 
 }
 
 // The arguments that both directions of the policy loss begin with: logp, old_logp, advantages,
-// ref_logp, mask, offsets, clip_low, clip_high, dual_clip, kl_coef, denominator, reduce.
+// ref_logp, mask, offsets, clip_low, clip_high, dual_clip, kl_coef, denominator, reduce, per_sequence
+// (None: by the advantages' shape).
 struct Policy {
   const at::Tensor* t[6];
   dora_token_batch b;
   dora_policy_options o;
-  static constexpr int kCount = 12;
+  static constexpr int kCount = 13;
   bool read(PyObject* const* args) {
     double v[5];
     if (!tensors<6>(args, t) || !numbers<5>(args + 6, v) || !PyLong_Check(args[11]) || !t[0] ||
@@ -613,8 +614,9 @@ struct Policy {
     if (!floats_as(&x, x.sizes(), x) || !floats_as(t[1], x.sizes(), x) ||
         (t[3] && !floats_as(t[3], x.sizes(), x)) || !batch_ok(x.sizes(), x, t[4], t[5], b))
       return false;
-    const bool each = floats_as(t[2], x.sizes(), x);
-    if (!each && !vector_ok(t[2], b.sequences, at::kFloat, x)) return false;
+    if (args[12] != Py_None && !PyBool_Check(args[12])) return false;
+    const bool fits = floats_as(t[2], x.sizes(), x), each = args[12] == Py_None ? fits : args[12] == Py_False;
+    if (each ? !fits : !vector_ok(t[2], b.sequences, at::kFloat, x)) return false;
     o = {v[0], v[1], v[2], v[3], v[4], (int32_t)PyLong_AsLong(args[11]), !each};
     return true;
   }

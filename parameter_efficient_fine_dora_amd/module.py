@@ -282,12 +282,14 @@ class PolicyLossFunction(torch.autograd.Function):
 
 def policy_loss(logp: torch.Tensor, old_logp: torch.Tensor, advantages: torch.Tensor, *, ref_logp=None,
                 mask=None, offsets=None, clip=(0.2, 0.2), dual_clip=None, kl_coef: float = 0.0,
-                reduce: str = "token", denominator=None):
+                reduce: str = "token", denominator=None, per_sequence=None):
     """Clipped policy loss on token log probabilities, differentiable in ``logp``.
 
     logp, old_logp, ref_logp: float32 [sequences, length] or, with ``offsets`` (int64 [sequences +
-    1]), packed [tokens]; advantages: float32, of logp's shape or [sequences].  ``mask`` (bool) tells
-    the tokens that count.  The ratio exp(logp - old_logp) is bounded by 1 - clip[0] and 1 + clip[1]
+    1]), packed [tokens]; advantages: float32, of logp's shape or [sequences].  ``per_sequence`` (bool)
+    says which of both they are, and has to where a packed batch may have as many tokens as sequences:
+    without it advantages that fit both are the tokens'.  ``mask`` (bool) tells the tokens that count.
+    The ratio exp(logp - old_logp) is bounded by 1 - clip[0] and 1 + clip[1]
     (and by ``dual_clip`` where the advantage is negative); ``kl_coef`` weighs the divergence
     exp(d) - 1 - d, d = ref_logp - logp.  ``reduce`` is token (mean over tokens) or sequence (mean
     over sequences of their means); ``denominator`` replaces the number that is divided by.
@@ -296,7 +298,8 @@ def policy_loss(logp: torch.Tensor, old_logp: torch.Tensor, advantages: torch.Te
     tokens held by a bound, mean ratio, number of counted tokens.
     """
     _constants(old_logp=old_logp, advantages=advantages, ref_logp=ref_logp)
-    how = dict(clip=clip, dual_clip=dual_clip, kl_coef=kl_coef, reduce=reduce, denominator=denominator)
+    how = dict(clip=clip, dual_clip=dual_clip, kl_coef=kl_coef, reduce=reduce, denominator=denominator,
+               per_sequence=per_sequence)
     logp, old_logp, advantages, ref_logp, mask, offsets = _contiguous(logp, old_logp, advantages,
                                                                       ref_logp, mask, offsets)
     return PolicyLossFunction.apply(logp, old_logp, advantages, ref_logp, mask, offsets, how)

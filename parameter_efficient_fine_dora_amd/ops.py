@@ -584,7 +584,7 @@ def _policy_numbers(clip, dual_clip, kl_coef, reduce, denominator, ref_logp):
 
 
 def _policy_arguments(logp, old_logp, advantages, ref_logp, mask, offsets, clip, dual_clip, kl_coef,
-                      reduce, denominator):
+                      reduce, denominator, per_sequence):
     """Checks what both directions of the policy loss take; returns the batch and the options."""
     _need(logp, "logp", torch.float32)
     dev, shape = logp.device, logp.shape
@@ -594,8 +594,9 @@ def _policy_arguments(logp, old_logp, advantages, ref_logp, mask, offsets, clip,
         _need(ref_logp, "ref_logp", torch.float32, shape, dev)
     elif kl_coef:
         raise ValueError("kl_coef needs ref_logp")
-    # one advantage a token where the shapes agree, else one a sequence
-    each = isinstance(advantages, torch.Tensor) and advantages.shape == shape
+    # unless the caller says: one advantage a token where the shapes agree, else one a sequence
+    each = (isinstance(advantages, torch.Tensor) and advantages.shape == shape if per_sequence is None
+            else not per_sequence)
     _need(advantages, "advantages", torch.float32, shape if each else (batch.sequences,), dev)
     if denominator is not None and not denominator > 0:
         raise ValueError(f"denominator is {denominator}, expected more than 0")
@@ -607,12 +608,14 @@ def _policy_arguments(logp, old_logp, advantages, ref_logp, mask, offsets, clip,
 
 def dora_policy_loss(logp, old_logp, advantages, *, ref_logp=None, mask=None, offsets=None,
                      clip=(0.2, 0.2), dual_clip=None, kl_coef=0.0, reduce="token", denominator=None,
-                     workspace=None):
+                     per_sequence=None, workspace=None):
     """Clipped policy loss of tokens, with ``kl_coef`` times their divergence from a reference.
 
     logp, old_logp, ref_logp   float32 [sequences, length], or [tokens] with ``offsets`` (int64
                      [sequences + 1])
-    advantages       float32, one a token (logp's shape) or one a sequence ([sequences])
+    advantages       float32, one a token (logp's shape) or one a sequence ([sequences]), as
+                     ``per_sequence`` says; by their shape where it is None, and one a token where a
+                     packed batch has as many tokens as sequences and the shape does not tell
     mask             bool, of logp's shape: the tokens that count
     clip             the ratio's bounds are 1 - clip[0] and 1 + clip[1]; ``dual_clip`` bounds it from
                      above where the advantage is negative
@@ -626,11 +629,11 @@ def dora_policy_loss(logp, old_logp, advantages, *, ref_logp=None, mask=None, of
     if workspace is None and _on_gpu(logp):
         fast = _policy_numbers(clip, dual_clip, kl_coef, reduce, denominator, ref_logp)
         out = fast and _compiled().policy_loss(logp, old_logp, advantages, ref_logp, mask, offsets, *fast,
-                                               _stream(logp.device))
+                                               per_sequence, _stream(logp.device))
         if out is not None:
             return out
     batch, how = _policy_arguments(logp, old_logp, advantages, ref_logp, mask, offsets, clip,
-                                   dual_clip, kl_coef, reduce, denominator)
+                                   dual_clip, kl_coef, reduce, denominator, per_sequence)
     dev = logp.device
     loss = torch.empty((), dtype=torch.float32, device=dev)
     stats = torch.empty(4, dtype=torch.float32, device=dev)
@@ -647,17 +650,18 @@ def dora_policy_loss(logp, old_logp, advantages, *, ref_logp=None, mask=None, of
 
 def dora_policy_loss_backward(grad_loss, weight, logp, old_logp, advantages, *, ref_logp=None,
                               mask=None, offsets=None, clip=(0.2, 0.2), dual_clip=None, kl_coef=0.0,
-                              reduce="token", denominator=None, grad_logp=None):
+                              reduce="token", denominator=None, per_sequence=None, grad_logp=None):
     """Gradient of dora_policy_loss's loss with respect to logp, float32 of its shape; grad_loss is a
-    float32 scalar on the device, weight as the forward returned it."""
+    float32 scalar on the device, weight as the forward returned it, the rest as the forward took it."""
     if grad_logp is None and _on_gpu(logp):
         fast = _policy_numbers(clip, dual_clip, kl_coef, reduce, denominator, ref_logp)
         out = fast and _compiled().policy_loss_backward(logp, old_logp, advantages, ref_logp, mask, offsets,
-                                                        *fast, grad_loss, weight, _stream(logp.device))
+                                                        *fast, per_sequence, grad_loss, weight,
+                                                        _stream(logp.device))
         if out is not None:
             return out
     batch, how = _policy_arguments(logp, old_logp, advantages, ref_logp, mask, offsets, clip,
-                                   dual_clip, kl_coef, reduce, denominator)
+                                   dual_clip, kl_coef, reduce, denominator, per_sequence)
     dev = logp.device
     if _need(grad_loss, "grad_loss", torch.float32, None, dev).numel() != 1:
         raise ValueError("grad_loss must be one number")
