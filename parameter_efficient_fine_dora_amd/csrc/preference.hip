@@ -252,6 +252,18 @@ int check_options(const dora_preference_options* o) {
 int check_pairs(int64_t pairs) {
   return pairs < 0 || pairs >= kMaxSequences ? DORA_ERR_SHAPE : DORA_OK;
 }
+// Whether a launch of its own looks for every sequence's coefficient.  Otherwise each wave looks through all
+// pairs, 64 at a time, for each sequence that its round of tokens meets, which is less than another launch
+// for up to eight such looks: of 256 pairs and 512 sequences of 8, 32, 64 and 128 tokens, 128, 32, 16
+// and 8 looks, the waves' own take 44, 13.3, 8.1 and 5.7 us, the launch 21.3, 9.4, 8.5 and 8.5; of 64 sequences
+// of 64 and 128 tokens 13.9 and 8.8, the launch 9.1 and 8.5; of 4 pairs of 8 sequences of 16 and 64 tokens, 16
+// and 4 looks, 9.5 and 6.0, the launch 7.9 and 7.6.  Many pairs are looked through once for a sequence, however
+// many waves it has (127 pairs of 2 x 1031 tokens: loss and gradient 19.5 us in all, with the launch 22.8).
+constexpr int64_t kMostLooks = 8, kMostPairs = 256;
+bool looks_first(const Batch& b, int64_t pairs) {
+  const int64_t each = (pairs + 63) / 64;
+  return pairs > kMostPairs || (double)b.sequences * kRound * each > (double)kMostLooks * b.tokens;
+}
 Numbers numbers(const dora_preference_options& o) {
   return {o.beta, o.margin, o.smoothing, o.kind, o.normalize == 1};
 }
@@ -339,9 +351,7 @@ DORA_API int dora_preference_backward(const dora_token_batch* batch,
   double* coef = reinterpret_cast<double*>(parts_at(l, ws).own);
   hipStream_t st = reinterpret_cast<hipStream_t>(hip_stream);
   const Pairs p = {numbers(*options), no_seq ? 0 : pairs, grad_loss, logit, count, chosen, rejected};
-  // Up to 256 pairs are looked through by every wave, four loads one after the other, which is less
-  // than another launch (127 pairs of 2 x 1031 tokens: loss and gradient 19.5 us in all against 22.8).
-  const bool known = p.count > 256;
+  const bool known = looks_first(b, p.count);
   if (known) {
     LaunchTimer timer("preference_coef", st);
     hipLaunchKernelGGL(dora_preference_coef, dim3(wave_grid(b.sequences)), dim3(kThreads), 0, st, b, p,
