@@ -167,11 +167,17 @@ typedef struct {
 /*
  * out = the iteration's last X for each of `count` matrices (`matrices` and the
  * coefficients are host arrays, read during the call only).  Matrices of any sizes
- * share launches; the workspace holds 2 bytes (bf16) or 8 (float32; 4 for a shorter side
- * n <= 64) an element, 20 n^2, and partial sums; sides are padded to 128 (n <= 64: to
- * 64).  Sums are float32, and float32 results have float32's precision.  A matrix of
- * zeros stays zero; one with a NaN
- * or an infinity becomes NaN throughout, the others of the call do not.
+ * share launches.  Sums are float32, and float32 results have float32's precision.  A
+ * matrix of zeros stays zero; one with a NaN or an infinity becomes NaN throughout, the
+ * others of the call do not.
+ *
+ * The workspace holds 2 to 8 bytes an element, 20 n^2 (n the shorter side) and partial
+ * sums, with sides padded to 128 (n <= 64: to 64, the longer one to 128).  Ask for it:
+ * how many bytes an element depends on how often the coefficients make the precision
+ * ask for a new S on the way.  bf16 matrices take 2 where never, 6 where once, 8 where
+ * more often; float32 ones 4 where never, or up to twice with n <= 64, else 8.  The
+ * usual five steps ask for none for bf16 and for two for float32, ten for one and for
+ * four.
  */
 DORA_API size_t dora_orthogonalize_workspace_bytes(const dora_matrix* matrices, int64_t count,
                                                    const dora_orthogonalize_options* options);
@@ -207,8 +213,9 @@ typedef struct {
  *   p = p (1 - lr weight_decay) - lr scale X(u),  X(u) the iteration's last X from u
  * m and the update are float32; p is rounded once.  u is taken to 22 bits of its largest element,
  * whatever that is.  A NaN or an infinity in a gradient makes its own element of m, and its own
- * matrix, NaN.  The workspace holds 4 (bf16 parameters without masters, or n <= 64) or 8 bytes an
- * element beside what dora_orthogonalize's holds for n.
+ * matrix, NaN.  The workspace is a float32 dora_orthogonalize's, with a new S less often: the usual
+ * five steps ask for none for bf16 parameters without masters (4 bytes an element) and for one for
+ * the others (4 with n <= 64, else 8).
  */
 DORA_API size_t dora_muon_workspace_bytes(const dora_muon_tensor* tensors, int64_t count,
                                           const dora_muon_options* options);
