@@ -987,13 +987,16 @@ class MuonPlan:
                    and p.is_contiguous() and m.is_contiguous() and m.shape == p.shape
                    for e, p, m, w in zip(self.table, self.params, self.momenta, masters))
 
-
     def _take_grads(self, grads, adjust):
         """Checks the gradients and notes them and their updates' factors; returns their dtype's code."""
         if len(grads) != len(self.params):
             raise ValueError(f"{len(grads)} gradients for {len(self.params)} params")
         if not self.unchanged():
             raise ValueError("a tensor's storage has changed since the plan was made")
+        for nm, lst, dt in (("params", self.params, self.dtype), ("momenta", self.momenta, torch.float32),
+                            ("masters", self.masters, torch.float32)):
+            for i, (t, p) in enumerate(zip(lst or (), self.params)):
+                _need(t, f"{nm}[{i}]", dt, p.shape, self.device)
         gdt = grads[0].dtype if isinstance(grads[0], torch.Tensor) else None
         if gdt is not None and gdt not in _DT:
             raise ValueError(f"unsupported dtype {gdt}; use float32 or bfloat16")
@@ -1030,13 +1033,14 @@ def dora_muon(plan, grads, *, lr, momentum=0.95, nesterov=True, weight_decay=0.0
     the step writes.
     """
     grads = grads if isinstance(grads, list) else list(grads)
-    code = None
-    if adjust != "spectral":
-        factor = None if adjust == "rms" else update_factor(adjust, 1, 1)
-        code = _compiled().muon_grads(plan.params, plan.momenta, plan.masters, plan._address, grads, factor,
-                                      ctypes.addressof(plan._spans), len(plan._written))
+    factor = None if adjust == "rms" else update_factor(adjust, 1, 1)
+    code = _compiled().muon_grads(plan.params, plan.momenta, plan.masters, plan._address, grads, factor,
+                                  ctypes.addressof(plan._spans), len(plan._written))
     if code is None or plan.params[0].dtype != plan.dtype:
         code = plan._take_grads(grads, adjust)
+    elif adjust == "spectral":
+        for e in plan.table:
+            e.scale = update_factor(adjust, e.rows, e.cols)
     iteration, _held = _iteration(coefficients, eps)
     how = _lib.DoraMuonOptions(iteration, plan.param_code, code, int(bool(nesterov)), 0, float(lr),
                                float(momentum), float(weight_decay))

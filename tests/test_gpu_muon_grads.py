@@ -1,4 +1,4 @@
-"""Gradients of a Muon step over the memory that it writes, in the compiled way and in the checked one."""
+"""Gradients of a Muon step over the memory that it writes."""
 from __future__ import annotations
 
 import pytest
@@ -15,7 +15,7 @@ def ops():
     return ops
 
 
-@pytest.mark.parametrize("adjust", ["rms", "spectral"])   # (the latter takes the checked way)
+@pytest.mark.parametrize("adjust", ["rms", "spectral"])
 def test_gradients_over_what_a_step_writes_are_refused(ops, adjust):
     room = torch.randn(1000, device="cuda")
 

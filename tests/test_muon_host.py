@@ -151,3 +151,17 @@ def test_gradients_over_what_a_step_writes_are_refused(compiled):
         ops.dora_muon(plan, [w], lr=0.1)
     with pytest.raises(ValueError, match="params.0. share memory"):
         ops.dora_muon(plan, [p], lr=0.1)
+
+
+@pytest.mark.parametrize("change", ["transposed", "type"])
+@pytest.mark.parametrize("of", ["params", "momenta", "masters"])
+def test_a_tensor_that_lies_otherwise_in_the_same_storage_is_refused(compiled, of, change):
+    """Addresses and sizes are as they were; the step would take rows for columns, or bits for others."""
+    p, m, w = torch.ones(8, 8, dtype=torch.bfloat16), torch.zeros(8, 8), torch.ones(8, 8)
+    plan = ops.MuonPlan([p], [m], masters=[w])
+    ops.dora_muon(plan, [torch.ones(8, 8)], lr=0.1)
+    t = getattr(plan, of)[0]
+    t.data = t.data.t() if change == "transposed" else t.data.view(torch.float16 if of == "params" else torch.int32)
+    with pytest.raises(ValueError, match="contiguous|dtype|storage"):
+        ops.dora_muon(plan, [torch.ones(8, 8)], lr=0.1)
+    assert len(compiled.steps) == 1
