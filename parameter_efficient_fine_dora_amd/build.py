@@ -24,8 +24,7 @@ BIND = os.path.join(HERE, "_bind.so")   # csrc/bind.cpp
 SOURCES = ["api.hip", "gemm.hip", "gram.hip", "rowwise.hip", "small.hip", "probe.hip", "noalloc.hip",
            "layernorm.hip", "logprob.hip", "adamw.hip", "preference.hip", "policy.hip",
            "orthogonal.hip"]
-HEADERS = ["common.h", "kernels.h", "entry.h", "elem.h", "checks.h", "launch_cut.h", "sequences.h",
-           "exponential.h"]
+HEADERS = ["common.h", "kernels.h", "entry.h", "elem.h", "checks.h", "launch_cut.h", "sequences.h"]
 ARCH = "gfx950"
 
 
