@@ -211,11 +211,11 @@ typedef struct {
  *   m = momentum m + (1 - momentum) grad
  *   u = momentum m + (1 - momentum) grad with nesterov, else m
  *   p = p (1 - lr weight_decay) - lr scale X(u),  X(u) the iteration's last X from u
- * m and the update are float32; p is rounded once.  u is taken to 22 bits of its largest element,
- * whatever that is.  A NaN or an infinity in a gradient makes its own element of m, and its own
- * matrix, NaN.  The workspace is a float32 dora_orthogonalize's, with a new S less often: the usual
- * five steps ask for none for bf16 parameters without masters (4 bytes an element) and for one for
- * the others (4 with n <= 64, else 8).
+ * m and the update are float32; p is rounded once.  u is taken to 22 bits, down to 2^-38 of its
+ * largest element, whatever that is.  A NaN or an infinity in a gradient makes its own element of
+ * m NaN or infinite, and its own matrix NaN.  The workspace is a float32 dora_orthogonalize's, with
+ * a new S less often: the usual five steps ask for none for bf16 parameters without masters (4 bytes
+ * an element) and for one for the others (4 with n <= 64, else 8).
  */
 DORA_API size_t dora_muon_workspace_bytes(const dora_muon_tensor* tensors, int64_t count,
                                           const dora_muon_options* options);

@@ -18,8 +18,9 @@
 // A bf16 X is one half precision number exactly (its bits below 2^-38 of its largest element are
 // left out), a float32 X and every update are hi + lo, scaled by a power of two that X's largest element
 // asks for, so that any finite X is held to 22 bits.  (That costs a pass over gradient and momentum.
-// Two bf16 numbers, which hold float32's range, would save it for bf16 parameters, 24 rank-384 layers'
-// step 1.42 ms instead of 1.62, but keep 16 bits, raised 485 times, and squares overflow from 2^104 eps on.)
+// Two bf16 numbers, which hold float32's range, would save it for bf16 parameters, on one card 24 rank-384
+// layers' step 1.42 ms instead of 1.62, but keep 16 bits, raised 485 times, and their squares overflow from
+// 2^104 eps on.)
 //
 // Layout.  A "pair" row holds blocks of 32 columns: 32 hi, then 32 lo, so that the 128 bytes that
 // a stage copies of a row are the hi and lo of 32 columns; a "single" row holds 64 columns there.
@@ -1398,7 +1399,7 @@ __device__ __forceinline__ void last_product(uint8_t* sm, const Group& g, uint8_
 
 // What the parameter was where a tile from (row0, col0) of X on will go: read before the products.
 // Behind them each line would wait for its own, since the stores between cannot be told apart from the
-// loads (24 high-rank layers' QX: 457 us, so 472).
+// loads (56 layers' masters, in dora_orthogonal_last, 113 us, so 119; 24 high-rank layers' step is level).
 template <typename P, bool BF, Result WHAT>
 __device__ __forceinline__ void read_before(const Sinks& a, const Where& here, int64_t row0, int64_t col0,
                                             int rows, int cols, float (&before)[P::kLines][8]) {
@@ -1683,8 +1684,8 @@ constexpr int64_t kEnough = 256;
 constexpr int64_t kFewTiles = 384;   // of a launch of n x n products
 constexpr int64_t kCus = 256;
 // Workgroups of the sums over m, and the least stages of 64 of one's part.  Parts cost their partial
-// sums, few of them leave CUs empty or the last ones waiting: 24 layers' step 1.43 ms, with 768
-// wanted 1.45; four matrices of 384 x 8192 190 us, with parts of four stages 201; with tiles of 64
+// sums, few of them leave CUs empty or the last ones waiting: 24 layers' step 1.57 ms, with 768
+// wanted 1.60; four matrices of 384 x 8192 190 us, with parts of four stages 201; with tiles of 64
 // 1031 x 517 172 us, with parts of eight 177.  For n <= 64 three lie on a CU (dora_orthogonal_fold).
 constexpr int64_t kWantSums = 1024, kWantSmall = 768;
 constexpr int64_t kLeastPart = 8, kLeastSmall = 4;

@@ -243,8 +243,8 @@ __global__ __launch_bounds__(kFinish) void dora_policy_finish(int64_t sequences,
   finish<SEQ>(sequences, means, totals, groups, to, lds);
 }
 // All of a small batch's loss by one workgroup, a round a wave: one launch (from Python eight answers of
-// 256 tokens 6.8 us, in two launches 10.1; of 512 8.7 and 10.1; of 1024, two rounds a wave, 12.6 and
-// 9.9; means of 64 sequences of 32 19.8 and 19.2).
+// 256 tokens 7.4 us, in two launches 9.2; of 512 9.3 and 9.2; of 1024, two rounds a wave, 13.7 and
+// 9.2; means of 64 sequences of 32 20.3 and 19.2).
 template <bool SEQ, bool PER>
 __global__ __launch_bounds__(kFinish) void dora_policy_small(const Batch b, const Parts parts, int64_t chunk,
                                                              const Tokens k, const Results to) {

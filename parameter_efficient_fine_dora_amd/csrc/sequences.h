@@ -175,7 +175,7 @@ inline Batch device_batch(const dora_token_batch& b) {
 
 // Tokens of a wave's chunk: one round until there are `most` of them.  Sums leave parts of each
 // chunk behind; the policy's gradient leaves nothing, and waves of one round hide each other's loads best (4.2M
-// tokens' policy gradient 19 us, with four rounds a wave 22.6).
+// tokens' policy gradient, over and over on the same tokens, 20.0 us, with four rounds a wave 21.2).
 constexpr int64_t kMostSums = 4096, kMostGrads = int64_t(1) << 22;
 inline int64_t chunk_of(int64_t tokens, int64_t most) {
   const int64_t rounds = (tokens + kRound - 1) / kRound;
